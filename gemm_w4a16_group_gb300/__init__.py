@@ -15,12 +15,22 @@ Affine form w = scale * q + bias (MLX affine 4-bit checkpoints):
     pa = repack_affine(qweight, scales, biases, N, K, group)
     xs = xsum(x, K, group)                 # group sums of x, shared by every weight on x
     y = gemm_affine(x, pa, N, K, group, xs)
+
+The rest of a verify step of drafted token trees over a paged key/value cache
+(k_cache, v_cache [pages, kv heads, page rows, dim], bf16 or float8_e4m3fn):
+
+    kv_reserve(table, refs, rows, want, page_rows)                 # pages for the new tokens
+    kv_append(k, v, k_cache, v_cache, table, lengths, starts)      # per layer
+    o = tree_attention(q, k_cache, v_cache, table, lengths, starts, mask, max_tree)
+    path, count, token = tree_accept(target, draft, mask, starts, max_tree)
+    lengths = kv_compact(k_layers, v_layers, table, lengths, path, count)
 """
 from __future__ import annotations
 
 import ctypes
 import functools
 import os
+import struct as _struct
 
 from . import build as _build
 
@@ -32,6 +42,8 @@ __all__ = [
     "AFFINE", "repack_affine", "repack_affine_gateup", "xsum_bytes", "xsum", "gemm_affine", "gateup_silu_affine",
     "gemm_affine_noalloc", "topk", "gemm_topk", "affine_bits_repacked_bytes", "repack_affine_bits",
     "affine_bits_scratch_bytes", "gemm_affine_bits", "dequantize_affine_bits",
+    "MAX_TREE", "MAX_ROWS", "kv_append", "tree_attention_workspace_bytes", "tree_attention", "tree_accept", "kv_compact",
+    "kv_free", "kv_fork", "kv_reserve",
 ]
 
 # symbols declared in include/w4a16.h
@@ -43,6 +55,8 @@ EXPORTS = (
     "w4a16_xsum", "w4a16_gemm_affine", "w4a16_gateup_silu_affine", "w4a16_gemm_affine_noalloc",
     "w4a16_topk", "w4a16_gemm_topk", "w4a16_affine_bits_repacked_bytes", "w4a16_repack_affine_bits",
     "w4a16_affine_bits_scratch_bytes", "w4a16_gemm_affine_bits", "w4a16_dequantize_affine_bits",
+    "w4a16_kv_append", "w4a16_tree_attention_workspace_bytes", "w4a16_tree_attention", "w4a16_tree_accept",
+    "w4a16_kv_compact", "w4a16_kv_free", "w4a16_kv_fork", "w4a16_kv_reserve",
 )
 KERNEL_AUTO, KERNEL_GEMV, KERNEL_SMALLM, KERNEL_TC, KERNEL_XSTAGED, KERNEL_DECODE_TC = 0, 1, 2, 3, 4, 5
 # the `sym` argument: 0 zero points, 1 symmetric (z = 8), AFFINE scale * q + bias
@@ -129,6 +143,23 @@ def lib(auto_build: bool = True) -> ctypes.CDLL:
     L.w4a16_gemm_affine_bits.restype = i32
     L.w4a16_dequantize_affine_bits.argtypes = [P, i32, i32, i32, i32, P, P]
     L.w4a16_dequantize_affine_bits.restype = i32
+    i64, f32 = ctypes.c_int64, ctypes.c_float
+    L.w4a16_kv_append.argtypes = [P, P, i64, i64, i64, i64, P, P, i32, P, P, i32, i32, P]
+    L.w4a16_kv_append.restype = i32
+    L.w4a16_tree_attention_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    L.w4a16_tree_attention_workspace_bytes.restype = sz
+    L.w4a16_tree_attention.argtypes = [P, i64, i64, P, P, i32, P, P, P, i32, i32, i32, i32, f32, P, P, P]
+    L.w4a16_tree_attention.restype = i32
+    L.w4a16_tree_accept.argtypes = [P, P, P, P, i32, i32, i32, P, P, P, P]
+    L.w4a16_tree_accept.restype = i32
+    L.w4a16_kv_compact.argtypes = [P, P, i32, P, P, P, i32, i32, P, P]
+    L.w4a16_kv_compact.restype = i32
+    L.w4a16_kv_free.argtypes = [P, i32, i32, P, P, i32, P, i32, P]
+    L.w4a16_kv_free.restype = i32
+    L.w4a16_kv_fork.argtypes = [P, P, i32, i32, P, P, P, P, i32, P, P]
+    L.w4a16_kv_fork.restype = i32
+    L.w4a16_kv_reserve.argtypes = [P, i32, i32, P, i32, i32, P, P, i32, P, P]
+    L.w4a16_kv_reserve.restype = i32
     _lib = L
     return L
 
@@ -551,8 +582,232 @@ def dequantize(packed, N, K, group, sym, stream=None):
     return out
 
 
+# ---------------------------------------------------------------------------
+# Paged key/value cache and the attention of drafted token trees
+# ---------------------------------------------------------------------------
+MAX_TREE = 64     # new tokens of a sequence in one attention or acceptance call
+MAX_ROWS = 4096   # rows that one fork, free or reserve call may name
+
+# w4a16_kv_cache: k, v, k_scale, v_scale; layer, page, head and row strides of
+# each; layers, pages, kv_heads, page_rows, dim, type
+_KV_CACHE = _struct.Struct("=4Q8q6i")
+
+
+def _kv_cache(k_cache, v_cache, k_scale, v_scale, one_layer, d):
+    """The w4a16_kv_cache bytes of a cache given as [pages, kv heads, page
+    rows, dim] tensors (any strides, dim contiguous), or with a leading layer
+    axis unless `one_layer`."""
+    torch = _torch()
+    shape = k_cache.shape
+    if len(shape) != 4 and (one_layer or len(shape) != 5):
+        raise ValueError("k_cache must be [pages, kv heads, page rows, dim]" +
+                         ("" if one_layer else ", or that with a leading layer axis"))
+    if v_cache.shape != shape:
+        raise ValueError(f"v_cache has shape {tuple(v_cache.shape)}, k_cache {tuple(shape)}")
+    dt = k_cache.dtype
+    e4m3 = dt == torch.float8_e4m3fn
+    if (not e4m3 and dt != torch.bfloat16) or v_cache.dtype != dt:
+        raise TypeError(f"k_cache, v_cache: dtypes {dt}, {v_cache.dtype} are not both bfloat16 or both float8_e4m3fn")
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not _is_device_tensor(t):
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.device != d:
+            raise ValueError(f"{name} is on {t.device}, the call's other tensors on {d}")
+    ks, vs = k_cache.stride(), v_cache.stride()
+    if ks[-1] != 1 or vs[-1] != 1:
+        raise ValueError("k_cache, v_cache: the last axis must be contiguous")
+    if len(shape) == 4:
+        shape, ks, vs = (1, *shape), (0, *ks), (0, *vs)
+    kp = vp = 0
+    if e4m3 and one_layer:
+        if k_scale is None or v_scale is None:
+            raise ValueError("a float8_e4m3fn cache needs k_scale and v_scale")
+        kp = _ptr(k_scale, (torch.float32,), "k_scale", 4 * shape[2], d).value
+        vp = _ptr(v_scale, (torch.float32,), "v_scale", 4 * shape[2], d).value
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("k_scale and v_scale belong to float8_e4m3fn caches")
+    return _KV_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), kp, vp, *ks[:4], *vs[:4], *shape, int(e4m3)), shape
+
+
+def _int32(t, name, shape, d):
+    """Data pointer of an int32 index tensor of exactly `shape` (-1: any size)."""
+    if t.dim() != len(shape) or any(w >= 0 and w != g for w, g in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
+    return _ptr(t, (_torch().int32,), name, 0, d)
+
+
+def _token_rows(t, name, heads, dim, d):
+    """Pointer and strides of a bf16 [tokens, heads, dim] tensor whose last axis is contiguous."""
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, {dim}], not {list(t.shape)}")
+    if t.dtype != _torch().bfloat16:
+        raise TypeError(f"{name}: dtype {t.dtype} is not bfloat16")
+    if not _is_device_tensor(t):
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != d:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {d}")
+    s = t.stride()
+    if s[2] != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    return t.data_ptr(), s[0], s[1]
+
+
+def kv_append(k, v, k_cache, v_cache, page_table, lengths, starts, k_scale=None, v_scale=None, stream=None):
+    """Write the new tokens' keys and values (bf16 [tokens, kv heads, dim],
+    strided views allowed) behind each row's context: token starts[b] + i goes
+    to position lengths[b] + i of row b. page_table int32 [rows, max pages],
+    lengths int32 [rows], starts int32 [rows + 1]. e4m3 caches store x /
+    scale[head], rounded to nearest and saturated."""
+    d = k.device
+    cache, (_, _, heads, _, dim) = _kv_cache(k_cache, v_cache, k_scale, v_scale, True, d)
+    kp, kt, kh = _token_rows(k, "k", heads, dim, d)
+    vp, vt, vh = _token_rows(v, "v", heads, dim, d)
+    if v.shape[0] != k.shape[0]:
+        raise ValueError(f"k has {k.shape[0]} tokens, v {v.shape[0]}")
+    table = _int32(page_table, "page_table", (-1, -1), d)
+    rows, width = page_table.shape
+    rc = lib().w4a16_kv_append(kp, vp, kt, kh, vt, vh, cache, table, width, _int32(lengths, "lengths", (rows,), d),
+                               _int32(starts, "starts", (rows + 1,), d), rows, k.shape[0], _stream(stream, d))
+    _check(rc, "w4a16_kv_append")
+
+
+@functools.lru_cache(maxsize=1024)
+def tree_attention_workspace_bytes(heads: int, kv_heads: int, dim: int, max_tree: int) -> int:
+    return int(lib().w4a16_tree_attention_workspace_bytes(heads, kv_heads, dim, max_tree))
+
+
+def tree_attention(q, k_cache, v_cache, page_table, lengths, starts, mask, max_tree, scale=None, k_scale=None,
+                   v_scale=None, out=None, workspace=None, stream=None):
+    """bf16 [tokens, heads, dim]: attention of the new tokens over their rows'
+    paged contexts and, as the int64 [tokens] mask words say (bit j: new token
+    j of the row; None: a causal chain), over one another. q bf16 [tokens,
+    heads, dim] (strided views allowed); every row has at most max_tree <=
+    MAX_TREE new tokens, appended before. scale defaults to dim ** -0.5. A token
+    that sees nothing gets 0; padding tokens (at starts[rows] and above) are
+    left as they are in `out`. `workspace` (uint8,
+    tree_attention_workspace_bytes) is allocated when not given."""
+    torch = _torch()
+    d = q.device
+    cache, (_, _, kv_heads, _, dim) = _kv_cache(k_cache, v_cache, k_scale, v_scale, True, d)
+    qp, qt, qh = _token_rows(q, "q", None, dim, d)
+    tokens, heads = q.shape[0], q.shape[1]
+    need = tree_attention_workspace_bytes(heads, kv_heads, dim, max_tree)
+    if need == 0:
+        raise W4A16Error(f"tree_attention: unsupported heads={heads} kv_heads={kv_heads} dim={dim} max_tree={max_tree}")
+    table = _int32(page_table, "page_table", (-1, -1), d)
+    rows, width = page_table.shape
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=d)
+    if out is None:
+        out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=d)
+    rc = lib().w4a16_tree_attention(qp, qt, qh, cache, table, width, _int32(lengths, "lengths", (rows,), d),
+                                    _int32(starts, "starts", (rows + 1,), d),
+                                    _ptr(mask, (torch.int64,), "mask", 8 * tokens, d), rows, tokens, heads, max_tree,
+                                    dim ** -0.5 if scale is None else scale,
+                                    _ptr(out, (torch.bfloat16,), "out", 2 * tokens * heads * dim, d),
+                                    _ptr(workspace, (torch.uint8,), "workspace", need, d), _stream(stream, d))
+    _check(rc, "w4a16_tree_attention")
+    return out
+
+
+def tree_accept(target, draft, mask, starts, max_tree, path=None, count=None, token=None, stream=None):
+    """Greedy walk down each row's draft tree: target int64 [tokens] the
+    model's pick after each node (gemm_argmax), draft int64 [tokens] the drafted
+    tokens, mask as in tree_attention. Returns (path int32 [rows, max_tree]:
+    the accepted nodes, then -1; count int32 [rows]; token int64 [rows]: the
+    pick after the last accepted node)."""
+    torch = _torch()
+    d = target.device
+    tokens, rows = target.numel(), starts.numel() - 1
+    if path is None:
+        path = torch.empty((rows, max_tree), dtype=torch.int32, device=d)
+    if count is None:
+        count = torch.empty(rows, dtype=torch.int32, device=d)
+    if token is None:
+        token = torch.empty(rows, dtype=torch.int64, device=d)
+    i64 = (torch.int64,)
+    rc = lib().w4a16_tree_accept(_ptr(target, i64, "target", 0, d), _ptr(draft, i64, "draft", 8 * tokens, d),
+                                 _ptr(mask, i64, "mask", 8 * tokens, d), _int32(starts, "starts", (-1,), d), rows,
+                                 tokens, max_tree, _int32(path, "path", (rows, max_tree), d),
+                                 _int32(count, "count", (rows,), d), _ptr(token, i64, "token", 8 * rows, d),
+                                 _stream(stream, d))
+    _check(rc, "w4a16_tree_accept")
+    return path, count, token
+
+
+def kv_compact(k_cache, v_cache, page_table, lengths, path, count, lengths_out=None, stream=None):
+    """Move the accepted rows together in every layer of the cache ([layers,]
+    pages, kv heads, page rows, dim): position lengths[b] + path[b, i] to
+    lengths[b] + i for i < count[b]. Returns the new lengths, lengths + count
+    (a new tensor, or `lengths_out`, which must not be `lengths`)."""
+    torch = _torch()
+    d = k_cache.device
+    cache, _ = _kv_cache(k_cache, v_cache, None, None, False, d)
+    table = _int32(page_table, "page_table", (-1, -1), d)
+    rows, width = page_table.shape
+    if lengths_out is None:
+        lengths_out = torch.empty(rows, dtype=torch.int32, device=d)
+    rc = lib().w4a16_kv_compact(cache, table, width, _int32(lengths, "lengths", (rows,), d),
+                                _int32(path, "path", (rows, -1), d), _int32(count, "count", (rows,), d), rows,
+                                path.shape[1], _int32(lengths_out, "lengths_out", (rows,), d), _stream(stream, d))
+    _check(rc, "w4a16_kv_compact")
+    return lengths_out
+
+
+def kv_free(page_table, lengths, refs, rows, stream=None):
+    """Drop the table rows `rows` (int32 [n], distinct): one reference (refs
+    int32 [pages]) of each page they hold; their entries become -1, their
+    lengths 0."""
+    d = page_table.device
+    table = _int32(page_table, "page_table", (-1, -1), d)
+    table_rows, width = page_table.shape
+    rc = lib().w4a16_kv_free(table, width, table_rows, _int32(lengths, "lengths", (table_rows,), d),
+                             _int32(refs, "refs", (-1,), d), refs.numel(), _int32(rows, "rows", (-1,), d),
+                             rows.numel(), _stream(stream, d))
+    _check(rc, "w4a16_kv_free")
+
+
+def kv_fork(k_cache, v_cache, page_table, lengths, refs, src, dst, ok=None, stream=None):
+    """Branch: the empty table row dst[j] becomes a copy of row src[j] (int32
+    [n]). Whole pages are shared, a part-filled last page is copied in every
+    layer into the lowest free page. Returns ok int32 [1]: 1, or 0 when the
+    free pages did not suffice and nothing changed."""
+    torch = _torch()
+    d = page_table.device
+    cache, shape = _kv_cache(k_cache, v_cache, None, None, False, d)
+    table = _int32(page_table, "page_table", (-1, -1), d)
+    table_rows, width = page_table.shape
+    if ok is None:
+        ok = torch.empty(1, dtype=torch.int32, device=d)
+    n = src.numel()
+    rc = lib().w4a16_kv_fork(cache, table, width, table_rows, _int32(lengths, "lengths", (table_rows,), d),
+                             _int32(refs, "refs", (shape[1],), d), _int32(src, "src", (n,), d),
+                             _int32(dst, "dst", (n,), d), n, _int32(ok, "ok", (1,), d), _stream(stream, d))
+    _check(rc, "w4a16_kv_fork")
+    return ok
+
+
+def kv_reserve(page_table, refs, rows, want, page_rows, ok=None, stream=None):
+    """Room to grow: table row rows[j] gets the lowest free pages until it
+    holds want[j] tokens (int32 [n] each). Returns ok int32 [1]: 1, or 0 when
+    the free pages did not suffice and nothing changed."""
+    torch = _torch()
+    d = page_table.device
+    table = _int32(page_table, "page_table", (-1, -1), d)
+    table_rows, width = page_table.shape
+    if ok is None:
+        ok = torch.empty(1, dtype=torch.int32, device=d)
+    n = rows.numel()
+    rc = lib().w4a16_kv_reserve(table, width, table_rows, _int32(refs, "refs", (-1,), d), refs.numel(), page_rows,
+                                _int32(rows, "rows", (n,), d), _int32(want, "want", (n,), d), n,
+                                _int32(ok, "ok", (1,), d), _stream(stream, d))
+    _check(rc, "w4a16_kv_reserve")
+    return ok
+
+
 def kernel_status() -> int:
-    """Synchronise and return (and clear) the kernels' timeout flag: 0 or -5."""
+    """Synchronise and return (and clear) the kernels' status: 0, -5 (a bounded
+    wait gave up) or -6 (a cache call skipped an index outside its buffers)."""
     return int(lib().w4a16_kernel_status())
 
 

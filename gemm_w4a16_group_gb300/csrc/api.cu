@@ -1,10 +1,12 @@
 // C ABI (include/w4a16.h): argument checks, device checks and kernel choice.
 // Nothing is launched when a check fails; every check that needs no GPU runs
 // before the first CUDA call.
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
 #include <cstdio>
 #include <mutex>
+#include <utility>
 
 #include "w4a16.h"
 #include "w4a16_internal.h"
@@ -131,6 +133,73 @@ long long gateup_rows(int N_each) {
   return rows >= (1LL << 31) / 16 ? -1 : rows;
 }
 
+// ---- paged cache calls ----
+bool rows_ok(int rows, int max_pages) { return rows >= 1 && rows <= W4A16_MAX_SEQUENCES && max_pages >= 1; }
+bool tokens_ok(long long tokens) { return tokens >= 1 && tokens < (1LL << 31) / 16; }
+bool stride_ok(int64_t elements, int elt) { return elements >= 0 && elements * elt % 16 == 0; }
+
+int page_shift_of(int page_rows) {
+  for (int s = 4; s <= 8; ++s)
+    if (page_rows == 1 << s) return s;
+  return -1;
+}
+
+// No two elements of one side share an address: taken by ascending stride,
+// each dimension steps past all that the smaller ones cover.
+bool side_disjoint(int64_t dim, int64_t row, int64_t rows, int64_t head, int64_t heads, int64_t page, int64_t pages,
+                   int64_t layer, int64_t layers) {
+  std::pair<int64_t, int64_t> d[4] = {{row, rows}, {head, heads}, {page, pages}, {layer, layers}};
+  std::sort(d, d + 4);
+  int64_t extent = dim;
+  for (const auto &x : d) {
+    if (x.second == 1) continue;
+    if (x.first < extent || x.first > (int64_t(1) << 60) / x.second) return false;
+    extent += x.first * (x.second - 1);
+  }
+  return true;
+}
+
+// The checked form of a cache, strides in bytes; W4A16_OK or an error code.
+// `values`: the call computes with the values (one layer, and scales for 8 bits); otherwise it moves rows.
+int check_cache(const w4a16_kv_cache *c, bool values, KvCache &out) {
+  if (!c || !c->k || !c->v) return W4A16_ERR_INVALID_ARG;
+  if (c->type != W4A16_KV_BF16 && c->type != W4A16_KV_E4M3) return W4A16_ERR_INVALID_ARG;
+  const bool e4m3 = c->type == W4A16_KV_E4M3;
+  if (values && (e4m3 ? !c->k_scale || !c->v_scale : c->k_scale || c->v_scale)) return W4A16_ERR_INVALID_ARG;
+  if (values && c->layers != 1) return W4A16_ERR_INVALID_ARG;
+  if (c->layers < 1 || c->pages < 1 || c->kv_heads < 1 || c->kv_heads > 1024) return W4A16_ERR_INVALID_ARG;
+  if (c->dim != 64 && c->dim != 128 && c->dim != 256) return W4A16_ERR_INVALID_ARG;
+  const int shift = page_shift_of(c->page_rows);
+  if (shift < 0) return W4A16_ERR_INVALID_ARG;
+  const int elt = e4m3 ? 1 : 2;
+  const int64_t strides[] = {c->k_layer, c->k_page, c->k_head, c->k_row, c->v_layer, c->v_page, c->v_head, c->v_row};
+  for (int64_t s : strides)
+    if (s < 0) return W4A16_ERR_INVALID_ARG;
+  if (!side_disjoint(c->dim, c->k_row, c->page_rows, c->k_head, c->kv_heads, c->k_page, c->pages, c->k_layer, c->layers) ||
+      !side_disjoint(c->dim, c->v_row, c->page_rows, c->v_head, c->kv_heads, c->v_page, c->pages, c->v_layer, c->layers))
+    return W4A16_ERR_INVALID_ARG;
+  for (int64_t s : strides)
+    if (!stride_ok(s, elt)) return W4A16_ERR_MISALIGNED;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+    return W4A16_ERR_MISALIGNED;
+  out.k = KvSide{static_cast<uint8_t *>(c->k), c->k_scale, c->k_layer * elt, c->k_page * elt, c->k_head * elt,
+                 c->k_row * elt};
+  out.v = KvSide{static_cast<uint8_t *>(c->v), c->v_scale, c->v_layer * elt, c->v_page * elt, c->v_head * elt,
+                 c->v_row * elt};
+  out.layers = c->layers;
+  out.pages = c->pages;
+  out.kv_heads = c->kv_heads;
+  out.page_rows = c->page_rows;
+  out.page_shift = shift;
+  out.dim = c->dim;
+  out.e4m3 = e4m3;
+  return W4A16_OK;
+}
+
+bool attn_sizes_ok(int heads, int kv_heads, int dim, int max_tree) {
+  return (dim == 64 || dim == 128 || dim == 256) && kv_heads >= 1 && kv_heads <= 1024 && heads >= kv_heads &&
+         heads <= 65535 && heads % kv_heads == 0 && max_tree >= 1 && max_tree <= W4A16_MAX_TREE;
+}
 
 }  // namespace
 
@@ -450,6 +519,158 @@ int w4a16_dequantize(const void *packed, int N, int K, int group, int sym, float
                                          reinterpret_cast<cudaStream_t>(stream)));
 }
 
+int w4a16_kv_append(const uint16_t *k, const uint16_t *v, int64_t k_token, int64_t k_head_stride, int64_t v_token,
+                    int64_t v_head_stride, const w4a16_kv_cache *cache, const int32_t *page_table, int max_pages,
+                    const int32_t *lengths, const int32_t *starts, int rows, int tokens, w4a16_stream_t stream) {
+  AppendCall c;
+  if (!k || !v || !page_table || !lengths || !starts) return W4A16_ERR_INVALID_ARG;
+  if (!rows_ok(rows, max_pages) || !tokens_ok(tokens)) return W4A16_ERR_INVALID_ARG;
+  int st = check_cache(cache, true, c.cache);
+  if (st != W4A16_OK) return st;
+  const int64_t strides[] = {k_token, k_head_stride, v_token, v_head_stride};
+  for (int64_t s : strides)
+    if (s < 0) return W4A16_ERR_INVALID_ARG;
+  for (int64_t s : strides)
+    if (!stride_ok(s, 2)) return W4A16_ERR_MISALIGNED;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(page_table, 4) || !aligned(lengths, 4) || !aligned(starts, 4))
+    return W4A16_ERR_MISALIGNED;
+  DeviceInfo d;
+  st = current_device(d);
+  if (st != W4A16_OK) return st;
+  c.k = k;
+  c.v = v;
+  c.k_token = k_token;
+  c.k_head = k_head_stride;
+  c.v_token = v_token;
+  c.v_head = v_head_stride;
+  c.rows = KvRows{page_table, lengths, starts, max_pages, rows, tokens};
+  c.err = d.err;
+  c.stream = reinterpret_cast<cudaStream_t>(stream);
+  return finish_launch(launch_kv_append(c));
+}
+
+size_t w4a16_tree_attention_workspace_bytes(int heads, int kv_heads, int dim, int max_tree) {
+  if (!attn_sizes_ok(heads, kv_heads, dim, max_tree)) return 0;
+  return tree_attn_workspace_bytes(heads, kv_heads, dim, max_tree);
+}
+
+int w4a16_tree_attention(const uint16_t *q, int64_t q_token, int64_t q_head, const w4a16_kv_cache *cache,
+                         const int32_t *page_table, int max_pages, const int32_t *lengths, const int32_t *starts,
+                         const int64_t *mask, int rows, int tokens, int heads, int max_tree, float scale,
+                         uint16_t *out, void *workspace, w4a16_stream_t stream) {
+  AttnCall c;
+  if (!q || !page_table || !lengths || !starts || !out || !workspace) return W4A16_ERR_INVALID_ARG;
+  if (!rows_ok(rows, max_pages) || !tokens_ok(tokens)) return W4A16_ERR_INVALID_ARG;
+  int st = check_cache(cache, true, c.cache);
+  if (st != W4A16_OK) return st;
+  if (!attn_sizes_ok(heads, c.cache.kv_heads, c.cache.dim, max_tree)) return W4A16_ERR_INVALID_ARG;
+  if (q_token < 0 || q_head < 0 || !(scale > 0.f) || scale > 1e30f) return W4A16_ERR_INVALID_ARG;
+  if (!stride_ok(q_token, 2) || !stride_ok(q_head, 2)) return W4A16_ERR_MISALIGNED;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256) || !aligned(page_table, 4) ||
+      !aligned(lengths, 4) || !aligned(starts, 4) || !aligned(mask, 8))
+    return W4A16_ERR_MISALIGNED;
+  DeviceInfo d;
+  st = current_device(d);
+  if (st != W4A16_OK) return st;
+  c.q = q;
+  c.q_token = q_token;
+  c.q_head = q_head;
+  c.rows = KvRows{page_table, lengths, starts, max_pages, rows, tokens};
+  c.mask = mask;
+  c.heads = heads;
+  c.max_tree = max_tree;
+  c.scale = scale;
+  c.out = out;
+  c.workspace = workspace;
+  c.err = d.err;
+  c.device = d.device;
+  c.sm_count = d.sm_count;
+  c.stream = reinterpret_cast<cudaStream_t>(stream);
+  return finish_launch(launch_tree_attention(c));
+}
+
+int w4a16_tree_accept(const int64_t *target, const int64_t *draft, const int64_t *mask, const int32_t *starts,
+                      int rows, int tokens, int max_tree, int32_t *path, int32_t *count, int64_t *token,
+                      w4a16_stream_t stream) {
+  if (!target || !draft || !starts || !path || !count || !token) return W4A16_ERR_INVALID_ARG;
+  if (!rows_ok(rows, 1) || !tokens_ok(tokens) || max_tree < 1 || max_tree > W4A16_MAX_TREE)
+    return W4A16_ERR_INVALID_ARG;
+  if (!aligned(target, 8) || !aligned(draft, 8) || !aligned(mask, 8) || !aligned(starts, 4) || !aligned(path, 4) ||
+      !aligned(count, 4) || !aligned(token, 8))
+    return W4A16_ERR_MISALIGNED;
+  DeviceInfo d;
+  int st = current_device(d);
+  if (st != W4A16_OK) return st;
+  return finish_launch(launch_tree_accept(target, draft, mask, starts, rows, tokens, max_tree, path, count, token,
+                                          d.err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int w4a16_kv_compact(const w4a16_kv_cache *cache, const int32_t *page_table, int max_pages, const int32_t *lengths,
+                     const int32_t *path, const int32_t *count, int rows, int max_tree, int32_t *lengths_out,
+                     w4a16_stream_t stream) {
+  KvCache c;
+  if (!page_table || !lengths || !path || !count || !lengths_out) return W4A16_ERR_INVALID_ARG;
+  if (!rows_ok(rows, max_pages) || max_tree < 1 || max_tree > W4A16_MAX_TREE) return W4A16_ERR_INVALID_ARG;
+  if (lengths_out < lengths + rows && lengths < lengths_out + rows) return W4A16_ERR_INVALID_ARG;
+  int st = check_cache(cache, false, c);
+  if (st != W4A16_OK) return st;
+  if (!aligned(page_table, 4) || !aligned(lengths, 4) || !aligned(path, 4) || !aligned(count, 4) ||
+      !aligned(lengths_out, 4))
+    return W4A16_ERR_MISALIGNED;
+  DeviceInfo d;
+  st = current_device(d);
+  if (st != W4A16_OK) return st;
+  return finish_launch(launch_kv_compact(c, KvRows{page_table, lengths, nullptr, max_pages, rows, 0}, path, count,
+                                         max_tree, lengths_out, d.err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int w4a16_kv_free(int32_t *page_table, int max_pages, int table_rows, int32_t *lengths, int32_t *refs, int pages,
+                  const int32_t *rows, int n, w4a16_stream_t stream) {
+  if (!page_table || !lengths || !refs || !rows) return W4A16_ERR_INVALID_ARG;
+  if (max_pages < 1 || table_rows < 1 || pages < 1 || n < 1 || n > W4A16_MAX_ROWS) return W4A16_ERR_INVALID_ARG;
+  if (!aligned(page_table, 4) || !aligned(lengths, 4) || !aligned(refs, 4) || !aligned(rows, 4))
+    return W4A16_ERR_MISALIGNED;
+  DeviceInfo d;
+  int st = current_device(d);
+  if (st != W4A16_OK) return st;
+  return finish_launch(launch_kv_free(TableCall{page_table, lengths, refs, max_pages, table_rows, pages, d.err,
+                                                reinterpret_cast<cudaStream_t>(stream)},
+                                      rows, n));
+}
+
+int w4a16_kv_fork(const w4a16_kv_cache *cache, int32_t *page_table, int max_pages, int table_rows, int32_t *lengths,
+                  int32_t *refs, const int32_t *src, const int32_t *dst, int n, int32_t *ok, w4a16_stream_t stream) {
+  KvCache c;
+  if (!page_table || !lengths || !refs || !src || !dst || !ok) return W4A16_ERR_INVALID_ARG;
+  if (max_pages < 1 || table_rows < 1 || n < 1 || n > W4A16_MAX_ROWS) return W4A16_ERR_INVALID_ARG;
+  int st = check_cache(cache, false, c);
+  if (st != W4A16_OK) return st;
+  if (!aligned(page_table, 4) || !aligned(lengths, 4) || !aligned(refs, 4) || !aligned(src, 4) || !aligned(dst, 4) ||
+      !aligned(ok, 4))
+    return W4A16_ERR_MISALIGNED;
+  DeviceInfo d;
+  st = current_device(d);
+  if (st != W4A16_OK) return st;
+  return finish_launch(launch_kv_fork(TableCall{page_table, lengths, refs, max_pages, table_rows, c.pages, d.err,
+                                                reinterpret_cast<cudaStream_t>(stream)},
+                                      c, src, dst, n, ok));
+}
+
+int w4a16_kv_reserve(int32_t *page_table, int max_pages, int table_rows, int32_t *refs, int pages, int page_rows,
+                     const int32_t *rows, const int32_t *want, int n, int32_t *ok, w4a16_stream_t stream) {
+  const int shift = page_shift_of(page_rows);
+  if (!page_table || !refs || !rows || !want || !ok || shift < 0) return W4A16_ERR_INVALID_ARG;
+  if (max_pages < 1 || table_rows < 1 || pages < 1 || n < 1 || n > W4A16_MAX_ROWS) return W4A16_ERR_INVALID_ARG;
+  if (!aligned(page_table, 4) || !aligned(refs, 4) || !aligned(rows, 4) || !aligned(want, 4) || !aligned(ok, 4))
+    return W4A16_ERR_MISALIGNED;
+  DeviceInfo d;
+  int st = current_device(d);
+  if (st != W4A16_OK) return st;
+  return finish_launch(launch_kv_reserve(TableCall{page_table, nullptr, refs, max_pages, table_rows, pages, d.err,
+                                                   reinterpret_cast<cudaStream_t>(stream)},
+                                         shift, rows, want, n, ok));
+}
+
 int w4a16_kernel_status(void) {
   DeviceInfo d;
   int st = current_device(d);
@@ -461,7 +682,7 @@ int w4a16_kernel_status(void) {
   if (v != 0) {
     const int zero = 0;
     if ((e = cudaMemcpyToSymbol(g_kernel_error, &zero, sizeof(int))) != cudaSuccess) return cuda_fail(e);
-    return W4A16_ERR_TIMEOUT;
+    return v & kErrTimeout ? W4A16_ERR_TIMEOUT : W4A16_ERR_INDEX;
   }
   return W4A16_OK;
 }
@@ -474,6 +695,7 @@ const char *w4a16_strerror(int status) {
     case W4A16_ERR_UNSUPPORTED: return "unsupported device (built for sm_103a)";
     case W4A16_ERR_CUDA: return "CUDA error (see w4a16_last_cuda_error)";
     case W4A16_ERR_TIMEOUT: return "a bounded wait inside a kernel gave up";
+    case W4A16_ERR_INDEX: return "a kernel skipped an index outside its buffers (page id, position, row or offset)";
     default: return "unknown status";
   }
 }

@@ -162,6 +162,7 @@ __device__ __forceinline__ float bf16hi_to_f32(uint32_t v) { return __uint_as_fl
 // Error word written by kernels (bounded waits that gave up).
 // ---------------------------------------------------------------------------
 constexpr int kErrTimeout = 1;
+constexpr int kErrIndex = 2;  // an index outside its buffers was skipped (or-ed in)
 constexpr unsigned long long kWaitLimitNs = 1000000000ull;  // 1 s per wait
 
 __device__ __forceinline__ unsigned long long globaltimer_ns() {

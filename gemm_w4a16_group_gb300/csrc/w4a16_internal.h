@@ -85,4 +85,76 @@ constexpr int kTopkMaxK = 1024;
 cudaError_t launch_topk(const uint16_t *y, int M, int N, int k, int64_t *idx, uint16_t *vals, bool overlap,
                         int device, cudaStream_t stream);
 
+// ---------------------------------------------------------------------------
+// Paged key/value cache (the checked form of w4a16_kv_cache): strides in bytes
+// ---------------------------------------------------------------------------
+struct KvSide {
+  uint8_t *base;
+  const float *scale;  // e4m3: per kv head; else null
+  long long layer, page, head, row;
+};
+struct KvCache {
+  KvSide k, v;
+  int layers, pages, kv_heads, page_rows, page_shift, dim;
+  bool e4m3;
+  int row_bytes() const { return dim * (e4m3 ? 1 : 2); }
+};
+
+// The sequences of a call: table rows of `max_pages` entries, context
+// lengths, and (where there are new tokens) their offsets
+struct KvRows {
+  const int32_t *table;
+  const int32_t *lengths;
+  const int32_t *starts;
+  int max_pages, rows, tokens;
+};
+
+constexpr int kMaxTree = 64;
+constexpr int kMaxRows = 4096;
+
+struct AppendCall {
+  const uint16_t *k, *v;
+  long long k_token, k_head, v_token, v_head;  // elements
+  KvCache cache;
+  KvRows rows;
+  int *err;
+  cudaStream_t stream;
+};
+cudaError_t launch_kv_append(const AppendCall &c);
+
+cudaError_t launch_tree_accept(const int64_t *target, const int64_t *draft, const int64_t *mask, const int32_t *starts,
+                               int rows, int tokens, int max_tree, int32_t *path, int32_t *count, int64_t *token,
+                               int *err, cudaStream_t stream);
+cudaError_t launch_kv_compact(const KvCache &cache, const KvRows &r, const int32_t *path, const int32_t *count,
+                              int max_tree, int32_t *lengths_out, int *err, cudaStream_t stream);
+
+struct TableCall {
+  int32_t *table, *lengths, *refs;
+  int max_pages, table_rows, pages;
+  int *err;
+  cudaStream_t stream;
+};
+cudaError_t launch_kv_free(const TableCall &t, const int32_t *rows, int n);
+cudaError_t launch_kv_fork(const TableCall &t, const KvCache &cache, const int32_t *src, const int32_t *dst, int n,
+                           int32_t *ok);
+cudaError_t launch_kv_reserve(const TableCall &t, int page_shift, const int32_t *rows, const int32_t *want, int n,
+                              int32_t *ok);
+
+struct AttnCall {
+  const uint16_t *q;
+  long long q_token, q_head;  // elements
+  KvCache cache;
+  KvRows rows;
+  const int64_t *mask;  // or null: the new tokens up to the row's own
+  int heads, max_tree;
+  float scale;
+  uint16_t *out;
+  void *workspace;
+  int *err;
+  int device, sm_count;
+  cudaStream_t stream;
+};
+size_t tree_attn_workspace_bytes(int heads, int kv_heads, int dim, int max_tree);
+cudaError_t launch_tree_attention(const AttnCall &c);
+
 }  // namespace w4a16

@@ -67,6 +67,7 @@ typedef struct CUstream_st *w4a16_stream_t;
 #define W4A16_ERR_UNSUPPORTED (-3)  /* the current device is not an sm_103 GPU */
 #define W4A16_ERR_CUDA (-4)         /* a CUDA call failed; see w4a16_last_cuda_error() */
 #define W4A16_ERR_TIMEOUT (-5)      /* a bounded wait inside a kernel gave up */
+#define W4A16_ERR_INDEX (-6)        /* a kernel met an index outside its buffers and skipped it */
 
 /* Weight forms (the `sym` argument). */
 #define W4A16_ZERO_POINTS 0
@@ -323,11 +324,161 @@ int w4a16_gemm_affine_bits(const uint16_t *x, void *scratch, const void *packed,
 int w4a16_dequantize_affine_bits(const void *packed, int N, int K, int group, int bits, float *w_out,
                                  w4a16_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Attention of drafted tokens over a paged key/value cache, and the cache
+ * itself. These calls are the rest of a speculative verify step around the
+ * products above (2-16 drafted rows checked at once: GRIMOIRE v1.8 release
+ * notes, "INT4 verify faster"; the greedy pick on the GPU: lucebox PR #823).
+ *
+ * One step: w4a16_kv_reserve gives every sequence room, w4a16_kv_append
+ * writes the drafted tokens' keys and values behind each context (per layer),
+ * w4a16_tree_attention attends (per layer), the head's w4a16_gemm_argmax
+ * picks a token for every node, w4a16_tree_accept walks down the tree, and
+ * w4a16_kv_compact moves the accepted rows together and advances the lengths.
+ *
+ * Arrays, all device memory:
+ *   page_table  int32 [rows][max_pages]  page ids of row b's context in order;
+ *               entries past the pages a row holds are -1
+ *   lengths     int32 [rows]             cached tokens of each row
+ *   starts      int32 [rows + 1]         tokens starts[b] .. starts[b+1] - 1 are
+ *               row b's new tokens; starts[0] = 0, ascending. Tokens at
+ *               starts[rows] and above are padding: not read, not written
+ *   mask        int64 [tokens]           bit j of a token's word: it attends to
+ *               new token j of its row (itself included: its own bit). Bits at
+ *               the row's number of new tokens and above are ignored
+ *   refs        int32 [pages]            how many rows hold each page; 0 = free
+ * New token i of row b has position lengths[b] + i; position p is row
+ * p % page_rows of page page_table[b][p / page_rows].
+ *
+ * What only the device can see is checked there: a page id outside the
+ * cache, a position past the table, starts that descend or exceed max_tree,
+ * a row index outside the table. Nothing outside a buffer is touched; the
+ * offending key, row or sequence is skipped and w4a16_kernel_status()
+ * returns W4A16_ERR_INDEX.
+ * ------------------------------------------------------------------------ */
+
+/* Element types of a cache. */
+#define W4A16_KV_BF16 0
+#define W4A16_KV_E4M3 1 /* value = code * scale[kv head] */
+
+/*
+ * A paged cache. Element (layer, page, head, row, d) of the keys sits at
+ * k + layer * k_layer + page * k_page + head * k_head + row * k_row + d, in
+ * elements; the values likewise. Every stride and both bases are multiples
+ * of 16 bytes. dim 64, 128 or 256; page_rows 16, 32, 64, 128 or 256. Calls on
+ * one layer (append, attention) take layers = 1. Pages and layers must not
+ * overlap.
+ */
+typedef struct w4a16_kv_cache {
+  void *k, *v;
+  const float *k_scale, *v_scale; /* W4A16_KV_E4M3: float32 [kv_heads], positive; else NULL (calls that only move rows: not read) */
+  int64_t k_layer, k_page, k_head, k_row;
+  int64_t v_layer, v_page, v_head, v_row;
+  int32_t layers, pages, kv_heads, page_rows, dim, type;
+} w4a16_kv_cache;
+
+/* Most new tokens of a sequence in one attention or acceptance call (bits of
+ * a mask word), and most rows one fork, free or reserve call may name. */
+#define W4A16_MAX_TREE 64
+#define W4A16_MAX_ROWS 4096
+#define W4A16_MAX_SEQUENCES 65535 /* rows of one append, attention, acceptance or compaction */
+
+/*
+ * Writes the new tokens' keys and values (bf16 [tokens][kv_heads][dim];
+ * element (t, h, d) at t * k_token + h * k_head_stride + d, strides multiples
+ * of 8 elements, bases 16-byte aligned) into their pages. bf16 caches: moved
+ * bit by bit. E4M3 caches: x / scale[head] in float32, rounded to the nearest
+ * code (ties to even) and saturated at +-448; NaN stays NaN. Any number of
+ * new tokens per row, so prompts too.
+ */
+int w4a16_kv_append(const uint16_t *k, const uint16_t *v, int64_t k_token, int64_t k_head_stride, int64_t v_token,
+                    int64_t v_head_stride, const w4a16_kv_cache *cache, const int32_t *page_table, int max_pages,
+                    const int32_t *lengths, const int32_t *starts, int rows, int tokens, w4a16_stream_t stream);
+
+/*
+ * out[t][h] (bf16 [tokens][heads][dim], row-major) = softmax(q . K^T * scale) . V
+ * over the positions token t sees: all lengths[b] cached ones, and new token
+ * j where bit j of mask[t] is set (mask NULL: the new tokens up to and
+ * including t). Query head h reads kv head h / (heads / kv_heads). A token
+ * that sees nothing gets 0. Keys and values at positions a token does not see
+ * do not touch its result, whatever they hold. The new tokens' keys and
+ * values are read from the cache (w4a16_kv_append first).
+ *
+ *   q          element (t, h, d) at t * q_token + h * q_head + d, strides
+ *              multiples of 8 elements, base 16-byte aligned
+ *   max_tree   1 .. W4A16_MAX_TREE, at least every row's number of new tokens
+ *   workspace  w4a16_tree_attention_workspace_bytes(heads, kv_heads, dim,
+ *              max_tree) bytes, 256-byte aligned, used only while the call
+ *              runs on `stream`; no content is kept or expected
+ *
+ * Scores, softmax statistics and sums are float32. Results are bitwise
+ * reproducible run to run on one device.
+ */
+size_t w4a16_tree_attention_workspace_bytes(int heads, int kv_heads, int dim, int max_tree);
+int w4a16_tree_attention(const uint16_t *q, int64_t q_token, int64_t q_head, const w4a16_kv_cache *cache,
+                         const int32_t *page_table, int max_pages, const int32_t *lengths, const int32_t *starts,
+                         const int64_t *mask, int rows, int tokens, int heads, int max_tree, float scale,
+                         uint16_t *out, void *workspace, w4a16_stream_t stream);
+
+/*
+ * Greedy acceptance. target[t] is the model's pick after token t
+ * (w4a16_gemm_argmax), draft[t] the drafted token at node t, mask as above
+ * with ancestors at lower indices: a node's parent is its highest set bit
+ * below its own. From node 0 (always accepted: the step's last committed
+ * token) the walk goes to the lowest child whose draft equals the target of
+ * the node it stands on, until there is none.
+ *   path   int32 [rows][max_tree]  accepted nodes in order, then -1
+ *   count  int32 [rows]            how many (0 for a row without new tokens)
+ *   token  int64 [rows]            the target of the last one (-1 without)
+ * mask NULL: one chain, node i's parent is i - 1.
+ */
+int w4a16_tree_accept(const int64_t *target, const int64_t *draft, const int64_t *mask, const int32_t *starts,
+                      int rows, int tokens, int max_tree, int32_t *path, int32_t *count, int64_t *token,
+                      w4a16_stream_t stream);
+
+/*
+ * Keeps the accepted rows: in every layer and head, position lengths[b] +
+ * path[b][i] moves to lengths[b] + i for i < count[b], and lengths_out[b] =
+ * lengths[b] + count[b]. path[b] ascends (as w4a16_tree_accept gives it).
+ * lengths_out must not overlap lengths.
+ */
+int w4a16_kv_compact(const w4a16_kv_cache *cache, const int32_t *page_table, int max_pages, const int32_t *lengths,
+                     const int32_t *path, const int32_t *count, int rows, int max_tree, int32_t *lengths_out,
+                     w4a16_stream_t stream);
+
+/*
+ * Drops the `n` table rows rows[0 .. n-1] (distinct): one reference of every
+ * page they hold, their table entries become -1 and their lengths 0.
+ */
+int w4a16_kv_free(int32_t *page_table, int max_pages, int table_rows, int32_t *lengths, int32_t *refs, int pages,
+                  const int32_t *rows, int n, w4a16_stream_t stream);
+
+/*
+ * Branches: for each j < n, the empty table row dst[j] becomes a copy of row
+ * src[j]. Whole pages are shared (one more reference); a part-filled last
+ * page is copied, in every layer, into a free page of its own (only the rows
+ * in use). dst are distinct and empty (freed, or never used); a src may be named many times. Free
+ * pages are taken lowest id first, in the order of j. All or nothing: ok[0] =
+ * 1, or 0 and nothing changed when the free pages do not suffice (or an index
+ * is bad: then W4A16_ERR_INDEX too). Pages that a src holds past its length
+ * (w4a16_kv_reserve) are not shared.
+ */
+int w4a16_kv_fork(const w4a16_kv_cache *cache, int32_t *page_table, int max_pages, int table_rows, int32_t *lengths,
+                  int32_t *refs, const int32_t *src, const int32_t *dst, int n, int32_t *ok, w4a16_stream_t stream);
+
+/*
+ * Room to grow: row rows[j] (distinct) gets free pages, lowest id first in
+ * the order of j, until it holds want[j] tokens. All or nothing, as above.
+ */
+int w4a16_kv_reserve(int32_t *page_table, int max_pages, int table_rows, int32_t *refs, int pages, int page_rows,
+                     const int32_t *rows, const int32_t *want, int n, int32_t *ok, w4a16_stream_t stream);
+
 /*
  * Waits for all work on the current device, then reads and clears the
  * device error word that a kernel sets when one of its bounded waits gave up
- * (W4A16_ERR_TIMEOUT; the kernel's outputs are then undefined). W4A16_OK
- * when no kernel gave up since the last call.
+ * (W4A16_ERR_TIMEOUT; the kernel's outputs are then undefined) or when one
+ * of the cache calls skipped an index outside its buffers (W4A16_ERR_INDEX).
+ * W4A16_OK when neither happened since the last call.
  */
 int w4a16_kernel_status(void);
 
