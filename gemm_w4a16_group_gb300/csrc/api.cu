@@ -564,6 +564,7 @@ int w4a16_tree_attention(const uint16_t *q, int64_t q_token, int64_t q_head, con
   int st = check_cache(cache, true, c.cache);
   if (st != W4A16_OK) return st;
   if (!attn_sizes_ok(heads, c.cache.kv_heads, c.cache.dim, max_tree)) return W4A16_ERR_INVALID_ARG;
+  if ((long long)tokens * heads >= 1LL << 31) return W4A16_ERR_INVALID_ARG;
   if (q_token < 0 || q_head < 0 || !(scale > 0.f) || scale > 1e30f) return W4A16_ERR_INVALID_ARG;
   if (!stride_ok(q_token, 2) || !stride_ok(q_head, 2)) return W4A16_ERR_MISALIGNED;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256) || !aligned(page_table, 4) ||

@@ -3,129 +3,837 @@
 //   s_j = scale * q . k_j,  out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m)
 //
 // over the positions j that the token sees (its row's context and, by its
-// mask word, the row's new tokens). One pass: a running maximum m and sum, the
-// sums rescaled when m grows.
+// mask word, the row's new tokens). One pass over the keys with a running
+// maximum m and sum; the sums are rescaled when m grows.
+//
+// This file: the kernel on mma.sync (m16n8k16), for up to 64 query rows per
+// kv head at a time, and the kernel that joins partial results. A decode step
+// has G to 16 * G query rows against the whole cache, so it is bound by HBM:
+// every key and value is read once per tile of 16, 32 or 64 rows.
+//
+//  * 4 computing warps and a copying warp. A stage is 64 keys: the copying
+//    warp's lanes each fetch one box (up to 64 rows of a page by 128 bytes) of
+//    keys or values by TMA, swizzled as ldmatrix wants it.
+//  * RW warps side by side take 16 query rows each; the 4 / RW warps of one
+//    such group take every (4 / RW)-th run of 64 / (4 / RW) keys of a stage,
+//    and meet at the end of an item. With one row tile no key is multiplied
+//    twice, and with four every warp sees all keys.
+//  * bf16 caches: products of bf16 are exact in float32; the weights e^(s - m)
+//    go into the second product as two bf16 parts (hi + lo, 16 bits of
+//    mantissa), which the tensor cores have time for.
+//  * e4m3 caches: codes become f16 exactly (one conversion per pair), q is
+//    scaled by a power of two per row so that its largest element is near 2^14
+//    and becomes f16 (elements below 2^-24 of the largest lose bits, no more
+//    than float32 sums lose anyway), and the weights, times 2^8, are f16 with
+//    11 bits.
+//  * Only tiles that hold new tokens or the end of the context take the masked
+//    path. There, values that are not finite are zeroed in shared memory
+//    before the product (0 * NaN is NaN) and added at the end to the rows that
+//    see them.
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
-#include "w4a16_internal.h"
+#include <algorithm>
+
+#include "tree_attn.cuh"
 
 namespace w4a16 {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kKt = 64;  // keys of a stage
+constexpr int kComputeWarps = 4;
+constexpr int kThreads = (kComputeWarps + 1) * 32;
+constexpr int kMinTiles = 2;
 
-struct SimpleParams {
-  const uint16_t *q;
-  long long q_token, q_head;
-  KvCache c;
-  KvRows r;
-  const int64_t *mask;
-  int heads, group, max_tree;
-  float scale;
-  uint16_t *out;
-  int *err;
+template <int DIM, bool E4M3, int RWT>
+struct RowsGeo {
+  static constexpr int RW = RWT, KW = kComputeWarps / RWT;
+  static constexpr int ROWS = 16 * RW;
+  static constexpr int KPW = kKt / KW;         // keys of a warp per stage
+  static constexpr int ELT = E4M3 ? 1 : 2;
+  static constexpr int ROWB = DIM * ELT;       // bytes of a cache row
+  static constexpr int CW = ROWB < 128 ? ROWB : 128;  // box width
+  static constexpr int CH = ROWB / CW;
+  static constexpr int SUB = kKt * CW;         // one box column of a stage
+  static constexpr int SIDE = CH * SUB;
+  static constexpr int STAGE = 2 * SIDE;
+  static constexpr int CTAS = DIM == 256 ? 1 : 2;  // per SM
+  static constexpr int STAGES = (DIM == 256 ? 192 : 96) * 1024 / STAGE;
+  static constexpr int KS = DIM / 16;          // k steps of the first product
+  static constexpr int NT = KPW / 8;           // 8-key tiles of a warp
+  static constexpr int OT = DIM / 8;           // 8-wide output tiles
+  static constexpr int Q_BYTES = ROWS * DIM * 2;
+  static constexpr int RED_BYTES = KW > 1 ? RW * 16 * DIM * 4 / (RW > 1 ? 2 : 1) : 0;
+  static constexpr int OFF_Q = STAGES * STAGE;  // q fragments; then the sums that warps exchange
+  static constexpr int OFF_ML = OFF_Q + (Q_BYTES > RED_BYTES ? Q_BYTES : RED_BYTES);
+  static constexpr int OFF_QS = OFF_ML + (KW > 1 ? KW * ROWS * 8 : 0);
+  static constexpr int OFF_BAR = OFF_QS + (E4M3 ? ROWS * 4 : 0);
+  static constexpr int OFF_INFO = OFF_BAR + 2 * STAGES * 8;
+  static constexpr int OFF_MISC = OFF_INFO + STAGES * 4;
+  static constexpr int OFF_PLAN = (OFF_MISC + 16 + 15) / 16 * 16;
+  static constexpr int SMEM = OFF_PLAN + (int)sizeof(PlanShared);
+  static_assert(CTAS * (SMEM + 1024) <= 228 * 1024 && SMEM <= 227 * 1024, "shared memory budget");
+  static_assert(STAGES >= 3 && SUB % 512 == 0, "stages");
 };
 
-template <bool E4M3, int N>
-__device__ __forceinline__ void load_row(const uint8_t *p, float (&x)[N]) {
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// the two e4m3 codes in the low half of x as f16x2 (exact)
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t x) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x & 0xFFFFu), __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t *>(&b);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t *>(&h);
+}
+
+// the 16-bit or 8-bit elements of x that are not finite, as a byte mask
+template <bool E4M3>
+__device__ __forceinline__ uint32_t not_finite(uint32_t x) {
+  uint32_t m = 0;
+  if (E4M3) {
 #pragma unroll
-  for (int i = 0; i < N; i += 2) {
-    if (E4M3) {
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(*reinterpret_cast<const uint16_t *>(p + i), __NV_E4M3);
-      x[i] = __half2float(__half(__half_raw{h.x}));
-      x[i + 1] = __half2float(__half(__half_raw{h.y}));
-    } else {
-      const uint32_t w = *reinterpret_cast<const uint32_t *>(p + 2 * i);
-      x[i] = bf16lo_to_f32(w);
-      x[i + 1] = bf16hi_to_f32(w);
+    for (int i = 0; i < 4; ++i)
+      if (((x >> (8 * i)) & 0x7Fu) == 0x7Fu) m |= 0xFFu << (8 * i);
+  } else {
+    if ((x & 0x7F80u) == 0x7F80u) m |= 0xFFFFu;
+    if ((x & 0x7F800000u) == 0x7F800000u) m |= 0xFFFF0000u;
+  }
+  return m;
+}
+
+__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// byte offset of 16-byte chunk `c` of row `row` in a box column
+template <int CW>
+__device__ __forceinline__ uint32_t swz(uint32_t row, uint32_t c) {
+  return row * CW + ((c ^ (CW == 128 ? row & 7u : (row >> 1) & 3u)) << 4);
+}
+
+// value element d of position `pos`, 0 where there is none
+template <bool E4M3>
+__device__ float value_at(const AttnParams &p, int b, int head, long long pos, int d) {
+  const long long pi = pos >> p.c.page_shift;
+  if (pi >= p.r.max_pages) return 0.f;
+  const int id = p.r.table[(long long)b * p.r.max_pages + pi];
+  if ((unsigned)id >= (unsigned)p.c.pages) return 0.f;
+  const uint8_t *a = p.c.v.base + (long long)id * p.c.v.page + (long long)head * p.c.v.head +
+                     (pos & (p.c.page_rows - 1)) * p.c.v.row;
+  if (E4M3) return __half2float(__half(__nv_cvt_fp8_to_halfraw(a[d], __NV_E4M3)));
+  return __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(a)[d] << 16);
+}
+
+template <int DIM, bool E4M3, int RWT>
+__global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
+    rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                const __grid_constant__ AttnParams p) {
+  using G = RowsGeo<DIM, E4M3, RWT>;
+  constexpr int RW = G::RW, KW = G::KW, NT = G::NT, OT = G::OT, KS = G::KS;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + G::OFF_MISC);
+  uint32_t *odd_values = reinterpret_cast<uint32_t *>(smem + G::OFF_MISC + 8);  // new tokens with values not finite
+  PlanShared &plan = *reinterpret_cast<PlanShared *>(smem + G::OFF_PLAN);
+  if (sbase & 1023u) {  // the swizzle counts from multiples of 1,024 (dynamic shared memory starts at one)
+    if (tid == 0) atomicOr(p.err, kErrTimeout);
+    return;
+  }
+  auto full = [&](uint32_t s) { return sbase + G::OFF_BAR + 8 * s; };
+  auto empty = [&](uint32_t s) { return sbase + G::OFF_BAR + 8 * (G::STAGES + s); };
+
+  if (tid == 0) {
+    for (int i = 0; i < G::STAGES; ++i) {
+      mbar_init(full(i), 1);
+      mbar_init(empty(i), kComputeWarps);
     }
+    *abort_flag = 0;
+    odd_values[0] = odd_values[1] = 0;
+    fence_mbar_init();
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();
+  plan_share<G::ROWS, kKt, kThreads>(p, plan, kMinTiles);
+  __syncthreads();
+  Cursor cur{plan.at, plan.end, plan.b, plan.head, plan.rt, plan.kt};
+  Segment sg;
+
+  if (warp == kComputeWarps) {
+    // ------------------------------------------------------------ copies
+    const int br = min(p.c.page_rows, kKt), parts = kKt / br;
+    const int part = lane % parts, col = lane / parts % G::CH, side = lane / parts / G::CH;
+    const bool has_box = side < 2;
+    uint64_t pol;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    uint32_t st = 0;
+    bool ok = true;
+    while (ok && next_segment<G::ROWS, kKt>(p, cur, sg)) {
+      const int32_t *ids = p.r.table + (long long)sg.b * p.r.max_pages;
+      auto id_of = [&](int kt) {  // -1: past the keys
+        const long long key = (long long)kt * kKt + part * br;
+        return kt < sg.kt1 && key < sg.i.keys ? ids[key >> p.c.page_shift] : -1;
+      };
+      int next = id_of(sg.kt0);
+      for (int kt = sg.kt0; kt < sg.kt1; ++kt, ++st) {
+        const int id = next;
+        next = id_of(kt + 1);
+        const uint32_t s = st % G::STAGES;
+        ok = mbar_wait(empty(s), ((st / G::STAGES) & 1) ^ 1, abort_flag);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        const int key = kt * kKt + part * br;
+        const bool valid = (unsigned)id < (unsigned)p.c.pages;
+        const bool load = has_box && valid;
+        if (has_box && !valid && key < sg.i.keys && side == 0 && col == 0) attn_flag(p.err);
+        const uint32_t loads = __ballot_sync(0xFFFFFFFFu, load);
+        if (lane == 0) {
+          // which 16-key groups are there: those of the parts that load
+          uint32_t groups = 0;
+          for (int i = 0; i < parts; ++i)
+            if (loads >> i & 1) groups |= ((1u << (br / 16)) - 1) << (i * br / 16);
+          *reinterpret_cast<volatile uint32_t *>(smem + G::OFF_INFO + 4 * s) = groups;
+          mbar_arrive_expect_tx(full(s), __popc(loads) * br * G::CW);
+        }
+        __syncwarp();
+        if (load)
+          tma_load_4d(sbase + s * G::STAGE + side * G::SIDE + col * G::SUB + part * br * G::CW, side ? &tm_v : &tm_k,
+                      col * (G::CW / G::ELT), key & (p.c.page_rows - 1), sg.head, id, full(s), pol);
+        __syncwarp();
+      }
+    }
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      atomicOr(p.err, kErrTimeout);
+      // every copy issued lands before the CTA can exit
+      for (uint32_t i = 0; i < (uint32_t)G::STAGES && i < st; ++i) {
+        const uint32_t u = st - 1 - i;
+        mbar_wait_drain(full(u % G::STAGES), (u / G::STAGES) & 1);
+      }
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- products
+  const int rw = warp % RW, kw = warp / RW;
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t qaddr = sbase + G::OFF_Q + rw * (KS * 512) + lane * 16;
+  float *ml = reinterpret_cast<float *>(smem + G::OFF_ML);
+  float *qscale = reinterpret_cast<float *>(smem + G::OFF_QS);
+  uint32_t st = 0;
+  bool ok = true;  // after a wait that gave up: no more waits, but every barrier below is still met
+
+  while (next_segment<G::ROWS, kKt>(p, cur, sg)) {
+    const int rows = min(G::ROWS, sg.i.n * p.group - sg.rt * G::ROWS);
+    // ---- q in the order of the A fragments (16 bytes per lane and k step)
+    compute_sync();  // the last item's exchange is over
+    if (E4M3) {
+      // one row per 8 threads: its largest exponent, as the power of two that takes it to 2^14
+      for (int r = tid >> 3; r < G::ROWS; r += kComputeWarps * 4) {
+        const int rr = sg.rt * G::ROWS + r;
+        uint32_t top = 0;
+        if (r < rows) {
+          const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (sg.i.start + rr / p.group) * p.q_token +
+                                                             (sg.head * p.group + rr % p.group) * p.q_head);
+          for (int i = tid & 7; i < DIM / 8; i += 8) {
+            const uint4 x = src[i];
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max((w[e] >> 7) & 0xFFu, (w[e] >> 23) & 0xFFu));
+          }
+        }
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        // 2^(14 - (top - 127)), within float32's exponents; a row that is not finite stays as it is
+        const int e = top == 0xFFu ? 0 : min(141 - (int)top, 120);
+        if ((tid & 7) == 0) qscale[r] = __uint_as_float((uint32_t)(127 + e) << 23);
+      }
+      compute_sync();
+    }
+    for (int i = tid; i < G::ROWS * (DIM / 8); i += kComputeWarps * 32) {
+      const int r = i / (DIM / 8), c8 = i % (DIM / 8);  // 8 elements from 8 * c8
+      const int rr = sg.rt * G::ROWS + r;
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (r < rows)
+        x = *reinterpret_cast<const uint4 *>(p.q + (sg.i.start + rr / p.group) * p.q_token +
+                                             (sg.head * p.group + rr % p.group) * p.q_head + 8 * c8);
+      uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      const int step = c8 >> 1, half = c8 & 1, hi = (r >> 3) & 1;
+      const uint32_t base = sbase + G::OFF_Q + (r >> 4) * (KS * 512) + step * 512 + (r & 7) * 64;
+      if (E4M3) {
+        const float f = qscale[r];
+        // a lane's four k of a step are d = 4t .. 4t + 3, as four codes of a key come
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t y = pack_f16(bf16lo_to_f32(w[e]) * f, bf16hi_to_f32(w[e]) * f);
+          const int tt = half * 2 + (e >> 1);
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + tt * 16 + (hi + 2 * (e & 1)) * 4), "r"(y) : "memory");
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + e * 16 + (hi + 2 * half) * 4), "r"(w[e]) : "memory");
+      }
+    }
+    // this thread's two rows (g and g + 8 of the warp's 16): mask word, score factor
+    unsigned long long word[2];
+    float factor[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = rw * 16 + g + 8 * i;
+      const int tok = (sg.rt * G::ROWS + r) / p.group;
+      word[i] = 0;
+      if (r < rows) word[i] = p.mask ? (unsigned long long)p.mask[sg.i.start + tok] : (2ull << tok) - 1;
+      factor[i] = p.scale_log2;
+    }
+    if (tid < 2) odd_values[tid] = 0;
+    compute_sync();
+    if (E4M3) {
+      const float ks = p.c.k.scale[sg.head];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) factor[i] = p.scale_log2 * ks / qscale[rw * 16 + g + 8 * i];
+    }
+    constexpr bool QREG = KS <= 8;
+    uint32_t qf[QREG ? KS : 1][4];
+    if (QREG) {
+#pragma unroll
+      for (int c = 0; c < KS; ++c) {
+        const uint4 x = lds128(qaddr + c * 512);
+        qf[QREG ? c : 0][0] = x.x;
+        qf[QREG ? c : 0][1] = x.y;
+        qf[QREG ? c : 0][2] = x.z;
+        qf[QREG ? c : 0][3] = x.w;
+      }
+    }
+    float o[OT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float lsum[4] = {0.f, 0.f, 0.f, 0.f};  // 8 bits: the sums of the weights as they were rounded, by one more product
+#pragma unroll
+    for (int i = 0; i < OT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+    for (int kt = sg.kt0; kt < sg.kt1; ++kt, ++st) {
+      const uint32_t stage = st % G::STAGES;
+      if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait<true>(full(stage), (st / G::STAGES) & 1, abort_flag));
+      const uint32_t groups = *reinterpret_cast<volatile uint32_t *>(smem + G::OFF_INFO + 4 * stage);
+      const uint32_t kbase = sbase + stage * G::STAGE, vbase = kbase + G::SIDE;
+      const int key0 = kt * kKt;
+      const bool masked = key0 + kKt > sg.i.len || groups != 0xFu;
+      if (masked) {
+        // Values that must not meet a weight of 0, in the rows that this warp will read. Warps that share rows
+        // write the same to them, so no barrier is needed.
+        for (int i = lane; i < G::KPW * (G::ROWB / 16); i += 32) {
+          const int j = kw * G::KPW + i / (G::ROWB / 16), c = i % (G::ROWB / 16);
+          const int key = key0 + j;
+          const bool there = key < sg.i.keys && (groups >> (j >> 4) & 1);
+          if (there && key < sg.i.len) continue;
+          const uint32_t a = vbase + (c / (G::CW / 16)) * G::SUB + swz<G::CW>(j, c % (G::CW / 16));
+          uint4 x = make_uint4(0, 0, 0, 0);
+          bool clean = false;
+          if (there) {
+            x = lds128(a);
+            const uint32_t b0 = not_finite<E4M3>(x.x), b1 = not_finite<E4M3>(x.y), b2 = not_finite<E4M3>(x.z),
+                           b3 = not_finite<E4M3>(x.w);
+            clean = !(b0 | b1 | b2 | b3);
+            if (!clean) {
+              x = make_uint4(x.x & ~b0, x.y & ~b1, x.z & ~b2, x.w & ~b3);
+              const int n = key - sg.i.len;
+              atomicOr(&odd_values[n >> 5], 1u << (n & 31));
+            }
+          }
+          if (!clean) sts128(a, x);
+        }
+        __syncwarp();
+      }
+      // ---- scores of the warp's keys
+      float s[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+      const uint32_t krow = kw * G::KPW + (lane & 7);
+      if constexpr (E4M3) {
+        // one ldmatrix: 8 keys by 64 codes, 4 k steps
+#pragma unroll
+        for (int cc = 0; cc < DIM / 64; ++cc) {
+          uint32_t a[4][4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            if constexpr (QREG) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) a[u][e] = qf[cc * 4 + u][e];
+            } else {
+              const uint4 x = lds128(qaddr + (cc * 4 + u) * 512);
+              a[u][0] = x.x; a[u][1] = x.y; a[u][2] = x.z; a[u][3] = x.w;
+            }
+          }
+          const uint32_t ch = cc * 4 + (lane >> 3);
+          const uint32_t colb = kbase + (ch / (G::CW / 16)) * G::SUB;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            uint32_t b[4];
+            ldsm4(colb + swz<G::CW>(krow + n * 8, ch % (G::CW / 16)), b);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) mma16816<true>(s[n], a[u], e4m3x2_f16x2(b[u]), e4m3x2_f16x2(b[u] >> 16));
+          }
+        }
+      } else {
+        // one ldmatrix: 8 keys by 32 elements, 2 k steps
+#pragma unroll
+        for (int cc = 0; cc < DIM / 32; ++cc) {
+          uint32_t a[2][4];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if constexpr (QREG) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) a[u][e] = qf[cc * 2 + u][e];
+            } else {
+              const uint4 x = lds128(qaddr + (cc * 2 + u) * 512);
+              a[u][0] = x.x; a[u][1] = x.y; a[u][2] = x.z; a[u][3] = x.w;
+            }
+          }
+          const uint32_t ch = cc * 4 + (lane >> 3);
+          const uint32_t colb = kbase + (ch >> 3) * G::SUB;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            uint32_t b[4];
+            ldsm4(colb + swz<128>(krow + n * 8, ch & 7), b);
+            mma16816<false>(s[n], a[0], b[0], b[1]);
+            mma16816<false>(s[n], a[1], b[2], b[3]);
+          }
+        }
+      }
+      // ---- softmax
+      if (masked) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = kw * G::KPW + n * 8 + 2 * t + (e & 1), key = key0 + j, nw = key - sg.i.len;
+            const bool sees = (groups >> (j >> 4) & 1) && key < sg.i.keys && (nw < 0 || (word[e >> 1] >> nw & 1));
+            if (!sees) s[n][e] = -INFINITY;
+          }
+      }
+      float base[2], alpha[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) top = fmaxf(top, fmaxf(s[n][2 * i], s[n][2 * i + 1]));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        const float mn = fmaxf(m[i], top * factor[i]);
+        base[i] = mn == -INFINITY ? 0.f : mn;
+        alpha[i] = exp2_approx(m[i] - base[i]);
+        m[i] = mn;
+        if (E4M3) base[i] -= 8.f;  // weights times 2^8: f16 keeps small ones better
+        l[i] *= alpha[i];
+        lsum[2 * i] *= alpha[i];
+      }
+      if (__any_sync(0xFFFFFFFFu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+        for (int i = 0; i < OT; ++i) {
+          o[i][0] *= alpha[0];
+          o[i][1] *= alpha[0];
+          o[i][2] *= alpha[1];
+          o[i][3] *= alpha[1];
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = exp2_approx(fmaf(s[n][e], factor[e >> 1], -base[e >> 1]));
+        if (!E4M3) {
+          l[0] += s[n][0] + s[n][1];
+          l[1] += s[n][2] + s[n][3];
+        }
+      }
+      // ---- weights . values, 16 keys at a time
+      const uint32_t vrow = kw * G::KPW + (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+      for (int n = 0; n < NT; n += 2) {
+        if constexpr (E4M3) {
+          const uint32_t a[4] = {pack_f16(s[n][0], s[n][1]), pack_f16(s[n][2], s[n][3]),
+                                 pack_f16(s[n + 1][0], s[n + 1][1]), pack_f16(s[n + 1][2], s[n + 1][3])};
+          mma16816<true>(lsum, a, 0x3C003C00u, 0x3C003C00u);
+          // 16 keys by 32 codes; a register holds two codes of each of two keys: element 2u and 2u + 1 of a run of
+          // 16, which go to two output tiles
+#pragma unroll
+          for (int cc = 0; cc < DIM / 32; ++cc) {
+            const uint32_t ch = cc * 2 + (lane >> 4);
+            uint32_t b[4];
+            ldsm4t(vbase + (ch / (G::CW / 16)) * G::SUB + swz<G::CW>(vrow + n * 8, ch % (G::CW / 16)), b);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t x0 = __byte_perm(b[2 * u], 0, 0x3120), x1 = __byte_perm(b[2 * u + 1], 0, 0x3120);
+              mma16816<true>(o[cc * 4 + 2 * u], a, e4m3x2_f16x2(x0), e4m3x2_f16x2(x1));
+              mma16816<true>(o[cc * 4 + 2 * u + 1], a, e4m3x2_f16x2(x0 >> 16), e4m3x2_f16x2(x1 >> 16));
+            }
+          }
+        } else {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float x = s[n + (u >> 1)][2 * (u & 1)], y = s[n + (u >> 1)][2 * (u & 1) + 1];
+            hi[u] = pack_bf16(x, y);
+            lo[u] = pack_bf16(x - bf16lo_to_f32(hi[u]), y - bf16hi_to_f32(hi[u]));
+          }
+#pragma unroll
+          for (int cc = 0; cc < DIM / 16; ++cc) {
+            const uint32_t ch = cc * 2 + (lane >> 4);
+            uint32_t b[4];
+            ldsm4t(vbase + (ch >> 3) * G::SUB + swz<128>(vrow + n * 8, ch & 7), b);
+            mma16816<false>(o[2 * cc], hi, b[0], b[1]);
+            mma16816<false>(o[2 * cc + 1], hi, b[2], b[3]);
+            mma16816<false>(o[2 * cc], lo, b[0], b[1]);
+            mma16816<false>(o[2 * cc + 1], lo, b[2], b[3]);
+          }
+        }
+      }
+      if (masked) fence_proxy_async_smem();  // zeroed values, before the next copy into this stage
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(stage));
+    }
+
+    // ---- the item's sums: over the quad, then over the warps that shared its keys
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
+      if (E4M3) l[i] = lsum[2 * i];
+    }
+    constexpr int SLICE = OT / KW;  // output tiles that a warp ends up with
+    if constexpr (KW > 1) {
+      if (t == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float *x = ml + 2 * (kw * G::ROWS + rw * 16 + g + 8 * i);
+          x[0] = m[i];
+          x[1] = l[i];
+        }
+      }
+      compute_sync();
+      float f[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float *x = ml + 2 * (rw * 16 + g + 8 * i);
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int k = 0; k < KW; ++k) M = fmaxf(M, x[2 * k * G::ROWS]);
+        const float b = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int k = 0; k < KW; ++k) L += x[2 * k * G::ROWS + 1] * exp2_approx(x[2 * k * G::ROWS] - b);
+        f[i] = exp2_approx(m[i] - b);
+        m[i] = M;
+        l[i] = L;
+      }
+#pragma unroll
+      for (int i = 0; i < OT; ++i) {
+        o[i][0] *= f[0];
+        o[i][1] *= f[0];
+        o[i][2] *= f[1];
+        o[i][3] *= f[1];
+      }
+      // round r: warp kw passes slice (kw + r) % KW on, and takes its own slice from warp (kw - r) % KW. The buffer
+      // holds one slice per warp (two halves of one, with two row tiles).
+      constexpr int PART = RW > 1 ? SLICE / 2 : SLICE;
+      float4 *buf = reinterpret_cast<float4 *>(smem + G::OFF_Q);
+#pragma unroll 1
+      for (int r = 1; r < KW; ++r) {
+#pragma unroll
+        for (int part = 0; part < SLICE / PART; ++part) {
+          const int to = (kw + r) % KW;
+#pragma unroll
+          for (int sl = 0; sl < KW; ++sl)
+            if (sl == to) {
+#pragma unroll
+              for (int i = 0; i < PART; ++i) {
+                const float(&x)[4] = o[sl * SLICE + part * PART + i];
+                buf[((rw * KW + to) * PART + i) * 32 + lane] = make_float4(x[0], x[1], x[2], x[3]);
+              }
+            }
+          compute_sync();
+#pragma unroll
+          for (int sl = 0; sl < KW; ++sl)
+            if (sl == kw) {
+#pragma unroll
+              for (int i = 0; i < PART; ++i) {
+                const float4 x = buf[((rw * KW + kw) * PART + i) * 32 + lane];
+                float(&y)[4] = o[sl * SLICE + part * PART + i];
+                y[0] += x.x;
+                y[1] += x.y;
+                y[2] += x.z;
+                y[3] += x.w;
+              }
+            }
+          compute_sync();
+        }
+      }
+    }
+    if (KW == 1) compute_sync();  // odd_values is complete
+    const uint32_t odd[2] = {odd_values[0], odd_values[1]};
+    const bool whole = sg.whole();
+    // slot 0: the item began before this share; slot 1: it goes on after it
+    const int slot = sg.kt0 > 0 ? 0 : 1;
+    float *part = p.partials + ((long long)blockIdx.x * 2 + slot) * G::ROWS * (DIM + 2);
+    const float vs = E4M3 ? p.c.v.scale[sg.head] : 1.f;
+#pragma unroll
+    for (int sl = 0; sl < KW; ++sl) {
+      if (sl != kw) continue;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = rw * 16 + g + 8 * i;
+        if (r >= rows) continue;
+        const int rr = sg.rt * G::ROWS + r, tok = sg.i.start + rr / p.group, h = sg.head * p.group + rr % p.group;
+        const float inv = l[i] > 0.f || l[i] != l[i] ? vs / l[i] : 0.f;
+        uint16_t *out = p.out + ((long long)tok * p.heads + h) * DIM;
+        float *po = part + (long long)r * (DIM + 2);
+#pragma unroll
+        for (int n = 0; n < SLICE; n += (E4M3 ? 2 : 1)) {
+          // the thread's columns: 8n + 2t, 8n + 2t + 1, or with 8-bit values 4 in a run over two tiles
+          constexpr int NC = E4M3 ? 4 : 2;
+          const int nt = sl * SLICE + n, d0 = E4M3 ? nt * 8 + 4 * t : nt * 8 + 2 * t;
+          float x[NC];
+          if constexpr (E4M3) {
+            x[0] = o[nt][2 * i];
+            x[1] = o[nt + 1][2 * i];
+            x[2] = o[nt][2 * i + 1];
+            x[3] = o[nt + 1][2 * i + 1];
+          } else {
+            x[0] = o[nt][2 * i];
+            x[1] = o[nt][2 * i + 1];
+          }
+          if (odd[0] | odd[1]) {
+            for (int j = 0; j < sg.i.n; ++j)
+              if ((odd[j >> 5] >> (j & 31) & 1) && (word[i] >> j & 1))
+#pragma unroll
+                for (int e = 0; e < NC; ++e) {
+                  const float v = value_at<E4M3>(p, sg.b, sg.head, (long long)sg.i.len + j, d0 + e);
+                  if (!(fabsf(v) < INFINITY)) x[e] += v;
+                }
+          }
+          if (whole) {
+            if constexpr (E4M3)
+              *reinterpret_cast<uint2 *>(out + d0) =
+                  make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
+            else
+              *reinterpret_cast<uint32_t *>(out + d0) = pack_bf16(x[0] * inv, x[1] * inv);
+          } else {
+#pragma unroll
+            for (int e = 0; e < NC; e += 2) *reinterpret_cast<float2 *>(po + d0 + e) = make_float2(x[e], x[e + 1]);
+          }
+        }
+        if (!whole && t == 0 && sl == 0) *reinterpret_cast<float2 *>(po + DIM) = make_float2(m[i], l[i]);
+      }
+    }
+  }
+  if (!ok) {
+    *abort_flag = 1;
+    if (lane == 0) atomicOr(p.err, kErrTimeout);
   }
 }
 
-// One CTA per (token, head), keys dealt to its warps; a lane holds DIM / 32
-// consecutive elements.
-template <int DIM, bool E4M3>
-__global__ void __launch_bounds__(kThreads) simple_kernel(const SimpleParams p) {
-  constexpr int N = DIM / 32, W = kThreads / 32;
-  __shared__ float sm[W], sl[W], so[W][DIM];
-  const int t = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// ---------------------------------------------------------------------------
+// Joining partials: WPR warps per query row (a token's head). The weights
+// 2^(m_c - M) of the CTAs' partials are formed first, so the sums over them
+// have no chain of dependent steps.
+// ---------------------------------------------------------------------------
+template <int DIM, int ROWS, int KT, int WPR>
+__global__ void __launch_bounds__(256) join_kernel(const AttnParams p) {
+  constexpr int V = DIM / 32;
+  __shared__ float acc[WPR > 1 ? 8 : 1][DIM];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long row = (long long)blockIdx.x * (8 / WPR) + warp / WPR;
+  const int wi = warp % WPR;
+  const int tok = (int)(row / p.heads), h = (int)(row % p.heads);
+  if (tok >= p.r.tokens) return;  // WPR is 1 or 8: whole blocks leave, or no barrier follows
   int b = 0;
   for (int hi = p.r.rows; b < hi;) {
     const int mid = (b + hi) >> 1;
-    if (p.r.starts[mid + 1] > t) hi = mid;
+    if (p.r.starts[mid + 1] > tok) hi = mid;
     else b = mid + 1;
   }
-  if (b >= p.r.rows) return;  // padding
-  const int s0 = p.r.starts[b], n = p.r.starts[b + 1] - s0, len = p.r.lengths[b], i = t - s0;
-  if (s0 < 0 || i < 0 || n > p.max_tree || len < 0) {
-    if (threadIdx.x == 0) atomicOr(p.err, kErrIndex);
-    return;
-  }
-  const unsigned long long word = p.mask ? (unsigned long long)p.mask[t] : (2ull << i) - 1;
-  const int kh = h / p.group;
-  float q[N], o[N], m = -INFINITY, l = 0.f;
-  load_row<false>(reinterpret_cast<const uint8_t *>(p.q + t * p.q_token + h * p.q_head + lane * N), q);
+  if (b >= p.r.rows) return;
+  const RowInfo i = row_info(p, b, false);
+  if (i.n == 0 || tok < i.start || tok >= i.start + i.n) return;
+  const int head = h / p.group, rr = (tok - i.start) * p.group + h % p.group;
+  const int kt = key_tiles<KT>(i);
+  const long long share = p.plan[0];
+  const long long t0 = p.plan[1 + b] + ((long long)head * row_tiles<ROWS>(i, p.group) + rr / ROWS) * kt;
+  const int c0 = (int)(t0 / share), c1 = (int)((t0 + kt - 1) / share);
+  if (c0 == c1) return;  // finished where it was computed
+  const int n = c1 - c0 + 1;
+  auto part = [&](int c) {
+    return p.partials + (((long long)(c0 + c) * 2 + (c == 0 ? 1 : 0)) * ROWS + rr % ROWS) * (DIM + 2);
+  };
+  float M = -INFINITY;
+  for (int c = lane; c < n; c += 32) M = fmaxf(M, part(c)[DIM]);
 #pragma unroll
-  for (int e = 0; e < N; ++e) o[e] = 0.f;
-  const float ks = E4M3 ? p.c.k.scale[kh] : 1.f, vs = E4M3 ? p.c.v.scale[kh] : 1.f;
-  for (long long j = warp; j < (long long)len + n; j += W) {
-    if (j >= len && !((word >> (j - len)) & 1)) continue;
-    const long long pi = j >> p.c.page_shift;
-    const int id = pi < p.r.max_pages ? p.r.table[(long long)b * p.r.max_pages + pi] : -1;
-    if ((unsigned)id >= (unsigned)p.c.pages) {
-      if (lane == 0) atomicOr(p.err, kErrIndex);
-      continue;
+  for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
+  const float base = M == -INFINITY ? 0.f : M;
+  float L = 0.f;
+  for (int c = lane; c < n; c += 32) L += part(c)[DIM + 1] * exp2_approx(part(c)[DIM] - base);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, d);
+  float x[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) x[e] = 0.f;
+#pragma unroll 4
+  for (int c = wi; c < n; c += WPR) {
+    const float *s = part(c);
+    const float w = exp2_approx(s[DIM] - base);
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+      const float2 y = *reinterpret_cast<const float2 *>(s + e * 32 + lane * 2);
+      x[e] = fmaf(w, y.x, x[e]);
+      x[e + 1] = fmaf(w, y.y, x[e + 1]);
     }
-    const long long row = j & (p.c.page_rows - 1);
-    float k[N], v[N], s = 0.f;
-    load_row<E4M3>(p.c.k.base + id * p.c.k.page + kh * p.c.k.head + row * p.c.k.row + lane * N * (E4M3 ? 1 : 2), k);
-    load_row<E4M3>(p.c.v.base + id * p.c.v.page + kh * p.c.v.head + row * p.c.v.row + lane * N * (E4M3 ? 1 : 2), v);
-#pragma unroll
-    for (int e = 0; e < N; ++e) s = fmaf(q[e], k[e], s);
-#pragma unroll
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    s *= p.scale * ks;
-    const float mn = fmaxf(m, s), a = __expf(m - mn), w = __expf(s - mn);
-    l = l * a + w;
-#pragma unroll
-    for (int e = 0; e < N; ++e) o[e] = fmaf(w, v[e], o[e] * a);
-    m = mn;
   }
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
+  const float inv = (L > 0.f || L != L) ? (p.c.e4m3 ? p.c.v.scale[head] : 1.f) / L : 0.f;
+  uint32_t *out = reinterpret_cast<uint32_t *>(p.out + ((long long)tok * p.heads + h) * DIM);
+  if constexpr (WPR == 1) {
 #pragma unroll
-  for (int e = 0; e < N; ++e) so[warp][lane * N + e] = o[e];
-  __syncthreads();
-  float M = -INFINITY, L = 0.f;
-  for (int w = 0; w < W; ++w) M = fmaxf(M, sm[w]);
-  for (int w = 0; w < W; ++w) L += M == -INFINITY ? 0.f : sl[w] * __expf(sm[w] - M);
-  for (int d = threadIdx.x; d < DIM; d += kThreads) {
-    float x = 0.f;
-    for (int w = 0; w < W; ++w) x += M == -INFINITY ? 0.f : so[w][d] * __expf(sm[w] - M);
-    const __nv_bfloat16 y = __float2bfloat16_rn(L > 0.f ? x / L * vs : 0.f);
-    p.out[((long long)t * p.heads + h) * DIM + d] = *reinterpret_cast<const uint16_t *>(&y);
+    for (int e = 0; e < V; e += 2) out[e * 16 + lane] = pack_bf16(x[e] * inv, x[e + 1] * inv);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; e += 2) *reinterpret_cast<float2 *>(&acc[warp][e * 32 + lane * 2]) = make_float2(x[e], x[e + 1]);
+    __syncthreads();
+    for (int d = threadIdx.x; d < DIM / 2; d += 256) {
+      float a = 0.f, c = 0.f;
+#pragma unroll
+      for (int w = 0; w < WPR; ++w) {
+        a += acc[w][2 * d];
+        c += acc[w][2 * d + 1];
+      }
+      out[d] = pack_bf16(a * inv, c * inv);
+    }
   }
 }
 
+// ---------------------------------------------------------------------------
+// launch
+// ---------------------------------------------------------------------------
+template <class... K, class... A>
+cudaError_t launch_dependent(void (*kern)(K...), unsigned grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(grid, 1, 1);
+  lc.blockDim = dim3(threads, 1, 1);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kern, args...);
+}
+
+constexpr size_t kPlanBytes = ((size_t)(65536 + 2) * 8 + 255) / 256 * 256;
+
+template <int DIM, bool E4M3, int RW>
+cudaError_t launch_rows(const AttnCall &c, AttnParams &p) {
+  using G = RowsGeo<DIM, E4M3, RW>;
+  auto kern = rows_kernel<DIM, E4M3, RW>;
+  static PerDevice configured;
+  if (!configured.v[c.device].load(std::memory_order_relaxed)) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
+    if (e != cudaSuccess) return e;
+    configured.v[c.device].store(1, std::memory_order_relaxed);
+  }
+  CUtensorMap tk, tv;
+  const int br = std::min(c.cache.page_rows, kKt);
+  if (!encode_cache(&tk, c.cache.k, c.cache, br, G::CW) || !encode_cache(&tv, c.cache.v, c.cache, br, G::CW))
+    return cudaErrorInvalidValue;
+  const int grid = std::min(G::CTAS * c.sm_count, kMaxCtas);
+  cudaError_t e = launch_dependent(kern, grid, kThreads, G::SMEM, c.stream, tk, tv, p);
+  if (e != cudaSuccess) return e;
+  // Few items: each is split over many CTAs, so eight warps join a row; many: one warp does
+  const long long items = (long long)c.rows.rows * c.cache.kv_heads * ((c.max_tree * p.group + G::ROWS - 1) / G::ROWS);
+  const long long rows = (long long)c.rows.tokens * c.heads;
+  if (items * 4 <= grid)
+    return launch_dependent(join_kernel<DIM, G::ROWS, kKt, 8>, (unsigned)rows, 256, 0, c.stream, p);
+  return launch_dependent(join_kernel<DIM, G::ROWS, kKt, 1>, (unsigned)((rows + 7) / 8), 256, 0, c.stream, p);
+}
+
 template <int DIM, bool E4M3>
-cudaError_t run_simple(const AttnCall &c) {
-  SimpleParams p{c.q, c.q_token, c.q_head, c.cache, c.rows, c.mask, c.heads, c.heads / c.cache.kv_heads,
-                 c.max_tree, c.scale, c.out, c.err};
-  simple_kernel<DIM, E4M3><<<dim3(c.rows.tokens, c.heads), kThreads, 0, c.stream>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_dim(const AttnCall &c, AttnParams &p) {
+  const int rows = c.max_tree * p.group;
+  if (rows <= 16) return launch_rows<DIM, E4M3, 1>(c, p);
+  if (rows <= 32) return launch_rows<DIM, E4M3, 2>(c, p);
+  return launch_rows<DIM, E4M3, 4>(c, p);
 }
 
 }  // namespace
 
-size_t tree_attn_workspace_bytes(int heads, int kv_heads, int dim, int max_tree) { return 256; }
+bool encode_cache(CUtensorMap *m, const KvSide &s, const KvCache &c, int box_rows, int box_bytes) {
+  const int elt = c.e4m3 ? 1 : 2;
+  // an axis of one entry is never stepped along; its stride only has to be one that a map may have
+  auto step = [&](int n, long long stride) { return (uint64_t)(n > 1 ? stride : c.row_bytes()); };
+  const uint64_t dims[4] = {(uint64_t)c.dim, (uint64_t)c.page_rows, (uint64_t)c.kv_heads, (uint64_t)c.pages};
+  const uint64_t strides[3] = {step(c.page_rows, s.row), step(c.kv_heads, s.head), step(c.pages, s.page)};
+  const uint32_t box[4] = {(uint32_t)(box_bytes / elt), (uint32_t)box_rows, 1, 1};
+  return encode_4d(m, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, s.base, dims, strides,
+                   box, box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+size_t tree_attn_workspace_bytes(int heads, int kv_heads, int dim, int max_tree) {
+  const int rows = max_tree * (heads / kv_heads);
+  const int tile = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  return kPlanBytes + align_up((size_t)kMaxCtas * 2 * tile * (dim + 2) * sizeof(float), 256);
+}
 
 cudaError_t launch_tree_attention(const AttnCall &c) {
+  AttnParams p;
+  p.q = c.q;
+  p.q_token = c.q_token;
+  p.q_head = c.q_head;
+  p.c = c.cache;
+  p.r = c.rows;
+  p.mask = c.mask;
+  p.heads = c.heads;
+  p.group = c.heads / c.cache.kv_heads;
+  p.max_tree = c.max_tree;
+  p.scale_log2 = c.scale * kLog2e;
+  p.out = c.out;
+  p.plan = static_cast<long long *>(c.workspace);
+  p.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(c.workspace) + kPlanBytes);
+  p.err = c.err;
   switch (c.cache.dim) {
-    case 64: return c.cache.e4m3 ? run_simple<64, true>(c) : run_simple<64, false>(c);
-    case 128: return c.cache.e4m3 ? run_simple<128, true>(c) : run_simple<128, false>(c);
-    default: return c.cache.e4m3 ? run_simple<256, true>(c) : run_simple<256, false>(c);
+    case 64: return c.cache.e4m3 ? launch_dim<64, true>(c, p) : launch_dim<64, false>(c, p);
+    case 128: return c.cache.e4m3 ? launch_dim<128, true>(c, p) : launch_dim<128, false>(c, p);
+    default: return c.cache.e4m3 ? launch_dim<256, true>(c, p) : launch_dim<256, false>(c, p);
   }
 }
 

@@ -1,0 +1,204 @@
+// What the attention kernels over the paged cache share: the work list, the
+// partial results and their workspace, and the rules for single keys.
+//
+// Work list. Row b of the page table with T new tokens and L cached ones has
+// K = L + T keys; its T * G query rows of one kv head (G query heads each) are
+// packed token by token into tiles of ROWS rows, so its items are
+// (kv head, row tile), each of ceil(K / KT) key tiles. All key tiles of all
+// items, in the order (b, head, row tile, key tile), form one list, and every
+// CTA takes an equal, contiguous share of it, whatever the lengths are: long
+// contexts are split over many CTAs, short ones share one. An item whose tiles
+// lie in one share is finished there; otherwise each CTA leaves a partial
+// result (running maximum, sum and unnormalised output per row) in the
+// workspace, and a second kernel joins them in the order of the CTAs, so
+// results do not depend on timing. A CTA leaves at most two partials: of the
+// item it begins in the middle of (slot 0), and of the one it does not end
+// (slot 1).
+#pragma once
+
+#include "w4a16_internal.h"
+
+namespace w4a16 {
+
+constexpr int kMaxCtas = 320;  // CTAs of an attention launch: shares of the work list
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct AttnParams {
+  const uint16_t *q;
+  long long q_token, q_head;
+  KvCache c;
+  KvRows r;
+  const int64_t *mask;
+  int heads, group, max_tree;
+  float scale_log2;  // scale * log2(e): scores are kept in powers of two
+  uint16_t *out;
+  float *partials;       // [kMaxCtas][2][ROWS][DIM + 2]
+  long long *plan;       // [0] share, [1 + b] first tile of row b
+  int *err;
+};
+
+// One row of the table as the work list sees it
+struct RowInfo {
+  int start, n, len, keys;  // first token, new tokens, cached, len + n (no more than the table holds)
+};
+
+__device__ __forceinline__ void attn_flag(int *err) { atomicOr(err, kErrIndex); }
+
+// n = 0 for a row without new tokens or with numbers that cannot be; `flag`: report those
+__device__ __forceinline__ RowInfo row_info(const AttnParams &p, int b, bool flag) {
+  RowInfo i;
+  i.start = p.r.starts[b];
+  const int end = p.r.starts[b + 1];
+  i.len = p.r.lengths[b];
+  i.n = end - i.start;
+  if (i.start < 0 || end > p.r.tokens || i.n < 0 || i.n > p.max_tree || i.len < 0) {
+    if (flag) attn_flag(p.err);
+    i.n = 0;
+  }
+  const long long room = (long long)p.r.max_pages << p.c.page_shift;
+  const long long keys = (long long)i.len + i.n;
+  if (i.n > 0 && keys > room && flag) attn_flag(p.err);
+  i.keys = (int)min(keys, min(room, (long long)INT32_MAX - 4096));
+  return i;
+}
+
+template <int KT>
+__device__ __forceinline__ int key_tiles(const RowInfo &i) {
+  return (i.keys + KT - 1) / KT;
+}
+template <int ROWS>
+__device__ __forceinline__ int row_tiles(const RowInfo &i, int group) {
+  return (i.n * group + ROWS - 1) / ROWS;
+}
+template <int ROWS, int KT>
+__device__ __forceinline__ long long tiles_of(const RowInfo &i, const AttnParams &p) {
+  return i.n > 0 ? (long long)p.c.kv_heads * row_tiles<ROWS>(i, p.group) * key_tiles<KT>(i) : 0;
+}
+
+// A CTA's place in the work list
+struct Cursor {
+  long long at, end;  // tiles [at, end) are left
+  int b, head, rt, kt;
+};
+
+struct PlanShared {
+  long long sums[16];
+  long long at, end;
+  int b, head, rt, kt;
+};
+
+// The CTA's share, found by all NT threads: thread i sums the tiles of its
+// own run of rows, a block scan places the runs, and the thread whose run holds
+// the share's first tile walks it. CTA 0 also writes the plan that the joining
+// kernel reads. The caller synchronises before it reads `s`.
+template <int ROWS, int KT, int NT>
+__device__ void plan_share(const AttnParams &p, PlanShared &s, int min_tiles) {
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int per = (p.r.rows + NT - 1) / NT;
+  const int b0 = min(tid * per, p.r.rows), b1 = min(b0 + per, p.r.rows);
+  const bool flag = blockIdx.x == 0;
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += tiles_of<ROWS, KT>(row_info(p, b, flag), p);
+  long long upto = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+    if (lane >= d) upto += o;
+  }
+  if (lane == 31) s.sums[w] = upto;
+  __syncthreads();
+  long long before = 0, total = 0;
+#pragma unroll
+  for (int i = 0; i < (NT + 31) / 32; ++i) {
+    const long long x = s.sums[i];
+    if (i < w) before += x;
+    total += x;
+  }
+  const long long first = before + upto - mine;
+  // as many CTAs as get min_tiles each, and no share larger than it has to be
+  const long long ctas = max(1ll, min((long long)gridDim.x, total / min_tiles));
+  const long long share = max(1ll, (total + ctas - 1) / ctas);
+  const long long at = min(share * blockIdx.x, total), end = min(at + share, total);
+  if (flag) {
+    long long f = first;
+    for (int b = b0; b < b1; ++b) {
+      p.plan[1 + b] = f;
+      f += tiles_of<ROWS, KT>(row_info(p, b, false), p);
+    }
+    if (tid == 0) p.plan[0] = share;
+  }
+  if (tid == 0) {
+    s.at = at;
+    s.end = end;
+  }
+  if (at < end && first <= at && at < first + mine) {
+    long long f = first;
+    for (int b = b0; b < b1; ++b) {
+      const RowInfo i = row_info(p, b, false);
+      const long long n = tiles_of<ROWS, KT>(i, p);
+      if (at < f + n) {
+        const int kt = key_tiles<KT>(i), rt = row_tiles<ROWS>(i, p.group);
+        const long long o = at - f;
+        s.b = b;
+        s.kt = (int)(o % kt);
+        s.rt = (int)(o / kt % rt);
+        s.head = (int)(o / kt / rt);
+        break;
+      }
+      f += n;
+    }
+  }
+}
+
+// The part of an item that a CTA works on: key tiles [kt0, kt1)
+struct Segment {
+  RowInfo i;
+  int b, head, rt, kt0, kt1, ktiles;
+  __device__ bool whole() const { return kt0 == 0 && kt1 == ktiles; }
+};
+
+// Next segment of the share (false: none is left)
+template <int ROWS, int KT>
+__device__ __forceinline__ bool next_segment(const AttnParams &p, Cursor &c, Segment &s) {
+  if (c.at >= c.end) return false;
+  s.i = row_info(p, c.b, false);
+  while (s.i.n == 0) s.i = row_info(p, ++c.b, false);  // rows without work; tiles are left, so one with work follows
+  s.b = c.b;
+  s.head = c.head;
+  s.rt = c.rt;
+  s.kt0 = c.kt;
+  s.ktiles = key_tiles<KT>(s.i);
+  s.kt1 = (int)min((long long)s.ktiles, s.kt0 + (c.end - c.at));
+  c.at += s.kt1 - s.kt0;
+  c.kt = 0;
+  if (++c.rt == row_tiles<ROWS>(s.i, p.group)) {
+    c.rt = 0;
+    if (++c.head == p.c.kv_heads) {
+      c.head = 0;
+      ++c.b;
+    }
+  }
+  return true;
+}
+
+// Tensor map of one side of a cache layer: (element, row, head, page), boxes of
+// `box_rows` rows by `box_bytes` bytes, swizzled over the box's width
+bool encode_cache(CUtensorMap *m, const KvSide &s, const KvCache &c, int box_rows, int box_bytes);
+
+// 4-D tiled TMA load
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int c0, int c1, int c2, int c3, uint32_t bar,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+}  // namespace w4a16

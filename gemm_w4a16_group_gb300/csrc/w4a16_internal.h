@@ -69,6 +69,9 @@ cudaError_t launch_prompt_tc(const GemmCall &c, int sm_count);   // any M
 // or rejected
 bool encode_2d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t outer,
                uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw);
+// the same for 4 dimensions, innermost first; strides (bytes) of the outer three
+bool encode_4d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, const uint64_t (&dims)[4],
+               const uint64_t (&strides)[3], const uint32_t (&box)[4], CUtensorMapSwizzle sw);
 // tcgen05 decode kernel: 1 <= M <= 32, plain zero-point or symmetric GEMM
 bool smallm_tc_supports(const GemmCall &c);
 cudaError_t launch_smallm_tc(const GemmCall &c, int sm_count);
