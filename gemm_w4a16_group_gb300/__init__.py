@@ -195,7 +195,9 @@ def _stream(stream, device=None):
         raise ValueError(f"the tensors are on {device} but the current CUDA device is "
                          f"cuda:{torch.cuda.current_device()}: the library launches on the current device")
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the current stream's handle without the Stream object around it (0.1 against 2.8 us)
+        index = torch.cuda.current_device() if device is None else device.index
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(index))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -593,63 +595,134 @@ MAX_ROWS = 4096   # rows that one fork, free or reserve call may name
 _KV_CACHE = _struct.Struct("=4Q8q6i")
 
 
-def _kv_cache(k_cache, v_cache, k_scale, v_scale, one_layer, d):
+class _Types:
+    """torch's dtypes, looked up once (the module loads without torch)."""
+    def __init__(self):
+        torch = _torch()
+        self.bf16, self.e4m3, self.i32, self.i64 = torch.bfloat16, torch.float8_e4m3fn, torch.int32, torch.int64
+        self.f32, self.u8, self.empty = torch.float32, torch.uint8, torch.empty
+
+
+_types = functools.lru_cache(maxsize=1)(_Types)
+
+
+# These calls are short on the device, so their checks are written for speed:
+# get_device() (an int) stands for the device, and a message is only put
+# together once something is wrong.
+def _refuse(t, dtype, name, dev, need=None):
+    """Raise what is wrong with tensor `t`: its type, place, order or size."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype} is not {dtype}")
+    if not _is_device_tensor(t):
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on device {dev}")
+    if need is not None and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if need is not None:
+        raise ValueError(f"{name} has shape {list(t.shape)}, the call needs {need} elements")
+
+
+def _flat(t, dtype, name, need, dev):
+    """Data pointer of a contiguous tensor of exactly `need` elements."""
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() != need or not t.is_contiguous():
+        _refuse(t, dtype, name, dev, need)
+    return t.data_ptr()
+
+
+def _table(t, dev):
+    """Data pointer, rows and width of an int32 page table."""
+    if t.dtype is not _types().i32 or t.get_device() != dev or t.dim() != 2 or not t.is_contiguous():
+        _refuse(t, _types().i32, "page_table", dev, "[rows, max pages] int32")
+    rows, width = t.shape
+    return t.data_ptr(), rows, width
+
+
+def _place(t, name):
+    """The device number of the tensor that names the call's device."""
+    dev = t.get_device()
+    if dev < 0 and not _is_device_tensor(t):
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def _on(stream, t):
+    """The call's stream handle, as _stream gives it."""
+    return _stream(stream, t.device)
+
+
+def _empty(shape, dtype, like, stream):
+    """A new tensor on `like`'s device, taken from the pool of the stream that
+    will write it (so that nothing still running elsewhere uses its memory)."""
+    if stream is None:
+        return _types().empty(shape, dtype=dtype, device=like.device)
+    with _torch().cuda.stream(stream):
+        return _types().empty(shape, dtype=dtype, device=like.device)
+
+
+_workspaces = {}
+
+
+def _workspace(need, like, dev, stream, handle):
+    """The scratch of calls that bring none: one buffer per device and stream,
+    used by one call after the other in the stream's order, and grown when a
+    call needs more. A call under capture gets a buffer of its own from the
+    graph's pool, which lives as long as the graph."""
+    if _torch().cuda.is_current_stream_capturing():
+        return _empty(need, _types().u8, like, stream)
+    key = (dev, handle)
+    ws = _workspaces.get(key)
+    if ws is None or ws.numel() < need:
+        ws = _workspaces[key] = _empty(need, _types().u8, like, stream)
+    return ws
+
+
+def _kv_cache(k_cache, v_cache, k_scale, v_scale, one_layer, dev):
     """The w4a16_kv_cache bytes of a cache given as [pages, kv heads, page
     rows, dim] tensors (any strides, dim contiguous), or with a leading layer
-    axis unless `one_layer`."""
-    torch = _torch()
+    axis unless `one_layer`; and its shape with that axis."""
+    ty = _types()
     shape = k_cache.shape
-    if len(shape) != 4 and (one_layer or len(shape) != 5):
+    axes = len(shape)
+    if axes != 4 and (one_layer or axes != 5):
         raise ValueError("k_cache must be [pages, kv heads, page rows, dim]" +
                          ("" if one_layer else ", or that with a leading layer axis"))
     if v_cache.shape != shape:
-        raise ValueError(f"v_cache has shape {tuple(v_cache.shape)}, k_cache {tuple(shape)}")
+        raise ValueError(f"v_cache has shape {list(v_cache.shape)}, k_cache {list(shape)}")
     dt = k_cache.dtype
-    e4m3 = dt == torch.float8_e4m3fn
-    if (not e4m3 and dt != torch.bfloat16) or v_cache.dtype != dt:
+    e4m3 = dt is ty.e4m3
+    if (not e4m3 and dt is not ty.bf16) or v_cache.dtype is not dt:
         raise TypeError(f"k_cache, v_cache: dtypes {dt}, {v_cache.dtype} are not both bfloat16 or both float8_e4m3fn")
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not _is_device_tensor(t):
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if t.device != d:
-            raise ValueError(f"{name} is on {t.device}, the call's other tensors on {d}")
+    if k_cache.get_device() != dev:
+        _refuse(k_cache, dt, "k_cache", dev)
+    if v_cache.get_device() != dev:
+        _refuse(v_cache, dt, "v_cache", dev)
     ks, vs = k_cache.stride(), v_cache.stride()
     if ks[-1] != 1 or vs[-1] != 1:
         raise ValueError("k_cache, v_cache: the last axis must be contiguous")
-    if len(shape) == 4:
+    if axes == 4:
         shape, ks, vs = (1, *shape), (0, *ks), (0, *vs)
     kp = vp = 0
     if e4m3 and one_layer:
         if k_scale is None or v_scale is None:
             raise ValueError("a float8_e4m3fn cache needs k_scale and v_scale")
-        kp = _ptr(k_scale, (torch.float32,), "k_scale", 4 * shape[2], d).value
-        vp = _ptr(v_scale, (torch.float32,), "v_scale", 4 * shape[2], d).value
+        kp = _flat(k_scale, ty.f32, "k_scale", shape[2], dev)
+        vp = _flat(v_scale, ty.f32, "v_scale", shape[2], dev)
     elif k_scale is not None or v_scale is not None:
         raise ValueError("k_scale and v_scale belong to float8_e4m3fn caches")
-    return _KV_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), kp, vp, *ks[:4], *vs[:4], *shape, int(e4m3)), shape
+    return _KV_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), kp, vp, *ks[:4], *vs[:4], *shape, e4m3), shape
 
 
-def _int32(t, name, shape, d):
-    """Data pointer of an int32 index tensor of exactly `shape` (-1: any size)."""
-    if t.dim() != len(shape) or any(w >= 0 and w != g for w, g in zip(shape, t.shape)):
-        raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
-    return _ptr(t, (_torch().int32,), name, 0, d)
-
-
-def _token_rows(t, name, heads, dim, d):
-    """Pointer and strides of a bf16 [tokens, heads, dim] tensor whose last axis is contiguous."""
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != dim:
-        raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, {dim}], not {list(t.shape)}")
-    if t.dtype != _torch().bfloat16:
-        raise TypeError(f"{name}: dtype {t.dtype} is not bfloat16")
-    if not _is_device_tensor(t):
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device != d:
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {d}")
-    s = t.stride()
+def _token_rows(t, name, dim, dev):
+    """Pointer, strides and sizes of a bf16 [tokens, heads, dim] tensor whose last axis is contiguous."""
+    if t.dtype is not _types().bf16 or t.get_device() != dev:
+        _refuse(t, _types().bf16, name, dev)
+    shape, s = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens, heads, {dim}], not {list(shape)}")
     if s[2] != 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
-    return t.data_ptr(), s[0], s[1]
+    return t.data_ptr(), s[0], s[1], shape[0], shape[1]
 
 
 def kv_append(k, v, k_cache, v_cache, page_table, lengths, starts, k_scale=None, v_scale=None, stream=None):
@@ -658,16 +731,15 @@ def kv_append(k, v, k_cache, v_cache, page_table, lengths, starts, k_scale=None,
     to position lengths[b] + i of row b. page_table int32 [rows, max pages],
     lengths int32 [rows], starts int32 [rows + 1]. e4m3 caches store x /
     scale[head], rounded to nearest and saturated."""
-    d = k.device
-    cache, (_, _, heads, _, dim) = _kv_cache(k_cache, v_cache, k_scale, v_scale, True, d)
-    kp, kt, kh = _token_rows(k, "k", heads, dim, d)
-    vp, vt, vh = _token_rows(v, "v", heads, dim, d)
-    if v.shape[0] != k.shape[0]:
-        raise ValueError(f"k has {k.shape[0]} tokens, v {v.shape[0]}")
-    table = _int32(page_table, "page_table", (-1, -1), d)
-    rows, width = page_table.shape
-    rc = lib().w4a16_kv_append(kp, vp, kt, kh, vt, vh, cache, table, width, _int32(lengths, "lengths", (rows,), d),
-                               _int32(starts, "starts", (rows + 1,), d), rows, k.shape[0], _stream(stream, d))
+    ty, dev = _types(), _place(k, "k")
+    cache, (_, _, heads, _, dim) = _kv_cache(k_cache, v_cache, k_scale, v_scale, True, dev)
+    kp, kt, kh, tokens, k_heads = _token_rows(k, "k", dim, dev)
+    vp, vt, vh, v_tokens, v_heads = _token_rows(v, "v", dim, dev)
+    if v_tokens != tokens or k_heads != heads or v_heads != heads:
+        raise ValueError(f"k and v must both be [tokens, {heads}, {dim}], not {list(k.shape)} and {list(v.shape)}")
+    table, rows, width = _table(page_table, dev)
+    rc = lib().w4a16_kv_append(kp, vp, kt, kh, vt, vh, cache, table, width, _flat(lengths, ty.i32, "lengths", rows, dev),
+                               _flat(starts, ty.i32, "starts", rows + 1, dev), rows, tokens, _on(stream, k))
     _check(rc, "w4a16_kv_append")
 
 
@@ -684,28 +756,28 @@ def tree_attention(q, k_cache, v_cache, page_table, lengths, starts, mask, max_t
     heads, dim] (strided views allowed); every row has at most max_tree <=
     MAX_TREE new tokens, appended before. scale defaults to dim ** -0.5. A token
     that sees nothing gets 0; padding tokens (at starts[rows] and above) are
-    left as they are in `out`. `workspace` (uint8,
-    tree_attention_workspace_bytes) is allocated when not given."""
-    torch = _torch()
-    d = q.device
-    cache, (_, _, kv_heads, _, dim) = _kv_cache(k_cache, v_cache, k_scale, v_scale, True, d)
-    qp, qt, qh = _token_rows(q, "q", None, dim, d)
-    tokens, heads = q.shape[0], q.shape[1]
+    left as they are in `out`. Without a `workspace` (uint8,
+    tree_attention_workspace_bytes) the call uses one that the module keeps
+    for its stream."""
+    ty, dev = _types(), _place(q, "q")
+    cache, (_, _, kv_heads, _, dim) = _kv_cache(k_cache, v_cache, k_scale, v_scale, True, dev)
+    qp, qt, qh, tokens, heads = _token_rows(q, "q", dim, dev)
     need = tree_attention_workspace_bytes(heads, kv_heads, dim, max_tree)
     if need == 0:
         raise W4A16Error(f"tree_attention: unsupported heads={heads} kv_heads={kv_heads} dim={dim} max_tree={max_tree}")
-    table = _int32(page_table, "page_table", (-1, -1), d)
-    rows, width = page_table.shape
+    table, rows, width = _table(page_table, dev)
+    handle = _on(stream, q)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=d)
+        workspace = _workspace(need, q, dev, stream, handle.value)
+    elif workspace.dtype is not ty.u8 or workspace.get_device() != dev or not workspace.is_contiguous() or workspace.numel() < need:
+        _refuse(workspace, ty.u8, "workspace", dev, need)
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=d)
-    rc = lib().w4a16_tree_attention(qp, qt, qh, cache, table, width, _int32(lengths, "lengths", (rows,), d),
-                                    _int32(starts, "starts", (rows + 1,), d),
-                                    _ptr(mask, (torch.int64,), "mask", 8 * tokens, d), rows, tokens, heads, max_tree,
-                                    dim ** -0.5 if scale is None else scale,
-                                    _ptr(out, (torch.bfloat16,), "out", 2 * tokens * heads * dim, d),
-                                    _ptr(workspace, (torch.uint8,), "workspace", need, d), _stream(stream, d))
+        out = _empty((tokens, heads, dim), ty.bf16, q, stream)
+    rc = lib().w4a16_tree_attention(qp, qt, qh, cache, table, width, _flat(lengths, ty.i32, "lengths", rows, dev),
+                                    _flat(starts, ty.i32, "starts", rows + 1, dev),
+                                    None if mask is None else _flat(mask, ty.i64, "mask", tokens, dev), rows, tokens,
+                                    heads, max_tree, dim ** -0.5 if scale is None else scale,
+                                    _flat(out, ty.bf16, "out", tokens * heads * dim, dev), workspace.data_ptr(), handle)
     _check(rc, "w4a16_tree_attention")
     return out
 
@@ -716,21 +788,20 @@ def tree_accept(target, draft, mask, starts, max_tree, path=None, count=None, to
     tokens, mask as in tree_attention. Returns (path int32 [rows, max_tree]:
     the accepted nodes, then -1; count int32 [rows]; token int64 [rows]: the
     pick after the last accepted node)."""
-    torch = _torch()
-    d = target.device
+    ty, dev = _types(), _place(target, "target")
     tokens, rows = target.numel(), starts.numel() - 1
     if path is None:
-        path = torch.empty((rows, max_tree), dtype=torch.int32, device=d)
+        path = _empty((rows, max_tree), ty.i32, target, stream)
     if count is None:
-        count = torch.empty(rows, dtype=torch.int32, device=d)
+        count = _empty(rows, ty.i32, target, stream)
     if token is None:
-        token = torch.empty(rows, dtype=torch.int64, device=d)
-    i64 = (torch.int64,)
-    rc = lib().w4a16_tree_accept(_ptr(target, i64, "target", 0, d), _ptr(draft, i64, "draft", 8 * tokens, d),
-                                 _ptr(mask, i64, "mask", 8 * tokens, d), _int32(starts, "starts", (-1,), d), rows,
-                                 tokens, max_tree, _int32(path, "path", (rows, max_tree), d),
-                                 _int32(count, "count", (rows,), d), _ptr(token, i64, "token", 8 * rows, d),
-                                 _stream(stream, d))
+        token = _empty(rows, ty.i64, target, stream)
+    rc = lib().w4a16_tree_accept(_flat(target, ty.i64, "target", tokens, dev), _flat(draft, ty.i64, "draft", tokens, dev),
+                                 None if mask is None else _flat(mask, ty.i64, "mask", tokens, dev),
+                                 _flat(starts, ty.i32, "starts", rows + 1, dev), rows, tokens, max_tree,
+                                 _flat(path, ty.i32, "path", rows * max_tree, dev),
+                                 _flat(count, ty.i32, "count", rows, dev), _flat(token, ty.i64, "token", rows, dev),
+                                 _on(stream, target))
     _check(rc, "w4a16_tree_accept")
     return path, count, token
 
@@ -740,16 +811,18 @@ def kv_compact(k_cache, v_cache, page_table, lengths, path, count, lengths_out=N
     pages, kv heads, page rows, dim): position lengths[b] + path[b, i] to
     lengths[b] + i for i < count[b]. Returns the new lengths, lengths + count
     (a new tensor, or `lengths_out`, which must not be `lengths`)."""
-    torch = _torch()
-    d = k_cache.device
-    cache, _ = _kv_cache(k_cache, v_cache, None, None, False, d)
-    table = _int32(page_table, "page_table", (-1, -1), d)
-    rows, width = page_table.shape
+    ty, dev = _types(), _place(k_cache, "k_cache")
+    cache, _ = _kv_cache(k_cache, v_cache, None, None, False, dev)
+    table, rows, width = _table(page_table, dev)
+    if path.dim() != 2:
+        raise ValueError(f"path must be [{rows}, max_tree], not {list(path.shape)}")
+    max_tree = path.shape[1]
     if lengths_out is None:
-        lengths_out = torch.empty(rows, dtype=torch.int32, device=d)
-    rc = lib().w4a16_kv_compact(cache, table, width, _int32(lengths, "lengths", (rows,), d),
-                                _int32(path, "path", (rows, -1), d), _int32(count, "count", (rows,), d), rows,
-                                path.shape[1], _int32(lengths_out, "lengths_out", (rows,), d), _stream(stream, d))
+        lengths_out = _empty(rows, ty.i32, k_cache, stream)
+    rc = lib().w4a16_kv_compact(cache, table, width, _flat(lengths, ty.i32, "lengths", rows, dev),
+                                _flat(path, ty.i32, "path", rows * max_tree, dev),
+                                _flat(count, ty.i32, "count", rows, dev), rows, max_tree,
+                                _flat(lengths_out, ty.i32, "lengths_out", rows, dev), _on(stream, k_cache))
     _check(rc, "w4a16_kv_compact")
     return lengths_out
 
@@ -758,12 +831,12 @@ def kv_free(page_table, lengths, refs, rows, stream=None):
     """Drop the table rows `rows` (int32 [n], distinct): one reference (refs
     int32 [pages]) of each page they hold; their entries become -1, their
     lengths 0."""
-    d = page_table.device
-    table = _int32(page_table, "page_table", (-1, -1), d)
-    table_rows, width = page_table.shape
-    rc = lib().w4a16_kv_free(table, width, table_rows, _int32(lengths, "lengths", (table_rows,), d),
-                             _int32(refs, "refs", (-1,), d), refs.numel(), _int32(rows, "rows", (-1,), d),
-                             rows.numel(), _stream(stream, d))
+    i32, dev = _types().i32, _place(page_table, "page_table")
+    table, table_rows, width = _table(page_table, dev)
+    pages, n = refs.numel(), rows.numel()
+    rc = lib().w4a16_kv_free(table, width, table_rows, _flat(lengths, i32, "lengths", table_rows, dev),
+                             _flat(refs, i32, "refs", pages, dev), pages, _flat(rows, i32, "rows", n, dev), n,
+                             _on(stream, page_table))
     _check(rc, "w4a16_kv_free")
 
 
@@ -772,17 +845,16 @@ def kv_fork(k_cache, v_cache, page_table, lengths, refs, src, dst, ok=None, stre
     [n]). Whole pages are shared, a part-filled last page is copied in every
     layer into the lowest free page. Returns ok int32 [1]: 1, or 0 when the
     free pages did not suffice and nothing changed."""
-    torch = _torch()
-    d = page_table.device
-    cache, shape = _kv_cache(k_cache, v_cache, None, None, False, d)
-    table = _int32(page_table, "page_table", (-1, -1), d)
-    table_rows, width = page_table.shape
+    ty, dev = _types(), _place(page_table, "page_table")
+    i32 = ty.i32
+    cache, shape = _kv_cache(k_cache, v_cache, None, None, False, dev)
+    table, table_rows, width = _table(page_table, dev)
     if ok is None:
-        ok = torch.empty(1, dtype=torch.int32, device=d)
+        ok = _empty(1, i32, page_table, stream)
     n = src.numel()
-    rc = lib().w4a16_kv_fork(cache, table, width, table_rows, _int32(lengths, "lengths", (table_rows,), d),
-                             _int32(refs, "refs", (shape[1],), d), _int32(src, "src", (n,), d),
-                             _int32(dst, "dst", (n,), d), n, _int32(ok, "ok", (1,), d), _stream(stream, d))
+    rc = lib().w4a16_kv_fork(cache, table, width, table_rows, _flat(lengths, i32, "lengths", table_rows, dev),
+                             _flat(refs, i32, "refs", shape[1], dev), _flat(src, i32, "src", n, dev),
+                             _flat(dst, i32, "dst", n, dev), n, _flat(ok, i32, "ok", 1, dev), _on(stream, page_table))
     _check(rc, "w4a16_kv_fork")
     return ok
 
@@ -791,16 +863,15 @@ def kv_reserve(page_table, refs, rows, want, page_rows, ok=None, stream=None):
     """Room to grow: table row rows[j] gets the lowest free pages until it
     holds want[j] tokens (int32 [n] each). Returns ok int32 [1]: 1, or 0 when
     the free pages did not suffice and nothing changed."""
-    torch = _torch()
-    d = page_table.device
-    table = _int32(page_table, "page_table", (-1, -1), d)
-    table_rows, width = page_table.shape
+    ty, dev = _types(), _place(page_table, "page_table")
+    i32 = ty.i32
+    table, table_rows, width = _table(page_table, dev)
     if ok is None:
-        ok = torch.empty(1, dtype=torch.int32, device=d)
-    n = rows.numel()
-    rc = lib().w4a16_kv_reserve(table, width, table_rows, _int32(refs, "refs", (-1,), d), refs.numel(), page_rows,
-                                _int32(rows, "rows", (n,), d), _int32(want, "want", (n,), d), n,
-                                _int32(ok, "ok", (1,), d), _stream(stream, d))
+        ok = _empty(1, i32, page_table, stream)
+    n, pages = rows.numel(), refs.numel()
+    rc = lib().w4a16_kv_reserve(table, width, table_rows, _flat(refs, i32, "refs", pages, dev), pages, page_rows,
+                                _flat(rows, i32, "rows", n, dev), _flat(want, i32, "want", n, dev), n,
+                                _flat(ok, i32, "ok", 1, dev), _on(stream, page_table))
     _check(rc, "w4a16_kv_reserve")
     return ok
 
