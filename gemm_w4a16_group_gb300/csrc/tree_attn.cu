@@ -40,7 +40,6 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kKt = 64;  // keys of a stage
 constexpr int kComputeWarps = 4;
 constexpr int kThreads = (kComputeWarps + 1) * 32;
 constexpr int kMinTiles = 2;
@@ -49,12 +48,13 @@ template <int DIM, bool E4M3, int RWT>
 struct RowsGeo {
   static constexpr int RW = RWT, KW = kComputeWarps / RWT;
   static constexpr int ROWS = 16 * RW;
-  static constexpr int KPW = kKt / KW;         // keys of a warp per stage
+  static constexpr int KT = RW <= 2 && (DIM * (E4M3 ? 1 : 2) <= 128 || (DIM == 256 && E4M3)) ? 128 : 64;  // keys of a stage
+  static constexpr int KPW = KT / KW;         // keys of a warp per stage
   static constexpr int ELT = E4M3 ? 1 : 2;
   static constexpr int ROWB = DIM * ELT;       // bytes of a cache row
   static constexpr int CW = ROWB < 128 ? ROWB : 128;  // box width
   static constexpr int CH = ROWB / CW;
-  static constexpr int SUB = kKt * CW;         // one box column of a stage
+  static constexpr int SUB = KT * CW;         // one box column of a stage
   static constexpr int SIDE = CH * SUB;
   static constexpr int STAGE = 2 * SIDE;
   static constexpr int CTAS = DIM == 256 ? 1 : 2;  // per SM
@@ -184,14 +184,14 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
   }
   grid_dependency_wait();
   grid_launch_dependents();
-  plan_share<G::ROWS, kKt, kThreads>(p, plan, kMinTiles);
+  plan_share<G::ROWS, G::KT, kThreads>(p, plan, kMinTiles);
   __syncthreads();
   Cursor cur{plan.at, plan.end, plan.b, plan.head, plan.rt, plan.kt};
   Segment sg;
 
   if (warp == kComputeWarps) {
     // ------------------------------------------------------------ copies
-    const int br = min(p.c.page_rows, kKt), parts = kKt / br;
+    const int br = min(p.c.page_rows, G::KT), parts = G::KT / br;
     const int part = lane % parts, col = lane / parts % G::CH, side = lane / parts / G::CH;
     const bool has_box = side < 2;
     uint64_t pol;
@@ -202,10 +202,10 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
     }
     uint32_t st = 0;
     bool ok = true;
-    while (ok && next_segment<G::ROWS, kKt>(p, cur, sg)) {
+    while (ok && next_segment<G::ROWS, G::KT>(p, cur, sg)) {
       const int32_t *ids = p.r.table + (long long)sg.b * p.r.max_pages;
       auto id_of = [&](int kt) {  // -1: past the keys
-        const long long key = (long long)kt * kKt + part * br;
+        const long long key = (long long)kt * G::KT + part * br;
         return kt < sg.kt1 && key < sg.i.keys ? ids[key >> p.c.page_shift] : -1;
       };
       int next = id_of(sg.kt0);
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
         ok = mbar_wait(empty(s), ((st / G::STAGES) & 1) ^ 1, abort_flag);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
-        const int key = kt * kKt + part * br;
+        const int key = kt * G::KT + part * br;
         const bool valid = (unsigned)id < (unsigned)p.c.pages;
         const bool load = has_box && valid;
         if (has_box && !valid && key < sg.i.keys && side == 0 && col == 0) attn_flag(p.err);
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
   uint32_t st = 0;
   bool ok = true;  // after a wait that gave up: no more waits, but every barrier below is still met
 
-  while (next_segment<G::ROWS, kKt>(p, cur, sg)) {
+  while (next_segment<G::ROWS, G::KT>(p, cur, sg)) {
     const int rows = min(G::ROWS, sg.i.n * p.group - sg.rt * G::ROWS);
     // ---- q in the order of the A fragments (16 bytes per lane and k step)
     compute_sync();  // the last item's exchange is over
@@ -349,8 +349,8 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
       if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait<true>(full(stage), (st / G::STAGES) & 1, abort_flag));
       const uint32_t groups = *reinterpret_cast<volatile uint32_t *>(smem + G::OFF_INFO + 4 * stage);
       const uint32_t kbase = sbase + stage * G::STAGE, vbase = kbase + G::SIDE;
-      const int key0 = kt * kKt;
-      const bool masked = key0 + kKt > sg.i.len || groups != 0xFu;
+      const int key0 = kt * G::KT;
+      const bool masked = key0 + G::KT > sg.i.len || groups != (1u << (G::KT / 16)) - 1;
       if (masked) {
         // Values that must not meet a weight of 0, in the rows that this warp will read. Warps that share rows
         // write the same to them, so no barrier is needed.
@@ -745,22 +745,16 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p) {
 // ---------------------------------------------------------------------------
 // launch
 // ---------------------------------------------------------------------------
-template <class... K, class... A>
-cudaError_t launch_dependent(void (*kern)(K...), unsigned grid, int threads, size_t smem, cudaStream_t stream, A... args) {
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(grid, 1, 1);
-  lc.blockDim = dim3(threads, 1, 1);
-  lc.dynamicSmemBytes = smem;
-  lc.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, kern, args...);
-}
-
 constexpr size_t kPlanBytes = ((size_t)(65536 + 2) * 8 + 255) / 256 * 256;
+
+template <int DIM, int ROWS, int KT>
+cudaError_t launch_join(const AttnCall &c, const AttnParams &p, int grid) {
+  // Few items: each is split over many CTAs, so eight warps join a row; many: one warp does
+  const long long items = (long long)c.rows.rows * c.cache.kv_heads * ((c.max_tree * p.group + ROWS - 1) / ROWS);
+  const long long rows = (long long)c.rows.tokens * c.heads;
+  if (items * 4 <= grid) return launch_dependent(join_kernel<DIM, ROWS, KT, 8>, (unsigned)rows, 256, 0, c.stream, p);
+  return launch_dependent(join_kernel<DIM, ROWS, KT, 1>, (unsigned)((rows + 7) / 8), 256, 0, c.stream, p);
+}
 
 template <int DIM, bool E4M3, int RW>
 cudaError_t launch_rows(const AttnCall &c, AttnParams &p) {
@@ -773,23 +767,27 @@ cudaError_t launch_rows(const AttnCall &c, AttnParams &p) {
     configured.v[c.device].store(1, std::memory_order_relaxed);
   }
   CUtensorMap tk, tv;
-  const int br = std::min(c.cache.page_rows, kKt);
+  const int br = std::min(c.cache.page_rows, G::KT);
   if (!encode_cache(&tk, c.cache.k, c.cache, br, G::CW) || !encode_cache(&tv, c.cache.v, c.cache, br, G::CW))
     return cudaErrorInvalidValue;
   const int grid = std::min(G::CTAS * c.sm_count, kMaxCtas);
   cudaError_t e = launch_dependent(kern, grid, kThreads, G::SMEM, c.stream, tk, tv, p);
   if (e != cudaSuccess) return e;
-  // Few items: each is split over many CTAs, so eight warps join a row; many: one warp does
-  const long long items = (long long)c.rows.rows * c.cache.kv_heads * ((c.max_tree * p.group + G::ROWS - 1) / G::ROWS);
-  const long long rows = (long long)c.rows.tokens * c.heads;
-  if (items * 4 <= grid)
-    return launch_dependent(join_kernel<DIM, G::ROWS, kKt, 8>, (unsigned)rows, 256, 0, c.stream, p);
-  return launch_dependent(join_kernel<DIM, G::ROWS, kKt, 1>, (unsigned)((rows + 7) / 8), 256, 0, c.stream, p);
+  return launch_join<DIM, G::ROWS, G::KT>(c, p, grid);
 }
+
+template <int DIM>
+cudaError_t launch_tc(const AttnCall &c, AttnParams &p) {
+  cudaError_t e = launch_tree_tc(c, p);
+  if (e != cudaSuccess) return e;
+  return launch_join<DIM, kTcAttnRows, tc_attn_keys(DIM)>(c, p, std::min(c.sm_count, kMaxCtas));
+}
+bool uses_tc(int rows, bool e4m3) { return !e4m3 && rows > 32; }
 
 template <int DIM, bool E4M3>
 cudaError_t launch_dim(const AttnCall &c, AttnParams &p) {
   const int rows = c.max_tree * p.group;
+  if (!E4M3 && uses_tc(rows, E4M3)) return launch_tc<DIM>(c, p);
   if (rows <= 16) return launch_rows<DIM, E4M3, 1>(c, p);
   if (rows <= 32) return launch_rows<DIM, E4M3, 2>(c, p);
   return launch_rows<DIM, E4M3, 4>(c, p);
@@ -810,7 +808,7 @@ bool encode_cache(CUtensorMap *m, const KvSide &s, const KvCache &c, int box_row
 
 size_t tree_attn_workspace_bytes(int heads, int kv_heads, int dim, int max_tree) {
   const int rows = max_tree * (heads / kv_heads);
-  const int tile = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  const int tile = rows <= 16 ? 16 : rows <= 32 ? 32 : kTcAttnRows;
   return kPlanBytes + align_up((size_t)kMaxCtas * 2 * tile * (dim + 2) * sizeof(float), 256);
 }
 

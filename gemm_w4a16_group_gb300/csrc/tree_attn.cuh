@@ -21,6 +21,10 @@
 namespace w4a16 {
 
 constexpr int kMaxCtas = 320;  // CTAs of an attention launch: shares of the work list
+// the tcgen05 kernel (tree_attn_tc.cu): query rows of an item, keys of a tile, least tiles of a CTA
+constexpr int kTcAttnRows = 128;
+constexpr int tc_attn_keys(int dim) { return dim == 256 ? 64 : 128; }
+constexpr int kTcAttnMinTiles = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttnParams {
@@ -179,6 +183,23 @@ __device__ __forceinline__ bool next_segment(const AttnParams &p, Cursor &c, Seg
     }
   }
   return true;
+}
+
+cudaError_t launch_tree_tc(const AttnCall &c, const AttnParams &p);
+
+template <class... K, class... A>
+inline cudaError_t launch_dependent(void (*kern)(K...), unsigned grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(grid, 1, 1);
+  lc.blockDim = dim3(threads, 1, 1);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kern, args...);
 }
 
 // Tensor map of one side of a cache layer: (element, row, head, page), boxes of

@@ -1,0 +1,580 @@
+// Attention of drafted tokens over a paged bf16 cache on the fifth-generation
+// tensor cores (tcgen05), for rows of the page table with many query rows per
+// kv head (wide draft trees, large head groups).
+//
+// An item is 128 query rows (tokens times the heads of one kv head) of one
+// kv head. S = Q . K^T and O += P . V are M = 128 MMAs with their accumulators
+// in TMEM: a TMEM lane is one query row, so a softmax thread owns a row and
+// needs no exchange. With up to 128 query rows the cache is read once and HBM
+// bounds the kernel (a 128-key tile at dim 128 is 64 KB, 2,800 clocks of an
+// SM's share of HBM, against 1,024 clocks of MMA); with more, the row tiles
+// read it again from L2 and MMA time, softmax and L2 come near one another.
+//
+//   warp 0        copies: K and V tiles by TMA through the page table, into one
+//                 ring of slots in the order in which the MMAs take them
+//                 (K0, K1, V0, K2, V1, ...)
+//   warp 1        one thread issues all MMAs; TMEM allocation
+//   warps 4-7     softmax of the even tiles of the item
+//   warps 8-11    softmax of the odd tiles (dim 64 and 128)
+//
+// The two softmax groups keep maxima, sums and output accumulators of their
+// own, so neither waits for the other; their outputs meet at the item's end,
+// where each group forms half of the columns (both can read the lanes of
+// both). P (bf16) replaces S in TMEM and is the second MMA's A operand there;
+// V, [key][dim] in shared memory, is its B operand as it lies (MN-major). At
+// dim 256 the output takes half of TMEM, so there is one group, with two S
+// buffers. An output accumulator is rescaled only when a row's maximum has
+// grown by more than 2^8: until then the weights are up to 2^8, and the sums
+// are float32.
+//
+// P is rounded to bf16 once (2^-9 of a weight on average against the output's
+// own 2^-9); sums use the unrounded weights.
+#include <algorithm>
+
+#include "tree_attn.cuh"
+
+namespace w4a16 {
+namespace {
+
+constexpr int kTcThreads = 384;
+constexpr int kWarpCopy = 0, kWarpMma = 1, kWarpSoftmax = 4;
+constexpr int kRows = kTcAttnRows;
+constexpr int kInfo = 16;  // tiles whose key-group words are kept
+
+template <int DIM>
+struct TcGeo {
+  static constexpr int STREAMS = DIM == 256 ? 1 : 2;  // softmax groups
+  static constexpr int KT = tc_attn_keys(DIM);        // keys of a tile
+  static constexpr int CH = DIM / 64;                 // 128-byte columns of a row
+  static constexpr int SUB = KT * 128;                // one column of a K or V tile
+  static constexpr int SLOT = CH * SUB;
+  static constexpr int QSUB = kRows * 128;
+  static constexpr int Q_BYTES = CH * QSUB;
+  static constexpr int SLOTS = DIM == 64 ? 12 : DIM == 128 ? 6 : 5;
+  static constexpr int SBUFS = 2;                     // S buffers: one per stream, or two of the one
+  // TMEM columns: S (P over its first half), then O
+  static constexpr int COL_O = SBUFS * KT;
+  static constexpr int OFF_SLOT = Q_BYTES;
+  static constexpr int OFF_ML = OFF_SLOT + SLOTS * SLOT;
+  static constexpr int OFF_BAR = OFF_ML + STREAMS * kRows * 8;
+  static constexpr int NBARS = 2 * SLOTS + 2 * SBUFS + 2;
+  static constexpr int OFF_INFO = OFF_BAR + NBARS * 8;
+  static constexpr int OFF_MISC = OFF_INFO + kInfo * 4;  // TMEM address, abort flag, odd values
+  static constexpr int OFF_PLAN = OFF_MISC + 16;
+  static constexpr int SMEM = OFF_PLAN + (int)sizeof(PlanShared);
+  static_assert(COL_O + STREAMS * DIM <= 512, "TMEM budget");
+  static_assert(SMEM <= 227 * 1024 && OFF_SLOT % 1024 == 0 && OFF_PLAN % 8 == 0, "shared memory budget");
+  static_assert(SLOTS / 2 + 2 < kInfo, "a tile's word outlives its use");
+};
+
+// K-major (rows of 128 bytes, 8-row atoms 1,024 bytes apart) or MN-major (64
+// elements of the long axis per 128-byte row, `mn_block` bytes to the next 64;
+// 8 rows of the short axis per atom) operand with the 128-byte swizzle
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t mn_block) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(mn_block >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// B is MN-major
+constexpr uint32_t kIdescBMn = 1u << 16;
+
+__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// 16 / 32 consecutive columns of this thread's lane
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&f)[32]) {
+  const uint32_t *v = reinterpret_cast<const uint32_t *>(f);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+      "%30,%31,%32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t *>(&b);
+}
+
+template <int THREADS>
+__device__ __forceinline__ void softmax_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
+
+__device__ __forceinline__ uint32_t not_finite_bf16(uint32_t x) {
+  return ((x & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((x & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+}
+
+// Which of keys 32c .. 32c + 31 of a tile a row sees: `ctx` keys of the tile
+// are cached ones, then the new tokens follow, by the row's mask word
+__device__ __forceinline__ uint32_t seen_bits(int c, int ctx, unsigned long long word, uint32_t groups) {
+  const int j0 = 32 * c, off = j0 - ctx;  // off: new-token index of the first key
+  uint32_t v;
+  if (off >= 0) v = off < 64 ? (uint32_t)(word >> off) : 0u;
+  else if (off <= -32) v = 0xFFFFFFFFu;
+  else v = ((1u << -off) - 1) | ((uint32_t)word << -off);
+  const uint32_t g = groups >> (2 * c);
+  return v & ((g & 1 ? 0xFFFFu : 0u) | (g & 2 ? 0xFFFF0000u : 0u));
+}
+
+template <int DIM>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ AttnParams p) {
+  using G = TcGeo<DIM>;
+  constexpr int KT = G::KT, STREAMS = G::STREAMS;
+  constexpr int SOFT = STREAMS * 128;  // softmax threads
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + G::OFF_MISC);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + G::OFF_MISC + 4);
+  uint32_t *odd_values = reinterpret_cast<uint32_t *>(smem + G::OFF_MISC + 8);
+  volatile uint32_t *info = reinterpret_cast<volatile uint32_t *>(smem + G::OFF_INFO);
+  PlanShared &plan = *reinterpret_cast<PlanShared *>(smem + G::OFF_PLAN);
+  if (sbase & 1023u) {  // the swizzle counts from multiples of 1,024 (dynamic shared memory starts at one)
+    if (tid == 0) atomicOr(p.err, kErrTimeout);
+    return;
+  }
+  const uint32_t bars = sbase + G::OFF_BAR;
+  auto full = [&](uint32_t s) { return bars + 8 * s; };
+  auto empty = [&](uint32_t s) { return bars + 8 * (G::SLOTS + s); };
+  auto s_full = [&](uint32_t b) { return bars + 8 * (2 * G::SLOTS + b); };               // S written
+  auto p_full = [&](uint32_t b) { return bars + 8 * (2 * G::SLOTS + G::SBUFS + b); };    // P written, O rescaled
+  const uint32_t q_full = bars + 8 * (2 * G::SLOTS + 2 * G::SBUFS);  // Q written, TMEM of the last item read
+  const uint32_t o_full = q_full + 8;                                // the item's MMAs are done
+
+  if (tid == 0) {
+    for (int i = 0; i < G::SLOTS; ++i) {
+      mbar_init(full(i), 1);
+      mbar_init(empty(i), 1);
+    }
+    for (int i = 0; i < G::SBUFS; ++i) {
+      mbar_init(s_full(i), 1);
+      mbar_init(p_full(i), 4);
+    }
+    mbar_init(q_full, SOFT / 32);
+    mbar_init(o_full, 1);
+    *abort_flag = 0;
+    odd_values[0] = odd_values[1] = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();
+  plan_share<kRows, KT, kTcThreads>(p, plan, kTcAttnMinTiles);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Cursor cur{plan.at, plan.end, plan.b, plan.head, plan.rt, plan.kt};
+  Segment sg;
+
+  if (warp == kWarpCopy) {
+    // ------------------------------------------------------------ copies
+    const int br = min(p.c.page_rows, KT), parts = KT / br;
+    const int part = lane % parts, col = lane / parts;
+    const bool has_box = col < G::CH;
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    uint64_t pol;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
+    uint64_t keep;  // several row tiles come back for the same keys
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
+    uint32_t ring = 0, tile = 0;
+    bool ok = true;
+    while (ok && next_segment<kRows, KT>(p, cur, sg)) {
+      const int32_t *ids = p.r.table + (long long)sg.b * p.r.max_pages;
+      const uint64_t policy = sg.i.n * p.group > kRows ? keep : pol;
+      auto id_of = [&](int kt) {  // -1: past the keys
+        const long long key = (long long)kt * KT + part * br;
+        return kt < sg.kt1 && key < sg.i.keys ? ids[key >> p.c.page_shift] : -1;
+      };
+      auto copy = [&](const CUtensorMap *tm, int kt, int id, bool load, uint32_t loads) {
+        const uint32_t s = ring % G::SLOTS;
+        ok = ok && mbar_wait(empty(s), ((ring / G::SLOTS) & 1) ^ 1, abort_flag);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) return;
+        if (lane == 0) mbar_arrive_expect_tx(full(s), __popc(loads) * br * 128);
+        __syncwarp();
+        if (load)
+          tma_load_4d(sbase + G::OFF_SLOT + s * G::SLOT + col * G::SUB + part * br * 128, tm, col * 64,
+                      (kt * KT + part * br) & (p.c.page_rows - 1), sg.head, id, full(s), policy);
+        __syncwarp();
+        ++ring;
+      };
+      int next = id_of(sg.kt0), before = -1;
+      uint32_t loads_before = 0;
+      for (int kt = sg.kt0; ok && kt < sg.kt1; ++kt, ++tile) {
+        const int id = next;
+        next = id_of(kt + 1);
+        const bool valid = (unsigned)id < (unsigned)p.c.pages;
+        if (col == 0 && !valid && kt * KT + part * br < sg.i.keys) attn_flag(p.err);
+        const uint32_t loads = __ballot_sync(0xFFFFFFFFu, has_box && valid);
+        if (lane == 0) {
+          uint32_t groups = 0;  // 16-key groups that are there (lanes 0 .. parts - 1: the first column's boxes)
+          for (int i = 0; i < parts; ++i)
+            if (loads >> i & 1) groups |= ((1u << (br / 16)) - 1) << (i * br / 16);
+          info[tile % kInfo] = groups;
+        }
+        copy(&tm_k, kt, id, has_box && valid, loads);
+        if (kt > sg.kt0) copy(&tm_v, kt - 1, before, loads_before >> lane & 1, loads_before);
+        before = id;
+        loads_before = loads;
+      }
+      copy(&tm_v, sg.kt1 - 1, before, loads_before >> lane & 1, loads_before);
+    }
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      atomicOr(p.err, kErrTimeout);
+      // every copy issued lands before the CTA can exit
+      for (uint32_t i = 0; i < (uint32_t)G::SLOTS && i < ring; ++i) {
+        const uint32_t u = ring - 1 - i;
+        mbar_wait_drain(full(u % G::SLOTS), (u / G::SLOTS) & 1);
+      }
+    }
+  } else if (warp == kWarpMma) {
+    // ------------------------------------------------------------ MMAs
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, KT);
+      constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, DIM) | kIdescBMn;
+      uint32_t ring = 0, item = 0, tile = 0;  // tile: S buffer tile % 2, its phase tile / 2
+      bool ok = true;
+      auto take = [&]() {
+        ok = ok && mbar_wait(full(ring % G::SLOTS), (ring / G::SLOTS) & 1, abort_flag);
+        return sbase + G::OFF_SLOT + (ring % G::SLOTS) * G::SLOT;
+      };
+      auto give = [&]() {
+        tc_commit(empty(ring % G::SLOTS));
+        ++ring;
+      };
+      // O of tile `t`'s stream += P . V; `first`: the stream's first tile of the item
+      auto output = [&](uint32_t t, bool first) {
+        const uint32_t b = t % G::SBUFS;
+        ok = ok && mbar_wait(p_full(b), (t / G::SBUFS) & 1, abort_flag);
+        const uint32_t v = take();
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t o = tmem + G::COL_O + (STREAMS == 2 ? b * DIM : 0);
+#pragma unroll
+        for (int c = 0; c < KT / 16; ++c)
+          tc_mma_f16_ts(o, tmem + b * KT + 8 * c, smem_desc(v + c * 2048, G::SUB), idesc_o, first && c == 0 ? 0u : 1u);
+        give();
+      };
+      while (ok && next_segment<kRows, KT>(p, cur, sg)) {
+        ok = mbar_wait(q_full, item & 1, abort_flag);
+        ++item;
+        const int n = sg.kt1 - sg.kt0;
+        for (int i = 0; ok && i < n; ++i, ++tile) {
+          const uint32_t k = take();
+          if (!ok) break;
+          tc_fence_after();
+          // the S buffer's last P was taken by an MMA issued before this one
+#pragma unroll
+          for (int c = 0; c < DIM / 16; ++c)
+            tc_mma_f16(tmem + (tile % G::SBUFS) * KT, smem_desc(sbase + (c / 4) * G::QSUB + (c % 4) * 32, 16),
+                       smem_desc(k + (c / 4) * G::SUB + (c % 4) * 32, 16), idesc_s, c != 0 ? 1u : 0u);
+          tc_commit(s_full(tile % G::SBUFS));
+          give();
+          if (i > 0) output(tile - 1, i - 1 < STREAMS);
+        }
+        if (ok) output(tile - 1, n - 1 < STREAMS);
+        tc_commit(o_full);
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        atomicOr(p.err, kErrTimeout);
+        // every MMA issued has completed before TMEM is freed (the loop's last commit covers them)
+        if (item > 0) mbar_wait_drain(o_full, (item - 1) & 1);
+      }
+    }
+  } else if (warp >= kWarpSoftmax && warp < kWarpSoftmax + 4 * STREAMS) {
+    // ------------------------------------------------------------ softmax
+    const int stream = (warp - kWarpSoftmax) >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;  // query row of the tile: TMEM lane
+    const int st = tid - kWarpSoftmax * 32;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t o_col = lanes + G::COL_O + stream * DIM;
+    float2 *ml = reinterpret_cast<float2 *>(smem + G::OFF_ML);
+    uint32_t tile = 0, item = 0, ring = 0;
+    bool ok = true;  // after a wait that gave up: no more waits, but the barriers below are still met
+    while (next_segment<kRows, KT>(p, cur, sg)) {
+      const int rows = min(kRows, sg.i.n * p.group - sg.rt * kRows);
+      // ---- Q: K-major, 128-byte swizzle; rows past the item's are zero
+      for (int i = st; i < kRows * (DIM / 8); i += SOFT) {
+        const int r = i / (DIM / 8), c = i % (DIM / 8);
+        const int rr = sg.rt * kRows + r;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < rows)
+          x = *reinterpret_cast<const uint4 *>(p.q + (sg.i.start + rr / p.group) * p.q_token +
+                                               (sg.head * p.group + rr % p.group) * p.q_head + 8 * c);
+        sts128(sbase + (c >> 3) * G::QSUB + r * 128 + (((c & 7) ^ (r & 7)) << 4), x);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      if (st < 2) odd_values[st] = 0;
+      softmax_sync<SOFT>();
+      if (lane == 0) mbar_arrive(q_full);
+      const int rr = sg.rt * kRows + row, tok = rr / p.group;
+      unsigned long long word = 0;
+      if (row < rows) {
+        word = p.mask ? (unsigned long long)p.mask[sg.i.start + tok] : (2ull << tok) - 1;
+        if (sg.i.n < 64) word &= (1ull << sg.i.n) - 1;
+      }
+      float m = -INFINITY, l = 0.f;
+      const int n = sg.kt1 - sg.kt0;
+      const bool idle = quarter * 32 >= rows;  // a warp without rows: its P is never looked at
+      for (int i = 0; i < n; ++i, ++tile) {
+        // slots of the item: K0, K1, V0, K2, V1, ..., K(n-1), V(n-2), V(n-1)
+        const uint32_t v_slot = ring + (i + 1 < n ? 2 * i + 2 : 2 * n - 1);
+        if (STREAMS == 2 && (int)(tile & 1) != stream) continue;
+        const uint32_t b = tile % G::SBUFS;
+        const uint32_t s_col = lanes + b * KT;
+        if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(s_full(b), (tile / G::SBUFS) & 1, abort_flag));
+        tc_fence_after();
+        const uint32_t groups = info[tile % kInfo];
+        const int key0 = (sg.kt0 + i) * KT;
+        const bool masked = key0 + KT > sg.i.len || groups != (1u << (KT / 16)) - 1;
+        if (masked) {
+          // Values that must not meet a weight of 0: zeroed before the MMA reads them. All threads of this group.
+          const uint32_t v = v_slot % G::SLOTS;
+          if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(full(v), (v_slot / G::SLOTS) & 1, abort_flag));
+          const uint32_t vbase = sbase + G::OFF_SLOT + v * G::SLOT;
+          for (int e = st & 127; e < KT * (DIM / 8); e += 128) {
+            const int j = e / (DIM / 8), c = e % (DIM / 8), key = key0 + j;
+            const bool there = key < sg.i.keys && (groups >> (j >> 4) & 1);
+            if (there && key < sg.i.len) continue;
+            const uint32_t a = vbase + (c >> 3) * G::SUB + j * 128 + (((c & 7) ^ (j & 7)) << 4);
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (there) {
+              x = lds128(a);
+              const uint32_t b0 = not_finite_bf16(x.x), b1 = not_finite_bf16(x.y), b2 = not_finite_bf16(x.z),
+                             b3 = not_finite_bf16(x.w);
+              if (!(b0 | b1 | b2 | b3)) continue;
+              x = make_uint4(x.x & ~b0, x.y & ~b1, x.z & ~b2, x.w & ~b3);
+              const int nw = key - sg.i.len;
+              atomicOr(&odd_values[nw >> 5], 1u << (nw & 31));
+            }
+            sts128(a, x);
+          }
+          fence_proxy_async_smem();
+        }
+        if (!idle) {
+          // ---- maximum of the row
+          const int ctx = sg.i.len - key0;
+          float top = -INFINITY;
+          {
+            float x[2][32];
+            tmem_ld32_nowait(s_col, x[0]);
+#pragma unroll
+            for (int c = 0; c < KT / 32; ++c) {
+              tmem_wait_ld();
+              if (c + 1 < KT / 32) tmem_ld32_nowait(s_col + 32 * (c + 1), x[(c + 1) & 1]);
+              float(&y)[32] = x[c & 1];
+              if (masked) {
+                const uint32_t seen = seen_bits(c, ctx, word, groups);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) y[e] = seen >> e & 1 ? y[e] : -INFINITY;
+              }
+              float t4[4] = {y[0], y[1], y[2], y[3]};
+#pragma unroll
+              for (int e = 4; e < 32; ++e) t4[e & 3] = fmaxf(t4[e & 3], y[e]);
+              top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
+            }
+          }
+          const float mn = fmaxf(m, top * p.scale_log2);
+          // rescale when the maximum has grown by more than 2^8 (or was -inf)
+          const bool grow = mn > m + 8.f;
+          const bool first = i < STREAMS;  // this stream's first tile: no output yet
+          if (__any_sync(0xFFFFFFFFu, grow)) {
+            const float alpha = grow ? exp2_approx(m - mn) : 1.f;
+            if (grow) m = mn;
+            l *= alpha;
+            if (!first) {
+#pragma unroll
+              for (int c = 0; c < DIM / 32; ++c) {
+                float x[32];
+                tmem_ld32_nowait(o_col + 32 * c, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] *= alpha;
+                tmem_st32(o_col + 32 * c, x);
+              }
+            }
+          }
+          // ---- weights, over the first half of S's columns (each chunk is read before any P reaches it)
+          const float base = m == -INFINITY ? 0.f : m;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          {
+            float x[2][32];
+            tmem_ld32_nowait(s_col, x[0]);
+#pragma unroll
+            for (int c = 0; c < KT / 32; ++c) {
+              tmem_wait_ld();
+              if (c + 1 < KT / 32) tmem_ld32_nowait(s_col + 32 * (c + 1), x[(c + 1) & 1]);
+              float(&y)[32] = x[c & 1];
+              if (masked) {
+                const uint32_t seen = seen_bits(c, ctx, word, groups);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) y[e] = seen >> e & 1 ? y[e] : -INFINITY;
+              }
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const float a = exp2_approx(fmaf(y[e], p.scale_log2, -base));
+                const float d = exp2_approx(fmaf(y[e + 1], p.scale_log2, -base));
+                sum[e & 2] += a;
+                sum[(e & 2) + 1] += d;
+                w[e >> 1] = pack2(a, d);
+              }
+              tmem_st16(s_col + 16 * c, w);
+            }
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(b));
+      }
+      ring += 2 * n;
+      // ---- the item's output
+      ml[stream * kRows + row] = make_float2(m, l);
+      if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(o_full, item & 1, abort_flag));
+      ++item;
+      softmax_sync<SOFT>();
+      tc_fence_after();
+      if (!idle) {
+        // streams with tiles: the one of the item's first tile, and the other when there are two
+        const uint32_t t0 = tile - n;
+        const int s0 = STREAMS == 2 ? (int)(t0 & 1) : 0;
+        const bool both = STREAMS == 2 && n > 1;
+        const float2 a = ml[s0 * kRows + row], c2 = both ? ml[(s0 ^ 1) * kRows + row] : make_float2(-INFINITY, 0.f);
+        const float M = fmaxf(a.x, c2.x), base = M == -INFINITY ? 0.f : M;
+        const float f0 = exp2_approx(a.x - base), f1 = exp2_approx(c2.x - base);
+        const float L = a.y * f0 + c2.y * f1;
+        const bool whole = sg.whole(), mine = row < rows;
+        const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+        const float g0 = whole ? f0 * inv : f0, g1 = whole ? f1 * inv : f1;
+        // slot 0: the item began before this share; slot 1: it goes on after it
+        float *po = p.partials + (((long long)blockIdx.x * 2 + (sg.kt0 > 0 ? 0 : 1)) * kRows + row) * (DIM + 2);
+        uint16_t *out = p.out + ((long long)(sg.i.start + tok) * p.heads + sg.head * p.group + rr % p.group) * DIM;
+        const uint32_t odd[2] = {odd_values[0], odd_values[1]};
+        const uint32_t oc = lanes + G::COL_O;
+        constexpr int COLS = DIM / STREAMS;  // columns of a group
+#pragma unroll 1
+        for (int c = stream * COLS; c < (stream + 1) * COLS; c += 32) {
+          float x[32];
+          tmem_ld32_nowait(oc + s0 * DIM + c, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] *= g0;
+          if (both) {
+            float y[32];
+            tmem_ld32_nowait(oc + (s0 ^ 1) * DIM + c, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = fmaf(y[e], g1, x[e]);
+          }
+          if (odd[0] | odd[1]) {
+            for (int j = 0; j < sg.i.n; ++j) {
+              if (!(odd[j >> 5] >> (j & 31) & 1) || !(word >> j & 1)) continue;
+              const long long pos = (long long)sg.i.len + j;
+              const int id = p.r.table[(long long)sg.b * p.r.max_pages + (pos >> p.c.page_shift)];
+              const uint16_t *v = reinterpret_cast<const uint16_t *>(p.c.v.base + (long long)id * p.c.v.page +
+                                                                     (long long)sg.head * p.c.v.head +
+                                                                     (pos & (p.c.page_rows - 1)) * p.c.v.row);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float f = __uint_as_float((uint32_t)v[c + e] << 16);
+                if (!(fabsf(f) < INFINITY)) x[e] += f;
+              }
+            }
+          }
+          if (mine && whole) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              *reinterpret_cast<uint4 *>(out + c + e) = make_uint4(pack2(x[e], x[e + 1]), pack2(x[e + 2], x[e + 3]),
+                                                                   pack2(x[e + 4], x[e + 5]), pack2(x[e + 6], x[e + 7]));
+          } else if (mine) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) *reinterpret_cast<float2 *>(po + c + e) = make_float2(x[e], x[e + 1]);
+          }
+        }
+        if (mine && !whole && stream == 0) *reinterpret_cast<float2 *>(po + DIM) = make_float2(M, L);
+      }
+      // the next item's Q, odd values and maxima: after everyone is here
+      softmax_sync<SOFT>();
+    }
+    if (!ok) {
+      *abort_flag = 1;
+      if (lane == 0) atomicOr(p.err, kErrTimeout);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int DIM>
+cudaError_t launch_tc_dim(const AttnCall &c, const AttnParams &p) {
+  using G = TcGeo<DIM>;
+  auto kern = tree_tc_kernel<DIM>;
+  static PerDevice configured;
+  if (!configured.v[c.device].load(std::memory_order_relaxed)) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
+    if (e != cudaSuccess) return e;
+    configured.v[c.device].store(1, std::memory_order_relaxed);
+  }
+  CUtensorMap tk, tv;
+  const int br = std::min(c.cache.page_rows, G::KT);
+  if (!encode_cache(&tk, c.cache.k, c.cache, br, 128) || !encode_cache(&tv, c.cache.v, c.cache, br, 128))
+    return cudaErrorInvalidValue;
+  return launch_dependent(kern, std::min(c.sm_count, kMaxCtas), kTcThreads, G::SMEM, c.stream, tk, tv, p);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_tc(const AttnCall &c, const AttnParams &p) {
+  switch (c.cache.dim) {
+    case 64: return launch_tc_dim<64>(c, p);
+    case 128: return launch_tc_dim<128>(c, p);
+    default: return launch_tc_dim<256>(c, p);
+  }
+}
+
+}  // namespace w4a16
