@@ -605,7 +605,8 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
     const bool whole = sg.whole();
     // slot 0: the item began before this share; slot 1: it goes on after it
     const int slot = sg.kt0 > 0 ? 0 : 1;
-    float *part = p.partials + ((long long)blockIdx.x * 2 + slot) * G::ROWS * (DIM + 2);
+    const Partial<DIM, G::ROWS> part(p.partials, blockIdx.x, slot);
+    if (tid == 0 && sg.kt0 > 0 && sg.kt1 == sg.ktiles) leave_record<G::ROWS>(p, sg, plan.at, plan.share, rows);
     const float vs = E4M3 ? p.c.v.scale[sg.head] : 1.f;
 #pragma unroll
     for (int sl = 0; sl < KW; ++sl) {
@@ -617,7 +618,6 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
         const int rr = sg.rt * G::ROWS + r, tok = sg.i.start + rr / p.group, h = sg.head * p.group + rr % p.group;
         const float inv = l[i] > 0.f || l[i] != l[i] ? vs / l[i] : 0.f;
         uint16_t *out = p.out + ((long long)tok * p.heads + h) * DIM;
-        float *po = part + (long long)r * (DIM + 2);
 #pragma unroll
         for (int n = 0; n < SLICE; n += (E4M3 ? 2 : 1)) {
           // the thread's columns: 8n + 2t, 8n + 2t + 1, or with 8-bit values 4 in a run over two tiles
@@ -648,12 +648,13 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
                   make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
             else
               *reinterpret_cast<uint32_t *>(out + d0) = pack_bf16(x[0] * inv, x[1] * inv);
+          } else if constexpr (E4M3) {
+            *reinterpret_cast<float4 *>(part.at(r, d0)) = make_float4(x[0], x[1], x[2], x[3]);
           } else {
-#pragma unroll
-            for (int e = 0; e < NC; e += 2) *reinterpret_cast<float2 *>(po + d0 + e) = make_float2(x[e], x[e + 1]);
+            *reinterpret_cast<float2 *>(part.at(r, d0)) = make_float2(x[0], x[1]);
           }
         }
-        if (!whole && t == 0 && sl == 0) *reinterpret_cast<float2 *>(po + DIM) = make_float2(m[i], l[i]);
+        if (!whole && t == 0 && sl == 0) *part.ml(r) = make_float2(m[i], l[i]);
       }
     }
   }
@@ -664,80 +665,112 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
 }
 
 // ---------------------------------------------------------------------------
-// Joining partials: WPR warps per query row (a token's head). The weights
-// 2^(m_c - M) of the CTAs' partials are formed first, so the sums over them
-// have no chain of dependent steps.
+// Joining partials: WPR warps per query row of an item that was split. Every
+// block lists the records (a scan over one number per CTA) and takes its share
+// of their rows. The weights 2^(m_c - M) of a row's partials are formed first,
+// so the sums over them have no chain of dependent steps.
 // ---------------------------------------------------------------------------
-template <int DIM, int ROWS, int KT, int WPR>
-__global__ void __launch_bounds__(256) join_kernel(const AttnParams p) {
-  constexpr int V = DIM / 32;
-  __shared__ float acc[WPR > 1 ? 8 : 1][DIM];
+constexpr int kJoinThreads = 256;
+
+template <int DIM, int ROWS, int WPR>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnParams p, int ctas) {
+  constexpr int V = DIM > 128 ? DIM / 128 : 1;  // blocks of four elements of a lane
+  constexpr int TEAMS = 8 / WPR;
+  using Part = Partial<DIM, ROWS>;
+  __shared__ int ends[kMaxCtas];  // rows of records 0 .. c
+  __shared__ int sums[8];
+  __shared__ float4 acc[WPR > 1 ? 8 : 1][DIM / 4];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * (8 / WPR) + warp / WPR;
-  const int wi = warp % WPR;
-  const int tok = (int)(row / p.heads), h = (int)(row % p.heads);
-  if (tok >= p.r.tokens) return;  // WPR is 1 or 8: whole blocks leave, or no barrier follows
-  int b = 0;
-  for (int hi = p.r.rows; b < hi;) {
-    const int mid = (b + hi) >> 1;
-    if (p.r.starts[mid + 1] > tok) hi = mid;
-    else b = mid + 1;
-  }
-  if (b >= p.r.rows) return;
-  const RowInfo i = row_info(p, b, false);
-  if (i.n == 0 || tok < i.start || tok >= i.start + i.n) return;
-  const int head = h / p.group, rr = (tok - i.start) * p.group + h % p.group;
-  const int kt = key_tiles<KT>(i);
-  const long long share = p.plan[0];
-  const long long t0 = p.plan[1 + b] + ((long long)head * row_tiles<ROWS>(i, p.group) + rr / ROWS) * kt;
-  const int c0 = (int)(t0 / share), c1 = (int)((t0 + kt - 1) / share);
-  if (c0 == c1) return;  // finished where it was computed
-  const int n = c1 - c0 + 1;
-  auto part = [&](int c) {
-    return p.partials + (((long long)(c0 + c) * 2 + (c == 0 ? 1 : 0)) * ROWS + rr % ROWS) * (DIM + 2);
-  };
-  float M = -INFINITY;
-  for (int c = lane; c < n; c += 32) M = fmaxf(M, part(c)[DIM]);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int total = 0;
+  for (int c0 = 0; c0 < ctas; c0 += kJoinThreads) {
+    int v = c0 + tid < ctas ? p.joins[c0 + tid] : 0;
 #pragma unroll
-  for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
-  const float base = M == -INFINITY ? 0.f : M;
-  float L = 0.f;
-  for (int c = lane; c < n; c += 32) L += part(c)[DIM + 1] * exp2_approx(part(c)[DIM] - base);
-#pragma unroll
-  for (int d = 16; d; d >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, d);
-  float x[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) x[e] = 0.f;
-#pragma unroll 4
-  for (int c = wi; c < n; c += WPR) {
-    const float *s = part(c);
-    const float w = exp2_approx(s[DIM] - base);
-#pragma unroll
-    for (int e = 0; e < V; e += 2) {
-      const float2 y = *reinterpret_cast<const float2 *>(s + e * 32 + lane * 2);
-      x[e] = fmaf(w, y.x, x[e]);
-      x[e + 1] = fmaf(w, y.y, x[e + 1]);
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+      if (lane >= d) v += o;
     }
-  }
-  const float inv = (L > 0.f || L != L) ? (p.c.e4m3 ? p.c.v.scale[head] : 1.f) / L : 0.f;
-  uint32_t *out = reinterpret_cast<uint32_t *>(p.out + ((long long)tok * p.heads + h) * DIM);
-  if constexpr (WPR == 1) {
-#pragma unroll
-    for (int e = 0; e < V; e += 2) out[e * 16 + lane] = pack_bf16(x[e] * inv, x[e + 1] * inv);
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; e += 2) *reinterpret_cast<float2 *>(&acc[warp][e * 32 + lane * 2]) = make_float2(x[e], x[e + 1]);
+    if (lane == 31) sums[warp] = v;
     __syncthreads();
-    for (int d = threadIdx.x; d < DIM / 2; d += 256) {
-      float a = 0.f, c = 0.f;
+    int before = total;
 #pragma unroll
-      for (int w = 0; w < WPR; ++w) {
-        a += acc[w][2 * d];
-        c += acc[w][2 * d + 1];
+    for (int w = 0; w < 8; ++w) {
+      if (w < warp) before += sums[w];
+      total += sums[w];
+    }
+    if (c0 + tid < ctas) ends[c0 + tid] = before + v;
+    __syncthreads();
+  }
+  const int team = warp / WPR, wi = warp % WPR;
+  const int step = gridDim.x * TEAMS;
+  // (with WPR = 8 a block is one team, so all of it goes round together)
+  for (int e = blockIdx.x * TEAMS + team; e < total; e += step) {
+    int c1 = 0;
+    for (int hi = ctas; c1 < hi;) {
+      const int mid = (c1 + hi) >> 1;
+      if (ends[mid] > e) hi = mid;
+      else c1 = mid + 1;
+    }
+    const int r = e - (c1 ? ends[c1 - 1] : 0);
+    const int4 rec = reinterpret_cast<const int4 *>(p.joins + kMaxCtas)[c1];
+    const int c0 = rec.x, n = c1 - c0 + 1;
+    // the first CTA ended its share inside the item (slot 1), the others began theirs in it (slot 0)
+    auto part = [&](int c) { return Part(p.partials, c0 + c, c == 0 ? 1 : 0); };
+    float M = -INFINITY;
+    for (int c = lane; c < n; c += 32) M = fmaxf(M, part(c).ml(r)->x);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
+    const float base = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    for (int c = lane; c < n; c += 32) {
+      const float2 ml = *part(c).ml(r);
+      L += ml.y * exp2_approx(ml.x - base);
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, d);
+    float4 x[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int c = wi; c < n; c += WPR) {
+      const Part s = part(c);
+      const float w = exp2_approx(s.ml(r)->x - base);
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        if (lane >= DIM / 4) continue;
+        const float4 y = *reinterpret_cast<const float4 *>(s.at(r, 4 * (lane + 32 * k)));
+        x[k].x = fmaf(w, y.x, x[k].x);
+        x[k].y = fmaf(w, y.y, x[k].y);
+        x[k].z = fmaf(w, y.z, x[k].z);
+        x[k].w = fmaf(w, y.w, x[k].w);
       }
-      out[d] = pack_bf16(a * inv, c * inv);
+    }
+    const float inv = (L > 0.f || L != L) ? (p.c.e4m3 ? p.c.v.scale[rec.w] : 1.f) / L : 0.f;
+    const int rr = rec.z + r, tok = rec.y + rr / p.group;
+    uint2 *out = reinterpret_cast<uint2 *>(p.out + ((long long)tok * p.heads + rec.w * p.group + rr % p.group) * DIM);
+    auto store = [&](int d4, const float4 &y) {
+      out[d4] = make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+    };
+    if constexpr (WPR == 1) {
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (lane < DIM / 4) store(lane + 32 * k, x[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (lane < DIM / 4) acc[warp][lane + 32 * k] = x[k];
+      __syncthreads();
+      if (tid < DIM / 4) {
+        float4 y = acc[0][tid];
+#pragma unroll
+        for (int w = 1; w < WPR; ++w) {
+          const float4 z = acc[w][tid];
+          y = make_float4(y.x + z.x, y.y + z.y, y.z + z.z, y.w + z.w);
+        }
+        store(tid, y);
+      }
+      __syncthreads();
     }
   }
 }
@@ -745,15 +778,17 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p) {
 // ---------------------------------------------------------------------------
 // launch
 // ---------------------------------------------------------------------------
-constexpr size_t kPlanBytes = ((size_t)(65536 + 2) * 8 + 255) / 256 * 256;
+constexpr size_t kJoinBytes = ((size_t)kMaxCtas * 5 * sizeof(int) + 255) / 256 * 256;
 
-template <int DIM, int ROWS, int KT>
-cudaError_t launch_join(const AttnCall &c, const AttnParams &p, int grid) {
+template <int DIM, int ROWS>
+cudaError_t launch_join(const AttnCall &c, const AttnParams &p, int ctas) {
   // Few items: each is split over many CTAs, so eight warps join a row; many: one warp does
   const long long items = (long long)c.rows.rows * c.cache.kv_heads * ((c.max_tree * p.group + ROWS - 1) / ROWS);
-  const long long rows = (long long)c.rows.tokens * c.heads;
-  if (items * 4 <= grid) return launch_dependent(join_kernel<DIM, ROWS, KT, 8>, (unsigned)rows, 256, 0, c.stream, p);
-  return launch_dependent(join_kernel<DIM, ROWS, KT, 1>, (unsigned)((rows + 7) / 8), 256, 0, c.stream, p);
+  // at most one record per CTA and per item, of at most ROWS rows
+  const long long rows = std::min((long long)ctas, items) * std::min(ROWS, c.max_tree * p.group);
+  if (items * 4 <= ctas)
+    return launch_dependent(join_kernel<DIM, ROWS, 8>, (unsigned)std::min(rows, 8LL * c.sm_count), kJoinThreads, 0, c.stream, p, ctas);
+  return launch_dependent(join_kernel<DIM, ROWS, 1>, (unsigned)std::min((rows + 7) / 8, 4LL * c.sm_count), kJoinThreads, 0, c.stream, p, ctas);
 }
 
 template <int DIM, bool E4M3, int RW>
@@ -773,16 +808,16 @@ cudaError_t launch_rows(const AttnCall &c, AttnParams &p) {
   const int grid = std::min(G::CTAS * c.sm_count, kMaxCtas);
   cudaError_t e = launch_dependent(kern, grid, kThreads, G::SMEM, c.stream, tk, tv, p);
   if (e != cudaSuccess) return e;
-  return launch_join<DIM, G::ROWS, G::KT>(c, p, grid);
+  return launch_join<DIM, G::ROWS>(c, p, grid);
 }
 
 template <int DIM>
 cudaError_t launch_tc(const AttnCall &c, AttnParams &p) {
   cudaError_t e = launch_tree_tc(c, p);
   if (e != cudaSuccess) return e;
-  return launch_join<DIM, kTcAttnRows, tc_attn_keys(DIM)>(c, p, std::min(c.sm_count, kMaxCtas));
+  return launch_join<DIM, kTcAttnRows>(c, p, std::min(c.sm_count, kMaxCtas));
 }
-bool uses_tc(int rows, bool e4m3) { return !e4m3 && rows > 32; }
+bool uses_tc(int rows, bool e4m3) { return !e4m3 && rows > 16; }
 
 template <int DIM, bool E4M3>
 cudaError_t launch_dim(const AttnCall &c, AttnParams &p) {
@@ -808,8 +843,8 @@ bool encode_cache(CUtensorMap *m, const KvSide &s, const KvCache &c, int box_row
 
 size_t tree_attn_workspace_bytes(int heads, int kv_heads, int dim, int max_tree) {
   const int rows = max_tree * (heads / kv_heads);
-  const int tile = rows <= 16 ? 16 : rows <= 32 ? 32 : kTcAttnRows;
-  return kPlanBytes + align_up((size_t)kMaxCtas * 2 * tile * (dim + 2) * sizeof(float), 256);
+  const int tile = rows <= 16 ? 16 : kTcAttnRows;
+  return kJoinBytes + align_up((size_t)kMaxCtas * 2 * tile * (dim + 2) * sizeof(float), 256);
 }
 
 cudaError_t launch_tree_attention(const AttnCall &c) {
@@ -825,8 +860,8 @@ cudaError_t launch_tree_attention(const AttnCall &c) {
   p.max_tree = c.max_tree;
   p.scale_log2 = c.scale * kLog2e;
   p.out = c.out;
-  p.plan = static_cast<long long *>(c.workspace);
-  p.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(c.workspace) + kPlanBytes);
+  p.joins = static_cast<int *>(c.workspace);
+  p.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(c.workspace) + kJoinBytes);
   p.err = c.err;
   switch (c.cache.dim) {
     case 64: return c.cache.e4m3 ? launch_dim<64, true>(c, p) : launch_dim<64, false>(c, p);

@@ -13,7 +13,8 @@
 // workspace, and a second kernel joins them in the order of the CTAs, so
 // results do not depend on timing. A CTA leaves at most two partials: of the
 // item it begins in the middle of (slot 0), and of the one it does not end
-// (slot 1).
+// (slot 1). The CTA that ends an item which others began leaves a record of it,
+// at most one per CTA, and the joining kernel works through the records.
 #pragma once
 
 #include "w4a16_internal.h"
@@ -36,9 +37,22 @@ struct AttnParams {
   int heads, group, max_tree;
   float scale_log2;  // scale * log2(e): scores are kept in powers of two
   uint16_t *out;
-  float *partials;       // [kMaxCtas][2][ROWS][DIM + 2]
-  long long *plan;       // [0] share, [1 + b] first tile of row b
+  float *partials;       // [kMaxCtas][2] partials, see Partial
+  int *joins;            // [kMaxCtas] query rows of the item that a CTA ended for others (0: none), then
+                         // [kMaxCtas] of its first CTA, first token, first query row and kv head
   int *err;
+};
+
+// One partial: unnormalised outputs as [DIM / 4][ROWS] blocks of four elements
+// of a row, so that threads that own neighbouring rows write neighbouring
+// addresses, then maximum and sum of every row
+template <int DIM, int ROWS>
+struct Partial {
+  static constexpr int kFloats = ROWS * (DIM + 2);
+  float *base;
+  __device__ Partial(float *all, long long cta, int slot) : base(all + (cta * 2 + slot) * kFloats) {}
+  __device__ float *at(int r, int d) const { return base + ((d >> 2) * ROWS + r) * 4 + (d & 3); }
+  __device__ float2 *ml(int r) const { return reinterpret_cast<float2 *>(base + ROWS * DIM) + r; }
 };
 
 // One row of the table as the work list sees it
@@ -87,20 +101,20 @@ struct Cursor {
 
 struct PlanShared {
   long long sums[16];
-  long long at, end;
+  long long at, end, share;
   int b, head, rt, kt;
 };
 
 // The CTA's share, found by all NT threads: thread i sums the tiles of its
 // own run of rows, a block scan places the runs, and the thread whose run holds
-// the share's first tile walks it. CTA 0 also writes the plan that the joining
-// kernel reads. The caller synchronises before it reads `s`.
+// the share's first tile walks it. The CTA's record is cleared. The caller
+// synchronises before it reads `s`.
 template <int ROWS, int KT, int NT>
 __device__ void plan_share(const AttnParams &p, PlanShared &s, int min_tiles) {
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int per = (p.r.rows + NT - 1) / NT;
   const int b0 = min(tid * per, p.r.rows), b1 = min(b0 + per, p.r.rows);
-  const bool flag = blockIdx.x == 0;
+  const bool flag = blockIdx.x == 0;  // one CTA reports rows that cannot be
   long long mine = 0;
   for (int b = b0; b < b1; ++b) mine += tiles_of<ROWS, KT>(row_info(p, b, flag), p);
   long long upto = mine;
@@ -123,17 +137,11 @@ __device__ void plan_share(const AttnParams &p, PlanShared &s, int min_tiles) {
   const long long ctas = max(1ll, min((long long)gridDim.x, total / min_tiles));
   const long long share = max(1ll, (total + ctas - 1) / ctas);
   const long long at = min(share * blockIdx.x, total), end = min(at + share, total);
-  if (flag) {
-    long long f = first;
-    for (int b = b0; b < b1; ++b) {
-      p.plan[1 + b] = f;
-      f += tiles_of<ROWS, KT>(row_info(p, b, false), p);
-    }
-    if (tid == 0) p.plan[0] = share;
-  }
   if (tid == 0) {
     s.at = at;
     s.end = end;
+    s.share = share;
+    p.joins[blockIdx.x] = 0;
   }
   if (at < end && first <= at && at < first + mine) {
     long long f = first;
@@ -160,6 +168,15 @@ struct Segment {
   int b, head, rt, kt0, kt1, ktiles;
   __device__ bool whole() const { return kt0 == 0 && kt1 == ktiles; }
 };
+
+// Leaves the record of an item that this CTA ends and others began (one
+// thread; `kt0` > 0 only at the share's start)
+template <int ROWS>
+__device__ __forceinline__ void leave_record(const AttnParams &p, const Segment &s, long long at, long long share, int rows) {
+  int4 *rec = reinterpret_cast<int4 *>(p.joins + kMaxCtas);
+  rec[blockIdx.x] = make_int4((int)((at - s.kt0) / share), s.i.start, s.rt * ROWS, s.head);
+  p.joins[blockIdx.x] = rows;
+}
 
 // Next segment of the share (false: none is left)
 template <int ROWS, int KT>

@@ -121,6 +121,29 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<uint32_t *>(&b);
 }
 
+// two float32 values in one 64-bit register, and the packed operations on them
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 halves(f32x2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 template <int THREADS>
 __device__ __forceinline__ void softmax_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
@@ -198,6 +221,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   Cursor cur{plan.at, plan.end, plan.b, plan.head, plan.rt, plan.kt};
   Segment sg;
 
+  // A softmax thread holds a row's 128 scores. The block is launched with 384 x 168 registers; the first warpgroup
+  // (copies, MMAs) keeps 56 each, and the two softmax groups (at dim 256 one of them) get 224 each:
+  // 128 * 56 + 256 * 224 = 384 * 168.
+  if (warp < kWarpSoftmax) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == kWarpCopy) {
     // ------------------------------------------------------------ copies
     const int br = min(p.c.page_rows, KT), parts = KT / br;
@@ -318,7 +346,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (item > 0) mbar_wait_drain(o_full, (item - 1) & 1);
       }
     }
-  } else if (warp >= kWarpSoftmax && warp < kWarpSoftmax + 4 * STREAMS) {
+  }
+  } else if (warp < kWarpSoftmax + 4 * STREAMS) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     // ------------------------------------------------------------ softmax
     const int stream = (warp - kWarpSoftmax) >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;  // query row of the tile: TMEM lane
@@ -331,14 +361,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     while (next_segment<kRows, KT>(p, cur, sg)) {
       const int rows = min(kRows, sg.i.n * p.group - sg.rt * kRows);
       // ---- Q: K-major, 128-byte swizzle; rows past the item's are zero
-      for (int i = st; i < kRows * (DIM / 8); i += SOFT) {
-        const int r = i / (DIM / 8), c = i % (DIM / 8);
-        const int rr = sg.rt * kRows + r;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < rows)
-          x = *reinterpret_cast<const uint4 *>(p.q + (sg.i.start + rr / p.group) * p.q_token +
-                                               (sg.head * p.group + rr % p.group) * p.q_head + 8 * c);
-        sts128(sbase + (c >> 3) * G::QSUB + r * 128 + (((c & 7) ^ (r & 7)) << 4), x);
+      long long *q_row = reinterpret_cast<long long *>(smem + G::OFF_ML);  // between two items' use of it
+      if (st < kRows) {
+        const int rr = sg.rt * kRows + st;
+        q_row[st] = st < rows ? (sg.i.start + rr / p.group) * p.q_token + (sg.head * p.group + rr % p.group) * p.q_head : -1;
+      }
+      softmax_sync<SOFT>();
+      constexpr int QN = kRows * (DIM / 8) / SOFT, QB = QN < 8 ? QN : 8;  // 16-byte pieces of a thread, and per batch
+#pragma unroll 1
+      for (int i0 = 0; i0 < QN; i0 += QB) {
+        uint4 x[QB];
+#pragma unroll
+        for (int u = 0; u < QB; ++u) {
+          const int e = st + (i0 + u) * SOFT;
+          const long long q = q_row[e / (DIM / 8)];
+          x[u] = q >= 0 ? *reinterpret_cast<const uint4 *>(p.q + q + 8 * (e % (DIM / 8))) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < QB; ++u) {
+          const int e = st + (i0 + u) * SOFT, r = e / (DIM / 8), c = e % (DIM / 8);
+          sts128(sbase + (c >> 3) * G::QSUB + r * 128 + (((c & 7) ^ (r & 7)) << 4), x[u]);
+        }
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -390,28 +433,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           fence_proxy_async_smem();
         }
         if (!idle) {
-          // ---- maximum of the row
-          const int ctx = sg.i.len - key0;
-          float top = -INFINITY;
-          {
-            float x[2][32];
-            tmem_ld32_nowait(s_col, x[0]);
+          // ---- the row's scores of the tile, all in registers, and their maximum
+          float x[KT / 32][32];
+#pragma unroll
+          for (int c = 0; c < KT / 32; ++c) tmem_ld32_nowait(s_col + 32 * c, x[c]);
+          tmem_wait_ld();
+          if (masked) {
 #pragma unroll
             for (int c = 0; c < KT / 32; ++c) {
-              tmem_wait_ld();
-              if (c + 1 < KT / 32) tmem_ld32_nowait(s_col + 32 * (c + 1), x[(c + 1) & 1]);
-              float(&y)[32] = x[c & 1];
-              if (masked) {
-                const uint32_t seen = seen_bits(c, ctx, word, groups);
+              const uint32_t seen = seen_bits(c, sg.i.len - key0, word, groups);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) y[e] = seen >> e & 1 ? y[e] : -INFINITY;
-              }
-              float t4[4] = {y[0], y[1], y[2], y[3]};
-#pragma unroll
-              for (int e = 4; e < 32; ++e) t4[e & 3] = fmaxf(t4[e & 3], y[e]);
-              top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
+              for (int e = 0; e < 32; ++e) x[c][e] = seen >> e & 1 ? x[c][e] : -INFINITY;
             }
           }
+          float t4[4] = {x[0][0], x[0][1], x[0][2], x[0][3]};
+#pragma unroll
+          for (int c = 0; c < KT / 32; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) t4[k] = fmaxf(fmaxf(t4[k], x[c][e + k]), x[c][e + 4 + k]);
+          const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
           const float mn = fmaxf(m, top * p.scale_log2);
           // rescale when the maximum has grown by more than 2^8 (or was -inf)
           const bool grow = mn > m + 8.f;
@@ -423,44 +465,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!first) {
 #pragma unroll
               for (int c = 0; c < DIM / 32; ++c) {
-                float x[32];
-                tmem_ld32_nowait(o_col + 32 * c, x);
+                float y[32];
+                tmem_ld32_nowait(o_col + 32 * c, y);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] *= alpha;
-                tmem_st32(o_col + 32 * c, x);
+                for (int e = 0; e < 32; ++e) y[e] *= alpha;
+                tmem_st32(o_col + 32 * c, y);
               }
             }
           }
-          // ---- weights, over the first half of S's columns (each chunk is read before any P reaches it)
+          // ---- weights, over the first half of S's columns
           const float base = m == -INFINITY ? 0.f : m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          {
-            float x[2][32];
-            tmem_ld32_nowait(s_col, x[0]);
+          const f32x2 scale2 = pair(p.scale_log2, p.scale_log2), base2 = pair(-base, -base);
+          f32x2 sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
 #pragma unroll
-            for (int c = 0; c < KT / 32; ++c) {
-              tmem_wait_ld();
-              if (c + 1 < KT / 32) tmem_ld32_nowait(s_col + 32 * (c + 1), x[(c + 1) & 1]);
-              float(&y)[32] = x[c & 1];
-              if (masked) {
-                const uint32_t seen = seen_bits(c, ctx, word, groups);
+          for (int c = 0; c < KT / 32; ++c) {
+            uint32_t w[16];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) y[e] = seen >> e & 1 ? y[e] : -INFINITY;
-              }
-              uint32_t w[16];
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                const float a = exp2_approx(fmaf(y[e], p.scale_log2, -base));
-                const float d = exp2_approx(fmaf(y[e + 1], p.scale_log2, -base));
-                sum[e & 2] += a;
-                sum[(e & 2) + 1] += d;
-                w[e >> 1] = pack2(a, d);
-              }
-              tmem_st16(s_col + 16 * c, w);
+            for (int e = 0; e < 32; e += 2) {
+              const float2 y = halves(fma2(pair(x[c][e], x[c][e + 1]), scale2, base2));
+              const float a = exp2_approx(y.x), d = exp2_approx(y.y);
+              sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair(a, d));
+              w[e >> 1] = pack2(a, d);
             }
+            tmem_st16(s_col + 16 * c, w);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          const float2 sums = halves(add2(sum[0], sum[1]));
+          l += sums.x + sums.y;
           tmem_wait_st();
         }
         tc_fence_before();
@@ -487,7 +518,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
         const float g0 = whole ? f0 * inv : f0, g1 = whole ? f1 * inv : f1;
         // slot 0: the item began before this share; slot 1: it goes on after it
-        float *po = p.partials + (((long long)blockIdx.x * 2 + (sg.kt0 > 0 ? 0 : 1)) * kRows + row) * (DIM + 2);
+        const Partial<DIM, kRows> part(p.partials, blockIdx.x, sg.kt0 > 0 ? 0 : 1);
+        if (st == 0 && sg.kt0 > 0 && sg.kt1 == sg.ktiles) leave_record<kRows>(p, sg, plan.at, plan.share, rows);
         uint16_t *out = p.out + ((long long)(sg.i.start + tok) * p.heads + sg.head * p.group + rr % p.group) * DIM;
         const uint32_t odd[2] = {odd_values[0], odd_values[1]};
         const uint32_t oc = lanes + G::COL_O;
@@ -528,10 +560,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                                                    pack2(x[e + 4], x[e + 5]), pack2(x[e + 6], x[e + 7]));
           } else if (mine) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) *reinterpret_cast<float2 *>(po + c + e) = make_float2(x[e], x[e + 1]);
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4 *>(part.at(row, c + e)) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
           }
         }
-        if (mine && !whole && stream == 0) *reinterpret_cast<float2 *>(po + DIM) = make_float2(M, L);
+        if (mine && !whole && stream == 0) *part.ml(row) = make_float2(M, L);
       }
       // the next item's Q, odd values and maxima: after everyone is here
       softmax_sync<SOFT>();
