@@ -57,18 +57,36 @@ struct AppendParams {
   int *err;
 };
 
+// x / s correctly rounded, from r = 1 / s: the quotient x * r corrected once by
+// its residual (P. Markstein, "IA-64 and Elementary Functions", ch. 8). Scales
+// outside 2^-60 .. 2^60, where a residual could underflow, take the division;
+// results that are not finite, or past what any code holds, stay as they are
+// (they saturate, or are NaN).
+struct Divisor {
+  float s, r;
+  bool plain;
+  __device__ static Divisor of(float v) {
+    return Divisor{v, __fdiv_rn(1.f, v), !(v > 8.6736174e-19f && v < 1.1529215e18f)};
+  }
+  __device__ float operator()(float x) const {
+    if (plain) return __fdiv_rn(x, s);
+    const float q = x * r;
+    return fabsf(q) < 1024.f ? fmaf(fmaf(-q, s, x), r, q) : q;
+  }
+};
+
 // 8 bf16 -> 8 e4m3 codes of x / scale
-__device__ __forceinline__ uint2 to_e4m3(const uint4 &x, float scale) {
+__device__ __forceinline__ uint2 to_e4m3(const uint4 &x, const Divisor &d) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = make_float2(__fdiv_rn(bf16lo_to_f32(w[i]), scale), __fdiv_rn(bf16hi_to_f32(w[i]), scale));
-    c[i] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
-  }
+  for (int i = 0; i < 4; ++i)
+    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(d(bf16lo_to_f32(w[i])), d(bf16hi_to_f32(w[i]))), __NV_SATFINITE, __NV_E4M3);
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
+// A block's data does not depend on where it goes, so its first batch of loads
+// is in flight while a few threads look up the places.
 template <bool E4M3>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p) {
   __shared__ long long off[2][kAppendTokens];
@@ -76,6 +94,44 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
   grid_launch_dependents();
   const int t0 = blockIdx.x * p.tokens_per_block;
   const int nt = min(p.tokens_per_block, p.r.tokens - t0);
+  // items of the block: (side, token, head, 16-byte chunk), chunk fastest
+  const int per_token = p.kv_heads << p.dim_chunks_log2;
+  const int per_side = nt * per_token, items = 2 * per_side;
+  constexpr int U = 4;
+  uint4 x[U];
+  int where[U];  // side * kAppendTokens + token, head and chunk
+  int piece[U];
+  auto load = [&](int e0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int e = e0 + u * kAppendThreads;
+      where[u] = -1;
+      if (e >= items) continue;
+      const int side = e >= per_side;
+      const int i = e - side * per_side;
+      const int t = i / per_token, rest = i - t * per_token;
+      const int h = rest >> p.dim_chunks_log2, c = rest & ((1 << p.dim_chunks_log2) - 1);
+      x[u] = *reinterpret_cast<const uint4 *>(p.src[side] + (long long)(t0 + t) * p.token_stride[side] +
+                                              (long long)h * p.head_stride[side] + c * 8);
+      where[u] = side * kAppendTokens + t;
+      piece[u] = rest;
+    }
+  };
+  auto store = [&]() {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (where[u] < 0) continue;
+      const int side = where[u] >= kAppendTokens;
+      const long long o = off[side][where[u] - side * kAppendTokens];
+      if (o < 0) continue;
+      const KvSide &s = p.side[side];
+      const int h = piece[u] >> p.dim_chunks_log2, c = piece[u] & ((1 << p.dim_chunks_log2) - 1);
+      uint8_t *dst = s.base + o + (long long)h * s.head + c * (E4M3 ? 8 : 16);
+      if (E4M3) *reinterpret_cast<uint2 *>(dst) = to_e4m3(x[u], Divisor::of(s.scale[h]));
+      else *reinterpret_cast<uint4 *>(dst) = x[u];
+    }
+  };
+  load(threadIdx.x);
   if ((int)threadIdx.x < nt) {
     const int t = t0 + threadIdx.x;
     const int b = owner_of(p.r.starts, p.r.rows, t);
@@ -95,37 +151,10 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
     off[1][threadIdx.x] = ov;
   }
   __syncthreads();
-  // items of the block: (side, token, head, 16-byte chunk), chunk fastest
-  const int per_token = p.kv_heads << p.dim_chunks_log2;
-  const int per_side = nt * per_token, items = 2 * per_side;
-  constexpr int U = 4;
-  for (int e0 = threadIdx.x; e0 < items; e0 += U * kAppendThreads) {
-    uint4 x[U];
-    uint8_t *dst[U];
-    float scale[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int e = e0 + u * kAppendThreads;
-      dst[u] = nullptr;
-      if (e >= items) continue;
-      const int side = e >= per_side;
-      const int i = e - side * per_side;
-      const int t = i / per_token, rest = i - t * per_token;
-      const int h = rest >> p.dim_chunks_log2, c = rest & ((1 << p.dim_chunks_log2) - 1);
-      const long long o = off[side][t];
-      if (o < 0) continue;
-      const KvSide &s = p.side[side];
-      x[u] = *reinterpret_cast<const uint4 *>(p.src[side] + (long long)(t0 + t) * p.token_stride[side] +
-                                              (long long)h * p.head_stride[side] + c * 8);
-      dst[u] = s.base + o + (long long)h * s.head + c * (E4M3 ? 8 : 16);
-      if (E4M3) scale[u] = s.scale[h];
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (!dst[u]) continue;
-      if (E4M3) *reinterpret_cast<uint2 *>(dst[u]) = to_e4m3(x[u], scale[u]);
-      else *reinterpret_cast<uint4 *>(dst[u]) = x[u];
-    }
+  store();
+  for (int e0 = threadIdx.x + U * kAppendThreads; e0 < items; e0 += U * kAppendThreads) {
+    load(e0);
+    store();
   }
 }
 
