@@ -54,34 +54,44 @@ struct AppendParams {
   KvRows r;
   int kv_heads, dim_chunks_log2, page_shift, pages;
   int tokens_per_block;
+  uint32_t token_magic;  // ceil(2^32 / chunks of a token): a block has under 2^16 of them
   int *err;
 };
 
-// x / s correctly rounded, from r = 1 / s: the quotient x * r corrected once by
-// its residual (P. Markstein, "IA-64 and Elementary Functions", ch. 8). Scales
-// outside 2^-60 .. 2^60, where a residual could underflow, take the division;
-// results that are not finite, or past what any code holds, stay as they are
-// (they saturate, or are NaN).
-struct Divisor {
-  float s, r;
-  bool plain;
-  __device__ static Divisor of(float v) {
-    return Divisor{v, __fdiv_rn(1.f, v), !(v > 8.6736174e-19f && v < 1.1529215e18f)};
-  }
-  __device__ float operator()(float x) const {
-    if (plain) return __fdiv_rn(x, s);
-    const float q = x * r;
-    return fabsf(q) < 1024.f ? fmaf(fmaf(-q, s, x), r, q) : q;
-  }
-};
-
-// 8 bf16 -> 8 e4m3 codes of x / scale
-__device__ __forceinline__ uint2 to_e4m3(const uint4 &x, const Divisor &d) {
+// Eight quotients x / s, correctly rounded, from r = 1 / s: x * r corrected
+// once by its residual (P. Markstein, "IA-64 and Elementary Functions", ch. 8).
+// r = 0 stands for a scale outside 2^-60 .. 2^60, where a residual could
+// underflow: those take the division. A quotient of 1,024 or more saturates
+// whatever its last bits, and its residual need not be finite: it stays as it
+// is.
+__device__ __forceinline__ float2 divisor_of(float s) {
+  return make_float2(s, s > 8.6736174e-19f && s < 1.1529215e18f ? __fdiv_rn(1.f, s) : 0.f);
+}
+__device__ __forceinline__ uint2 to_e4m3(const uint4 &x, const float2 &d) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  const f32x2 r2 = f32_pair(d.y, d.y), minus_s2 = f32_pair(-d.x, -d.x);
+  f32x2 f[4], q2[4];
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[i] = f32_pair(bf16lo_to_f32(w[i]), bf16hi_to_f32(w[i]));
+    q2[i] = mul2(f[i], r2);
+    const float2 q = f32_halves(q2[i]);
+    top = fmaxf(fmaxf(top, fabsf(q.x)), fabsf(q.y));
+  }
+  float2 q[4];
+  if (d.y != 0.f && top < 1024.f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = f32_halves(fma2(fma2(q2[i], minus_s2, f[i]), r2, q2[i]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      q[i] = make_float2(__fdiv_rn(bf16lo_to_f32(w[i]), d.x), __fdiv_rn(bf16hi_to_f32(w[i]), d.x));
+  }
   uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(d(bf16lo_to_f32(w[i])), d(bf16hi_to_f32(w[i]))), __NV_SATFINITE, __NV_E4M3);
+    c[i] = __nv_cvt_float2_to_fp8x2(q[i], __NV_SATFINITE, __NV_E4M3);
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
@@ -90,6 +100,7 @@ __device__ __forceinline__ uint2 to_e4m3(const uint4 &x, const Divisor &d) {
 template <bool E4M3>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p) {
   __shared__ long long off[2][kAppendTokens];
+  extern __shared__ float2 divisor[];  // [2][kv_heads]
   grid_dependency_wait();
   grid_launch_dependents();
   const int t0 = blockIdx.x * p.tokens_per_block;
@@ -109,7 +120,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
       if (e >= items) continue;
       const int side = e >= per_side;
       const int i = e - side * per_side;
-      const int t = i / per_token, rest = i - t * per_token;
+      const int t = __umulhi(i, p.token_magic), rest = i - t * per_token;
       const int h = rest >> p.dim_chunks_log2, c = rest & ((1 << p.dim_chunks_log2) - 1);
       x[u] = *reinterpret_cast<const uint4 *>(p.src[side] + (long long)(t0 + t) * p.token_stride[side] +
                                               (long long)h * p.head_stride[side] + c * 8);
@@ -127,11 +138,14 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
       const KvSide &s = p.side[side];
       const int h = piece[u] >> p.dim_chunks_log2, c = piece[u] & ((1 << p.dim_chunks_log2) - 1);
       uint8_t *dst = s.base + o + (long long)h * s.head + c * (E4M3 ? 8 : 16);
-      if (E4M3) *reinterpret_cast<uint2 *>(dst) = to_e4m3(x[u], Divisor::of(s.scale[h]));
+      if (E4M3) *reinterpret_cast<uint2 *>(dst) = to_e4m3(x[u], divisor[side * p.kv_heads + h]);
       else *reinterpret_cast<uint4 *>(dst) = x[u];
     }
   };
   load(threadIdx.x);
+  if (E4M3)
+    for (int i = threadIdx.x; i < 2 * p.kv_heads; i += kAppendThreads)
+      divisor[i] = divisor_of(i < p.kv_heads ? p.side[0].scale[i] : p.side[1].scale[i - p.kv_heads]);
   if ((int)threadIdx.x < nt) {
     const int t = t0 + threadIdx.x;
     const int b = owner_of(p.r.starts, p.r.rows, t);
@@ -611,10 +625,11 @@ int log2_of(int v) {
 // Every kernel here waits for the work before it (griddepcontrol.wait) before
 // its first access, so it may always be launched while that work ends.
 template <class... K, class... A>
-cudaError_t launch(void (*kern)(K...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+cudaError_t launch_smem(void (*kern)(K...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t lc = {};
   lc.gridDim = grid;
   lc.blockDim = dim3(threads, 1, 1);
+  lc.dynamicSmemBytes = smem;
   lc.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -622,6 +637,10 @@ cudaError_t launch(void (*kern)(K...), dim3 grid, int threads, cudaStream_t stre
   lc.attrs = attr;
   lc.numAttrs = 1;
   return cudaLaunchKernelEx(&lc, kern, args...);
+}
+template <class... K, class... A>
+cudaError_t launch(void (*kern)(K...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+  return launch_smem(kern, grid, threads, 0, stream, args...);
 }
 
 }  // namespace
@@ -645,8 +664,9 @@ cudaError_t launch_kv_append(const AppendCall &c) {
   // four 16-byte chunks per thread, or what one token has
   const int per_token = 2 * c.cache.kv_heads * (c.cache.dim / 8);
   p.tokens_per_block = std::min(kAppendTokens, std::max(1, 4 * kAppendThreads / per_token));
+  p.token_magic = (uint32_t)(((1ull << 32) + per_token / 2 - 1) / (per_token / 2));
   const dim3 grid((c.rows.tokens + p.tokens_per_block - 1) / p.tokens_per_block);
-  return c.cache.e4m3 ? launch(kv_append_kernel<true>, grid, kAppendThreads, c.stream, p)
+  return c.cache.e4m3 ? launch_smem(kv_append_kernel<true>, grid, kAppendThreads, 2 * c.cache.kv_heads * sizeof(float2), c.stream, p)
                       : launch(kv_append_kernel<false>, grid, kAppendThreads, c.stream, p);
 }
 

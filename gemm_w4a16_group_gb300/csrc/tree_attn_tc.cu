@@ -121,29 +121,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<uint32_t *>(&b);
 }
 
-// two float32 values in one 64-bit register, and the packed operations on them
-using f32x2 = unsigned long long;
-__device__ __forceinline__ f32x2 pair(float a, float b) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 halves(f32x2 x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 template <int THREADS>
 __device__ __forceinline__ void softmax_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
@@ -476,21 +453,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           // ---- weights, over the first half of S's columns
           const float base = m == -INFINITY ? 0.f : m;
-          const f32x2 scale2 = pair(p.scale_log2, p.scale_log2), base2 = pair(-base, -base);
-          f32x2 sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+          const f32x2 scale2 = f32_pair(p.scale_log2, p.scale_log2), base2 = f32_pair(-base, -base);
+          f32x2 sum[2] = {f32_pair(0.f, 0.f), f32_pair(0.f, 0.f)};
 #pragma unroll
           for (int c = 0; c < KT / 32; ++c) {
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float2 y = halves(fma2(pair(x[c][e], x[c][e + 1]), scale2, base2));
+              const float2 y = f32_halves(fma2(f32_pair(x[c][e], x[c][e + 1]), scale2, base2));
               const float a = exp2_approx(y.x), d = exp2_approx(y.y);
-              sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair(a, d));
+              sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], f32_pair(a, d));
               w[e >> 1] = pack2(a, d);
             }
             tmem_st16(s_col + 16 * c, w);
           }
-          const float2 sums = halves(add2(sum[0], sum[1]));
+          const float2 sums = f32_halves(add2(sum[0], sum[1]));
           l += sums.x + sums.y;
           tmem_wait_st();
         }
