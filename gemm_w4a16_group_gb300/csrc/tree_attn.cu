@@ -42,13 +42,13 @@ namespace {
 
 constexpr int kComputeWarps = 4;
 constexpr int kThreads = (kComputeWarps + 1) * 32;
-constexpr int kMinTiles = 2;
 
 template <int DIM, bool E4M3, int RWT>
 struct RowsGeo {
   static constexpr int RW = RWT, KW = kComputeWarps / RWT;
   static constexpr int ROWS = 16 * RW;
   static constexpr int KT = RW <= 2 && (DIM * (E4M3 ? 1 : 2) <= 128 || (DIM == 256 && E4M3)) ? 128 : 64;  // keys of a stage
+  using Tiles = Tiling<ROWS, KT, ROWS>;
   static constexpr int KPW = KT / KW;         // keys of a warp per stage
   static constexpr int ELT = E4M3 ? 1 : 2;
   static constexpr int ROWB = DIM * ELT;       // bytes of a cache row
@@ -184,9 +184,10 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
   }
   grid_dependency_wait();
   grid_launch_dependents();
-  plan_share<G::ROWS, G::KT, kThreads>(p, plan, kMinTiles);
+  plan_share<typename G::Tiles, kThreads>(p, plan);
   __syncthreads();
-  Cursor cur{plan.at, plan.end, plan.b, plan.head, plan.rt, plan.kt};
+  Cursor cur{plan.at, plan.end, plan.at < plan.end ? plan.unit : plan.end, plan.b, plan.head, plan.rt};
+  const long long share = plan.share;
   Segment sg;
 
   if (warp == kComputeWarps) {
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
     }
     uint32_t st = 0;
     bool ok = true;
-    while (ok && next_segment<G::ROWS, G::KT>(p, cur, sg)) {
+    while (ok && next_segment<typename G::Tiles>(p, cur, share, sg)) {
       const int32_t *ids = p.r.table + (long long)sg.b * p.r.max_pages;
       auto id_of = [&](int kt) {  // -1: past the keys
         const long long key = (long long)kt * G::KT + part * br;
@@ -257,8 +258,8 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
   uint32_t st = 0;
   bool ok = true;  // after a wait that gave up: no more waits, but every barrier below is still met
 
-  while (next_segment<G::ROWS, G::KT>(p, cur, sg)) {
-    const int rows = min(G::ROWS, sg.i.n * p.group - sg.rt * G::ROWS);
+  while (next_segment<typename G::Tiles>(p, cur, share, sg)) {
+    const int rows = sg.rows;
     // ---- q in the order of the A fragments (16 bytes per lane and k step)
     compute_sync();  // the last item's exchange is over
     if (E4M3) {
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
     // slot 0: the item began before this share; slot 1: it goes on after it
     const int slot = sg.kt0 > 0 ? 0 : 1;
     const Partial<DIM, G::ROWS> part(p.partials, blockIdx.x, slot);
-    if (tid == 0 && sg.kt0 > 0 && sg.kt1 == sg.ktiles) leave_record<G::ROWS>(p, sg, plan.at, plan.share, rows);
+    if (tid == 0 && sg.kt0 > 0 && sg.kt1 == sg.ktiles) leave_record<typename G::Tiles>(p, sg);
     const float vs = E4M3 ? p.c.v.scale[sg.head] : 1.f;
 #pragma unroll
     for (int sl = 0; sl < KW; ++sl) {
@@ -815,7 +816,7 @@ template <int DIM>
 cudaError_t launch_tc(const AttnCall &c, AttnParams &p) {
   cudaError_t e = launch_tree_tc(c, p);
   if (e != cudaSuccess) return e;
-  return launch_join<DIM, kTcAttnRows>(c, p, std::min(c.sm_count, kMaxCtas));
+  return launch_join<DIM, tc_attn_rows(DIM)>(c, p, std::min(c.sm_count, kTcMaxCtas));
 }
 bool uses_tc(int rows, bool e4m3) { return !e4m3 && rows > 16; }
 
@@ -843,8 +844,9 @@ bool encode_cache(CUtensorMap *m, const KvSide &s, const KvCache &c, int box_row
 
 size_t tree_attn_workspace_bytes(int heads, int kv_heads, int dim, int max_tree) {
   const int rows = max_tree * (heads / kv_heads);
-  const int tile = rows <= 16 ? 16 : kTcAttnRows;
-  return kJoinBytes + align_up((size_t)kMaxCtas * 2 * tile * (dim + 2) * sizeof(float), 256);
+  if (uses_tc(rows, false))  // (an 8-bit cache never needs more)
+    return kJoinBytes + align_up((size_t)kTcMaxCtas * 2 * tc_attn_rows(dim) * (dim + 2) * sizeof(float), 256);
+  return kJoinBytes + align_up((size_t)kMaxCtas * 2 * 16 * (dim + 2) * sizeof(float), 256);
 }
 
 cudaError_t launch_tree_attention(const AttnCall &c) {

@@ -4,10 +4,12 @@
 // Work list. Row b of the page table with T new tokens and L cached ones has
 // K = L + T keys; its T * G query rows of one kv head (G query heads each) are
 // packed token by token into tiles of ROWS rows, so its items are
-// (kv head, row tile), each of ceil(K / KT) key tiles. All key tiles of all
-// items, in the order (b, head, row tile, key tile), form one list, and every
-// CTA takes an equal, contiguous share of it, whatever the lengths are: long
-// contexts are split over many CTAs, short ones share one. An item whose tiles
+// (kv head, row tile), each of ceil(K / KT) key tiles. A key tile counts one
+// unit per UNIT query rows (the tcgen05 kernel works on 256 rows at a time, and
+// takes twice as long over more than 128). All key tiles of all items, in the
+// order (b, head, row tile, key tile), form one list of units, and every CTA
+// takes an equal, contiguous share of it (to whole key tiles), whatever the
+// lengths are: long contexts are split over many CTAs, short ones share one. An item whose tiles
 // lie in one share is finished there; otherwise each CTA leaves a partial
 // result (running maximum, sum and unnormalised output per row) in the
 // workspace, and a second kernel joins them in the order of the CTAs, so
@@ -21,11 +23,11 @@
 
 namespace w4a16 {
 
-constexpr int kMaxCtas = 320;  // CTAs of an attention launch: shares of the work list
-// the tcgen05 kernel (tree_attn_tc.cu): query rows of an item, keys of a tile, least tiles of a CTA
-constexpr int kTcAttnRows = 128;
+constexpr int kMaxCtas = 320;    // CTAs of an attention launch: shares of the work list
+constexpr int kTcMaxCtas = 160;  // of the tcgen05 kernel
+// the tcgen05 kernel (tree_attn_tc.cu): query rows of an item, keys of a tile
+constexpr int tc_attn_rows(int dim) { return dim == 256 ? 128 : 256; }
 constexpr int tc_attn_keys(int dim) { return dim == 256 ? 64 : 128; }
-constexpr int kTcAttnMinTiles = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttnParams {
@@ -80,6 +82,12 @@ __device__ __forceinline__ RowInfo row_info(const AttnParams &p, int b, bool fla
   return i;
 }
 
+// Query rows of a tile, keys of a tile, query rows of a unit
+template <int ROWS_, int KT_, int UNIT_>
+struct Tiling {
+  static constexpr int ROWS = ROWS_, KT = KT_, UNIT = UNIT_;
+};
+
 template <int KT>
 __device__ __forceinline__ int key_tiles(const RowInfo &i) {
   return (i.keys + KT - 1) / KT;
@@ -88,35 +96,36 @@ template <int ROWS>
 __device__ __forceinline__ int row_tiles(const RowInfo &i, int group) {
   return (i.n * group + ROWS - 1) / ROWS;
 }
-template <int ROWS, int KT>
-__device__ __forceinline__ long long tiles_of(const RowInfo &i, const AttnParams &p) {
-  return i.n > 0 ? (long long)p.c.kv_heads * row_tiles<ROWS>(i, p.group) * key_tiles<KT>(i) : 0;
+template <class T>
+__device__ __forceinline__ long long units_of(const RowInfo &i, const AttnParams &p) {
+  return i.n > 0 ? (long long)p.c.kv_heads * row_tiles<T::UNIT>(i, p.group) * key_tiles<T::KT>(i) : 0;
 }
 
-// A CTA's place in the work list
+// A CTA's place in the work list: units [at, end) are its share, `unit` is the
+// first one of the item it has come to
 struct Cursor {
-  long long at, end;  // tiles [at, end) are left
-  int b, head, rt, kt;
+  long long at, end, unit;
+  int b, head, rt;
 };
 
 struct PlanShared {
   long long sums[16];
-  long long at, end, share;
-  int b, head, rt, kt;
+  long long at, end, share, unit;
+  int b, head, rt;
 };
 
 // The CTA's share, found by all NT threads: thread i sums the tiles of its
 // own run of rows, a block scan places the runs, and the thread whose run holds
 // the share's first tile walks it. The CTA's record is cleared. The caller
 // synchronises before it reads `s`.
-template <int ROWS, int KT, int NT>
-__device__ void plan_share(const AttnParams &p, PlanShared &s, int min_tiles) {
+template <class T, int NT>
+__device__ void plan_share(const AttnParams &p, PlanShared &s) {
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int per = (p.r.rows + NT - 1) / NT;
   const int b0 = min(tid * per, p.r.rows), b1 = min(b0 + per, p.r.rows);
   const bool flag = blockIdx.x == 0;  // one CTA reports rows that cannot be
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += tiles_of<ROWS, KT>(row_info(p, b, flag), p);
+  for (int b = b0; b < b1; ++b) mine += units_of<T>(row_info(p, b, flag), p);
   long long upto = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -133,8 +142,9 @@ __device__ void plan_share(const AttnParams &p, PlanShared &s, int min_tiles) {
     total += x;
   }
   const long long first = before + upto - mine;
-  // as many CTAs as get min_tiles each, and no share larger than it has to be
-  const long long ctas = max(1ll, min((long long)gridDim.x, total / min_tiles));
+  // as many CTAs as get two units each (a share then holds a whole key tile of any item), and no share larger than it
+  // has to be
+  const long long ctas = max(1ll, min((long long)gridDim.x, total / 2));
   const long long share = max(1ll, (total + ctas - 1) / ctas);
   const long long at = min(share * blockIdx.x, total), end = min(at + share, total);
   if (tid == 0) {
@@ -147,14 +157,14 @@ __device__ void plan_share(const AttnParams &p, PlanShared &s, int min_tiles) {
     long long f = first;
     for (int b = b0; b < b1; ++b) {
       const RowInfo i = row_info(p, b, false);
-      const long long n = tiles_of<ROWS, KT>(i, p);
+      const long long n = units_of<T>(i, p);
       if (at < f + n) {
-        const int kt = key_tiles<KT>(i), rt = row_tiles<ROWS>(i, p.group);
-        const long long o = at - f;
+        const int kt = key_tiles<T::KT>(i);
+        const long long per_head = (long long)row_tiles<T::UNIT>(i, p.group) * kt, o = at - f;
         s.b = b;
-        s.kt = (int)(o % kt);
-        s.rt = (int)(o / kt % rt);
-        s.head = (int)(o / kt / rt);
+        s.head = (int)(o / per_head);
+        s.rt = (int)(o % per_head / (kt * (T::ROWS / T::UNIT)));
+        s.unit = f + s.head * per_head + (long long)s.rt * kt * (T::ROWS / T::UNIT);
         break;
       }
       f += n;
@@ -165,41 +175,46 @@ __device__ void plan_share(const AttnParams &p, PlanShared &s, int min_tiles) {
 // The part of an item that a CTA works on: key tiles [kt0, kt1)
 struct Segment {
   RowInfo i;
-  int b, head, rt, kt0, kt1, ktiles;
+  int b, head, rt, rows, kt0, kt1, ktiles;
+  int first_cta;  // that has a part of the item
   __device__ bool whole() const { return kt0 == 0 && kt1 == ktiles; }
 };
 
-// Leaves the record of an item that this CTA ends and others began (one
-// thread; `kt0` > 0 only at the share's start)
-template <int ROWS>
-__device__ __forceinline__ void leave_record(const AttnParams &p, const Segment &s, long long at, long long share, int rows) {
-  int4 *rec = reinterpret_cast<int4 *>(p.joins + kMaxCtas);
-  rec[blockIdx.x] = make_int4((int)((at - s.kt0) / share), s.i.start, s.rt * ROWS, s.head);
-  p.joins[blockIdx.x] = rows;
+// Leaves the record of an item that this CTA ends and others began (one thread)
+template <class T>
+__device__ __forceinline__ void leave_record(const AttnParams &p, const Segment &s) {
+  reinterpret_cast<int4 *>(p.joins + kMaxCtas)[blockIdx.x] = make_int4(s.first_cta, s.i.start, s.rt * T::ROWS, s.head);
+  p.joins[blockIdx.x] = s.rows;
 }
 
 // Next segment of the share (false: none is left)
-template <int ROWS, int KT>
-__device__ __forceinline__ bool next_segment(const AttnParams &p, Cursor &c, Segment &s) {
-  if (c.at >= c.end) return false;
-  s.i = row_info(p, c.b, false);
-  while (s.i.n == 0) s.i = row_info(p, ++c.b, false);  // rows without work; tiles are left, so one with work follows
-  s.b = c.b;
-  s.head = c.head;
-  s.rt = c.rt;
-  s.kt0 = c.kt;
-  s.ktiles = key_tiles<KT>(s.i);
-  s.kt1 = (int)min((long long)s.ktiles, s.kt0 + (c.end - c.at));
-  c.at += s.kt1 - s.kt0;
-  c.kt = 0;
-  if (++c.rt == row_tiles<ROWS>(s.i, p.group)) {
-    c.rt = 0;
-    if (++c.head == p.c.kv_heads) {
-      c.head = 0;
-      ++c.b;
+template <class T>
+__device__ __forceinline__ bool next_segment(const AttnParams &p, Cursor &c, long long share, Segment &s) {
+  while (c.unit < c.end) {
+    s.i = row_info(p, c.b, false);
+    while (s.i.n == 0) s.i = row_info(p, ++c.b, false);  // rows without work; units are left, so one with work follows
+    s.b = c.b;
+    s.head = c.head;
+    s.rt = c.rt;
+    s.rows = min(T::ROWS, s.i.n * p.group - c.rt * T::ROWS);
+    s.ktiles = key_tiles<T::KT>(s.i);
+    const int cost = T::ROWS == T::UNIT ? 1 : (s.rows + T::UNIT - 1) / T::UNIT;
+    const long long unit = c.unit, units = (long long)s.ktiles * cost;
+    // a key tile belongs to the share that holds its last unit
+    s.kt0 = c.at > unit ? (int)((c.at - unit) / cost) : 0;
+    s.kt1 = c.end - unit >= units ? s.ktiles : (int)((c.end - unit) / cost);
+    s.first_cta = (int)((unit + cost - 1) / share);
+    c.unit += units;
+    if (++c.rt == row_tiles<T::ROWS>(s.i, p.group)) {
+      c.rt = 0;
+      if (++c.head == p.c.kv_heads) {
+        c.head = 0;
+        ++c.b;
+      }
     }
+    if (s.kt0 < s.kt1) return true;
   }
-  return true;
+  return false;
 }
 
 cudaError_t launch_tree_tc(const AttnCall &c, const AttnParams &p);

@@ -2,25 +2,25 @@
 // tensor cores (tcgen05), for rows of the page table with many query rows per
 // kv head (wide draft trees, large head groups).
 //
-// An item is 128 query rows (tokens times the heads of one kv head) of one
-// kv head. S = Q . K^T and O += P . V are M = 128 MMAs with their accumulators
-// in TMEM: a TMEM lane is one query row, so a softmax thread owns a row and
-// needs no exchange. With up to 128 query rows the cache is read once and HBM
-// bounds the kernel (a 128-key tile at dim 128 is 64 KB, 2,800 clocks of an
-// SM's share of HBM, against 1,024 clocks of MMA); with more, the row tiles
-// read it again from L2 and MMA time, softmax and L2 come near one another.
+// An item is up to 256 query rows (tokens times the heads of one kv head) of
+// one kv head. S = Q . K^T and O += P . V are M = 128 MMAs with their
+// accumulators in TMEM: a TMEM lane is one query row, so a softmax thread owns
+// a row and needs no exchange. With up to 128 query rows HBM bounds the kernel
+// (a 128-key tile at dim 128 is 64 KB, 2,800 clocks of an SM's share of HBM,
+// against 1,024 clocks of MMA); with up to 256 the cache is still read once,
+// and HBM, MMA time and softmax come near one another.
 //
 //   warp 0        copies: K and V tiles by TMA through the page table, into one
-//                 ring of slots in the order in which the MMAs take them
-//                 (K0, K1, V0, K2, V1, ...)
+//                 ring of slots (K0, V0, K1, V1, ...)
 //   warp 1        one thread issues all MMAs; TMEM allocation
-//   warps 4-7     softmax of the even tiles of the item
-//   warps 8-11    softmax of the odd tiles (dim 64 and 128)
+//   warps 4-7     softmax group 0
+//   warps 8-11    softmax group 1 (dim 64 and 128)
 //
 // The two softmax groups keep maxima, sums and output accumulators of their
-// own, so neither waits for the other; their outputs meet at the item's end,
-// where each group forms half of the columns (both can read the lanes of
-// both). P (bf16) replaces S in TMEM and is the second MMA's A operand there;
+// own, so neither waits for the other. In an item of more than 128 rows ("wide")
+// each has 128 of the rows and all tiles; else all rows, and every other tile:
+// their outputs then meet at the item's end, where each group forms half of
+// the columns (both can read the lanes of both). P (bf16) replaces S in TMEM and is the second MMA's A operand there;
 // V, [key][dim] in shared memory, is its B operand as it lies (MN-major). At
 // dim 256 the output takes half of TMEM, so there is one group, with two S
 // buffers. An output accumulator is rescaled only when a row's maximum has
@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kTcThreads = 384;
 constexpr int kWarpCopy = 0, kWarpMma = 1, kWarpSoftmax = 4;
-constexpr int kRows = kTcAttnRows;
+constexpr int kRows = 128;  // query rows of an MMA
 constexpr int kInfo = 16;  // tiles whose key-group words are kept
 
 template <int DIM>
@@ -49,8 +49,11 @@ struct TcGeo {
   static constexpr int SUB = KT * 128;                // one column of a K or V tile
   static constexpr int SLOT = CH * SUB;
   static constexpr int QSUB = kRows * 128;
-  static constexpr int Q_BYTES = CH * QSUB;
-  static constexpr int SLOTS = DIM == 64 ? 12 : DIM == 128 ? 6 : 5;
+  static constexpr int Q_TILE = CH * QSUB;
+  static constexpr int ROWS = tc_attn_rows(DIM);
+  static constexpr int Q_BYTES = ROWS / kRows * Q_TILE;
+  using Tiles = Tiling<ROWS, KT, kRows>;
+  static constexpr int SLOTS = DIM == 64 ? 12 : 5;
   static constexpr int SBUFS = 2;                     // S buffers: one per stream, or two of the one
   // TMEM columns: S (P over its first half), then O
   static constexpr int COL_O = SBUFS * KT;
@@ -190,12 +193,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   grid_dependency_wait();
   grid_launch_dependents();
-  plan_share<kRows, KT, kTcThreads>(p, plan, kTcAttnMinTiles);
+  plan_share<typename G::Tiles, kTcThreads>(p, plan);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Cursor cur{plan.at, plan.end, plan.b, plan.head, plan.rt, plan.kt};
+  Cursor cur{plan.at, plan.end, plan.at < plan.end ? plan.unit : plan.end, plan.b, plan.head, plan.rt};
+  const long long share = plan.share;
   Segment sg;
 
   // A softmax thread holds a row's 128 scores. The block is launched with 384 x 168 registers; the first warpgroup
@@ -218,9 +222,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
     uint32_t ring = 0, tile = 0;
     bool ok = true;
-    while (ok && next_segment<kRows, KT>(p, cur, sg)) {
+    while (ok && next_segment<typename G::Tiles>(p, cur, share, sg)) {
       const int32_t *ids = p.r.table + (long long)sg.b * p.r.max_pages;
-      const uint64_t policy = sg.i.n * p.group > kRows ? keep : pol;
+      const uint64_t policy = sg.i.n * p.group > G::ROWS ? keep : pol;
       auto id_of = [&](int kt) {  // -1: past the keys
         const long long key = (long long)kt * KT + part * br;
         return kt < sg.kt1 && key < sg.i.keys ? ids[key >> p.c.page_shift] : -1;
@@ -238,26 +242,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
         ++ring;
       };
-      int next = id_of(sg.kt0), before = -1;
-      uint32_t loads_before = 0;
+      int next = id_of(sg.kt0);
       for (int kt = sg.kt0; ok && kt < sg.kt1; ++kt, ++tile) {
         const int id = next;
         next = id_of(kt + 1);
-        const bool valid = (unsigned)id < (unsigned)p.c.pages;
+        const bool valid = (unsigned)id < (unsigned)p.c.pages, load = has_box && valid;
         if (col == 0 && !valid && kt * KT + part * br < sg.i.keys) attn_flag(p.err);
-        const uint32_t loads = __ballot_sync(0xFFFFFFFFu, has_box && valid);
+        const uint32_t loads = __ballot_sync(0xFFFFFFFFu, load);
         if (lane == 0) {
           uint32_t groups = 0;  // 16-key groups that are there (lanes 0 .. parts - 1: the first column's boxes)
           for (int i = 0; i < parts; ++i)
             if (loads >> i & 1) groups |= ((1u << (br / 16)) - 1) << (i * br / 16);
           info[tile % kInfo] = groups;
         }
-        copy(&tm_k, kt, id, has_box && valid, loads);
-        if (kt > sg.kt0) copy(&tm_v, kt - 1, before, loads_before >> lane & 1, loads_before);
-        before = id;
-        loads_before = loads;
+        copy(&tm_k, kt, id, load, loads);
+        copy(&tm_v, kt, id, load, loads);
       }
-      copy(&tm_v, sg.kt1 - 1, before, loads_before >> lane & 1, loads_before);
     }
     if (!ok && lane == 0) {
       *abort_flag = 1;
@@ -273,47 +273,82 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (lane == 0) {
       constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, KT);
       constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, DIM) | kIdescBMn;
-      uint32_t ring = 0, item = 0, tile = 0;  // tile: S buffer tile % 2, its phase tile / 2
+      uint32_t ring = 0, item = 0, turn = 0;
+      uint32_t made = 0;  // bit b: the parity of the scores written to S buffer b, the phase of its barriers
       bool ok = true;
-      auto take = [&]() {
-        ok = ok && mbar_wait(full(ring % G::SLOTS), (ring / G::SLOTS) & 1, abort_flag);
-        return sbase + G::OFF_SLOT + (ring % G::SLOTS) * G::SLOT;
+      auto slot = [&](uint32_t r) { return sbase + G::OFF_SLOT + (r % G::SLOTS) * G::SLOT; };
+      auto arrived = [&](uint32_t r) {
+        ok = ok && mbar_wait(full(r % G::SLOTS), (r / G::SLOTS) & 1, abort_flag);
+        tc_fence_after();
       };
-      auto give = [&]() {
-        tc_commit(empty(ring % G::SLOTS));
-        ++ring;
+      // S buffer b = Q tile qt . K^T of ring slot r. The buffer's last P was taken by an MMA issued before.
+      auto scores = [&](uint32_t b, int qt, uint32_t r) {
+        if (!ok) return;
+        const uint32_t q = sbase + qt * G::Q_TILE, k = slot(r);
+#pragma unroll
+        for (int c = 0; c < DIM / 16; ++c)
+          tc_mma_f16(tmem + b * KT, smem_desc(q + (c / 4) * G::QSUB + (c % 4) * 32, 16),
+                     smem_desc(k + (c / 4) * G::SUB + (c % 4) * 32, 16), idesc_s, c != 0 ? 1u : 0u);
+        tc_commit(s_full(b));
+        made ^= 1u << b;
       };
-      // O of tile `t`'s stream += P . V; `first`: the stream's first tile of the item
-      auto output = [&](uint32_t t, bool first) {
-        const uint32_t b = t % G::SBUFS;
-        ok = ok && mbar_wait(p_full(b), (t / G::SBUFS) & 1, abort_flag);
-        const uint32_t v = take();
+      // O of group `o` (+)= P of buffer b . V of ring slot r
+      auto output = [&](uint32_t b, uint32_t o, uint32_t r, bool first) {
+        ok = ok && mbar_wait(p_full(b), (made >> b & 1) ^ 1, abort_flag);
         if (!ok) return;
         tc_fence_after();
-        const uint32_t o = tmem + G::COL_O + (STREAMS == 2 ? b * DIM : 0);
+        const uint32_t v = slot(r), d = tmem + G::COL_O + o * DIM;
 #pragma unroll
         for (int c = 0; c < KT / 16; ++c)
-          tc_mma_f16_ts(o, tmem + b * KT + 8 * c, smem_desc(v + c * 2048, G::SUB), idesc_o, first && c == 0 ? 0u : 1u);
-        give();
+          tc_mma_f16_ts(d, tmem + b * KT + 8 * c, smem_desc(v + c * 2048, G::SUB), idesc_o, first && c == 0 ? 0u : 1u);
       };
-      while (ok && next_segment<kRows, KT>(p, cur, sg)) {
+      auto give = [&](uint32_t r) {
+        if (ok) tc_commit(empty(r % G::SLOTS));
+      };
+      while (ok && next_segment<typename G::Tiles>(p, cur, share, sg)) {
         ok = mbar_wait(q_full, item & 1, abort_flag);
         ++item;
         const int n = sg.kt1 - sg.kt0;
-        for (int i = 0; ok && i < n; ++i, ++tile) {
-          const uint32_t k = take();
-          if (!ok) break;
-          tc_fence_after();
-          // the S buffer's last P was taken by an MMA issued before this one
-#pragma unroll
-          for (int c = 0; c < DIM / 16; ++c)
-            tc_mma_f16(tmem + (tile % G::SBUFS) * KT, smem_desc(sbase + (c / 4) * G::QSUB + (c % 4) * 32, 16),
-                       smem_desc(k + (c / 4) * G::SUB + (c % 4) * 32, 16), idesc_s, c != 0 ? 1u : 0u);
-          tc_commit(s_full(tile % G::SBUFS));
-          give();
-          if (i > 0) output(tile - 1, i - 1 < STREAMS);
+        if (STREAMS == 2 && sg.rows > kRows) {
+          // wide: per key tile both groups, each output before the scores that take its buffer
+          for (int i = 0; ok && i <= n; ++i) {
+            const uint32_t k = ring + 2 * i, v = k - 1;
+            if (i > 0) {
+              arrived(v);
+              output(0, 0, v, i == 1);
+            }
+            if (i < n) {
+              arrived(k);
+              scores(0, 0, k);
+            }
+            if (i > 0) {
+              output(1, 1, v, i == 1);
+              give(v);
+            }
+            if (i < n) {
+              scores(1, 1, k);
+              give(k);
+            }
+          }
+        } else {
+          // the scores of tile i, then the output of tile i - 1
+          for (int i = 0; ok && i <= n; ++i) {
+            const uint32_t k = ring + 2 * i, v = k - 1;
+            const uint32_t b = STREAMS == 2 ? i & 1 : (turn + i) & 1;
+            if (i < n) {
+              arrived(k);
+              scores(b, 0, k);
+              give(k);
+            }
+            if (i > 0) {
+              arrived(v);
+              output(b ^ 1, STREAMS == 2 ? b ^ 1 : 0, v, i - 1 < STREAMS);
+              give(v);
+            }
+          }
+          turn += n;
         }
-        if (ok) output(tile - 1, n - 1 < STREAMS);
+        ring += 2 * n;
         tc_commit(o_full);
       }
       if (!ok) {
@@ -328,25 +363,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     // ------------------------------------------------------------ softmax
     const int stream = (warp - kWarpSoftmax) >> 2, quarter = warp & 3;
-    const int row = quarter * 32 + lane;  // query row of the tile: TMEM lane
+    const int lane_row = quarter * 32 + lane;  // query row of the MMA: TMEM lane
     const int st = tid - kWarpSoftmax * 32;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t o_col = lanes + G::COL_O + stream * DIM;
     float2 *ml = reinterpret_cast<float2 *>(smem + G::OFF_ML);
     uint32_t tile = 0, item = 0, ring = 0;
+    uint32_t took = 0;  // scores taken by this group (its S buffer, or the two in turn)
     bool ok = true;  // after a wait that gave up: no more waits, but the barriers below are still met
-    while (next_segment<kRows, KT>(p, cur, sg)) {
-      const int rows = min(kRows, sg.i.n * p.group - sg.rt * kRows);
+    while (next_segment<typename G::Tiles>(p, cur, share, sg)) {
+      const int rows = sg.rows;
+      const bool wide = STREAMS == 2 && rows > kRows;
+      const int row = lane_row + (wide ? stream * kRows : 0);  // this thread's query row of the item
       // ---- Q: K-major, 128-byte swizzle; rows past the item's are zero
       long long *q_row = reinterpret_cast<long long *>(smem + G::OFF_ML);  // between two items' use of it
-      if (st < kRows) {
-        const int rr = sg.rt * kRows + st;
-        q_row[st] = st < rows ? (sg.i.start + rr / p.group) * p.q_token + (sg.head * p.group + rr % p.group) * p.q_head : -1;
+      const int q_rows = wide ? 2 * kRows : kRows;
+      for (int r = st; r < q_rows; r += SOFT) {
+        const int rr = sg.rt * G::ROWS + r;
+        q_row[r] = r < rows ? (sg.i.start + rr / p.group) * p.q_token + (sg.head * p.group + rr % p.group) * p.q_head : -1;
       }
       softmax_sync<SOFT>();
       constexpr int QN = kRows * (DIM / 8) / SOFT, QB = QN < 8 ? QN : 8;  // 16-byte pieces of a thread, and per batch
+      const int qn = q_rows / kRows * QN;
 #pragma unroll 1
-      for (int i0 = 0; i0 < QN; i0 += QB) {
+      for (int i0 = 0; i0 < qn; i0 += QB) {
         uint4 x[QB];
 #pragma unroll
         for (int u = 0; u < QB; ++u) {
@@ -357,7 +397,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int u = 0; u < QB; ++u) {
           const int e = st + (i0 + u) * SOFT, r = e / (DIM / 8), c = e % (DIM / 8);
-          sts128(sbase + (c >> 3) * G::QSUB + r * 128 + (((c & 7) ^ (r & 7)) << 4), x[u]);
+          sts128(sbase + (r / kRows) * G::Q_TILE + (c >> 3) * G::QSUB + (r % kRows) * 128 + (((c & 7) ^ (r & 7)) << 4), x[u]);
         }
       }
       fence_proxy_async_smem();
@@ -365,7 +405,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (st < 2) odd_values[st] = 0;
       softmax_sync<SOFT>();
       if (lane == 0) mbar_arrive(q_full);
-      const int rr = sg.rt * kRows + row, tok = rr / p.group;
+      const int rr = sg.rt * G::ROWS + row, tok = rr / p.group;
       unsigned long long word = 0;
       if (row < rows) {
         word = p.mask ? (unsigned long long)p.mask[sg.i.start + tok] : (2ull << tok) - 1;
@@ -373,14 +413,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       float m = -INFINITY, l = 0.f;
       const int n = sg.kt1 - sg.kt0;
-      const bool idle = quarter * 32 >= rows;  // a warp without rows: its P is never looked at
+      const bool idle = row - lane >= rows;  // a warp without rows: its P is never looked at
       for (int i = 0; i < n; ++i, ++tile) {
-        // slots of the item: K0, K1, V0, K2, V1, ..., K(n-1), V(n-2), V(n-1)
-        const uint32_t v_slot = ring + (i + 1 < n ? 2 * i + 2 : 2 * n - 1);
-        if (STREAMS == 2 && (int)(tile & 1) != stream) continue;
-        const uint32_t b = tile % G::SBUFS;
+        if (STREAMS == 2 && !wide && (i & 1) != stream) continue;
+        const uint32_t v_slot = ring + 2 * i + 1;
+        const uint32_t b = STREAMS == 2 ? (uint32_t)stream : took & 1;
+        const uint32_t phase = STREAMS == 2 ? took & 1 : (took >> 1) & 1;
+        ++took;
         const uint32_t s_col = lanes + b * KT;
-        if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(s_full(b), (tile / G::SBUFS) & 1, abort_flag));
+        if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(s_full(b), phase, abort_flag));
         tc_fence_after();
         const uint32_t groups = info[tile % kInfo];
         const int key0 = (sg.kt0 + i) * KT;
@@ -434,7 +475,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const float mn = fmaxf(m, top * p.scale_log2);
           // rescale when the maximum has grown by more than 2^8 (or was -inf)
           const bool grow = mn > m + 8.f;
-          const bool first = i < STREAMS;  // this stream's first tile: no output yet
+          const bool first = i < (wide ? 1 : STREAMS);  // this group's first tile: no output yet
           if (__any_sync(0xFFFFFFFFu, grow)) {
             const float alpha = grow ? exp2_approx(m - mn) : 1.f;
             if (grow) m = mn;
@@ -477,17 +518,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       ring += 2 * n;
       // ---- the item's output
-      ml[stream * kRows + row] = make_float2(m, l);
+      ml[stream * kRows + lane_row] = make_float2(m, l);
       if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(o_full, item & 1, abort_flag));
       ++item;
       softmax_sync<SOFT>();
       tc_fence_after();
       if (!idle) {
-        // streams with tiles: the one of the item's first tile, and the other when there are two
-        const uint32_t t0 = tile - n;
-        const int s0 = STREAMS == 2 ? (int)(t0 & 1) : 0;
-        const bool both = STREAMS == 2 && n > 1;
-        const float2 a = ml[s0 * kRows + row], c2 = both ? ml[(s0 ^ 1) * kRows + row] : make_float2(-INFINITY, 0.f);
+        // the group whose accumulator this thread reads, and the other one if it has a part of the same rows
+        const int s0 = wide ? stream : 0;
+        const bool both = STREAMS == 2 && !wide && n > 1;
+        const float2 a = ml[s0 * kRows + lane_row], c2 = both ? ml[kRows + lane_row] : make_float2(-INFINITY, 0.f);
         const float M = fmaxf(a.x, c2.x), base = M == -INFINITY ? 0.f : M;
         const float f0 = exp2_approx(a.x - base), f1 = exp2_approx(c2.x - base);
         const float L = a.y * f0 + c2.y * f1;
@@ -495,14 +535,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
         const float g0 = whole ? f0 * inv : f0, g1 = whole ? f1 * inv : f1;
         // slot 0: the item began before this share; slot 1: it goes on after it
-        const Partial<DIM, kRows> part(p.partials, blockIdx.x, sg.kt0 > 0 ? 0 : 1);
-        if (st == 0 && sg.kt0 > 0 && sg.kt1 == sg.ktiles) leave_record<kRows>(p, sg, plan.at, plan.share, rows);
+        const Partial<DIM, G::ROWS> part(p.partials, blockIdx.x, sg.kt0 > 0 ? 0 : 1);
+        if (st == 0 && sg.kt0 > 0 && sg.kt1 == sg.ktiles) leave_record<typename G::Tiles>(p, sg);
         uint16_t *out = p.out + ((long long)(sg.i.start + tok) * p.heads + sg.head * p.group + rr % p.group) * DIM;
         const uint32_t odd[2] = {odd_values[0], odd_values[1]};
         const uint32_t oc = lanes + G::COL_O;
-        constexpr int COLS = DIM / STREAMS;  // columns of a group
+        const int cols = wide ? DIM : DIM / STREAMS, col0 = wide ? 0 : stream * cols;  // columns of this group
 #pragma unroll 1
-        for (int c = stream * COLS; c < (stream + 1) * COLS; c += 32) {
+        for (int c = col0; c < col0 + cols; c += 32) {
           float x[32];
           tmem_ld32_nowait(oc + s0 * DIM + c, x);
           tmem_wait_ld();
@@ -510,7 +550,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int e = 0; e < 32; ++e) x[e] *= g0;
           if (both) {
             float y[32];
-            tmem_ld32_nowait(oc + (s0 ^ 1) * DIM + c, y);
+            tmem_ld32_nowait(oc + DIM + c, y);
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[e] = fmaf(y[e], g1, x[e]);
@@ -541,7 +581,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               *reinterpret_cast<float4 *>(part.at(row, c + e)) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
           }
         }
-        if (mine && !whole && stream == 0) *part.ml(row) = make_float2(M, L);
+        if (mine && !whole && (wide || stream == 0)) *part.ml(row) = make_float2(M, L);
       }
       // the next item's Q, odd values and maxima: after everyone is here
       softmax_sync<SOFT>();
@@ -574,7 +614,7 @@ cudaError_t launch_tc_dim(const AttnCall &c, const AttnParams &p) {
   const int br = std::min(c.cache.page_rows, G::KT);
   if (!encode_cache(&tk, c.cache.k, c.cache, br, 128) || !encode_cache(&tv, c.cache.v, c.cache, br, 128))
     return cudaErrorInvalidValue;
-  return launch_dependent(kern, std::min(c.sm_count, kMaxCtas), kTcThreads, G::SMEM, c.stream, tk, tv, p);
+  return launch_dependent(kern, std::min(c.sm_count, kTcMaxCtas), kTcThreads, G::SMEM, c.stream, tk, tv, p);
 }
 
 }  // namespace
