@@ -12,7 +12,8 @@
 //
 //   warp 0        copies: K and V tiles by TMA through the page table, into one
 //                 ring of slots (K0, V0, K1, V1, ...)
-//   warp 1        one thread issues all MMAs; TMEM allocation
+//   warps 1, 2    one thread each issues the MMAs of a softmax group of a wide
+//                 item; otherwise warp 1 issues them all. TMEM allocation
 //   warps 4-7     softmax group 0
 //   warps 8-11    softmax group 1 (dim 64 and 128)
 //
@@ -175,14 +176,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < G::SLOTS; ++i) {
       mbar_init(full(i), 1);
-      mbar_init(empty(i), 1);
+      mbar_init(empty(i), STREAMS);
     }
     for (int i = 0; i < G::SBUFS; ++i) {
       mbar_init(s_full(i), 1);
       mbar_init(p_full(i), 4);
     }
     mbar_init(q_full, SOFT / 32);
-    mbar_init(o_full, 1);
+    mbar_init(o_full, STREAMS);
     *abort_flag = 0;
     odd_values[0] = odd_values[1] = 0;
     fence_mbar_init();
@@ -268,86 +269,87 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_wait_drain(full(u % G::SLOTS), (u / G::SLOTS) & 1);
       }
     }
-  } else if (warp == kWarpMma) {
+  } else if (warp < kWarpMma + STREAMS) {
     // ------------------------------------------------------------ MMAs
     if (lane == 0) {
       constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, KT);
       constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, DIM) | kIdescBMn;
+      const int mine = warp - kWarpMma;  // the softmax group served
       uint32_t ring = 0, item = 0, turn = 0;
       uint32_t made = 0;  // bit b: the parity of the scores written to S buffer b, the phase of its barriers
       bool ok = true;
-      auto slot = [&](uint32_t r) { return sbase + G::OFF_SLOT + (r % G::SLOTS) * G::SLOT; };
+      const uint64_t q_desc = smem_desc(sbase, 16);
+      // Ring slot r has arrived. (A parity only tells two uses of a slot apart: whoever waits here has itself waited for
+      // the slot's use before, or for the end of the item that it was part of.)
       auto arrived = [&](uint32_t r) {
-        ok = ok && mbar_wait(full(r % G::SLOTS), (r / G::SLOTS) & 1, abort_flag);
-        tc_fence_after();
+        return mbar_wait<true>(full(r % G::SLOTS), (r / G::SLOTS) & 1, abort_flag);
       };
-      // S buffer b = Q tile qt . K^T of ring slot r. The buffer's last P was taken by an MMA issued before.
-      auto scores = [&](uint32_t b, int qt, uint32_t r) {
-        if (!ok) return;
-        const uint32_t q = sbase + qt * G::Q_TILE, k = slot(r);
-#pragma unroll
-        for (int c = 0; c < DIM / 16; ++c)
-          tc_mma_f16(tmem + b * KT, smem_desc(q + (c / 4) * G::QSUB + (c % 4) * 32, 16),
-                     smem_desc(k + (c / 4) * G::SUB + (c % 4) * 32, 16), idesc_s, c != 0 ? 1u : 0u);
-        tc_commit(s_full(b));
-        made ^= 1u << b;
-      };
-      // O of group `o` (+)= P of buffer b . V of ring slot r
-      auto output = [&](uint32_t b, uint32_t o, uint32_t r, bool first) {
-        ok = ok && mbar_wait(p_full(b), (made >> b & 1) ^ 1, abort_flag);
-        if (!ok) return;
-        tc_fence_after();
-        const uint32_t v = slot(r), d = tmem + G::COL_O + o * DIM;
-#pragma unroll
-        for (int c = 0; c < KT / 16; ++c)
-          tc_mma_f16_ts(d, tmem + b * KT + 8 * c, smem_desc(v + c * 2048, G::SUB), idesc_o, first && c == 0 ? 0u : 1u);
-      };
-      auto give = [&](uint32_t r) {
-        if (ok) tc_commit(empty(r % G::SLOTS));
+      // a slot is free once both threads' MMAs have read it; where one thread issues them all it gives it back for both
+      auto release = [&](uint32_t slot, bool wide) {
+        tc_commit(empty(slot));
+        if (STREAMS == 2 && !wide) tc_commit(empty(slot));
       };
       while (ok && next_segment<typename G::Tiles>(p, cur, share, sg)) {
         ok = mbar_wait(q_full, item & 1, abort_flag);
         ++item;
         const int n = sg.kt1 - sg.kt0;
-        if (STREAMS == 2 && sg.rows > kRows) {
-          // wide: per key tile both groups, each output before the scores that take its buffer
-          for (int i = 0; ok && i <= n; ++i) {
-            const uint32_t k = ring + 2 * i, v = k - 1;
-            if (i > 0) {
-              arrived(v);
-              output(0, 0, v, i == 1);
+        const bool wide = STREAMS == 2 && sg.rows > kRows;
+        // Visits to the S buffers in turn. Each first takes the P that the buffer holds (its last scores' weights) into
+        // the output, then writes the next scores: tile v / 2 of group v % 2, or tile v.
+        const int scores = wide ? 2 * n : n;
+        const int step = wide ? 2 : 1, last = wide || mine == 0 ? scores + 2 : 0;
+        for (int v = wide ? mine : 0; ok && v < last; v += step) {
+          const uint32_t b = STREAMS == 2 ? v & 1 : (turn + v) & 1;
+          const int was = v - 2;
+          if (was >= 0) {
+            const uint32_t r = ring + 2 * (wide ? was >> 1 : was) + 1;  // the values' ring slot
+            ok = arrived(r) && mbar_wait<true>(p_full(b), (made >> b & 1) ^ 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            uint64_t vd = smem_desc(sbase + G::OFF_SLOT + (r % G::SLOTS) * G::SLOT, G::SUB);
+            uint32_t pa = tmem + b * KT;
+            const uint32_t d = tmem + G::COL_O + (STREAMS == 2 ? b * DIM : 0);
+            uint32_t add = was >= (wide ? 2 : STREAMS);  // the group's first output of the item overwrites
+#pragma unroll
+            for (int c = 0; c < KT / 64; ++c) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                tc_mma_f16_ts(d, pa + 8 * k, vd + k * (2048 >> 4), idesc_o, add);
+                add = 1;
+              }
+              pa += 32;
+              vd += 4 * (2048 >> 4);
             }
-            if (i < n) {
-              arrived(k);
-              scores(0, 0, k);
-            }
-            if (i > 0) {
-              output(1, 1, v, i == 1);
-              give(v);
-            }
-            if (i < n) {
-              scores(1, 1, k);
-              give(k);
-            }
+            release(r % G::SLOTS, wide);
           }
-        } else {
-          // the scores of tile i, then the output of tile i - 1
-          for (int i = 0; ok && i <= n; ++i) {
-            const uint32_t k = ring + 2 * i, v = k - 1;
-            const uint32_t b = STREAMS == 2 ? i & 1 : (turn + i) & 1;
-            if (i < n) {
-              arrived(k);
-              scores(b, 0, k);
-              give(k);
+          if (v < scores) {
+            const uint32_t r = ring + 2 * (wide ? v >> 1 : v);  // the keys' ring slot
+            ok = arrived(r);
+            if (!ok) break;
+            tc_fence_after();
+            uint64_t kd = smem_desc(sbase + G::OFF_SLOT + (r % G::SLOTS) * G::SLOT, 16);
+            uint64_t qd = q_desc + (wide && b ? G::Q_TILE >> 4 : 0);
+            const uint32_t d = tmem + b * KT;
+            uint32_t add = 0;
+#pragma unroll
+            for (int c = 0; c < G::CH; ++c) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                tc_mma_f16(d, qd + 2 * k, kd + 2 * k, idesc_s, add);
+                add = 1;
+              }
+              qd += G::QSUB >> 4;
+              kd += G::SUB >> 4;
             }
-            if (i > 0) {
-              arrived(v);
-              output(b ^ 1, STREAMS == 2 ? b ^ 1 : 0, v, i - 1 < STREAMS);
-              give(v);
-            }
+            tc_commit(s_full(b));
+            made ^= 1u << b;
+            release(r % G::SLOTS, wide);
           }
-          turn += n;
         }
+        // the phases of the buffers that the other thread wrote
+        if (wide) made ^= (n & 1u) << (mine ^ 1);
+        else if (mine == 1) made ^= ((n + 1) / 2 & 1u) | (n / 2 & 1u) << 1;
+        turn += n;
         ring += 2 * n;
         tc_commit(o_full);
       }
