@@ -666,27 +666,30 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
 }
 
 // ---------------------------------------------------------------------------
-// Joining partials: WPR warps per query row of an item that was split. Every
-// block lists the records (a scan over one number per CTA) and takes its share
-// of their rows. The weights 2^(m_c - M) of a row's partials are formed first,
-// so the sums over them have no chain of dependent steps.
+// Joining the partials of an item that was split. A block lists the records (a
+// scan over one number per CTA) and takes its share of their groups of 8 query
+// rows. A warp covers 8 rows by 16 elements, so that its loads are whole
+// 128-byte lines of the partials and its stores whole sectors. The weights
+// 2^(m_c - M) need maxima and sums alone, so the sums over partials are no
+// chain of dependent loads. SPLIT: the block's eight warps share one such
+// square's partials (few items, each over many CTAs); otherwise they stand side
+// by side along the row.
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 
-template <int DIM, int ROWS, int WPR>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnParams p, int ctas) {
-  constexpr int V = DIM > 128 ? DIM / 128 : 1;  // blocks of four elements of a lane
-  constexpr int TEAMS = 8 / WPR;
+template <int DIM, int ROWS, bool SPLIT>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnParams p, int ctas) {
+  constexpr int WARPS = kJoinThreads / 32, SQUARES = DIM / 16;  // squares along a row
   using Part = Partial<DIM, ROWS>;
-  __shared__ int ends[kMaxCtas];  // rows of records 0 .. c
-  __shared__ int sums[8];
-  __shared__ float4 acc[WPR > 1 ? 8 : 1][DIM / 4];
+  __shared__ int ends[kMaxCtas];  // work of records 0 .. c
+  __shared__ int sums[WARPS];
+  __shared__ float4 acc[SPLIT ? WARPS : 1][32];
   grid_dependency_wait();
   grid_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int total = 0;
   for (int c0 = 0; c0 < ctas; c0 += kJoinThreads) {
-    int v = c0 + tid < ctas ? p.joins[c0 + tid] : 0;
+    int v = c0 + tid < ctas ? (p.joins[c0 + tid] + 7) / 8 * (SPLIT ? SQUARES : 1) : 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
@@ -696,82 +699,66 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnParams p, 
     __syncthreads();
     int before = total;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
       if (w < warp) before += sums[w];
       total += sums[w];
     }
     if (c0 + tid < ctas) ends[c0 + tid] = before + v;
     __syncthreads();
   }
-  const int team = warp / WPR, wi = warp % WPR;
-  const int step = gridDim.x * TEAMS;
-  // (with WPR = 8 a block is one team, so all of it goes round together)
-  for (int e = blockIdx.x * TEAMS + team; e < total; e += step) {
+  for (int e = blockIdx.x; e < total; e += gridDim.x) {  // (the whole block goes round together)
     int c1 = 0;
     for (int hi = ctas; c1 < hi;) {
       const int mid = (c1 + hi) >> 1;
       if (ends[mid] > e) hi = mid;
       else c1 = mid + 1;
     }
-    const int r = e - (c1 ? ends[c1 - 1] : 0);
+    const int local = e - (c1 ? ends[c1 - 1] : 0);
     const int4 rec = reinterpret_cast<const int4 *>(p.joins + kMaxCtas)[c1];
-    const int c0 = rec.x, n = c1 - c0 + 1;
+    const int rows = p.joins[c1], c0 = rec.x, n = c1 - c0 + 1;
+    const int r0 = (SPLIT ? local / SQUARES : local) * 8 + (lane & 7), r = min(r0, rows - 1);
     // the first CTA ended its share inside the item (slot 1), the others began theirs in it (slot 0)
     auto part = [&](int c) { return Part(p.partials, c0 + c, c == 0 ? 1 : 0); };
     float M = -INFINITY;
-    for (int c = lane; c < n; c += 32) M = fmaxf(M, part(c).ml(r)->x);
-#pragma unroll
-    for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
+#pragma unroll 4
+    for (int c = 0; c < n; ++c) M = fmaxf(M, part(c).ml(r)->x);
     const float base = M == -INFINITY ? 0.f : M;
     float L = 0.f;
-    for (int c = lane; c < n; c += 32) {
+#pragma unroll 4
+    for (int c = 0; c < n; ++c) {
       const float2 ml = *part(c).ml(r);
       L += ml.y * exp2_approx(ml.x - base);
     }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, d);
-    float4 x[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int c = wi; c < n; c += WPR) {
-      const Part s = part(c);
-      const float w = exp2_approx(s.ml(r)->x - base);
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        if (lane >= DIM / 4) continue;
-        const float4 y = *reinterpret_cast<const float4 *>(s.at(r, 4 * (lane + 32 * k)));
-        x[k].x = fmaf(w, y.x, x[k].x);
-        x[k].y = fmaf(w, y.y, x[k].y);
-        x[k].z = fmaf(w, y.z, x[k].z);
-        x[k].w = fmaf(w, y.w, x[k].w);
-      }
-    }
     const float inv = (L > 0.f || L != L) ? (p.c.e4m3 ? p.c.v.scale[rec.w] : 1.f) / L : 0.f;
     const int rr = rec.z + r, tok = rec.y + rr / p.group;
-    uint2 *out = reinterpret_cast<uint2 *>(p.out + ((long long)tok * p.heads + rec.w * p.group + rr % p.group) * DIM);
-    auto store = [&](int d4, const float4 &y) {
-      out[d4] = make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
-    };
-    if constexpr (WPR == 1) {
-#pragma unroll
-      for (int k = 0; k < V; ++k)
-        if (lane < DIM / 4) store(lane + 32 * k, x[k]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < V; ++k)
-        if (lane < DIM / 4) acc[warp][lane + 32 * k] = x[k];
-      __syncthreads();
-      if (tid < DIM / 4) {
-        float4 y = acc[0][tid];
-#pragma unroll
-        for (int w = 1; w < WPR; ++w) {
-          const float4 z = acc[w][tid];
-          y = make_float4(y.x + z.x, y.y + z.y, y.z + z.z, y.w + z.w);
-        }
-        store(tid, y);
+    uint16_t *out = p.out + ((long long)tok * p.heads + rec.w * p.group + rr % p.group) * DIM;
+    for (int sq = SPLIT ? local % SQUARES : warp; sq < SQUARES; sq += SPLIT ? SQUARES : WARPS) {
+      const int d = sq * 16 + (lane >> 3) * 4;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int c = SPLIT ? warp : 0; c < n; c += SPLIT ? WARPS : 1) {
+        const Part s = part(c);
+        const float w = exp2_approx(s.ml(r)->x - base);
+        const float4 y = *reinterpret_cast<const float4 *>(s.at(r, d));
+        x.x = fmaf(w, y.x, x.x);
+        x.y = fmaf(w, y.y, x.y);
+        x.z = fmaf(w, y.z, x.z);
+        x.w = fmaf(w, y.w, x.w);
       }
-      __syncthreads();
+      if constexpr (SPLIT) {
+        acc[warp][lane] = x;
+        __syncthreads();
+        if (warp == 0) {
+#pragma unroll
+          for (int w = 1; w < WARPS; ++w) {
+            const float4 y = acc[w][lane];
+            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+          }
+        }
+      }
+      if (r0 < rows && (!SPLIT || warp == 0))
+        *reinterpret_cast<uint2 *>(out + d) = make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+      if (SPLIT) __syncthreads();
     }
   }
 }
@@ -783,13 +770,14 @@ constexpr size_t kJoinBytes = ((size_t)kMaxCtas * 5 * sizeof(int) + 255) / 256 *
 
 template <int DIM, int ROWS>
 cudaError_t launch_join(const AttnCall &c, const AttnParams &p, int ctas) {
-  // Few items: each is split over many CTAs, so eight warps join a row; many: one warp does
+  // Few items: each is split over many CTAs, so a block's warps share the partials of a square
   const long long items = (long long)c.rows.rows * c.cache.kv_heads * ((c.max_tree * p.group + ROWS - 1) / ROWS);
-  // at most one record per CTA and per item, of at most ROWS rows
-  const long long rows = std::min((long long)ctas, items) * std::min(ROWS, c.max_tree * p.group);
-  if (items * 4 <= ctas)
-    return launch_dependent(join_kernel<DIM, ROWS, 8>, (unsigned)std::min(rows, 8LL * c.sm_count), kJoinThreads, 0, c.stream, p, ctas);
-  return launch_dependent(join_kernel<DIM, ROWS, 1>, (unsigned)std::min((rows + 7) / 8, 4LL * c.sm_count), kJoinThreads, 0, c.stream, p, ctas);
+  // at most one record per CTA and per item
+  const long long groups = std::min((long long)ctas, items) * ((std::min(ROWS, c.max_tree * p.group) + 7) / 8);
+  const bool split = items * 8 <= ctas;
+  const unsigned grid = (unsigned)std::min(groups * (split ? DIM / 16 : 1), 8LL * c.sm_count);
+  return split ? launch_dependent(join_kernel<DIM, ROWS, true>, grid, kJoinThreads, 0, c.stream, p, ctas)
+               : launch_dependent(join_kernel<DIM, ROWS, false>, grid, kJoinThreads, 0, c.stream, p, ctas);
 }
 
 template <int DIM, bool E4M3, int RW>
