@@ -13,7 +13,8 @@
 //   warp 0        copies: K and V tiles by TMA through the page table, into one
 //                 ring of slots (K0, V0, K1, V1, ...)
 //   warps 1, 2    one thread each issues the MMAs of a softmax group of a wide
-//                 item; otherwise warp 1 issues them all. TMEM allocation
+//                 item, taking turns; otherwise warp 1 issues them all. TMEM
+//                 allocation
 //   warps 4-7     softmax group 0
 //   warps 8-11    softmax group 1 (dim 64 and 128)
 //
@@ -61,7 +62,7 @@ struct TcGeo {
   static constexpr int OFF_SLOT = Q_BYTES;
   static constexpr int OFF_ML = OFF_SLOT + SLOTS * SLOT;
   static constexpr int OFF_BAR = OFF_ML + STREAMS * kRows * 8;
-  static constexpr int NBARS = 2 * SLOTS + 2 * SBUFS + 2;
+  static constexpr int NBARS = 2 * SLOTS + 2 * SBUFS + 4;
   static constexpr int OFF_INFO = OFF_BAR + NBARS * 8;
   static constexpr int OFF_MISC = OFF_INFO + kInfo * 4;  // TMEM address, abort flag, odd values
   static constexpr int OFF_PLAN = OFF_MISC + 16;
@@ -172,6 +173,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   auto p_full = [&](uint32_t b) { return bars + 8 * (2 * G::SLOTS + G::SBUFS + b); };    // P written, O rescaled
   const uint32_t q_full = bars + 8 * (2 * G::SLOTS + 2 * G::SBUFS);  // Q written, TMEM of the last item read
   const uint32_t o_full = q_full + 8;                                // the item's MMAs are done
+  auto turn_of = [&](uint32_t w) { return o_full + 8 + 8 * w; };     // an MMA thread's turn to issue
 
   if (tid == 0) {
     for (int i = 0; i < G::SLOTS; ++i) {
@@ -184,6 +186,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     mbar_init(q_full, SOFT / 32);
     mbar_init(o_full, STREAMS);
+    mbar_init(turn_of(0), 1);
+    mbar_init(turn_of(1), 1);
     *abort_flag = 0;
     odd_values[0] = odd_values[1] = 0;
     fence_mbar_init();
@@ -276,6 +280,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, DIM) | kIdescBMn;
       const int mine = warp - kWarpMma;  // the softmax group served
       uint32_t ring = 0, item = 0, turn = 0;
+      // Turns: a visit's two products are issued in one go. Left to themselves the two threads' MMAs mix, both groups
+      // wait for both, and then both do softmax while the tensor core rests; in turn, one group's softmax runs under
+      // the other's MMAs.
+      uint32_t turns = 0;
       uint32_t made = 0;  // bit b: the parity of the scores written to S buffer b, the phase of its barriers
       bool ok = true;
       const uint64_t q_desc = smem_desc(sbase, 16);
@@ -288,6 +296,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       auto release = [&](uint32_t slot, bool wide) {
         tc_commit(empty(slot));
         if (STREAMS == 2 && !wide) tc_commit(empty(slot));
+      };
+      // thread 0 goes first; later turns come from the other thread
+      auto my_turn = [&]() {
+        const uint32_t parity = mine == 0 ? (turns & 1) ^ 1 : turns & 1;
+        ++turns;
+        return mbar_wait<true>(turn_of(mine), parity, abort_flag);
       };
       while (ok && next_segment<typename G::Tiles>(p, cur, share, sg)) {
         ok = mbar_wait(q_full, item & 1, abort_flag);
@@ -304,6 +318,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (was >= 0) {
             const uint32_t r = ring + 2 * (wide ? was >> 1 : was) + 1;  // the values' ring slot
             ok = arrived(r) && mbar_wait<true>(p_full(b), (made >> b & 1) ^ 1, abort_flag);
+            if (wide) ok = ok && (v >= scores || arrived(r + 1)) && my_turn();  // (r + 1: the keys that follow)
             if (!ok) break;
             tc_fence_after();
             uint64_t vd = smem_desc(sbase + G::OFF_SLOT + (r % G::SLOTS) * G::SLOT, G::SUB);
@@ -324,9 +339,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           if (v < scores) {
             const uint32_t r = ring + 2 * (wide ? v >> 1 : v);  // the keys' ring slot
-            ok = arrived(r);
-            if (!ok) break;
-            tc_fence_after();
+            if (!wide || was < 0) {
+              ok = arrived(r) && (!wide || my_turn());
+              if (!ok) break;
+              tc_fence_after();
+            }
             uint64_t kd = smem_desc(sbase + G::OFF_SLOT + (r % G::SLOTS) * G::SLOT, 16);
             uint64_t qd = q_desc + (wide && b ? G::Q_TILE >> 4 : 0);
             const uint32_t d = tmem + b * KT;
@@ -345,6 +362,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             made ^= 1u << b;
             release(r % G::SLOTS, wide);
           }
+          if (wide) mbar_arrive(turn_of(mine ^ 1));
         }
         // the phases of the buffers that the other thread wrote
         if (wide) made ^= (n & 1u) << (mine ^ 1);
