@@ -40,6 +40,9 @@
 namespace w4a16 {
 namespace {
 
+// What beginning and ending an item costs, in key tiles: with 2 rather than none, 48
+// ragged rows of an e4m3 cache 153 -> 146 us; with 3, 143 us, but one short row 13.8 -> 15.1 us.
+constexpr int kRowsLead = 2;
 constexpr int kComputeWarps = 4;
 constexpr int kThreads = (kComputeWarps + 1) * 32;
 
@@ -48,7 +51,7 @@ struct RowsGeo {
   static constexpr int RW = RWT, KW = kComputeWarps / RWT;
   static constexpr int ROWS = 16 * RW;
   static constexpr int KT = RW <= 2 && (DIM * (E4M3 ? 1 : 2) <= 128 || (DIM == 256 && E4M3)) ? 128 : 64;  // keys of a stage
-  using Tiles = Tiling<ROWS, KT, ROWS>;
+  using Tiles = Tiling<ROWS, KT, ROWS, kRowsLead>;
   static constexpr int KPW = KT / KW;         // keys of a warp per stage
   static constexpr int ELT = E4M3 ? 1 : 2;
   static constexpr int ROWB = DIM * ELT;       // bytes of a cache row

@@ -6,10 +6,11 @@
 // packed token by token into tiles of ROWS rows, so its items are
 // (kv head, row tile), each of ceil(K / KT) key tiles. A key tile counts one
 // unit per UNIT query rows (the tcgen05 kernel works on 256 rows at a time, and
-// takes twice as long over more than 128). All key tiles of all items, in the
-// order (b, head, row tile, key tile), form one list of units, and every CTA
-// takes an equal, contiguous share of it (to whole key tiles), whatever the
-// lengths are: long contexts are split over many CTAs, short ones share one. An item whose tiles
+// takes twice as long over more than 128), and an item counts LEAD units before
+// its first tile, for what beginning and ending an item costs. All items, in
+// the order (b, head, row tile), form one list of units, and every CTA takes an
+// equal, contiguous share of it (to whole key tiles), whatever the lengths are:
+// long contexts are split over many CTAs, short ones share one. An item whose tiles
 // lie in one share is finished there; otherwise each CTA leaves a partial
 // result (running maximum, sum and unnormalised output per row) in the
 // workspace, and a second kernel joins them in the order of the CTAs, so
@@ -82,10 +83,10 @@ __device__ __forceinline__ RowInfo row_info(const AttnParams &p, int b, bool fla
   return i;
 }
 
-// Query rows of a tile, keys of a tile, query rows of a unit
-template <int ROWS_, int KT_, int UNIT_>
+// Query rows of a tile, keys of a tile, query rows of a unit, units that an item costs by itself
+template <int ROWS_, int KT_, int UNIT_, int LEAD_>
 struct Tiling {
-  static constexpr int ROWS = ROWS_, KT = KT_, UNIT = UNIT_;
+  static constexpr int ROWS = ROWS_, KT = KT_, UNIT = UNIT_, LEAD = LEAD_;
 };
 
 template <int KT>
@@ -98,7 +99,9 @@ __device__ __forceinline__ int row_tiles(const RowInfo &i, int group) {
 }
 template <class T>
 __device__ __forceinline__ long long units_of(const RowInfo &i, const AttnParams &p) {
-  return i.n > 0 ? (long long)p.c.kv_heads * row_tiles<T::UNIT>(i, p.group) * key_tiles<T::KT>(i) : 0;
+  if (i.n == 0) return 0;
+  return p.c.kv_heads * ((long long)row_tiles<T::UNIT>(i, p.group) * key_tiles<T::KT>(i) +
+                         row_tiles<T::ROWS>(i, p.group) * T::LEAD);
 }
 
 // A CTA's place in the work list: units [at, end) are its share, `unit` is the
@@ -142,9 +145,9 @@ __device__ void plan_share(const AttnParams &p, PlanShared &s) {
     total += x;
   }
   const long long first = before + upto - mine;
-  // as many CTAs as get two units each (a share then holds a whole key tile of any item), and no share larger than it
-  // has to be
-  const long long ctas = max(1ll, min((long long)gridDim.x, total / 2));
+  // as many CTAs as get LEAD + 2 units each (a share then holds a whole key tile of any item), and no share larger
+  // than it has to be
+  const long long ctas = max(1ll, min((long long)gridDim.x, total / (T::LEAD + 2)));
   const long long share = max(1ll, (total + ctas - 1) / ctas);
   const long long at = min(share * blockIdx.x, total), end = min(at + share, total);
   if (tid == 0) {
@@ -159,12 +162,12 @@ __device__ void plan_share(const AttnParams &p, PlanShared &s) {
       const RowInfo i = row_info(p, b, false);
       const long long n = units_of<T>(i, p);
       if (at < f + n) {
-        const int kt = key_tiles<T::KT>(i);
-        const long long per_head = (long long)row_tiles<T::UNIT>(i, p.group) * kt, o = at - f;
+        const long long per_head = n / p.c.kv_heads, o = at - f;
+        const long long per_tile = (long long)key_tiles<T::KT>(i) * (T::ROWS / T::UNIT) + T::LEAD;  // of a full row tile
         s.b = b;
         s.head = (int)(o / per_head);
-        s.rt = (int)(o % per_head / (kt * (T::ROWS / T::UNIT)));
-        s.unit = f + s.head * per_head + (long long)s.rt * kt * (T::ROWS / T::UNIT);
+        s.rt = (int)(o % per_head / per_tile);
+        s.unit = f + s.head * per_head + s.rt * per_tile;
         break;
       }
       f += n;
@@ -199,12 +202,12 @@ __device__ __forceinline__ bool next_segment(const AttnParams &p, Cursor &c, lon
     s.rows = min(T::ROWS, s.i.n * p.group - c.rt * T::ROWS);
     s.ktiles = key_tiles<T::KT>(s.i);
     const int cost = T::ROWS == T::UNIT ? 1 : (s.rows + T::UNIT - 1) / T::UNIT;
-    const long long unit = c.unit, units = (long long)s.ktiles * cost;
+    const long long first = c.unit + T::LEAD, units = (long long)s.ktiles * cost;  // of the item's first tile
     // a key tile belongs to the share that holds its last unit
-    s.kt0 = c.at > unit ? (int)((c.at - unit) / cost) : 0;
-    s.kt1 = c.end - unit >= units ? s.ktiles : (int)((c.end - unit) / cost);
-    s.first_cta = (int)((unit + cost - 1) / share);
-    c.unit += units;
+    s.kt0 = c.at > first ? (int)((c.at - first) / cost) : 0;
+    s.kt1 = c.end - first >= units ? s.ktiles : c.end > first ? (int)((c.end - first) / cost) : 0;
+    s.first_cta = (int)((first + cost - 1) / share);
+    c.unit = first + units;
     if (++c.rt == row_tiles<T::ROWS>(s.i, p.group)) {
       c.rt = 0;
       if (++c.head == p.c.kv_heads) {

@@ -40,6 +40,10 @@ namespace {
 
 constexpr int kTcThreads = 384;
 constexpr int kWarpCopy = 0, kWarpMma = 1, kWarpSoftmax = 4;
+// What beginning and ending an item costs (Q, filling and draining the pipeline, the output), in tiles of 128 query
+// rows: with 4 rather than none, 16 ragged trees of up to 64 nodes 87 -> 71 us; with 6, 68 us, but 12 rows of up to 8
+// nodes 28.5 -> 29.7 us and one 16-node tree 22.6 -> 24.0 us.
+constexpr int kTcLead = 4;
 constexpr int kRows = 128;  // query rows of an MMA
 constexpr int kInfo = 16;  // tiles whose key-group words are kept
 
@@ -54,7 +58,7 @@ struct TcGeo {
   static constexpr int Q_TILE = CH * QSUB;
   static constexpr int ROWS = tc_attn_rows(DIM);
   static constexpr int Q_BYTES = ROWS / kRows * Q_TILE;
-  using Tiles = Tiling<ROWS, KT, kRows>;
+  using Tiles = Tiling<ROWS, KT, kRows, kTcLead>;
   static constexpr int SLOTS = DIM == 64 ? 12 : 5;
   static constexpr int SBUFS = 2;                     // S buffers: one per stream, or two of the one
   // TMEM columns: S (P over its first half), then O
