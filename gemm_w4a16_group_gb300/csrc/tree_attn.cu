@@ -190,7 +190,6 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
   plan_share<typename G::Tiles, kThreads>(p, plan);
   __syncthreads();
   Cursor cur{plan.at, plan.end, plan.at < plan.end ? plan.unit : plan.end, plan.b, plan.head, plan.rt};
-  const long long share = plan.share;
   Segment sg;
 
   if (warp == kComputeWarps) {
@@ -206,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
     }
     uint32_t st = 0;
     bool ok = true;
-    while (ok && next_segment<typename G::Tiles>(p, cur, share, sg)) {
+    while (ok && next_segment<typename G::Tiles>(p, cur, sg)) {
       const int32_t *ids = p.r.table + (long long)sg.b * p.r.max_pages;
       auto id_of = [&](int kt) {  // -1: past the keys
         const long long key = (long long)kt * G::KT + part * br;
@@ -261,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
   uint32_t st = 0;
   bool ok = true;  // after a wait that gave up: no more waits, but every barrier below is still met
 
-  while (next_segment<typename G::Tiles>(p, cur, share, sg)) {
+  while (next_segment<typename G::Tiles>(p, cur, sg)) {
     const int rows = sg.rows;
     // ---- q in the order of the A fragments (16 bytes per lane and k step)
     compute_sync();  // the last item's exchange is over
@@ -610,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
     // slot 0: the item began before this share; slot 1: it goes on after it
     const int slot = sg.kt0 > 0 ? 0 : 1;
     const Partial<DIM, G::ROWS> part(p.partials, blockIdx.x, slot);
-    if (tid == 0 && sg.kt0 > 0 && sg.kt1 == sg.ktiles) leave_record<typename G::Tiles>(p, sg);
+    if (tid == 0 && sg.kt0 > 0 && sg.kt1 == sg.ktiles) leave_record<typename G::Tiles>(p, sg, plan.share);
     const float vs = E4M3 ? p.c.v.scale[sg.head] : 1.f;
 #pragma unroll
     for (int sl = 0; sl < KW; ++sl) {

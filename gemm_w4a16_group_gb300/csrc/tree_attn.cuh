@@ -58,6 +58,12 @@ struct Partial {
   __device__ float2 *ml(int r) const { return reinterpret_cast<float2 *>(base + ROWS * DIM) + r; }
 };
 
+// a / b of numbers that are not negative. A 64-bit division takes some hundred
+// instructions, and nearly every work list fits 32 bits.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // One row of the table as the work list sees it
 struct RowInfo {
   int start, n, len, keys;  // first token, new tokens, cached, len + n (no more than the table holds)
@@ -147,8 +153,8 @@ __device__ void plan_share(const AttnParams &p, PlanShared &s) {
   const long long first = before + upto - mine;
   // as many CTAs as get LEAD + 2 units each (a share then holds a whole key tile of any item), and no share larger
   // than it has to be
-  const long long ctas = max(1ll, min((long long)gridDim.x, total / (T::LEAD + 2)));
-  const long long share = max(1ll, (total + ctas - 1) / ctas);
+  const long long ctas = max(1ll, min((long long)gridDim.x, quotient(total, T::LEAD + 2)));
+  const long long share = max(1ll, quotient(total + ctas - 1, ctas));
   const long long at = min(share * blockIdx.x, total), end = min(at + share, total);
   if (tid == 0) {
     s.at = at;
@@ -162,11 +168,11 @@ __device__ void plan_share(const AttnParams &p, PlanShared &s) {
       const RowInfo i = row_info(p, b, false);
       const long long n = units_of<T>(i, p);
       if (at < f + n) {
-        const long long per_head = n / p.c.kv_heads, o = at - f;
+        const long long per_head = quotient(n, p.c.kv_heads), o = at - f;
         const long long per_tile = (long long)key_tiles<T::KT>(i) * (T::ROWS / T::UNIT) + T::LEAD;  // of a full row tile
         s.b = b;
-        s.head = (int)(o / per_head);
-        s.rt = (int)(o % per_head / per_tile);
+        s.head = (int)quotient(o, per_head);
+        s.rt = (int)quotient(o - s.head * per_head, per_tile);
         s.unit = f + s.head * per_head + s.rt * per_tile;
         break;
       }
@@ -179,20 +185,22 @@ __device__ void plan_share(const AttnParams &p, PlanShared &s) {
 struct Segment {
   RowInfo i;
   int b, head, rt, rows, kt0, kt1, ktiles;
-  int first_cta;  // that has a part of the item
+  long long first;  // unit of the item's first key tile
+  int cost;         // units of a key tile
   __device__ bool whole() const { return kt0 == 0 && kt1 == ktiles; }
 };
 
 // Leaves the record of an item that this CTA ends and others began (one thread)
 template <class T>
-__device__ __forceinline__ void leave_record(const AttnParams &p, const Segment &s) {
-  reinterpret_cast<int4 *>(p.joins + kMaxCtas)[blockIdx.x] = make_int4(s.first_cta, s.i.start, s.rt * T::ROWS, s.head);
+__device__ __forceinline__ void leave_record(const AttnParams &p, const Segment &s, long long share) {
+  const int first_cta = (int)quotient(s.first + s.cost - 1, share);  // that has a part of the item
+  reinterpret_cast<int4 *>(p.joins + kMaxCtas)[blockIdx.x] = make_int4(first_cta, s.i.start, s.rt * T::ROWS, s.head);
   p.joins[blockIdx.x] = s.rows;
 }
 
 // Next segment of the share (false: none is left)
 template <class T>
-__device__ __forceinline__ bool next_segment(const AttnParams &p, Cursor &c, long long share, Segment &s) {
+__device__ __forceinline__ bool next_segment(const AttnParams &p, Cursor &c, Segment &s) {
   while (c.unit < c.end) {
     s.i = row_info(p, c.b, false);
     while (s.i.n == 0) s.i = row_info(p, ++c.b, false);  // rows without work; units are left, so one with work follows
@@ -201,12 +209,14 @@ __device__ __forceinline__ bool next_segment(const AttnParams &p, Cursor &c, lon
     s.rt = c.rt;
     s.rows = min(T::ROWS, s.i.n * p.group - c.rt * T::ROWS);
     s.ktiles = key_tiles<T::KT>(s.i);
-    const int cost = T::ROWS == T::UNIT ? 1 : (s.rows + T::UNIT - 1) / T::UNIT;
+    static_assert(T::ROWS <= 2 * T::UNIT, "a key tile costs one unit or two");
+    const int cost = s.rows > T::UNIT ? 2 : 1;
     const long long first = c.unit + T::LEAD, units = (long long)s.ktiles * cost;  // of the item's first tile
     // a key tile belongs to the share that holds its last unit
-    s.kt0 = c.at > first ? (int)((c.at - first) / cost) : 0;
-    s.kt1 = c.end - first >= units ? s.ktiles : c.end > first ? (int)((c.end - first) / cost) : 0;
-    s.first_cta = (int)((first + cost - 1) / share);
+    s.kt0 = c.at > first ? (int)(cost == 1 ? c.at - first : (c.at - first) >> 1) : 0;
+    s.kt1 = c.end - first >= units ? s.ktiles : c.end > first ? (int)(cost == 1 ? c.end - first : (c.end - first) >> 1) : 0;
+    s.first = first;
+    s.cost = cost;
     c.unit = first + units;
     if (++c.rt == row_tiles<T::ROWS>(s.i, p.group)) {
       c.rt = 0;

@@ -208,7 +208,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   Cursor cur{plan.at, plan.end, plan.at < plan.end ? plan.unit : plan.end, plan.b, plan.head, plan.rt};
-  const long long share = plan.share;
   Segment sg;
 
   // A softmax thread holds a row's 128 scores. The block is launched with 384 x 168 registers; the first warpgroup
@@ -231,7 +230,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
     uint32_t ring = 0, tile = 0;
     bool ok = true;
-    while (ok && next_segment<typename G::Tiles>(p, cur, share, sg)) {
+    while (ok && next_segment<typename G::Tiles>(p, cur, sg)) {
       const int32_t *ids = p.r.table + (long long)sg.b * p.r.max_pages;
       const uint64_t policy = sg.i.n * p.group > G::ROWS ? keep : pol;
       auto id_of = [&](int kt) {  // -1: past the keys
@@ -307,7 +306,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         ++turns;
         return mbar_wait<true>(turn_of(mine), parity, abort_flag);
       };
-      while (ok && next_segment<typename G::Tiles>(p, cur, share, sg)) {
+      while (ok && next_segment<typename G::Tiles>(p, cur, sg)) {
         ok = mbar_wait(q_full, item & 1, abort_flag);
         ++item;
         const int n = sg.kt1 - sg.kt0;
@@ -395,7 +394,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint32_t tile = 0, item = 0, ring = 0;
     uint32_t took = 0;  // scores taken by this group (its S buffer, or the two in turn)
     bool ok = true;  // after a wait that gave up: no more waits, but the barriers below are still met
-    while (next_segment<typename G::Tiles>(p, cur, share, sg)) {
+    while (next_segment<typename G::Tiles>(p, cur, sg)) {
       const int rows = sg.rows;
       const bool wide = STREAMS == 2 && rows > kRows;
       const int row = lane_row + (wide ? stream * kRows : 0);  // this thread's query row of the item
@@ -560,7 +559,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const float g0 = whole ? f0 * inv : f0, g1 = whole ? f1 * inv : f1;
         // slot 0: the item began before this share; slot 1: it goes on after it
         const Partial<DIM, G::ROWS> part(p.partials, blockIdx.x, sg.kt0 > 0 ? 0 : 1);
-        if (st == 0 && sg.kt0 > 0 && sg.kt1 == sg.ktiles) leave_record<typename G::Tiles>(p, sg);
+        if (st == 0 && sg.kt0 > 0 && sg.kt1 == sg.ktiles) leave_record<typename G::Tiles>(p, sg, plan.share);
         uint16_t *out = p.out + ((long long)(sg.i.start + tok) * p.heads + sg.head * p.group + rr % p.group) * DIM;
         const uint32_t odd[2] = {odd_values[0], odd_values[1]};
         const uint32_t oc = lanes + G::COL_O;
