@@ -66,7 +66,7 @@ struct TcGeo {
   static constexpr int OFF_SLOT = Q_BYTES;
   static constexpr int OFF_ML = OFF_SLOT + SLOTS * SLOT;
   static constexpr int OFF_BAR = OFF_ML + STREAMS * kRows * 8;
-  static constexpr int NBARS = 2 * SLOTS + 2 * SBUFS + 4;
+  static constexpr int NBARS = 2 * SLOTS + 2 * SBUFS + 5;
   static constexpr int OFF_INFO = OFF_BAR + NBARS * 8;
   static constexpr int OFF_MISC = OFF_INFO + kInfo * 4;  // TMEM address, abort flag, odd values
   static constexpr int OFF_PLAN = OFF_MISC + 16;
@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   auto p_full = [&](uint32_t b) { return bars + 8 * (2 * G::SLOTS + G::SBUFS + b); };    // P written, O rescaled
   const uint32_t q_full = bars + 8 * (2 * G::SLOTS + 2 * G::SBUFS);  // Q written, TMEM of the last item read
   const uint32_t o_full = q_full + 8;                                // the item's MMAs are done
+  const uint32_t o_done = o_full + 24;                               // one group: a tile's output is in the accumulator
   auto turn_of = [&](uint32_t w) { return o_full + 8 + 8 * w; };     // an MMA thread's turn to issue
 
   if (tid == 0) {
@@ -190,6 +191,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     mbar_init(q_full, SOFT / 32);
     mbar_init(o_full, STREAMS);
+    mbar_init(o_done, 1);
     mbar_init(turn_of(0), 1);
     mbar_init(turn_of(1), 1);
     *abort_flag = 0;
@@ -338,6 +340,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               pa += 32;
               vd += 4 * (2048 >> 4);
             }
+            if (STREAMS == 1) tc_commit(o_done);
             release(r % G::SLOTS, wide);
           }
           if (v < scores) {
@@ -504,6 +507,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (grow) m = mn;
             l *= alpha;
             if (!first) {
+              // With two groups, these scores were made after the group's last output. The one group's were made ahead
+              // of it: it may still be under way.
+              if (STREAMS == 1 && ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait<true>(o_done, took & 1, abort_flag));
+              if (STREAMS == 1) tc_fence_after();
 #pragma unroll
               for (int c = 0; c < DIM / 32; ++c) {
                 float y[32];

@@ -199,6 +199,25 @@ def test_large_scores(size):
     check(s, run(s, scale=3.0), scale=3.0)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("size", [1, 6, 30, 64])
+@pytest.mark.parametrize("every", [16, 64, 128])
+def test_a_maximum_that_keeps_growing(dim, size, every):
+    """Scores that rise by 9 powers of two every so many keys, values that fall as fast: each stretch counts as much as
+    the last, and what was summed before has to be scaled down in time, once, and whole. (13 stretches: the first weight
+    is 2^-108, within float32's normal numbers.)"""
+    n = 13 * every - size
+    s = Step([n], [size], 8, 2, dim, 32, seed=every)
+    ids, rows = s.slots(0, n + size)
+    step = torch.arange(n + size, device="cuda") // every
+    s.q.zero_()
+    s.q[:, :, 0] = 4.0
+    s.k.zero_()
+    s.k[ids, :, rows, 0] = (step * (9 * math.log(2) / 4))[:, None].to(BF16)
+    s.v[ids, :, rows] = (s.v[ids, :, rows].float() * 2.0 ** (72 - 9 * step)[:, None, None]).to(BF16)
+    check(s, run(s, scale=1.0), scale=1.0)
+
+
 @pytest.mark.parametrize("size", [4, 30])
 def test_views_and_side_streams(size):
     """q a slice of a fused query/key/value product; the call on another stream, into given buffers."""
