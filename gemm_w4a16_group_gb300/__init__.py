@@ -592,7 +592,8 @@ MAX_ROWS = 4096   # rows that one fork, free or reserve call may name
 
 # w4a16_kv_cache: k, v, k_scale, v_scale; layer, page, head and row strides of
 # each; layers, pages, kv_heads, page_rows, dim, type
-_KV_CACHE = _struct.Struct("=4Q8q6i")
+_KV_BASES = _struct.Struct("=4Q")
+_KV_SHAPE = _struct.Struct("=8q6i")
 
 
 class _Types:
@@ -677,6 +678,16 @@ def _workspace(need, like, dev, stream, handle):
     return ws
 
 
+@functools.lru_cache(maxsize=1024)
+def _kv_shape(shape, ks, vs, e4m3):
+    """The part of w4a16_kv_cache that shape and strides make (the same for all layers of a model)."""
+    if ks[-1] != 1 or vs[-1] != 1:
+        raise ValueError("k_cache, v_cache: the last axis must be contiguous")
+    if len(ks) == 4:
+        ks, vs = (0, *ks), (0, *vs)
+    return _KV_SHAPE.pack(*ks[:4], *vs[:4], *shape, e4m3)
+
+
 def _kv_cache(k_cache, v_cache, k_scale, v_scale, one_layer, dev):
     """The w4a16_kv_cache bytes of a cache given as [pages, kv heads, page
     rows, dim] tensors (any strides, dim contiguous), or with a leading layer
@@ -697,11 +708,9 @@ def _kv_cache(k_cache, v_cache, k_scale, v_scale, one_layer, dev):
         _refuse(k_cache, dt, "k_cache", dev)
     if v_cache.get_device() != dev:
         _refuse(v_cache, dt, "v_cache", dev)
-    ks, vs = k_cache.stride(), v_cache.stride()
-    if ks[-1] != 1 or vs[-1] != 1:
-        raise ValueError("k_cache, v_cache: the last axis must be contiguous")
     if axes == 4:
-        shape, ks, vs = (1, *shape), (0, *ks), (0, *vs)
+        shape = (1, *shape)
+    tail = _kv_shape(shape, k_cache.stride(), v_cache.stride(), e4m3)
     kp = vp = 0
     if e4m3 and one_layer:
         if k_scale is None or v_scale is None:
@@ -710,7 +719,7 @@ def _kv_cache(k_cache, v_cache, k_scale, v_scale, one_layer, dev):
         vp = _flat(v_scale, ty.f32, "v_scale", shape[2], dev)
     elif k_scale is not None or v_scale is not None:
         raise ValueError("k_scale and v_scale belong to float8_e4m3fn caches")
-    return _KV_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), kp, vp, *ks[:4], *vs[:4], *shape, e4m3), shape
+    return _KV_BASES.pack(k_cache.data_ptr(), v_cache.data_ptr(), kp, vp) + tail, shape
 
 
 def _token_rows(t, name, dim, dev):

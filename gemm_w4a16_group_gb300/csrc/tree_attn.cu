@@ -799,14 +799,14 @@ cudaError_t launch_rows(const AttnCall &c, AttnParams &p) {
   const int grid = std::min(G::CTAS * c.sm_count, kMaxCtas);
   cudaError_t e = launch_dependent(kern, grid, kThreads, G::SMEM, c.stream, tk, tv, p);
   if (e != cudaSuccess) return e;
-  return launch_join<DIM, G::ROWS>(c, p, grid);
+  return p.whole ? cudaSuccess : launch_join<DIM, G::ROWS>(c, p, grid);
 }
 
 template <int DIM>
 cudaError_t launch_tc(const AttnCall &c, AttnParams &p) {
   cudaError_t e = launch_tree_tc(c, p);
   if (e != cudaSuccess) return e;
-  return launch_join<DIM, tc_attn_rows(DIM)>(c, p, std::min(c.sm_count, kTcMaxCtas));
+  return p.whole ? cudaSuccess : launch_join<DIM, tc_attn_rows(DIM)>(c, p, std::min(c.sm_count, kTcMaxCtas));
 }
 bool uses_tc(int rows, bool e4m3) { return !e4m3 && rows > 16; }
 
@@ -850,6 +850,7 @@ cudaError_t launch_tree_attention(const AttnCall &c) {
   p.heads = c.heads;
   p.group = c.heads / c.cache.kv_heads;
   p.max_tree = c.max_tree;
+  p.whole = (long long)c.rows.max_pages * c.cache.page_rows <= kWholeKeys;
   p.scale_log2 = c.scale * kLog2e;
   p.out = c.out;
   p.joins = static_cast<int *>(c.workspace);
