@@ -661,6 +661,32 @@ def _empty(shape, dtype, like, stream):
         return _types().empty(shape, dtype=dtype, device=like.device)
 
 
+_small_outputs = {}
+_SMALL, _AT_ONCE = 4096, 32
+
+
+def _int_out(shape, dtype, like, dev, stream, handle):
+    """A new integer tensor, as _empty gives it. Small ones are made 32 at a
+    time, as rows of one allocation: on their own three of them cost more than
+    the call that fills them (10 us against 6). Each is handed out once; their
+    common memory goes back to the stream's pool with the last of them. Under
+    capture every output comes from the graph's pool."""
+    if _torch().cuda.is_current_stream_capturing():
+        return _empty(shape, dtype, like, stream)
+    key = (shape, dtype, dev, handle)
+    ready = _small_outputs.get(key)
+    if not ready:
+        n = 8
+        for d in shape:
+            n *= d
+        if n > _SMALL:
+            return _empty(shape, dtype, like, stream)
+        if len(_small_outputs) >= 256:
+            _small_outputs.clear()
+        ready = _small_outputs[key] = list(_empty((_AT_ONCE, *shape), dtype, like, stream).unbind(0))
+    return ready.pop()
+
+
 _workspaces = {}
 
 
@@ -799,18 +825,19 @@ def tree_accept(target, draft, mask, starts, max_tree, path=None, count=None, to
     pick after the last accepted node)."""
     ty, dev = _types(), _place(target, "target")
     tokens, rows = target.numel(), starts.numel() - 1
+    handle = _on(stream, target)
     if path is None:
-        path = _empty((rows, max_tree), ty.i32, target, stream)
+        path = _int_out((rows, max_tree), ty.i32, target, dev, stream, handle.value)
     if count is None:
-        count = _empty(rows, ty.i32, target, stream)
+        count = _int_out((rows,), ty.i32, target, dev, stream, handle.value)
     if token is None:
-        token = _empty(rows, ty.i64, target, stream)
+        token = _int_out((rows,), ty.i64, target, dev, stream, handle.value)
     rc = lib().w4a16_tree_accept(_flat(target, ty.i64, "target", tokens, dev), _flat(draft, ty.i64, "draft", tokens, dev),
                                  None if mask is None else _flat(mask, ty.i64, "mask", tokens, dev),
                                  _flat(starts, ty.i32, "starts", rows + 1, dev), rows, tokens, max_tree,
                                  _flat(path, ty.i32, "path", rows * max_tree, dev),
                                  _flat(count, ty.i32, "count", rows, dev), _flat(token, ty.i64, "token", rows, dev),
-                                 _on(stream, target))
+                                 handle)
     _check(rc, "w4a16_tree_accept")
     return path, count, token
 
@@ -826,12 +853,13 @@ def kv_compact(k_cache, v_cache, page_table, lengths, path, count, lengths_out=N
     if path.dim() != 2:
         raise ValueError(f"path must be [{rows}, max_tree], not {list(path.shape)}")
     max_tree = path.shape[1]
+    handle = _on(stream, k_cache)
     if lengths_out is None:
-        lengths_out = _empty(rows, ty.i32, k_cache, stream)
+        lengths_out = _int_out((rows,), ty.i32, k_cache, dev, stream, handle.value)
     rc = lib().w4a16_kv_compact(cache, table, width, _flat(lengths, ty.i32, "lengths", rows, dev),
                                 _flat(path, ty.i32, "path", rows * max_tree, dev),
                                 _flat(count, ty.i32, "count", rows, dev), rows, max_tree,
-                                _flat(lengths_out, ty.i32, "lengths_out", rows, dev), _on(stream, k_cache))
+                                _flat(lengths_out, ty.i32, "lengths_out", rows, dev), handle)
     _check(rc, "w4a16_kv_compact")
     return lengths_out
 
@@ -858,12 +886,13 @@ def kv_fork(k_cache, v_cache, page_table, lengths, refs, src, dst, ok=None, stre
     i32 = ty.i32
     cache, shape = _kv_cache(k_cache, v_cache, None, None, False, dev)
     table, table_rows, width = _table(page_table, dev)
+    handle = _on(stream, page_table)
     if ok is None:
-        ok = _empty(1, i32, page_table, stream)
+        ok = _int_out((1,), i32, page_table, dev, stream, handle.value)
     n = src.numel()
     rc = lib().w4a16_kv_fork(cache, table, width, table_rows, _flat(lengths, i32, "lengths", table_rows, dev),
                              _flat(refs, i32, "refs", shape[1], dev), _flat(src, i32, "src", n, dev),
-                             _flat(dst, i32, "dst", n, dev), n, _flat(ok, i32, "ok", 1, dev), _on(stream, page_table))
+                             _flat(dst, i32, "dst", n, dev), n, _flat(ok, i32, "ok", 1, dev), handle)
     _check(rc, "w4a16_kv_fork")
     return ok
 
@@ -875,12 +904,13 @@ def kv_reserve(page_table, refs, rows, want, page_rows, ok=None, stream=None):
     ty, dev = _types(), _place(page_table, "page_table")
     i32 = ty.i32
     table, table_rows, width = _table(page_table, dev)
+    handle = _on(stream, page_table)
     if ok is None:
-        ok = _empty(1, i32, page_table, stream)
+        ok = _int_out((1,), i32, page_table, dev, stream, handle.value)
     n, pages = rows.numel(), refs.numel()
     rc = lib().w4a16_kv_reserve(table, width, table_rows, _flat(refs, i32, "refs", pages, dev), pages, page_rows,
                                 _flat(rows, i32, "rows", n, dev), _flat(want, i32, "want", n, dev), n,
-                                _flat(ok, i32, "ok", 1, dev), _on(stream, page_table))
+                                _flat(ok, i32, "ok", 1, dev), handle)
     _check(rc, "w4a16_kv_reserve")
     return ok
 

@@ -294,3 +294,19 @@ def test_on_another_stream():
     p.host.reserve([2], [40])
     p.host.free([0])
     p.same()
+
+
+def test_outputs_are_new_each_time():
+    """Small outputs share allocations, never memory: each keeps its values while others are made, in and out of order."""
+    to = lambda *a: torch.tensor(a, device="cuda")  # noqa: E731
+    starts, draft = to(0, 3).int(), to(9, 1, 2)
+    kept = []
+    for i in range(100):
+        out = w4.tree_accept(to(1, 2, 100 + i), draft, None, starts, 3 + i % 2)
+        if i % 3:
+            kept.append((i, out))
+    assert ok() == 0
+    for i, (path, count, token) in kept:
+        assert path[0].tolist() == [0, 1, 2] + [-1] * (i % 2) and int(count) == 3 and int(token) == 100 + i
+    at = sorted((t.data_ptr(), t.nbytes) for _, out in kept for t in out)
+    assert all(a + n <= b for (a, n), (b, _) in zip(at, at[1:]))
