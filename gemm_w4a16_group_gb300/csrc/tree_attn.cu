@@ -106,12 +106,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// the two e4m3 codes in the low half of x as f16x2 (exact)
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t x) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x & 0xFFFFu), __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
-}
-
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t *>(&b);
@@ -407,7 +401,11 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
             uint32_t b[4];
             ldsm4(colb + swz<G::CW>(krow + n * 8, ch % (G::CW / 16)), b);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) mma16816<true>(s[n], a[u], e4m3x2_f16x2(b[u]), e4m3x2_f16x2(b[u] >> 16));
+            for (int u = 0; u < 4; ++u) {
+              uint32_t lo, hi;
+              e4m3x4_f16(b[u], lo, hi);
+              mma16816<true>(s[n], a[u], lo, hi);
+            }
           }
         }
       } else {
@@ -498,9 +496,11 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
             ldsm4t(vbase + (ch / (G::CW / 16)) * G::SUB + swz<G::CW>(vrow + n * 8, ch % (G::CW / 16)), b);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              const uint32_t x0 = __byte_perm(b[2 * u], 0, 0x3120), x1 = __byte_perm(b[2 * u + 1], 0, 0x3120);
-              mma16816<true>(o[cc * 4 + 2 * u], a, e4m3x2_f16x2(x0), e4m3x2_f16x2(x1));
-              mma16816<true>(o[cc * 4 + 2 * u + 1], a, e4m3x2_f16x2(x0 >> 16), e4m3x2_f16x2(x1 >> 16));
+              uint32_t even[2], odd[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) e4m3x4_f16(__byte_perm(b[2 * u + k], 0, 0x3120), even[k], odd[k]);
+              mma16816<true>(o[cc * 4 + 2 * u], a, even[0], even[1]);
+              mma16816<true>(o[cc * 4 + 2 * u + 1], a, odd[0], odd[1]);
             }
           }
         } else {
@@ -794,7 +794,7 @@ cudaError_t launch_rows(const AttnCall &c, AttnParams &p) {
   }
   CUtensorMap tk, tv;
   const int br = std::min(c.cache.page_rows, G::KT);
-  if (!encode_cache(&tk, c.cache.k, c.cache, br, G::CW) || !encode_cache(&tv, c.cache.v, c.cache, br, G::CW))
+  if (!encode_cache(&tk, c.cache.k, c.cache, br, G::CW, true) || !encode_cache(&tv, c.cache.v, c.cache, br, G::CW, true))
     return cudaErrorInvalidValue;
   const int grid = std::min(G::CTAS * c.sm_count, kMaxCtas);
   cudaError_t e = launch_dependent(kern, grid, kThreads, G::SMEM, c.stream, tk, tv, p);
@@ -802,18 +802,18 @@ cudaError_t launch_rows(const AttnCall &c, AttnParams &p) {
   return p.whole ? cudaSuccess : launch_join<DIM, G::ROWS>(c, p, grid);
 }
 
-template <int DIM>
+template <int DIM, bool E4M3>
 cudaError_t launch_tc(const AttnCall &c, AttnParams &p) {
   cudaError_t e = launch_tree_tc(c, p);
   if (e != cudaSuccess) return e;
-  return p.whole ? cudaSuccess : launch_join<DIM, tc_attn_rows(DIM)>(c, p, std::min(c.sm_count, kTcMaxCtas));
+  return p.whole ? cudaSuccess : launch_join<DIM, tc_attn_rows(DIM, E4M3)>(c, p, std::min(c.sm_count, kTcMaxCtas));
 }
-bool uses_tc(int rows, bool e4m3) { return !e4m3 && rows > 16; }
+bool uses_tc(int rows) { return rows > 16; }
 
 template <int DIM, bool E4M3>
 cudaError_t launch_dim(const AttnCall &c, AttnParams &p) {
   const int rows = c.max_tree * p.group;
-  if (!E4M3 && uses_tc(rows, E4M3)) return launch_tc<DIM>(c, p);
+  if (uses_tc(rows)) return launch_tc<DIM, E4M3>(c, p);
   if (rows <= 16) return launch_rows<DIM, E4M3, 1>(c, p);
   if (rows <= 32) return launch_rows<DIM, E4M3, 2>(c, p);
   return launch_rows<DIM, E4M3, 4>(c, p);
@@ -821,7 +821,7 @@ cudaError_t launch_dim(const AttnCall &c, AttnParams &p) {
 
 }  // namespace
 
-bool encode_cache(CUtensorMap *m, const KvSide &s, const KvCache &c, int box_rows, int box_bytes) {
+bool encode_cache(CUtensorMap *m, const KvSide &s, const KvCache &c, int box_rows, int box_bytes, bool swizzled) {
   const int elt = c.e4m3 ? 1 : 2;
   // an axis of one entry is never stepped along; its stride only has to be one that a map may have
   auto step = [&](int n, long long stride) { return (uint64_t)(n > 1 ? stride : c.row_bytes()); };
@@ -829,13 +829,15 @@ bool encode_cache(CUtensorMap *m, const KvSide &s, const KvCache &c, int box_row
   const uint64_t strides[3] = {step(c.page_rows, s.row), step(c.kv_heads, s.head), step(c.pages, s.page)};
   const uint32_t box[4] = {(uint32_t)(box_bytes / elt), (uint32_t)box_rows, 1, 1};
   return encode_4d(m, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, s.base, dims, strides,
-                   box, box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+                   box, !swizzled          ? CU_TENSOR_MAP_SWIZZLE_NONE
+                         : box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                            : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 size_t tree_attn_workspace_bytes(int heads, int kv_heads, int dim, int max_tree) {
   const int rows = max_tree * (heads / kv_heads);
-  if (uses_tc(rows, false))  // (an 8-bit cache never needs more)
-    return kJoinBytes + align_up((size_t)kTcMaxCtas * 2 * tc_attn_rows(dim) * (dim + 2) * sizeof(float), 256);
+  if (uses_tc(rows))  // (an 8-bit cache never needs more)
+    return kJoinBytes + align_up((size_t)kTcMaxCtas * 2 * tc_attn_rows(dim, false) * (dim + 2) * sizeof(float), 256);
   return kJoinBytes + align_up((size_t)kMaxCtas * 2 * 16 * (dim + 2) * sizeof(float), 256);
 }
 

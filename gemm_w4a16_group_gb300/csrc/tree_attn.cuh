@@ -27,7 +27,7 @@ namespace w4a16 {
 constexpr int kMaxCtas = 320;    // CTAs of an attention launch: shares of the work list
 constexpr int kTcMaxCtas = 160;  // of the tcgen05 kernel
 // the tcgen05 kernel (tree_attn_tc.cu): query rows of an item, keys of a tile
-constexpr int tc_attn_rows(int dim) { return dim == 256 ? 128 : 256; }
+constexpr int tc_attn_rows(int dim, bool e4m3) { return dim == 256 || e4m3 ? 128 : 256; }
 constexpr int tc_attn_keys(int dim) { return dim == 256 ? 64 : 128; }
 // Tables of so few keys are worked on without splitting items, so nothing has
 // to be joined: no second launch (2.3 us of the host's time, 4 us on the
@@ -259,8 +259,8 @@ inline cudaError_t launch_dependent(void (*kern)(K...), unsigned grid, int threa
 }
 
 // Tensor map of one side of a cache layer: (element, row, head, page), boxes of
-// `box_rows` rows by `box_bytes` bytes, swizzled over the box's width
-bool encode_cache(CUtensorMap *m, const KvSide &s, const KvCache &c, int box_rows, int box_bytes);
+// `box_rows` rows by `box_bytes` bytes, swizzled over the box's width if asked
+bool encode_cache(CUtensorMap *m, const KvSide &s, const KvCache &c, int box_rows, int box_bytes, bool swizzled);
 
 // 4-D tiled TMA load
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int c0, int c1, int c2, int c3, uint32_t bar,
@@ -270,6 +270,16 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int 
       " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "l"(policy)
       : "memory");
+}
+
+// four e4m3 codes as two f16x2 (codes 0 and 1, codes 2 and 3), exactly
+__device__ __forceinline__ void e4m3x4_f16(uint32_t x, uint32_t &lo, uint32_t &hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {

@@ -31,6 +31,9 @@
 //
 // P is rounded to bf16 once (2^-9 of a weight on average against the output's
 // own 2^-9); sums use the unrounded weights.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
 #include <algorithm>
 
 #include "tree_attn.cuh"
@@ -38,17 +41,18 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kTcThreads = 384;
-constexpr int kWarpCopy = 0, kWarpMma = 1, kWarpSoftmax = 4;
+constexpr int kWarpCopy = 0, kWarpMma = 1, kWarpSoftmax = 4, kWarpConvert = 12;
 // What beginning and ending an item costs (Q, filling and draining the pipeline, the output), in tiles of 128 query
 // rows: with 4 rather than none, 16 ragged trees of up to 64 nodes 87 -> 71 us; with 6, 68 us, but 12 rows of up to 8
 // nodes 28.5 -> 29.7 us and one 16-node tree 22.6 -> 24.0 us.
 constexpr int kTcLead = 4;
 constexpr int kRows = 128;  // query rows of an MMA
 constexpr int kInfo = 16;  // tiles whose key-group words are kept
+constexpr int kOdd = 8;    // items whose words of odd values are kept: more than tiles converted ahead
 
-template <int DIM>
+template <int DIM, bool E4M3>
 struct TcGeo {
+  static constexpr int THREADS = E4M3 ? 512 : 384;
   static constexpr int STREAMS = DIM == 256 ? 1 : 2;  // softmax groups
   static constexpr int KT = tc_attn_keys(DIM);        // keys of a tile
   static constexpr int CH = DIM / 64;                 // 128-byte columns of a row
@@ -56,20 +60,26 @@ struct TcGeo {
   static constexpr int SLOT = CH * SUB;
   static constexpr int QSUB = kRows * 128;
   static constexpr int Q_TILE = CH * QSUB;
-  static constexpr int ROWS = tc_attn_rows(DIM);
+  static constexpr int ROWS = tc_attn_rows(DIM, E4M3);
   static constexpr int Q_BYTES = ROWS / kRows * Q_TILE;
   using Tiles = Tiling<ROWS, KT, kRows, kTcLead>;
-  static constexpr int SLOTS = DIM == 64 ? 12 : 5;
+  static constexpr int SLOTS = E4M3 ? (DIM == 64 ? 8 : 4) : DIM == 64 ? 12 : 5;
+  // what is copied: boxes of BW bytes by up to KT rows, BCH of them side by side. 8-bit tiles go to slots of their own
+  static constexpr int ELT = E4M3 ? 1 : 2;
+  static constexpr int BW = DIM * ELT < 128 ? DIM * ELT : 128, BCH = DIM * ELT / BW, BSUB = KT * BW;
+  static constexpr int RAW_SLOT = KT * DIM;
+  static constexpr int RAW = E4M3 ? (DIM == 64 ? 8 : DIM == 128 ? 4 : 2) : 0;
   static constexpr int SBUFS = 2;                     // S buffers: one per stream, or two of the one
   // TMEM columns: S (P over its first half), then O
   static constexpr int COL_O = SBUFS * KT;
   static constexpr int OFF_SLOT = Q_BYTES;
-  static constexpr int OFF_ML = OFF_SLOT + SLOTS * SLOT;
-  static constexpr int OFF_BAR = OFF_ML + STREAMS * kRows * 8;
-  static constexpr int NBARS = 2 * SLOTS + 2 * SBUFS + 5;
+  static constexpr int OFF_RAW = OFF_SLOT + SLOTS * SLOT;
+  static constexpr int OFF_ML = OFF_RAW + RAW * RAW_SLOT;
+  static constexpr int OFF_BAR = OFF_ML + 2 * kRows * 8;
+  static constexpr int NBARS = 2 * SLOTS + 2 * SBUFS + 5 + 2 * RAW;
   static constexpr int OFF_INFO = OFF_BAR + NBARS * 8;
   static constexpr int OFF_MISC = OFF_INFO + kInfo * 4;  // TMEM address, abort flag, odd values
-  static constexpr int OFF_PLAN = OFF_MISC + 16;
+  static constexpr int OFF_PLAN = OFF_MISC + 8 + kOdd * 8;
   static constexpr int SMEM = OFF_PLAN + (int)sizeof(PlanShared);
   static_assert(COL_O + STREAMS * DIM <= 512, "TMEM budget");
   static_assert(SMEM <= 227 * 1024 && OFF_SLOT % 1024 == 0 && OFF_PLAN % 8 == 0, "shared memory budget");
@@ -85,6 +95,8 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t mn_block) 
 }
 // B is MN-major
 constexpr uint32_t kIdescBMn = 1u << 16;
+// A and B are f16 (type 0) and not bf16 (type 1)
+constexpr uint32_t kIdescF16 = ~((1u << 7) | (1u << 10));
 
 __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, float (&v)[32]) {
   uint32_t r[32];
@@ -125,6 +137,10 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&f)[32]) 
       : "memory");
 }
 
+__device__ __forceinline__ uint32_t pack2_f16(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t *>(&h);
+}
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t *>(&b);
@@ -135,6 +151,14 @@ __device__ __forceinline__ void softmax_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 
+// e4m3 codes of NaN, as a byte mask
+__device__ __forceinline__ uint32_t nan_codes(uint32_t x) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (((x >> (8 * i)) & 0x7Fu) == 0x7Fu) m |= 0xFFu << (8 * i);
+  return m;
+}
 __device__ __forceinline__ uint32_t not_finite_bf16(uint32_t x) {
   return ((x & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((x & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
 }
@@ -151,11 +175,11 @@ __device__ __forceinline__ uint32_t seen_bits(int c, int ctx, unsigned long long
   return v & ((g & 1 ? 0xFFFFu : 0u) | (g & 2 ? 0xFFFF0000u : 0u));
 }
 
-template <int DIM>
-__global__ void __launch_bounds__(kTcThreads, 1)
+template <int DIM, bool E4M3>
+__global__ void __launch_bounds__(TcGeo<DIM, E4M3>::THREADS, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ AttnParams p) {
-  using G = TcGeo<DIM>;
+  using G = TcGeo<DIM, E4M3>;
   constexpr int KT = G::KT, STREAMS = G::STREAMS;
   constexpr int SOFT = STREAMS * 128;  // softmax threads
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -178,12 +202,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t q_full = bars + 8 * (2 * G::SLOTS + 2 * G::SBUFS);  // Q written, TMEM of the last item read
   const uint32_t o_full = q_full + 8;                                // the item's MMAs are done
   const uint32_t o_done = o_full + 24;                               // one group: a tile's output is in the accumulator
+  auto raw_full = [&](uint32_t s) { return o_full + 32 + 8 * s; };   // 8 bits: copied
+  auto raw_empty = [&](uint32_t s) { return o_full + 32 + 8 * (G::RAW + s); };  // ... and converted
   auto turn_of = [&](uint32_t w) { return o_full + 8 + 8 * w; };     // an MMA thread's turn to issue
 
   if (tid == 0) {
     for (int i = 0; i < G::SLOTS; ++i) {
-      mbar_init(full(i), 1);
+      mbar_init(full(i), E4M3 ? 4 : 1);
       mbar_init(empty(i), STREAMS);
+    }
+    for (int i = 0; i < G::RAW; ++i) {
+      mbar_init(raw_full(i), 1);
+      mbar_init(raw_empty(i), 4);
     }
     for (int i = 0; i < G::SBUFS; ++i) {
       mbar_init(s_full(i), 1);
@@ -195,7 +225,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     mbar_init(turn_of(0), 1);
     mbar_init(turn_of(1), 1);
     *abort_flag = 0;
-    odd_values[0] = odd_values[1] = 0;
+    for (int i = 0; i < 2 * kOdd; ++i) odd_values[i] = 0;
     fence_mbar_init();
   }
   if (warp == kWarpMma) {
@@ -204,7 +234,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   grid_dependency_wait();
   grid_launch_dependents();
-  plan_share<typename G::Tiles, kTcThreads>(p, plan);
+  plan_share<typename G::Tiles, G::THREADS>(p, plan);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -212,16 +242,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   Cursor cur{plan.at, plan.end, plan.at < plan.end ? plan.unit : plan.end, plan.b, plan.head, plan.rt};
   Segment sg;
 
-  // A softmax thread holds a row's 128 scores. The block is launched with 384 x 168 registers; the first warpgroup
-  // (copies, MMAs) keeps 56 each, and the two softmax groups (at dim 256 one of them) get 224 each:
-  // 128 * 56 + 256 * 224 = 384 * 168.
+  // A softmax thread holds a row's 128 scores. The block is launched with 384 x 168 (8 bits: 512 x 128) registers; the
+  // first warpgroup (copies, MMAs) keeps 56 each, the converting one 72, and the softmax groups (at dim 256 one of them)
+  // get 224 (192) each: 128 * 56 + 256 * 224 = 384 * 168, and 128 * (56 + 72) + 256 * 192 = 512 * 128.
   if (warp < kWarpSoftmax) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == kWarpCopy) {
     // ------------------------------------------------------------ copies
     const int br = min(p.c.page_rows, KT), parts = KT / br;
     const int part = lane % parts, col = lane / parts;
-    const bool has_box = col < G::CH;
+    const bool has_box = col < G::BCH;
     if (lane == 0) {
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
@@ -240,15 +270,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         return kt < sg.kt1 && key < sg.i.keys ? ids[key >> p.c.page_shift] : -1;
       };
       auto copy = [&](const CUtensorMap *tm, int kt, int id, bool load, uint32_t loads) {
-        const uint32_t s = ring % G::SLOTS;
-        ok = ok && mbar_wait(empty(s), ((ring / G::SLOTS) & 1) ^ 1, abort_flag);
+        constexpr int N = E4M3 ? G::RAW : G::SLOTS;
+        const uint32_t s = ring % N, bar = E4M3 ? raw_full(s) : full(s);
+        ok = ok && mbar_wait(E4M3 ? raw_empty(s) : empty(s), ((ring / N) & 1) ^ 1, abort_flag);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) return;
-        if (lane == 0) mbar_arrive_expect_tx(full(s), __popc(loads) * br * 128);
+        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(loads) * br * G::BW);
         __syncwarp();
         if (load)
-          tma_load_4d(sbase + G::OFF_SLOT + s * G::SLOT + col * G::SUB + part * br * 128, tm, col * 64,
-                      (kt * KT + part * br) & (p.c.page_rows - 1), sg.head, id, full(s), policy);
+          tma_load_4d(sbase + (E4M3 ? G::OFF_RAW + s * G::RAW_SLOT : G::OFF_SLOT + s * G::SLOT) + col * G::BSUB + part * br * G::BW,
+                      tm, col * (G::BW / G::ELT), (kt * KT + part * br) & (p.c.page_rows - 1), sg.head, id, bar, policy);
         __syncwarp();
         ++ring;
       };
@@ -273,16 +304,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       *abort_flag = 1;
       atomicOr(p.err, kErrTimeout);
       // every copy issued lands before the CTA can exit
-      for (uint32_t i = 0; i < (uint32_t)G::SLOTS && i < ring; ++i) {
+      constexpr uint32_t N = E4M3 ? G::RAW : G::SLOTS;
+      for (uint32_t i = 0; i < N && i < ring; ++i) {
         const uint32_t u = ring - 1 - i;
-        mbar_wait_drain(full(u % G::SLOTS), (u / G::SLOTS) & 1);
+        mbar_wait_drain(E4M3 ? raw_full(u % N) : full(u % N), (u / N) & 1);
       }
     }
   } else if (warp < kWarpMma + STREAMS) {
     // ------------------------------------------------------------ MMAs
     if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, KT);
-      constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, DIM) | kIdescBMn;
+      constexpr uint32_t types = E4M3 ? kIdescF16 : ~0u;
+      constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, KT) & types;
+      constexpr uint32_t idesc_o = (idesc_bf16_f32(kRows, DIM) & types) | kIdescBMn;
       const int mine = warp - kWarpMma;  // the softmax group served
       uint32_t ring = 0, item = 0, turn = 0;
       // Turns: a visit's two products are issued in one go. Left to themselves the two threads' MMAs mix, both groups
@@ -386,7 +419,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   }
   } else if (warp < kWarpSoftmax + 4 * STREAMS) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    if constexpr (E4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     // ------------------------------------------------------------ softmax
     const int stream = (warp - kWarpSoftmax) >> 2, quarter = warp & 3;
     const int lane_row = quarter * 32 + lane;  // query row of the MMA: TMEM lane
@@ -403,6 +437,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int row = lane_row + (wide ? stream * kRows : 0);  // this thread's query row of the item
       // ---- Q: K-major, 128-byte swizzle; rows past the item's are zero
       long long *q_row = reinterpret_cast<long long *>(smem + G::OFF_ML);  // between two items' use of it
+      float *q_scale = reinterpret_cast<float *>(q_row + kRows);  // 8 bits (items of 128 rows)
       const int q_rows = wide ? 2 * kRows : kRows;
       for (int r = st; r < q_rows; r += SOFT) {
         const int rr = sg.rt * G::ROWS + r;
@@ -423,14 +458,35 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int u = 0; u < QB; ++u) {
           const int e = st + (i0 + u) * SOFT, r = e / (DIM / 8), c = e % (DIM / 8);
+          if constexpr (E4M3) {
+            // f16, times the power of two that takes the row's largest element to 2^14 (a row's pieces are in
+            // neighbouring lanes); a row that is not finite stays as it is
+            uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w}, high = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) high = max(high, max((w[k] >> 7) & 0xFFu, (w[k] >> 23) & 0xFFu));
+#pragma unroll
+            for (int d = 1; d < DIM / 8; d <<= 1) high = max(high, __shfl_xor_sync(0xFFFFFFFFu, high, d));
+            const int power = high == 0xFFu ? 0 : min(141 - (int)high, 120);
+            const float f = __uint_as_float((uint32_t)(127 + power) << 23);
+            if (c == 0) q_scale[r] = f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = pack2_f16(bf16lo_to_f32(w[k]) * f, bf16hi_to_f32(w[k]) * f);
+            x[u] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
           sts128(sbase + (r / kRows) * G::Q_TILE + (c >> 3) * G::QSUB + (r % kRows) * 128 + (((c & 7) ^ (r & 7)) << 4), x[u]);
         }
       }
       fence_proxy_async_smem();
       tc_fence_before();
-      if (st < 2) odd_values[st] = 0;
+      if (st < 2) odd_values[2 * ((item - 1) % kOdd) + st] = 0;  // the last item's
       softmax_sync<SOFT>();
       if (lane == 0) mbar_arrive(q_full);
+      uint32_t *odd_of = odd_values + 2 * (item % kOdd);
+      float factor = p.scale_log2, v_scale = 1.f;
+      if constexpr (E4M3) {
+        factor *= p.c.k.scale[sg.head] / q_scale[lane_row];
+        v_scale = p.c.v.scale[sg.head];
+      }
       const int rr = sg.rt * G::ROWS + row, tok = rr / p.group;
       unsigned long long word = 0;
       if (row < rows) {
@@ -452,7 +508,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t groups = info[tile % kInfo];
         const int key0 = (sg.kt0 + i) * KT;
         const bool masked = key0 + KT > sg.i.len || groups != (1u << (KT / 16)) - 1;
-        if (masked) {
+        if (!E4M3 && masked) {  // (8 bits: where they are converted)
           // Values that must not meet a weight of 0: zeroed before the MMA reads them. All threads of this group.
           const uint32_t v = v_slot % G::SLOTS;
           if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(full(v), (v_slot / G::SLOTS) & 1, abort_flag));
@@ -470,7 +526,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               if (!(b0 | b1 | b2 | b3)) continue;
               x = make_uint4(x.x & ~b0, x.y & ~b1, x.z & ~b2, x.w & ~b3);
               const int nw = key - sg.i.len;
-              atomicOr(&odd_values[nw >> 5], 1u << (nw & 31));
+              atomicOr(&odd_of[nw >> 5], 1u << (nw & 31));
             }
             sts128(a, x);
           }
@@ -498,8 +554,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
               for (int k = 0; k < 4; ++k) t4[k] = fmaxf(fmaxf(t4[k], x[c][e + k]), x[c][e + 4 + k]);
           const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-          const float mn = fmaxf(m, top * p.scale_log2);
-          // rescale when the maximum has grown by more than 2^8 (or was -inf)
+          const float mn = fmaxf(m, __fmul_rn(top, factor));
+          // rescale when the maximum has grown by more than 2^8 (or was -inf); f16 weights end at 2^16
           const bool grow = mn > m + 8.f;
           const bool first = i < (wide ? 1 : STREAMS);  // this group's first tile: no output yet
           if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -524,17 +580,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           // ---- weights, over the first half of S's columns
           const float base = m == -INFINITY ? 0.f : m;
-          const f32x2 scale2 = f32_pair(p.scale_log2, p.scale_log2), base2 = f32_pair(-base, -base);
+          const f32x2 scale2 = f32_pair(factor, factor), base2 = f32_pair(-base, -base);
           f32x2 sum[2] = {f32_pair(0.f, 0.f), f32_pair(0.f, 0.f)};
 #pragma unroll
           for (int c = 0; c < KT / 32; ++c) {
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float2 y = f32_halves(fma2(f32_pair(x[c][e], x[c][e + 1]), scale2, base2));
+              // (8 bits: in two roundings, as the maximum was formed, so that its own weight is 1; a weight and the sums
+              // then agree where one key has it all, although f16 rounds the weights alone. The products are single ones:
+              // the compiler makes an fma of a packed product and sum.)
+              const float2 y = f32_halves(E4M3 ? add2(f32_pair(__fmul_rn(x[c][e], factor), __fmul_rn(x[c][e + 1], factor)), base2)
+                                               : fma2(f32_pair(x[c][e], x[c][e + 1]), scale2, base2));
               const float a = exp2_approx(y.x), d = exp2_approx(y.y);
               sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], f32_pair(a, d));
-              w[e >> 1] = pack2(a, d);
+              w[e >> 1] = E4M3 ? pack2_f16(a, d) : pack2(a, d);
             }
             tmem_st16(s_col + 16 * c, w);
           }
@@ -548,8 +608,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       ring += 2 * n;
       // ---- the item's output
-      ml[stream * kRows + lane_row] = make_float2(m, l);
+      // (all MMAs are done, so all threads have begun their tiles and none still needs what lay here)
       if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(o_full, item & 1, abort_flag));
+      ml[stream * kRows + lane_row] = make_float2(m, l);
       ++item;
       softmax_sync<SOFT>();
       tc_fence_after();
@@ -562,13 +623,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const float f0 = exp2_approx(a.x - base), f1 = exp2_approx(c2.x - base);
         const float L = a.y * f0 + c2.y * f1;
         const bool whole = sg.whole(), mine = row < rows;
-        const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+        const float inv = L > 0.f || L != L ? v_scale / L : 0.f;
         const float g0 = whole ? f0 * inv : f0, g1 = whole ? f1 * inv : f1;
         // slot 0: the item began before this share; slot 1: it goes on after it
         const Partial<DIM, G::ROWS> part(p.partials, blockIdx.x, sg.kt0 > 0 ? 0 : 1);
         if (st == 0 && sg.kt0 > 0 && sg.kt1 == sg.ktiles) leave_record<typename G::Tiles>(p, sg, plan.share);
         uint16_t *out = p.out + ((long long)(sg.i.start + tok) * p.heads + sg.head * p.group + rr % p.group) * DIM;
-        const uint32_t odd[2] = {odd_values[0], odd_values[1]};
+        const uint32_t odd[2] = {odd_of[0], odd_of[1]};
         const uint32_t oc = lanes + G::COL_O;
         const int cols = wide ? DIM : DIM / STREAMS, col0 = wide ? 0 : stream * cols;  // columns of this group
 #pragma unroll 1
@@ -590,13 +651,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               if (!(odd[j >> 5] >> (j & 31) & 1) || !(word >> j & 1)) continue;
               const long long pos = (long long)sg.i.len + j;
               const int id = p.r.table[(long long)sg.b * p.r.max_pages + (pos >> p.c.page_shift)];
-              const uint16_t *v = reinterpret_cast<const uint16_t *>(p.c.v.base + (long long)id * p.c.v.page +
-                                                                     (long long)sg.head * p.c.v.head +
-                                                                     (pos & (p.c.page_rows - 1)) * p.c.v.row);
+              const uint8_t *v = p.c.v.base + (long long)id * p.c.v.page + (long long)sg.head * p.c.v.head +
+                                 (pos & (p.c.page_rows - 1)) * p.c.v.row + (long long)c * G::ELT;
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
-                const float f = __uint_as_float((uint32_t)v[c + e] << 16);
-                if (!(fabsf(f) < INFINITY)) x[e] += f;
+                if (E4M3) {
+                  if ((v[e] & 0x7Fu) == 0x7Fu) x[e] = NAN;
+                } else {
+                  const float f = __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(v)[e] << 16);
+                  if (!(fabsf(f) < INFINITY)) x[e] += f;
+                }
               }
             }
           }
@@ -620,6 +684,81 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       *abort_flag = 1;
       if (lane == 0) atomicOr(p.err, kErrTimeout);
     }
+  } else if constexpr (E4M3) {
+    if (warp >= kWarpConvert) {
+      // ---------------------------------------------------------- codes to f16
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+      const int ct = tid - kWarpConvert * 32;
+      uint32_t ring = 0, tile = 0, item = 0;
+      bool ok = true;
+      while (ok && next_segment<typename G::Tiles>(p, cur, sg)) {
+        for (int kt = sg.kt0; ok && kt < sg.kt1; ++kt, ++tile) {
+#pragma unroll 1
+          for (int side = 0; side < 2; ++side, ++ring) {
+            const uint32_t rs = ring % G::RAW, s = ring % G::SLOTS;
+            ok = ok && mbar_wait(raw_full(rs), (ring / G::RAW) & 1, abort_flag) &&
+                 mbar_wait(empty(s), ((ring / G::SLOTS) & 1) ^ 1, abort_flag);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            const uint32_t groups = info[tile % kInfo];
+            const int key0 = kt * KT;
+            const bool clean = side == 0 || (key0 + KT <= sg.i.len && groups == (1u << (KT / 16)) - 1);
+            // A thread takes 16-code pieces: of key j = ct / 4 + 32 (u / SUBS), the (ct % 4)-th of 64-element column
+            // u % SUBS, so that all its addresses are constants apart.
+            constexpr int SUBS = G::CH, N = KT / 32 * SUBS;
+            const int j0 = ct >> 2, c4 = ct & 3;
+            const uint32_t from = sbase + G::OFF_RAW + rs * G::RAW_SLOT + j0 * G::BW + c4 * 16;
+            const uint32_t to = sbase + G::OFF_SLOT + s * G::SLOT + j0 * 128;
+            const uint32_t lo16 = ((2 * c4) ^ (j0 & 7)) << 4, hi16 = ((2 * c4 + 1) ^ (j0 & 7)) << 4;
+            uint4 x[N];
+#pragma unroll
+            for (int u = 0; u < N; ++u) {
+              const int sub = u % SUBS;
+              x[u] = lds128(from + (u / SUBS) * 32 * G::BW + sub * 64 / G::BW * G::BSUB + sub * 64 % G::BW);
+            }
+            if (!clean) {
+              // values that must not meet a weight of 0
+#pragma unroll
+              for (int u = 0; u < N; ++u) {
+                const int j = j0 + 32 * (u / SUBS), key = key0 + j;
+                const bool there = key < sg.i.keys && (groups >> (j >> 4) & 1);
+                if (there && key < sg.i.len) continue;
+                const uint4 m = there ? make_uint4(nan_codes(x[u].x), nan_codes(x[u].y), nan_codes(x[u].z), nan_codes(x[u].w))
+                                      : make_uint4(~0u, ~0u, ~0u, ~0u);
+                if (there && (m.x | m.y | m.z | m.w)) {
+                  const int nw = key - sg.i.len;
+                  atomicOr(&odd_values[2 * (item % kOdd) + (nw >> 5)], 1u << (nw & 31));
+                }
+                x[u] = make_uint4(x[u].x & ~m.x, x[u].y & ~m.y, x[u].z & ~m.z, x[u].w & ~m.w);
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < N; ++u) {
+              // 16 codes are 32 bytes of a 128-byte row
+              uint4 y[2];
+              e4m3x4_f16(x[u].x, y[0].x, y[0].y);
+              e4m3x4_f16(x[u].y, y[0].z, y[0].w);
+              e4m3x4_f16(x[u].z, y[1].x, y[1].y);
+              e4m3x4_f16(x[u].w, y[1].z, y[1].w);
+              const uint32_t row = to + (u % SUBS) * G::SUB + (u / SUBS) * 32 * 128;
+              sts128(row + lo16, y[0]);
+              sts128(row + hi16, y[1]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(full(s));
+              mbar_arrive(raw_empty(rs));
+            }
+          }
+        }
+        ++item;
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        if (lane == 0) atomicOr(p.err, kErrTimeout);
+      }
+    }
   }
 
   tc_fence_before();
@@ -630,10 +769,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-template <int DIM>
+template <int DIM, bool E4M3>
 cudaError_t launch_tc_dim(const AttnCall &c, const AttnParams &p) {
-  using G = TcGeo<DIM>;
-  auto kern = tree_tc_kernel<DIM>;
+  using G = TcGeo<DIM, E4M3>;
+  auto kern = tree_tc_kernel<DIM, E4M3>;
   static PerDevice configured;
   if (!configured.v[c.device].load(std::memory_order_relaxed)) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
@@ -642,19 +781,24 @@ cudaError_t launch_tc_dim(const AttnCall &c, const AttnParams &p) {
   }
   CUtensorMap tk, tv;
   const int br = std::min(c.cache.page_rows, G::KT);
-  if (!encode_cache(&tk, c.cache.k, c.cache, br, 128) || !encode_cache(&tv, c.cache.v, c.cache, br, 128))
+  if (!encode_cache(&tk, c.cache.k, c.cache, br, G::BW, !E4M3) || !encode_cache(&tv, c.cache.v, c.cache, br, G::BW, !E4M3))
     return cudaErrorInvalidValue;
-  return launch_dependent(kern, std::min(c.sm_count, kTcMaxCtas), kTcThreads, G::SMEM, c.stream, tk, tv, p);
+  return launch_dependent(kern, std::min(c.sm_count, kTcMaxCtas), G::THREADS, G::SMEM, c.stream, tk, tv, p);
+}
+
+template <bool E4M3>
+cudaError_t launch_tc_type(const AttnCall &c, const AttnParams &p) {
+  switch (c.cache.dim) {
+    case 64: return launch_tc_dim<64, E4M3>(c, p);
+    case 128: return launch_tc_dim<128, E4M3>(c, p);
+    default: return launch_tc_dim<256, E4M3>(c, p);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_tree_tc(const AttnCall &c, const AttnParams &p) {
-  switch (c.cache.dim) {
-    case 64: return launch_tc_dim<64>(c, p);
-    case 128: return launch_tc_dim<128>(c, p);
-    default: return launch_tc_dim<256>(c, p);
-  }
+  return c.cache.e4m3 ? launch_tc_type<true>(c, p) : launch_tc_type<false>(c, p);
 }
 
 }  // namespace w4a16
