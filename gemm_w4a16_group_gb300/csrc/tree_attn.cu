@@ -6,18 +6,20 @@
 // mask word, the row's new tokens). One pass over the keys with a running
 // maximum m and sum; the sums are rescaled when m grows.
 //
-// This file: the kernel on mma.sync (m16n8k16), for up to 64 query rows per
-// kv head at a time, and the kernel that joins partial results. A decode step
-// has G to 16 * G query rows against the whole cache, so it is bound by HBM:
-// every key and value is read once per tile of 16, 32 or 64 rows.
+// This file: the kernel on mma.sync (m16n8k16) for up to 16 query rows per kv
+// head (one token of any model, a few tokens of small head groups), and the
+// kernel that joins partial results; tree_attn_tc.cu has more rows. 16 rows
+// against the whole cache are bound by HBM: every key and value is read once.
+// Measured against the copy peak of 6.78 TB/s: bf16 6.34 TB/s at 64 rows of
+// 4,096 keys (dim 64, 128 and 256 alike), e4m3 5.5 TB/s (the conversions take
+// half of the integer pipe).
 //
-//  * 4 computing warps and a copying warp. A stage is 64 keys: the copying
-//    warp's lanes each fetch one box (up to 64 rows of a page by 128 bytes) of
-//    keys or values by TMA, swizzled as ldmatrix wants it.
-//  * RW warps side by side take 16 query rows each; the 4 / RW warps of one
-//    such group take every (4 / RW)-th run of 64 / (4 / RW) keys of a stage,
-//    and meet at the end of an item. With one row tile no key is multiplied
-//    twice, and with four every warp sees all keys.
+//  * 4 computing warps and a copying warp. A stage is 64 or 128 keys: the
+//    copying warp's lanes each fetch one box (up to a page's rows by 128 bytes)
+//    of keys or values by TMA, swizzled as ldmatrix wants it.
+//  * Each computing warp takes its quarter of a stage's keys with all 16 rows,
+//    with a maximum, sums and outputs of its own; they meet at the end of an
+//    item, through shared memory.
 //  * bf16 caches: products of bf16 are exact in float32; the weights e^(s - m)
 //    go into the second product as two bf16 parts (hi + lo, 16 bits of
 //    mantissa), which the tensor cores have time for.
@@ -40,17 +42,19 @@
 namespace w4a16 {
 namespace {
 
-// What beginning and ending an item costs, in key tiles: with 2 rather than none, 48
-// ragged rows of an e4m3 cache 153 -> 146 us; with 3, 143 us, but one short row 13.8 -> 15.1 us.
-constexpr int kRowsLead = 2;
+// What beginning and ending an item costs, in key tiles: with 4 rather than 2, 48 ragged rows of an e4m3 cache 116.8 ->
+// 112.3 us, 64 even rows of a bf16 cache 174 -> 171 us.
+constexpr int kRowsLead = 4;
 constexpr int kComputeWarps = 4;
 constexpr int kThreads = (kComputeWarps + 1) * 32;
 
-template <int DIM, bool E4M3, int RWT>
+template <int DIM, bool E4M3>
 struct RowsGeo {
-  static constexpr int RW = RWT, KW = kComputeWarps / RWT;
-  static constexpr int ROWS = 16 * RW;
-  static constexpr int KT = RW <= 2 && (DIM * (E4M3 ? 1 : 2) <= 128 || (DIM == 256 && E4M3)) ? 128 : 64;  // keys of a stage
+  static constexpr int KW = kComputeWarps;     // warps that share a stage's keys
+  static constexpr int ROWS = 16;
+  // keys of a stage: 128 where three such stages fit (e4m3, 48 ragged rows of up to 16,384 keys: 117 us, with 64 keys
+  // 138 us)
+  static constexpr int KT = DIM * (E4M3 ? 1 : 2) <= 128 || (DIM == 256 && E4M3) ? 128 : 64;
   using Tiles = Tiling<ROWS, KT, ROWS, kRowsLead>;
   static constexpr int KPW = KT / KW;         // keys of a warp per stage
   static constexpr int ELT = E4M3 ? 1 : 2;
@@ -66,10 +70,10 @@ struct RowsGeo {
   static constexpr int NT = KPW / 8;           // 8-key tiles of a warp
   static constexpr int OT = DIM / 8;           // 8-wide output tiles
   static constexpr int Q_BYTES = ROWS * DIM * 2;
-  static constexpr int RED_BYTES = KW > 1 ? RW * 16 * DIM * 4 / (RW > 1 ? 2 : 1) : 0;
+  static constexpr int RED_BYTES = ROWS * DIM * 4;
   static constexpr int OFF_Q = STAGES * STAGE;  // q fragments; then the sums that warps exchange
   static constexpr int OFF_ML = OFF_Q + (Q_BYTES > RED_BYTES ? Q_BYTES : RED_BYTES);
-  static constexpr int OFF_QS = OFF_ML + (KW > 1 ? KW * ROWS * 8 : 0);
+  static constexpr int OFF_QS = OFF_ML + KW * ROWS * 8;
   static constexpr int OFF_BAR = OFF_QS + (E4M3 ? ROWS * 4 : 0);
   static constexpr int OFF_INFO = OFF_BAR + 2 * STAGES * 8;
   static constexpr int OFF_MISC = OFF_INFO + STAGES * 4;
@@ -151,12 +155,12 @@ __device__ float value_at(const AttnParams &p, int b, int head, long long pos, i
   return __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(a)[d] << 16);
 }
 
-template <int DIM, bool E4M3, int RWT>
-__global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
+template <int DIM, bool E4M3>
+__global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3>::CTAS)
     rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                 const __grid_constant__ AttnParams p) {
-  using G = RowsGeo<DIM, E4M3, RWT>;
-  constexpr int RW = G::RW, KW = G::KW, NT = G::NT, OT = G::OT, KS = G::KS;
+  using G = RowsGeo<DIM, E4M3>;
+  constexpr int KW = G::KW, NT = G::NT, OT = G::OT, KS = G::KS;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -246,9 +250,9 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
   }
 
   // -------------------------------------------------------------- products
-  const int rw = warp % RW, kw = warp / RW;
+  const int kw = warp;
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t qaddr = sbase + G::OFF_Q + rw * (KS * 512) + lane * 16;
+  const uint32_t qaddr = sbase + G::OFF_Q + lane * 16;
   float *ml = reinterpret_cast<float *>(smem + G::OFF_ML);
   float *qscale = reinterpret_cast<float *>(smem + G::OFF_QS);
   uint32_t st = 0;
@@ -290,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
                                              (sg.head * p.group + rr % p.group) * p.q_head + 8 * c8);
       uint32_t w[4] = {x.x, x.y, x.z, x.w};
       const int step = c8 >> 1, half = c8 & 1, hi = (r >> 3) & 1;
-      const uint32_t base = sbase + G::OFF_Q + (r >> 4) * (KS * 512) + step * 512 + (r & 7) * 64;
+      const uint32_t base = sbase + G::OFF_Q + step * 512 + (r & 7) * 64;
       if (E4M3) {
         const float f = qscale[r];
         // a lane's four k of a step are d = 4t .. 4t + 3, as four codes of a key come
@@ -311,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
     float factor[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int r = rw * 16 + g + 8 * i;
+      const int r = g + 8 * i;
       const int tok = (sg.rt * G::ROWS + r) / p.group;
       word[i] = 0;
       if (r < rows) word[i] = p.mask ? (unsigned long long)p.mask[sg.i.start + tok] : (2ull << tok) - 1;
@@ -322,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
     if (E4M3) {
       const float ks = p.c.k.scale[sg.head];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) factor[i] = p.scale_log2 * ks / qscale[rw * 16 + g + 8 * i];
+      for (int i = 0; i < 2; ++i) factor[i] = p.scale_log2 * ks / qscale[g + 8 * i];
     }
     constexpr bool QREG = KS <= 8;
     uint32_t qf[QREG ? KS : 1][4];
@@ -349,8 +353,7 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
       const int key0 = kt * G::KT;
       const bool masked = key0 + G::KT > sg.i.len || groups != (1u << (G::KT / 16)) - 1;
       if (masked) {
-        // Values that must not meet a weight of 0, in the rows that this warp will read. Warps that share rows
-        // write the same to them, so no barrier is needed.
+        // values that must not meet a weight of 0, in the rows that this warp will read
         for (int i = lane; i < G::KPW * (G::ROWB / 16); i += 32) {
           const int j = kw * G::KPW + i / (G::ROWB / 16), c = i % (G::ROWB / 16);
           const int key = key0 + j;
@@ -536,11 +539,11 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
       if (E4M3) l[i] = lsum[2 * i];
     }
     constexpr int SLICE = OT / KW;  // output tiles that a warp ends up with
-    if constexpr (KW > 1) {
+    {
       if (t == 0) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float *x = ml + 2 * (kw * G::ROWS + rw * 16 + g + 8 * i);
+          float *x = ml + 2 * (kw * G::ROWS + g + 8 * i);
           x[0] = m[i];
           x[1] = l[i];
         }
@@ -549,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
       float f[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float *x = ml + 2 * (rw * 16 + g + 8 * i);
+        const float *x = ml + 2 * (g + 8 * i);
         float M = -INFINITY, L = 0.f;
 #pragma unroll
         for (int k = 0; k < KW; ++k) M = fmaxf(M, x[2 * k * G::ROWS]);
@@ -567,43 +570,37 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
         o[i][2] *= f[1];
         o[i][3] *= f[1];
       }
-      // round r: warp kw passes slice (kw + r) % KW on, and takes its own slice from warp (kw - r) % KW. The buffer
-      // holds one slice per warp (two halves of one, with two row tiles).
-      constexpr int PART = RW > 1 ? SLICE / 2 : SLICE;
+      // round r: warp kw passes slice (kw + r) % KW on, and takes its own slice from warp (kw - r) % KW
       float4 *buf = reinterpret_cast<float4 *>(smem + G::OFF_Q);
 #pragma unroll 1
       for (int r = 1; r < KW; ++r) {
+        const int to = (kw + r) % KW;
 #pragma unroll
-        for (int part = 0; part < SLICE / PART; ++part) {
-          const int to = (kw + r) % KW;
+        for (int sl = 0; sl < KW; ++sl)
+          if (sl == to) {
 #pragma unroll
-          for (int sl = 0; sl < KW; ++sl)
-            if (sl == to) {
-#pragma unroll
-              for (int i = 0; i < PART; ++i) {
-                const float(&x)[4] = o[sl * SLICE + part * PART + i];
-                buf[((rw * KW + to) * PART + i) * 32 + lane] = make_float4(x[0], x[1], x[2], x[3]);
-              }
+            for (int i = 0; i < SLICE; ++i) {
+              const float(&x)[4] = o[sl * SLICE + i];
+              buf[(to * SLICE + i) * 32 + lane] = make_float4(x[0], x[1], x[2], x[3]);
             }
-          compute_sync();
+          }
+        compute_sync();
 #pragma unroll
-          for (int sl = 0; sl < KW; ++sl)
-            if (sl == kw) {
+        for (int sl = 0; sl < KW; ++sl)
+          if (sl == kw) {
 #pragma unroll
-              for (int i = 0; i < PART; ++i) {
-                const float4 x = buf[((rw * KW + kw) * PART + i) * 32 + lane];
-                float(&y)[4] = o[sl * SLICE + part * PART + i];
-                y[0] += x.x;
-                y[1] += x.y;
-                y[2] += x.z;
-                y[3] += x.w;
-              }
+            for (int i = 0; i < SLICE; ++i) {
+              const float4 x = buf[(kw * SLICE + i) * 32 + lane];
+              float(&y)[4] = o[sl * SLICE + i];
+              y[0] += x.x;
+              y[1] += x.y;
+              y[2] += x.z;
+              y[3] += x.w;
             }
-          compute_sync();
-        }
+          }
+        compute_sync();
       }
     }
-    if (KW == 1) compute_sync();  // odd_values is complete
     const uint32_t odd[2] = {odd_values[0], odd_values[1]};
     const bool whole = sg.whole();
     // slot 0: the item began before this share; slot 1: it goes on after it
@@ -616,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3, RWT>::CTAS)
       if (sl != kw) continue;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int r = rw * 16 + g + 8 * i;
+        const int r = g + 8 * i;
         if (r >= rows) continue;
         const int rr = sg.rt * G::ROWS + r, tok = sg.i.start + rr / p.group, h = sg.head * p.group + rr % p.group;
         const float inv = l[i] > 0.f || l[i] != l[i] ? vs / l[i] : 0.f;
@@ -782,10 +779,10 @@ cudaError_t launch_join(const AttnCall &c, const AttnParams &p, int ctas) {
                : launch_dependent(join_kernel<DIM, ROWS, false>, grid, kJoinThreads, 0, c.stream, p, ctas);
 }
 
-template <int DIM, bool E4M3, int RW>
+template <int DIM, bool E4M3>
 cudaError_t launch_rows(const AttnCall &c, AttnParams &p) {
-  using G = RowsGeo<DIM, E4M3, RW>;
-  auto kern = rows_kernel<DIM, E4M3, RW>;
+  using G = RowsGeo<DIM, E4M3>;
+  auto kern = rows_kernel<DIM, E4M3>;
   static PerDevice configured;
   if (!configured.v[c.device].load(std::memory_order_relaxed)) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
@@ -808,15 +805,15 @@ cudaError_t launch_tc(const AttnCall &c, AttnParams &p) {
   if (e != cudaSuccess) return e;
   return p.whole ? cudaSuccess : launch_join<DIM, tc_attn_rows(DIM, E4M3)>(c, p, std::min(c.sm_count, kTcMaxCtas));
 }
+// The tcgen05 kernel from 17 query rows per kv head on: its MMAs take 128 rows
+// in the time of one. (When this file still had 32- and 64-row forms: 16
+// sequences of 32 rows 63 us here, 53 there; 64 rows 121 and 57; 8-bit caches
+// 77 and 63, 133 and 66.)
 bool uses_tc(int rows) { return rows > 16; }
 
 template <int DIM, bool E4M3>
 cudaError_t launch_dim(const AttnCall &c, AttnParams &p) {
-  const int rows = c.max_tree * p.group;
-  if (uses_tc(rows)) return launch_tc<DIM, E4M3>(c, p);
-  if (rows <= 16) return launch_rows<DIM, E4M3, 1>(c, p);
-  if (rows <= 32) return launch_rows<DIM, E4M3, 2>(c, p);
-  return launch_rows<DIM, E4M3, 4>(c, p);
+  return uses_tc(c.max_tree * p.group) ? launch_tc<DIM, E4M3>(c, p) : launch_rows<DIM, E4M3>(c, p);
 }
 
 }  // namespace
@@ -836,7 +833,7 @@ bool encode_cache(CUtensorMap *m, const KvSide &s, const KvCache &c, int box_row
 
 size_t tree_attn_workspace_bytes(int heads, int kv_heads, int dim, int max_tree) {
   const int rows = max_tree * (heads / kv_heads);
-  if (uses_tc(rows))  // (an 8-bit cache never needs more)
+  if (uses_tc(rows))  // (an 8-bit cache needs no more)
     return kJoinBytes + align_up((size_t)kTcMaxCtas * 2 * tc_attn_rows(dim, false) * (dim + 2) * sizeof(float), 256);
   return kJoinBytes + align_up((size_t)kMaxCtas * 2 * 16 * (dim + 2) * sizeof(float), 256);
 }
