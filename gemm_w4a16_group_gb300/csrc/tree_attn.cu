@@ -849,7 +849,7 @@ cudaError_t launch_tree_attention(const AttnCall &c) {
   p.heads = c.heads;
   p.group = c.heads / c.cache.kv_heads;
   p.max_tree = c.max_tree;
-  p.whole = (long long)c.rows.max_pages * c.cache.page_rows <= kWholeKeys;
+  p.whole = (long long)c.rows.max_pages * c.cache.page_rows <= (uses_tc(c.max_tree * p.group) ? kTcWholeKeys : kWholeKeys);
   p.scale_log2 = c.scale * kLog2e;
   p.out = c.out;
   p.joins = static_cast<int *>(c.workspace);
