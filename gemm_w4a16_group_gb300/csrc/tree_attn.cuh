@@ -4,10 +4,10 @@
 // Work list. Row b of the page table with T new tokens and L cached ones has
 // K = L + T keys; its T * G query rows of one kv head (G query heads each) are
 // packed token by token into tiles of ROWS rows, so its items are
-// (kv head, row tile), each of ceil(K / KT) key tiles. A key tile counts one
-// unit per UNIT query rows (the tcgen05 kernel works on 256 rows at a time, and
-// takes twice as long over more than 128), and an item counts LEAD units before
-// its first tile, for what beginning and ending an item costs. All items, in
+// (kv head, row tile), each of ceil(K / KT) key tiles. A key tile counts some
+// units by its query rows (the tcgen05 kernel works on up to 256, and takes half
+// as long again over more than 128 as over fewer), and an item counts LEAD key
+// tiles more, for what beginning and ending an item costs. All items, in
 // the order (b, head, row tile), form one list of units, and every CTA takes an
 // equal, contiguous share of it (to whole key tiles), whatever the lengths are:
 // long contexts are split over many CTAs, short ones share one. An item whose tiles
@@ -96,10 +96,17 @@ __device__ __forceinline__ RowInfo row_info(const AttnParams &p, int b, bool fla
   return i;
 }
 
-// Query rows of a tile, keys of a tile, query rows of a unit, units that an item costs by itself
-template <int ROWS_, int KT_, int UNIT_, int LEAD_>
+// Query rows of an item, keys of a tile, query rows of a narrow item, key tiles that an item costs by itself
+template <int ROWS_, int KT_, int NARROW_, int LEAD_>
 struct Tiling {
-  static constexpr int ROWS = ROWS_, KT = KT_, UNIT = UNIT_, LEAD = LEAD_;
+  static constexpr int ROWS = ROWS_, KT = KT_, NARROW = NARROW_, LEAD = LEAD_;
+  static constexpr int FULL_COST = ROWS > NARROW ? 3 : 1;  // units of a key tile of a full item
+  static __device__ __forceinline__ int cost(int rows) { return ROWS > NARROW ? (rows > NARROW ? 3 : 2) : 1; }
+  // key tiles in some of an item's units (fewer than 2^32: an item has under 2^31 keys)
+  static __device__ __forceinline__ int tiles(long long units, int cost) {
+    const uint32_t u = (uint32_t)units;
+    return (int)(ROWS > NARROW ? (cost == 3 ? u / 3u : u >> 1) : u);
+  }
 };
 
 template <int KT>
@@ -113,8 +120,9 @@ __device__ __forceinline__ int row_tiles(const RowInfo &i, int group) {
 template <class T>
 __device__ __forceinline__ long long units_of(const RowInfo &i, const AttnParams &p) {
   if (i.n == 0) return 0;
-  return p.c.kv_heads * ((long long)row_tiles<T::UNIT>(i, p.group) * key_tiles<T::KT>(i) +
-                         row_tiles<T::ROWS>(i, p.group) * T::LEAD);
+  const int rows = i.n * p.group, full = (rows - 1) / T::ROWS;  // (the last item is full or less)
+  return (long long)p.c.kv_heads * (key_tiles<T::KT>(i) + T::LEAD) *
+         (full * T::FULL_COST + T::cost(rows - full * T::ROWS));
 }
 
 // A CTA's place in the work list: units [at, end) are its share, `unit` is the
@@ -158,9 +166,9 @@ __device__ void plan_share(const AttnParams &p, PlanShared &s) {
     total += x;
   }
   const long long first = before + upto - mine;
-  // as many CTAs as get LEAD + 2 units each (a share then holds a whole key tile of any item), and no share larger
-  // than it has to be
-  const long long ctas = max(1ll, min((long long)gridDim.x, quotient(total, T::LEAD + 2)));
+  // as many CTAs as get LEAD + 2 key tiles each (a share then holds a whole one of any item), and no share larger than
+  // it has to be
+  const long long ctas = max(1ll, min((long long)gridDim.x, quotient(total, (T::LEAD + 2) * T::FULL_COST)));
   const long long share = max(1ll, quotient(total + ctas - 1, ctas));
   const long long at = min(share * blockIdx.x, total), end = min(at + share, total);
   if (tid == 0) {
@@ -176,7 +184,7 @@ __device__ void plan_share(const AttnParams &p, PlanShared &s) {
       const long long n = units_of<T>(i, p);
       if (at < f + n) {
         const long long per_head = quotient(n, p.c.kv_heads), o = at - f;
-        const long long per_tile = (long long)key_tiles<T::KT>(i) * (T::ROWS / T::UNIT) + T::LEAD;  // of a full row tile
+        const long long per_tile = (long long)(key_tiles<T::KT>(i) + T::LEAD) * T::FULL_COST;  // a full item
         s.b = b;
         s.head = (int)quotient(o, per_head);
         s.rt = (int)quotient(o - s.head * per_head, per_tile);
@@ -216,13 +224,12 @@ __device__ __forceinline__ bool next_segment(const AttnParams &p, Cursor &c, Seg
     s.rt = c.rt;
     s.rows = min(T::ROWS, s.i.n * p.group - c.rt * T::ROWS);
     s.ktiles = key_tiles<T::KT>(s.i);
-    static_assert(T::ROWS <= 2 * T::UNIT, "a key tile costs one unit or two");
-    const int cost = s.rows > T::UNIT ? 2 : 1;
+    const int cost = T::cost(s.rows);
     const bool mine = c.unit >= c.at;  // whole items: this share's (the list ends it at the first beyond)
-    const long long first = c.unit + T::LEAD, units = (long long)s.ktiles * cost;  // of the item's first tile
+    const long long first = c.unit + T::LEAD * cost, units = (long long)s.ktiles * cost;  // of the item's first tile
     // a key tile belongs to the share that holds its last unit
-    s.kt0 = c.at > first ? (int)(cost == 1 ? c.at - first : (c.at - first) >> 1) : 0;
-    s.kt1 = c.end - first >= units ? s.ktiles : c.end > first ? (int)(cost == 1 ? c.end - first : (c.end - first) >> 1) : 0;
+    s.kt0 = c.at > first ? T::tiles(c.at - first, cost) : 0;
+    s.kt1 = c.end - first >= units ? s.ktiles : c.end > first ? T::tiles(c.end - first, cost) : 0;
     if (p.whole) {
       s.kt0 = 0;
       s.kt1 = mine ? s.ktiles : 0;

@@ -1,14 +1,14 @@
-// Attention of drafted tokens over a paged bf16 cache on the fifth-generation
-// tensor cores (tcgen05), for rows of the page table with many query rows per
-// kv head (wide draft trees, large head groups).
+// Attention of drafted tokens over a paged cache on the fifth-generation tensor
+// cores (tcgen05), for rows of the page table with many query rows per kv head
+// (wide draft trees, large head groups).
 //
-// An item is up to 256 query rows (tokens times the heads of one kv head) of
-// one kv head. S = Q . K^T and O += P . V are M = 128 MMAs with their
-// accumulators in TMEM: a TMEM lane is one query row, so a softmax thread owns
-// a row and needs no exchange. With up to 128 query rows HBM bounds the kernel
-// (a 128-key tile at dim 128 is 64 KB, 2,800 clocks of an SM's share of HBM,
-// against 1,024 clocks of MMA); with up to 256 the cache is still read once,
-// and HBM, MMA time and softmax come near one another.
+// An item is up to 256 query rows (tokens times the heads of one kv head; 128 at
+// dim 256 and for 8-bit caches) of one kv head. S = Q . K^T and O += P . V are
+// M = 128 MMAs with their accumulators in TMEM: a TMEM lane is one query row, so
+// a softmax thread owns a row and needs no exchange. With up to 128 query rows
+// HBM bounds the kernel (a 128-key tile at dim 128 is 64 KB, 2,800 clocks of an
+// SM's share of HBM, against 1,024 clocks of MMA); with up to 256 the cache is
+// still read once, and HBM, MMA time and softmax come near one another.
 //
 //   warp 0        copies: K and V tiles by TMA through the page table, into one
 //                 ring of slots (K0, V0, K1, V1, ...)
@@ -17,20 +17,29 @@
 //                 allocation
 //   warps 4-7     softmax group 0
 //   warps 8-11    softmax group 1 (dim 64 and 128)
+//   warps 12-15   8-bit caches: copied tiles of codes to f16, into the ring
 //
 // The two softmax groups keep maxima, sums and output accumulators of their
 // own, so neither waits for the other. In an item of more than 128 rows ("wide")
 // each has 128 of the rows and all tiles; else all rows, and every other tile:
 // their outputs then meet at the item's end, where each group forms half of
-// the columns (both can read the lanes of both). P (bf16) replaces S in TMEM and is the second MMA's A operand there;
-// V, [key][dim] in shared memory, is its B operand as it lies (MN-major). At
-// dim 256 the output takes half of TMEM, so there is one group, with two S
-// buffers. An output accumulator is rescaled only when a row's maximum has
-// grown by more than 2^8: until then the weights are up to 2^8, and the sums
-// are float32.
+// the columns (both can read the lanes of both). P (bf16; f16 for 8-bit caches)
+// replaces S in TMEM and is the second MMA's A operand there; V, [key][dim] in
+// shared memory, is its B operand as it lies (MN-major). At dim 256 the output
+// takes half of TMEM, so there is one group, with two S buffers. An output
+// accumulator is rescaled only when a row's maximum has grown by more than 2^8:
+// until then the weights are up to 2^8, and the sums are float32.
 //
-// P is rounded to bf16 once (2^-9 of a weight on average against the output's
-// own 2^-9); sums use the unrounded weights.
+// P is rounded once (bf16: 2^-9 of a weight at most, against the output's own
+// 2^-9); sums use the unrounded weights.
+//
+// Measured, dim 128, bf16: 16 rows of 4,096 keys and 8 kv heads (268 MB) with 32,
+// 64 and 128 query rows per kv head 55, 58 and 63 us (4.9, 4.7, 4.4 TB/s); 4 rows
+// of 16,384 keys with 256 75 us, 920 TFLOP/s. A wide tile takes some 3,500 clocks:
+// a group's chain is 1,300 for its two products, 1,550 for its softmax and its
+// stores, and 600 of waiting for the other's turn and of handing over. (Handing P
+// over in two halves: 2 % slower. Fetching the next item's Q by a warp of its own
+// during the output of the one before: 1 to 3 % slower.)
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -42,9 +51,9 @@ namespace w4a16 {
 namespace {
 
 constexpr int kWarpCopy = 0, kWarpMma = 1, kWarpSoftmax = 4, kWarpConvert = 12;
-// What beginning and ending an item costs (Q, filling and draining the pipeline, the output), in tiles of 128 query
-// rows: with 4 rather than none, 16 ragged trees of up to 64 nodes 87 -> 71 us; with 6, 68 us, but 12 rows of up to 8
-// nodes 28.5 -> 29.7 us and one 16-node tree 22.6 -> 24.0 us.
+// What beginning and ending an item costs (Q, filling and draining the pipeline, the output), in key tiles. 16 ragged
+// trees of up to 64 nodes, 12 rows of up to 8 nodes, one 16-node tree: with 3 68.6, 28.9 and 25.2 us, with 4 65.4, 28.1
+// and 25.1, with 5 66.5, 28.9 and 26.3.
 constexpr int kTcLead = 4;
 constexpr int kRows = 128;  // query rows of an MMA
 constexpr int kInfo = 16;  // tiles whose key-group words are kept
@@ -246,178 +255,178 @@ __global__ void __launch_bounds__(TcGeo<DIM, E4M3>::THREADS, 1)
   // first warpgroup (copies, MMAs) keeps 56 each, the converting one 72, and the softmax groups (at dim 256 one of them)
   // get 224 (192) each: 128 * 56 + 256 * 224 = 384 * 168, and 128 * (56 + 72) + 256 * 192 = 512 * 128.
   if (warp < kWarpSoftmax) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-  if (warp == kWarpCopy) {
-    // ------------------------------------------------------------ copies
-    const int br = min(p.c.page_rows, KT), parts = KT / br;
-    const int part = lane % parts, col = lane / parts;
-    const bool has_box = col < G::BCH;
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
-    }
-    uint64_t pol;
-    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
-    uint64_t keep;  // several row tiles come back for the same keys
-    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
-    uint32_t ring = 0, tile = 0;
-    bool ok = true;
-    while (ok && next_segment<typename G::Tiles>(p, cur, sg)) {
-      const int32_t *ids = p.r.table + (long long)sg.b * p.r.max_pages;
-      const uint64_t policy = sg.i.n * p.group > G::ROWS ? keep : pol;
-      auto id_of = [&](int kt) {  // -1: past the keys
-        const long long key = (long long)kt * KT + part * br;
-        return kt < sg.kt1 && key < sg.i.keys ? ids[key >> p.c.page_shift] : -1;
-      };
-      auto copy = [&](const CUtensorMap *tm, int kt, int id, bool load, uint32_t loads) {
-        constexpr int N = E4M3 ? G::RAW : G::SLOTS;
-        const uint32_t s = ring % N, bar = E4M3 ? raw_full(s) : full(s);
-        ok = ok && mbar_wait(E4M3 ? raw_empty(s) : empty(s), ((ring / N) & 1) ^ 1, abort_flag);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) return;
-        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(loads) * br * G::BW);
-        __syncwarp();
-        if (load)
-          tma_load_4d(sbase + (E4M3 ? G::OFF_RAW + s * G::RAW_SLOT : G::OFF_SLOT + s * G::SLOT) + col * G::BSUB + part * br * G::BW,
-                      tm, col * (G::BW / G::ELT), (kt * KT + part * br) & (p.c.page_rows - 1), sg.head, id, bar, policy);
-        __syncwarp();
-        ++ring;
-      };
-      int next = id_of(sg.kt0);
-      for (int kt = sg.kt0; ok && kt < sg.kt1; ++kt, ++tile) {
-        const int id = next;
-        next = id_of(kt + 1);
-        const bool valid = (unsigned)id < (unsigned)p.c.pages, load = has_box && valid;
-        if (col == 0 && !valid && kt * KT + part * br < sg.i.keys) attn_flag(p.err);
-        const uint32_t loads = __ballot_sync(0xFFFFFFFFu, load);
-        if (lane == 0) {
-          uint32_t groups = 0;  // 16-key groups that are there (lanes 0 .. parts - 1: the first column's boxes)
-          for (int i = 0; i < parts; ++i)
-            if (loads >> i & 1) groups |= ((1u << (br / 16)) - 1) << (i * br / 16);
-          info[tile % kInfo] = groups;
-        }
-        copy(&tm_k, kt, id, load, loads);
-        copy(&tm_v, kt, id, load, loads);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == kWarpCopy) {
+      // ------------------------------------------------------------ copies
+      const int br = min(p.c.page_rows, KT), parts = KT / br;
+      const int part = lane % parts, col = lane / parts;
+      const bool has_box = col < G::BCH;
+      if (lane == 0) {
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
       }
-    }
-    if (!ok && lane == 0) {
-      *abort_flag = 1;
-      atomicOr(p.err, kErrTimeout);
-      // every copy issued lands before the CTA can exit
-      constexpr uint32_t N = E4M3 ? G::RAW : G::SLOTS;
-      for (uint32_t i = 0; i < N && i < ring; ++i) {
-        const uint32_t u = ring - 1 - i;
-        mbar_wait_drain(E4M3 ? raw_full(u % N) : full(u % N), (u / N) & 1);
-      }
-    }
-  } else if (warp < kWarpMma + STREAMS) {
-    // ------------------------------------------------------------ MMAs
-    if (lane == 0) {
-      constexpr uint32_t types = E4M3 ? kIdescF16 : ~0u;
-      constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, KT) & types;
-      constexpr uint32_t idesc_o = (idesc_bf16_f32(kRows, DIM) & types) | kIdescBMn;
-      const int mine = warp - kWarpMma;  // the softmax group served
-      uint32_t ring = 0, item = 0, turn = 0;
-      // Turns: a visit's two products are issued in one go. Left to themselves the two threads' MMAs mix, both groups
-      // wait for both, and then both do softmax while the tensor core rests; in turn, one group's softmax runs under
-      // the other's MMAs.
-      uint32_t turns = 0;
-      uint32_t made = 0;  // bit b: the parity of the scores written to S buffer b, the phase of its barriers
+      uint64_t pol;
+      asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
+      uint64_t keep;  // several row tiles come back for the same keys
+      asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
+      uint32_t ring = 0, tile = 0;
       bool ok = true;
-      const uint64_t q_desc = smem_desc(sbase, 16);
-      // Ring slot r has arrived. (A parity only tells two uses of a slot apart: whoever waits here has itself waited for
-      // the slot's use before, or for the end of the item that it was part of.)
-      auto arrived = [&](uint32_t r) {
-        return mbar_wait<true>(full(r % G::SLOTS), (r / G::SLOTS) & 1, abort_flag);
-      };
-      // a slot is free once both threads' MMAs have read it; where one thread issues them all it gives it back for both
-      auto release = [&](uint32_t slot, bool wide) {
-        tc_commit(empty(slot));
-        if (STREAMS == 2 && !wide) tc_commit(empty(slot));
-      };
-      // thread 0 goes first; later turns come from the other thread
-      auto my_turn = [&]() {
-        const uint32_t parity = mine == 0 ? (turns & 1) ^ 1 : turns & 1;
-        ++turns;
-        return mbar_wait<true>(turn_of(mine), parity, abort_flag);
-      };
       while (ok && next_segment<typename G::Tiles>(p, cur, sg)) {
-        ok = mbar_wait(q_full, item & 1, abort_flag);
-        ++item;
-        const int n = sg.kt1 - sg.kt0;
-        const bool wide = STREAMS == 2 && sg.rows > kRows;
-        // Visits to the S buffers in turn. Each first takes the P that the buffer holds (its last scores' weights) into
-        // the output, then writes the next scores: tile v / 2 of group v % 2, or tile v.
-        const int scores = wide ? 2 * n : n;
-        const int step = wide ? 2 : 1, last = wide || mine == 0 ? scores + 2 : 0;
-        for (int v = wide ? mine : 0; ok && v < last; v += step) {
-          const uint32_t b = STREAMS == 2 ? v & 1 : (turn + v) & 1;
-          const int was = v - 2;
-          if (was >= 0) {
-            const uint32_t r = ring + 2 * (wide ? was >> 1 : was) + 1;  // the values' ring slot
-            ok = arrived(r) && mbar_wait<true>(p_full(b), (made >> b & 1) ^ 1, abort_flag);
-            if (wide) ok = ok && (v >= scores || arrived(r + 1)) && my_turn();  // (r + 1: the keys that follow)
-            if (!ok) break;
-            tc_fence_after();
-            uint64_t vd = smem_desc(sbase + G::OFF_SLOT + (r % G::SLOTS) * G::SLOT, G::SUB);
-            uint32_t pa = tmem + b * KT;
-            const uint32_t d = tmem + G::COL_O + (STREAMS == 2 ? b * DIM : 0);
-            uint32_t add = was >= (wide ? 2 : STREAMS);  // the group's first output of the item overwrites
-#pragma unroll
-            for (int c = 0; c < KT / 64; ++c) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                tc_mma_f16_ts(d, pa + 8 * k, vd + k * (2048 >> 4), idesc_o, add);
-                add = 1;
-              }
-              pa += 32;
-              vd += 4 * (2048 >> 4);
-            }
-            if (STREAMS == 1) tc_commit(o_done);
-            release(r % G::SLOTS, wide);
+        const int32_t *ids = p.r.table + (long long)sg.b * p.r.max_pages;
+        const uint64_t policy = sg.i.n * p.group > G::ROWS ? keep : pol;
+        auto id_of = [&](int kt) {  // -1: past the keys
+          const long long key = (long long)kt * KT + part * br;
+          return kt < sg.kt1 && key < sg.i.keys ? ids[key >> p.c.page_shift] : -1;
+        };
+        auto copy = [&](const CUtensorMap *tm, int kt, int id, bool load, uint32_t loads) {
+          constexpr int N = E4M3 ? G::RAW : G::SLOTS;
+          const uint32_t s = ring % N, bar = E4M3 ? raw_full(s) : full(s);
+          ok = ok && mbar_wait(E4M3 ? raw_empty(s) : empty(s), ((ring / N) & 1) ^ 1, abort_flag);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) return;
+          if (lane == 0) mbar_arrive_expect_tx(bar, __popc(loads) * br * G::BW);
+          __syncwarp();
+          if (load)
+            tma_load_4d(sbase + (E4M3 ? G::OFF_RAW + s * G::RAW_SLOT : G::OFF_SLOT + s * G::SLOT) + col * G::BSUB + part * br * G::BW,
+                        tm, col * (G::BW / G::ELT), (kt * KT + part * br) & (p.c.page_rows - 1), sg.head, id, bar, policy);
+          __syncwarp();
+          ++ring;
+        };
+        int next = id_of(sg.kt0);
+        for (int kt = sg.kt0; ok && kt < sg.kt1; ++kt, ++tile) {
+          const int id = next;
+          next = id_of(kt + 1);
+          const bool valid = (unsigned)id < (unsigned)p.c.pages, load = has_box && valid;
+          if (col == 0 && !valid && kt * KT + part * br < sg.i.keys) attn_flag(p.err);
+          const uint32_t loads = __ballot_sync(0xFFFFFFFFu, load);
+          if (lane == 0) {
+            uint32_t groups = 0;  // 16-key groups that are there (lanes 0 .. parts - 1: the first column's boxes)
+            for (int i = 0; i < parts; ++i)
+              if (loads >> i & 1) groups |= ((1u << (br / 16)) - 1) << (i * br / 16);
+            info[tile % kInfo] = groups;
           }
-          if (v < scores) {
-            const uint32_t r = ring + 2 * (wide ? v >> 1 : v);  // the keys' ring slot
-            if (!wide || was < 0) {
-              ok = arrived(r) && (!wide || my_turn());
-              if (!ok) break;
-              tc_fence_after();
-            }
-            uint64_t kd = smem_desc(sbase + G::OFF_SLOT + (r % G::SLOTS) * G::SLOT, 16);
-            uint64_t qd = q_desc + (wide && b ? G::Q_TILE >> 4 : 0);
-            const uint32_t d = tmem + b * KT;
-            uint32_t add = 0;
-#pragma unroll
-            for (int c = 0; c < G::CH; ++c) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                tc_mma_f16(d, qd + 2 * k, kd + 2 * k, idesc_s, add);
-                add = 1;
-              }
-              qd += G::QSUB >> 4;
-              kd += G::SUB >> 4;
-            }
-            tc_commit(s_full(b));
-            made ^= 1u << b;
-            release(r % G::SLOTS, wide);
-          }
-          if (wide) mbar_arrive(turn_of(mine ^ 1));
+          copy(&tm_k, kt, id, load, loads);
+          copy(&tm_v, kt, id, load, loads);
         }
-        // the phases of the buffers that the other thread wrote
-        if (wide) made ^= (n & 1u) << (mine ^ 1);
-        else if (mine == 1) made ^= ((n + 1) / 2 & 1u) | (n / 2 & 1u) << 1;
-        turn += n;
-        ring += 2 * n;
-        tc_commit(o_full);
       }
-      if (!ok) {
+      if (!ok && lane == 0) {
         *abort_flag = 1;
         atomicOr(p.err, kErrTimeout);
-        // every MMA issued has completed before TMEM is freed (the loop's last commit covers them)
-        if (item > 0) mbar_wait_drain(o_full, (item - 1) & 1);
+        // every copy issued lands before the CTA can exit
+        constexpr uint32_t N = E4M3 ? G::RAW : G::SLOTS;
+        for (uint32_t i = 0; i < N && i < ring; ++i) {
+          const uint32_t u = ring - 1 - i;
+          mbar_wait_drain(E4M3 ? raw_full(u % N) : full(u % N), (u / N) & 1);
+        }
+      }
+    } else if (warp < kWarpMma + STREAMS) {
+      // ------------------------------------------------------------ MMAs
+      if (lane == 0) {
+        constexpr uint32_t types = E4M3 ? kIdescF16 : ~0u;
+        constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, KT) & types;
+        constexpr uint32_t idesc_o = (idesc_bf16_f32(kRows, DIM) & types) | kIdescBMn;
+        const int mine = warp - kWarpMma;  // the softmax group served
+        uint32_t ring = 0, item = 0, turn = 0;
+        // Turns: a visit's two products are issued in one go. Left to themselves the two threads' MMAs mix, both groups
+        // wait for both, and then both do softmax while the tensor core rests; in turn, one group's softmax runs under
+        // the other's MMAs.
+        uint32_t turns = 0;
+        uint32_t made = 0;  // bit b: the parity of the scores written to S buffer b, the phase of its barriers
+        bool ok = true;
+        const uint64_t q_desc = smem_desc(sbase, 16);
+        // Ring slot r has arrived. (A parity only tells two uses of a slot apart: whoever waits here has itself waited for
+        // the slot's use before, or for the end of the item that it was part of.)
+        auto arrived = [&](uint32_t r) {
+          return mbar_wait<true>(full(r % G::SLOTS), (r / G::SLOTS) & 1, abort_flag);
+        };
+        // a slot is free once both threads' MMAs have read it; where one thread issues them all it gives it back for both
+        auto release = [&](uint32_t slot, bool wide) {
+          if (STREAMS == 2 && !wide) mbar_arrive(empty(slot));
+          tc_commit(empty(slot));
+        };
+        // thread 0 goes first; later turns come from the other thread
+        auto my_turn = [&]() {
+          const uint32_t parity = mine == 0 ? (turns & 1) ^ 1 : turns & 1;
+          ++turns;
+          return mbar_wait<true>(turn_of(mine), parity, abort_flag);
+        };
+        while (ok && next_segment<typename G::Tiles>(p, cur, sg)) {
+          ok = mbar_wait(q_full, item & 1, abort_flag);
+          ++item;
+          const int n = sg.kt1 - sg.kt0;
+          const bool wide = STREAMS == 2 && sg.rows > kRows;
+          // Visits to the S buffers in turn. Each first takes the P that the buffer holds (its last scores' weights) into
+          // the output, then writes the next scores: tile v / 2 of group v % 2, or tile v.
+          const int scores = wide ? 2 * n : n;
+          const int step = wide ? 2 : 1, last = wide || mine == 0 ? scores + 2 : 0;
+          for (int v = wide ? mine : 0; ok && v < last; v += step) {
+            const uint32_t b = STREAMS == 2 ? v & 1 : (turn + v) & 1;
+            const int was = v - 2;
+            if (was >= 0) {
+              const uint32_t r = ring + 2 * (wide ? was >> 1 : was) + 1;  // the values' ring slot
+              ok = arrived(r) && mbar_wait<true>(p_full(b), (made >> b & 1) ^ 1, abort_flag);
+              if (wide) ok = ok && (v >= scores || arrived(r + 1)) && my_turn();  // (r + 1: the keys that follow)
+              if (!ok) break;
+              tc_fence_after();
+              uint64_t vd = smem_desc(sbase + G::OFF_SLOT + (r % G::SLOTS) * G::SLOT, G::SUB);
+              uint32_t pa = tmem + b * KT;
+              const uint32_t d = tmem + G::COL_O + (STREAMS == 2 ? b * DIM : 0);
+              uint32_t add = was >= (wide ? 2 : STREAMS);  // the group's first output of the item overwrites
+#pragma unroll
+              for (int c = 0; c < KT / 64; ++c) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  tc_mma_f16_ts(d, pa + 8 * k, vd + k * (2048 >> 4), idesc_o, add);
+                  add = 1;
+                }
+                pa += 32;
+                vd += 4 * (2048 >> 4);
+              }
+              if (STREAMS == 1) tc_commit(o_done);
+              release(r % G::SLOTS, wide);
+            }
+            if (v < scores) {
+              const uint32_t r = ring + 2 * (wide ? v >> 1 : v);  // the keys' ring slot
+              if (!wide || was < 0) {
+                ok = arrived(r) && (!wide || my_turn());
+                if (!ok) break;
+                tc_fence_after();
+              }
+              uint64_t kd = smem_desc(sbase + G::OFF_SLOT + (r % G::SLOTS) * G::SLOT, 16);
+              uint64_t qd = q_desc + (wide && b ? G::Q_TILE >> 4 : 0);
+              const uint32_t d = tmem + b * KT;
+              uint32_t add = 0;
+#pragma unroll
+              for (int c = 0; c < G::CH; ++c) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  tc_mma_f16(d, qd + 2 * k, kd + 2 * k, idesc_s, add);
+                  add = 1;
+                }
+                qd += G::QSUB >> 4;
+                kd += G::SUB >> 4;
+              }
+              tc_commit(s_full(b));
+              made ^= 1u << b;
+              release(r % G::SLOTS, wide);
+            }
+            if (wide) mbar_arrive(turn_of(mine ^ 1));
+          }
+          // the phases of the buffers that the other thread wrote
+          if (wide) made ^= (n & 1u) << (mine ^ 1);
+          else if (mine == 1) made ^= ((n + 1) / 2 & 1u) | (n / 2 & 1u) << 1;
+          turn += n;
+          ring += 2 * n;
+          tc_commit(o_full);
+        }
+        if (!ok) {
+          *abort_flag = 1;
+          atomicOr(p.err, kErrTimeout);
+          // every MMA issued has completed before TMEM is freed (the loop's last commit covers them)
+          if (item > 0) mbar_wait_drain(o_full, (item - 1) & 1);
+        }
       }
     }
-  }
   } else if (warp < kWarpSoftmax + 4 * STREAMS) {
     if constexpr (E4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
