@@ -29,11 +29,27 @@ __device__ __forceinline__ long long row_offset(const KvSide &s, const KvRows &r
   return (long long)id * s.page + (pos & ((1 << page_shift) - 1)) * s.row;
 }
 
-// The row a token belongs to: the last b with starts[b] <= token (rows
-// without tokens are passed over); `rows` when the token is padding.
+// The row that each lane's token belongs to: the last b with starts[b] <= token
+// (rows without tokens are passed over); `rows` when the token is padding.
+// `token` ascends by one from lane to lane. The warp looks for lane 0's row, 32
+// starts at a time; most lanes' tokens are in the same one.
 __device__ __forceinline__ int owner_of(const int32_t *starts, int rows, int token) {
-  int lo = 0, hi = rows;  // first b in [0, rows) with starts[b + 1] > token
-  while (lo < hi) {
+  const int lane = threadIdx.x & 31, token0 = token - lane;
+  int lo = 0, n = rows;  // lane 0's row, the first b with starts[b + 1] > token0, is one of lo .. lo + n
+  while (n > 0) {
+    const int step = (n + 31) / 32, probe = lo + min((lane + 1) * step, n);
+    const uint32_t above = __ballot_sync(0xFFFFFFFFu, starts[probe] > token0);
+    if (!above) {
+      lo += n;
+      break;
+    }
+    const int part = __ffs(above) - 1;
+    lo += part * step;
+    n = min(step, n - part * step) - 1;
+  }
+  if (lo >= rows || starts[lo + 1] > token) return lo;
+  int hi = rows;
+  for (++lo; lo < hi;) {
     const int mid = (lo + hi) >> 1;
     if (starts[mid + 1] > token) hi = mid;
     else lo = mid + 1;
@@ -42,14 +58,15 @@ __device__ __forceinline__ int owner_of(const int32_t *starts, int rows, int tok
 }
 
 // ---------------------------------------------------------------------------
-// append: 16 bytes of input per thread and step, four steps in flight. Bound by
-// HBM; in 8 bits nearly as much by the integer pipe, which unpacks and converts:
-// 25,446 tokens of 8 heads of 128 to e4m3 (156 MB) 32.5 us, 4.8 TB/s (with six
-// steps 33.0 us, with eight 35.6).
+// append: a thread has one 16-byte chunk of one head in four tokens, all in
+// flight at once. Bound by HBM; in 8 bits nearly as much by the integer pipe,
+// which unpacks and converts: 25,446 tokens of 8 heads of 128 to e4m3 (156 MB)
+// 28.2 us, 5.5 TB/s (blocks of 256 threads 29.3 us, of 512 35.2; eight tokens a
+// thread 28.5).
 // ---------------------------------------------------------------------------
-constexpr int kAppendThreads = 256;
-constexpr int kAppendTokens = 64;  // most tokens of a block
-constexpr int kAppendBatch = 4;    // 16-byte loads of a thread in flight
+constexpr int kAppendThreads = 128;
+constexpr int kAppendBatch = 4;  // tokens of a thread
+constexpr int kAppendTokens = kAppendThreads / 8 * kAppendBatch;  // of a block at most (a token has 8 chunks or more)
 
 struct AppendParams {
   const uint16_t *src[2];
@@ -57,8 +74,7 @@ struct AppendParams {
   KvSide side[2];
   KvRows r;
   int kv_heads, dim_chunks_log2, page_shift, pages;
-  int tokens_per_block;
-  uint32_t token_magic;  // ceil(2^32 / chunks of a token): a block has under 2^16 of them
+  int per_token, groups;  // chunks of a token; tokens side by side in a block
   int *err;
 };
 
@@ -99,70 +115,56 @@ __device__ __forceinline__ uint2 to_e4m3(const uint4 &x, const float2 &d) {
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-// A block moves some tokens' rows of one side (blockIdx.y). Its data does not
-// depend on where it goes, so its first batch of loads is in flight while a few
-// threads look up the places.
+// A block moves some tokens' rows of one side (blockIdx.y), or of heads with
+// more chunks than it has threads a part (blockIdx.z). Its data does not depend
+// on where it goes, so the loads are in flight while some threads look up the
+// places.
 template <bool E4M3>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ AppendParams p) {
   __shared__ long long off[kAppendTokens];
-  extern __shared__ float2 divisor[];  // [kv_heads]
   grid_dependency_wait();
   grid_launch_dependents();
   const bool values = blockIdx.y != 0;
-  const uint16_t *src = values ? p.src[1] : p.src[0];
-  const long long token_stride = values ? p.token_stride[1] : p.token_stride[0];
-  const long long head_stride = values ? p.head_stride[1] : p.head_stride[0];
   const KvSide &s = values ? p.side[1] : p.side[0];
-  const int t0 = blockIdx.x * p.tokens_per_block;
-  const int nt = min(p.tokens_per_block, p.r.tokens - t0);
-  // items of the block: (token, head, 16-byte chunk), chunk fastest
-  const int per_token = p.kv_heads << p.dim_chunks_log2, items = nt * per_token;
-  constexpr int U = kAppendBatch;
-  uint4 x[U];
-  uint32_t where[U];  // token << 16 | head and chunk
-  auto load = [&](int e0) {
+  const long long token_stride = values ? p.token_stride[1] : p.token_stride[0];
+  const int t0 = blockIdx.x * p.groups * kAppendBatch;
+  const int nt = min(p.groups * kAppendBatch, p.r.tokens - t0);
+  const int group = threadIdx.x / p.per_token, chunk = blockIdx.z * kAppendThreads + threadIdx.x - group * p.per_token;
+  const int h = chunk >> p.dim_chunks_log2, c = chunk & ((1 << p.dim_chunks_log2) - 1);
+  const int n = group < p.groups && chunk < p.per_token ? nt : 0;  // (the last threads may have no chunk)
+  uint4 x[kAppendBatch];
+  float scale = 0.f;
+  if (n > 0) {
+    const uint16_t *src = (values ? p.src[1] : p.src[0]) + (long long)(t0 + group) * token_stride +
+                          h * (values ? p.head_stride[1] : p.head_stride[0]) + c * 8;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int e = e0 + u * kAppendThreads;
-      if (e >= items) continue;
-      const int t = __umulhi(e, p.token_magic), rest = e - t * per_token;
-      const int h = rest >> p.dim_chunks_log2, c = rest & ((1 << p.dim_chunks_log2) - 1);
-      x[u] = *reinterpret_cast<const uint4 *>(src + (long long)(t0 + t) * token_stride + (long long)h * head_stride + c * 8);
-      where[u] = (uint32_t)t << 16 | (uint32_t)rest;
-    }
-  };
-  auto store = [&](int e0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (e0 + u * kAppendThreads >= items) continue;
-      const long long o = off[where[u] >> 16];
-      if (o < 0) continue;
-      const int rest = where[u] & 0xFFFFu, h = rest >> p.dim_chunks_log2, c = rest & ((1 << p.dim_chunks_log2) - 1);
-      uint8_t *dst = s.base + o + (long long)h * s.head + c * (E4M3 ? 8 : 16);
-      if (E4M3) *reinterpret_cast<uint2 *>(dst) = to_e4m3(x[u], divisor[h]);
-      else *reinterpret_cast<uint4 *>(dst) = x[u];
-    }
-  };
-  load(threadIdx.x);
-  if (E4M3)
-    for (int i = threadIdx.x; i < p.kv_heads; i += kAppendThreads) divisor[i] = divisor_of(s.scale[i]);
-  if ((int)threadIdx.x < nt) {
+    for (int u = 0; u < kAppendBatch; ++u)
+      if (group + u * p.groups < n) x[u] = *reinterpret_cast<const uint4 *>(src + u * p.groups * token_stride);
+    if (E4M3) scale = s.scale[h];
+  }
+  if ((int)(threadIdx.x & ~31u) < nt) {
     const int t = t0 + threadIdx.x;
     const int b = owner_of(p.r.starts, p.r.rows, t);
     long long o = -1;
-    if (b < p.r.rows) {
+    if (b < p.r.rows && (int)threadIdx.x < nt) {
       const int first = p.r.starts[b], len = p.r.lengths[b];
       // (starts that descend or do not begin at 0 leave a token before its row's first)
       if (t >= first && len >= 0) o = row_offset(s, p.r, p.page_shift, p.pages, b, (long long)len + (t - first));
       if (o < 0) flag_index(p.err);
     }
-    off[threadIdx.x] = o;
+    if ((int)threadIdx.x < nt) off[threadIdx.x] = o;
   }
+  const float2 divisor = E4M3 ? divisor_of(scale) : make_float2(0.f, 0.f);
   __syncthreads();
-  store(threadIdx.x);
-  for (int e0 = threadIdx.x + U * kAppendThreads; e0 < items; e0 += U * kAppendThreads) {
-    load(e0);
-    store(e0);
+  uint8_t *dst = s.base + h * s.head + c * (E4M3 ? 8 : 16);
+#pragma unroll
+  for (int u = 0; u < kAppendBatch; ++u) {
+    const int t = group + u * p.groups;
+    if (t >= n) break;
+    const long long o = off[t];
+    if (o < 0) continue;
+    if (E4M3) *reinterpret_cast<uint2 *>(dst + o) = to_e4m3(x[u], divisor);
+    else *reinterpret_cast<uint4 *>(dst + o) = x[u];
   }
 }
 
@@ -627,11 +629,10 @@ int log2_of(int v) {
 // Every kernel here waits for the work before it (griddepcontrol.wait) before
 // its first access, so it may always be launched while that work ends.
 template <class... K, class... A>
-cudaError_t launch_smem(void (*kern)(K...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+cudaError_t launch(void (*kern)(K...), dim3 grid, int threads, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t lc = {};
   lc.gridDim = grid;
   lc.blockDim = dim3(threads, 1, 1);
-  lc.dynamicSmemBytes = smem;
   lc.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -639,10 +640,6 @@ cudaError_t launch_smem(void (*kern)(K...), dim3 grid, int threads, size_t smem,
   lc.attrs = attr;
   lc.numAttrs = 1;
   return cudaLaunchKernelEx(&lc, kern, args...);
-}
-template <class... K, class... A>
-cudaError_t launch(void (*kern)(K...), dim3 grid, int threads, cudaStream_t stream, A... args) {
-  return launch_smem(kern, grid, threads, 0, stream, args...);
 }
 
 }  // namespace
@@ -663,13 +660,13 @@ cudaError_t launch_kv_append(const AppendCall &c) {
   p.page_shift = c.cache.page_shift;
   p.pages = c.cache.pages;
   p.err = c.err;
-  // a batch of chunks per thread, or what one token has
-  const int per_token = c.cache.kv_heads * (c.cache.dim / 8);
-  p.tokens_per_block = std::min(kAppendTokens, std::max(1, kAppendBatch * kAppendThreads / per_token));
-  p.token_magic = (uint32_t)(((1ull << 32) + per_token - 1) / per_token);
-  const dim3 grid((c.rows.tokens + p.tokens_per_block - 1) / p.tokens_per_block, 2);
-  return c.cache.e4m3 ? launch_smem(kv_append_kernel<true>, grid, kAppendThreads, c.cache.kv_heads * sizeof(float2), c.stream, p)
-                      : launch(kv_append_kernel<false>, grid, kAppendThreads, c.stream, p);
+  p.per_token = c.cache.kv_heads * (c.cache.dim / 8);
+  p.groups = std::max(1, kAppendThreads / p.per_token);
+  const int tokens = p.groups * kAppendBatch, parts = (p.per_token + kAppendThreads - 1) / kAppendThreads;
+  // whole warps (they look for rows together)
+  const int threads = std::min(kAppendThreads, (p.groups * p.per_token + 31) / 32 * 32);
+  const dim3 grid((c.rows.tokens + tokens - 1) / tokens, 2, parts);
+  return launch(c.cache.e4m3 ? kv_append_kernel<true> : kv_append_kernel<false>, grid, threads, c.stream, p);
 }
 
 cudaError_t launch_tree_accept(const int64_t *target, const int64_t *draft, const int64_t *mask, const int32_t *starts,
