@@ -54,6 +54,32 @@ def test_append(dim, kv, page, layout, e4m3, sizes):
         assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("dim,kv,rows", [(64, 5, 70), (256, 20, 33), (128, 33, 4), (64, 1, 1100), (128, 2, 1025)])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_append_many_rows_and_heads(dim, kv, rows, e4m3):
+    """More rows than a warp looks at, heads off a block's threads, rows without tokens in between."""
+    rng = np.random.default_rng(rows)
+    sizes, lengths = rng.choice([0, 0, 1, 2, 40], rows).tolist(), rng.integers(0, 50, rows).tolist()
+    n = sum(sizes)
+    s = Step(lengths, sizes, kv, kv, dim, 16, e4m3=e4m3, masks=np.zeros(n, np.uint64))
+    k, v = (torch.randn((n, kv, dim), device="cuda").to(BF16) for _ in range(2))
+    want_k, want_v = s.k.clone(), s.v.clone()
+    row = np.repeat(np.arange(rows), sizes)
+    pos = np.asarray(lengths)[row] + np.arange(n) - np.asarray(s.starts_h)[row]
+    ids, at = (torch.from_numpy(x.astype(np.int64)).cuda() for x in (np.asarray(s.table_h)[row, pos // 16], pos % 16))
+    for want, x, scale in ((want_k, k, s.ks), (want_v, v, s.vs)):
+        if e4m3:
+            x = (x.float() / scale[:, None]).clamp(-448, 448).to(E4M3)
+        bits(want)[ids, :, at] = bits(x)
+    w4.kv_append(k, v, s.k, s.v, s.table, s.lengths, s.starts, k_scale=s.ks, v_scale=s.vs)
+    assert ok() == 0
+    for got, want in ((s.k, want_k), (s.v, want_v)):
+        got, want = bits(got), bits(want)
+        if e4m3:  # a NaN code's sign is free
+            got, want = (torch.where(x & 0x7F == 0x7F, 0x7F, x) for x in (got, want))
+        assert torch.equal(got, want)
+
+
 def test_append_every_e4m3_rounding():
     """Each code, the halfway points between codes and their bf16 neighbours, at two scales."""
     codes = torch.arange(256, dtype=torch.uint8).view(E4M3).float()
