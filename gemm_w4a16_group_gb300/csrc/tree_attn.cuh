@@ -31,9 +31,9 @@ constexpr int tc_attn_rows(int dim, bool e4m3) { return dim == 256 || e4m3 ? 128
 constexpr int tc_attn_keys(int dim) { return dim == 256 ? 64 : 128; }
 // Tables of so few keys are worked on without splitting items, so nothing has
 // to be joined, and no second launch is made (2.3 us of the host's time). On the
-// device, whole against split: one row of 400 keys 13.0 and 16.8 us, 40 rows of
-// 400 24.3 and 24.2, of 700 34.8 and 29.7; on the tcgen05 kernel 12 rows of 700
-// keys 19.3 and 24.4 us, one of 1,000 with 40 nodes 29.8 and 26.7.
+// device, whole against split: one row of 400 keys 13.1 and 14.3 us, 40 rows of
+// 400 24.4 and 24.4, of 700 34.9 and 29.8; on the tcgen05 kernel 12 rows of 700
+// keys 19.6 and 24.5 us, one of 1,000 with 40 nodes 30.0 and 24.0.
 constexpr long long kWholeKeys = 512, kTcWholeKeys = 768;
 constexpr float kLog2e = 1.4426950408889634f;
 
