@@ -117,12 +117,12 @@ template <int ROWS>
 __device__ __forceinline__ int row_tiles(const RowInfo &i, int group) {
   return (i.n * group + ROWS - 1) / ROWS;
 }
+// of one kv head; all of them count the same
 template <class T>
 __device__ __forceinline__ long long units_of(const RowInfo &i, const AttnParams &p) {
   if (i.n == 0) return 0;
   const int rows = i.n * p.group, full = (rows - 1) / T::ROWS;  // (the last item is full or less)
-  return (long long)p.c.kv_heads * (key_tiles<T::KT>(i) + T::LEAD) *
-         (full * T::FULL_COST + T::cost(rows - full * T::ROWS));
+  return (long long)(key_tiles<T::KT>(i) + T::LEAD) * (full * T::FULL_COST + T::cost(rows - full * T::ROWS));
 }
 
 // A CTA's place in the work list: units [at, end) are its share, `unit` is the
@@ -148,8 +148,13 @@ __device__ void plan_share(const AttnParams &p, PlanShared &s) {
   const int per = (p.r.rows + NT - 1) / NT;
   const int b0 = min(tid * per, p.r.rows), b1 = min(b0 + per, p.r.rows);
   const bool flag = blockIdx.x == 0;  // one CTA reports rows that cannot be
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += units_of<T>(row_info(p, b, flag), p);
+  long long mine = 0, per_head = 0;
+  RowInfo i;  // of the run's last row (nearly always its only one)
+  for (int b = b0; b < b1; ++b) {
+    i = row_info(p, b, flag);
+    per_head = units_of<T>(i, p);
+    mine += per_head * p.c.kv_heads;
+  }
   long long upto = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -180,20 +185,27 @@ __device__ void plan_share(const AttnParams &p, PlanShared &s) {
   }
   if (at < end && first <= at && at < first + mine) {
     long long f = first;
-    for (int b = b0; b < b1; ++b) {
-      const RowInfo i = row_info(p, b, false);
-      const long long n = units_of<T>(i, p);
-      if (at < f + n) {
-        const long long per_head = quotient(n, p.c.kv_heads), o = at - f;
-        const long long per_tile = (long long)(key_tiles<T::KT>(i) + T::LEAD) * T::FULL_COST;  // a full item
-        s.b = b;
-        s.head = (int)quotient(o, per_head);
-        s.rt = (int)quotient(o - s.head * per_head, per_tile);
-        s.unit = f + s.head * per_head + s.rt * per_tile;
-        break;
+    int b = b0;
+    if (per > 1)
+      for (;; ++b) {
+        i = row_info(p, b, false);
+        per_head = units_of<T>(i, p);
+        if (at < f + per_head * p.c.kv_heads) break;
+        f += per_head * p.c.kv_heads;
       }
-      f += n;
+    const long long o = at - f;
+    const int head = (int)quotient(o, per_head);
+    int rt = 0;
+    long long unit = f + head * per_head;
+    if (i.n * p.group > T::ROWS) {
+      const long long per_tile = (long long)(key_tiles<T::KT>(i) + T::LEAD) * T::FULL_COST;  // a full item
+      rt = (int)quotient(at - unit, per_tile);
+      unit += rt * per_tile;
     }
+    s.b = b;
+    s.head = head;
+    s.rt = rt;
+    s.unit = unit;
   }
 }
 
