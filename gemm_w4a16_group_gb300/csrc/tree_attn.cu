@@ -681,6 +681,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   constexpr int WARPS = kJoinThreads / 32, SQUARES = DIM / 16;  // squares along a row
   using Part = Partial<DIM, ROWS>;
   __shared__ int ends[kMaxCtas];  // work of records 0 .. c
+  __shared__ int rows_of[kMaxCtas];
+  __shared__ int4 records[kMaxCtas];
   __shared__ int sums[WARPS];
   __shared__ float4 acc[SPLIT ? WARPS : 1][32];
   grid_dependency_wait();
@@ -688,7 +690,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int total = 0;
   for (int c0 = 0; c0 < ctas; c0 += kJoinThreads) {
-    int v = c0 + tid < ctas ? (p.joins[c0 + tid] + 7) / 8 * (SPLIT ? SQUARES : 1) : 0;
+    int v = 0;
+    if (c0 + tid < ctas) {
+      records[c0 + tid] = reinterpret_cast<const int4 *>(p.joins + kMaxCtas)[c0 + tid];  // (without rows: never looked at)
+      rows_of[c0 + tid] = p.joins[c0 + tid];
+      v = (rows_of[c0 + tid] + 7) / 8 * (SPLIT ? SQUARES : 1);
+    }
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
@@ -713,21 +720,34 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       else c1 = mid + 1;
     }
     const int local = e - (c1 ? ends[c1 - 1] : 0);
-    const int4 rec = reinterpret_cast<const int4 *>(p.joins + kMaxCtas)[c1];
-    const int rows = p.joins[c1], c0 = rec.x, n = c1 - c0 + 1;
+    const int4 rec = records[c1];
+    const int rows = rows_of[c1], c0 = rec.x, n = c1 - c0 + 1;
     const int r0 = (SPLIT ? local / SQUARES : local) * 8 + (lane & 7), r = min(r0, rows - 1);
     // the first CTA ended its share inside the item (slot 1), the others began theirs in it (slot 0)
     auto part = [&](int c) { return Part(p.partials, c0 + c, c == 0 ? 1 : 0); };
-    float M = -INFINITY;
-#pragma unroll 4
-    for (int c = 0; c < n; ++c) M = fmaxf(M, part(c).ml(r)->x);
-    const float base = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
-#pragma unroll 4
-    for (int c = 0; c < n; ++c) {
-      const float2 ml = *part(c).ml(r);
-      L += ml.y * exp2_approx(ml.x - base);
+    // maximum and sum: the four lanes of a row take the partials in turn, eight loads in flight
+    float M = -INFINITY, L = 0.f;
+    auto add = [&](float m, float l) {
+      const float top = fmaxf(M, m), b = top == -INFINITY ? 0.f : top;
+      L = L * exp2_approx(M - b) + l * exp2_approx(m - b);
+      M = top;
+    };
+    for (int k = lane >> 3; k < n; k += 32) {
+      float2 ml[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) ml[u] = k + 4 * u < n ? *part(k + 4 * u).ml(r) : make_float2(-INFINITY, 0.f);
+      float top = ml[0].x;
+#pragma unroll
+      for (int u = 1; u < 8; ++u) top = fmaxf(top, ml[u].x);
+      const float b = top == -INFINITY ? 0.f : top;
+      float l = 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) l += ml[u].y * exp2_approx(ml[u].x - b);
+      add(top, l);
     }
+#pragma unroll
+    for (int d = 8; d < 32; d <<= 1) add(__shfl_xor_sync(0xFFFFFFFFu, M, d), __shfl_xor_sync(0xFFFFFFFFu, L, d));
+    const float base = M == -INFINITY ? 0.f : M;
     const float inv = (L > 0.f || L != L) ? (p.c.e4m3 ? p.c.v.scale[rec.w] : 1.f) / L : 0.f;
     const int rr = rec.z + r, tok = rec.y + rr / p.group;
     uint16_t *out = p.out + ((long long)tok * p.heads + rec.w * p.group + rr % p.group) * DIM;
