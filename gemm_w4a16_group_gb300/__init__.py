@@ -662,21 +662,21 @@ def _empty(shape, dtype, like, stream):
 
 
 _small_outputs = {}
-_SMALL, _AT_ONCE = 4096, 32
+_SMALL, _AT_ONCE = 16384, 32  # bytes of a small output, how many are made at once
 
 
-def _int_out(shape, dtype, like, dev, stream, handle):
-    """A new integer tensor, as _empty gives it. Small ones are made 32 at a
-    time, as rows of one allocation: on their own three of them cost more than
-    the call that fills them (10 us against 6). Each is handed out once; their
-    common memory goes back to the stream's pool with the last of them. Under
-    capture every output comes from the graph's pool."""
+def _small_out(shape, dtype, like, dev, stream, handle):
+    """A new tensor, as _empty gives it. Small ones are made 32 at a time, as
+    rows of one allocation: on their own three of them cost more than the call
+    that fills them (10 us against 6). Each is handed out once; their common
+    memory goes back to the stream's pool with the last of them. Under capture
+    every output comes from the graph's pool."""
     if _torch().cuda.is_current_stream_capturing():
         return _empty(shape, dtype, like, stream)
     key = (shape, dtype, dev, handle)
     ready = _small_outputs.get(key)
     if not ready:
-        n = 8
+        n = dtype.itemsize
         for d in shape:
             n *= d
         if n > _SMALL:
@@ -807,7 +807,11 @@ def tree_attention(q, k_cache, v_cache, page_table, lengths, starts, mask, max_t
     elif workspace.dtype is not ty.u8 or workspace.get_device() != dev or not workspace.is_contiguous() or workspace.numel() < need:
         _refuse(workspace, ty.u8, "workspace", dev, need)
     if out is None:
-        out = _empty((tokens, heads, dim), ty.bf16, q, stream)
+        # (the sizes of one or two tokens; a larger call is longer on the device than here)
+        if 2 * tokens * heads * dim <= _SMALL:
+            out = _small_out((tokens, heads, dim), ty.bf16, q, dev, stream, handle.value)
+        else:
+            out = _empty((tokens, heads, dim), ty.bf16, q, stream)
     rc = lib().w4a16_tree_attention(qp, qt, qh, cache, table, width, _flat(lengths, ty.i32, "lengths", rows, dev),
                                     _flat(starts, ty.i32, "starts", rows + 1, dev),
                                     None if mask is None else _flat(mask, ty.i64, "mask", tokens, dev), rows, tokens,
@@ -827,11 +831,11 @@ def tree_accept(target, draft, mask, starts, max_tree, path=None, count=None, to
     tokens, rows = target.numel(), starts.numel() - 1
     handle = _on(stream, target)
     if path is None:
-        path = _int_out((rows, max_tree), ty.i32, target, dev, stream, handle.value)
+        path = _small_out((rows, max_tree), ty.i32, target, dev, stream, handle.value)
     if count is None:
-        count = _int_out((rows,), ty.i32, target, dev, stream, handle.value)
+        count = _small_out((rows,), ty.i32, target, dev, stream, handle.value)
     if token is None:
-        token = _int_out((rows,), ty.i64, target, dev, stream, handle.value)
+        token = _small_out((rows,), ty.i64, target, dev, stream, handle.value)
     rc = lib().w4a16_tree_accept(_flat(target, ty.i64, "target", tokens, dev), _flat(draft, ty.i64, "draft", tokens, dev),
                                  None if mask is None else _flat(mask, ty.i64, "mask", tokens, dev),
                                  _flat(starts, ty.i32, "starts", rows + 1, dev), rows, tokens, max_tree,
@@ -855,7 +859,7 @@ def kv_compact(k_cache, v_cache, page_table, lengths, path, count, lengths_out=N
     max_tree = path.shape[1]
     handle = _on(stream, k_cache)
     if lengths_out is None:
-        lengths_out = _int_out((rows,), ty.i32, k_cache, dev, stream, handle.value)
+        lengths_out = _small_out((rows,), ty.i32, k_cache, dev, stream, handle.value)
     rc = lib().w4a16_kv_compact(cache, table, width, _flat(lengths, ty.i32, "lengths", rows, dev),
                                 _flat(path, ty.i32, "path", rows * max_tree, dev),
                                 _flat(count, ty.i32, "count", rows, dev), rows, max_tree,
@@ -888,7 +892,7 @@ def kv_fork(k_cache, v_cache, page_table, lengths, refs, src, dst, ok=None, stre
     table, table_rows, width = _table(page_table, dev)
     handle = _on(stream, page_table)
     if ok is None:
-        ok = _int_out((1,), i32, page_table, dev, stream, handle.value)
+        ok = _small_out((1,), i32, page_table, dev, stream, handle.value)
     n = src.numel()
     rc = lib().w4a16_kv_fork(cache, table, width, table_rows, _flat(lengths, i32, "lengths", table_rows, dev),
                              _flat(refs, i32, "refs", shape[1], dev), _flat(src, i32, "src", n, dev),
@@ -906,7 +910,7 @@ def kv_reserve(page_table, refs, rows, want, page_rows, ok=None, stream=None):
     table, table_rows, width = _table(page_table, dev)
     handle = _on(stream, page_table)
     if ok is None:
-        ok = _int_out((1,), i32, page_table, dev, stream, handle.value)
+        ok = _small_out((1,), i32, page_table, dev, stream, handle.value)
     n, pages = rows.numel(), refs.numel()
     rc = lib().w4a16_kv_reserve(table, width, table_rows, _flat(refs, i32, "refs", pages, dev), pages, page_rows,
                                 _flat(rows, i32, "rows", n, dev), _flat(want, i32, "want", n, dev), n,

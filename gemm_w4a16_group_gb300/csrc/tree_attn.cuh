@@ -171,10 +171,10 @@ __device__ void plan_share(const AttnParams &p, PlanShared &s) {
     total += x;
   }
   const long long first = before + upto - mine;
-  // As many CTAs as get three key tiles of a narrow item each (a share then holds a whole one of any item), and no share
-  // larger than it has to be. With twice as many each, one row of 2,048 keys took 24.2 us with 16 nodes and not 17.5, of
-  // 8,191 keys 25.1 and not 21.6, one token over 2,048 keys 17.4 and not 15.9.
-  const long long ctas = max(1ll, min((long long)gridDim.x, quotient(total, 3 * T::cost(1))));
+  // As many CTAs as get two key tiles of a narrow item each (a share then holds a whole one of any item), and no share
+  // larger than it has to be. One token, or 16 nodes, over 2,048 keys: 13.7 and 16.0 us; with three 14.6 and 16.6, with
+  // four 14.4 and 17.4.
+  const long long ctas = max(1ll, min((long long)gridDim.x, quotient(total, 2 * T::cost(1))));
   const long long share = max(1ll, quotient(total + ctas - 1, ctas));
   const long long at = min(share * blockIdx.x, total), end = min(at + share, total);
   if (tid == 0) {

@@ -136,7 +136,7 @@ def fake(monkeypatch):
     monkeypatch.setattr(w4, "_is_device_tensor", lambda t: True)
     monkeypatch.setattr(w4, "_stream", lambda stream, device=None: ctypes.c_void_p(0))
     monkeypatch.setattr(w4, "_workspace", lambda need, like, dev, stream, handle: torch.empty(need, dtype=torch.uint8))
-    monkeypatch.setattr(w4, "_int_out", lambda shape, dtype, like, dev, stream, handle: torch.empty(shape, dtype=dtype))
+    monkeypatch.setattr(w4, "_small_out", lambda shape, dtype, like, dev, stream, handle: torch.empty(shape, dtype=dtype))
     return f
 
 
