@@ -672,7 +672,10 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3>::CTAS)
 // 2^(m_c - M) need maxima and sums alone, so the sums over partials are no
 // chain of dependent loads. SPLIT: the block's eight warps share one such
 // square's partials (few items, each over many CTAs); otherwise they stand side
-// by side along the row.
+// by side along the row. Bound by latency: counts, records, maxima and sums, and
+// outputs are loads that wait for one another. (One lane after the other reading
+// a row's maxima and sums: one 16-node tree over 8,191 keys 21.1 us, not 18.9;
+// five tokens over 131,071 keys 96 and not 91.)
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 
