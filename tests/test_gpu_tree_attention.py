@@ -262,6 +262,26 @@ def test_same_bits_every_time_and_in_a_graph(size, e4m3):
     check(s, out)
 
 
+@pytest.mark.parametrize("dim,size,heads", [(64, 1, 1), (128, 3, 4), (128, 20, 1), (128, 64, 3), (256, 30, 1)])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_one_item_over_every_share(dim, size, heads, e4m3):
+    """One kv head and a long context: more partial results than are joined at a time."""
+    s = Step([40000], [size], heads, 1, dim, 64, e4m3=e4m3, seed=dim + size)
+    check(s, run(s))
+
+
+def test_outputs_are_handed_out_once():
+    s = Step([40, 7], [1, 1], 8, 2, 64, 16)
+    outs, q = [], s.q.clone()
+    for i in range(70):  # small outputs are made some dozens at a time
+        s.q.copy_(q * (i + 1))
+        outs.append(run(s))
+    assert len({o.data_ptr() for o in outs}) == 70
+    for i in (0, 31, 32, 69):
+        s.q.copy_(q * (i + 1))
+        assert torch.equal(outs[i], run(s, out=torch.empty_like(outs[i])))
+
+
 def test_padding_tokens_are_left_alone():
     s = Step([20, 30], [2, 3], 4, 2, 64, 16, seed=6)
     want = run(s)
