@@ -26,8 +26,8 @@
 //  * e4m3 caches: codes become f16 exactly (one conversion per pair), q is
 //    scaled by a power of two per row so that its largest element is near 2^14
 //    and becomes f16 (elements below 2^-24 of the largest lose bits, no more
-//    than float32 sums lose anyway), and the weights, times 2^8, are f16 with
-//    11 bits.
+//    than float32 sums lose anyway), and the weights, times 2^15, are f16 with
+//    11 bits (down to 2^-29 of the maximum; smaller ones have fewer).
 //  * Only tiles that hold new tokens or the end of the context take the masked
 //    path. There, values that are not finite are zeroed in shared memory
 //    before the product (0 * NaN is NaN) and added at the end to the rows that
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3>::CTAS)
         base[i] = mn == -INFINITY ? 0.f : mn;
         alpha[i] = exp2_approx(m[i] - base[i]);
         m[i] = mn;
-        if (E4M3) base[i] -= 8.f;  // weights times 2^8: f16 keeps small ones better
+        if (E4M3) base[i] -= 15.f;  // weights times 2^15: f16 ends at 2^16, and loses bits below 2^-14
         l[i] *= alpha[i];
         lsum[2 * i] *= alpha[i];
       }

@@ -27,11 +27,14 @@
 // replaces S in TMEM and is the second MMA's A operand there; V, [key][dim] in
 // shared memory, is its B operand as it lies (MN-major). At dim 256 the output
 // takes half of TMEM, so there is one group, with two S buffers. An output
-// accumulator is rescaled only when a row's maximum has grown by more than 2^8:
-// until then the weights are up to 2^8, and the sums are float32.
+// accumulator is rescaled only when a row's maximum has grown by more than 2^8
+// (8-bit caches: 2^3): until then the weights are up to 2^8, and the sums are float32.
 //
-// P is rounded once (bf16: 2^-9 of a weight at most, against the output's own
-// 2^-9); sums use the unrounded weights.
+// P is rounded once; sums use the unrounded weights. bf16: 2^-8 of a weight at
+// most, as the output's own rounding. 8-bit caches: f16 times 2^12, so up to 2^15,
+// 2^-11 of a weight down to 2^-26 of the maximum: many keys far below one other
+// still count together. (Sums of the rounded weights cost registers: 16 rows of
+// 4,096 keys, dim 128, 64 query rows 69.1 us; so 64.0.)
 //
 // Measured, dim 128, bf16: 16 rows of 4,096 keys and 8 kv heads (268 MB) with 32,
 // 64 and 128 query rows per kv head 55, 58 and 63 us (4.9, 4.7, 4.4 TB/s); 4 rows
@@ -64,6 +67,9 @@ struct TcGeo {
   static constexpr int THREADS = E4M3 ? 512 : 384;
   static constexpr int STREAMS = DIM == 256 ? 1 : 2;  // softmax groups
   static constexpr int KT = tc_attn_keys(DIM);        // keys of a tile
+  // How far (powers of two) a row's maximum may pass the one that its weights count from, and what the weights are
+  // multiplied by: f16 ends at 2^16, and loses bits below 2^-14.
+  static constexpr float LAG = E4M3 ? 3.f : 8.f, WEIGHT_LOG2 = E4M3 ? 12.f : 0.f;
   static constexpr int CH = DIM / 64;                 // 128-byte columns of a row
   static constexpr int SUB = KT * 128;                // one column of a K or V tile
   static constexpr int SLOT = CH * SUB;
@@ -564,8 +570,7 @@ __global__ void __launch_bounds__(TcGeo<DIM, E4M3>::THREADS, 1)
               for (int k = 0; k < 4; ++k) t4[k] = fmaxf(fmaxf(t4[k], x[c][e + k]), x[c][e + 4 + k]);
           const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
           const float mn = fmaxf(m, __fmul_rn(top, factor));
-          // rescale when the maximum has grown by more than 2^8 (or was -inf); f16 weights end at 2^16
-          const bool grow = mn > m + 8.f;
+          const bool grow = mn > m + G::LAG;  // (or m was -inf)
           const bool first = i < (wide ? 1 : STREAMS);  // this group's first tile: no output yet
           if (__any_sync(0xFFFFFFFFu, grow)) {
             const float alpha = grow ? exp2_approx(m - mn) : 1.f;
@@ -588,19 +593,20 @@ __global__ void __launch_bounds__(TcGeo<DIM, E4M3>::THREADS, 1)
             }
           }
           // ---- weights, over the first half of S's columns
-          const float base = m == -INFINITY ? 0.f : m;
+          const float base = (m == -INFINITY ? 0.f : m) - G::WEIGHT_LOG2;
           const f32x2 scale2 = f32_pair(factor, factor), base2 = f32_pair(-base, -base);
+          f32x2 zero2;  // (not known to the compiler, which would make one fma of a product and a sum)
+          asm volatile("mov.b64 %0, 0;" : "=l"(zero2));
           f32x2 sum[2] = {f32_pair(0.f, 0.f), f32_pair(0.f, 0.f)};
 #pragma unroll
           for (int c = 0; c < KT / 32; ++c) {
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              // (8 bits: in two roundings, as the maximum was formed, so that its own weight is 1; a weight and the sums
-              // then agree where one key has it all, although f16 rounds the weights alone. The products are single ones:
-              // the compiler makes an fma of a packed product and sum.)
-              const float2 y = f32_halves(E4M3 ? add2(f32_pair(__fmul_rn(x[c][e], factor), __fmul_rn(x[c][e + 1], factor)), base2)
-                                               : fma2(f32_pair(x[c][e], x[c][e + 1]), scale2, base2));
+              // (8 bits: in two roundings, as the maximum was formed, so that its own weight is a power of two; it and the sums
+              // then agree where one key has it all, although f16 rounds the weights alone)
+              const f32x2 xx = f32_pair(x[c][e], x[c][e + 1]);
+              const float2 y = f32_halves(E4M3 ? add2(fma2(xx, scale2, zero2), base2) : fma2(xx, scale2, base2));
               const float a = exp2_approx(y.x), d = exp2_approx(y.y);
               sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], f32_pair(a, d));
               w[e >> 1] = E4M3 ? pack2_f16(a, d) : pack2(a, d);
