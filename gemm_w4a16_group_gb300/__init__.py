@@ -31,6 +31,7 @@ import ctypes
 import functools
 import os
 import struct as _struct
+import threading as _threading
 
 from . import build as _build
 
@@ -688,19 +689,26 @@ def _small_out(shape, dtype, like, dev, stream, handle):
 
 
 _workspaces = {}
+_KEPT = 8  # workspaces kept, of the streams that began to use one last
+# Held while a call takes the kept workspace and makes its launches: there are
+# two, and another host thread's on the same stream must not come between them.
+_kept_workspace = _threading.RLock()
 
 
 def _workspace(need, like, dev, stream, handle):
     """The scratch of calls that bring none: one buffer per device and stream,
-    used by one call after the other in the stream's order, and grown when a
-    call needs more. A call under capture gets a buffer of its own from the
-    graph's pool, which lives as long as the graph."""
+    used by one call after the other in the stream's order (the caller holds
+    _kept_workspace), and grown when a call needs more. A call under capture
+    gets a buffer of its own from the graph's pool, which lives as long as the
+    graph."""
     if _torch().cuda.is_current_stream_capturing():
         return _empty(need, _types().u8, like, stream)
     key = (dev, handle)
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < need:
         ws = _workspaces[key] = _empty(need, _types().u8, like, stream)
+        while len(_workspaces) > _KEPT:  # goes back to its stream's pool, behind the calls that use it
+            del _workspaces[next(iter(_workspaces))]
     return ws
 
 
@@ -793,7 +801,8 @@ def tree_attention(q, k_cache, v_cache, page_table, lengths, starts, mask, max_t
     that sees nothing gets 0; padding tokens (at starts[rows] and above) are
     left as they are in `out`. Without a `workspace` (uint8,
     tree_attention_workspace_bytes) the call uses one that the module keeps
-    for its stream."""
+    for its stream; a given one belongs to one call at a time (host threads
+    that share a stream need one each)."""
     ty, dev = _types(), _place(q, "q")
     cache, (_, _, kv_heads, _, dim) = _kv_cache(k_cache, v_cache, k_scale, v_scale, True, dev)
     qp, qt, qh, tokens, heads = _token_rows(q, "q", dim, dev)
@@ -802,9 +811,7 @@ def tree_attention(q, k_cache, v_cache, page_table, lengths, starts, mask, max_t
         raise W4A16Error(f"tree_attention: unsupported heads={heads} kv_heads={kv_heads} dim={dim} max_tree={max_tree}")
     table, rows, width = _table(page_table, dev)
     handle = _on(stream, q)
-    if workspace is None:
-        workspace = _workspace(need, q, dev, stream, handle.value)
-    elif workspace.dtype is not ty.u8 or workspace.get_device() != dev or not workspace.is_contiguous() or workspace.numel() < need:
+    if workspace is not None and (workspace.dtype is not ty.u8 or workspace.get_device() != dev or not workspace.is_contiguous() or workspace.numel() < need):
         _refuse(workspace, ty.u8, "workspace", dev, need)
     if out is None:
         # (the sizes of one or two tokens; a larger call is longer on the device than here)
@@ -812,11 +819,16 @@ def tree_attention(q, k_cache, v_cache, page_table, lengths, starts, mask, max_t
             out = _small_out((tokens, heads, dim), ty.bf16, q, dev, stream, handle.value)
         else:
             out = _empty((tokens, heads, dim), ty.bf16, q, stream)
-    rc = lib().w4a16_tree_attention(qp, qt, qh, cache, table, width, _flat(lengths, ty.i32, "lengths", rows, dev),
-                                    _flat(starts, ty.i32, "starts", rows + 1, dev),
-                                    None if mask is None else _flat(mask, ty.i64, "mask", tokens, dev), rows, tokens,
-                                    heads, max_tree, dim ** -0.5 if scale is None else scale,
-                                    _flat(out, ty.bf16, "out", tokens * heads * dim, dev), workspace.data_ptr(), handle)
+    args = (qp, qt, qh, cache, table, width, _flat(lengths, ty.i32, "lengths", rows, dev),
+            _flat(starts, ty.i32, "starts", rows + 1, dev), None if mask is None else _flat(mask, ty.i64, "mask", tokens, dev),
+            rows, tokens, heads, max_tree, dim ** -0.5 if scale is None else scale,
+            _flat(out, ty.bf16, "out", tokens * heads * dim, dev))
+    call = lib().w4a16_tree_attention
+    if workspace is not None:
+        rc = call(*args, workspace.data_ptr(), handle)
+    else:
+        with _kept_workspace:
+            rc = call(*args, _workspace(need, q, dev, stream, handle.value).data_ptr(), handle)
     _check(rc, "w4a16_tree_attention")
     return out
 

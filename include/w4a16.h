@@ -409,7 +409,9 @@ int w4a16_kv_append(const uint16_t *k, const uint16_t *v, int64_t k_token, int64
  *   max_tree   1 .. W4A16_MAX_TREE, at least every row's number of new tokens
  *   workspace  w4a16_tree_attention_workspace_bytes(heads, kv_heads, dim,
  *              max_tree) bytes, 256-byte aligned, used only while the call
- *              runs on `stream`; no content is kept or expected
+ *              runs on `stream`; no content is kept or expected. A call makes
+ *              up to two launches that share it: host threads that call at the
+ *              same time need one each, also on one stream
  *
  * Scores, softmax statistics and sums are float32. Results are bitwise
  * reproducible run to run on one device.
