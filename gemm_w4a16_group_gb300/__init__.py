@@ -662,6 +662,15 @@ def _empty(shape, dtype, like, stream):
         return _types().empty(shape, dtype=dtype, device=like.device)
 
 
+def _capturing(stream):
+    """Whether the call's stream (the current one if None) is being captured."""
+    cuda = _torch().cuda
+    if stream is None:
+        return cuda.is_current_stream_capturing()
+    with cuda.stream(stream):
+        return cuda.is_current_stream_capturing()
+
+
 _small_outputs = {}
 _SMALL, _AT_ONCE = 16384, 32  # bytes of a small output, how many are made at once
 
@@ -676,7 +685,7 @@ def _small_out(shape, dtype, like, dev, stream, handle):
     their common memory goes back to the stream's pool with the last of them.
     Under capture every output comes from the graph's pool."""
     torch = _torch()
-    if torch.cuda.is_current_stream_capturing():
+    if _capturing(stream):
         return _empty(shape, dtype, like, stream)
     key = (shape, dtype, dev, handle)
     try:
@@ -713,7 +722,7 @@ def _workspace(need, like, dev, stream, handle):
     _kept_workspace), and grown when a call needs more. A call under capture
     gets a buffer of its own from the graph's pool, which lives as long as the
     graph."""
-    if _torch().cuda.is_current_stream_capturing():
+    if _capturing(stream):
         return _empty(need, _types().u8, like, stream)
     key = (dev, handle)
     ws = _workspaces.get(key)

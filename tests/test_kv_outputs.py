@@ -100,3 +100,36 @@ def test_a_batch_that_another_thread_empties(monkeypatch):
         w4._small_outputs[key] = Emptied()
     second = out()
     assert second.data_ptr() != first.data_ptr() and second.shape == first.shape
+
+
+def test_the_stream_that_is_asked_about_capture(monkeypatch):
+    """A captured stream's buffers come from the graph, also when it is given to the call and another one is current."""
+    current, made = ["outer"], []
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            current.append(self.stream)
+
+        def __exit__(self, *a):
+            current.pop()
+
+    def empty(shape, dtype, like, stream):
+        made.append(stream)
+        return torch.empty(shape, dtype=dtype)
+
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: current[-1] == "captured")
+    monkeypatch.setattr(w4, "_empty", empty)
+    like = torch.zeros(1)
+    w4._workspaces.clear()
+    for _ in range(2):
+        assert w4._workspace(100, like, -1, "captured", 5).numel() == 100
+        assert w4._small_out((3,), torch.int32, like, -1, "captured", 5).untyped_storage().nbytes() == 12
+    assert made == ["captured"] * 4 and not w4._workspaces and not w4._small_outputs
+    w4._workspace(100, like, -1, "other", 6)
+    w4._small_out((3,), torch.int32, like, -1, "other", 6)
+    assert len(w4._workspaces) == len(w4._small_outputs) == 1
+    w4._workspaces.clear()

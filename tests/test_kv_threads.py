@@ -86,6 +86,7 @@ def test_a_given_workspace_waits_for_nobody(slow):
 
 def test_few_workspaces_are_kept(slow, monkeypatch):
     """One per stream, of the streams used last."""
+    monkeypatch.setattr(w4, "_capturing", lambda stream: False)
     monkeypatch.setattr(w4, "_empty", lambda shape, dtype, like, stream: torch.empty(shape, dtype=dtype))
     for stream in range(1, 101):
         attention(stream=stream)
