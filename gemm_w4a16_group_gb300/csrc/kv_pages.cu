@@ -61,7 +61,7 @@ __device__ __forceinline__ int owner_of(const int32_t *starts, int rows, int tok
 // append: a thread has one 16-byte chunk of one head in four tokens, all in
 // flight at once. Bound by HBM; in 8 bits nearly as much by the integer pipe,
 // which unpacks and converts: 25,446 tokens of 8 heads of 128 to e4m3 (156 MB)
-// 28.2 us, 5.5 TB/s (blocks of 256 threads 29.3 us, of 512 35.2; eight tokens a
+// 28.7 us, 5.4 TB/s (blocks of 256 threads 29.3 us, of 512 35.2; eight tokens a
 // thread 28.5).
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 128;
@@ -80,29 +80,31 @@ struct AppendParams {
 
 // Eight quotients x / s, correctly rounded, from r = 1 / s: x * r corrected
 // once by its residual (P. Markstein, "IA-64 and Elementary Functions", ch. 8).
-// r = 0 stands for a scale outside 2^-60 .. 2^60, where a residual could
-// underflow: those take the division. A quotient of 1,024 or more saturates
-// whatever its last bits, and its residual need not be finite: it stays as it
-// is.
+// The residual is formed as q * s - x and taken off: with x - q * s added, the
+// quotient of a negative zero would lose its sign. r = 0 stands for a scale
+// outside 2^-60 .. 2^60, where a residual could underflow; there, and where one
+// of the eight quotients is 1,024 or more (its residual need not be finite),
+// all eight take the division, which gives the same codes.
 __device__ __forceinline__ float2 divisor_of(float s) {
   return make_float2(s, s > 8.6736174e-19f && s < 1.1529215e18f ? __fdiv_rn(1.f, s) : 0.f);
 }
 __device__ __forceinline__ uint2 to_e4m3(const uint4 &x, const float2 &d) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  const f32x2 r2 = f32_pair(d.y, d.y), minus_s2 = f32_pair(-d.x, -d.x);
-  f32x2 f[4], q2[4];
+  const f32x2 minus_r2 = f32_pair(-d.y, -d.y), s2 = f32_pair(d.x, d.x);
+  f32x2 minus[4], q2[4];  // -x, x * r
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f[i] = f32_pair(bf16lo_to_f32(w[i]), bf16hi_to_f32(w[i]));
-    q2[i] = mul2(f[i], r2);
+    const uint32_t v = w[i] ^ 0x80008000u;
+    minus[i] = f32_pair(bf16lo_to_f32(v), bf16hi_to_f32(v));
+    q2[i] = mul2(minus[i], minus_r2);
     const float2 q = f32_halves(q2[i]);
     top = fmaxf(fmaxf(top, fabsf(q.x)), fabsf(q.y));
   }
   float2 q[4];
   if (d.y != 0.f && top < 1024.f) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = f32_halves(fma2(fma2(q2[i], minus_s2, f[i]), r2, q2[i]));
+    for (int i = 0; i < 4; ++i) q[i] = f32_halves(fma2(fma2(q2[i], s2, minus[i]), minus_r2, q2[i]));
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
