@@ -586,7 +586,9 @@ def dequantize(packed, N, K, group, sym, stream=None):
 
 
 # ---------------------------------------------------------------------------
-# Paged key/value cache and the attention of drafted token trees
+# Paged key/value cache and the attention of drafted token trees. A call with
+# nothing to do (no rows, no new tokens, no rows named) checks its arguments,
+# launches nothing, and its outputs say so.
 # ---------------------------------------------------------------------------
 MAX_TREE = 64     # new tokens of a sequence in one attention or acceptance call
 MAX_ROWS = 4096   # rows that one fork, free or reserve call may name
@@ -789,6 +791,14 @@ def _token_rows(t, name, dim, dev):
     return t.data_ptr(), s[0], s[1], shape[0], shape[1]
 
 
+def _fill(t, value, stream):
+    """`value` throughout an output of a call that has nothing to launch."""
+    if stream is None:
+        return t.fill_(value)
+    with _torch().cuda.stream(stream):
+        return t.fill_(value)
+
+
 def kv_append(k, v, k_cache, v_cache, page_table, lengths, starts, k_scale=None, v_scale=None, stream=None):
     """Write the new tokens' keys and values (bf16 [tokens, kv heads, dim],
     strided views allowed) behind each row's context: token starts[b] + i goes
@@ -802,8 +812,10 @@ def kv_append(k, v, k_cache, v_cache, page_table, lengths, starts, k_scale=None,
     if v_tokens != tokens or k_heads != heads or v_heads != heads:
         raise ValueError(f"k and v must both be [tokens, {heads}, {dim}], not {list(k.shape)} and {list(v.shape)}")
     table, rows, width = _table(page_table, dev)
-    rc = lib().w4a16_kv_append(kp, vp, kt, kh, vt, vh, cache, table, width, _flat(lengths, ty.i32, "lengths", rows, dev),
-                               _flat(starts, ty.i32, "starts", rows + 1, dev), rows, tokens, _on(stream, k))
+    lengths, starts = _flat(lengths, ty.i32, "lengths", rows, dev), _flat(starts, ty.i32, "starts", rows + 1, dev)
+    if rows == 0 or tokens == 0:
+        return
+    rc = lib().w4a16_kv_append(kp, vp, kt, kh, vt, vh, cache, table, width, lengths, starts, rows, tokens, _on(stream, k))
     _check(rc, "w4a16_kv_append")
 
 
@@ -844,6 +856,8 @@ def tree_attention(q, k_cache, v_cache, page_table, lengths, starts, mask, max_t
             _flat(starts, ty.i32, "starts", rows + 1, dev), None if mask is None else _flat(mask, ty.i64, "mask", tokens, dev),
             rows, tokens, heads, max_tree, dim ** -0.5 if scale is None else scale,
             _flat(out, ty.bf16, "out", tokens * heads * dim, dev))
+    if rows == 0 or tokens == 0:
+        return out
     call = lib().w4a16_tree_attention
     if workspace is not None:
         rc = call(*args, workspace.data_ptr(), handle)
@@ -869,13 +883,15 @@ def tree_accept(target, draft, mask, starts, max_tree, path=None, count=None, to
         count = _small_out((rows,), ty.i32, target, dev, stream, handle.value)
     if token is None:
         token = _small_out((rows,), ty.i64, target, dev, stream, handle.value)
-    rc = lib().w4a16_tree_accept(_flat(target, ty.i64, "target", tokens, dev), _flat(draft, ty.i64, "draft", tokens, dev),
-                                 None if mask is None else _flat(mask, ty.i64, "mask", tokens, dev),
-                                 _flat(starts, ty.i32, "starts", rows + 1, dev), rows, tokens, max_tree,
-                                 _flat(path, ty.i32, "path", rows * max_tree, dev),
-                                 _flat(count, ty.i32, "count", rows, dev), _flat(token, ty.i64, "token", rows, dev),
-                                 handle)
-    _check(rc, "w4a16_tree_accept")
+    args = (_flat(target, ty.i64, "target", tokens, dev), _flat(draft, ty.i64, "draft", tokens, dev),
+            None if mask is None else _flat(mask, ty.i64, "mask", tokens, dev),
+            _flat(starts, ty.i32, "starts", rows + 1, dev), rows, tokens, max_tree,
+            _flat(path, ty.i32, "path", rows * max_tree, dev), _flat(count, ty.i32, "count", rows, dev),
+            _flat(token, ty.i64, "token", rows, dev), handle)
+    if rows == 0 or tokens == 0:
+        _check(0 if 1 <= max_tree <= MAX_TREE else -1, "w4a16_tree_accept")
+        return _fill(path, -1, stream), _fill(count, 0, stream), _fill(token, -1, stream)
+    _check(lib().w4a16_tree_accept(*args), "w4a16_tree_accept")
     return path, count, token
 
 
@@ -893,11 +909,11 @@ def kv_compact(k_cache, v_cache, page_table, lengths, path, count, lengths_out=N
     handle = _on(stream, k_cache)
     if lengths_out is None:
         lengths_out = _small_out((rows,), ty.i32, k_cache, dev, stream, handle.value)
-    rc = lib().w4a16_kv_compact(cache, table, width, _flat(lengths, ty.i32, "lengths", rows, dev),
-                                _flat(path, ty.i32, "path", rows * max_tree, dev),
-                                _flat(count, ty.i32, "count", rows, dev), rows, max_tree,
-                                _flat(lengths_out, ty.i32, "lengths_out", rows, dev), handle)
-    _check(rc, "w4a16_kv_compact")
+    args = (cache, table, width, _flat(lengths, ty.i32, "lengths", rows, dev),
+            _flat(path, ty.i32, "path", rows * max_tree, dev), _flat(count, ty.i32, "count", rows, dev), rows, max_tree,
+            _flat(lengths_out, ty.i32, "lengths_out", rows, dev), handle)
+    if rows:
+        _check(lib().w4a16_kv_compact(*args), "w4a16_kv_compact")
     return lengths_out
 
 
@@ -908,10 +924,10 @@ def kv_free(page_table, lengths, refs, rows, stream=None):
     i32, dev = _types().i32, _place(page_table, "page_table")
     table, table_rows, width = _table(page_table, dev)
     pages, n = refs.numel(), rows.numel()
-    rc = lib().w4a16_kv_free(table, width, table_rows, _flat(lengths, i32, "lengths", table_rows, dev),
-                             _flat(refs, i32, "refs", pages, dev), pages, _flat(rows, i32, "rows", n, dev), n,
-                             _on(stream, page_table))
-    _check(rc, "w4a16_kv_free")
+    args = (table, width, table_rows, _flat(lengths, i32, "lengths", table_rows, dev), _flat(refs, i32, "refs", pages, dev),
+            pages, _flat(rows, i32, "rows", n, dev), n, _on(stream, page_table))
+    if n:
+        _check(lib().w4a16_kv_free(*args), "w4a16_kv_free")
 
 
 def kv_fork(k_cache, v_cache, page_table, lengths, refs, src, dst, ok=None, stream=None):
@@ -927,10 +943,12 @@ def kv_fork(k_cache, v_cache, page_table, lengths, refs, src, dst, ok=None, stre
     if ok is None:
         ok = _small_out((1,), i32, page_table, dev, stream, handle.value)
     n = src.numel()
-    rc = lib().w4a16_kv_fork(cache, table, width, table_rows, _flat(lengths, i32, "lengths", table_rows, dev),
-                             _flat(refs, i32, "refs", shape[1], dev), _flat(src, i32, "src", n, dev),
-                             _flat(dst, i32, "dst", n, dev), n, _flat(ok, i32, "ok", 1, dev), handle)
-    _check(rc, "w4a16_kv_fork")
+    args = (cache, table, width, table_rows, _flat(lengths, i32, "lengths", table_rows, dev),
+            _flat(refs, i32, "refs", shape[1], dev), _flat(src, i32, "src", n, dev), _flat(dst, i32, "dst", n, dev), n,
+            _flat(ok, i32, "ok", 1, dev), handle)
+    if n == 0:
+        return _fill(ok, 1, stream)
+    _check(lib().w4a16_kv_fork(*args), "w4a16_kv_fork")
     return ok
 
 
@@ -945,10 +963,12 @@ def kv_reserve(page_table, refs, rows, want, page_rows, ok=None, stream=None):
     if ok is None:
         ok = _small_out((1,), i32, page_table, dev, stream, handle.value)
     n, pages = rows.numel(), refs.numel()
-    rc = lib().w4a16_kv_reserve(table, width, table_rows, _flat(refs, i32, "refs", pages, dev), pages, page_rows,
-                                _flat(rows, i32, "rows", n, dev), _flat(want, i32, "want", n, dev), n,
-                                _flat(ok, i32, "ok", 1, dev), handle)
-    _check(rc, "w4a16_kv_reserve")
+    args = (table, width, table_rows, _flat(refs, i32, "refs", pages, dev), pages, page_rows,
+            _flat(rows, i32, "rows", n, dev), _flat(want, i32, "want", n, dev), n, _flat(ok, i32, "ok", 1, dev), handle)
+    if n == 0:
+        _check(0 if page_rows in (16, 32, 64, 128, 256) else -1, "w4a16_kv_reserve")
+        return _fill(ok, 1, stream)
+    _check(lib().w4a16_kv_reserve(*args), "w4a16_kv_reserve")
     return ok
 
 

@@ -348,7 +348,8 @@ int w4a16_dequantize_affine_bits(const void *packed, int N, int K, int group, in
  *               the row's number of new tokens and above are ignored
  *   refs        int32 [pages]            how many rows hold each page; 0 = free
  * New token i of row b has position lengths[b] + i; position p is row
- * p % page_rows of page page_table[b][p / page_rows].
+ * p % page_rows of page page_table[b][p / page_rows]. rows, tokens and n are
+ * at least 1: a caller with nothing to do makes no call.
  *
  * What only the device can see is checked there: a page id outside the
  * cache, a position past the table, starts that descend or exceed max_tree,
