@@ -1,5 +1,6 @@
 """Attention over a paged cache where the softmax weights lie far apart: many
-keys that only count together, maxima that keep growing. Against float64."""
+keys that only count together, maxima that keep growing, weights that round
+badly. Against float64."""
 import math
 
 import numpy as np
@@ -75,3 +76,27 @@ def test_a_maximum_that_keeps_growing_in_eight_bits(dim, size, every, rise):
     ref, mag = s.attention(scale=1.0)
     err = (run(s, scale=1.0) - ref).abs() / attention_bound(ref, mag)
     assert err.max() <= 1, f"{float(err.max())} of the bound"
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("keys", [400, 3000])
+def test_sixteen_bits_of_a_weight(dim, keys):
+    """One query row per head of a bf16 cache: weights keep 16 bits. All but one are just under half way between two
+    bf16 numbers, so that one part alone would be off by nearly 2^-8, all the same way. The output's own rounding is
+    2^-8; two parts, float32 scores, exponentials and sums stay below 2^-12."""
+    a = (128 + torch.arange(128)).double() / 128  # bf16 in [1, 2)
+    weight = torch.exp(-(a[:, None] * a[None, :]) / 4)  # k = -a / 4, q = a
+    over = weight * 2.0 ** -torch.floor(torch.log2(weight)) - 1  # mantissa
+    best = int((((over * 128) % 1 - 0.48).abs() + over).argmin())  # an ulp is 2^-7; a mantissa near 1 loses most
+    qa, ka = float(a[best // 128]), -float(a[best % 128]) / 4
+    s = Step([keys - 1], [1], 4, 2, dim, 64, seed=dim)
+    ids, rows = s.slots(0, keys)
+    heavy = (torch.arange(keys, device="cuda") == 5)[:, None, None]
+    put(s.k, ids, rows, torch.where(heavy, 0.0, ka).expand(-1, 1, dim))
+    v = torch.rand((1, 2, dim), generator=torch.Generator().manual_seed(3)).cuda() + 0.5
+    put(s.v, ids, rows, torch.where(heavy, 0.0, v))
+    s.q.zero_()
+    s.q[:, :, 0] = qa
+    ref, mag = s.attention(scale=1.0)
+    err = (run(s, scale=1.0) - ref).abs()
+    assert (err <= 2.0 ** -8 * ref.abs() + 2.0 ** -12 * mag).all()
