@@ -21,8 +21,9 @@
 //    with a maximum, sums and outputs of its own; they meet at the end of an
 //    item, through shared memory.
 //  * bf16 caches: products of bf16 are exact in float32; the weights e^(s - m)
-//    go into the second product as two bf16 parts (hi + lo, 16 bits of
-//    mantissa), which the tensor cores have time for.
+//    go into the second product as two bf16 parts (hi + lo, 15 bits of
+//    mantissa; neither is negative, and neither is 0 where the weight is not, so
+//    an infinite value stays infinite), which the tensor cores have time for.
 //  * e4m3 caches: codes become f16 exactly (one conversion per pair), q is
 //    scaled by a power of two per row so that its largest element is near 2^14
 //    and becomes f16 (elements below 2^-24 of the largest lose bits, no more
@@ -113,6 +114,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t *>(&b);
+}
+// The lower parts of two weights whose upper ones are `hi` (cut off, so that these are not negative), at least 2^-24 of
+// them: where a weight is above 0 both parts are, and an infinite value gives infinity in both products.
+__device__ __forceinline__ uint32_t low_part(uint32_t lo, uint32_t hi) {
+  const __nv_bfloat162 least = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&hi), __float2bfloat162_rn(5.9604645e-8f));
+  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162 *>(&lo), least);
+  return *reinterpret_cast<const uint32_t *>(&r);
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   __half2 h = __floats2half2_rn(lo, hi);
@@ -511,8 +519,8 @@ __global__ void __launch_bounds__(kThreads, RowsGeo<DIM, E4M3>::CTAS)
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const float x = s[n + (u >> 1)][2 * (u & 1)], y = s[n + (u >> 1)][2 * (u & 1) + 1];
-            hi[u] = pack_bf16(x, y);
-            lo[u] = pack_bf16(x - bf16lo_to_f32(hi[u]), y - bf16hi_to_f32(hi[u]));
+            hi[u] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);  // the upper halves
+            lo[u] = low_part(pack_bf16(x - bf16lo_to_f32(hi[u]), y - bf16hi_to_f32(hi[u])), hi[u]);
           }
 #pragma unroll
           for (int cc = 0; cc < DIM / 16; ++cc) {

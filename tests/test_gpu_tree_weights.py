@@ -100,3 +100,27 @@ def test_sixteen_bits_of_a_weight(dim, keys):
     ref, mag = s.attention(scale=1.0)
     err = (run(s, scale=1.0) - ref).abs()
     assert (err <= 2.0 ** -8 * ref.abs() + 2.0 ** -12 * mag).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("size", [1, 4, 20, 64])
+@pytest.mark.parametrize("keys", [300, 3000])
+def test_values_of_the_context_that_are_not_finite(dim, size, keys):
+    """Every token sees them, with a weight above 0: an infinite value makes its element infinite, a NaN or two
+    infinities of either sign make it NaN, and the other elements are as they were."""
+    s = Step([keys - size], [size], 4, 2, dim, 32, seed=dim + size)
+    ref, mag = s.attention()
+    ids, rows = s.slots(0, keys)
+    s.v[ids[7], :, rows[7], 3] = math.inf
+    s.v[ids[150], :, rows[150], 5] = -math.inf
+    s.v[ids[150], :, rows[150], 9] = math.inf
+    s.v[ids[201], :, rows[201], 9] = -math.inf
+    s.v[ids[keys - size - 1], :, rows[keys - size - 1], 11] = -math.inf  # in the tile that ends the context
+    s.v[ids[77], :, rows[77], 20] = math.nan
+    out = run(s)
+    assert torch.isposinf(out[..., 3]).all()
+    assert torch.isneginf(out[..., 5]).all() and torch.isneginf(out[..., 11]).all()
+    assert torch.isnan(out[..., 9]).all() and torch.isnan(out[..., 20]).all()
+    rest = torch.ones(dim, dtype=torch.bool)
+    rest[[3, 5, 9, 11, 20]] = False
+    assert ((out - ref).abs() <= attention_bound(ref, mag))[..., rest].all()
