@@ -10,9 +10,9 @@
 // head (one token of any model, a few tokens of small head groups), and the
 // kernel that joins partial results; tree_attn_tc.cu has more rows. 16 rows
 // against the whole cache are bound by HBM: every key and value is read once.
-// Measured against the copy peak of 6.78 TB/s: bf16 6.34 TB/s at 64 rows of
-// 4,096 keys (dim 64, 128 and 256 alike), e4m3 5.5 TB/s (the conversions take
-// half of the integer pipe).
+// Measured against the copy peak of 6.78 TB/s: bf16 6.2 TB/s at 64 rows of
+// 4,096 keys (dim 256: 6.5), e4m3 5.5 TB/s (the conversions take half of the
+// integer pipe).
 //
 //  * 4 computing warps and a copying warp. A stage is 64 or 128 keys: the
 //    copying warp's lanes each fetch one box (up to a page's rows by 128 bytes)
@@ -838,8 +838,8 @@ cudaError_t launch_tc(const AttnCall &c, AttnParams &p) {
 }
 // The tcgen05 kernel from 17 query rows per kv head on: its MMAs take 128 rows
 // in the time of one. (When this file still had 32- and 64-row forms: 16
-// sequences of 32 rows 63 us here, 53 there; 64 rows 121 and 57; 8-bit caches
-// 77 and 63, 133 and 66.)
+// sequences of 32 rows 63 us here, 55 there; 64 rows 121 and 57; 8-bit caches
+// 77 and 61, 133 and 64.)
 bool uses_tc(int rows) { return rows > 16; }
 
 template <int DIM, bool E4M3>

@@ -37,8 +37,9 @@
 // 4,096 keys, dim 128, 64 query rows 69.1 us; so 64.0.)
 //
 // Measured, dim 128, bf16: 16 rows of 4,096 keys and 8 kv heads (268 MB) with 32,
-// 64 and 128 query rows per kv head 55, 58 and 63 us (4.9, 4.7, 4.4 TB/s); 4 rows
-// of 16,384 keys with 256 75 us, 920 TFLOP/s. A wide tile takes some 3,500 clocks:
+// 64 and 128 query rows per kv head 55, 57 and 61 us (4.9, 4.8, 4.6 TB/s); 4 rows
+// of 16,384 keys with 256 72 us, 950 TFLOP/s; 8-bit caches 61 and 64 us with 32 and
+// 64 query rows, 101 with 256 (converting bounds them). A wide tile takes some 3,500 clocks:
 // a group's chain is 1,300 for its two products, 1,550 for its softmax and its
 // stores, and 600 of waiting for the other's turn and of handing over. (Handing P
 // over in two halves: 2 % slower. Fetching the next item's Q by a warp of its own
