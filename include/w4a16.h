@@ -414,8 +414,11 @@ int w4a16_kv_append(const uint16_t *k, const uint16_t *v, int64_t k_token, int64
  *              up to two launches that share it: host threads that call at the
  *              same time need one each, also on one stream
  *
- * Scores, softmax statistics and sums are float32. Results are bitwise
- * reproducible run to run on one device.
+ * Scores, softmax statistics and sums are float32; a weight e^(s - max) is
+ * rounded once, to 2^-8 of itself or better. Over an E4M3 cache that holds for
+ * weights down to 2^-26 of the row's largest; below, a weight is off by up to
+ * 2^-37 of the largest. Results are bitwise reproducible run to run on one
+ * device.
  */
 size_t w4a16_tree_attention_workspace_bytes(int heads, int kv_heads, int dim, int max_tree);
 int w4a16_tree_attention(const uint16_t *q, int64_t q_token, int64_t q_head, const w4a16_kv_cache *cache,

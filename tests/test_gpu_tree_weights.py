@@ -80,8 +80,8 @@ def test_a_maximum_that_keeps_growing_in_eight_bits(dim, size, every, rise):
 
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("keys", [400, 3000])
-def test_sixteen_bits_of_a_weight(dim, keys):
-    """One query row per head of a bf16 cache: weights keep 16 bits. All but one are just under half way between two
+def test_both_parts_of_a_weight(dim, keys):
+    """One query row per head of a bf16 cache: weights keep 15 bits, in two parts. All but one are just under half way between two
     bf16 numbers, so that one part alone would be off by nearly 2^-8, all the same way. The output's own rounding is
     2^-8; two parts, float32 scores, exponentials and sums stay below 2^-12."""
     a = (128 + torch.arange(128)).double() / 128  # bf16 in [1, 2)
