@@ -119,7 +119,8 @@ def _logits(gen, tokens, vocab):
     """A head's logits: a broad bulk, and a few dozen tokens that stand out."""
     x = torch.randn((tokens, vocab), generator=gen, device="cuda").mul_(2.0)
     few = torch.randint(0, vocab, (tokens, 40), generator=gen, device="cuda")
-    return x.scatter_(1, few, 9.0 + 3.0 * torch.randn((tokens, 40), generator=gen, device="cuda"))
+    # (amax: a token may be chosen twice, and the inputs go by the seed alone)
+    return x.scatter_reduce_(1, few, 9.0 + 3.0 * torch.randn((tokens, 40), generator=gen, device="cuda"), "amax")
 
 
 def _cuda(a):
