@@ -24,6 +24,12 @@ The rest of a verify step of drafted token trees over a paged key/value cache
     o = tree_attention(q, k_cache, v_cache, table, lengths, starts, mask, max_tree)
     path, count, token = tree_accept(target, draft, mask, starts, max_tree)
     lengths = kv_compact(k_layers, v_layers, table, lengths, path, count)
+
+For users who sample, and users with an adapter of their own:
+
+    y = lora_add(gemm(x, ...), x, a, b, adapter, starts)           # behind any product
+    p = probabilities(logits, temperature)                         # float32, of the head's logits
+    path, count, token = tree_sample(p, q, draft, mask, starts, u, max_tree)
 """
 from __future__ import annotations
 
@@ -45,6 +51,7 @@ __all__ = [
     "affine_bits_scratch_bytes", "gemm_affine_bits", "dequantize_affine_bits",
     "MAX_TREE", "MAX_ROWS", "kv_append", "tree_attention_workspace_bytes", "tree_attention", "tree_accept", "kv_compact",
     "kv_free", "kv_fork", "kv_reserve",
+    "MAX_ADAPTERS", "MAX_RANK", "probabilities", "tree_sample", "lora_workspace_bytes", "lora_add",
 ]
 
 # symbols declared in include/w4a16.h
@@ -58,6 +65,7 @@ EXPORTS = (
     "w4a16_affine_bits_scratch_bytes", "w4a16_gemm_affine_bits", "w4a16_dequantize_affine_bits",
     "w4a16_kv_append", "w4a16_tree_attention_workspace_bytes", "w4a16_tree_attention", "w4a16_tree_accept",
     "w4a16_kv_compact", "w4a16_kv_free", "w4a16_kv_fork", "w4a16_kv_reserve",
+    "w4a16_probabilities", "w4a16_tree_sample", "w4a16_lora_workspace_bytes", "w4a16_lora_add",
 )
 KERNEL_AUTO, KERNEL_GEMV, KERNEL_SMALLM, KERNEL_TC, KERNEL_XSTAGED, KERNEL_DECODE_TC = 0, 1, 2, 3, 4, 5
 # the `sym` argument: 0 zero points, 1 symmetric (z = 8), AFFINE scale * q + bias
@@ -161,6 +169,15 @@ def lib(auto_build: bool = True) -> ctypes.CDLL:
     L.w4a16_kv_fork.restype = i32
     L.w4a16_kv_reserve.argtypes = [P, i32, i32, P, i32, i32, P, P, i32, P, P]
     L.w4a16_kv_reserve.restype = i32
+    L.w4a16_probabilities.argtypes = [P, i64, P, P, i32, i32, P, P]
+    L.w4a16_probabilities.restype = i32
+    L.w4a16_tree_sample.argtypes = [P, i64, P, i64, i32, P, P, P, P, i32, i32, i32, P, P, P, P]
+    L.w4a16_tree_sample.restype = i32
+    L.w4a16_lora_workspace_bytes.argtypes = [i32, i32, i32]
+    L.w4a16_lora_workspace_bytes.restype = sz
+    L.w4a16_lora_add.argtypes = [P, i64, P, i64, P, i64, i64, P, i64, i64, P, P, P, i32, i32, i32, i32, i32, i32, P, i64,
+                                 P, P]
+    L.w4a16_lora_add.restype = i32
     _lib = L
     return L
 
@@ -895,6 +912,72 @@ def tree_accept(target, draft, mask, starts, max_tree, path=None, count=None, to
     return path, count, token
 
 
+def _matrix(t, dtype, name, dev):
+    """Pointer, row stride and sizes of a 2-D tensor whose last axis is contiguous."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, dtype, name, dev)
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have two axes, not {list(shape)}")
+    row, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    return t.data_ptr(), row, shape[0], shape[1]
+
+
+def probabilities(logits, temperature=None, floor=None, out=None, stream=None):
+    """float32 [tokens, vocab]: softmax of the bf16 logits [tokens, vocab]
+    (rows may be strided), each row at its temperature (float32 [tokens];
+    None: 1; 0 or less: 1 at the first maximum) and over its logits >= floor
+    (float32 [tokens], e.g. the last of topk's values; None: all)."""
+    ty, dev = _types(), _place(logits, "logits")
+    lp, row, tokens, vocab = _matrix(logits, ty.bf16, "logits", dev)
+    tp = None if temperature is None else _flat(temperature, ty.f32, "temperature", tokens, dev)
+    fp = None if floor is None else _flat(floor, ty.f32, "floor", tokens, dev)
+    if out is None:
+        out = _empty((tokens, vocab), ty.f32, logits, stream)
+    op = _flat(out, ty.f32, "out", tokens * vocab, dev)
+    if tokens == 0 or vocab == 0:
+        return out
+    _check(lib().w4a16_probabilities(lp, row, tp, fp, tokens, vocab, op, _on(stream, logits)), "w4a16_probabilities")
+    return out
+
+
+def tree_sample(p, q, draft, mask, starts, u, max_tree, path=None, count=None, token=None, stream=None):
+    """Sampled acceptance down each row's draft tree: p and q float32 [tokens,
+    vocab], the target's and the drafter's probabilities after each token (rows
+    may be strided; q None: the drafter picked its tokens without chance), u
+    float32 [tokens] random numbers in [0, 1), draft, mask and starts as in
+    tree_accept. Returns (path, count, token) as tree_accept does, token drawn
+    from what the refused children leave of p; accepted tokens and the drawn one
+    are distributed as sampled from p one by one."""
+    ty, dev = _types(), _place(p, "p")
+    pp, p_row, tokens, vocab = _matrix(p, ty.f32, "p", dev)
+    qp, q_row = None, 0
+    if q is not None:
+        qp, q_row, *shape = _matrix(q, ty.f32, "q", dev)
+        if shape != [tokens, vocab]:
+            raise ValueError(f"q has shape {shape}, p {[tokens, vocab]}")
+    rows = starts.numel() - 1
+    handle = _on(stream, p)
+    if path is None:
+        path = _small_out((rows, max_tree), ty.i32, p, dev, stream, handle.value)
+    if count is None:
+        count = _small_out((rows,), ty.i32, p, dev, stream, handle.value)
+    if token is None:
+        token = _small_out((rows,), ty.i64, p, dev, stream, handle.value)
+    args = (pp, p_row, qp, q_row, vocab, _flat(draft, ty.i64, "draft", tokens, dev),
+            None if mask is None else _flat(mask, ty.i64, "mask", tokens, dev),
+            _flat(starts, ty.i32, "starts", rows + 1, dev), _flat(u, ty.f32, "u", tokens, dev), rows, tokens, max_tree,
+            _flat(path, ty.i32, "path", rows * max_tree, dev), _flat(count, ty.i32, "count", rows, dev),
+            _flat(token, ty.i64, "token", rows, dev), handle)
+    if rows == 0 or tokens == 0:
+        _check(0 if 1 <= max_tree <= MAX_TREE else -1, "w4a16_tree_sample")
+        return _fill(path, -1, stream), _fill(count, 0, stream), _fill(token, -1, stream)
+    _check(lib().w4a16_tree_sample(*args), "w4a16_tree_sample")
+    return path, count, token
+
+
 def kv_compact(k_cache, v_cache, page_table, lengths, path, count, lengths_out=None, stream=None):
     """Move the accepted rows together in every layer of the cache ([layers,]
     pages, kv heads, page rows, dim): position lengths[b] + path[b, i] to
@@ -970,6 +1053,86 @@ def kv_reserve(page_table, refs, rows, want, page_rows, ok=None, stream=None):
         return _fill(ok, 1, stream)
     _check(lib().w4a16_kv_reserve(*args), "w4a16_kv_reserve")
     return ok
+
+
+# ---------------------------------------------------------------------------
+# Low-rank adapters of many requests beside a shared product
+# ---------------------------------------------------------------------------
+MAX_ADAPTERS = 4096  # in one store
+MAX_RANK = 128
+
+
+@functools.lru_cache(maxsize=1024)
+def lora_workspace_bytes(tokens: int, rank: int, inner: int) -> int:
+    return int(lib().w4a16_lora_workspace_bytes(tokens, rank, inner))
+
+
+def _store(t, name, dev):
+    """Pointer, strides and shape of a bf16 [adapters, ., .] tensor whose last axis is contiguous."""
+    if t.dtype is not _types().bf16 or t.get_device() != dev:
+        _refuse(t, _types().bf16, name, dev)
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must have three axes, not {list(shape)}")
+    s = t.stride()
+    if s[2] != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    return t.data_ptr(), s[0], s[1], shape
+
+
+def lora_add(y, x, a, b, adapter, starts=None, scale=None, out=None, workspace=None, stream=None):
+    """bf16 [tokens, outer]: y + scale[e] * (x . a[e]^T) . b[e]^T for every
+    token, e the adapter of its row; y where that is -1. y [tokens, outer] and x
+    [tokens, inner] bf16 (rows may be strided), a bf16 [adapters, rank, inner],
+    b bf16 [adapters, outer, rank] (rank a multiple of 8 up to MAX_RANK), adapter
+    int32 [rows], starts int32 [rows + 1] as in tree_attention (None: every token
+    is a row), scale float32 [adapters] (None: 1). `out` may be y itself; padding
+    tokens (at starts[rows] and above) are left as they are in it. Without a
+    `workspace` (uint8, lora_workspace_bytes) the call uses one that the module
+    keeps for its stream; a given one belongs to one call at a time."""
+    ty, dev = _types(), _place(y, "y")
+    yp, y_row, tokens, outer = _matrix(y, ty.bf16, "y", dev)
+    xp, x_row, x_tokens, inner = _matrix(x, ty.bf16, "x", dev)
+    ap, a_adapter, a_row, (adapters, rank, a_inner) = _store(a, "a", dev)
+    bp, b_adapter, b_row, b_shape = _store(b, "b", dev)
+    if x_tokens != tokens or a_inner != inner or b_shape != (adapters, outer, rank):
+        raise ValueError(f"shapes do not fit: y {list(y.shape)}, x {list(x.shape)}, a {list(a.shape)}, b {list(b_shape)}")
+    rows = adapter.numel()
+    if starts is None and rows != tokens:
+        raise ValueError(f"adapter has {rows} elements, without starts the call needs {tokens}")
+    if rows and tokens:
+        need = lora_workspace_bytes(tokens, rank, inner)
+        if need == 0:
+            raise W4A16Error(f"lora_add: unsupported tokens={tokens} rank={rank} inner={inner}")
+    handle = _on(stream, y)
+    if out is None:
+        # (as in tree_attention)
+        if 2 * tokens * outer <= _SMALL:
+            out = _small_out((tokens, outer), ty.bf16, y, dev, stream, handle.value)
+        else:
+            out = _empty((tokens, outer), ty.bf16, y, stream)
+        op, out_row = out.data_ptr(), outer
+    else:
+        op, out_row, *shape = _matrix(out, ty.bf16, "out", dev)
+        if shape != [tokens, outer]:
+            raise ValueError(f"out has shape {shape}, y {[tokens, outer]}")
+    args = (yp, y_row, xp, x_row, ap, a_adapter, a_row, bp, b_adapter, b_row,
+            None if scale is None else _flat(scale, ty.f32, "scale", adapters, dev),
+            _flat(adapter, ty.i32, "adapter", rows, dev),
+            None if starts is None else _flat(starts, ty.i32, "starts", rows + 1, dev), rows, tokens, adapters, rank, inner,
+            outer, op, out_row)
+    if rows == 0 or tokens == 0:
+        return out
+    call = lib().w4a16_lora_add
+    if workspace is not None:
+        if workspace.dtype is not ty.u8 or workspace.get_device() != dev or not workspace.is_contiguous() or workspace.numel() < need:
+            _refuse(workspace, ty.u8, "workspace", dev, need)
+        rc = call(*args, workspace.data_ptr(), handle)
+    else:
+        with _kept_workspace:
+            rc = call(*args, _workspace(need, y, dev, stream, handle.value).data_ptr(), handle)
+    _check(rc, "w4a16_lora_add")
+    return out
 
 
 def kernel_status() -> int:

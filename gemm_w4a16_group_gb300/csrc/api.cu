@@ -144,6 +144,25 @@ int page_shift_of(int page_rows) {
   return -1;
 }
 
+// ---- adapters ----
+bool lora_sizes_ok(int rank, int inner) {
+  return rank >= 8 && rank <= W4A16_MAX_RANK && rank % 8 == 0 && tokens_ok(inner) && inner % 8 == 0;
+}
+
+// Rows of `n` elements read at y and written at out: the same ones, or none
+// in common (other buffers, or other columns of one). Rows whose strides
+// differ must not lie in one range.
+bool rows_apart(const uint16_t *y, int64_t y_row, const uint16_t *out, int64_t out_row, int tokens, int n) {
+  const int64_t lim = int64_t(1) << 40;
+  if (y_row >= lim || out_row >= lim) return false;
+  const int64_t d = (reinterpret_cast<intptr_t>(out) - reinterpret_cast<intptr_t>(y)) / 2;
+  if (d == 0 && (y_row == out_row || tokens == 1)) return true;
+  if (d >= y_row * (tokens - 1) + n || -d >= out_row * (tokens - 1) + n) return true;
+  if (y_row != out_row || y_row == 0) return false;
+  const int64_t at = (d % y_row + y_row) % y_row;
+  return at >= n && y_row - at >= n;
+}
+
 // No two elements of one side share an address: taken by ascending stride,
 // each dimension steps past all that the smaller ones cover.
 bool side_disjoint(int64_t dim, int64_t row, int64_t rows, int64_t head, int64_t heads, int64_t page, int64_t pages,
@@ -604,6 +623,98 @@ int w4a16_tree_accept(const int64_t *target, const int64_t *draft, const int64_t
   if (st != W4A16_OK) return st;
   return finish_launch(launch_tree_accept(target, draft, mask, starts, rows, tokens, max_tree, path, count, token,
                                           d.err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int w4a16_probabilities(const uint16_t *logits, int64_t logits_row, const float *temperature, const float *floor,
+                        int tokens, int vocab, float *out, w4a16_stream_t stream) {
+  if (!logits || !out) return W4A16_ERR_INVALID_ARG;
+  if (!tokens_ok(tokens) || !tokens_ok(vocab) || logits_row < 0) return W4A16_ERR_INVALID_ARG;
+  if (!aligned(logits, 2) || !aligned(temperature, 4) || !aligned(floor, 4) || !aligned(out, 4))
+    return W4A16_ERR_MISALIGNED;
+  DeviceInfo d;
+  int st = current_device(d);
+  if (st != W4A16_OK) return st;
+  return finish_launch(launch_probabilities(logits, logits_row, temperature, floor, tokens, vocab, out, d.device,
+                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int w4a16_tree_sample(const float *p, int64_t p_row, const float *q, int64_t q_row, int vocab, const int64_t *draft,
+                      const int64_t *mask, const int32_t *starts, const float *u, int rows, int tokens, int max_tree,
+                      int32_t *path, int32_t *count, int64_t *token, w4a16_stream_t stream) {
+  if (!p || !draft || !starts || !u || !path || !count || !token) return W4A16_ERR_INVALID_ARG;
+  if (!rows_ok(rows, 1) || !tokens_ok(tokens) || !tokens_ok(vocab) || max_tree < 1 || max_tree > W4A16_MAX_TREE)
+    return W4A16_ERR_INVALID_ARG;
+  if (p_row < 0 || q_row < 0) return W4A16_ERR_INVALID_ARG;
+  if (!aligned(p, 4) || !aligned(q, 4) || !aligned(draft, 8) || !aligned(mask, 8) || !aligned(starts, 4) ||
+      !aligned(u, 4) || !aligned(path, 4) || !aligned(count, 4) || !aligned(token, 8))
+    return W4A16_ERR_MISALIGNED;
+  DeviceInfo d;
+  int st = current_device(d);
+  if (st != W4A16_OK) return st;
+  return finish_launch(launch_tree_sample(SampleCall{p, q, p_row, q ? q_row : 0, draft, mask, starts, u, rows, tokens,
+                                                     vocab, max_tree, path, count, token, d.err, d.device,
+                                                     reinterpret_cast<cudaStream_t>(stream)}));
+}
+
+size_t w4a16_lora_workspace_bytes(int tokens, int rank, int inner) {
+  if (!tokens_ok(tokens) || !lora_sizes_ok(rank, inner)) return 0;
+  return lora_workspace_bytes(tokens, rank, inner);
+}
+
+int w4a16_lora_add(const uint16_t *y, int64_t y_row, const uint16_t *x, int64_t x_row, const uint16_t *a,
+                   int64_t a_adapter, int64_t a_row, const uint16_t *b, int64_t b_adapter, int64_t b_row,
+                   const float *scale, const int32_t *adapter, const int32_t *starts, int rows, int tokens,
+                   int adapters, int rank, int inner, int outer, uint16_t *out, int64_t out_row, void *workspace,
+                   w4a16_stream_t stream) {
+  if (!y || !x || !a || !b || !adapter || !out || !workspace) return W4A16_ERR_INVALID_ARG;
+  if (!tokens_ok(tokens) || !tokens_ok(outer) || !lora_sizes_ok(rank, inner)) return W4A16_ERR_INVALID_ARG;
+  if (adapters < 1 || adapters > W4A16_MAX_ADAPTERS) return W4A16_ERR_INVALID_ARG;
+  if (starts ? rows < 1 || rows > W4A16_MAX_SEQUENCES : rows != tokens) return W4A16_ERR_INVALID_ARG;
+  if (tokens == 1) y_row = x_row = out_row = 0;  // (a stride that takes no step)
+  if (adapters == 1) a_adapter = b_adapter = 0;
+  if (outer == 1) b_row = 0;
+  const int64_t strides[] = {y_row, x_row, a_adapter, a_row, b_adapter, b_row, out_row};
+  for (int64_t s : strides)
+    if (s < 0) return W4A16_ERR_INVALID_ARG;
+  if (tokens > 1 && out_row < outer) return W4A16_ERR_INVALID_ARG;
+  if (!rows_apart(y, y_row, out, out_row, tokens, outer)) return W4A16_ERR_INVALID_ARG;
+  const int64_t wide[] = {x_row, a_adapter, a_row, b_adapter, b_row};
+  for (int64_t s : wide)
+    if (!stride_ok(s, 2)) return W4A16_ERR_MISALIGNED;
+  if (!aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(workspace, 256) || !aligned(y, 2) ||
+      !aligned(out, 2) || !aligned(scale, 4) || !aligned(adapter, 4) || !aligned(starts, 4))
+    return W4A16_ERR_MISALIGNED;
+  DeviceInfo d;
+  int st = current_device(d);
+  if (st != W4A16_OK) return st;
+  LoraCall c;
+  c.y = y;
+  c.x = x;
+  c.a = a;
+  c.b = b;
+  c.y_row = y_row;
+  c.x_row = x_row;
+  c.a_adapter = a_adapter;
+  c.a_row = a_row;
+  c.b_adapter = b_adapter;
+  c.b_row = b_row;
+  c.out_row = out_row;
+  c.scale = scale;
+  c.adapter = adapter;
+  c.starts = starts;
+  c.rows = rows;
+  c.tokens = tokens;
+  c.adapters = adapters;
+  c.rank = rank;
+  c.inner = inner;
+  c.outer = outer;
+  c.out = out;
+  c.workspace = static_cast<float *>(workspace);
+  c.err = d.err;
+  c.device = d.device;
+  c.sm_count = d.sm_count;
+  c.stream = reinterpret_cast<cudaStream_t>(stream);
+  return finish_launch(launch_lora_add(c));
 }
 
 int w4a16_kv_compact(const w4a16_kv_cache *cache, const int32_t *page_table, int max_pages, const int32_t *lengths,

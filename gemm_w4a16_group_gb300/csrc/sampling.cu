@@ -1,0 +1,646 @@
+// Sampled decoding after the output head: the probabilities of bf16 logits,
+// and the walk down a draft tree by two distributions and given random numbers
+// (the sampled form of the greedy tree_accept, kv_pages.cu).
+//
+// A row of the vocabulary belongs to one cluster of CTAs, each with a slice of
+// it; they exchange a few words through distributed shared memory. Both
+// kernels are bound by HBM where there are many rows, and by launch, loads that
+// depend on one another and the cluster's barriers where there is one.
+#include "w4a16_internal.h"
+
+namespace w4a16 {
+namespace {
+
+constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr int kMaxCluster = 16;
+
+// The halves of a cluster barrier: what a CTA does between them need not wait
+// for the others.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// A row of `n` elements seen in quads: quad k holds elements 4k - shift .. +3,
+// so that whole quads are aligned wherever the row begins. [lo, hi) are the
+// quads of part `i` of `parts`.
+struct Quads {
+  int shift, lo, hi;
+};
+__device__ __forceinline__ Quads quads_of(int n, int shift, uint32_t i, uint32_t parts) {
+  const long long all = (shift + (long long)n + 3) / 4;
+  return {shift, (int)(all * i / parts), (int)(all * (i + 1) / parts)};
+}
+
+// ---------------------------------------------------------------------------
+// probabilities: p_j = 2^((l_j - m) a) / sum_i 2^((l_i - m) a), a = log2(e) / T.
+// One pass: a thread holds its 32 logits' powers, relative to their own
+// maximum, in registers while the cluster agrees on maximum and sum. Slices
+// that do not fit are read twice.
+// ---------------------------------------------------------------------------
+constexpr int kProbThreads = 512;
+constexpr int kProbQuads = 8;  // of a thread
+constexpr uint32_t kNone = 0xFF80u;  // bf16 -inf: no probability
+
+struct ProbParams {
+  const uint16_t *logits;
+  long long row;  // elements from one row of logits to the next
+  const float *temperature, *floor;
+  float *out;
+  int vocab;
+};
+
+// log2(e) / T in two parts, so that the exponent of a small probability, which
+// is large, keeps its fraction: 2^y with y rounded to 24 bits would be off by
+// up to 2^-24 |y|.
+struct Power {
+  float hi, lo;
+  __device__ explicit Power(float t) {
+    const float high = 1.44269502f, low = 1.92596299e-8f;  // log2(e)
+    hi = fminf(__fdiv_rn(high, t), 1e30f);
+    lo = hi < 1e30f && t < 1e30f ? __fdiv_rn(fmaf(-hi, t, high) + low, t) : 0.f;
+  }
+  // e^(d / T) for d <= 0; 0 below 2^-152
+  __device__ __forceinline__ float operator()(float d) const {
+    const float y = d * hi;
+    const float rest = fmaf(d, hi, -y) + d * lo;
+    float r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(y));
+    r = fmaf(r, rest * 0.69314718f, r);
+    return y < -152.f ? 0.f : r;
+  }
+};
+
+// Four logits of the row, two to a word; kNone past its ends and below the floor.
+template <bool ALIGNED>
+__device__ __forceinline__ uint2 load_quad(const uint16_t *row, int k, int shift, int n, float floor) {
+  const int j = 4 * k - shift;
+  uint2 w;
+  if (ALIGNED && j >= 0 && j + 4 <= n) {
+    w = *reinterpret_cast<const uint2 *>(row + j);
+  } else {
+    uint32_t x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = j + i >= 0 && j + i < n ? row[j + i] : kNone;
+    w = make_uint2(x[0] | x[1] << 16, x[2] | x[3] << 16);
+  }
+  if (floor > -INFINITY) {
+    uint32_t *v = &w.x;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (bf16lo_to_f32(v[i]) < floor) v[i] = (v[i] & 0xFFFF0000u) | kNone;
+      if (bf16hi_to_f32(v[i]) < floor) v[i] = (v[i] & 0xFFFFu) | kNone << 16;
+    }
+  }
+  return w;
+}
+__device__ __forceinline__ float at(const uint2 &w, int i) {
+  const uint32_t v = i < 2 ? w.x : w.y;
+  return i & 1 ? bf16hi_to_f32(v) : bf16lo_to_f32(v);
+}
+template <bool ALIGNED>
+__device__ __forceinline__ void store_quad(float *row, int k, int shift, int n, const float (&v)[4]) {
+  const int j = 4 * k - shift;
+  if (ALIGNED && j >= 0 && j + 4 <= n) {
+    *reinterpret_cast<float4 *>(row + j) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (j + i >= 0 && j + i < n) row[j + i] = v[i];
+  }
+}
+
+// (maximum, sum of powers relative to it), joined
+__device__ __forceinline__ void join(float &m, float &s, float m2, float s2, const Power &pw) {
+  const float top = fmaxf(m, m2);
+  // (an empty part, m = -inf and s = 0, adds nothing, at an infinite temperature too)
+  s = (m == top || s == 0.f ? s : s * pw(m - top)) + (m2 == top || s2 == 0.f ? s2 : s2 * pw(m2 - top));
+  m = top;
+}
+
+__device__ __forceinline__ unsigned long long key_max(unsigned long long a, unsigned long long b) { return a > b ? a : b; }
+
+template <bool ALIGNED>
+__global__ void __launch_bounds__(kProbThreads, 2) probabilities_kernel(const ProbParams p) {
+  __shared__ unsigned long long slots[kMaxCluster], warps[kProbThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t S = cluster_nctarank(), rank = cluster_ctarank();
+  const long long r = cluster_id_x();
+  cluster_arrive();  // (a slot is written once its CTA runs)
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  const uint16_t *row = p.logits + r * p.row;
+  float *out = p.out + r * p.vocab;
+  const Quads q = quads_of(p.vocab, ALIGNED ? (int)(r * p.vocab & 3) : 0, rank, S);
+  const bool one = q.hi - q.lo <= kProbThreads * kProbQuads;  // each thread's logits stay in registers
+  const float t = p.temperature ? p.temperature[r] : 1.f, floor = p.floor ? p.floor[r] : -INFINITY;
+
+  if (!(t > 0.f)) {  // the first maximum has it all
+    unsigned long long best = 0;
+    for (int k = q.lo + tid; k < q.hi; k += kProbThreads) {
+      const uint2 w = load_quad<ALIGNED>(row, k, q.shift, p.vocab, floor);
+      const uint32_t x[4] = {w.x & 0xFFFFu, w.x >> 16, w.y & 0xFFFFu, w.y >> 16};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (x[i] != kNone) best = key_max(best, argmax_key(x[i], 4 * k - q.shift + i));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) best = key_max(best, __shfl_xor_sync(kFull, best, o));
+    if (lane == 0) warps[warp] = best;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kProbThreads / 32; ++w) best = key_max(best, warps[w]);
+    cluster_wait();
+    if (tid < (int)S) st_cluster_u64(mapa_shared(smem_u32(&slots[rank]), tid), best);
+    cluster_sync_all();
+    best = 0;
+    for (uint32_t i = 0; i < S; ++i) best = key_max(best, slots[i]);
+    const int first = best ? (int)(0xFFFFFFFFu - (uint32_t)best) : -1;
+    for (int k = q.lo + tid; k < q.hi; k += kProbThreads) {
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = first >= 0 && 4 * k - q.shift + i == first ? 1.f : 0.f;
+      store_quad<ALIGNED>(out, k, q.shift, p.vocab, v);
+    }
+    return;
+  }
+
+  const Power pw(t);
+  float e[kProbQuads][4], m = -INFINITY, s = 0.f;
+  for (int k0 = q.lo; k0 < q.hi; k0 += kProbThreads * kProbQuads) {
+    uint2 x[kProbQuads];
+#pragma unroll
+    for (int u = 0; u < kProbQuads; ++u) {
+      const int k = k0 + u * kProbThreads + tid;
+      x[u] = k < q.hi ? load_quad<ALIGNED>(row, k, q.shift, p.vocab, floor) : make_uint2(kNone * 0x10001u, kNone * 0x10001u);
+    }
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int u = 0; u < kProbQuads; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, at(x[u], i));  // (a NaN comes back in the sum)
+#pragma unroll
+    for (int u = 0; u < kProbQuads; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float l = at(x[u], i);
+        e[u][i] = l == -INFINITY ? 0.f : pw(l - top);
+        sum += e[u][i];
+      }
+    join(m, s, top, sum, pw);
+  }
+  const float mine = m;  // what e is relative to, where there is one chunk
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) join(m, s, __shfl_xor_sync(kFull, m, o), __shfl_xor_sync(kFull, s, o), pw);
+  if (lane == 0) warps[warp] = f32_pair(m, s);
+  __syncthreads();
+  if (warp == 0) {
+    const float2 v = lane < kProbThreads / 32 ? f32_halves(warps[lane]) : make_float2(-INFINITY, 0.f);
+    m = v.x;
+    s = v.y;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) join(m, s, __shfl_xor_sync(kFull, m, o), __shfl_xor_sync(kFull, s, o), pw);
+  }
+  cluster_wait();
+  if (tid < (int)S) st_cluster_u64(mapa_shared(smem_u32(&slots[rank]), tid), f32_pair(m, s));
+  cluster_sync_all();
+  m = -INFINITY;
+  s = 0.f;
+  for (uint32_t i = 0; i < S; ++i) {
+    const float2 v = f32_halves(slots[i]);
+    join(m, s, v.x, v.y, pw);
+  }
+  const float inv = s == 0.f ? 0.f : __fdiv_rn(1.f, s);
+  if (one) {
+    const float f = mine == m ? inv : mine == -INFINITY ? 0.f : inv * pw(mine - m);
+#pragma unroll
+    for (int u = 0; u < kProbQuads; ++u) {
+      const int k = q.lo + u * kProbThreads + tid;
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = e[u][i] * f;
+      if (k < q.hi) store_quad<ALIGNED>(out, k, q.shift, p.vocab, v);
+    }
+    return;
+  }
+  for (int k = q.lo + tid; k < q.hi; k += kProbThreads) {
+    const uint2 w = load_quad<ALIGNED>(row, k, q.shift, p.vocab, floor);
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float l = at(w, i);
+      v[i] = l == -INFINITY ? 0.f : pw(l - m) * inv;
+    }
+    store_quad<ALIGNED>(out, k, q.shift, p.vocab, v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// sampled acceptance. Children of a node come from the drafter's distribution q
+// at it. After k of them were refused, what is left of the target's p is
+//
+//   r_k = max(p - c_k q, 0) / S_k,  S_k = sum max(p - c_k q, 0),
+//   c_0 = 0, S_0 = 1,  c_{k+1} = c_k + S_k
+//
+// (max(r_k - q, 0), normalised, is r_{k+1}), so that a refusal costs one pass
+// over two rows, and nothing is written back. Child x with random number u is
+// accepted where u q(x) < r_k(x); with none left, the token is drawn from r_k
+// by the root's number. Children that were picked, not drawn (no q), have q = 1
+// at themselves: a refused one's probability is taken out.
+//
+// Sums are fixed point, 2^-56 in 64-bit integers: they do not depend on the
+// order, and the token drawn is the one that 64-bit floats give, also where the
+// number falls next to one of 248,320 borders (32-bit sums are off by 1e-7,
+// which moves it in one draw of a hundred).
+// ---------------------------------------------------------------------------
+constexpr int kSampleThreads = 512;
+constexpr int kSampleWarps = kSampleThreads / 32;
+constexpr int kFrac = 56;
+constexpr unsigned long long kOne = 1ull << kFrac;
+
+using u64 = unsigned long long;
+
+struct SampleParams {
+  const float *p, *q;  // q null: children that were picked
+  long long p_row, q_row;
+  const int64_t *draft, *mask;
+  const int32_t *starts;
+  const float *u;
+  int rows, tokens, vocab, max_tree;
+  int32_t *path, *count;
+  int64_t *token;
+  int *err;
+};
+
+enum { kDone = 0, kSum = 1, kDraw = 2 };
+
+// What the first CTA of a cluster tells the others to do next
+struct Order {
+  u64 c;
+  int what, row, gone;  // row: of p and q; gone: children taken out
+  float u;
+  int ids[kMaxTree];
+};
+
+struct SampleSmem {
+  Order order;
+  u64 sums[kMaxCluster], warps[kSampleWarps];
+  // first CTA: nodes of the tree
+  u64 kids[kMaxTree];
+  double px[kMaxTree], qx[kMaxTree];
+  float u[kMaxTree];
+  int ids[kMaxTree], path[kMaxTree];
+  int accepted;
+};
+
+__device__ __forceinline__ float sound(float p) { return fminf(fmaxf(p, 0.f), 1.f); }  // (NaN: 0)
+__device__ __forceinline__ u64 fixed(float p) { return __float2ull_rz(sound(p) * 72057594037927936.f); }
+
+// max(p - c q, 0)
+__device__ __forceinline__ u64 weight(float p, float q, u64 c) {
+  const u64 a = fixed(p), b = fixed(q);
+  const u64 t = c == kOne ? b : 2 * __umul64hi(b << (63 - kFrac), c);
+  return a > t ? a - t : 0;
+}
+
+template <bool ALIGNED>
+__device__ __forceinline__ void load_floats(const float *row, int k, int shift, int n, float (&x)[4]) {
+  const int j = 4 * k - shift;
+  if (ALIGNED && j >= 0 && j + 4 <= n) {
+    const float4 v = *reinterpret_cast<const float4 *>(row + j);
+    x[0] = v.x;
+    x[1] = v.y;
+    x[2] = v.z;
+    x[3] = v.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = j + i >= 0 && j + i < n ? row[j + i] : 0.f;
+  }
+}
+
+// The walk, as far as it gets without another sum over the vocabulary (one
+// thread of the first CTA; what it decides the others follow).
+struct Walk {
+  u64 c, total;  // of the node that it stands on; total: the sum that `order` asked for
+  u64 kids;
+  int node, asked, gone;
+  bool known;  // total belongs to c
+
+  __device__ void stand(int i, const SampleSmem &sm) {
+    node = i;
+    kids = sm.kids[i];
+    c = 0;
+    asked = gone = 0;
+    known = false;
+  }
+  __device__ void go(SampleSmem &sm, bool drawn, int first) {
+    Order &o = sm.order;
+    o.row = first + node;
+    while (kids) {
+      if (asked && !known) {
+        o.what = kSum;
+        o.c = c;
+        o.gone = 0;
+        return;
+      }
+      const int i = __ffsll((long long)kids) - 1;
+      kids &= kids - 1;
+      const double left = asked ? (double)total * 0x1p-56 : 1.0;
+      double r = sm.px[i];
+      if (drawn) r -= (double)c * 0x1p-56 * sm.qx[i];
+      for (int g = 0; g < gone; ++g)
+        if (o.ids[g] == sm.ids[i]) r = 0;
+      if ((double)sm.u[i] * sm.qx[i] * left < r) {
+        sm.path[sm.accepted++] = i;
+        stand(i, sm);
+        o.row = first + node;
+        continue;
+      }
+      if (drawn) {
+        c += asked ? total : kOne;
+        known = false;
+      } else {
+        bool twin = false;
+        for (int g = 0; g < gone; ++g) twin |= o.ids[g] == sm.ids[i];
+        if (!twin) {
+          o.ids[gone++] = sm.ids[i];
+          if (known) total -= min(total, fixed((float)sm.px[i]));
+        }
+      }
+      ++asked;
+    }
+    o.what = kDraw;
+    o.c = c;
+    o.gone = gone;
+  }
+  // the sum that was asked for
+  __device__ void learn(u64 sum, const SampleSmem &sm) {
+    total = sum;
+    for (int g = 0; g < gone; ++g) {
+      // (taken out one by one; px of a removed id is that of the child that was refused)
+      for (int i = 0; i < kMaxTree; ++i)
+        if (sm.kids[node] >> i & 1 && sm.ids[i] == sm.order.ids[g]) {
+          total -= min(total, fixed((float)sm.px[i]));
+          break;
+        }
+    }
+    known = true;
+  }
+};
+
+template <bool ALIGNED>
+__global__ void __launch_bounds__(kSampleThreads, 2) tree_sample_kernel(const SampleParams p) {
+  __shared__ SampleSmem sm;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t S = cluster_nctarank(), rank = cluster_ctarank();
+  const int b = cluster_id_x();
+  cluster_arrive();
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const bool drawn = p.q != nullptr;
+  Walk walk;
+  int n = 0, s0 = 0;
+  if (rank == 0) {
+    s0 = p.starts[b];
+    const int s1 = p.starts[b + 1];
+    n = s1 - s0;
+    if (s0 < 0 || n < 0 || n > p.max_tree || s1 > p.tokens) {
+      if (tid == 0) atomicOr(p.err, kErrIndex);
+      n = 0;
+    }
+    if (tid < kMaxTree) sm.kids[tid] = 0;
+    if (tid == 0) {
+      sm.accepted = 0;
+      sm.path[0] = 0;
+    }
+    __syncthreads();
+    if (tid < n) {
+      const u64 word = p.mask ? (u64)p.mask[s0 + tid] : ~0ull;
+      const u64 above = word & ((1ull << tid) - 1);
+      const int parent = above ? 63 - __clzll((long long)above) : -1;
+      sm.u[tid] = p.u[s0 + tid];
+      if (parent >= 0) {
+        const int64_t id = p.draft[s0 + tid];
+        if (id >= 0 && id < p.vocab) {
+          sm.ids[tid] = (int)id;
+          sm.px[tid] = sound(p.p[(s0 + parent) * p.p_row + id]);
+          sm.qx[tid] = drawn ? sound(p.q[(s0 + parent) * p.q_row + id]) : 1.0;
+          atomicOr(&sm.kids[parent], 1ull << tid);
+        } else {
+          atomicOr(p.err, kErrIndex);
+        }
+      }
+    }
+    __syncthreads();
+    if (tid == 0) {
+      sm.order.what = kDone;
+      if (n > 0) {
+        sm.accepted = 1;
+        sm.order.u = sm.u[0];
+        walk.stand(0, sm);
+        walk.go(sm, drawn, s0);
+      }
+    }
+  }
+  cluster_wait();
+  int64_t none = -1;
+  for (;;) {
+    if (rank == 0) {
+      __syncthreads();
+      const uint32_t words = sizeof(Order) / 4;
+      const uint32_t used = offsetof(Order, ids) / 4 + (sm.order.what == kDraw ? sm.order.gone : 0);
+      for (uint32_t i = tid; i < used * S; i += kSampleThreads) {
+        const uint32_t to = i / used, w = i % used;
+        if (to && w < words)
+          st_cluster_u32(mapa_shared(smem_u32(&sm.order) + 4 * w, to), reinterpret_cast<const uint32_t *>(&sm.order)[w]);
+      }
+    }
+    cluster_sync_all();
+    const int what = sm.order.what, row = sm.order.row, gone = sm.order.gone;
+    const u64 c = sm.order.c;
+    if (what == kDone) break;
+
+    // this warp's part of the row
+    const float *pr = p.p + row * p.p_row, *qr = p.q + row * p.q_row;
+    const int shift = ALIGNED ? (int)((row * p.p_row) & 3) : 0;
+    const Quads mine = quads_of(p.vocab, shift, rank * kSampleWarps + warp, S * kSampleWarps);
+    u64 sum = 0;
+    if (c == 0) {
+#pragma unroll 4
+      for (int k = mine.lo + lane; k < mine.hi; k += 32) {
+        float x[4];
+        load_floats<ALIGNED>(pr, k, shift, p.vocab, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum += fixed(x[i]);
+      }
+    } else {
+#pragma unroll 4
+      for (int k = mine.lo + lane; k < mine.hi; k += 32) {
+        float x[4], y[4];
+        load_floats<ALIGNED>(pr, k, shift, p.vocab, x);
+        load_floats<ALIGNED>(qr, k, shift, p.vocab, y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum += weight(x[i], y[i], c);
+      }
+    }
+    for (int g = lane; g < gone; g += 32) {
+      const int id = sm.order.ids[g], k = (id + shift) >> 2;
+      if (k >= mine.lo && k < mine.hi) sum -= fixed(pr[id]);  // (of the warp's sum; a lane's own may wrap)
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    if (lane == 0) sm.warps[warp] = sum;
+    __syncthreads();
+    if (tid < (int)S) {
+      u64 all = 0;
+#pragma unroll
+      for (int w = 0; w < kSampleWarps; ++w) all += sm.warps[w];
+      st_cluster_u64(mapa_shared(smem_u32(&sm.sums[rank]), tid), all);
+    }
+    const float u = sm.order.u;
+    cluster_sync_all();
+    u64 total = 0, before = 0;
+    for (uint32_t i = 0; i < S; ++i) {
+      if (i == rank) before = total;
+      total += sm.sums[i];
+    }
+    if (what == kSum) {
+      if (rank == 0 && tid == 0) {
+        walk.learn(total, sm);
+        walk.go(sm, drawn, s0);
+      }
+      continue;
+    }
+    if (total == 0) {  // nothing is left: p itself; nothing there either: no token
+      if (c == 0 && gone == 0) break;
+      if (rank == 0 && tid == 0) {
+        sm.order.c = 0;
+        sm.order.gone = 0;
+      }
+      continue;
+    }
+    none = 0;
+    // the first element at which the running sum passes u * total
+    const u64 goal = __umul64hi(total, __float2ull_rz(fminf(fmaxf(u, 0.f), 0.99999994f) * 18446744073709551616.f));
+    u64 run = before;
+    for (int w = 0; w < warp; ++w) run += sm.warps[w];
+    if (goal < run || goal - run >= sm.warps[warp]) break;
+    for (int k0 = mine.lo; k0 < mine.hi; k0 += 32) {
+      const int k = k0 + lane;
+      float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+      if (k < mine.hi) {
+        load_floats<ALIGNED>(pr, k, shift, p.vocab, x);
+        if (c) load_floats<ALIGNED>(qr, k, shift, p.vocab, y);
+      }
+      u64 part[4], four = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        part[i] = c ? weight(x[i], y[i], c) : fixed(x[i]);
+        for (int g = 0; g < gone; ++g)
+          if (sm.order.ids[g] == 4 * k - shift + i) part[i] = 0;
+        four += part[i];
+      }
+      u64 upto = four;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const u64 t = __shfl_up_sync(kFull, upto, o);
+        if (lane >= o) upto += t;
+      }
+      const uint32_t past = __ballot_sync(kFull, run + upto > goal);
+      if (past) {
+        if (lane == __ffs(past) - 1) {
+          u64 v = run + upto - four;
+          int i = 0;
+          while (i < 3 && v + part[i] <= goal) v += part[i++];
+          p.token[b] = 4 * k - shift + i;
+        }
+        break;
+      }
+      run += __shfl_sync(kFull, upto, 31);
+    }
+    break;
+  }
+  if (rank == 0) {
+    if (tid < p.max_tree) p.path[(long long)b * p.max_tree + tid] = tid < sm.accepted ? sm.path[tid] : -1;
+    if (tid == 0) {
+      p.count[b] = sm.accepted;
+      if (none) p.token[b] = -1;
+    }
+  }
+}
+
+// `rows` clusters of up to `want` CTAs (a power of two up to 16; 8 where
+// clusters of 16 do not fit)
+template <class P>
+cudaError_t launch_rows(void (*kern)(P), PerDevice &fits16, int rows, int want, int threads, int device,
+                        cudaStream_t stream, const P &params) {
+  if (want == kMaxCluster) {
+    int f = fits16.v[device].load(std::memory_order_relaxed);
+    if (f == 0) {
+      f = -1;
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
+        cudaLaunchConfig_t lc = {};
+        lc.gridDim = dim3(kMaxCluster, 1, 1);
+        lc.blockDim = dim3(threads, 1, 1);
+        cudaLaunchAttribute a;
+        a.id = cudaLaunchAttributeClusterDimension;
+        a.val.clusterDim.x = kMaxCluster;
+        a.val.clusterDim.y = 1;
+        a.val.clusterDim.z = 1;
+        lc.attrs = &a;
+        lc.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &lc) == cudaSuccess && n >= 1) f = 1;
+      }
+      (void)cudaGetLastError();
+      fits16.v[device].store(f, std::memory_order_relaxed);
+    }
+    if (f < 0) want = 8;
+  }
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)(rows * want), 1, 1);
+  lc.blockDim = dim3(threads, 1, 1);
+  lc.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = want;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 2;
+  return cudaLaunchKernelEx(&lc, kern, params);
+}
+
+// CTAs for a row: a power of two that leaves each about `least` elements
+int ctas_of(int vocab, int least) {
+  int s = 1;
+  while (s < kMaxCluster && vocab >= 2LL * least * s) s *= 2;
+  return s;
+}
+
+bool address(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+}  // namespace
+
+cudaError_t launch_probabilities(const uint16_t *logits, long long row, const float *temperature, const float *floor,
+                                 int tokens, int vocab, float *out, int device, cudaStream_t stream) {
+  static PerDevice fits[2];
+  // quads of logits and of probabilities are aligned together
+  const bool aligned = address(logits, 8) && address(out, 16) && (row - vocab) % 4 == 0;
+  const ProbParams p{logits, row, temperature, floor, out, vocab};
+  const int s = ctas_of(vocab, 8192);
+  return launch_rows(aligned ? probabilities_kernel<true> : probabilities_kernel<false>, fits[aligned], tokens, s,
+                     kProbThreads, device, stream, p);
+}
+
+cudaError_t launch_tree_sample(const SampleCall &c) {
+  static PerDevice fits[2];
+  const bool aligned = address(c.p, 16) && address(c.q, 16) && (!c.q || (c.q_row - c.p_row) % 4 == 0);
+  const SampleParams p{c.p, c.q, c.p_row, c.q_row, c.draft, c.mask, c.starts, c.u, c.rows, c.tokens, c.vocab, c.max_tree,
+                       c.path, c.count, c.token, c.err};
+  return launch_rows(aligned ? tree_sample_kernel<true> : tree_sample_kernel<false>, fits[aligned], c.rows,
+                     ctas_of(c.vocab, 4096), kSampleThreads, c.device, c.stream, p);
+}
+
+}  // namespace w4a16

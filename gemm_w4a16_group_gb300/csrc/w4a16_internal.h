@@ -157,6 +157,41 @@ struct AttnCall {
   int device, sm_count;
   cudaStream_t stream;
 };
+// float32 probabilities [tokens][vocab] of bf16 logits
+cudaError_t launch_probabilities(const uint16_t *logits, long long row, const float *temperature, const float *floor,
+                                 int tokens, int vocab, float *out, int device, cudaStream_t stream);
+
+struct SampleCall {
+  const float *p, *q;  // q null: picked children
+  long long p_row, q_row;  // elements
+  const int64_t *draft, *mask;
+  const int32_t *starts;
+  const float *u;
+  int rows, tokens, vocab, max_tree;
+  int32_t *path, *count;
+  int64_t *token;
+  int *err;
+  int device;
+  cudaStream_t stream;
+};
+cudaError_t launch_tree_sample(const SampleCall &c);
+
+// Low-rank adapters beside a product
+struct LoraCall {
+  const uint16_t *y, *x, *a, *b;
+  long long y_row, x_row, a_adapter, a_row, b_adapter, b_row, out_row;  // elements
+  const float *scale;  // or null: 1
+  const int32_t *adapter, *starts;  // starts null: a token a row
+  int rows, tokens, adapters, rank, inner, outer;
+  uint16_t *out;
+  float *workspace;
+  int *err;
+  int device, sm_count;
+  cudaStream_t stream;
+};
+size_t lora_workspace_bytes(int tokens, int rank, int inner);
+cudaError_t launch_lora_add(const LoraCall &c);
+
 size_t tree_attn_workspace_bytes(int heads, int kv_heads, int dim, int max_tree);
 cudaError_t launch_tree_attention(const AttnCall &c);
 

@@ -443,6 +443,57 @@ int w4a16_tree_accept(const int64_t *target, const int64_t *draft, const int64_t
                       w4a16_stream_t stream);
 
 /*
+ * Probabilities of the head's logits: out[t][j] (float32 [tokens][vocab],
+ * row-major) = e^(l_j / T) / sum_i e^(l_i / T), over the logits of row t that are
+ * not below its floor; the others get 0.
+ *
+ *   logits       bf16, element (t, j) at t * logits_row + j
+ *   temperature  float32 [tokens], or NULL: 1. A row with T <= 0 (or NaN) is
+ *                greedy: 1 at the first maximum, as w4a16_gemm_argmax, else 0
+ *   floor        float32 [tokens] (the last of the row's top-k values, w4a16_topk;
+ *                or its maximum + T * log(share)), or NULL: none
+ *
+ * A row with nothing above -inf gets 0 throughout; a NaN (or +inf) that is kept
+ * makes the row's kept probabilities NaN. Relative error below 2^-20 of each
+ * probability, small ones too.
+ */
+int w4a16_probabilities(const uint16_t *logits, int64_t logits_row, const float *temperature, const float *floor,
+                        int tokens, int vocab, float *out, w4a16_stream_t stream);
+
+/*
+ * Sampled acceptance: w4a16_tree_accept for a target that samples. p and q are
+ * the target's and the drafter's probabilities after each token (float32,
+ * element (t, j) at t * p_row + j; 0 <= p, q <= 1, a row's sum below 128). The
+ * children of a node were drawn from q at it, each on its own; q NULL: they were
+ * picked without chance (the likeliest tokens, a lookup). From node 0 (always
+ * accepted) the walk asks the children of the node it stands on, lowest first:
+ *
+ *   child x is accepted where u[x] * q(x) * S < max(p(x) - c * q(x), 0); the walk
+ *   goes on from there. c = 0 and S = 1 for the first child; a refusal makes
+ *   c += S, S = sum_j max(p_j - c * q_j, 0)
+ *   (q NULL: q is 1 at the child alone. A refused child's probability is taken
+ *   out of p, S is the sum of the rest, and the same token again is refused.)
+ *
+ * At the end the token is drawn from what is left there, w_j = max(p_j - c *
+ * q_j, 0): the first j with w_0 + ... + w_j > u[root] * sum w. Where that leaves
+ * nothing p itself is w; a row of p without probability gives token -1. So
+ * accepted tokens and the drawn one are distributed as if sampled from p one by
+ * one.
+ *
+ *   draft, mask, starts, max_tree, path, count as in w4a16_tree_accept
+ *   u      float32 [tokens], in [0, 1): each node's own number, the root's for
+ *          the token
+ *   token  int64 [rows]  the token drawn (-1 for a row without new tokens)
+ *
+ * A NaN or negative probability counts as 0, one above 1 as 1; a drafted token
+ * outside the vocabulary is passed over (W4A16_ERR_INDEX). Sums are 64-bit
+ * integers in units of 2^-56, tests double: results do not depend on any order.
+ */
+int w4a16_tree_sample(const float *p, int64_t p_row, const float *q, int64_t q_row, int vocab, const int64_t *draft,
+                      const int64_t *mask, const int32_t *starts, const float *u, int rows, int tokens, int max_tree,
+                      int32_t *path, int32_t *count, int64_t *token, w4a16_stream_t stream);
+
+/*
  * Keeps the accepted rows: in every layer and head, position lengths[b] +
  * path[b][i] moves to lengths[b] + i for i < count[b], and lengths_out[b] =
  * lengths[b] + count[b]. path[b] ascends (as w4a16_tree_accept gives it).
@@ -478,6 +529,46 @@ int w4a16_kv_fork(const w4a16_kv_cache *cache, int32_t *page_table, int max_page
  */
 int w4a16_kv_reserve(int32_t *page_table, int max_pages, int table_rows, int32_t *refs, int pages, int page_rows,
                      const int32_t *rows, const int32_t *want, int n, int32_t *ok, w4a16_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside one product:
+ *
+ *   out[t] = y[t] + scale[e] * (x[t] . A[e]^T) . B[e]^T,  e = adapter[b]
+ *
+ * for the tokens t of row b (starts[b] .. starts[b + 1] - 1, as above; starts
+ * NULL: rows = tokens and each token is a row). y is what a w4a16 product gave
+ * for the same x. A row with adapter -1 gets y, bit by bit.
+ *
+ *   y, out     bf16 [tokens][outer], element (t, n) at t * row stride + n. out
+ *              may be y (then rows without an adapter are not touched); it must
+ *              not overlap y otherwise, nor a, b or x's other rows
+ *   x          bf16 [tokens][inner], x_row a multiple of 8, base 16-byte aligned
+ *   a          bf16 [adapters][rank][inner], b bf16 [adapters][outer][rank]:
+ *              strides multiples of 8, bases 16-byte aligned
+ *   scale      float32 [adapters], or NULL: 1
+ *   adapter    int32 [rows]
+ *   adapters   1 .. W4A16_MAX_ADAPTERS; rank a multiple of 8 up to
+ *              W4A16_MAX_RANK (smaller adapters padded with zeros); inner a
+ *              multiple of 8; outer any
+ *   workspace  w4a16_lora_workspace_bytes(tokens, rank, inner) bytes, 256-byte
+ *              aligned, used only while the call runs on `stream`. A call makes
+ *              two launches that share it
+ *
+ * Sums are float32; x A^T goes into the second product with 16 bits of mantissa;
+ * out is rounded once. Results are bitwise reproducible, and a token's does not
+ * depend on the tokens beside it. Tokens at starts[rows] and above are not read
+ * and not written. An adapter outside -1 .. adapters - 1 counts as -1, a row whose
+ * offsets cannot be is left out (a token that descending offsets give to two rows
+ * is either's); w4a16_kernel_status() then returns W4A16_ERR_INDEX.
+ * ------------------------------------------------------------------------ */
+#define W4A16_MAX_ADAPTERS 4096
+#define W4A16_MAX_RANK 128
+size_t w4a16_lora_workspace_bytes(int tokens, int rank, int inner);
+int w4a16_lora_add(const uint16_t *y, int64_t y_row, const uint16_t *x, int64_t x_row, const uint16_t *a,
+                   int64_t a_adapter, int64_t a_row, const uint16_t *b, int64_t b_adapter, int64_t b_row,
+                   const float *scale, const int32_t *adapter, const int32_t *starts, int rows, int tokens,
+                   int adapters, int rank, int inner, int outer, uint16_t *out, int64_t out_row, void *workspace,
+                   w4a16_stream_t stream);
 
 /*
  * Waits for all work on the current device, then reads and clears the

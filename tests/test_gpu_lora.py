@@ -1,0 +1,221 @@
+"""lora_add against 64 bits: ranks, sizes, rows with shared, missing and bad
+adapters, padding, strides, in place, other streams and graphs."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import gemm_w4a16_group_gb300 as w4
+from sample_helpers import adapted, stored
+
+pytestmark = pytest.mark.gpu
+
+
+class Problem:
+    def __init__(self, sizes, which, rank, inner, outer, store, seed=0, pad=0, scaled=True):
+        gen = torch.Generator().manual_seed(seed)
+        self.tokens = sum(sizes) + pad
+        self.starts_h = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+        self.which = [e for n, e in zip(sizes, which) for _ in range(n)] + [-1] * pad
+        self.x, self.y = stored(gen, self.tokens, inner).cuda(), stored(gen, self.tokens, outer).cuda()
+        self.a = stored(gen, store, rank, inner, std=inner ** -0.5).cuda()
+        self.b = stored(gen, store, outer, rank, std=rank ** -0.5).cuda()
+        self.scale = (torch.rand(store, generator=gen) + 0.5).cuda() if scaled else None
+        self.adapter = torch.tensor(which, dtype=torch.int32, device="cuda")
+        self.starts = torch.from_numpy(self.starts_h).cuda()
+        self.live = sum(sizes)
+
+    def run(self, **kw):
+        return w4.lora_add(self.y, self.x, self.a, self.b, self.adapter, self.starts, self.scale, **kw)
+
+    def check(self, out):
+        want, bound = adapted(self.y, self.x, self.a, self.b, self.which, self.scale)
+        off = (out.double().cpu() - want).abs()[:self.live]
+        assert (off <= bound[:self.live]).all(), float((off / bound[:self.live].clamp(min=1e-300)).max())
+        for t in range(self.live):
+            if self.which[t] < 0:
+                assert torch.equal(out[t].view(torch.int16), self.y[t].view(torch.int16))
+
+
+@pytest.mark.parametrize("rank", [8, 16, 24, 32, 40, 64, 72, 128])
+@pytest.mark.parametrize("sizes,which,inner,outer", [
+    ([1], [0], 64, 64), ([1, 2, 5], [1, -1, 1], 520, 250), ([16, 1, 0, 17], [2, 0, 1, 2], 1288, 1000),
+    ([40, 33], [0, 1], 200, 333), ([1] * 20, [i % 3 for i in range(20)], 8, 1),
+])
+def test_few_tokens(rank, sizes, which, inner, outer):
+    p = Problem(sizes, which, rank, inner, outer, 3, seed=rank)
+    p.check(p.run())
+    assert w4.kernel_status() == 0
+
+
+@pytest.mark.parametrize("rank", [8, 16, 32, 64, 128])
+@pytest.mark.parametrize("sizes,which,inner,outer", [
+    ([600], [0], 328, 515), ([300, 7, 513, 1], [1, -1, 0, 1], 1024, 264), ([65, 64, 63, 400], [0, 1, 0, 1], 96, 776),
+])
+def test_prompts(rank, sizes, which, inner, outer):
+    p = Problem(sizes, which, rank, inner, outer, 2, seed=rank + 1)
+    p.check(p.run())
+    assert w4.kernel_status() == 0
+
+
+@pytest.mark.parametrize("sizes,which,rank,inner,outer,store", [
+    ([1], [3], 16, 5120, 5120, 8), ([1] * 48, [i % 12 for i in range(48)], 64, 5120, 2049, 12), ([8, 3, 1, 5], [0, 1, -1, 0], 32, 17408, 640, 2),
+])
+def test_model_sizes(sizes, which, rank, inner, outer, store):
+    p = Problem(sizes, which, rank, inner, outer, store)
+    p.check(p.run())
+
+
+def test_a_token_a_row():
+    p = Problem([1] * 37, [(i * 7) % 5 - 1 for i in range(37)], 16, 256, 300, 4, scaled=False)
+    p.starts = None
+    p.check(p.run())
+
+
+def test_a_token_does_not_depend_on_the_others():
+    p = Problem([3, 2, 9], [0, 1, 0], 16, 512, 512, 2)
+    whole = p.run()
+    for b in range(3):
+        s = slice(int(p.starts_h[b]), int(p.starts_h[b + 1]))
+        one = w4.lora_add(p.y[s], p.x[s], p.a, p.b, p.adapter[b:b + 1], torch.tensor([0, s.stop - s.start], dtype=torch.int32, device="cuda"), p.scale)
+        off = (one.double() - whole[s].double()).abs()  # (K is split otherwise: a rounding of bf16 apart at most)
+        assert (off <= 2.0 ** -7 * whole[s].double().abs() + 1e-5).all()
+    assert torch.equal(p.run(), whole)
+
+
+def test_in_place_and_padding():
+    for sizes, which in (([3, 2, 4], [1, -1, 0]), ([200, 100, 300], [0, -1, 1])):
+        p = Problem(sizes, which, 24, 320, 402, 2, pad=5)
+        p.x[p.live:] = math.nan
+        keep = p.y.clone()
+        want = p.run(out=torch.full_like(p.y, 3.0))
+        p.check(want)
+        assert (want[p.live:] == 3).all()  # padding is left alone
+        got = w4.lora_add(p.y, p.x, p.a, p.b, p.adapter, p.starts, p.scale, out=p.y)
+        assert got is p.y and torch.equal(got[:p.live], want[:p.live]) and torch.equal(got[p.live:], keep[p.live:])
+
+
+def test_columns_of_a_wider_product():
+    """Query columns of a fused product, in place, at any alignment; the columns beside stay."""
+    for lead, outer, width in ((0, 256, 512), (256, 128, 512), (8, 250, 264), (3, 101, 259), (0, 7, 7)):
+        p = Problem([4, 1, 6], [0, 1, -1], 16, 128, outer, 2, seed=lead)
+        wide = torch.randn((p.tokens, width + lead), device="cuda").to(torch.bfloat16)
+        before = wide.clone()
+        view = wide[:, lead:lead + outer]
+        p.y = view.clone()
+        w4.lora_add(view, p.x, p.a, p.b, p.adapter, p.starts, p.scale, out=view)
+        p.check(view.contiguous())
+        beside = torch.ones(wide.shape[1], dtype=torch.bool)
+        beside[lead:lead + outer] = False
+        assert torch.equal(wide[:, beside], before[:, beside])
+
+
+def test_strided_inputs():
+    p = Problem([4, 9], [1, 0], 32, 256, 200, 2)
+    want = p.run()
+    x = torch.empty((p.tokens, 300 + 4), dtype=torch.bfloat16, device="cuda")[:, 8:264]
+    x.copy_(p.x)
+    a = torch.empty((2, 32, 512), dtype=torch.bfloat16, device="cuda")[:, :, 128:384]
+    a.copy_(p.a)
+    b = torch.empty((200, 2, 48), dtype=torch.bfloat16, device="cuda").transpose(0, 1)[:, :, 16:]
+    b.copy_(p.b)
+    assert torch.equal(w4.lora_add(p.y, x, a, b, p.adapter, p.starts, p.scale), want)
+    one = p.y[:1].expand(p.tokens, 200)
+    p.y = one.contiguous()
+    assert torch.equal(w4.lora_add(one, x, a, b, p.adapter, p.starts, p.scale), p.run())
+
+
+def test_large_store_and_many_rows():
+    """More adapters and rows than a block has threads; most of them idle."""
+    rng = np.random.default_rng(0)
+    store, rows = 1000, 700
+    which = np.where(rng.random(rows) < 0.2, -1, rng.integers(0, store, rows)).tolist()
+    sizes = rng.integers(0, 3, rows).tolist()
+    p = Problem(sizes, which, 8, 64, 96, store)
+    p.check(p.run())
+    p = Problem([1] * 300, [5] * 150 + [4095] * 150, 8, 16, 24, 4096)
+    p.check(p.run())
+
+
+def test_bad_indices_are_left_out_and_reported():
+    p = Problem([2, 3, 4], [0, 2, -7], 16, 128, 128, 2)
+    out = p.run()
+    assert w4.kernel_status() == -6
+    p.which = [0, 0] + [-1] * 7
+    p.check(out)
+    for starts in ([0, 5, 2, 9], [-1, 2, 5, 9], [0, 2, 5, 10]):
+        q = Problem([2, 3, 4], [0, 1, -1], 16, 128, 128, 2)
+        q.starts = torch.tensor(starts, dtype=torch.int32, device="cuda")
+        keep = torch.full_like(q.y, 5.0)
+        q.run(out=keep)
+        assert w4.kernel_status() == -6
+        # (offsets that descend may give a token to two rows: it is either's)
+        sound = [(s, t, e) for s, t, e in zip(starts, starts[1:], [0, 1, -1]) if 0 <= s <= t <= 9]
+        for i in range(9):
+            mine = [e for s, t, e in sound if s <= i < t]
+            if not mine:
+                assert (keep[i] == 5).all()
+            elif len(mine) == 1:
+                want, bound = adapted(q.y[i:i + 1], q.x[i:i + 1], q.a, q.b, mine, q.scale)
+                assert ((keep[i].double().cpu() - want[0]).abs() <= bound[0]).all()
+
+
+def test_values_that_are_not_finite_stay_with_their_tokens():
+    p = Problem([3, 3, 3], [0, 1, -1], 16, 256, 128, 2)
+    p.x[1, 5], p.x[7, 5] = math.inf, math.nan  # the second belongs to a row without an adapter
+    p.y[4, 3], p.y[8, 9] = math.inf, math.nan
+    p.a[1, 2, 3] = math.nan
+    out = p.run()
+    assert out[0].isfinite().all() and out[2].isfinite().all()
+    assert not out[1].isfinite().any()
+    assert out[3:6].isnan().all()
+    assert torch.equal(out[6:].view(torch.int16), p.y[6:].view(torch.int16))
+
+
+def test_streams_graphs_and_repeats():
+    for sizes, which in (([3, 1, 4], [0, 1, 0]), ([300, 300], [0, 1])):
+        p = Problem(sizes, which, 32, 512, 1000, 2)
+        want = p.run()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        for _ in range(10):
+            got = p.run(stream=side)
+            mine = p.run()
+            side.synchronize()
+            assert torch.equal(got, want) and torch.equal(mine, want)
+        one, two = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(one):
+            a = p.run()
+        with torch.cuda.graph(two):
+            b = p.run()
+        side.wait_stream(torch.cuda.current_stream())
+        for _ in range(10):  # two graphs at once: each has a workspace of its own
+            one.replay()
+            with torch.cuda.stream(side):
+                two.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, want) and torch.equal(b, want)
+        p.adapter.fill_(-1)
+        one.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, p.y)
+
+
+def test_behind_a_product():
+    """gemm and lora_add in a row, as a decode step calls them: the second reads what the first has just written."""
+    import synth
+    M, N, K, G = 5, 384, 512, 128
+    prob = synth.make_problem(M, N, K, G, True, seed=0)
+    up = lambda v: torch.from_numpy(np.ascontiguousarray(v).view(np.int16) if v.dtype == np.uint16 else np.ascontiguousarray(v)).cuda()  # noqa: E731
+    packed = w4.repack(up(prob["qweight"]), up(prob["scales"]).view(torch.bfloat16), None, N, K, G, True)
+    x = up(prob["x"]).view(torch.bfloat16)
+    p = Problem([2, 3], [1, 0], 16, K, N, 2)
+    p.x = x
+    p.y = w4.gemm(x, packed, N, K, G, True)
+    torch.cuda.synchronize()
+    want = p.run()
+    p.check(want)
+    for _ in range(50):
+        y = w4.gemm(x, packed, N, K, G, True)
+        assert torch.equal(w4.lora_add(y, x, p.a, p.b, p.adapter, p.starts, p.scale, out=y), want)
