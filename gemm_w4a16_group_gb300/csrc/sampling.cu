@@ -11,8 +11,12 @@
 namespace w4a16 {
 namespace {
 
+#ifndef PROB_LEAST
+#define PROB_LEAST 8192
+#endif
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kMaxCluster = 16;
+using u64 = unsigned long long;
 
 // The halves of a cluster barrier: what a CTA does between them need not wait
 // for the others.
@@ -21,24 +25,28 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 
 // A row of `n` elements seen in quads: quad k holds elements 4k - shift .. +3,
 // so that whole quads are aligned wherever the row begins. [lo, hi) are the
-// quads of part `i` of `parts`.
+// quads of part `i` of 2^log2; whole quads: [first, first + whole).
 struct Quads {
-  int shift, lo, hi;
+  int shift, lo, hi, first, whole;
+  __device__ __forceinline__ Quads(int n, int shift, uint32_t i, int log2) : shift(shift) {
+    const uint32_t all = ((uint32_t)(shift + n) + 3) / 4, each = (all + (1u << log2) - 1) >> log2;
+    lo = (int)min(i * each, all);
+    hi = (int)min(i * each + each, all);
+    first = shift ? 1 : 0;
+    whole = (shift + n) / 4 - first;
+  }
+  __device__ __forceinline__ bool is_whole(int k) const { return (uint32_t)(k - first) < (uint32_t)max(whole, 0); }
 };
-__device__ __forceinline__ Quads quads_of(int n, int shift, uint32_t i, uint32_t parts) {
-  const long long all = (shift + (long long)n + 3) / 4;
-  return {shift, (int)(all * i / parts), (int)(all * (i + 1) / parts)};
-}
 
 // ---------------------------------------------------------------------------
 // probabilities: p_j = 2^((l_j - m) a) / sum_i 2^((l_i - m) a), a = log2(e) / T.
-// One pass: a thread holds its 32 logits' powers, relative to their own
+// One pass: a thread holds the powers of its logits, relative to their own
 // maximum, in registers while the cluster agrees on maximum and sum. Slices
 // that do not fit are read twice.
 // ---------------------------------------------------------------------------
 constexpr int kProbThreads = 512;
 constexpr int kProbQuads = 8;  // of a thread
-constexpr uint32_t kNone = 0xFF80u;  // bf16 -inf: no probability
+constexpr uint32_t kNone = 0xFF80FF80u;  // two bf16 -inf: no probability
 
 struct ProbParams {
   const uint16_t *logits;
@@ -48,79 +56,75 @@ struct ProbParams {
   int vocab;
 };
 
-// log2(e) / T in two parts, so that the exponent of a small probability, which
-// is large, keeps its fraction: 2^y with y rounded to 24 bits would be off by
-// up to 2^-24 |y|.
-struct Power {
-  float hi, lo;
-  __device__ explicit Power(float t) {
-    const float high = 1.44269502f, low = 1.92596299e-8f;  // log2(e)
-    hi = fminf(__fdiv_rn(high, t), 1e30f);
-    lo = hi < 1e30f && t < 1e30f ? __fdiv_rn(fmaf(-hi, t, high) + low, t) : 0.f;
-  }
-  // e^(d / T) for d <= 0; 0 below 2^-152
-  __device__ __forceinline__ float operator()(float d) const {
-    const float y = d * hi;
-    const float rest = fmaf(d, hi, -y) + d * lo;
-    float r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(y));
-    r = fmaf(r, rest * 0.69314718f, r);
-    return y < -152.f ? 0.f : r;
-  }
-};
-
-// Four logits of the row, two to a word; kNone past its ends and below the floor.
+// Four logits of the row, two to a word; -inf past its ends.
 template <bool ALIGNED>
-__device__ __forceinline__ uint2 load_quad(const uint16_t *row, int k, int shift, int n, float floor) {
-  const int j = 4 * k - shift;
-  uint2 w;
-  if (ALIGNED && j >= 0 && j + 4 <= n) {
-    w = *reinterpret_cast<const uint2 *>(row + j);
-  } else {
-    uint32_t x[4];
+__device__ __forceinline__ uint2 load_quad(const uint16_t *row, const Quads &q, int k, int n) {
+  const int j = 4 * k - q.shift;
+  if (ALIGNED && q.is_whole(k)) return *reinterpret_cast<const uint2 *>(row + j);
+  uint32_t x[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = j + i >= 0 && j + i < n ? row[j + i] : kNone;
-    w = make_uint2(x[0] | x[1] << 16, x[2] | x[3] << 16);
-  }
-  if (floor > -INFINITY) {
-    uint32_t *v = &w.x;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (bf16lo_to_f32(v[i]) < floor) v[i] = (v[i] & 0xFFFF0000u) | kNone;
-      if (bf16hi_to_f32(v[i]) < floor) v[i] = (v[i] & 0xFFFFu) | kNone << 16;
-    }
-  }
-  return w;
+  for (int i = 0; i < 4; ++i) x[i] = j + i >= 0 && j + i < n ? row[j + i] : kNone & 0xFFFFu;
+  return make_uint2(x[0] | x[1] << 16, x[2] | x[3] << 16);
 }
-__device__ __forceinline__ float at(const uint2 &w, int i) {
-  const uint32_t v = i < 2 ? w.x : w.y;
-  return i & 1 ? bf16hi_to_f32(v) : bf16lo_to_f32(v);
+// -inf where a logit is below the floor
+__device__ __forceinline__ void drop(uint2 &w, float floor) {
+  uint32_t *v = &w.x;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (bf16lo_to_f32(v[i]) < floor) v[i] = (v[i] & 0xFFFF0000u) | (kNone & 0xFFFFu);
+    if (bf16hi_to_f32(v[i]) < floor) v[i] = (v[i] & 0xFFFFu) | (kNone & 0xFFFF0000u);
+  }
 }
 template <bool ALIGNED>
-__device__ __forceinline__ void store_quad(float *row, int k, int shift, int n, const float (&v)[4]) {
-  const int j = 4 * k - shift;
-  if (ALIGNED && j >= 0 && j + 4 <= n) {
-    *reinterpret_cast<float4 *>(row + j) = make_float4(v[0], v[1], v[2], v[3]);
+__device__ __forceinline__ void store_quad(float *row, const Quads &q, int k, int n, float2 a, float2 b) {
+  const int j = 4 * k - q.shift;
+  if (ALIGNED && q.is_whole(k)) {
+    *reinterpret_cast<float4 *>(row + j) = make_float4(a.x, a.y, b.x, b.y);
   } else {
+    const float v[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (j + i >= 0 && j + i < n) row[j + i] = v[i];
   }
 }
 
-// (maximum, sum of powers relative to it), joined
-__device__ __forceinline__ void join(float &m, float &s, float m2, float s2, const Power &pw) {
-  const float top = fmaxf(m, m2);
-  // (an empty part, m = -inf and s = 0, adds nothing, at an infinite temperature too)
-  s = (m == top || s == 0.f ? s : s * pw(m - top)) + (m2 == top || s2 == 0.f ? s2 : s2 * pw(m2 - top));
-  m = top;
+__device__ __forceinline__ float exp2_fast(float y) {
+  float r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(y));
+  return r;
+}
+// 2^((l - m) a) of two logits
+__device__ __forceinline__ float2 powers(uint32_t w, f32x2 minus_m, f32x2 a) {
+  const float2 y = f32_halves(mul2(add2(f32_pair(bf16lo_to_f32(w), bf16hi_to_f32(w)), minus_m), a));
+  return make_float2(exp2_fast(y.x), exp2_fast(y.y));
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // (of a NaN and a number the number)
+  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-__device__ __forceinline__ unsigned long long key_max(unsigned long long a, unsigned long long b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {  // (of a NaN and a number the NaN)
+  const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+__device__ __forceinline__ u64 key_max(u64 a, u64 b) { return a > b ? a : b; }
+
+// (maximum, sum of powers relative to it) over the first N lanes' parts; an empty part is (lowest, 0)
+template <int N>
+__device__ __forceinline__ void join(float &m, float &s, float a) {
+  const float mine = m;
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+  s = mine == m ? s : s * exp2_fast((mine - m) * a);
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+}
 
 template <bool ALIGNED>
 __global__ void __launch_bounds__(kProbThreads, 2) probabilities_kernel(const ProbParams p) {
-  __shared__ unsigned long long slots[kMaxCluster], warps[kProbThreads / 32];
+  constexpr int kWarps = kProbThreads / 32;
+  __shared__ u64 slots[kMaxCluster], warps[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t S = cluster_nctarank(), rank = cluster_ctarank();
   const long long r = cluster_id_x();
@@ -130,107 +134,121 @@ __global__ void __launch_bounds__(kProbThreads, 2) probabilities_kernel(const Pr
 
   const uint16_t *row = p.logits + r * p.row;
   float *out = p.out + r * p.vocab;
-  const Quads q = quads_of(p.vocab, ALIGNED ? (int)(r * p.vocab & 3) : 0, rank, S);
-  const bool one = q.hi - q.lo <= kProbThreads * kProbQuads;  // each thread's logits stay in registers
+  const Quads q(p.vocab, ALIGNED ? (int)(r * p.vocab & 3) : 0, rank, __ffs(S) - 1);
   const float t = p.temperature ? p.temperature[r] : 1.f, floor = p.floor ? p.floor[r] : -INFINITY;
+  const bool greedy = !(t > 0.f);
 
-  if (!(t > 0.f)) {  // the first maximum has it all
-    unsigned long long best = 0;
-    for (int k = q.lo + tid; k < q.hi; k += kProbThreads) {
-      const uint2 w = load_quad<ALIGNED>(row, k, q.shift, p.vocab, floor);
-      const uint32_t x[4] = {w.x & 0xFFFFu, w.x >> 16, w.y & 0xFFFFu, w.y >> 16};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (x[i] != kNone) best = key_max(best, argmax_key(x[i], 4 * k - q.shift + i));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) best = key_max(best, __shfl_xor_sync(kFull, best, o));
-    if (lane == 0) warps[warp] = best;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kProbThreads / 32; ++w) best = key_max(best, warps[w]);
-    cluster_wait();
-    if (tid < (int)S) st_cluster_u64(mapa_shared(smem_u32(&slots[rank]), tid), best);
-    cluster_sync_all();
-    best = 0;
-    for (uint32_t i = 0; i < S; ++i) best = key_max(best, slots[i]);
-    const int first = best ? (int)(0xFFFFFFFFu - (uint32_t)best) : -1;
-    for (int k = q.lo + tid; k < q.hi; k += kProbThreads) {
-      float v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = first >= 0 && 4 * k - q.shift + i == first ? 1.f : 0.f;
-      store_quad<ALIGNED>(out, k, q.shift, p.vocab, v);
-    }
-    return;
-  }
-
-  const Power pw(t);
-  float e[kProbQuads][4], m = -INFINITY, s = 0.f;
+  // a logit of -inf stays -inf through difference and product, whatever the temperature
+  const float lowest = -3.40282347e38f, a = greedy ? 1.f : fmaxf(fminf(__fdiv_rn(1.44269502f, t), 1e30f), 1e-44f);
+  const f32x2 a2 = f32_pair(a, a);
+  float2 e[kProbQuads][2];
+  float m = lowest, s = 0.f, mine = lowest;
+  u64 best = 0;
   for (int k0 = q.lo; k0 < q.hi; k0 += kProbThreads * kProbQuads) {
     uint2 x[kProbQuads];
 #pragma unroll
     for (int u = 0; u < kProbQuads; ++u) {
       const int k = k0 + u * kProbThreads + tid;
-      x[u] = k < q.hi ? load_quad<ALIGNED>(row, k, q.shift, p.vocab, floor) : make_uint2(kNone * 0x10001u, kNone * 0x10001u);
+      x[u] = k < q.hi ? load_quad<ALIGNED>(row, q, k, p.vocab) : make_uint2(kNone, kNone);
     }
-    float top = -INFINITY, sum = 0.f;
+    if (floor > -INFINITY) {
 #pragma unroll
-    for (int u = 0; u < kProbQuads; ++u)
+      for (int u = 0; u < kProbQuads; ++u) drop(x[u], floor);
+    }
+    if (greedy) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) top = fmaxf(top, at(x[u], i));  // (a NaN comes back in the sum)
+      for (int u = 0; u < kProbQuads; ++u) {
+        // (most quads are behind the best one so far: a look at their maximum tells)
+        const uint32_t top = max2_nan(x[u].x, x[u].y);
+        const uint32_t high = max(order_key16(top), order_key16(top >> 16));
+        if (high <= (uint32_t)(best >> 32)) continue;
+        const uint32_t v[4] = {x[u].x & 0xFFFFu, x[u].x >> 16, x[u].y & 0xFFFFu, x[u].y >> 16};
 #pragma unroll
-    for (int u = 0; u < kProbQuads; ++u)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float l = at(x[u], i);
-        e[u][i] = l == -INFINITY ? 0.f : pw(l - top);
-        sum += e[u][i];
+        for (int i = 0; i < 4; ++i)
+          if (v[i] != (kNone & 0xFFFFu)) best = key_max(best, argmax_key(v[i], 4 * (k0 + u * kProbThreads + tid) - q.shift + i));
       }
-    join(m, s, top, sum, pw);
-  }
-  const float mine = m;  // what e is relative to, where there is one chunk
+      continue;
+    }
+    uint32_t top = kNone;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) join(m, s, __shfl_xor_sync(kFull, m, o), __shfl_xor_sync(kFull, s, o), pw);
+    for (int u = 0; u < kProbQuads; ++u) top = max2(top, max2(x[u].x, x[u].y));
+    mine = fmaxf(fmaxf(bf16lo_to_f32(top), bf16hi_to_f32(top)), lowest);
+    const f32x2 minus = f32_pair(-mine, -mine);
+    f32x2 sum = 0;
+#pragma unroll
+    for (int u = 0; u < kProbQuads; ++u) {
+      e[u][0] = powers(x[u].x, minus, a2);
+      e[u][1] = powers(x[u].y, minus, a2);
+      sum = add2(sum, add2(f32_pair(e[u][0].x, e[u][0].y), f32_pair(e[u][1].x, e[u][1].y)));
+    }
+    const float2 both = f32_halves(sum);
+    const float high = fmaxf(m, mine);  // (more than one chunk: joined with the ones before)
+    s = (m == high ? s : s * exp2_fast((m - high) * a)) + (mine == high ? 1.f : exp2_fast((mine - high) * a)) * (both.x + both.y);
+    m = high;
+  }
+  if (greedy) {  // the first maximum has it all
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) best = key_max(best, __shfl_xor_sync(kFull, best, o));
+    if (lane == 0) warps[warp] = best;
+    __syncthreads();
+    if (warp == 0) {
+      best = lane < kWarps ? warps[lane] : 0;
+#pragma unroll
+      for (int o = kWarps / 2; o > 0; o >>= 1) best = key_max(best, __shfl_xor_sync(kFull, best, o));
+    }
+    cluster_wait();
+    if (tid < (int)S) st_cluster_u64(mapa_shared(smem_u32(&slots[rank]), tid), best);
+    cluster_sync_all();
+    best = 0;
+    for (uint32_t i = 0; i < S; ++i) best = key_max(best, slots[i]);
+    const int first = best ? (int)(0xFFFFFFFFu - (uint32_t)best) : -4;
+    for (int k = q.lo + tid; k < q.hi; k += kProbThreads) {
+      const int at = first - (4 * k - q.shift);
+      store_quad<ALIGNED>(out, q, k, p.vocab, make_float2(at == 0, at == 1), make_float2(at == 2, at == 3));
+    }
+    return;
+  }
+  join<32>(m, s, a);
   if (lane == 0) warps[warp] = f32_pair(m, s);
   __syncthreads();
   if (warp == 0) {
-    const float2 v = lane < kProbThreads / 32 ? f32_halves(warps[lane]) : make_float2(-INFINITY, 0.f);
+    const float2 v = lane < kWarps ? f32_halves(warps[lane]) : make_float2(lowest, 0.f);
     m = v.x;
     s = v.y;
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) join(m, s, __shfl_xor_sync(kFull, m, o), __shfl_xor_sync(kFull, s, o), pw);
+    join<kWarps>(m, s, a);
   }
   cluster_wait();
   if (tid < (int)S) st_cluster_u64(mapa_shared(smem_u32(&slots[rank]), tid), f32_pair(m, s));
   cluster_sync_all();
-  m = -INFINITY;
-  s = 0.f;
-  for (uint32_t i = 0; i < S; ++i) {
-    const float2 v = f32_halves(slots[i]);
-    join(m, s, v.x, v.y, pw);
-  }
+  const float2 slot = (lane & 15) < (int)S ? f32_halves(slots[lane & 15]) : make_float2(lowest, 0.f);
+  m = slot.x;
+  s = slot.y;
+  join<kMaxCluster>(m, s, a);
   const float inv = s == 0.f ? 0.f : __fdiv_rn(1.f, s);
-  if (one) {
-    const float f = mine == m ? inv : mine == -INFINITY ? 0.f : inv * pw(mine - m);
+  // each thread's logits are still in registers, where the slice is one chunk and the sum is a number (else a dropped
+  // logit's 0 has to be told from a kept one's)
+  if (q.hi - q.lo <= kProbThreads * kProbQuads && s == s) {
+    const float f = mine == m ? inv : inv * exp2_fast((mine - m) * a);
+    const f32x2 f2 = f32_pair(f, f);
 #pragma unroll
     for (int u = 0; u < kProbQuads; ++u) {
       const int k = q.lo + u * kProbThreads + tid;
-      float v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = e[u][i] * f;
-      if (k < q.hi) store_quad<ALIGNED>(out, k, q.shift, p.vocab, v);
+      if (k < q.hi)
+        store_quad<ALIGNED>(out, q, k, p.vocab, f32_halves(mul2(f32_pair(e[u][0].x, e[u][0].y), f2)),
+                            f32_halves(mul2(f32_pair(e[u][1].x, e[u][1].y), f2)));
     }
     return;
   }
+  const f32x2 minus = f32_pair(-m, -m);
   for (int k = q.lo + tid; k < q.hi; k += kProbThreads) {
-    const uint2 w = load_quad<ALIGNED>(row, k, q.shift, p.vocab, floor);
-    float v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float l = at(w, i);
-      v[i] = l == -INFINITY ? 0.f : pw(l - m) * inv;
-    }
-    store_quad<ALIGNED>(out, k, q.shift, p.vocab, v);
+    uint2 w = load_quad<ALIGNED>(row, q, k, p.vocab);
+    drop(w, floor);
+    float2 v[2] = {powers(w.x, minus, a2), powers(w.y, minus, a2)};
+    v[0].x = bf16lo_to_f32(w.x) == -INFINITY ? 0.f : v[0].x * inv;
+    v[0].y = bf16hi_to_f32(w.x) == -INFINITY ? 0.f : v[0].y * inv;
+    v[1].x = bf16lo_to_f32(w.y) == -INFINITY ? 0.f : v[1].x * inv;
+    v[1].y = bf16hi_to_f32(w.y) == -INFINITY ? 0.f : v[1].y * inv;
+    store_quad<ALIGNED>(out, q, k, p.vocab, v[0], v[1]);
   }
 }
 
@@ -256,8 +274,6 @@ constexpr int kSampleThreads = 512;
 constexpr int kSampleWarps = kSampleThreads / 32;
 constexpr int kFrac = 56;
 constexpr unsigned long long kOne = 1ull << kFrac;
-
-using u64 = unsigned long long;
 
 struct SampleParams {
   const float *p, *q;  // q null: children that were picked
@@ -303,9 +319,9 @@ __device__ __forceinline__ u64 weight(float p, float q, u64 c) {
 }
 
 template <bool ALIGNED>
-__device__ __forceinline__ void load_floats(const float *row, int k, int shift, int n, float (&x)[4]) {
-  const int j = 4 * k - shift;
-  if (ALIGNED && j >= 0 && j + 4 <= n) {
+__device__ __forceinline__ void load_floats(const float *row, const Quads &q, int k, int n, float (&x)[4]) {
+  const int j = 4 * k - q.shift;
+  if (ALIGNED && q.is_whole(k)) {
     const float4 v = *reinterpret_cast<const float4 *>(row + j);
     x[0] = v.x;
     x[1] = v.y;
@@ -462,13 +478,13 @@ __global__ void __launch_bounds__(kSampleThreads, 2) tree_sample_kernel(const Sa
     // this warp's part of the row
     const float *pr = p.p + row * p.p_row, *qr = p.q + row * p.q_row;
     const int shift = ALIGNED ? (int)((row * p.p_row) & 3) : 0;
-    const Quads mine = quads_of(p.vocab, shift, rank * kSampleWarps + warp, S * kSampleWarps);
+    const Quads mine(p.vocab, shift, rank * kSampleWarps + warp, __ffs(S * kSampleWarps) - 1);
     u64 sum = 0;
     if (c == 0) {
 #pragma unroll 4
       for (int k = mine.lo + lane; k < mine.hi; k += 32) {
         float x[4];
-        load_floats<ALIGNED>(pr, k, shift, p.vocab, x);
+        load_floats<ALIGNED>(pr, mine, k, p.vocab, x);
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum += fixed(x[i]);
       }
@@ -476,8 +492,8 @@ __global__ void __launch_bounds__(kSampleThreads, 2) tree_sample_kernel(const Sa
 #pragma unroll 4
       for (int k = mine.lo + lane; k < mine.hi; k += 32) {
         float x[4], y[4];
-        load_floats<ALIGNED>(pr, k, shift, p.vocab, x);
-        load_floats<ALIGNED>(qr, k, shift, p.vocab, y);
+        load_floats<ALIGNED>(pr, mine, k, p.vocab, x);
+        load_floats<ALIGNED>(qr, mine, k, p.vocab, y);
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum += weight(x[i], y[i], c);
       }
@@ -528,8 +544,8 @@ __global__ void __launch_bounds__(kSampleThreads, 2) tree_sample_kernel(const Sa
       const int k = k0 + lane;
       float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
       if (k < mine.hi) {
-        load_floats<ALIGNED>(pr, k, shift, p.vocab, x);
-        if (c) load_floats<ALIGNED>(qr, k, shift, p.vocab, y);
+        load_floats<ALIGNED>(pr, mine, k, p.vocab, x);
+        if (c) load_floats<ALIGNED>(qr, mine, k, p.vocab, y);
       }
       u64 part[4], four = 0;
 #pragma unroll
@@ -629,7 +645,7 @@ cudaError_t launch_probabilities(const uint16_t *logits, long long row, const fl
   // quads of logits and of probabilities are aligned together
   const bool aligned = address(logits, 8) && address(out, 16) && (row - vocab) % 4 == 0;
   const ProbParams p{logits, row, temperature, floor, out, vocab};
-  const int s = ctas_of(vocab, 8192);
+  const int s = ctas_of(vocab, PROB_LEAST);
   return launch_rows(aligned ? probabilities_kernel<true> : probabilities_kernel<false>, fits[aligned], tokens, s,
                      kProbThreads, device, stream, p);
 }
