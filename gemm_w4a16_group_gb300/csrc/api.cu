@@ -635,7 +635,7 @@ int w4a16_probabilities(const uint16_t *logits, int64_t logits_row, const float 
   int st = current_device(d);
   if (st != W4A16_OK) return st;
   return finish_launch(launch_probabilities(logits, logits_row, temperature, floor, tokens, vocab, out, d.device,
-                                            reinterpret_cast<cudaStream_t>(stream)));
+                                            d.sm_count, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int w4a16_tree_sample(const float *p, int64_t p_row, const float *q, int64_t q_row, int vocab, const int64_t *draft,
@@ -653,7 +653,7 @@ int w4a16_tree_sample(const float *p, int64_t p_row, const float *q, int64_t q_r
   if (st != W4A16_OK) return st;
   return finish_launch(launch_tree_sample(SampleCall{p, q, p_row, q ? q_row : 0, draft, mask, starts, u, rows, tokens,
                                                      vocab, max_tree, path, count, token, d.err, d.device,
-                                                     reinterpret_cast<cudaStream_t>(stream)}));
+                                                     d.sm_count, reinterpret_cast<cudaStream_t>(stream)}));
 }
 
 size_t w4a16_lora_workspace_bytes(int tokens, int rank, int inner) {

@@ -11,9 +11,6 @@
 namespace w4a16 {
 namespace {
 
-#ifndef PROB_LEAST
-#define PROB_LEAST 8192
-#endif
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kMaxCluster = 16;
 using u64 = unsigned long long;
@@ -44,8 +41,8 @@ struct Quads {
 // maximum, in registers while the cluster agrees on maximum and sum. Slices
 // that do not fit are read twice.
 // ---------------------------------------------------------------------------
-constexpr int kProbThreads = 512;
-constexpr int kProbQuads = 8;  // of a thread
+constexpr int kProbThreads = 256;
+constexpr int kProbQuads = 16;  // of a thread
 constexpr uint32_t kNone = 0xFF80FF80u;  // two bf16 -inf: no probability
 
 struct ProbParams {
@@ -90,7 +87,7 @@ __device__ __forceinline__ void store_quad(float *row, const Quads &q, int k, in
 
 __device__ __forceinline__ float exp2_fast(float y) {
   float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(y));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
   return r;
 }
 // 2^((l - m) a) of two logits
@@ -122,7 +119,7 @@ __device__ __forceinline__ void join(float &m, float &s, float a) {
 }
 
 template <bool ALIGNED>
-__global__ void __launch_bounds__(kProbThreads, 2) probabilities_kernel(const ProbParams p) {
+__global__ void __launch_bounds__(kProbThreads, 4) probabilities_kernel(const ProbParams p) {
   constexpr int kWarps = kProbThreads / 32;
   __shared__ u64 slots[kMaxCluster], warps[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -141,11 +138,10 @@ __global__ void __launch_bounds__(kProbThreads, 2) probabilities_kernel(const Pr
   // a logit of -inf stays -inf through difference and product, whatever the temperature
   const float lowest = -3.40282347e38f, a = greedy ? 1.f : fmaxf(fminf(__fdiv_rn(1.44269502f, t), 1e30f), 1e-44f);
   const f32x2 a2 = f32_pair(a, a);
-  float2 e[kProbQuads][2];
+  uint2 x[kProbQuads];
   float m = lowest, s = 0.f, mine = lowest;
   u64 best = 0;
   for (int k0 = q.lo; k0 < q.hi; k0 += kProbThreads * kProbQuads) {
-    uint2 x[kProbQuads];
 #pragma unroll
     for (int u = 0; u < kProbQuads; ++u) {
       const int k = k0 + u * kProbThreads + tid;
@@ -177,9 +173,8 @@ __global__ void __launch_bounds__(kProbThreads, 2) probabilities_kernel(const Pr
     f32x2 sum = 0;
 #pragma unroll
     for (int u = 0; u < kProbQuads; ++u) {
-      e[u][0] = powers(x[u].x, minus, a2);
-      e[u][1] = powers(x[u].y, minus, a2);
-      sum = add2(sum, add2(f32_pair(e[u][0].x, e[u][0].y), f32_pair(e[u][1].x, e[u][1].y)));
+      const float2 v = powers(x[u].x, minus, a2), w = powers(x[u].y, minus, a2);
+      sum = add2(sum, add2(f32_pair(v.x, v.y), f32_pair(w.x, w.y)));
     }
     const float2 both = f32_halves(sum);
     const float high = fmaxf(m, mine);  // (more than one chunk: joined with the ones before)
@@ -191,10 +186,10 @@ __global__ void __launch_bounds__(kProbThreads, 2) probabilities_kernel(const Pr
     for (int o = 16; o > 0; o >>= 1) best = key_max(best, __shfl_xor_sync(kFull, best, o));
     if (lane == 0) warps[warp] = best;
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 0) {  // (every lane gets it: up to 16 write it to the cluster's CTAs)
       best = lane < kWarps ? warps[lane] : 0;
 #pragma unroll
-      for (int o = kWarps / 2; o > 0; o >>= 1) best = key_max(best, __shfl_xor_sync(kFull, best, o));
+      for (int o = 16; o > 0; o >>= 1) best = key_max(best, __shfl_xor_sync(kFull, best, o));
     }
     cluster_wait();
     if (tid < (int)S) st_cluster_u64(mapa_shared(smem_u32(&slots[rank]), tid), best);
@@ -215,7 +210,7 @@ __global__ void __launch_bounds__(kProbThreads, 2) probabilities_kernel(const Pr
     const float2 v = lane < kWarps ? f32_halves(warps[lane]) : make_float2(lowest, 0.f);
     m = v.x;
     s = v.y;
-    join<kWarps>(m, s, a);
+    join<32>(m, s, a);
   }
   cluster_wait();
   if (tid < (int)S) st_cluster_u64(mapa_shared(smem_u32(&slots[rank]), tid), f32_pair(m, s));
@@ -228,14 +223,13 @@ __global__ void __launch_bounds__(kProbThreads, 2) probabilities_kernel(const Pr
   // each thread's logits are still in registers, where the slice is one chunk and the sum is a number (else a dropped
   // logit's 0 has to be told from a kept one's)
   if (q.hi - q.lo <= kProbThreads * kProbQuads && s == s) {
-    const float f = mine == m ? inv : inv * exp2_fast((mine - m) * a);
-    const f32x2 f2 = f32_pair(f, f);
+    const f32x2 f2 = f32_pair(inv, inv), minus = f32_pair(-m, -m);
 #pragma unroll
     for (int u = 0; u < kProbQuads; ++u) {
       const int k = q.lo + u * kProbThreads + tid;
+      const float2 v = powers(x[u].x, minus, a2), w = powers(x[u].y, minus, a2);
       if (k < q.hi)
-        store_quad<ALIGNED>(out, q, k, p.vocab, f32_halves(mul2(f32_pair(e[u][0].x, e[u][0].y), f2)),
-                            f32_halves(mul2(f32_pair(e[u][1].x, e[u][1].y), f2)));
+        store_quad<ALIGNED>(out, q, k, p.vocab, f32_halves(mul2(f32_pair(v.x, v.y), f2)), f32_halves(mul2(f32_pair(w.x, w.y), f2)));
     }
     return;
   }
@@ -270,8 +264,6 @@ __global__ void __launch_bounds__(kProbThreads, 2) probabilities_kernel(const Pr
 // number falls next to one of 248,320 borders (32-bit sums are off by 1e-7,
 // which moves it in one draw of a hundred).
 // ---------------------------------------------------------------------------
-constexpr int kSampleThreads = 512;
-constexpr int kSampleWarps = kSampleThreads / 32;
 constexpr int kFrac = 56;
 constexpr unsigned long long kOne = 1ull << kFrac;
 
@@ -299,9 +291,9 @@ struct Order {
 
 struct SampleSmem {
   Order order;
-  u64 sums[kMaxCluster], warps[kSampleWarps];
+  u64 sums[kMaxCluster], warps[16], fine[16];
   // first CTA: nodes of the tree
-  u64 kids[kMaxTree];
+  u64 kids[kMaxTree], fits;  // fits: nodes that are accepted if they are asked first
   double px[kMaxTree], qx[kMaxTree];
   float u[kMaxTree];
   int ids[kMaxTree], path[kMaxTree];
@@ -309,7 +301,17 @@ struct SampleSmem {
 };
 
 __device__ __forceinline__ float sound(float p) { return fminf(fmaxf(p, 0.f), 1.f); }  // (NaN: 0)
-__device__ __forceinline__ u64 fixed(float p) { return __float2ull_rz(sound(p) * 72057594037927936.f); }
+// p in units of 2^-56, what is below cut off: the 24 bits of its mantissa, moved
+// to their place. (A conversion to 64-bit integers would run on the double
+// precision pipe: 32 rows of two times 248,320 took 85 us, three quarters of it
+// that pipe's.)
+__device__ __forceinline__ u64 fixed(float p) {
+  const uint32_t x = __float_as_uint(sound(p));
+  const u64 top = (u64)((x & 0x7FFFFFu) | 0x800000u) << 33;
+  u64 v;
+  asm("shr.u64 %0, %1, %2;" : "=l"(v) : "l"(top), "r"(127u - (x >> 23)));  // (64 places and more: 0)
+  return v;
+}
 
 // max(p - c q, 0)
 __device__ __forceinline__ u64 weight(float p, float q, u64 c) {
@@ -360,12 +362,15 @@ struct Walk {
       }
       const int i = __ffsll((long long)kids) - 1;
       kids &= kids - 1;
-      const double left = asked ? (double)total * 0x1p-56 : 1.0;
-      double r = sm.px[i];
-      if (drawn) r -= (double)c * 0x1p-56 * sm.qx[i];
-      for (int g = 0; g < gone; ++g)
-        if (o.ids[g] == sm.ids[i]) r = 0;
-      if ((double)sm.u[i] * sm.qx[i] * left < r) {
+      bool fits = sm.fits >> i & 1;
+      if (asked) {
+        double r = sm.px[i];
+        if (drawn) r -= (double)c * 0x1p-56 * sm.qx[i];
+        for (int g = 0; g < gone; ++g)
+          if (o.ids[g] == sm.ids[i]) r = 0;
+        fits = (double)sm.u[i] * sm.qx[i] * ((double)total * 0x1p-56) < r;
+      }
+      if (fits) {
         sm.path[sm.accepted++] = i;
         stand(i, sm);
         o.row = first + node;
@@ -403,8 +408,9 @@ struct Walk {
   }
 };
 
-template <bool ALIGNED>
-__global__ void __launch_bounds__(kSampleThreads, 2) tree_sample_kernel(const SampleParams p) {
+template <bool ALIGNED, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) tree_sample_kernel(const SampleParams p) {
+  static_assert(WARPS <= 16 && (WARPS & (WARPS - 1)) == 0 && WARPS * 32 >= kMaxTree, "parts of a row, nodes of a tree");
   __shared__ SampleSmem sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t S = cluster_nctarank(), rank = cluster_ctarank();
@@ -413,6 +419,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) tree_sample_kernel(const Sa
   grid_dependency_wait();
   grid_launch_dependents();
   const bool drawn = p.q != nullptr;
+  const int parts_log2 = __ffs(S * WARPS) - 1;
   Walk walk;
   int n = 0, s0 = 0;
   if (rank == 0) {
@@ -427,6 +434,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) tree_sample_kernel(const Sa
     if (tid == 0) {
       sm.accepted = 0;
       sm.path[0] = 0;
+      sm.fits = 0;
     }
     __syncthreads();
     if (tid < n) {
@@ -438,9 +446,12 @@ __global__ void __launch_bounds__(kSampleThreads, 2) tree_sample_kernel(const Sa
         const int64_t id = p.draft[s0 + tid];
         if (id >= 0 && id < p.vocab) {
           sm.ids[tid] = (int)id;
-          sm.px[tid] = sound(p.p[(s0 + parent) * p.p_row + id]);
-          sm.qx[tid] = drawn ? sound(p.q[(s0 + parent) * p.q_row + id]) : 1.0;
+          const double px = sound(p.p[(s0 + parent) * p.p_row + id]);
+          const double qx = drawn ? sound(p.q[(s0 + parent) * p.q_row + id]) : 1.0;
+          sm.px[tid] = px;
+          sm.qx[tid] = qx;
           atomicOr(&sm.kids[parent], 1ull << tid);
+          if ((double)sm.u[tid] * qx < px) atomicOr(&sm.fits, 1ull << tid);
         } else {
           atomicOr(p.err, kErrIndex);
         }
@@ -464,7 +475,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) tree_sample_kernel(const Sa
       __syncthreads();
       const uint32_t words = sizeof(Order) / 4;
       const uint32_t used = offsetof(Order, ids) / 4 + (sm.order.what == kDraw ? sm.order.gone : 0);
-      for (uint32_t i = tid; i < used * S; i += kSampleThreads) {
+      for (uint32_t i = tid; i < used * S; i += WARPS * 32) {
         const uint32_t to = i / used, w = i % used;
         if (to && w < words)
           st_cluster_u32(mapa_shared(smem_u32(&sm.order) + 4 * w, to), reinterpret_cast<const uint32_t *>(&sm.order)[w]);
@@ -478,7 +489,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) tree_sample_kernel(const Sa
     // this warp's part of the row
     const float *pr = p.p + row * p.p_row, *qr = p.q + row * p.q_row;
     const int shift = ALIGNED ? (int)((row * p.p_row) & 3) : 0;
-    const Quads mine(p.vocab, shift, rank * kSampleWarps + warp, __ffs(S * kSampleWarps) - 1);
+    const Quads mine(p.vocab, shift, rank * WARPS + warp, parts_log2);
     u64 sum = 0;
     if (c == 0) {
 #pragma unroll 4
@@ -509,7 +520,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) tree_sample_kernel(const Sa
     if (tid < (int)S) {
       u64 all = 0;
 #pragma unroll
-      for (int w = 0; w < kSampleWarps; ++w) all += sm.warps[w];
+      for (int w = 0; w < WARPS; ++w) all += sm.warps[w];
       st_cluster_u64(mapa_shared(smem_u32(&sm.sums[rank]), tid), all);
     }
     const float u = sm.order.u;
@@ -537,24 +548,42 @@ __global__ void __launch_bounds__(kSampleThreads, 2) tree_sample_kernel(const Sa
     none = 0;
     // the first element at which the running sum passes u * total
     const u64 goal = __umul64hi(total, __float2ull_rz(fminf(fmaxf(u, 0.f), 0.99999994f) * 18446744073709551616.f));
+    if (goal < before || goal - before >= sm.sums[rank]) break;
+    // in this CTA's slice: which warp's part of it, and all warps look through that
     u64 run = before;
-    for (int w = 0; w < warp; ++w) run += sm.warps[w];
-    if (goal < run || goal - run >= sm.warps[warp]) break;
-    for (int k0 = mine.lo; k0 < mine.hi; k0 += 32) {
-      const int k = k0 + lane;
-      float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
-      if (k < mine.hi) {
-        load_floats<ALIGNED>(pr, mine, k, p.vocab, x);
-        if (c) load_floats<ALIGNED>(qr, mine, k, p.vocab, y);
-      }
-      u64 part[4], four = 0;
+    int part = 0;
+    while (part < WARPS - 1 && goal - run >= sm.warps[part]) run += sm.warps[part++];
+    const Quads theirs(p.vocab, shift, rank * WARPS + part, parts_log2);
+    const int each = (theirs.hi - theirs.lo + WARPS - 1) / WARPS;
+    const int lo = theirs.lo + warp * each, hi = min(lo + each, theirs.hi);
+    auto weights = [&](int k, u64 (&v)[4]) {
+      float x[4], y[4] = {0.f, 0.f, 0.f, 0.f};
+      load_floats<ALIGNED>(pr, theirs, k, p.vocab, x);
+      if (c) load_floats<ALIGNED>(qr, theirs, k, p.vocab, y);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        part[i] = c ? weight(x[i], y[i], c) : fixed(x[i]);
+        v[i] = c ? weight(x[i], y[i], c) : fixed(x[i]);
         for (int g = 0; g < gone; ++g)
-          if (sm.order.ids[g] == 4 * k - shift + i) part[i] = 0;
-        four += part[i];
+          if (sm.order.ids[g] == 4 * k - shift + i) v[i] = 0;
       }
+    };
+    u64 v[4];
+    sum = 0;
+    for (int k = lo + lane; k < hi; k += 32) {
+      weights(k, v);
+      sum += v[0] + v[1] + v[2] + v[3];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    if (lane == 0) sm.fine[warp] = sum;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) run += sm.fine[w];
+    if (goal < run || goal - run >= sum) break;
+    for (int k0 = lo; k0 < hi; k0 += 32) {  // (a part of 2,048 elements: once)
+      const int k = k0 + lane;
+      if (k >= hi) v[0] = v[1] = v[2] = v[3] = 0;
+      if (k < hi && each > 32) weights(k, v);  // (else they are still there)
+      const u64 four = v[0] + v[1] + v[2] + v[3];
       u64 upto = four;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -564,9 +593,9 @@ __global__ void __launch_bounds__(kSampleThreads, 2) tree_sample_kernel(const Sa
       const uint32_t past = __ballot_sync(kFull, run + upto > goal);
       if (past) {
         if (lane == __ffs(past) - 1) {
-          u64 v = run + upto - four;
+          u64 at = run + upto - four;
           int i = 0;
-          while (i < 3 && v + part[i] <= goal) v += part[i++];
+          while (i < 3 && at + v[i] <= goal) at += v[i++];
           p.token[b] = 4 * k - shift + i;
         }
         break;
@@ -628,10 +657,12 @@ cudaError_t launch_rows(void (*kern)(P), PerDevice &fits16, int rows, int want, 
   return cudaLaunchKernelEx(&lc, kern, params);
 }
 
-// CTAs for a row: a power of two that leaves each about `least` elements
-int ctas_of(int vocab, int least) {
+// CTAs of a row: the fewest (a power of two) that leave each `most` elements at
+// most; with few rows more of them, up to `fit` in all, while each keeps `least`.
+int ctas_of(int rows, int vocab, int most, int least, int fit) {
   int s = 1;
-  while (s < kMaxCluster && vocab >= 2LL * least * s) s *= 2;
+  while (s < kMaxCluster && vocab > (long long)most * s) s *= 2;
+  while (s < kMaxCluster && 2LL * rows * s <= fit && vocab >= 2LL * least * s) s *= 2;
   return s;
 }
 
@@ -640,23 +671,28 @@ bool address(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 }  // namespace
 
 cudaError_t launch_probabilities(const uint16_t *logits, long long row, const float *temperature, const float *floor,
-                                 int tokens, int vocab, float *out, int device, cudaStream_t stream) {
+                                 int tokens, int vocab, float *out, int device, int sm_count, cudaStream_t stream) {
   static PerDevice fits[2];
   // quads of logits and of probabilities are aligned together
   const bool aligned = address(logits, 8) && address(out, 16) && (row - vocab) % 4 == 0;
   const ProbParams p{logits, row, temperature, floor, out, vocab};
-  const int s = ctas_of(vocab, PROB_LEAST);
+  const int s = ctas_of(tokens, vocab, kProbThreads * kProbQuads * 4, 1024, sm_count * 4);
   return launch_rows(aligned ? probabilities_kernel<true> : probabilities_kernel<false>, fits[aligned], tokens, s,
                      kProbThreads, device, stream, p);
 }
 
 cudaError_t launch_tree_sample(const SampleCall &c) {
-  static PerDevice fits[2];
+  static PerDevice fits[2][2];
   const bool aligned = address(c.p, 16) && address(c.q, 16) && (!c.q || (c.q_row - c.p_row) % 4 == 0);
   const SampleParams p{c.p, c.q, c.p_row, c.q_row, c.draft, c.mask, c.starts, c.u, c.rows, c.tokens, c.vocab, c.max_tree,
                        c.path, c.count, c.token, c.err};
-  return launch_rows(aligned ? tree_sample_kernel<true> : tree_sample_kernel<false>, fits[aligned], c.rows,
-                     ctas_of(c.vocab, 4096), kSampleThreads, c.device, c.stream, p);
+  // 16 warps a CTA while the rows' clusters are all there at once, 8 where that makes more of them
+  const int s = ctas_of(c.rows, c.vocab, 32768, 1024, c.sm_count * 2);
+  if ((long long)c.rows * s * 2 <= c.sm_count * 2)
+    return launch_rows(aligned ? tree_sample_kernel<true, 16> : tree_sample_kernel<false, 16>, fits[0][aligned], c.rows, s, 512,
+                       c.device, c.stream, p);
+  return launch_rows(aligned ? tree_sample_kernel<true, 8> : tree_sample_kernel<false, 8>, fits[1][aligned], c.rows,
+                     ctas_of(c.rows, c.vocab, 32768, 1024, c.sm_count * 4), 256, c.device, c.stream, p);
 }
 
 }  // namespace w4a16

@@ -159,7 +159,7 @@ struct AttnCall {
 };
 // float32 probabilities [tokens][vocab] of bf16 logits
 cudaError_t launch_probabilities(const uint16_t *logits, long long row, const float *temperature, const float *floor,
-                                 int tokens, int vocab, float *out, int device, cudaStream_t stream);
+                                 int tokens, int vocab, float *out, int device, int sm_count, cudaStream_t stream);
 
 struct SampleCall {
   const float *p, *q;  // q null: picked children
@@ -171,7 +171,7 @@ struct SampleCall {
   int32_t *path, *count;
   int64_t *token;
   int *err;
-  int device;
+  int device, sm_count;
   cudaStream_t stream;
 };
 cudaError_t launch_tree_sample(const SampleCall &c);

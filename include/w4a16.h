@@ -454,8 +454,8 @@ int w4a16_tree_accept(const int64_t *target, const int64_t *draft, const int64_t
  *                or its maximum + T * log(share)), or NULL: none
  *
  * A row with nothing above -inf gets 0 throughout; a NaN (or +inf) that is kept
- * makes the row's kept probabilities NaN. Relative error below 2^-20 of each
- * probability, small ones too.
+ * makes the row's kept probabilities NaN. A probability is off by less than 2^-17 +
+ * 2^-23 (max - l_j) / T of itself; below 2^-126 it may be 0.
  */
 int w4a16_probabilities(const uint16_t *logits, int64_t logits_row, const float *temperature, const float *floor,
                         int tokens, int vocab, float *out, w4a16_stream_t stream);

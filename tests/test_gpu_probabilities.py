@@ -14,8 +14,8 @@ BF16 = torch.bfloat16
 def reference(logits, temperature=None, floor=None):
     """float64 probabilities and their bounds. e^((l - m) / T): the exponential is off by 2^-21 (ex2.approx 2^-22, its
     factor), the difference l - m, rounded to float32, by 2^-24 of itself, and so is the argument's second part; the sum of
-    up to 32 values of a thread, 9 joinings and 16 slices by 2^-18, the division and the product by 2^-23. Below 2^-126
-    float32 keeps steps of 2^-149."""
+    up to 64 values of a thread, two at a time, 8 joinings and 16 slices by 2^-18, the division and the product by 2^-23. A
+    power below 2^-126, the smallest normal number, becomes 0: relative to a sum of at least 1, so off by at most that."""
     x = logits.double().cpu()
     out, bound = torch.zeros_like(x), torch.zeros_like(x)
     for i in range(x.shape[0]):
@@ -28,7 +28,7 @@ def reference(logits, temperature=None, floor=None):
         if t > 0:
             e = torch.exp((x[i][kept] - m) / t)
             out[i, kept] = e / e.sum()
-            bound[i, kept] = out[i, kept] * (2.0 ** -17 + 2.0 ** -23 * (m - x[i][kept]) / t) + 2.0 ** -147
+            bound[i, kept] = out[i, kept] * (2.0 ** -17 + 2.0 ** -23 * (m - x[i][kept]) / t) + 2.0 ** -126
         else:
             out[i, int(torch.nonzero(kept & (x[i] == m))[0])] = 1.0
     return out, bound
