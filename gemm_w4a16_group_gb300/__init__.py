@@ -943,6 +943,32 @@ def probabilities(logits, temperature=None, floor=None, out=None, stream=None):
     return out
 
 
+def _walk_outputs(rows, max_tree, like, dev, stream, handle):
+    """path, count and token of a walk's rows, as three _small_out calls give
+    them, looked up at once (1.0 us against 4.7)."""
+    ty = _types()
+    shapes = (((rows, max_tree), ty.i32), ((rows,), ty.i32), ((rows,), ty.i64))
+    if _capturing(stream):
+        return [_empty(shape, dtype, like, stream) for shape, dtype in shapes]
+    key = (rows, max_tree, dev, handle)
+    try:
+        return _small_outputs[key].pop()
+    except (KeyError, IndexError):
+        pass
+    if rows * max_tree * 4 > _SMALL or rows * 8 > _SMALL or rows == 0 or max_tree <= 0:
+        return [_empty(shape, dtype, like, stream) for shape, dtype in shapes]
+    torch = _torch()
+    if torch.is_inference_mode_enabled():
+        with torch.inference_mode(False):
+            return _walk_outputs(rows, max_tree, like, dev, stream, handle)
+    ready = list(zip(*(_empty((_AT_ONCE * rows, *shape[1:]), dtype, like, stream).unsafe_split(rows) for shape, dtype in shapes)))
+    out = ready.pop()
+    if len(_small_outputs) >= 256:
+        _small_outputs.clear()
+    _small_outputs[key] = ready
+    return out
+
+
 def tree_sample(p, q, draft, mask, starts, u, max_tree, path=None, count=None, token=None, stream=None):
     """Sampled acceptance down each row's draft tree: p and q float32 [tokens,
     vocab], the target's and the drafter's probabilities after each token (rows
@@ -960,17 +986,22 @@ def tree_sample(p, q, draft, mask, starts, u, max_tree, path=None, count=None, t
             raise ValueError(f"q has shape {shape}, p {[tokens, vocab]}")
     rows = starts.numel() - 1
     handle = _on(stream, p)
-    if path is None:
-        path = _small_out((rows, max_tree), ty.i32, p, dev, stream, handle.value)
-    if count is None:
-        count = _small_out((rows,), ty.i32, p, dev, stream, handle.value)
-    if token is None:
-        token = _small_out((rows,), ty.i64, p, dev, stream, handle.value)
+    if path is None and count is None and token is None:
+        path, count, token = _walk_outputs(rows, max_tree, p, dev, stream, handle.value)
+        outs = path.data_ptr(), count.data_ptr(), token.data_ptr()
+    else:
+        if path is None:
+            path = _small_out((rows, max_tree), ty.i32, p, dev, stream, handle.value)
+        if count is None:
+            count = _small_out((rows,), ty.i32, p, dev, stream, handle.value)
+        if token is None:
+            token = _small_out((rows,), ty.i64, p, dev, stream, handle.value)
+        outs = (_flat(path, ty.i32, "path", rows * max_tree, dev), _flat(count, ty.i32, "count", rows, dev),
+                _flat(token, ty.i64, "token", rows, dev))
     args = (pp, p_row, qp, q_row, vocab, _flat(draft, ty.i64, "draft", tokens, dev),
             None if mask is None else _flat(mask, ty.i64, "mask", tokens, dev),
             _flat(starts, ty.i32, "starts", rows + 1, dev), _flat(u, ty.f32, "u", tokens, dev), rows, tokens, max_tree,
-            _flat(path, ty.i32, "path", rows * max_tree, dev), _flat(count, ty.i32, "count", rows, dev),
-            _flat(token, ty.i64, "token", rows, dev), handle)
+            *outs, handle)
     if rows == 0 or tokens == 0:
         _check(0 if 1 <= max_tree <= MAX_TREE else -1, "w4a16_tree_sample")
         return _fill(path, -1, stream), _fill(count, 0, stream), _fill(token, -1, stream)
@@ -1067,17 +1098,16 @@ def lora_workspace_bytes(tokens: int, rank: int, inner: int) -> int:
     return int(lib().w4a16_lora_workspace_bytes(tokens, rank, inner))
 
 
-def _store(t, name, dev):
-    """Pointer, strides and shape of a bf16 [adapters, ., .] tensor whose last axis is contiguous."""
-    if t.dtype is not _types().bf16 or t.get_device() != dev:
-        _refuse(t, _types().bf16, name, dev)
-    shape = t.shape
-    if len(shape) != 3:
-        raise ValueError(f"{name} must have three axes, not {list(shape)}")
-    s = t.stride()
-    if s[2] != 1:
-        raise ValueError(f"{name}: the last axis must be contiguous")
-    return t.data_ptr(), s[0], s[1], shape
+def _refuse_lora(y, x, a, b, dev):
+    """Raise what is wrong with the operands of lora_add."""
+    for t, name, axes in ((y, "y", 2), (x, "x", 2), (a, "a", 3), (b, "b", 3)):
+        if t.dtype is not _types().bf16 or t.get_device() != dev:
+            _refuse(t, _types().bf16, name, dev)
+        if t.dim() != axes:
+            raise ValueError(f"{name} must have {axes} axes, not {list(t.shape)}")
+        if t.stride(-1) != 1 and t.shape[-1] > 1:
+            raise ValueError(f"{name}: the last axis must be contiguous")
+    raise ValueError(f"shapes do not fit: y {list(y.shape)}, x {list(x.shape)}, a {list(a.shape)}, b {list(b.shape)}")
 
 
 def lora_add(y, x, a, b, adapter, starts=None, scale=None, out=None, workspace=None, stream=None):
@@ -1091,38 +1121,43 @@ def lora_add(y, x, a, b, adapter, starts=None, scale=None, out=None, workspace=N
     `workspace` (uint8, lora_workspace_bytes) the call uses one that the module
     keeps for its stream; a given one belongs to one call at a time."""
     ty, dev = _types(), _place(y, "y")
-    yp, y_row, tokens, outer = _matrix(y, ty.bf16, "y", dev)
-    xp, x_row, x_tokens, inner = _matrix(x, ty.bf16, "x", dev)
-    ap, a_adapter, a_row, (adapters, rank, a_inner) = _store(a, "a", dev)
-    bp, b_adapter, b_row, b_shape = _store(b, "b", dev)
-    if x_tokens != tokens or a_inner != inner or b_shape != (adapters, outer, rank):
-        raise ValueError(f"shapes do not fit: y {list(y.shape)}, x {list(x.shape)}, a {list(a.shape)}, b {list(b_shape)}")
+    bf16 = ty.bf16
+    # (all four at once: one after the other they cost 2 us, these 1.3)
+    try:
+        (tokens, outer), (x_tokens, inner), (adapters, rank, a_inner) = y.shape, x.shape, a.shape
+        (y_row, y_one), (x_row, x_one), (a_adapter, a_row, a_one), (b_adapter, b_row, b_one) = y.stride(), x.stride(), a.stride(), b.stride()
+        fit = (x_tokens == tokens and a_inner == inner and b.shape == (adapters, outer, rank) and y.dtype is bf16 and x.dtype is bf16
+               and a.dtype is bf16 and b.dtype is bf16 and x.get_device() == dev and a.get_device() == dev and b.get_device() == dev
+               and (y_one == 1 or outer == 1) and (x_one == 1 or inner == 1) and (a_one == 1 or inner == 1) and (b_one == 1 or rank == 1))
+    except ValueError:
+        fit = False
+    if not fit:
+        _refuse_lora(y, x, a, b, dev)
     rows = adapter.numel()
     if starts is None and rows != tokens:
         raise ValueError(f"adapter has {rows} elements, without starts the call needs {tokens}")
-    if rows and tokens:
-        need = lora_workspace_bytes(tokens, rank, inner)
-        if need == 0:
-            raise W4A16Error(f"lora_add: unsupported tokens={tokens} rank={rank} inner={inner}")
     handle = _on(stream, y)
     if out is None:
         # (as in tree_attention)
         if 2 * tokens * outer <= _SMALL:
-            out = _small_out((tokens, outer), ty.bf16, y, dev, stream, handle.value)
+            out = _small_out((tokens, outer), bf16, y, dev, stream, handle.value)
         else:
-            out = _empty((tokens, outer), ty.bf16, y, stream)
+            out = _empty((tokens, outer), bf16, y, stream)
         op, out_row = out.data_ptr(), outer
     else:
-        op, out_row, *shape = _matrix(out, ty.bf16, "out", dev)
+        op, out_row, *shape = _matrix(out, bf16, "out", dev)
         if shape != [tokens, outer]:
             raise ValueError(f"out has shape {shape}, y {[tokens, outer]}")
-    args = (yp, y_row, xp, x_row, ap, a_adapter, a_row, bp, b_adapter, b_row,
+    args = (y.data_ptr(), y_row, x.data_ptr(), x_row, a.data_ptr(), a_adapter, a_row, b.data_ptr(), b_adapter, b_row,
             None if scale is None else _flat(scale, ty.f32, "scale", adapters, dev),
             _flat(adapter, ty.i32, "adapter", rows, dev),
             None if starts is None else _flat(starts, ty.i32, "starts", rows + 1, dev), rows, tokens, adapters, rank, inner,
             outer, op, out_row)
     if rows == 0 or tokens == 0:
         return out
+    need = lora_workspace_bytes(tokens, rank, inner)
+    if need == 0:
+        raise W4A16Error(f"lora_add: unsupported tokens={tokens} rank={rank} inner={inner}")
     call = lib().w4a16_lora_add
     if workspace is not None:
         if workspace.dtype is not ty.u8 or workspace.get_device() != dev or not workspace.is_contiguous() or workspace.numel() < need:

@@ -676,7 +676,7 @@ cudaError_t launch_probabilities(const uint16_t *logits, long long row, const fl
   // quads of logits and of probabilities are aligned together
   const bool aligned = address(logits, 8) && address(out, 16) && (row - vocab) % 4 == 0;
   const ProbParams p{logits, row, temperature, floor, out, vocab};
-  const int s = ctas_of(tokens, vocab, kProbThreads * kProbQuads * 4, 1024, sm_count * 4);
+  const int s = ctas_of(tokens, vocab, kProbThreads * kProbQuads * 4, 4096, sm_count * 4);
   return launch_rows(aligned ? probabilities_kernel<true> : probabilities_kernel<false>, fits[aligned], tokens, s,
                      kProbThreads, device, stream, p);
 }
