@@ -709,7 +709,7 @@ int w4a16_lora_add(const uint16_t *y, int64_t y_row, const uint16_t *x, int64_t 
   c.inner = inner;
   c.outer = outer;
   c.out = out;
-  c.workspace = static_cast<float *>(workspace);
+  c.workspace = workspace;
   c.err = d.err;
   c.device = d.device;
   c.sm_count = d.sm_count;

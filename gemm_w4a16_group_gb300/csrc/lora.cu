@@ -30,9 +30,12 @@ struct LoraParams {
   const int32_t *adapter, *starts;
   int rows, tokens, adapters, rank, inner, outer, ksplit;
   uint16_t *out;
-  float *parts;  // [ksplit][tokens][RP]
+  float *parts;  // few tokens: x A^T in parts, [ksplit][tokens][RP]
+  // prompts: x A^T as two bf16 parts, [tokens][2][RP]; how many tiles there are (with an adapter, in all); the tiles
+  uint16_t *low;
+  int *head, *lists;
   int *err;
-  bool in_place;
+  bool in_place, alike;  // alike: rows of y and of out begin equally far after 16-byte boundaries
 };
 
 __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -273,6 +276,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t *>(&b);
 }
+// Two values as two bf16 parts each (16 bits of mantissa): the upper ones, and
+// what they leave. (What an infinite value leaves is not a number: 0.)
+__device__ __forceinline__ uint2 two_parts(float a, float b) {
+  const uint32_t hi = pack_bf16(a, b);
+  const float x = bf16lo_to_f32(hi), y = bf16hi_to_f32(hi);
+  return make_uint2(hi, pack_bf16(fabsf(x) < INFINITY ? a - x : 0.f, fabsf(y) < INFINITY ? b - y : 0.f));
+}
+
 
 // eight columns of a row from column c on, `wide`: as one 16-byte access
 __device__ __forceinline__ uint4 load8(const uint16_t *row, int c, int n, bool wide) {
@@ -359,12 +370,9 @@ __global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const __grid_c
         }
         v.x *= scale;
         v.y *= scale;
-        const uint32_t hi = pack_bf16(v.x, v.y);
-        const float hx = bf16lo_to_f32(hi), hy = bf16hi_to_f32(hi);
-        // (what is left of an infinite value is not a number)
-        const uint32_t low = pack_bf16(fabsf(hx) < INFINITY ? v.x - hx : 0.f, fabsf(hy) < INFINITY ? v.y - hy : 0.f);
-        *reinterpret_cast<uint32_t *>(smem + row * G::ROW + r * 2) = hi;
-        *reinterpret_cast<uint32_t *>(smem + G::OFF_LO + row * G::ROW + r * 2) = low;
+        const uint2 both = two_parts(v.x, v.y);
+        *reinterpret_cast<uint32_t *>(smem + row * G::ROW + r * 2) = both.x;
+        *reinterpret_cast<uint32_t *>(smem + G::OFF_LO + row * G::ROW + r * 2) = both.y;
       }
       __syncthreads();
     }
@@ -407,21 +415,428 @@ __global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const __grid_c
 }
 
 // ---------------------------------------------------------------------------
+// Prompts. shrink: a cluster of CTAs has a tile of 64 tokens, each a part of K,
+// which it streams through shared memory 128 k at a time; their sums meet over
+// distributed shared memory, and x A^T is written once, in its two parts.
+// ---------------------------------------------------------------------------
+constexpr int kTile = 64;
+constexpr int kListInts = 68;  // a tile's tokens, adapter and number of tokens
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int RP>
+struct PromptShrinkGeo {
+  static constexpr int K = 128;                 // of a stage
+  static constexpr int NB = RP / 8;
+  static constexpr int X = kTile * K * 2, STAGE = X + RP * K * 2;
+  static constexpr int STAGES = RP <= 32 ? 4 : RP == 64 ? 3 : 4;
+  static constexpr int CTAS = RP <= 64 ? 2 : 1;  // per SM
+  static constexpr int STRIDE = RP + 8;         // floats of a token's sums
+  static constexpr int OFF_PART = 4 * kTile * STRIDE * 4;  // (the sums and the CTA's part take the stages' place)
+  static constexpr int OFF_LIST = STAGES * STAGE, OFF_TILES = OFF_LIST + kTile * 4;
+  static_assert(OFF_PART + kTile * RP * 4 <= OFF_LIST, "sums after the stages");
+  static int smem(int adapters) { return OFF_TILES + Tiles::ints(adapters) * 4; }
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
+template <int RP>
+__global__ void __launch_bounds__(kThreads, PromptShrinkGeo<RP>::CTAS) lora_prompt_shrink_kernel(const __grid_constant__ LoraParams p) {
+  using G = PromptShrinkGeo<RP>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  int *list = reinterpret_cast<int *>(smem + G::OFF_LIST);
+  Tiles tiles(reinterpret_cast<int *>(smem + G::OFF_TILES), p.adapters);
+  const int parts = (int)cluster_nctarank(), part = (int)cluster_ctarank(), tile = (int)cluster_id_x();
+  grid_dependency_wait();
+  grid_launch_dependents();
+  tiles.make<kTile>(p);
+  const int all = tiles.first[p.adapters + 1];
+  if (tile == 0 && part == 0 && threadIdx.x == 0) {
+    p.head[0] = tiles.first[p.adapters];
+    p.head[1] = all;
+  }
+  if (tile >= all) return;  // (all CTAs of the cluster do)
+  const int e = tiles.of(tile), lo = (tile - tiles.first[e]) * kTile, n = min(kTile, tiles.count[e] - lo);
+  if (e == p.adapters && p.in_place) return;
+  tiles.tokens(p, e, lo, lo + n, list);
+  if (part == 0) {
+    int *to = p.lists + (long long)tile * kListInts;
+    if (threadIdx.x < n) to[threadIdx.x] = list[threadIdx.x];
+    if (threadIdx.x == 0) {
+      to[kTile] = e;
+      to[kTile + 1] = n;
+    }
+  }
+  if (e == p.adapters) return;
+
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int mw = warp & 1, kw = warp >> 1;
+  const uint32_t base = smem_u32(smem);
+  const int steps = (p.inner + G::K - 1) / G::K;
+  const int s0 = (int)((long long)steps * part / parts), s1 = (int)((long long)steps * (part + 1) / parts);
+  // a thread copies the same 16 bytes of k of every 16th row
+  const int c = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+  const uint16_t *xr[kTile / 16];
+#pragma unroll
+  for (int i = 0; i < kTile / 16; ++i) xr[i] = r0 + i * 16 < n ? p.x + list[r0 + i * 16] * p.x_row : nullptr;
+  const uint16_t *ar = p.a + e * p.a_adapter + r0 * p.a_row;
+  // (every other row's halves change places: a fragment's rows then meet different banks)
+  const uint32_t to = base + r0 * 256 + ((c ^ ((r0 & 1) << 2)) << 4);
+  auto fetch = [&](int s) {
+    if (s < s1) {
+      const uint32_t at = to + (s - s0) % G::STAGES * G::STAGE;
+      const int k = s * G::K + c * 8;
+      const bool in = k < p.inner;
+#pragma unroll
+      for (int i = 0; i < kTile / 16; ++i)
+        if (xr[i]) copy16(at + i * 16 * 256, in ? xr[i] + k : xr[i], in);
+#pragma unroll
+      for (int i = 0; i < (RP + 15) / 16; ++i)
+        if (RP >= 16 || r0 < RP) {
+          const bool there = in && r0 + i * 16 < p.rank;
+          copy16(at + G::X + i * 16 * 256, there ? ar + i * 16 * p.a_row + k : ar, there);
+        }
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < G::STAGES - 1; ++i) fetch(s0 + i);
+  float acc[2][G::NB][4] = {};
+  const uint32_t from = base + g * 256 + (((kw * 4 + t) ^ ((g & 1) << 2)) << 4);
+  for (int s = s0; s < s1; ++s) {
+    copy_wait<G::STAGES - 2>();
+    __syncthreads();
+    fetch(s + G::STAGES - 1);
+    const uint32_t at = from + (s - s0) % G::STAGES * G::STAGE;
+    uint4 xv[2][2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) xv[m][h] = lds128(at + (mw * 32 + m * 16 + h * 8) * 256);
+#pragma unroll
+    for (int j = 0; j < G::NB; ++j) {
+      const uint4 av = lds128(at + G::X + j * 8 * 256);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        mma16(acc[m][j], xv[m][0].x, xv[m][1].x, xv[m][0].y, xv[m][1].y, av.x, av.y);
+        mma16(acc[m][j], xv[m][0].z, xv[m][1].z, xv[m][0].w, xv[m][1].w, av.z, av.w);
+      }
+    }
+  }
+  copy_wait<0>();
+  __syncthreads();
+  float *sums = reinterpret_cast<float *>(smem);
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int j = 0; j < G::NB; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float2 *>(sums + (kw * kTile + mw * 32 + m * 16 + h * 8 + g) * G::STRIDE + j * 8 + 2 * t) =
+            make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
+  __syncthreads();
+  for (int i = threadIdx.x; i < kTile * RP / 4; i += kThreads) {
+    const int row = i * 4 / RP, r = i * 4 % RP;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float4 u = *reinterpret_cast<const float4 *>(sums + (w * kTile + row) * G::STRIDE + r);
+      v.x += u.x;
+      v.y += u.y;
+      v.z += u.z;
+      v.w += u.w;
+    }
+    *reinterpret_cast<float4 *>(smem + G::OFF_PART + i * 16) = v;
+  }
+  cluster_sync_all();
+  const float scale = p.scale ? p.scale[e] : 1.f;
+  const int rows = kTile / parts;
+  for (int i = threadIdx.x; i < rows * RP / 4; i += kThreads) {
+    const int row = part * rows + i * 4 / RP, r = i * 4 % RP;
+    if (row >= n) break;
+    const uint32_t at = base + G::OFF_PART + (row * RP + r) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int q = 0; q < parts; ++q) {
+      const float4 u = ld_cluster_f4(mapa_shared(at, q));
+      v.x += u.x;
+      v.y += u.y;
+      v.z += u.z;
+      v.w += u.w;
+    }
+    const uint2 a = two_parts(v.x * scale, v.y * scale), b = two_parts(v.z * scale, v.w * scale);
+    uint16_t *out = p.low + (long long)list[row] * (2 * RP) + r;
+    *reinterpret_cast<uint2 *>(out) = make_uint2(a.x, b.x);
+    *reinterpret_cast<uint2 *>(out + RP) = make_uint2(a.y, b.y);
+  }
+  cluster_sync_all();  // (the others may still be reading this CTA's part)
+}
+
+// ---------------------------------------------------------------------------
+// expand: a CTA keeps 256 columns of B in registers for as many tiles of one
+// adapter as it comes by, 32 tokens a step. y is copied to shared memory two
+// steps ahead, x A^T with it; the products are added there in place, and a step
+// later the sums leave in whole rows of 512 bytes (the fragments' own 64 bytes
+// of eight rows reach 5.6 TB/s, rows 6.2: 4,096 x 34,816 elements, copied).
+//
+// Rows need not begin on 16 bytes: element c of a row that begins s elements
+// after such a boundary has place c + s, and places are moved eight at a time
+// (SHIFT; those at the ends of a row one by one).
+// ---------------------------------------------------------------------------
+template <int RP>
+struct PromptExpandGeo {
+  static constexpr int KS = RP < 32 ? 1 : RP / 32;
+  static constexpr int ROW = RP * 4 + (RP == 8 ? 16 : RP == 16 ? 32 : 64);  // bytes of a token: both parts, without bank conflicts
+  static constexpr int LOW = 32 * ROW;
+  static constexpr int PITCH = kColumns * 2 + 64;  // bytes of a token's y: 256 places and up to 7 more, without bank conflicts
+  static constexpr int OUT = 32 * PITCH;
+  static constexpr int OFF_OUT = 3 * LOW, OFF_LISTS = OFF_OUT + 4 * OUT;
+  static constexpr int SMEM = OFF_LISTS + 8 * kListInts * 4;
+  static constexpr int CTAS = RP <= 64 ? 2 : 1;  // per SM
+};
+
+template <int RP, bool SHIFT>
+__global__ void __launch_bounds__(kThreads, PromptExpandGeo<RP>::CTAS) lora_prompt_expand_kernel(const __grid_constant__ LoraParams p) {
+  using G = PromptExpandGeo<RP>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int *lists = reinterpret_cast<const int *>(smem + G::OFF_LISTS);
+  const uint32_t base = smem_u32(smem);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int chunks = (p.outer + kColumns - 1) / kColumns, tiles = __ldcg(p.head + (p.in_place ? 0 : 1));
+  const long long units = (long long)chunks * tiles, first = units * blockIdx.x / gridDim.x;
+  const int count = (int)(units * (blockIdx.x + 1) / gridDim.x - first);
+  if (count <= 0) return;
+
+  // A unit is a chunk of columns and a tile; the tiles of one chunk come one after the other. A step is half a unit's
+  // tokens. Unit i's list is in slot i of a ring of 8.
+  struct Step {
+    int unit, chunk, tile, half;
+  };
+  auto next_unit = [&](const Step &s) {
+    return s.tile + 1 < tiles ? Step{s.unit + 1, s.chunk, s.tile + 1, 0} : Step{s.unit + 1, s.chunk + 1, 0, 0};
+  };
+  auto list_of = [&](const Step &s) { return lists + (s.unit & 7) * kListInts; };
+  auto tokens_of = [&](const Step &s) { return min(list_of(s)[kTile + 1] - s.half * 32, 32); };
+  auto after = [&](const Step &s) {
+    return s.half == 0 && list_of(s)[kTile + 1] > 32 ? Step{s.unit, s.chunk, s.tile, 1} : next_unit(s);
+  };
+  auto fetch_list = [&](const Step &s) {
+    if (s.unit < count && threadIdx.x < kListInts / 4)
+      copy16(base + G::OFF_LISTS + (s.unit & 7) * kListInts * 4 + threadIdx.x * 16,
+             p.lists + (long long)s.tile * kListInts + threadIdx.x * 4, true);
+  };
+  // how many elements after a 16-byte boundary a token's row of out begins
+  auto shift_of = [&](int token) {
+    return SHIFT ? (int)((reinterpret_cast<uintptr_t>(p.out) / 2 + token * p.out_row) & 7) : 0;
+  };
+  // y and x A^T of a step; a warp brings y of four rows
+  auto fetch = [&](const Step &s, int low, int out) {
+    const int *list = list_of(s) + s.half * 32;
+    const int n = tokens_of(s), c0 = s.chunk * kColumns;
+    if (list_of(s)[kTile] < p.adapters) {
+#pragma unroll
+      for (int i = 0; i < (32 * RP / 4 + kThreads - 1) / kThreads; ++i) {
+        const int id = i * kThreads + threadIdx.x, row = id / (RP / 4), c = id % (RP / 4);
+        if (row < n)
+          copy16(base + low * G::LOW + row * G::ROW + c * 16, p.low + (long long)list[row] * (2 * RP) + c * 8, true);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = warp * 4 + i;
+      if (r >= n) break;
+      const int token = list[r], sh = shift_of(token), c = c0 + 8 * lane - sh;
+      const uint16_t *row = p.y + token * p.y_row;
+      const int at = G::OFF_OUT + out * G::OUT + r * G::PITCH + lane * 16;
+      if (c >= c0 && c + 8 <= p.outer && (!SHIFT || p.alike)) {
+        copy16(base + at, row + c, true);
+      } else {
+        uint16_t *to = reinterpret_cast<uint16_t *>(smem + at);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (c + k >= c0 && c + k < p.outer) to[k] = __ldcg(row + c + k);
+      }
+      if (SHIFT) {
+        const int last = c0 + kColumns - sh + lane;
+        if (lane < sh && last < p.outer)
+          *reinterpret_cast<uint16_t *>(smem + G::OFF_OUT + out * G::OUT + r * G::PITCH + (kColumns + lane) * 2) = __ldcg(row + last);
+      }
+    }
+  };
+  auto store = [&](const Step &s, int out) {
+    const int *list = list_of(s) + s.half * 32;
+    const int n = tokens_of(s), c0 = s.chunk * kColumns;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = warp * 4 + i;
+      if (r >= n) break;
+      const int token = list[r], sh = shift_of(token), c = c0 + 8 * lane - sh;
+      uint16_t *row = p.out + token * p.out_row;
+      const uint8_t *from = smem + G::OFF_OUT + out * G::OUT + r * G::PITCH;
+      const uint4 v = *reinterpret_cast<const uint4 *>(from + lane * 16);
+      if (c >= c0 && c + 8 <= p.outer) {
+        *reinterpret_cast<uint4 *>(row + c) = v;
+      } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (c + k >= c0 && c + k < p.outer) row[c + k] = (uint16_t)(w[k / 2] >> (k % 2 * 16));
+      }
+      if (SHIFT) {
+        const int last = c0 + kColumns - sh + lane;
+        if (lane < sh && last < p.outer) row[last] = *reinterpret_cast<const uint16_t *>(from + (kColumns + lane) * 2);
+      }
+    }
+  };
+
+  Step now{0, (int)(first / tiles), (int)(first % tiles), 0}, ahead = now;
+  Step listed = now;  // the next unit whose list is to be fetched
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    fetch_list(listed);
+    listed = next_unit(listed);
+  }
+  copy_commit();
+  copy_wait<0>();
+  __syncthreads();
+  // steps 0 and 1; a list is asked for when the unit two before it is fetched, and there two steps later
+  int low = 0, out = 0;  // slots of step `now`: 3 of x A^T, 4 of y
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (ahead.unit < count) {
+      fetch(ahead, i, i);
+      ahead = after(ahead);
+    }
+    copy_commit();
+  }
+  fetch_list(listed);
+  listed = next_unit(listed);
+  uint4 bv[4][G::KS];
+  int held_chunk = -1, held_adapter = -1;  // what bv is of
+  Step before = now;
+  bool begun = false;
+  while (now.unit < count) {
+    copy_wait<1>();
+    __syncthreads();  // this step's y and x A^T are there, and the sums of the step before
+    if (begun) store(before, (out + 3) & 3);
+    if (ahead.unit < count) {
+      const int unit = ahead.unit;
+      fetch(ahead, low == 0 ? 2 : low - 1, (out + 2) & 3);
+      ahead = after(ahead);
+      if (ahead.unit != unit) {
+        fetch_list(listed);
+        listed = next_unit(listed);
+      }
+    }
+    copy_commit();
+    const int e = list_of(now)[kTile], n = tokens_of(now);
+    if (e < p.adapters) {
+      if (now.chunk != held_chunk || e != held_adapter) {
+        held_chunk = now.chunk;
+        held_adapter = e;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int col = now.chunk * kColumns + warp * 32 + 8 * (g >> 1) + 2 * j + (g & 1);
+          const uint8_t *br = reinterpret_cast<const uint8_t *>(p.b + e * p.b_adapter + col * p.b_row);
+#pragma unroll
+          for (int s = 0; s < G::KS; ++s) {
+            const int k = RP < 32 ? t * (RP / 4) : s * 32 + t * 8;
+            bv[j][s] = col < p.outer && k < p.rank ? piece<RP>(br + k * 2) : make_uint4(0, 0, 0, 0);
+          }
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        if (m * 16 >= n) break;
+        float acc[4][4] = {};
+#pragma unroll
+        for (int s = 0; s < G::KS; ++s) {
+          const uint8_t *at = smem + low * G::LOW + (m * 16 + g) * G::ROW + (RP < 32 ? t * (RP / 2) : s * 64 + t * 16);
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            const uint4 a0 = piece<RP>(at + part * RP * 2), a1 = piece<RP>(at + part * RP * 2 + 8 * G::ROW);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              mma16(acc[j], a0.x, a1.x, a0.y, a1.y, bv[j][s].x, bv[j][s].y);
+              if (RP >= 32) mma16(acc[j], a0.z, a1.z, a0.w, a1.w, bv[j][s].z, bv[j][s].w);
+            }
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = m * 16 + h * 8 + g;
+          uint16_t *y = reinterpret_cast<uint16_t *>(smem + G::OFF_OUT + out * G::OUT + r * G::PITCH) + warp * 32 + 8 * t;
+          if (SHIFT) {
+            if (r >= n) continue;
+            y += shift_of(list_of(now)[now.half * 32 + r]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t v = pack_bf16(bf16lo_to_f32(y[2 * j]) + acc[j][2 * h], bf16lo_to_f32(y[2 * j + 1]) + acc[j][2 * h + 1]);
+              y[2 * j] = (uint16_t)v;
+              y[2 * j + 1] = (uint16_t)(v >> 16);
+            }
+          } else {
+            uint4 v = *reinterpret_cast<const uint4 *>(y);
+            v.x = pack_bf16(bf16lo_to_f32(v.x) + acc[0][2 * h], bf16hi_to_f32(v.x) + acc[0][2 * h + 1]);
+            v.y = pack_bf16(bf16lo_to_f32(v.y) + acc[1][2 * h], bf16hi_to_f32(v.y) + acc[1][2 * h + 1]);
+            v.z = pack_bf16(bf16lo_to_f32(v.z) + acc[2][2 * h], bf16hi_to_f32(v.z) + acc[2][2 * h + 1]);
+            v.w = pack_bf16(bf16lo_to_f32(v.w) + acc[3][2 * h], bf16hi_to_f32(v.w) + acc[3][2 * h + 1]);
+            *reinterpret_cast<uint4 *>(y) = v;
+          }
+        }
+      }
+    }
+    before = now;
+    begun = true;
+    now = after(now);
+    low = low == 2 ? 0 : low + 1;
+    out = (out + 1) & 3;
+  }
+  copy_wait<0>();
+  __syncthreads();
+  store(before, (out + 3) & 3);
+}
+
+// ---------------------------------------------------------------------------
 int padded_rank(int rank) { return rank <= 8 ? 8 : rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
 
-// Tokens of a tile: 16 while a tile of 64 would mostly be empty
-int tile_of(int tokens) { return tokens <= 512 ? 16 : 64; }
+// Few tokens take the first pair of kernels, 16 tokens a tile: a tile of 64
+// would mostly be empty.
+bool few(int tokens) { return tokens <= 512; }
 
-// Parts of K: as many CTAs as fit at once, but at least one step of 32 k for
-// each warp, and no more than 32 sums for expand to add up.
+// Few tokens: parts of K. As many CTAs as fit at once, but at least one step of
+// 32 k for each warp, and no more than 32 sums for expand to add up.
 int parts_of(int tokens, int rank, int inner) {
-  const int tile = tile_of(tokens), tiles = (tokens + tile - 1) / tile, step = 32 * (rank > 64 ? kWarps / 2 : kWarps);
-  const int want = (tile == 16 ? 304 : 152) / tiles, most = (inner + step - 1) / step;
+  const int tiles = (tokens + 15) / 16, step = 32 * (rank > 64 ? kWarps / 2 : kWarps);
+  const int want = 304 / tiles, most = (inner + step - 1) / step;
   return want < 1 ? 1 : want < most ? (want < 32 ? want : 32) : (most < 32 ? most : 32);
 }
 
+// Prompts: CTAs of a cluster, which share K: as many as bring the tiles to a
+// wave (two CTAs per SM), while each keeps 512 k.
+int cluster_of(int tokens, int inner, int sm_count) {
+  int s = 1;
+  while (s < 8 && (long long)(tokens / kTile) * s * 2 <= 2 * sm_count && inner >= 1024 * s) s *= 2;
+  return s;
+}
+
+// Prompts: tiles at most, whatever the rows' adapters
+long long most_tiles(int tokens, int groups) { return tokens / kTile + (long long)groups + 1; }
+
 template <class K>
-cudaError_t launch(K kern, unsigned grid, int smem, cudaStream_t stream, const LoraParams &p) {
+cudaError_t launch(K kern, unsigned grid, int cluster, int smem, cudaStream_t stream, const LoraParams &p) {
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -431,51 +846,79 @@ cudaError_t launch(K kern, unsigned grid, int smem, cudaStream_t stream, const L
   lc.blockDim = dim3(kThreads, 1, 1);
   lc.dynamicSmemBytes = smem;
   lc.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   lc.attrs = attr;
-  lc.numAttrs = 1;
+  lc.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&lc, kern, p);
 }
 
-template <int T, int RP>
-cudaError_t run(const LoraCall &c, const LoraParams &p, bool even) {
+template <int RP>
+cudaError_t run_few(const LoraCall &c, const LoraParams &p, bool even) {
   const int groups = c.adapters < c.rows ? c.adapters : c.rows;
-  const long long tiles = c.tokens / T + groups + 1;  // at most
+  const long long tiles = c.tokens / 16 + groups + 1;  // at most
   const long long shrink = tiles * p.ksplit, expand = tiles * ((c.outer + kColumns - 1) / kColumns);
   const long long cap = c.sm_count * 2;
-  const cudaError_t e = launch(lora_shrink_kernel<T, RP>, (unsigned)(shrink < cap ? shrink : cap),
-                               ShrinkGeo<T, RP>::smem(c.adapters), c.stream, p);
+  const cudaError_t e = launch(lora_shrink_kernel<16, RP>, (unsigned)(shrink < cap ? shrink : cap), 1,
+                               ShrinkGeo<16, RP>::smem(c.adapters), c.stream, p);
   if (e != cudaSuccess) return e;
-  return launch(even ? lora_expand_kernel<T, RP, true> : lora_expand_kernel<T, RP, false>,
-                (unsigned)(expand < cap ? expand : cap), ExpandGeo<T, RP>::smem(c.adapters), c.stream, p);
+  return launch(even ? lora_expand_kernel<16, RP, true> : lora_expand_kernel<16, RP, false>,
+                (unsigned)(expand < cap ? expand : cap), 1, ExpandGeo<16, RP>::smem(c.adapters), c.stream, p);
 }
 
-template <int T>
-cudaError_t run_rank(const LoraCall &c, const LoraParams &p, bool even) {
-  switch (padded_rank(c.rank)) {
-    case 8: return run<T, 8>(c, p, even);
-    case 16: return run<T, 16>(c, p, even);
-    case 32: return run<T, 32>(c, p, even);
-    case 64: return run<T, 64>(c, p, even);
-    default: return run<T, 128>(c, p, even);
-  }
+template <int RP>
+cudaError_t run_prompts(const LoraCall &c, const LoraParams &p, bool even) {
+  const int cluster = cluster_of(c.tokens, c.inner, c.sm_count);
+  const long long tiles = most_tiles(c.tokens, c.adapters < c.rows ? c.adapters : c.rows);
+  const cudaError_t e = launch(lora_prompt_shrink_kernel<RP>, (unsigned)(tiles * cluster), cluster,
+                               PromptShrinkGeo<RP>::smem(c.adapters), c.stream, p);
+  if (e != cudaSuccess) return e;
+  return launch(even ? lora_prompt_expand_kernel<RP, false> : lora_prompt_expand_kernel<RP, true>,
+                (unsigned)(c.sm_count * PromptExpandGeo<RP>::CTAS), 1, PromptExpandGeo<RP>::SMEM, c.stream, p);
+}
+
+template <int RP>
+cudaError_t run(const LoraCall &c, const LoraParams &p, bool even) {
+  return few(c.tokens) ? run_few<RP>(c, p, even) : run_prompts<RP>(c, p, even);
 }
 
 }  // namespace
 
 size_t lora_workspace_bytes(int tokens, int rank, int inner) {
-  return align_up((size_t)parts_of(tokens, rank, inner) * tokens * padded_rank(rank) * sizeof(float), 256);
+  const size_t row = padded_rank(rank) * sizeof(float);  // (two bf16 or one float32 a rank)
+  if (few(tokens)) return align_up((size_t)parts_of(tokens, rank, inner) * tokens * row, 256);
+  const int groups = tokens < kMaxAdapters ? tokens : kMaxAdapters;
+  return 256 + align_up(tokens * row, 256) + align_up((size_t)most_tiles(tokens, groups) * kListInts * sizeof(int), 256);
 }
 
 cudaError_t launch_lora_add(const LoraCall &c) {
-  const LoraParams p{c.y, c.x, c.a, c.b, c.y_row, c.x_row, c.a_adapter, c.a_row, c.b_adapter, c.b_row, c.out_row,
-                     c.scale, c.adapter, c.starts, c.rows, c.tokens, c.adapters, c.rank, c.inner, c.outer,
-                     parts_of(c.tokens, c.rank, c.inner), c.out, c.workspace, c.err, c.out == c.y && c.out_row == c.y_row};
+  LoraParams p{c.y, c.x, c.a, c.b, c.y_row, c.x_row, c.a_adapter, c.a_row, c.b_adapter, c.b_row, c.out_row,
+               c.scale, c.adapter, c.starts, c.rows, c.tokens, c.adapters, c.rank, c.inner, c.outer,
+               1, c.out, nullptr, nullptr, nullptr, nullptr, c.err, c.out == c.y && c.out_row == c.y_row,
+               (reinterpret_cast<uintptr_t>(c.out) - reinterpret_cast<uintptr_t>(c.y)) % 16 == 0 && (c.out_row - c.y_row) % 8 == 0};
+  uint8_t *ws = static_cast<uint8_t *>(c.workspace);
+  if (few(c.tokens)) {
+    p.ksplit = parts_of(c.tokens, c.rank, c.inner);
+    p.parts = reinterpret_cast<float *>(ws);
+  } else {
+    p.head = reinterpret_cast<int *>(ws);
+    p.low = reinterpret_cast<uint16_t *>(ws + 256);
+    p.lists = reinterpret_cast<int *>(ws + 256 + align_up((size_t)c.tokens * padded_rank(c.rank) * 4, 256));
+  }
   const uintptr_t bits = reinterpret_cast<uintptr_t>(c.y) | reinterpret_cast<uintptr_t>(c.out);
   const bool even = bits % 16 == 0 && c.y_row % 8 == 0 && c.out_row % 8 == 0;
-  return tile_of(c.tokens) == 16 ? run_rank<16>(c, p, even) : run_rank<64>(c, p, even);
+  switch (padded_rank(c.rank)) {
+    case 8: return run<8>(c, p, even);
+    case 16: return run<16>(c, p, even);
+    case 32: return run<32>(c, p, even);
+    case 64: return run<64>(c, p, even);
+    default: return run<128>(c, p, even);
+  }
 }
 
 }  // namespace w4a16

@@ -184,11 +184,12 @@ struct LoraCall {
   const int32_t *adapter, *starts;  // starts null: a token a row
   int rows, tokens, adapters, rank, inner, outer;
   uint16_t *out;
-  float *workspace;
+  void *workspace;
   int *err;
   int device, sm_count;
   cudaStream_t stream;
 };
+constexpr int kMaxAdapters = 4096;
 size_t lora_workspace_bytes(int tokens, int rank, int inner);
 cudaError_t launch_lora_add(const LoraCall &c);
 
