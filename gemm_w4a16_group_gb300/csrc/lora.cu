@@ -757,23 +757,31 @@ __global__ void __launch_bounds__(kThreads, PromptExpandGeo<RP>::CTAS) lora_prom
           }
         }
       }
+      // (both blocks of 16 tokens at once, eight sums that do not wait for one another)
+      float acc[2][4][4] = {};
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        if (m * 16 >= n) break;
-        float acc[4][4] = {};
+      for (int s = 0; s < G::KS; ++s)
 #pragma unroll
-        for (int s = 0; s < G::KS; ++s) {
-          const uint8_t *at = smem + low * G::LOW + (m * 16 + g) * G::ROW + (RP < 32 ? t * (RP / 2) : s * 64 + t * 16);
+        for (int part = 0; part < 2; ++part) {
+          uint4 a[2][2];
 #pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            const uint4 a0 = piece<RP>(at + part * RP * 2), a1 = piece<RP>(at + part * RP * 2 + 8 * G::ROW);
+          for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              mma16(acc[j], a0.x, a1.x, a0.y, a1.y, bv[j][s].x, bv[j][s].y);
-              if (RP >= 32) mma16(acc[j], a0.z, a1.z, a0.w, a1.w, bv[j][s].z, bv[j][s].w);
-            }
+            for (int h = 0; h < 2; ++h)
+              a[m][h] = piece<RP>(smem + low * G::LOW + (m * 16 + h * 8 + g) * G::ROW + part * RP * 2 + (RP < 32 ? t * (RP / 2) : s * 64 + t * 16));
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mma16(acc[m][j], a[m][0].x, a[m][1].x, a[m][0].y, a[m][1].y, bv[j][s].x, bv[j][s].y);
+          if (RP >= 32) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) mma16(acc[m][j], a[m][0].z, a[m][1].z, a[m][0].w, a[m][1].w, bv[j][s].z, bv[j][s].w);
           }
         }
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int r = m * 16 + h * 8 + g;
@@ -783,20 +791,19 @@ __global__ void __launch_bounds__(kThreads, PromptExpandGeo<RP>::CTAS) lora_prom
             y += shift_of(list_of(now)[now.half * 32 + r]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const uint32_t v = pack_bf16(bf16lo_to_f32(y[2 * j]) + acc[j][2 * h], bf16lo_to_f32(y[2 * j + 1]) + acc[j][2 * h + 1]);
+              const uint32_t v = pack_bf16(bf16lo_to_f32(y[2 * j]) + acc[m][j][2 * h], bf16lo_to_f32(y[2 * j + 1]) + acc[m][j][2 * h + 1]);
               y[2 * j] = (uint16_t)v;
               y[2 * j + 1] = (uint16_t)(v >> 16);
             }
           } else {
             uint4 v = *reinterpret_cast<const uint4 *>(y);
-            v.x = pack_bf16(bf16lo_to_f32(v.x) + acc[0][2 * h], bf16hi_to_f32(v.x) + acc[0][2 * h + 1]);
-            v.y = pack_bf16(bf16lo_to_f32(v.y) + acc[1][2 * h], bf16hi_to_f32(v.y) + acc[1][2 * h + 1]);
-            v.z = pack_bf16(bf16lo_to_f32(v.z) + acc[2][2 * h], bf16hi_to_f32(v.z) + acc[2][2 * h + 1]);
-            v.w = pack_bf16(bf16lo_to_f32(v.w) + acc[3][2 * h], bf16hi_to_f32(v.w) + acc[3][2 * h + 1]);
+            v.x = pack_bf16(bf16lo_to_f32(v.x) + acc[m][0][2 * h], bf16hi_to_f32(v.x) + acc[m][0][2 * h + 1]);
+            v.y = pack_bf16(bf16lo_to_f32(v.y) + acc[m][1][2 * h], bf16hi_to_f32(v.y) + acc[m][1][2 * h + 1]);
+            v.z = pack_bf16(bf16lo_to_f32(v.z) + acc[m][2][2 * h], bf16hi_to_f32(v.z) + acc[m][2][2 * h + 1]);
+            v.w = pack_bf16(bf16lo_to_f32(v.w) + acc[m][3][2 * h], bf16hi_to_f32(v.w) + acc[m][3][2 * h + 1]);
             *reinterpret_cast<uint4 *>(y) = v;
           }
         }
-      }
     }
     before = now;
     begun = true;
