@@ -16,6 +16,11 @@
 // agree, so a lane's 16 bytes of consecutive k serve two products as they come.
 #include "w4a16_internal.h"
 
+#ifndef PSTEP
+#define PSTEP 2
+#define PWANT 304
+#define PCAP 304
+#endif
 namespace w4a16 {
 namespace {
 
@@ -155,77 +160,63 @@ struct Tiles {
 // tokens and up to 64 ranks, and every eighth (RP = 128: fourth) 32 of the
 // part's k, straight from memory; the warps' sums meet in shared memory.
 // ---------------------------------------------------------------------------
-template <int T, int RP>
+template <int RP>
 struct ShrinkGeo {
-  static constexpr int MB = T / 16;                // blocks of 16 tokens
   static constexpr int NB = (RP < 64 ? RP : 64) / 8;  // blocks of 8 ranks of a warp
   static constexpr int KW = RP > 64 ? kWarps / 2 : kWarps;  // warps that share K
   static constexpr int STRIDE = NB * 8 + 8;        // floats of a token's sums
-  static constexpr int SUMS = kWarps * T * STRIDE * 4;
-  static constexpr int OFF_LIST = SUMS, OFF_TILES = OFF_LIST + T * 4;
+  static constexpr int SUMS = kWarps * 16 * STRIDE * 4;
+  static constexpr int OFF_LIST = SUMS, OFF_TILES = OFF_LIST + 16 * 4;
   static int smem(int adapters) { return OFF_TILES + Tiles::ints(adapters) * 4; }
 };
 
-template <int T, int RP>
-__global__ void __launch_bounds__(kThreads, T == 16 ? 2 : 1) lora_shrink_kernel(const __grid_constant__ LoraParams p) {
-  using G = ShrinkGeo<T, RP>;
+template <int RP>
+__global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(const __grid_constant__ LoraParams p) {
+  using G = ShrinkGeo<RP>;
   extern __shared__ __align__(16) uint8_t smem[];
   float *sums = reinterpret_cast<float *>(smem);
   int *list = reinterpret_cast<int *>(smem + G::OFF_LIST);
   Tiles tiles(reinterpret_cast<int *>(smem + G::OFF_TILES), p.adapters);
   grid_dependency_wait();
   grid_launch_dependents();  // (so all that came before is complete when expand begins)
-  tiles.make<T>(p);
+  tiles.make<16>(p);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int kw = warp % G::KW, rank0 = warp / G::KW * 64;
   const int steps = (p.inner + 31) / 32;
   const long long units = (long long)tiles.first[p.adapters] * p.ksplit;
   for (long long unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const int tile = (int)(unit / p.ksplit), part = (int)(unit % p.ksplit);
-    const int e = tiles.of(tile), lo = (tile - tiles.first[e]) * T, n = min(T, tiles.count[e] - lo);
+    const int e = tiles.of(tile), lo = (tile - tiles.first[e]) * 16, n = min(16, tiles.count[e] - lo);
     tiles.tokens(p, e, lo, lo + n, list);
-    const uint16_t *xr[G::MB][2];
+    const uint16_t *xr[2];
 #pragma unroll
-    for (int m = 0; m < G::MB; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int i = m * 16 + h * 8 + g;
-        xr[m][h] = i < n ? p.x + list[i] * p.x_row : nullptr;
-      }
+    for (int h = 0; h < 2; ++h) xr[h] = h * 8 + g < n ? p.x + list[h * 8 + g] * p.x_row : nullptr;
     const uint16_t *ar = p.a + e * p.a_adapter + (rank0 + g) * p.a_row;
-    float acc[G::MB][G::NB][4] = {};
+    float acc[G::NB][4] = {};
     const int s1 = (int)((long long)steps * (part + 1) / p.ksplit);
 #pragma unroll 2
     for (int s = (int)((long long)steps * part / p.ksplit) + kw; s < s1; s += G::KW) {
       const int k = s * 32 + t * 8;
       const bool in = k < p.inner;
       const uint4 zero = make_uint4(0, 0, 0, 0);
-      uint4 xv[G::MB][2], av[G::NB];
+      uint4 xv[2], av[G::NB];
 #pragma unroll
       for (int j = 0; j < G::NB; ++j)
         av[j] = in && rank0 + j * 8 + g < p.rank ? __ldg(reinterpret_cast<const uint4 *>(ar + j * 8 * p.a_row + k)) : zero;
 #pragma unroll
-      for (int m = 0; m < G::MB; ++m)
+      for (int h = 0; h < 2; ++h) xv[h] = in && xr[h] ? *reinterpret_cast<const uint4 *>(xr[h] + k) : zero;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) xv[m][h] = in && xr[m][h] ? *reinterpret_cast<const uint4 *>(xr[m][h] + k) : zero;
-#pragma unroll
-      for (int m = 0; m < G::MB; ++m) {
-        if (m * 16 >= n) break;
-#pragma unroll
-        for (int j = 0; j < G::NB; ++j) {
-          mma16(acc[m][j], xv[m][0].x, xv[m][1].x, xv[m][0].y, xv[m][1].y, av[j].x, av[j].y);
-          mma16(acc[m][j], xv[m][0].z, xv[m][1].z, xv[m][0].w, xv[m][1].w, av[j].z, av[j].w);
-        }
+      for (int j = 0; j < G::NB; ++j) {
+        mma16(acc[j], xv[0].x, xv[1].x, xv[0].y, xv[1].y, av[j].x, av[j].y);
+        mma16(acc[j], xv[0].z, xv[1].z, xv[0].w, xv[1].w, av[j].z, av[j].w);
       }
     }
 #pragma unroll
-    for (int m = 0; m < G::MB; ++m)
+    for (int j = 0; j < G::NB; ++j)
 #pragma unroll
-      for (int j = 0; j < G::NB; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<float2 *>(sums + (warp * T + m * 16 + h * 8 + g) * G::STRIDE + j * 8 + 2 * t) =
-              make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float2 *>(sums + (warp * 16 + h * 8 + g) * G::STRIDE + j * 8 + 2 * t) =
+            make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
     __syncthreads();
     float *out = p.parts + (long long)part * p.tokens * RP;
     for (int i = threadIdx.x; i < n * RP / 4; i += kThreads) {
@@ -233,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, T == 16 ? 2 : 1) lora_shrink_kernel(
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < G::KW; ++w) {
-        const float4 u = *reinterpret_cast<const float4 *>(sums + ((r / 64 * G::KW + w) * T + row) * G::STRIDE + r % 64);
+        const float4 u = *reinterpret_cast<const float4 *>(sums + ((r / 64 * G::KW + w) * 16 + row) * G::STRIDE + r % 64);
         v.x += u.x;
         v.y += u.y;
         v.z += u.z;
@@ -251,16 +242,32 @@ __global__ void __launch_bounds__(kThreads, T == 16 ? 2 : 1) lora_shrink_kernel(
 // mantissa: rounded once it would add an error of the size of the output's own
 // rounding). The rows of B that a product's eight columns stand for are chosen
 // such that a lane ends up with eight consecutive columns of a token: y is read
-// and written 16 bytes at a time.
+// and written 16 bytes at a time. B is what there is to read: every warp copies
+// its own columns to shared memory some units ahead, and begins before there is
+// a t.
 // ---------------------------------------------------------------------------
-template <int T, int RP>
+template <int RP>
 struct ExpandGeo {
-  static constexpr int MB = T / 16;
   static constexpr int KS = RP < 32 ? 1 : RP / 32;  // 16-byte pieces of k of a lane
   static constexpr int ROW = RP < 32 ? RP * 2 : RP == 32 ? 64 : RP * 2 + 64;  // bytes of a token's t, without bank conflicts
-  static constexpr int OFF_LO = T * ROW, OFF_LIST = 2 * T * ROW, OFF_TILES = OFF_LIST + T * 4;
+  static constexpr int CPR = RP / 8;                // 16-byte pieces of a row of B
+  static constexpr int SLOT = 32 * RP * 2, SLOTS = RP <= 16 ? 8 : RP == 32 ? 6 : RP == 64 ? 3 : 2;
+  static constexpr int CTAS = RP <= 64 ? 2 : 1;     // per SM
+  static constexpr int OFF_LO = 16 * ROW, OFF_RING = 2 * 16 * ROW, OFF_LIST = OFF_RING + kWarps * SLOTS * SLOT;
+  static constexpr int OFF_TILES = OFF_LIST + 16 * 4;
   static int smem(int adapters) { return OFF_TILES + Tiles::ints(adapters) * 4; }
+  // where piece c of row r is: every other row's halves change places, so that a fragment's rows meet different banks
+  static __device__ __forceinline__ int place(int r, int c) { return r * RP * 2 + ((RP >= 64 ? c ^ ((r & 1) << 2) : c) << 4); }
 };
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // A lane's piece of k: 8 consecutive values (RP >= 32), 4 (16) or 2 (8).
 template <int RP>
@@ -305,111 +312,150 @@ __device__ __forceinline__ void store8(uint16_t *row, int c, int n, bool wide, c
     if (c + i < n) row[c + i] = (uint16_t)(v[i / 2] >> (i % 2 * 16));
 }
 
-template <int T, int RP, bool EVEN>
-__global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const __grid_constant__ LoraParams p) {
-  using G = ExpandGeo<T, RP>;
+template <int RP, bool EVEN>
+__global__ void __launch_bounds__(kThreads, ExpandGeo<RP>::CTAS) lora_expand_kernel(const __grid_constant__ LoraParams p) {
+  using G = ExpandGeo<RP>;
   extern __shared__ __align__(16) uint8_t smem[];
   int *list = reinterpret_cast<int *>(smem + G::OFF_LIST);
   Tiles tiles(reinterpret_cast<int *>(smem + G::OFF_TILES), p.adapters);
   // What shrink waited for before it let this launch begin is complete: rows,
   // adapters, y and B may be read; t only after the wait below.
-  tiles.make<T>(p);
+  tiles.make<16>(p);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int chunks = (p.outer + kColumns - 1) / kColumns;
-  const long long units = (long long)tiles.first[p.in_place ? p.adapters : p.adapters + 1] * chunks;
-  const long long u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
-  int here = -1, e = 0, n = 0;
-  bool waited = false;
-  for (long long unit = u0; unit < u1; ++unit) {
-    const int tile = (int)(unit / chunks), c0 = (int)(unit % chunks) * kColumns + warp * 32, c = c0 + 8 * t;
-    const bool next = tile != here;
-    if (next) {
-      __syncthreads();  // (the tile before is done with)
-      here = tile;
-      e = tiles.of(tile);
-      const int lo = (tile - tiles.first[e]) * T;
-      n = min(T, tiles.count[e] - lo);
-      tiles.tokens(p, e, lo, lo + n, list);
-    }
-    const bool adapted = e < p.adapters, wide = EVEN && c + 8 <= p.outer;
-    uint4 bv[4][G::KS], yv[G::MB][2];
-    if (adapted) {
+  const int chunks = (p.outer + kColumns - 1) / kColumns, all = tiles.first[p.in_place ? p.adapters : p.adapters + 1];
+  // CTAs that share a tile's chunks, and tiles that are worked on at once: with
+  // a tile of its own a CTA makes one t (48 tokens of 12 adapters and 34,816
+  // columns: five or six chunks a CTA)
+  const int sharing = max(1, (int)gridDim.x / max(all, 1)), at_once = (int)gridDim.x / sharing;
+  const int share = (int)blockIdx.x % sharing;
+  const int c_lo = (int)((long long)chunks * share / sharing), c_hi = (int)((long long)chunks * (share + 1) / sharing);
+  int tile = (int)blockIdx.x / sharing;
+  if (tile >= at_once || c_lo >= c_hi) tile = all;
+
+  // the warp's columns of B, SLOTS - 1 units ahead; a lane copies one piece of every (32 / CPR)th row
+  constexpr int kEach = 32 / G::CPR;
+  const uint32_t ring = smem_u32(smem) + G::OFF_RING + warp * G::SLOTS * G::SLOT;
+  const uint32_t lane_to = G::place(lane / G::CPR, lane % G::CPR);
+  const uint16_t *lane_b = p.b + (warp * 32 + lane / G::CPR) * p.b_row + lane % G::CPR * 8;
+  const bool lane_in = lane % G::CPR * 8 < p.rank;
+  int next_tile = tile, next_chunk = c_lo, next_slot = 0;
+  const uint16_t *next_b = nullptr;  // null: of no adapter
+  auto fetch = [&]() {
+    if (next_tile < all) {
+      if (next_chunk == c_lo) {
+        const int e = tiles.of(next_tile);
+        next_b = e < p.adapters ? lane_b + e * p.b_adapter + (long long)c_lo * kColumns * p.b_row : nullptr;
+      }
+      if (next_b) {
+        const int rows = p.outer - next_chunk * kColumns - warp * 32 - lane / G::CPR;  // from the lane's first row to the last
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int col = c0 + 8 * (g >> 1) + 2 * j + (g & 1);
-        const uint8_t *br = reinterpret_cast<const uint8_t *>(p.b + e * p.b_adapter + col * p.b_row);
-#pragma unroll
-        for (int s = 0; s < G::KS; ++s) {
-          const int k = RP < 32 ? t * (RP / 4) : s * 32 + t * 8;
-          bv[j][s] = col < p.outer && k < p.rank ? piece<RP>(br + k * 2) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < G::CPR; ++i) {
+          const bool in = lane_in && i * kEach < rows;
+          copy16(ring + next_slot * G::SLOT + lane_to + i * kEach * RP * 2, in ? next_b + i * kEach * p.b_row : p.b, in);
         }
+        next_b += kColumns * p.b_row;
       }
+      if (++next_chunk == c_hi) {
+        next_chunk = c_lo;
+        next_tile += at_once;
+      }
+      next_slot = next_slot + 1 == G::SLOTS ? 0 : next_slot + 1;
     }
+    copy_commit();
+  };
+  static_assert(RP < 64 || kEach % 2 == 0, "a lane's rows are all even or all odd: their pieces have one place");
 #pragma unroll
-    for (int m = 0; m < G::MB; ++m)
+  for (int i = 0; i < G::SLOTS - 1; ++i) fetch();
+
+  int slot = 0;
+  bool waited = false;
+  for (; tile < all; tile += at_once) {
+    __syncthreads();  // (the tile before is done with)
+    const int e = tiles.of(tile), lo = (tile - tiles.first[e]) * 16, n = min(16, tiles.count[e] - lo);
+    tiles.tokens(p, e, lo, lo + n, list);
+    const uint16_t *yr[2];
+    uint16_t *to[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int i = m * 16 + h * 8 + g;
-        if (i < n) yv[m][h] = load8(p.y + list[i] * p.y_row, c, p.outer, wide);
-      }
+    for (int h = 0; h < 2; ++h) {
+      const int token = h * 8 + g < n ? list[h * 8 + g] : 0;
+      yr[h] = p.y + token * p.y_row;
+      to[h] = p.out + token * p.out_row;
+    }
+    uint4 yv[2];
+    auto fetch_y = [&](int chunk) {
+      const int c = chunk * kColumns + warp * 32 + 8 * t;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (h * 8 + g < n) yv[h] = load8(yr[h], c, p.outer, EVEN && c + 8 <= p.outer);
+    };
+    fetch_y(c_lo);
     if (!waited) {
       grid_dependency_wait();
       waited = true;
     }
-    if (next && adapted) {
+    if (e < p.adapters) {
       const float scale = p.scale ? p.scale[e] : 1.f;
       for (int i = threadIdx.x; i < n * RP / 2; i += kThreads) {
         const int row = i * 2 / RP, r = i * 2 % RP;
         const float *from = p.parts + (long long)list[row] * RP + r;
         float2 v = make_float2(0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
         for (int s = 0; s < p.ksplit; ++s) {
           const float2 u = __ldcg(reinterpret_cast<const float2 *>(from + (long long)s * p.tokens * RP));
           v.x += u.x;
           v.y += u.y;
         }
-        v.x *= scale;
-        v.y *= scale;
-        const uint2 both = two_parts(v.x, v.y);
+        const uint2 both = two_parts(v.x * scale, v.y * scale);
         *reinterpret_cast<uint32_t *>(smem + row * G::ROW + r * 2) = both.x;
         *reinterpret_cast<uint32_t *>(smem + G::OFF_LO + row * G::ROW + r * 2) = both.y;
       }
       __syncthreads();
     }
-#pragma unroll
-    for (int m = 0; m < G::MB; ++m) {
-      if (m * 16 >= n) break;
-      if (adapted) {
+    for (int chunk = c_lo; chunk < c_hi; ++chunk) {
+      const int c = chunk * kColumns + warp * 32 + 8 * t;
+      fetch();
+      copy_wait<G::SLOTS - 1>();
+      __syncwarp();
+      if (e < p.adapters) {
         float acc[4][4] = {};
 #pragma unroll
         for (int s = 0; s < G::KS; ++s) {
-          const int at = (m * 16 + g) * G::ROW + (RP < 32 ? t * (RP / 2) : s * 64 + t * 16);
+          uint4 bv[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int r = 8 * (g >> 1) + 2 * j + (g & 1);
+            const uint8_t *from = smem + G::OFF_RING + (warp * G::SLOTS + slot) * G::SLOT;
+            bv[j] = piece<RP>(from + (RP < 32 ? r * RP * 2 + t * (RP / 2) : G::place(r, s * 4 + t)));
+          }
+          const int at = g * G::ROW + (RP < 32 ? t * (RP / 2) : s * 64 + t * 16);
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             const uint8_t *from = smem + (half ? G::OFF_LO : 0) + at;
             const uint4 a0 = piece<RP>(from), a1 = piece<RP>(from + 8 * G::ROW);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              mma16(acc[j], a0.x, a1.x, a0.y, a1.y, bv[j][s].x, bv[j][s].y);
-              if (RP >= 32) mma16(acc[j], a0.z, a1.z, a0.w, a1.w, bv[j][s].z, bv[j][s].w);
+              mma16(acc[j], a0.x, a1.x, a0.y, a1.y, bv[j].x, bv[j].y);
+              if (RP >= 32) mma16(acc[j], a0.z, a1.z, a0.w, a1.w, bv[j].z, bv[j].w);
             }
           }
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t *v = &yv[m][h].x;
+          uint32_t *v = &yv[h].x;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             v[j] = pack_bf16(bf16lo_to_f32(v[j]) + acc[j][2 * h], bf16hi_to_f32(v[j]) + acc[j][2 * h + 1]);
         }
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int i = m * 16 + h * 8 + g;
-        if (i < n) store8(p.out + list[i] * p.out_row, c, p.outer, wide, yv[m][h]);
-      }
+      for (int h = 0; h < 2; ++h)
+        if (h * 8 + g < n) store8(to[h], c, p.outer, EVEN && c + 8 <= p.outer, yv[h]);
+      __syncwarp();  // (the slot is free)
+      slot = slot + 1 == G::SLOTS ? 0 : slot + 1;
+      if (chunk + 1 < c_hi) fetch_y(chunk + 1);
     }
   }
+  copy_wait<0>();
   if (!waited) grid_dependency_wait();
   grid_launch_dependents();
 }
@@ -421,15 +467,6 @@ __global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const __grid_c
 // ---------------------------------------------------------------------------
 constexpr int kTile = 64;
 constexpr int kListInts = 68;  // a tile's tokens, adapter and number of tokens
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 template <int RP>
 struct PromptShrinkGeo {
@@ -826,8 +863,8 @@ bool few(int tokens) { return tokens <= 512; }
 // Few tokens: parts of K. As many CTAs as fit at once, but at least one step of
 // 32 k for each warp, and no more than 32 sums for expand to add up.
 int parts_of(int tokens, int rank, int inner) {
-  const int tiles = (tokens + 15) / 16, step = 32 * (rank > 64 ? kWarps / 2 : kWarps);
-  const int want = 304 / tiles, most = (inner + step - 1) / step;
+  const int tiles = (tokens + 15) / 16, step = PSTEP * 32 * (rank > 64 ? kWarps / 2 : kWarps);
+  const int want = PWANT / tiles, most = (inner + step - 1) / step;
   return want < 1 ? 1 : want < most ? (want < 32 ? want : 32) : (most < 32 ? most : 32);
 }
 
@@ -870,12 +907,12 @@ cudaError_t run_few(const LoraCall &c, const LoraParams &p, bool even) {
   const int groups = c.adapters < c.rows ? c.adapters : c.rows;
   const long long tiles = c.tokens / 16 + groups + 1;  // at most
   const long long shrink = tiles * p.ksplit, expand = tiles * ((c.outer + kColumns - 1) / kColumns);
-  const long long cap = c.sm_count * 2;
-  const cudaError_t e = launch(lora_shrink_kernel<16, RP>, (unsigned)(shrink < cap ? shrink : cap), 1,
-                               ShrinkGeo<16, RP>::smem(c.adapters), c.stream, p);
+  const long long cap = PCAP;
+  const cudaError_t e = launch(lora_shrink_kernel<RP>, (unsigned)(shrink < cap ? shrink : cap), 1,
+                               ShrinkGeo<RP>::smem(c.adapters), c.stream, p);
   if (e != cudaSuccess) return e;
-  return launch(even ? lora_expand_kernel<16, RP, true> : lora_expand_kernel<16, RP, false>,
-                (unsigned)(expand < cap ? expand : cap), 1, ExpandGeo<16, RP>::smem(c.adapters), c.stream, p);
+  return launch(even ? lora_expand_kernel<RP, true> : lora_expand_kernel<RP, false>,
+                (unsigned)(expand < c.sm_count * ExpandGeo<RP>::CTAS ? expand : c.sm_count * ExpandGeo<RP>::CTAS), 1, ExpandGeo<RP>::smem(c.adapters), c.stream, p);
 }
 
 template <int RP>

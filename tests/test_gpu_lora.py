@@ -134,8 +134,11 @@ def test_large_store_and_many_rows():
     sizes = rng.integers(0, 3, rows).tolist()
     p = Problem(sizes, which, 8, 64, 96, store)
     p.check(p.run())
-    p = Problem([1] * 300, [5] * 150 + [4095] * 150, 8, 16, 24, 4096)
-    p.check(p.run())
+    for rank in (8, 64, 128):
+        p = Problem([1] * 300, [5] * 150 + [4095] * 150, rank, 16, 24, 4096)
+        p.check(p.run())
+        p = Problem([500, 0, 180], [4095, 3, 4000], rank, 16, 24, 4096)
+        p.check(p.run())
 
 
 def test_bad_indices_are_left_out_and_reported():
