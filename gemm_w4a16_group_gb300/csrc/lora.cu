@@ -16,11 +16,6 @@
 // agree, so a lane's 16 bytes of consecutive k serve two products as they come.
 #include "w4a16_internal.h"
 
-#ifndef PSTEP
-#define PSTEP 2
-#define PWANT 304
-#define PCAP 304
-#endif
 namespace w4a16 {
 namespace {
 
@@ -101,6 +96,7 @@ __device__ __forceinline__ int row_adapter(const LoraParams &p, int b) {
 struct Tiles {
   int *count, *first, *sums;
   int bins;
+  int mine, mine_at, mine_n;  // adapter, first token and number of tokens of row threadIdx.x (the block's first pass over the rows)
 
   static __host__ __device__ int ints(int adapters) { return 2 * adapters + 3 + kWarps; }
   __device__ Tiles(int *mem, int adapters)
@@ -108,9 +104,16 @@ struct Tiles {
 
   template <int T>
   __device__ void make(const LoraParams &p) {
+    mine = -1;
+    mine_at = mine_n = 0;
+    if ((int)threadIdx.x < p.rows) {
+      mine = row_adapter(p, threadIdx.x);
+      mine_n = row_tokens(p, threadIdx.x, mine_at);
+    }
     for (int e = threadIdx.x; e < bins; e += kThreads) count[e] = 0;
     __syncthreads();
-    for (int b = threadIdx.x; b < p.rows; b += kThreads) {
+    if (mine_n) atomicAdd(&count[mine], mine_n);
+    for (int b = kThreads + threadIdx.x; b < p.rows; b += kThreads) {
       int s;
       const int n = row_tokens(p, b, s);
       if (n) atomicAdd(&count[row_adapter(p, b)], n);
@@ -143,10 +146,13 @@ struct Tiles {
   __device__ void tokens(const LoraParams &p, int e, int lo, int hi, int *list) const {
     int done = 0;
     for (int b0 = 0; b0 < p.rows && done < hi; b0 += kThreads) {
-      const int b = b0 + threadIdx.x;
-      int s = 0, n = 0, total;
-      if (b < p.rows && row_adapter(p, b) == e) n = row_tokens(p, b, s);
-      __syncthreads();
+      int s = mine_at, n = mine == e ? mine_n : 0, total;
+      if (b0) {
+        const int b = b0 + threadIdx.x;
+        n = 0;
+        if (b < p.rows && row_adapter(p, b) == e) n = row_tokens(p, b, s);
+        __syncthreads();
+      }
       const int at = done + block_scan(n, sums, total);
       for (int i = max(lo, at); i < min(hi, at + n); ++i) list[i - lo] = s + i - at;
       done += total;
@@ -251,8 +257,8 @@ struct ExpandGeo {
   static constexpr int KS = RP < 32 ? 1 : RP / 32;  // 16-byte pieces of k of a lane
   static constexpr int ROW = RP < 32 ? RP * 2 : RP == 32 ? 64 : RP * 2 + 64;  // bytes of a token's t, without bank conflicts
   static constexpr int CPR = RP / 8;                // 16-byte pieces of a row of B
-  static constexpr int SLOT = 32 * RP * 2, SLOTS = RP <= 16 ? 8 : RP == 32 ? 6 : RP == 64 ? 3 : 2;
-  static constexpr int CTAS = RP <= 64 ? 2 : 1;     // per SM
+  static constexpr int SLOT = 32 * RP * 2, SLOTS = RP <= 16 ? 8 : RP == 32 ? 3 : 2;
+  static constexpr int CTAS = RP <= 16 ? 2 : RP <= 64 ? 3 : 1;  // per SM
   static constexpr int OFF_LO = 16 * ROW, OFF_RING = 2 * 16 * ROW, OFF_LIST = OFF_RING + kWarps * SLOTS * SLOT;
   static constexpr int OFF_TILES = OFF_LIST + 16 * 4;
   static int smem(int adapters) { return OFF_TILES + Tiles::ints(adapters) * 4; }
@@ -262,6 +268,9 @@ struct ExpandGeo {
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -337,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, ExpandGeo<RP>::CTAS) lora_expand_ker
   const uint32_t ring = smem_u32(smem) + G::OFF_RING + warp * G::SLOTS * G::SLOT;
   const uint32_t lane_to = G::place(lane / G::CPR, lane % G::CPR);
   const uint16_t *lane_b = p.b + (warp * 32 + lane / G::CPR) * p.b_row + lane % G::CPR * 8;
-  const bool lane_in = lane % G::CPR * 8 < p.rank;
+  const bool lane_in = lane % G::CPR * 8 < p.rank, dense = p.rank == RP && p.b_row == RP;
   int next_tile = tile, next_chunk = c_lo, next_slot = 0;
   const uint16_t *next_b = nullptr;  // null: of no adapter
   auto fetch = [&]() {
@@ -347,11 +356,17 @@ __global__ void __launch_bounds__(kThreads, ExpandGeo<RP>::CTAS) lora_expand_ker
         next_b = e < p.adapters ? lane_b + e * p.b_adapter + (long long)c_lo * kColumns * p.b_row : nullptr;
       }
       if (next_b) {
-        const int rows = p.outer - next_chunk * kColumns - warp * 32 - lane / G::CPR;  // from the lane's first row to the last
+        const uint32_t to = ring + next_slot * G::SLOT + lane_to;
+        const int rows = p.outer - next_chunk * kColumns - warp * 32;  // from the warp's first row to the last
+        if (dense && rows >= 32) {  // (addresses a constant apart)
 #pragma unroll
-        for (int i = 0; i < G::CPR; ++i) {
-          const bool in = lane_in && i * kEach < rows;
-          copy16(ring + next_slot * G::SLOT + lane_to + i * kEach * RP * 2, in ? next_b + i * kEach * p.b_row : p.b, in);
+          for (int i = 0; i < G::CPR; ++i) copy16(to + i * kEach * RP * 2, next_b + i * kEach * RP);
+        } else {
+#pragma unroll
+          for (int i = 0; i < G::CPR; ++i) {
+            const bool in = lane_in && i * kEach + lane / G::CPR < rows;
+            copy16(to + i * kEach * RP * 2, in ? next_b + i * kEach * p.b_row : p.b, in);
+          }
         }
         next_b += kColumns * p.b_row;
       }
@@ -860,11 +875,12 @@ int padded_rank(int rank) { return rank <= 8 ? 8 : rank <= 16 ? 16 : rank <= 32 
 // would mostly be empty.
 bool few(int tokens) { return tokens <= 512; }
 
-// Few tokens: parts of K. As many CTAs as fit at once, but at least one step of
-// 32 k for each warp, and no more than 32 sums for expand to add up.
+// Few tokens: parts of K. As many CTAs as fit at once, but at least two steps of
+// 32 k for each warp (one token: 5.4 us, with one step 6.1, with four 6.1), and
+// no more than 32 sums for expand to add up.
 int parts_of(int tokens, int rank, int inner) {
-  const int tiles = (tokens + 15) / 16, step = PSTEP * 32 * (rank > 64 ? kWarps / 2 : kWarps);
-  const int want = PWANT / tiles, most = (inner + step - 1) / step;
+  const int tiles = (tokens + 15) / 16, step = 2 * 32 * (rank > 64 ? kWarps / 2 : kWarps);
+  const int want = 304 / tiles, most = (inner + step - 1) / step;
   return want < 1 ? 1 : want < most ? (want < 32 ? want : 32) : (most < 32 ? most : 32);
 }
 
@@ -907,7 +923,7 @@ cudaError_t run_few(const LoraCall &c, const LoraParams &p, bool even) {
   const int groups = c.adapters < c.rows ? c.adapters : c.rows;
   const long long tiles = c.tokens / 16 + groups + 1;  // at most
   const long long shrink = tiles * p.ksplit, expand = tiles * ((c.outer + kColumns - 1) / kColumns);
-  const long long cap = PCAP;
+  const long long cap = c.sm_count * 2;
   const cudaError_t e = launch(lora_shrink_kernel<RP>, (unsigned)(shrink < cap ? shrink : cap), 1,
                                ShrinkGeo<RP>::smem(c.adapters), c.stream, p);
   if (e != cudaSuccess) return e;
