@@ -476,25 +476,26 @@ __global__ void __launch_bounds__(kThreads, ExpandGeo<RP>::CTAS) lora_expand_ker
 }
 
 // ---------------------------------------------------------------------------
-// Prompts. shrink: a cluster of CTAs has a tile of 64 tokens, each a part of K,
-// which it streams through shared memory 128 k at a time; their sums meet over
-// distributed shared memory, and x A^T is written once, in its two parts.
+// Prompts. shrink: a cluster of CTAs has up to 128 tokens of one adapter, each
+// CTA a part of K, which it streams through shared memory 64 k at a time into
+// tcgen05 products (128 tokens by RP ranks, sums in TMEM): the warps only copy.
+// (With mma.sync, whose fragments come from shared memory, six prompts of rank 64
+// took 33 us here.) The parts of the sums meet over distributed shared memory, and
+// x A^T is written once, in its two bf16 parts.
 // ---------------------------------------------------------------------------
-constexpr int kTile = 64;
-constexpr int kListInts = 68;  // a tile's tokens, adapter and number of tokens
+constexpr int kTile = 64;       // tokens of a list
+constexpr int kListInts = 68;   // a tile's tokens, adapter and number of tokens
 
 template <int RP>
 struct PromptShrinkGeo {
-  static constexpr int K = 128;                 // of a stage
-  static constexpr int NB = RP / 8;
-  static constexpr int X = kTile * K * 2, STAGE = X + RP * K * 2;
-  static constexpr int STAGES = RP <= 32 ? 4 : RP == 64 ? 3 : 4;
-  static constexpr int CTAS = RP <= 64 ? 2 : 1;  // per SM
-  static constexpr int STRIDE = RP + 8;         // floats of a token's sums
-  static constexpr int OFF_PART = 4 * kTile * STRIDE * 4;  // (the sums and the CTA's part take the stages' place)
-  static constexpr int OFF_LIST = STAGES * STAGE, OFF_TILES = OFF_LIST + kTile * 4;
-  static_assert(OFF_PART + kTile * RP * 4 <= OFF_LIST, "sums after the stages");
-  static int smem(int adapters) { return OFF_TILES + Tiles::ints(adapters) * 4; }
+  static constexpr int NR = RP < 16 ? 16 : RP;   // ranks of a product
+  static constexpr int X = 128 * 128, STAGE = X + NR * 128;  // bytes: rows of 64 k, swizzled
+  static constexpr int STAGES = RP <= 32 ? 5 : RP == 64 ? 4 : 3;
+  static constexpr int COLS = NR < 32 ? 32 : NR;  // of TMEM
+  static constexpr int PITCH = RP + 4;            // floats of a token's sums (they take the stages' place)
+  static constexpr int OFF_LIST = STAGES * STAGE, OFF_BAR = OFF_LIST + 128 * 4, OFF_TILES = OFF_BAR + STAGES * 8 + 16;
+  static_assert(128 * PITCH * 4 <= OFF_LIST && STAGE % 1024 == 0, "sums in the stages' place, stages on whole atoms");
+  static int smem(int adapters) { return OFF_TILES + Tiles::ints(adapters) * 4 + 1024; }
 };
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t a) {
@@ -504,120 +505,134 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t a) {
 }
 
 template <int RP>
-__global__ void __launch_bounds__(kThreads, PromptShrinkGeo<RP>::CTAS) lora_prompt_shrink_kernel(const __grid_constant__ LoraParams p) {
+__global__ void __launch_bounds__(kThreads, 2) lora_prompt_shrink_kernel(const __grid_constant__ LoraParams p) {
   using G = PromptShrinkGeo<RP>;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(16) uint8_t raw[];
+  uint8_t *smem = raw + (1024 - smem_u32(raw) % 1024) % 1024;  // (the swizzle goes by address)
   int *list = reinterpret_cast<int *>(smem + G::OFF_LIST);
+  volatile int *abort = reinterpret_cast<volatile int *>(smem + G::OFF_BAR + G::STAGES * 8);
+  const uint32_t base = smem_u32(smem), bar = base + G::OFF_BAR, slot = bar + G::STAGES * 8 + 4;
   Tiles tiles(reinterpret_cast<int *>(smem + G::OFF_TILES), p.adapters);
   const int parts = (int)cluster_nctarank(), part = (int)cluster_ctarank(), tile = (int)cluster_id_x();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dependency_wait();
   grid_launch_dependents();
-  tiles.make<kTile>(p);
+  tiles.make<2 * kTile>(p);
   const int all = tiles.first[p.adapters + 1];
   if (tile == 0 && part == 0 && threadIdx.x == 0) {
-    p.head[0] = tiles.first[p.adapters];
-    p.head[1] = all;
+    p.head[0] = 2 * tiles.first[p.adapters];
+    p.head[1] = 2 * all;
   }
-  if (tile >= all) return;  // (all CTAs of the cluster do)
-  const int e = tiles.of(tile), lo = (tile - tiles.first[e]) * kTile, n = min(kTile, tiles.count[e] - lo);
+  if (tile >= all) return;  // (all CTAs of the cluster do, here and below)
+  const int e = tiles.of(tile), lo = (tile - tiles.first[e]) * 2 * kTile, n = min(2 * kTile, tiles.count[e] - lo);
   if (e == p.adapters && p.in_place) return;
   tiles.tokens(p, e, lo, lo + n, list);
-  if (part == 0) {
-    int *to = p.lists + (long long)tile * kListInts;
-    if (threadIdx.x < n) to[threadIdx.x] = list[threadIdx.x];
-    if (threadIdx.x == 0) {
-      to[kTile] = e;
-      to[kTile + 1] = n;
+  if (part == 0) {  // two lists, the second one perhaps empty
+    int *to = p.lists + 2ll * tile * kListInts;
+    for (int i = threadIdx.x; i < n; i += kThreads) to[i / kTile * kListInts + i % kTile] = list[i];
+    if (threadIdx.x < 2) {
+      to[threadIdx.x * kListInts + kTile] = e;
+      to[threadIdx.x * kListInts + kTile + 1] = max(0, min(kTile, n - (int)threadIdx.x * kTile));
     }
   }
   if (e == p.adapters) return;
 
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int mw = warp & 1, kw = warp >> 1;
-  const uint32_t base = smem_u32(smem);
-  const int steps = (p.inner + G::K - 1) / G::K;
-  const int s0 = (int)((long long)steps * part / parts), s1 = (int)((long long)steps * (part + 1) / parts);
-  // a thread copies the same 16 bytes of k of every 16th row
-  const int c = threadIdx.x & 15, r0 = threadIdx.x >> 4;
-  const uint16_t *xr[kTile / 16];
+  __syncwarp();
+  if (warp == 0) {
+    tmem_alloc(slot, G::COLS);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    *abort = 0;
+    for (int i = 0; i < G::STAGES; ++i) mbar_init(bar + 8 * i, 1);
+    fence_mbar_init();
+  }
+  const int steps = (p.inner + 63) / 64;
+  const int s0 = (int)((long long)steps * part / parts), count = (int)((long long)steps * (part + 1) / parts) - s0;
+  // a thread copies the same 16 bytes of k of every 32nd row
+  const int c = threadIdx.x & 7, r0 = threadIdx.x >> 3;
+  const uint16_t *xr[4];
 #pragma unroll
-  for (int i = 0; i < kTile / 16; ++i) xr[i] = r0 + i * 16 < n ? p.x + list[r0 + i * 16] * p.x_row : nullptr;
-  const uint16_t *ar = p.a + e * p.a_adapter + r0 * p.a_row;
-  // (every other row's halves change places: a fragment's rows then meet different banks)
-  const uint32_t to = base + r0 * 256 + ((c ^ ((r0 & 1) << 2)) << 4);
-  auto fetch = [&](int s) {
-    if (s < s1) {
-      const uint32_t at = to + (s - s0) % G::STAGES * G::STAGE;
-      const int k = s * G::K + c * 8;
-      const bool in = k < p.inner;
+  for (int i = 0; i < 4; ++i) xr[i] = r0 + i * 32 < n ? p.x + list[r0 + i * 32] * p.x_row + c * 8 : nullptr;
+  const uint16_t *ar = p.a + e * p.a_adapter + r0 * p.a_row + c * 8;
+  const uint32_t to = base + r0 * 128 + ((c ^ (r0 & 7)) << 4);
+  auto fetch = [&](int i) {
+    if (i < count) {
+      const uint32_t at = to + i % G::STAGES * G::STAGE;
+      const int k = (s0 + i) * 64;
+      const bool in = k + c * 8 < p.inner;
 #pragma unroll
-      for (int i = 0; i < kTile / 16; ++i)
-        if (xr[i]) copy16(at + i * 16 * 256, in ? xr[i] + k : xr[i], in);
+      for (int r = 0; r < 4; ++r)
+        if (xr[r]) copy16(at + r * 32 * 128, in ? xr[r] + k : p.x, in);
 #pragma unroll
-      for (int i = 0; i < (RP + 15) / 16; ++i)
-        if (RP >= 16 || r0 < RP) {
-          const bool there = in && r0 + i * 16 < p.rank;
-          copy16(at + G::X + i * 16 * 256, there ? ar + i * 16 * p.a_row + k : ar, there);
+      for (int r = 0; r < (G::NR + 31) / 32; ++r)
+        if (G::NR >= 32 || r0 < G::NR) {
+          const bool there = in && r0 + r * 32 < p.rank;
+          copy16(at + G::X + r * 32 * 128, there ? ar + r * 32 * p.a_row + k : p.a, there);
         }
     }
     copy_commit();
   };
 #pragma unroll
-  for (int i = 0; i < G::STAGES - 1; ++i) fetch(s0 + i);
-  float acc[2][G::NB][4] = {};
-  const uint32_t from = base + g * 256 + (((kw * 4 + t) ^ ((g & 1) << 2)) << 4);
-  for (int s = s0; s < s1; ++s) {
-    copy_wait<G::STAGES - 2>();
-    __syncthreads();
-    fetch(s + G::STAGES - 1);
-    const uint32_t at = from + (s - s0) % G::STAGES * G::STAGE;
-    uint4 xv[2][2];
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) xv[m][h] = lds128(at + (mw * 32 + m * 16 + h * 8) * 256);
-#pragma unroll
-    for (int j = 0; j < G::NB; ++j) {
-      const uint4 av = lds128(at + G::X + j * 8 * 256);
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        mma16(acc[m][j], xv[m][0].x, xv[m][1].x, xv[m][0].y, xv[m][1].y, av.x, av.y);
-        mma16(acc[m][j], xv[m][0].z, xv[m][1].z, xv[m][0].w, xv[m][1].w, av.z, av.w);
-      }
+  for (int i = 0; i < G::STAGES - 1; ++i) fetch(i);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = lds32(slot);
+  __syncwarp();
+  bool ok = true;
+  auto wait = [&](int i) {
+    if (ok && !mbar_wait<true>(bar + i % G::STAGES * 8, i / G::STAGES & 1, abort)) {
+      ok = false;
+      *abort = 1;
+      atomicOr(p.err, kErrTimeout);
     }
+  };
+  for (int i = 0; i < count; ++i) {
+    copy_wait<G::STAGES - 2>();
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(128, G::NR);
+      const uint64_t x = sw128_desc(base + i % G::STAGES * G::STAGE), a = sw128_desc(base + i % G::STAGES * G::STAGE + G::X);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tc_mma_f16(tmem, x + 2 * k, a + 2 * k, idesc, (uint32_t)(i | k));
+      tc_commit(bar + i % G::STAGES * 8);
+    }
+    if (i) wait(i - 1);  // (its stage is the one that the next copies go to)
+    fetch(i + G::STAGES - 1);
   }
   copy_wait<0>();
-  __syncthreads();
-  float *sums = reinterpret_cast<float *>(smem);
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int j = 0; j < G::NB; ++j)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<float2 *>(sums + (kw * kTile + mw * 32 + m * 16 + h * 8 + g) * G::STRIDE + j * 8 + 2 * t) =
-            make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
-  __syncthreads();
-  for (int i = threadIdx.x; i < kTile * RP / 4; i += kThreads) {
-    const int row = i * 4 / RP, r = i * 4 % RP;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float4 u = *reinterpret_cast<const float4 *>(sums + (w * kTile + row) * G::STRIDE + r);
-      v.x += u.x;
-      v.y += u.y;
-      v.z += u.z;
-      v.w += u.w;
-    }
-    *reinterpret_cast<float4 *>(smem + G::OFF_PART + i * 16) = v;
+  if (count) {
+    wait(count - 1);
+    if (!ok) mbar_wait_drain(bar + (count - 1) % G::STAGES * 8, (count - 1) / G::STAGES & 1);
   }
+  tc_fence_after();
+  __syncthreads();  // (nobody writes sums before everybody's products are done)
+  float *sums = reinterpret_cast<float *>(smem);
+  {
+    const int row = (warp & 3) * 32 + lane, c0 = warp < 4 ? 0 : G::NR / 2;
+#pragma unroll
+    for (int q = 0; q < (G::NR >= 32 ? G::NR / 32 : 1); ++q) {
+      if (G::NR < 32 && warp >= 4) break;
+      float v[16];
+      tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + c0 + q * 16, v);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (c0 + q * 16 + k * 4 < RP)
+          *reinterpret_cast<float4 *>(sums + row * G::PITCH + c0 + q * 16 + k * 4) =
+              count ? make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, G::COLS);
   cluster_sync_all();
   const float scale = p.scale ? p.scale[e] : 1.f;
-  const int rows = kTile / parts;
+  const int rows = 128 / parts;
   for (int i = threadIdx.x; i < rows * RP / 4; i += kThreads) {
     const int row = part * rows + i * 4 / RP, r = i * 4 % RP;
     if (row >= n) break;
-    const uint32_t at = base + G::OFF_PART + (row * RP + r) * 4;
+    const uint32_t at = base + (row * G::PITCH + r) * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int q = 0; q < parts; ++q) {
       const float4 u = ld_cluster_f4(mapa_shared(at, q));
@@ -794,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, PromptExpandGeo<RP>::CTAS) lora_prom
     }
     copy_commit();
     const int e = list_of(now)[kTile], n = tokens_of(now);
-    if (e < p.adapters) {
+    if (e < p.adapters && n > 0) {
       if (now.chunk != held_chunk || e != held_adapter) {
         held_chunk = now.chunk;
         held_adapter = e;
@@ -884,16 +899,16 @@ int parts_of(int tokens, int rank, int inner) {
   return want < 1 ? 1 : want < most ? (want < 32 ? want : 32) : (most < 32 ? most : 32);
 }
 
-// Prompts: CTAs of a cluster, which share K: as many as bring the tiles to a
-// wave (two CTAs per SM), while each keeps 512 k.
+// Prompts: CTAs of a cluster, which share K: as many as bring 128 tokens each to
+// a wave (two CTAs per SM), while each keeps 512 k.
 int cluster_of(int tokens, int inner, int sm_count) {
   int s = 1;
-  while (s < 8 && (long long)(tokens / kTile) * s * 2 <= 2 * sm_count && inner >= 1024 * s) s *= 2;
+  while (s < 4 && (long long)((tokens + 127) / 128) * s * 2 <= 2 * sm_count && inner >= 1024 * s) s *= 2;
   return s;
 }
 
-// Prompts: tiles at most, whatever the rows' adapters
-long long most_tiles(int tokens, int groups) { return tokens / kTile + (long long)groups + 1; }
+// Prompts: clusters at most, whatever the rows' adapters; each has two lists
+long long most_clusters(int tokens, int groups) { return tokens / (2 * kTile) + (long long)groups + 1; }
 
 template <class K>
 cudaError_t launch(K kern, unsigned grid, int cluster, int smem, cudaStream_t stream, const LoraParams &p) {
@@ -934,8 +949,8 @@ cudaError_t run_few(const LoraCall &c, const LoraParams &p, bool even) {
 template <int RP>
 cudaError_t run_prompts(const LoraCall &c, const LoraParams &p, bool even) {
   const int cluster = cluster_of(c.tokens, c.inner, c.sm_count);
-  const long long tiles = most_tiles(c.tokens, c.adapters < c.rows ? c.adapters : c.rows);
-  const cudaError_t e = launch(lora_prompt_shrink_kernel<RP>, (unsigned)(tiles * cluster), cluster,
+  const long long clusters = most_clusters(c.tokens, c.adapters < c.rows ? c.adapters : c.rows);
+  const cudaError_t e = launch(lora_prompt_shrink_kernel<RP>, (unsigned)(clusters * cluster), cluster,
                                PromptShrinkGeo<RP>::smem(c.adapters), c.stream, p);
   if (e != cudaSuccess) return e;
   return launch(even ? lora_prompt_expand_kernel<RP, false> : lora_prompt_expand_kernel<RP, true>,
@@ -953,7 +968,7 @@ size_t lora_workspace_bytes(int tokens, int rank, int inner) {
   const size_t row = padded_rank(rank) * sizeof(float);  // (two bf16 or one float32 a rank)
   if (few(tokens)) return align_up((size_t)parts_of(tokens, rank, inner) * tokens * row, 256);
   const int groups = tokens < kMaxAdapters ? tokens : kMaxAdapters;
-  return 256 + align_up(tokens * row, 256) + align_up((size_t)most_tiles(tokens, groups) * kListInts * sizeof(int), 256);
+  return 256 + align_up(tokens * row, 256) + align_up((size_t)most_clusters(tokens, groups) * 2 * kListInts * sizeof(int), 256);
 }
 
 cudaError_t launch_lora_add(const LoraCall &c) {
