@@ -708,6 +708,13 @@ __global__ void __launch_bounds__(kThreads, PromptExpandGeo<RP>::CTAS) lora_prom
   auto shift_of = [&](int token) {
     return SHIFT ? (int)((reinterpret_cast<uintptr_t>(p.out) / 2 + token * p.out_row) & 7) : 0;
   };
+  // y's columns c .. c + 7 of a row, one by one, to shared memory
+  auto slow = [&](const uint16_t *row, int c, int c0, int to) {
+    uint16_t *v = reinterpret_cast<uint16_t *>(smem + to);
+#pragma unroll 1
+    for (int k = 0; k < 8; ++k)
+      if (c + k >= c0 && c + k < p.outer) v[k] = __ldcg(row + c + k);
+  };
   // y and x A^T of a step; a warp brings y of four rows
   auto fetch = [&](const Step &s, int low, int out) {
     const int *list = list_of(s) + s.half * 32;
@@ -726,19 +733,21 @@ __global__ void __launch_bounds__(kThreads, PromptExpandGeo<RP>::CTAS) lora_prom
       if (r >= n) break;
       const int token = list[r], sh = shift_of(token), c = c0 + 8 * lane - sh;
       const uint16_t *row = p.y + token * p.y_row;
-      const int at = G::OFF_OUT + out * G::OUT + r * G::PITCH + lane * 16;
-      if (c >= c0 && c + 8 <= p.outer && (!SHIFT || p.alike)) {
-        copy16(base + at, row + c, true);
+      const int at = G::OFF_OUT + out * G::OUT + r * G::PITCH;
+      if (!SHIFT) {
+        if (c + 8 <= p.outer) copy16(base + at + lane * 16, row + c);
+        else slow(row, c, c0, at + lane * 16);
       } else {
-        uint16_t *to = reinterpret_cast<uint16_t *>(smem + at);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (c + k >= c0 && c + k < p.outer) to[k] = __ldcg(row + c + k);
-      }
-      if (SHIFT) {
-        const int last = c0 + kColumns - sh + lane;
-        if (lane < sh && last < p.outer)
-          *reinterpret_cast<uint16_t *>(smem + G::OFF_OUT + out * G::OUT + r * G::PITCH + (kColumns + lane) * 2) = __ldcg(row + last);
+        // whole pieces, with what they hold of the columns beside (which is not used); not where that is not y's
+        const uint16_t *end = p.y + (p.tokens - 1) * p.y_row + p.outer;
+        auto piece_of = [&](int l) {
+          const int cl = c0 + 8 * l - sh;
+          if (cl >= p.outer) return;
+          if (p.alike && row + cl >= p.y && row + cl + 8 <= end) copy16(base + at + l * 16, row + cl);
+          else slow(row, cl, c0, at + l * 16);
+        };
+        piece_of(lane);
+        if (sh && lane == 0) piece_of(32);
       }
     }
   };
@@ -752,18 +761,18 @@ __global__ void __launch_bounds__(kThreads, PromptExpandGeo<RP>::CTAS) lora_prom
       const int token = list[r], sh = shift_of(token), c = c0 + 8 * lane - sh;
       uint16_t *row = p.out + token * p.out_row;
       const uint8_t *from = smem + G::OFF_OUT + out * G::OUT + r * G::PITCH;
-      const uint4 v = *reinterpret_cast<const uint4 *>(from + lane * 16);
-      if (c >= c0 && c + 8 <= p.outer) {
-        *reinterpret_cast<uint4 *>(row + c) = v;
-      } else {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (c + k >= c0 && c + k < p.outer) row[c + k] = (uint16_t)(w[k / 2] >> (k % 2 * 16));
-      }
-      if (SHIFT) {
+      if (c >= c0 && c + 8 <= p.outer) *reinterpret_cast<uint4 *>(row + c) = *reinterpret_cast<const uint4 *>(from + lane * 16);
+      // the places before the first whole piece, past the chunk's 256, and of the row's last piece, one a lane
+      const uint16_t *one = reinterpret_cast<const uint16_t *>(from);
+      if (SHIFT && sh) {
+        if (lane < 8 && lane >= sh && c0 - sh + lane < p.outer) row[c0 - sh + lane] = one[lane];
         const int last = c0 + kColumns - sh + lane;
-        if (lane < sh && last < p.outer) row[last] = *reinterpret_cast<const uint16_t *>(from + (kColumns + lane) * 2);
+        if (lane < sh && last < p.outer) row[last] = one[kColumns + lane];
+      }
+      const int left = p.outer - c0 + sh;  // places of the row from here on
+      if (left < kColumns && left % 8) {
+        const int place = left / 8 * 8 + lane;
+        if (place < left && place >= (sh ? 8 : 0)) row[c0 - sh + place] = one[place];
       }
     }
   };
@@ -855,12 +864,19 @@ __global__ void __launch_bounds__(kThreads, PromptExpandGeo<RP>::CTAS) lora_prom
           uint16_t *y = reinterpret_cast<uint16_t *>(smem + G::OFF_OUT + out * G::OUT + r * G::PITCH) + warp * 32 + 8 * t;
           if (SHIFT) {
             if (r >= n) continue;
-            y += shift_of(list_of(now)[now.half * 32 + r]);
+            // two places to a word; with an odd shift the first and the last share theirs with other lanes
+            const int place = warp * 32 + 8 * t + shift_of(list_of(now)[now.half * 32 + r]);
+            uint32_t *w = reinterpret_cast<uint32_t *>(smem + G::OFF_OUT + out * G::OUT + r * G::PITCH + (place & ~1) * 2);
+            uint16_t *one = reinterpret_cast<uint16_t *>(w);
+            auto add = [](uint32_t v, float lo, float hi) { return pack_bf16(bf16lo_to_f32(v) + lo, bf16hi_to_f32(v) + hi); };
+            if (place & 1) {
+              one[1] = (uint16_t)add(one[1], acc[m][0][2 * h], 0.f);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t v = pack_bf16(bf16lo_to_f32(y[2 * j]) + acc[m][j][2 * h], bf16lo_to_f32(y[2 * j + 1]) + acc[m][j][2 * h + 1]);
-              y[2 * j] = (uint16_t)v;
-              y[2 * j + 1] = (uint16_t)(v >> 16);
+              for (int j = 0; j < 3; ++j) w[j + 1] = add(w[j + 1], acc[m][j][2 * h + 1], acc[m][j + 1][2 * h]);
+              one[8] = (uint16_t)add(one[8], acc[m][3][2 * h + 1], 0.f);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) w[j] = add(w[j], acc[m][j][2 * h], acc[m][j][2 * h + 1]);
             }
           } else {
             uint4 v = *reinterpret_cast<const uint4 *>(y);
