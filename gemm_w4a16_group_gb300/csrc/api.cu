@@ -676,6 +676,7 @@ int w4a16_lora_add(const uint16_t *y, int64_t y_row, const uint16_t *x, int64_t 
   const int64_t strides[] = {y_row, x_row, a_adapter, a_row, b_adapter, b_row, out_row};
   for (int64_t s : strides)
     if (s < 0) return W4A16_ERR_INVALID_ARG;
+  if (y_row >= 1 << 30 || x_row >= 1 << 30 || out_row >= 1 << 30) return W4A16_ERR_INVALID_ARG;
   if (tokens > 1 && out_row < outer) return W4A16_ERR_INVALID_ARG;
   if (!rows_apart(y, y_row, out, out_row, tokens, outer)) return W4A16_ERR_INVALID_ARG;
   const int64_t wide[] = {x_row, a_adapter, a_row, b_adapter, b_row};

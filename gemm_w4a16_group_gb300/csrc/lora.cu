@@ -25,7 +25,9 @@ constexpr int kColumns = kWarps * 32;  // of a unit of expand
 
 struct LoraParams {
   const uint16_t *y, *x, *a, *b;
-  long long y_row, x_row, a_adapter, a_row, b_adapter, b_row, out_row;
+  int y_row, x_row;  // elements (32 bits: a token's offset is one wide multiplication)
+  long long a_adapter, a_row, b_adapter, b_row;
+  int out_row;
   const float *scale;
   const int32_t *adapter, *starts;
   int rows, tokens, adapters, rank, inner, outer, ksplit;
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(const __grid_c
     tiles.tokens(p, e, lo, lo + n, list);
     const uint16_t *xr[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) xr[h] = h * 8 + g < n ? p.x + list[h * 8 + g] * p.x_row : nullptr;
+    for (int h = 0; h < 2; ++h) xr[h] = h * 8 + g < n ? p.x + (long long)list[h * 8 + g] * p.x_row : nullptr;
     const uint16_t *ar = p.a + e * p.a_adapter + (rank0 + g) * p.a_row;
     float acc[G::NB][4] = {};
     const int s1 = (int)((long long)steps * (part + 1) / p.ksplit);
@@ -393,8 +395,8 @@ __global__ void __launch_bounds__(kThreads, ExpandGeo<RP>::CTAS) lora_expand_ker
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int token = h * 8 + g < n ? list[h * 8 + g] : 0;
-      yr[h] = p.y + token * p.y_row;
-      to[h] = p.out + token * p.out_row;
+      yr[h] = p.y + (long long)token * p.y_row;
+      to[h] = p.out + (long long)token * p.out_row;
     }
     uint4 yv[2];
     auto fetch_y = [&](int chunk) {
@@ -553,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_prompt_shrink_kernel(const _
   const int c = threadIdx.x & 7, r0 = threadIdx.x >> 3;
   const uint16_t *xr[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) xr[i] = r0 + i * 32 < n ? p.x + list[r0 + i * 32] * p.x_row + c * 8 : nullptr;
+  for (int i = 0; i < 4; ++i) xr[i] = r0 + i * 32 < n ? p.x + (long long)list[r0 + i * 32] * p.x_row + c * 8 : nullptr;
   const uint16_t *ar = p.a + e * p.a_adapter + r0 * p.a_row + c * 8;
   const uint32_t to = base + r0 * 128 + ((c ^ (r0 & 7)) << 4);
   auto fetch = [&](int i) {
@@ -705,15 +707,14 @@ __global__ void __launch_bounds__(kThreads, PromptExpandGeo<RP>::CTAS) lora_prom
              p.lists + (long long)s.tile * kListInts + threadIdx.x * 4, true);
   };
   // how many elements after a 16-byte boundary a token's row of out begins
-  auto shift_of = [&](int token) {
-    return SHIFT ? (int)((reinterpret_cast<uintptr_t>(p.out) / 2 + token * p.out_row) & 7) : 0;
-  };
+  const uint32_t out_at = (uint32_t)(reinterpret_cast<uintptr_t>(p.out) / 2);
+  auto shift_of = [&](int token) { return SHIFT ? (int)(out_at + (uint32_t)token * (uint32_t)p.out_row & 7u) : 0; };
   // y's columns c .. c + 7 of a row, one by one, to shared memory
-  auto slow = [&](const uint16_t *row, int c, int c0, int to) {
+  auto slow = [&](const uint16_t *from, int c, int c0, int to) {
     uint16_t *v = reinterpret_cast<uint16_t *>(smem + to);
 #pragma unroll 1
     for (int k = 0; k < 8; ++k)
-      if (c + k >= c0 && c + k < p.outer) v[k] = __ldcg(row + c + k);
+      if (c + k >= c0 && c + k < p.outer) v[k] = __ldcg(from + k);
   };
   // y and x A^T of a step; a warp brings y of four rows
   auto fetch = [&](const Step &s, int low, int out) {
@@ -724,55 +725,57 @@ __global__ void __launch_bounds__(kThreads, PromptExpandGeo<RP>::CTAS) lora_prom
       for (int i = 0; i < (32 * RP / 4 + kThreads - 1) / kThreads; ++i) {
         const int id = i * kThreads + threadIdx.x, row = id / (RP / 4), c = id % (RP / 4);
         if (row < n)
-          copy16(base + low * G::LOW + row * G::ROW + c * 16, p.low + (long long)list[row] * (2 * RP) + c * 8, true);
+          copy16(base + low * G::LOW + row * G::ROW + c * 16, p.low + (long long)list[row] * (2 * RP) + c * 8);
       }
     }
+    const int4 four = *reinterpret_cast<const int4 *>(list + warp * 4);
+    const int tokens[4] = {four.x, four.y, four.z, four.w};
+    const bool inner = c0 > 0 && c0 + kColumns + 8 <= p.outer && (!SHIFT || p.alike);  // whole pieces on all sides
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = warp * 4 + i;
+      const int r = warp * 4 + i, token = tokens[i];
       if (r >= n) break;
-      const int token = list[r], sh = shift_of(token), c = c0 + 8 * lane - sh;
-      const uint16_t *row = p.y + token * p.y_row;
+      const int sh = shift_of(token);
+      const uint16_t *row = p.y + (long long)token * p.y_row + (c0 - sh);
       const int at = G::OFF_OUT + out * G::OUT + r * G::PITCH;
-      if (!SHIFT) {
-        if (c + 8 <= p.outer) copy16(base + at + lane * 16, row + c);
-        else slow(row, c, c0, at + lane * 16);
+      // (a piece is brought with what it holds of the columns beside, which is not used; where that is not y's, slowly)
+      if (inner) {
+        copy16(base + at + lane * 16, row + 8 * lane);
+        if (SHIFT && lane == 0) copy16(base + at + kColumns * 2, row + kColumns);
       } else {
-        // whole pieces, with what they hold of the columns beside (which is not used); not where that is not y's
-        const uint16_t *end = p.y + (p.tokens - 1) * p.y_row + p.outer;
-        auto piece_of = [&](int l) {
-          const int cl = c0 + 8 * l - sh;
-          if (cl >= p.outer) return;
-          if (p.alike && row + cl >= p.y && row + cl + 8 <= end) copy16(base + at + l * 16, row + cl);
-          else slow(row, cl, c0, at + l * 16);
-        };
-        piece_of(lane);
-        if (sh && lane == 0) piece_of(32);
+        for (int l = lane; l < (SHIFT ? 33 : 32); l += 32) {
+          const int c = c0 - sh + 8 * l;
+          if (c >= p.outer || c + 8 <= c0) continue;
+          if ((!SHIFT || p.alike) && (c >= 0 || token > 0) && (c + 8 <= p.outer || token + 1 < p.tokens && SHIFT))
+            copy16(base + at + l * 16, row + 8 * l);
+          else slow(row + 8 * l, c, c0, at + l * 16);
+        }
       }
     }
   };
   auto store = [&](const Step &s, int out) {
     const int *list = list_of(s) + s.half * 32;
     const int n = tokens_of(s), c0 = s.chunk * kColumns;
+    const int4 four = *reinterpret_cast<const int4 *>(list + warp * 4);
+    const int tokens[4] = {four.x, four.y, four.z, four.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = warp * 4 + i;
+      const int r = warp * 4 + i, token = tokens[i];
       if (r >= n) break;
-      const int token = list[r], sh = shift_of(token), c = c0 + 8 * lane - sh;
-      uint16_t *row = p.out + token * p.out_row;
+      const int sh = shift_of(token), left = p.outer - c0 + sh;  // places of the row from here on
+      uint16_t *row = p.out + (long long)token * p.out_row + (c0 - sh);
       const uint8_t *from = smem + G::OFF_OUT + out * G::OUT + r * G::PITCH;
-      if (c >= c0 && c + 8 <= p.outer) *reinterpret_cast<uint4 *>(row + c) = *reinterpret_cast<const uint4 *>(from + lane * 16);
-      // the places before the first whole piece, past the chunk's 256, and of the row's last piece, one a lane
+      if (8 * lane >= sh && 8 * lane + 8 <= left)
+        *reinterpret_cast<uint4 *>(row + 8 * lane) = *reinterpret_cast<const uint4 *>(from + lane * 16);
+      // the places before the first whole piece and past the chunk's 256, and of the row's last piece, one a lane
       const uint16_t *one = reinterpret_cast<const uint16_t *>(from);
       if (SHIFT && sh) {
-        if (lane < 8 && lane >= sh && c0 - sh + lane < p.outer) row[c0 - sh + lane] = one[lane];
-        const int last = c0 + kColumns - sh + lane;
-        if (lane < sh && last < p.outer) row[last] = one[kColumns + lane];
+        const int place = lane >= sh && lane < 8 ? lane : kColumns + lane;
+        if (place < kColumns + sh && place < left) row[place] = one[place];
       }
-      const int left = p.outer - c0 + sh;  // places of the row from here on
       if (left < kColumns && left % 8) {
         const int place = left / 8 * 8 + lane;
-        if (place < left && place >= (sh ? 8 : 0)) row[c0 - sh + place] = one[place];
+        if (place < left && place >= (sh ? 8 : 0)) row[place] = one[place];
       }
     }
   };
@@ -833,6 +836,29 @@ __global__ void __launch_bounds__(kThreads, PromptExpandGeo<RP>::CTAS) lora_prom
           }
         }
       }
+      // y at the lane's places, read before there are sums to add: eight columns of four tokens. (SHIFT: from the word
+      // that the first is in; with an odd place the first and the last word are shared with other lanes.)
+      uint32_t *at[2][2], yw[2][2][SHIFT ? 5 : 4];
+      bool odd[2][2];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = m * 16 + h * 8 + g;
+          const int place = warp * 32 + 8 * t + shift_of(list_of(now)[now.half * 32 + r]);
+          odd[m][h] = place & 1;
+          at[m][h] = reinterpret_cast<uint32_t *>(smem + G::OFF_OUT + out * G::OUT + r * G::PITCH + (place & ~1) * 2);
+          if (SHIFT) {
+#pragma unroll
+            for (int j = 0; j < 5; ++j) yw[m][h][j] = at[m][h][j];
+          } else {
+            const uint4 v = *reinterpret_cast<const uint4 *>(at[m][h]);
+            yw[m][h][0] = v.x;
+            yw[m][h][1] = v.y;
+            yw[m][h][2] = v.z;
+            yw[m][h][3] = v.w;
+          }
+        }
       // (both blocks of 16 tokens at once, eight sums that do not wait for one another)
       float acc[2][4][4] = {};
 #pragma unroll
@@ -860,31 +886,24 @@ __global__ void __launch_bounds__(kThreads, PromptExpandGeo<RP>::CTAS) lora_prom
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int r = m * 16 + h * 8 + g;
-          uint16_t *y = reinterpret_cast<uint16_t *>(smem + G::OFF_OUT + out * G::OUT + r * G::PITCH) + warp * 32 + 8 * t;
-          if (SHIFT) {
-            if (r >= n) continue;
-            // two places to a word; with an odd shift the first and the last share theirs with other lanes
-            const int place = warp * 32 + 8 * t + shift_of(list_of(now)[now.half * 32 + r]);
-            uint32_t *w = reinterpret_cast<uint32_t *>(smem + G::OFF_OUT + out * G::OUT + r * G::PITCH + (place & ~1) * 2);
-            uint16_t *one = reinterpret_cast<uint16_t *>(w);
-            auto add = [](uint32_t v, float lo, float hi) { return pack_bf16(bf16lo_to_f32(v) + lo, bf16hi_to_f32(v) + hi); };
-            if (place & 1) {
-              one[1] = (uint16_t)add(one[1], acc[m][0][2 * h], 0.f);
+          uint32_t *to = at[m][h], v[4];
 #pragma unroll
-              for (int j = 0; j < 3; ++j) w[j + 1] = add(w[j + 1], acc[m][j][2 * h + 1], acc[m][j + 1][2 * h]);
-              one[8] = (uint16_t)add(one[8], acc[m][3][2 * h + 1], 0.f);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) w[j] = add(w[j], acc[m][j][2 * h], acc[m][j][2 * h + 1]);
-            }
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t y = SHIFT ? __funnelshift_r(yw[m][h][j], yw[m][h][SHIFT ? j + 1 : j], odd[m][h] ? 16 : 0) : yw[m][h][j];
+            v[j] = pack_bf16(bf16lo_to_f32(y) + acc[m][j][2 * h], bf16hi_to_f32(y) + acc[m][j][2 * h + 1]);
+          }
+          if (!SHIFT) {
+            *reinterpret_cast<uint4 *>(to) = make_uint4(v[0], v[1], v[2], v[3]);
           } else {
-            uint4 v = *reinterpret_cast<const uint4 *>(y);
-            v.x = pack_bf16(bf16lo_to_f32(v.x) + acc[m][0][2 * h], bf16hi_to_f32(v.x) + acc[m][0][2 * h + 1]);
-            v.y = pack_bf16(bf16lo_to_f32(v.y) + acc[m][1][2 * h], bf16hi_to_f32(v.y) + acc[m][1][2 * h + 1]);
-            v.z = pack_bf16(bf16lo_to_f32(v.z) + acc[m][2][2 * h], bf16hi_to_f32(v.z) + acc[m][2][2 * h + 1]);
-            v.w = pack_bf16(bf16lo_to_f32(v.w) + acc[m][3][2 * h], bf16hi_to_f32(v.w) + acc[m][3][2 * h + 1]);
-            *reinterpret_cast<uint4 *>(y) = v;
+            uint16_t *one = reinterpret_cast<uint16_t *>(to);
+            if (odd[m][h]) {
+              one[1] = (uint16_t)v[0];
+              one[8] = (uint16_t)(v[3] >> 16);
+            } else {
+              to[0] = v[0];
+            }
+#pragma unroll
+            for (int j = 1; j < 4; ++j) to[j] = odd[m][h] ? __funnelshift_r(v[j - 1], v[j], 16) : v[j];
           }
         }
     }
@@ -988,10 +1007,11 @@ size_t lora_workspace_bytes(int tokens, int rank, int inner) {
 }
 
 cudaError_t launch_lora_add(const LoraCall &c) {
-  LoraParams p{c.y, c.x, c.a, c.b, c.y_row, c.x_row, c.a_adapter, c.a_row, c.b_adapter, c.b_row, c.out_row,
+  LoraParams p{c.y, c.x, c.a, c.b, (int)c.y_row, (int)c.x_row, c.a_adapter, c.a_row, c.b_adapter, c.b_row, (int)c.out_row,
                c.scale, c.adapter, c.starts, c.rows, c.tokens, c.adapters, c.rank, c.inner, c.outer,
                1, c.out, nullptr, nullptr, nullptr, nullptr, c.err, c.out == c.y && c.out_row == c.y_row,
-               (reinterpret_cast<uintptr_t>(c.out) - reinterpret_cast<uintptr_t>(c.y)) % 16 == 0 && (c.out_row - c.y_row) % 8 == 0};
+               (reinterpret_cast<uintptr_t>(c.out) - reinterpret_cast<uintptr_t>(c.y)) % 16 == 0 && (c.out_row - c.y_row) % 8 == 0 &&
+                   (c.y_row >= c.outer || c.tokens == 1)};
   uint8_t *ws = static_cast<uint8_t *>(c.workspace);
   if (few(c.tokens)) {
     p.ksplit = parts_of(c.tokens, c.rank, c.inner);

@@ -539,7 +539,8 @@ int w4a16_kv_reserve(int32_t *page_table, int max_pages, int table_rows, int32_t
  * NULL: rows = tokens and each token is a row). y is what a w4a16 product gave
  * for the same x. A row with adapter -1 gets y, bit by bit.
  *
- *   y, out     bf16 [tokens][outer], element (t, n) at t * row stride + n. out
+ *   y, out     bf16 [tokens][outer], element (t, n) at t * row stride + n (row
+ *              strides of y, out and x below 2^30 elements). out
  *              may be y (then rows without an adapter are not touched); it must
  *              not overlap y otherwise, nor a, b or x's other rows
  *   x          bf16 [tokens][inner], x_row a multiple of 8, base 16-byte aligned
