@@ -652,11 +652,14 @@ __global__ void __launch_bounds__(kThreads, 2) lora_prompt_shrink_kernel(const _
 }
 
 // ---------------------------------------------------------------------------
-// expand: a CTA keeps 256 columns of B in registers for as many tiles of one
-// adapter as it comes by, 32 tokens a step. y is copied to shared memory two
-// steps ahead, x A^T with it; the products are added there in place, and a step
-// later the sums leave in whole rows of 512 bytes (the fragments' own 64 bytes
-// of eight rows reach 5.6 TB/s, rows 6.2: 4,096 x 34,816 elements, copied).
+// expand: a step is 128 tokens of one adapter and NC columns. x A^T of the
+// tokens stays in shared memory (both parts side by side, so that one row of B
+// serves the two), B comes for each step, the product is tcgen05's, 128 by NC, in
+// one of two TMEM buffers. y is copied to shared memory two steps ahead; the
+// products are added there in place, and a step later the sums leave in whole
+// rows. Bound by HBM, which does 6.0 - 6.2 TB/s of such rows read and written.
+// (With mma.sync and B in registers the warps had 460 - 560 instructions for
+// 1,024 elements and ranks of 64 took 63 us where 16 took 36.)
 //
 // Rows need not begin on 16 bytes: element c of a row that begins s elements
 // after such a boundary has place c + s, and places are moved eight at a time
@@ -664,51 +667,90 @@ __global__ void __launch_bounds__(kThreads, 2) lora_prompt_shrink_kernel(const _
 // ---------------------------------------------------------------------------
 template <int RP>
 struct PromptExpandGeo {
-  static constexpr int KS = RP < 32 ? 1 : RP / 32;
-  static constexpr int ROW = RP * 4 + (RP == 8 ? 16 : RP == 16 ? 32 : 64);  // bytes of a token: both parts, without bank conflicts
-  static constexpr int LOW = 32 * ROW;
-  static constexpr int PITCH = kColumns * 2 + 64;  // bytes of a token's y: 256 places and up to 7 more, without bank conflicts
-  static constexpr int OUT = 32 * PITCH;
-  static constexpr int OFF_OUT = 3 * LOW, OFF_LISTS = OFF_OUT + 4 * OUT;
-  static constexpr int SMEM = OFF_LISTS + 8 * kListInts * 4;
-  static constexpr int CTAS = RP <= 64 ? 2 : 1;  // per SM
+  static constexpr int THREADS = 512;
+  static constexpr int NC = RP <= 64 ? 128 : 64;
+  static constexpr int A_PANELS = (2 * RP + 63) / 64, A = A_PANELS * 128 * 128;  // of 64 k, rows of 128 bytes, swizzled
+  static constexpr int B_PANELS = (RP + 63) / 64, B_PANEL = NC * 128, B = B_PANELS * B_PANEL;
+  static constexpr int PITCH = NC * 2 + 16;  // bytes of a token's y: NC places and up to 7 more, without bank conflicts
+  static constexpr int OUT = 128 * PITCH;
+  static constexpr int OFF_B = A, OFF_OUT = OFF_B + 3 * B, OFF_LISTS = OFF_OUT + 4 * OUT;
+  static constexpr int OFF_BAR = OFF_LISTS + 8 * 2 * kListInts * 4;
+  static constexpr int SMEM = OFF_BAR + 32 + 1024;
+  static constexpr int COLS = 2 * NC;         // of TMEM
+  static constexpr int LANES = NC / 8;        // 16-byte pieces of a row
+  static constexpr int ROWS = 32 / LANES;     // rows of a warp's copy
+  static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
 template <int RP, bool SHIFT>
-__global__ void __launch_bounds__(kThreads, PromptExpandGeo<RP>::CTAS) lora_prompt_expand_kernel(const __grid_constant__ LoraParams p) {
+__global__ void __launch_bounds__(512, 1) lora_prompt_expand_kernel(const __grid_constant__ LoraParams p) {
   using G = PromptExpandGeo<RP>;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(16) uint8_t raw[];
+  uint8_t *smem = raw + (1024 - smem_u32(raw) % 1024) % 1024;  // (the swizzle goes by address)
   const int *lists = reinterpret_cast<const int *>(smem + G::OFF_LISTS);
-  const uint32_t base = smem_u32(smem);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  volatile int *abort = reinterpret_cast<volatile int *>(smem + G::OFF_BAR + 16);
+  const uint32_t base = smem_u32(smem), bar = base + G::OFF_BAR, slot = bar + 20;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int chunks = (p.outer + kColumns - 1) / kColumns, tiles = __ldcg(p.head + (p.in_place ? 0 : 1));
-  const long long units = (long long)chunks * tiles, first = units * blockIdx.x / gridDim.x;
-  const int count = (int)(units * (blockIdx.x + 1) / gridDim.x - first);
+  const int chunks = (p.outer + G::NC - 1) / G::NC, tiles = __ldcg(p.head + (p.in_place ? 0 : 1)) / 2;
+  const long long steps = (long long)chunks * tiles, first = steps * blockIdx.x / gridDim.x;
+  const int count = (int)(steps * (blockIdx.x + 1) / gridDim.x - first);
   if (count <= 0) return;
+  if (warp == 0) {
+    tmem_alloc(slot, G::COLS);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    *abort = 0;
+    mbar_init(bar, 1);
+    mbar_init(bar + 8, 1);
+    fence_mbar_init();
+  }
 
-  // A unit is a chunk of columns and a tile; the tiles of one chunk come one after the other. A step is half a unit's
-  // tokens. Unit i's list is in slot i of a ring of 8.
+  // Step i of this CTA's: a tile and a chunk of columns; the chunks of one tile come one after the other. A tile's two
+  // lists are in a slot of a ring of 8.
   struct Step {
-    int unit, chunk, tile, half;
+    int i, tile, chunk;
   };
-  auto next_unit = [&](const Step &s) {
-    return s.tile + 1 < tiles ? Step{s.unit + 1, s.chunk, s.tile + 1, 0} : Step{s.unit + 1, s.chunk + 1, 0, 0};
-  };
-  auto list_of = [&](const Step &s) { return lists + (s.unit & 7) * kListInts; };
-  auto tokens_of = [&](const Step &s) { return min(list_of(s)[kTile + 1] - s.half * 32, 32); };
-  auto after = [&](const Step &s) {
-    return s.half == 0 && list_of(s)[kTile + 1] > 32 ? Step{s.unit, s.chunk, s.tile, 1} : next_unit(s);
-  };
-  auto fetch_list = [&](const Step &s) {
-    if (s.unit < count && threadIdx.x < kListInts / 4)
-      copy16(base + G::OFF_LISTS + (s.unit & 7) * kListInts * 4 + threadIdx.x * 16,
-             p.lists + (long long)s.tile * kListInts + threadIdx.x * 4, true);
+  auto after = [&](const Step &s) { return s.chunk + 1 < chunks ? Step{s.i + 1, s.tile, s.chunk + 1} : Step{s.i + 1, s.tile + 1, 0}; };
+  auto list_of = [&](int tile) { return lists + (tile & 7) * 2 * kListInts; };
+  auto token_of = [&](int tile, int r) { return list_of(tile)[r + (r < kTile ? 0 : kListInts - kTile)]; };
+  auto adapter_of = [&](int tile) { return list_of(tile)[kTile]; };
+  auto tokens_of = [&](int tile) { return list_of(tile)[kTile + 1] + list_of(tile)[kListInts + kTile + 1]; };
+  auto fetch_list = [&](int tile) {
+    if (tile < tiles && threadIdx.x < 2 * kListInts / 4)
+      copy16(base + G::OFF_LISTS + (tile & 7) * 2 * kListInts * 4 + threadIdx.x * 16,
+             p.lists + 2ll * tile * kListInts + threadIdx.x * 4);
   };
   // how many elements after a 16-byte boundary a token's row of out begins
   const uint32_t out_at = (uint32_t)(reinterpret_cast<uintptr_t>(p.out) / 2);
   auto shift_of = [&](int token) { return SHIFT ? (int)(out_at + (uint32_t)token * (uint32_t)p.out_row & 7u) : 0; };
+
+  auto fetch_a = [&](int tile) {  // x A^T of a tile
+    const int n = tokens_of(tile);
+#pragma unroll 4
+    for (int id = threadIdx.x; id < 128 * RP / 4; id += G::THREADS) {
+      const int r = id / (RP / 4), c = id % (RP / 4);
+      if (r < n)
+        copy16(base + c / 8 * 128 * 128 + r * 128 + ((c % 8 ^ (r & 7)) << 4), p.low + (long long)token_of(tile, r) * (2 * RP) + c * 8);
+    }
+  };
+  auto fetch_b = [&](const Step &s) {
+    const int e = adapter_of(s.tile);
+    if (e >= p.adapters) return;
+    const uint16_t *b = p.b + e * p.b_adapter + (long long)s.chunk * G::NC * p.b_row;
+    const int rows = p.outer - s.chunk * G::NC;
+    const uint32_t to = base + G::OFF_B + s.i % 3 * G::B;
+#pragma unroll
+    for (int id = threadIdx.x; id < G::NC * RP / 8; id += G::THREADS) {
+      const int r = id / (RP / 8), c = id % (RP / 8);
+      if (r < rows) {
+        const bool in = c * 8 < p.rank;
+        copy16(to + c / 8 * G::B_PANEL + r * 128 + ((c % 8 ^ (r & 7)) << 4), in ? b + r * p.b_row + c * 8 : p.b, in);
+      }
+    }
+  };
   // y's columns c .. c + 7 of a row, one by one, to shared memory
   auto slow = [&](const uint16_t *from, int c, int c0, int to) {
     uint16_t *v = reinterpret_cast<uint16_t *>(smem + to);
@@ -716,210 +758,207 @@ __global__ void __launch_bounds__(kThreads, PromptExpandGeo<RP>::CTAS) lora_prom
     for (int k = 0; k < 8; ++k)
       if (c + k >= c0 && c + k < p.outer) v[k] = __ldcg(from + k);
   };
-  // y and x A^T of a step; a warp brings y of four rows
-  auto fetch = [&](const Step &s, int low, int out) {
-    const int *list = list_of(s) + s.half * 32;
-    const int n = tokens_of(s), c0 = s.chunk * kColumns;
-    if (list_of(s)[kTile] < p.adapters) {
-#pragma unroll
-      for (int i = 0; i < (32 * RP / 4 + kThreads - 1) / kThreads; ++i) {
-        const int id = i * kThreads + threadIdx.x, row = id / (RP / 4), c = id % (RP / 4);
-        if (row < n)
-          copy16(base + low * G::LOW + row * G::ROW + c * 16, p.low + (long long)list[row] * (2 * RP) + c * 8);
-      }
-    }
-    const int4 four = *reinterpret_cast<const int4 *>(list + warp * 4);
-    const int tokens[4] = {four.x, four.y, four.z, four.w};
-    const bool inner = c0 > 0 && c0 + kColumns + 8 <= p.outer && (!SHIFT || p.alike);  // whole pieces on all sides
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = warp * 4 + i, token = tokens[i];
-      if (r >= n) break;
-      const int sh = shift_of(token);
-      const uint16_t *row = p.y + (long long)token * p.y_row + (c0 - sh);
-      const int at = G::OFF_OUT + out * G::OUT + r * G::PITCH;
-      // (a piece is brought with what it holds of the columns beside, which is not used; where that is not y's, slowly)
+  auto fetch_y = [&](const Step &s) {
+    const int n = tokens_of(s.tile), c0 = s.chunk * G::NC, at = G::OFF_OUT + (s.i & 3) * G::OUT;
+    const bool inner = c0 > 0 && c0 + G::NC + 8 <= p.outer && (!SHIFT || p.alike);  // whole pieces on all sides
+    // piece l of row r (brought with what it holds of the columns beside, which is not used; where that is not y's, slowly)
+    auto bring = [&](int r, int l) {
+      if (r >= n) return;
+      const int token = token_of(s.tile, r), c = c0 - shift_of(token) + 8 * l;
+      const uint16_t *from = p.y + (long long)token * p.y_row + c;
       if (inner) {
-        copy16(base + at + lane * 16, row + 8 * lane);
-        if (SHIFT && lane == 0) copy16(base + at + kColumns * 2, row + kColumns);
-      } else {
-        for (int l = lane; l < (SHIFT ? 33 : 32); l += 32) {
-          const int c = c0 - sh + 8 * l;
-          if (c >= p.outer || c + 8 <= c0) continue;
-          if ((!SHIFT || p.alike) && (c >= 0 || token > 0) && (c + 8 <= p.outer || token + 1 < p.tokens && SHIFT))
-            copy16(base + at + l * 16, row + 8 * l);
-          else slow(row + 8 * l, c, c0, at + l * 16);
+        copy16(base + at + r * G::PITCH + l * 16, from);
+      } else if (c < p.outer && c + 8 > c0) {
+        if ((!SHIFT || p.alike) && (c >= 0 || token > 0) && (c + 8 <= p.outer || (SHIFT && token + 1 < p.tokens)))
+          copy16(base + at + r * G::PITCH + l * 16, from);
+        else slow(from, c, c0, at + r * G::PITCH + l * 16);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < 8 / G::ROWS; ++i) bring(warp * 8 + i * G::ROWS + lane / G::LANES, lane % G::LANES);
+    if (SHIFT && lane < 8) bring(warp * 8 + lane, G::LANES);
+  };
+  auto store = [&](const Step &s) {
+    const int n = tokens_of(s.tile), c0 = s.chunk * G::NC;
+    const uint8_t *from = smem + G::OFF_OUT + (s.i & 3) * G::OUT;
+#pragma unroll
+    for (int i = 0; i < 8 / G::ROWS; ++i) {
+      const int r = warp * 8 + i * G::ROWS + lane / G::LANES, l = lane % G::LANES;
+      if (r >= n) continue;
+      const int token = token_of(s.tile, r), sh = shift_of(token), left = p.outer - c0 + sh;  // places of the row from here on
+      if (8 * l >= sh && 8 * l + 8 <= left)
+        *reinterpret_cast<uint4 *>(p.out + (long long)token * p.out_row + (c0 - sh) + 8 * l) =
+            *reinterpret_cast<const uint4 *>(from + r * G::PITCH + l * 16);
+    }
+    // the places before the first whole piece and past the chunk's, and of the row's last piece, one a thread
+    const bool last = c0 + G::NC >= p.outer;
+    if (SHIFT || (last && p.outer % 8)) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = warp * 8 + i * 4 + lane / 8, k = lane % 8;
+        if (r >= n) continue;
+        const int token = token_of(s.tile, r), sh = shift_of(token), left = p.outer - c0 + sh;
+        uint16_t *row = p.out + (long long)token * p.out_row + (c0 - sh);
+        const uint16_t *one = reinterpret_cast<const uint16_t *>(from + r * G::PITCH);
+        if (SHIFT && sh) {
+          const int place = k >= sh ? k : G::NC + k;
+          if (place < left) row[place] = one[place];
+        }
+        if (left < G::NC && left % 8) {
+          const int place = left / 8 * 8 + k;
+          if (place < left && place >= (sh ? 8 : 0)) row[place] = one[place];
         }
       }
     }
   };
-  auto store = [&](const Step &s, int out) {
-    const int *list = list_of(s) + s.half * 32;
-    const int n = tokens_of(s), c0 = s.chunk * kColumns;
-    const int4 four = *reinterpret_cast<const int4 *>(list + warp * 4);
-    const int tokens[4] = {four.x, four.y, four.z, four.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = warp * 4 + i, token = tokens[i];
-      if (r >= n) break;
-      const int sh = shift_of(token), left = p.outer - c0 + sh;  // places of the row from here on
-      uint16_t *row = p.out + (long long)token * p.out_row + (c0 - sh);
-      const uint8_t *from = smem + G::OFF_OUT + out * G::OUT + r * G::PITCH;
-      if (8 * lane >= sh && 8 * lane + 8 <= left)
-        *reinterpret_cast<uint4 *>(row + 8 * lane) = *reinterpret_cast<const uint4 *>(from + lane * 16);
-      // the places before the first whole piece and past the chunk's 256, and of the row's last piece, one a lane
-      const uint16_t *one = reinterpret_cast<const uint16_t *>(from);
-      if (SHIFT && sh) {
-        const int place = lane >= sh && lane < 8 ? lane : kColumns + lane;
-        if (place < kColumns + sh && place < left) row[place] = one[place];
-      }
-      if (left < kColumns && left % 8) {
-        const int place = left / 8 * 8 + lane;
-        if (place < left && place >= (sh ? 8 : 0)) row[place] = one[place];
-      }
-    }
-  };
 
-  Step now{0, (int)(first / tiles), (int)(first % tiles), 0}, ahead = now;
-  Step listed = now;  // the next unit whose list is to be fetched
+  Step now{0, (int)(first / chunks), (int)(first % chunks)}, before = now;
+  Step next = after(now), ahead_y = now, ahead_b = now;  // ahead: the next ones to be fetched
+  int listed = now.tile, held = now.tile;  // the next list to be fetched; the tile that A is of
 #pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    fetch_list(listed);
-    listed = next_unit(listed);
-  }
+  for (int i = 0; i < 4; ++i) fetch_list(listed++);
   copy_commit();
   copy_wait<0>();
   __syncthreads();
-  // steps 0 and 1; a list is asked for when the unit two before it is fetched, and there two steps later
-  int low = 0, out = 0;  // slots of step `now`: 3 of x A^T, 4 of y
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (ahead.unit < count) {
-      fetch(ahead, i, i);
-      ahead = after(ahead);
+  tc_fence_after();
+  const uint32_t tmem = lds32(slot);
+  __syncwarp();
+
+  bool ok = true;
+  int issued = 0;  // products so far: number m goes to TMEM buffer and barrier m % 2
+  auto wait = [&](int m) {
+    if (ok && !mbar_wait<true>(bar + 8 * (m & 1), m >> 1 & 1, abort)) {
+      ok = false;
+      *abort = 1;
+      atomicOr(p.err, kErrTimeout);
     }
-    copy_commit();
-  }
-  fetch_list(listed);
-  listed = next_unit(listed);
-  uint4 bv[4][G::KS];
-  int held_chunk = -1, held_adapter = -1;  // what bv is of
-  Step before = now;
-  bool begun = false;
-  while (now.unit < count) {
+  };
+  auto multiply = [&](const Step &s) {  // (what it needs is in shared memory, and fenced)
+    if (adapter_of(s.tile) >= p.adapters) return;
+    if (threadIdx.x == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(128, G::NC);
+      const uint32_t b = base + G::OFF_B + s.i % 3 * G::B, d = tmem + (issued & 1) * G::NC;
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int k = 0; k < RP; k += 16) {
+          const int ka = part * RP + k;
+          tc_mma_f16(d, sw128_desc(base + ka / 64 * 128 * 128) + ka % 64 / 8, sw128_desc(b + k / 64 * G::B_PANEL) + k % 64 / 8, idesc,
+                     (uint32_t)(ka != 0));
+        }
+      tc_commit(bar + 8 * (issued & 1));
+    }
+    ++issued;
+  };
+  auto fetch_y_next = [&]() {
+    if (ahead_y.i < count) {
+      fetch_y(ahead_y);
+      const int tile = ahead_y.tile;
+      ahead_y = after(ahead_y);
+      if (ahead_y.tile != tile) fetch_list(listed++);  // (of the tile three on: B is a step ahead of y)
+    }
+  };
+  auto fetch_b_next = [&]() {
+    if (ahead_b.i < count) {
+      fetch_b(ahead_b);
+      ahead_b = after(ahead_b);
+    }
+  };
+  fetch_a(now.tile);
+  fetch_b_next();
+  copy_commit();
+  fetch_y_next();
+  fetch_b_next();
+  copy_commit();
+  fetch_y_next();
+  fetch_b_next();
+  copy_commit();
+  copy_wait<2>();
+  fence_proxy_async_smem();
+  __syncthreads();
+  multiply(now);
+  for (; now.i < count; before = now, now = next, next = after(next)) {
     copy_wait<1>();
-    __syncthreads();  // this step's y and x A^T are there, and the sums of the step before
-    if (begun) store(before, (out + 3) & 3);
-    if (ahead.unit < count) {
-      const int unit = ahead.unit;
-      fetch(ahead, low == 0 ? 2 : low - 1, (out + 2) & 3);
-      ahead = after(ahead);
-      if (ahead.unit != unit) {
-        fetch_list(listed);
-        listed = next_unit(listed);
-      }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();  // this step's y and the next one's B are there, the sums of the step before, and its TMEM is read
+    tc_fence_after();
+    const int mine = issued - 1;
+    const bool adapted = adapter_of(now.tile) < p.adapters;
+    if (next.i < count && next.tile != held) {
+      if (adapted) wait(mine);  // (A is still being read)
+      held = next.tile;
+      if (adapter_of(held) < p.adapters) fetch_a(held);
+      copy_commit();
+      copy_wait<0>();
+      fence_proxy_async_smem();
+      __syncthreads();
     }
+    if (next.i < count) multiply(next);
+    if (adapted) wait(mine);
+    fetch_y_next();
+    fetch_b_next();
     copy_commit();
-    const int e = list_of(now)[kTile], n = tokens_of(now);
-    if (e < p.adapters && n > 0) {
-      if (now.chunk != held_chunk || e != held_adapter) {
-        held_chunk = now.chunk;
-        held_adapter = e;
+    if (now.i) store(before);
+    if (adapted) {
+      tc_fence_after();
+      constexpr int W = G::NC / 4;  // columns of a warp
+      const int r = (warp & 3) * 32 + lane, c = (warp >> 2) * W;
+      const bool there = r < tokens_of(now.tile);
+      const int place = c + (SHIFT && there ? shift_of(token_of(now.tile, r)) : 0);
+      uint8_t *row = smem + G::OFF_OUT + (now.i & 3) * G::OUT + r * G::PITCH;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int col = now.chunk * kColumns + warp * 32 + 8 * (g >> 1) + 2 * j + (g & 1);
-          const uint8_t *br = reinterpret_cast<const uint8_t *>(p.b + e * p.b_adapter + col * p.b_row);
+      for (int q = 0; q < W / 16; ++q) {
+        float v[16];
+        __syncwarp();
+        tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (mine & 1) * G::NC + c + q * 16, v);
+        if (!there) continue;
 #pragma unroll
-          for (int s = 0; s < G::KS; ++s) {
-            const int k = RP < 32 ? t * (RP / 4) : s * 32 + t * 8;
-            bv[j][s] = col < p.outer && k < p.rank ? piece<RP>(br + k * 2) : make_uint4(0, 0, 0, 0);
-          }
-        }
-      }
-      // y at the lane's places, read before there are sums to add: eight columns of four tokens. (SHIFT: from the word
-      // that the first is in; with an odd place the first and the last word are shared with other lanes.)
-      uint32_t *at[2][2], yw[2][2][SHIFT ? 5 : 4];
-      bool odd[2][2];
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = m * 16 + h * 8 + g;
-          const int place = warp * 32 + 8 * t + shift_of(list_of(now)[now.half * 32 + r]);
-          odd[m][h] = place & 1;
-          at[m][h] = reinterpret_cast<uint32_t *>(smem + G::OFF_OUT + out * G::OUT + r * G::PITCH + (place & ~1) * 2);
-          if (SHIFT) {
-#pragma unroll
-            for (int j = 0; j < 5; ++j) yw[m][h][j] = at[m][h][j];
-          } else {
-            const uint4 v = *reinterpret_cast<const uint4 *>(at[m][h]);
-            yw[m][h][0] = v.x;
-            yw[m][h][1] = v.y;
-            yw[m][h][2] = v.z;
-            yw[m][h][3] = v.w;
-          }
-        }
-      // (both blocks of 16 tokens at once, eight sums that do not wait for one another)
-      float acc[2][4][4] = {};
-#pragma unroll
-      for (int s = 0; s < G::KS; ++s)
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          uint4 a[2][2];
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              a[m][h] = piece<RP>(smem + low * G::LOW + (m * 16 + h * 8 + g) * G::ROW + part * RP * 2 + (RP < 32 ? t * (RP / 2) : s * 64 + t * 16));
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) mma16(acc[m][j], a[m][0].x, a[m][1].x, a[m][0].y, a[m][1].y, bv[j][s].x, bv[j][s].y);
-          if (RP >= 32) {
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) mma16(acc[m][j], a[m][0].z, a[m][1].z, a[m][0].w, a[m][1].w, bv[j][s].z, bv[j][s].w);
-          }
-        }
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t *to = at[m][h], v[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t y = SHIFT ? __funnelshift_r(yw[m][h][j], yw[m][h][SHIFT ? j + 1 : j], odd[m][h] ? 16 : 0) : yw[m][h][j];
-            v[j] = pack_bf16(bf16lo_to_f32(y) + acc[m][j][2 * h], bf16hi_to_f32(y) + acc[m][j][2 * h + 1]);
-          }
+        for (int o = 0; o < 16; o += 8) {
           if (!SHIFT) {
-            *reinterpret_cast<uint4 *>(to) = make_uint4(v[0], v[1], v[2], v[3]);
+            uint4 *at = reinterpret_cast<uint4 *>(row + (place + q * 16 + o) * 2);
+            uint4 y = *at;
+            y.x = pack_bf16(bf16lo_to_f32(y.x) + v[o], bf16hi_to_f32(y.x) + v[o + 1]);
+            y.y = pack_bf16(bf16lo_to_f32(y.y) + v[o + 2], bf16hi_to_f32(y.y) + v[o + 3]);
+            y.z = pack_bf16(bf16lo_to_f32(y.z) + v[o + 4], bf16hi_to_f32(y.z) + v[o + 5]);
+            y.w = pack_bf16(bf16lo_to_f32(y.w) + v[o + 6], bf16hi_to_f32(y.w) + v[o + 7]);
+            *at = y;
           } else {
-            uint16_t *one = reinterpret_cast<uint16_t *>(to);
-            if (odd[m][h]) {
-              one[1] = (uint16_t)v[0];
-              one[8] = (uint16_t)(v[3] >> 16);
+            // from the word that the first place is in; with an odd place the first and the last word are shared
+            const bool odd = place & 1;
+            uint32_t *at = reinterpret_cast<uint32_t *>(row + ((place & ~1) + q * 16 + o) * 2), w[5], x[4];
+#pragma unroll
+            for (int j = 0; j < 5; ++j) w[j] = at[j];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t y = __funnelshift_r(w[j], w[j + 1], odd ? 16 : 0);
+              x[j] = pack_bf16(bf16lo_to_f32(y) + v[o + 2 * j], bf16hi_to_f32(y) + v[o + 2 * j + 1]);
+            }
+            uint16_t *one = reinterpret_cast<uint16_t *>(at);
+            if (odd) {
+              one[1] = (uint16_t)x[0];
+              one[8] = (uint16_t)(x[3] >> 16);
             } else {
-              to[0] = v[0];
+              at[0] = x[0];
             }
 #pragma unroll
-            for (int j = 1; j < 4; ++j) to[j] = odd[m][h] ? __funnelshift_r(v[j - 1], v[j], 16) : v[j];
+            for (int j = 1; j < 4; ++j) at[j] = odd ? __funnelshift_r(x[j - 1], x[j], 16) : x[j];
           }
         }
+      }
     }
-    before = now;
-    begun = true;
-    now = after(now);
-    low = low == 2 ? 0 : low + 1;
-    out = (out + 1) & 3;
   }
   copy_wait<0>();
+  tc_fence_before();
   __syncthreads();
-  store(before, (out + 3) & 3);
+  store(before);
+  if (!ok && issued) mbar_wait_drain(bar + 8 * (issued - 1 & 1), issued - 1 >> 1 & 1);
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, G::COLS);
 }
 
 // ---------------------------------------------------------------------------
-int padded_rank(int rank) { return rank <= 8 ? 8 : rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
+int padded_rank(int rank, bool few) { return rank <= 8 && few ? 8 : rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
 
 // Few tokens take the first pair of kernels, 16 tokens a tile: a tile of 64
 // would mostly be empty.
@@ -946,14 +985,14 @@ int cluster_of(int tokens, int inner, int sm_count) {
 long long most_clusters(int tokens, int groups) { return tokens / (2 * kTile) + (long long)groups + 1; }
 
 template <class K>
-cudaError_t launch(K kern, unsigned grid, int cluster, int smem, cudaStream_t stream, const LoraParams &p) {
+cudaError_t launch(K kern, unsigned grid, int cluster, int smem, cudaStream_t stream, const LoraParams &p, int threads = kThreads) {
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(grid, 1, 1);
-  lc.blockDim = dim3(kThreads, 1, 1);
+  lc.blockDim = dim3(threads, 1, 1);
   lc.dynamicSmemBytes = smem;
   lc.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -989,18 +1028,19 @@ cudaError_t run_prompts(const LoraCall &c, const LoraParams &p, bool even) {
                                PromptShrinkGeo<RP>::smem(c.adapters), c.stream, p);
   if (e != cudaSuccess) return e;
   return launch(even ? lora_prompt_expand_kernel<RP, false> : lora_prompt_expand_kernel<RP, true>,
-                (unsigned)(c.sm_count * PromptExpandGeo<RP>::CTAS), 1, PromptExpandGeo<RP>::SMEM, c.stream, p);
+                (unsigned)c.sm_count, 1, PromptExpandGeo<RP>::SMEM, c.stream, p, PromptExpandGeo<RP>::THREADS);
 }
 
 template <int RP>
 cudaError_t run(const LoraCall &c, const LoraParams &p, bool even) {
-  return few(c.tokens) ? run_few<RP>(c, p, even) : run_prompts<RP>(c, p, even);
+  if (few(c.tokens)) return run_few<RP>(c, p, even);
+  return run_prompts<(RP < 16 ? 16 : RP)>(c, p, even);
 }
 
 }  // namespace
 
 size_t lora_workspace_bytes(int tokens, int rank, int inner) {
-  const size_t row = padded_rank(rank) * sizeof(float);  // (two bf16 or one float32 a rank)
+  const size_t row = padded_rank(rank, few(tokens)) * sizeof(float);  // (two bf16 or one float32 a rank)
   if (few(tokens)) return align_up((size_t)parts_of(tokens, rank, inner) * tokens * row, 256);
   const int groups = tokens < kMaxAdapters ? tokens : kMaxAdapters;
   return 256 + align_up(tokens * row, 256) + align_up((size_t)most_clusters(tokens, groups) * 2 * kListInts * sizeof(int), 256);
@@ -1019,11 +1059,11 @@ cudaError_t launch_lora_add(const LoraCall &c) {
   } else {
     p.head = reinterpret_cast<int *>(ws);
     p.low = reinterpret_cast<uint16_t *>(ws + 256);
-    p.lists = reinterpret_cast<int *>(ws + 256 + align_up((size_t)c.tokens * padded_rank(c.rank) * 4, 256));
+    p.lists = reinterpret_cast<int *>(ws + 256 + align_up((size_t)c.tokens * padded_rank(c.rank, false) * 4, 256));
   }
   const uintptr_t bits = reinterpret_cast<uintptr_t>(c.y) | reinterpret_cast<uintptr_t>(c.out);
   const bool even = bits % 16 == 0 && c.y_row % 8 == 0 && c.out_row % 8 == 0;
-  switch (padded_rank(c.rank)) {
+  switch (padded_rank(c.rank, few(c.tokens))) {
     case 8: return run<8>(c, p, even);
     case 16: return run<16>(c, p, even);
     case 32: return run<32>(c, p, even);
