@@ -651,6 +651,25 @@ __global__ void __launch_bounds__(kThreads, 2) lora_prompt_shrink_kernel(const _
   cluster_sync_all();  // (the others may still be reading this CTA's part)
 }
 
+// 16 lanes of TMEM by 16 or 32 columns: thread 4g + t has of lane g columns 8i + 2t
+// and the next in v[4i], v[4i + 1], of lane g + 8 in v[4i + 2], v[4i + 3]
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(taddr)
+               : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
 // ---------------------------------------------------------------------------
 // expand: a step is 128 tokens of one adapter and NC columns. x A^T of the
 // tokens stays in shared memory (both parts side by side, so that one row of B
@@ -902,47 +921,58 @@ __global__ void __launch_bounds__(512, 1) lora_prompt_expand_kernel(const __grid
     if (now.i) store(before);
     if (adapted) {
       tc_fence_after();
-      constexpr int W = G::NC / 4;  // columns of a warp
-      const int r = (warp & 3) * 32 + lane, c = (warp >> 2) * W;
-      const bool there = r < tokens_of(now.tile);
-      const int place = c + (SHIFT && there ? shift_of(token_of(now.tile, r)) : 0);
-      uint8_t *row = smem + G::OFF_OUT + (now.i & 3) * G::OUT + r * G::PITCH;
+      constexpr int W = G::NC / 4;  // columns of a warp, which has 32 tokens
+      const int r0 = (warp & 3) * 32, c = (warp >> 2) * W, n = tokens_of(now.tile);
+      const uint32_t sums = tmem + ((uint32_t)r0 << 16) + (mine & 1) * G::NC + c;
+      uint8_t *out = smem + G::OFF_OUT + (now.i & 3) * G::OUT;
+      __syncwarp();
+      if (!SHIFT) {  // a token a lane, eight columns at a time
+        uint8_t *row = out + (r0 + lane) * G::PITCH + c * 2;
 #pragma unroll
-      for (int q = 0; q < W / 16; ++q) {
-        float v[16];
-        __syncwarp();
-        tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (mine & 1) * G::NC + c + q * 16, v);
-        if (!there) continue;
+        for (int q = 0; q < W; q += 16) {
+          float v[16];
+          tmem_ld16(sums + q, v);
 #pragma unroll
-        for (int o = 0; o < 16; o += 8) {
-          if (!SHIFT) {
-            uint4 *at = reinterpret_cast<uint4 *>(row + (place + q * 16 + o) * 2);
+          for (int o = 0; o < 16; o += 8) {
+            uint4 *at = reinterpret_cast<uint4 *>(row + (q + o) * 2);
             uint4 y = *at;
             y.x = pack_bf16(bf16lo_to_f32(y.x) + v[o], bf16hi_to_f32(y.x) + v[o + 1]);
             y.y = pack_bf16(bf16lo_to_f32(y.y) + v[o + 2], bf16hi_to_f32(y.y) + v[o + 3]);
             y.z = pack_bf16(bf16lo_to_f32(y.z) + v[o + 4], bf16hi_to_f32(y.z) + v[o + 5]);
             y.w = pack_bf16(bf16lo_to_f32(y.w) + v[o + 6], bf16hi_to_f32(y.w) + v[o + 7]);
             *at = y;
-          } else {
-            // from the word that the first place is in; with an odd place the first and the last word are shared
-            const bool odd = place & 1;
-            uint32_t *at = reinterpret_cast<uint32_t *>(row + ((place & ~1) + q * 16 + o) * 2), w[5], x[4];
+          }
+        }
+      } else {
+        // Two columns of eight tokens a lane (columns 8i + 2t, 8i + 2t + 1), so that the lanes' words, wherever the
+        // tokens' rows begin, are in different banks. Of a row that begins at an odd place a lane has columns
+        // 8i + 2t + 1 and the next instead, to make up a word, and the first and the last column go alone.
+        const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-            for (int j = 0; j < 5; ++j) w[j] = at[j];
+        for (int up = 0; up < 32; up += 16) {
+          uint32_t v[W / 2];
+          tmem_ld_16x256b(sums + ((uint32_t)up << 16), v);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t y = __funnelshift_r(w[j], w[j + 1], odd ? 16 : 0);
-              x[j] = pack_bf16(bf16lo_to_f32(y) + v[o + 2 * j], bf16hi_to_f32(y) + v[o + 2 * j + 1]);
+          for (int h = 0; h < 2; ++h) {
+            const int r = r0 + up + h * 8 + g, sh = r < n ? shift_of(token_of(now.tile, r)) : 0;
+            const bool odd = sh & 1;
+            uint16_t *y = reinterpret_cast<uint16_t *>(out + r * G::PITCH) + c + sh;  // the row's column c
+            uint32_t *words = reinterpret_cast<uint32_t *>(y + 2 * t + odd);
+#pragma unroll
+            for (int i = 0; i < W / 8; ++i) {
+              const float lo = __uint_as_float(v[4 * i + 2 * h]), hi = __uint_as_float(v[4 * i + 2 * h + 1]);
+              // (lane 3's next column is lane 0's of the next eight)
+              const uint32_t mine_next = t == 0 && i + 1 < W / 8 ? v[4 * (i + 1 < W / 8 ? i + 1 : i) + 2 * h] : v[4 * i + 2 * h];
+              const float next_lo = __uint_as_float(__shfl_sync(kFull, mine_next, (lane & ~3) | (t + 1 & 3)));
+              if (odd && i == 0 && t == 0) y[0] = (uint16_t)pack_bf16(bf16lo_to_f32(y[0]) + lo, 0.f);
+              const float a = odd ? hi : lo, b = odd ? next_lo : hi;
+              if (odd && i == W / 8 - 1 && t == 3) {
+                y[W - 1] = (uint16_t)pack_bf16(bf16lo_to_f32(y[W - 1]) + a, 0.f);
+              } else {
+                const uint32_t w = words[4 * i];
+                words[4 * i] = pack_bf16(bf16lo_to_f32(w) + a, bf16hi_to_f32(w) + b);
+              }
             }
-            uint16_t *one = reinterpret_cast<uint16_t *>(at);
-            if (odd) {
-              one[1] = (uint16_t)x[0];
-              one[8] = (uint16_t)(x[3] >> 16);
-            } else {
-              at[0] = x[0];
-            }
-#pragma unroll
-            for (int j = 1; j < 4; ++j) at[j] = odd ? __funnelshift_r(x[j - 1], x[j], 16) : x[j];
           }
         }
       }
