@@ -944,9 +944,8 @@ __global__ void __launch_bounds__(512, 1) lora_prompt_expand_kernel(const __grid
           }
         }
       } else {
-        // Two columns of eight tokens a lane (columns 8i + 2t, 8i + 2t + 1), so that the lanes' words, wherever the
-        // tokens' rows begin, are in different banks. Of a row that begins at an odd place a lane has columns
-        // 8i + 2t + 1 and the next instead, to make up a word, and the first and the last column go alone.
+        // two columns of eight tokens a lane (columns 8i + 2t, 8i + 2t + 1), one by one, so that the lanes' places,
+        // wherever the tokens' rows begin, are in different banks
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int up = 0; up < 32; up += 16) {
@@ -955,23 +954,18 @@ __global__ void __launch_bounds__(512, 1) lora_prompt_expand_kernel(const __grid
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int r = r0 + up + h * 8 + g, sh = r < n ? shift_of(token_of(now.tile, r)) : 0;
-            const bool odd = sh & 1;
-            uint16_t *y = reinterpret_cast<uint16_t *>(out + r * G::PITCH) + c + sh;  // the row's column c
-            uint32_t *words = reinterpret_cast<uint32_t *>(y + 2 * t + odd);
+            uint16_t *y = reinterpret_cast<uint16_t *>(out + r * G::PITCH) + c + sh + 2 * t, x[W / 4];
 #pragma unroll
             for (int i = 0; i < W / 8; ++i) {
-              const float lo = __uint_as_float(v[4 * i + 2 * h]), hi = __uint_as_float(v[4 * i + 2 * h + 1]);
-              // (lane 3's next column is lane 0's of the next eight)
-              const uint32_t mine_next = t == 0 && i + 1 < W / 8 ? v[4 * (i + 1 < W / 8 ? i + 1 : i) + 2 * h] : v[4 * i + 2 * h];
-              const float next_lo = __uint_as_float(__shfl_sync(kFull, mine_next, (lane & ~3) | (t + 1 & 3)));
-              if (odd && i == 0 && t == 0) y[0] = (uint16_t)pack_bf16(bf16lo_to_f32(y[0]) + lo, 0.f);
-              const float a = odd ? hi : lo, b = odd ? next_lo : hi;
-              if (odd && i == W / 8 - 1 && t == 3) {
-                y[W - 1] = (uint16_t)pack_bf16(bf16lo_to_f32(y[W - 1]) + a, 0.f);
-              } else {
-                const uint32_t w = words[4 * i];
-                words[4 * i] = pack_bf16(bf16lo_to_f32(w) + a, bf16hi_to_f32(w) + b);
-              }
+              x[2 * i] = y[8 * i];
+              x[2 * i + 1] = y[8 * i + 1];
+            }
+#pragma unroll
+            for (int i = 0; i < W / 8; ++i) {
+              const uint32_t w = pack_bf16(bf16lo_to_f32(x[2 * i]) + __uint_as_float(v[4 * i + 2 * h]),
+                                           bf16lo_to_f32(x[2 * i + 1]) + __uint_as_float(v[4 * i + 2 * h + 1]));
+              y[8 * i] = (uint16_t)w;
+              y[8 * i + 1] = (uint16_t)(w >> 16);
             }
           }
         }
