@@ -259,10 +259,10 @@ __global__ void __launch_bounds__(kProbThreads, 4) probabilities_kernel(const Pr
 // by the root's number. Children that were picked, not drawn (no q), have q = 1
 // at themselves: a refused one's probability is taken out.
 //
-// Sums are fixed point, 2^-56 in 64-bit integers: they do not depend on the
-// order, and the token drawn is the one that 64-bit floats give, also where the
-// number falls next to one of 248,320 borders (32-bit sums are off by 1e-7,
-// which moves it in one draw of a hundred).
+// Sums are 64-bit integers of probabilities in units of 2^-46: they do not depend
+// on the order, and the token drawn is the one that 64-bit floats give, also where
+// the number falls next to one of 248,320 borders (they differ in less than one
+// draw of a million; 32-bit sums, off by 1e-7, in one of a hundred).
 // ---------------------------------------------------------------------------
 constexpr int kFrac = 56;
 constexpr unsigned long long kOne = 1ull << kFrac;
@@ -301,16 +301,33 @@ struct SampleSmem {
 };
 
 __device__ __forceinline__ float sound(float p) { return fminf(fmaxf(p, 0.f), 1.f); }  // (NaN: 0)
-// p in units of 2^-56, what is below cut off: the 24 bits of its mantissa, moved
-// to their place. (A conversion to 64-bit integers would run on the double
-// precision pipe: 32 rows of two times 248,320 took 85 us, three quarters of it
-// that pipe's.)
+
+// Two probabilities, rounded to the nearest multiple of 2^-46, in two whole
+// numbers each: added to 1 the upper 23 bits of x are the mantissa's, what that
+// leaves of x is exact, and added to 1.5 * 2^-23 it has its mantissa in units of
+// 2^-46. Their sums are sums of bit patterns, two 32-bit additions for a pair.
+// (Conversions to 64-bit integers run on the double precision pipe: 32 rows of
+// two times 248,320 took 85 us, three quarters of it that pipe's; moving the
+// mantissa to its place with 64-bit shifts took 49.)
+constexpr uint32_t kUpper = 0x3F800000u, kLower = 0x34400000u;  // 1, 1.5 * 2^-23
+struct Bits {
+  uint32_t hi_a, hi_b, lo_a, lo_b;
+};
+__device__ __forceinline__ Bits bits_of(float a, float b) {
+  const f32x2 x = f32_pair(a, b), one = f32_pair(1.f, 1.f), minus = f32_pair(-1.f, -1.f);
+  const f32x2 small = f32_pair(__uint_as_float(kLower), __uint_as_float(kLower));
+  const f32x2 t = add2(x, one), low = add2(fma2(add2(t, minus), minus, x), small);
+  const float2 h = f32_halves(t), l = f32_halves(low);
+  return {__float_as_uint(h.x), __float_as_uint(h.y), __float_as_uint(l.x), __float_as_uint(l.y)};
+}
+constexpr int kBitsQuads = 32;  // 128 differences of below 2^23 each
+constexpr int kUnits = kFrac - 46;  // sums are in units of 2^-56, as what c q cuts off is
+__device__ __forceinline__ u64 join_bits(uint32_t hi, uint32_t lo) {
+  return ((u64)hi << 23) + (u64)(int64_t)(int32_t)lo << kUnits;
+}
 __device__ __forceinline__ u64 fixed(float p) {
-  const uint32_t x = __float_as_uint(sound(p));
-  const u64 top = (u64)((x & 0x7FFFFFu) | 0x800000u) << 33;
-  u64 v;
-  asm("shr.u64 %0, %1, %2;" : "=l"(v) : "l"(top), "r"(127u - (x >> 23)));  // (64 places and more: 0)
-  return v;
+  const Bits x = bits_of(sound(p), 0.f);
+  return join_bits(x.hi_a - kUpper, x.lo_a - kLower);
 }
 
 // max(p - c q, 0)
@@ -408,7 +425,9 @@ struct Walk {
   }
 };
 
-template <bool ALIGNED, int WARPS>
+// SINGLE: no row has a child (max_tree 1), so that every CTA knows what to do by
+// itself and the cluster need not be told.
+template <bool ALIGNED, bool SINGLE, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) tree_sample_kernel(const SampleParams p) {
   static_assert(WARPS <= 16 && (WARPS & (WARPS - 1)) == 0 && WARPS * 32 >= kMaxTree, "parts of a row, nodes of a tree");
   __shared__ SampleSmem sm;
@@ -422,7 +441,19 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) tree_sample_kernel(con
   const int parts_log2 = __ffs(S * WARPS) - 1;
   Walk walk;
   int n = 0, s0 = 0;
-  if (rank == 0) {
+  if (SINGLE) {
+    s0 = p.starts[b];
+    const int s1 = p.starts[b + 1];
+    n = s0 >= 0 && s1 == s0 + 1 && s1 <= p.tokens ? 1 : 0;
+    if (n != 1 && (s0 < 0 || s1 != s0 || s1 > p.tokens) && rank == 0 && tid == 0) atomicOr(p.err, kErrIndex);
+    if (tid == 0) {
+      sm.accepted = n;
+      sm.path[0] = 0;
+      sm.order.row = n ? s0 : -1;
+      sm.order.u = n ? p.u[s0] : 0.f;
+    }
+    __syncthreads();
+  } else if (rank == 0) {
     s0 = p.starts[b];
     const int s1 = p.starts[b + 1];
     n = s1 - s0;
@@ -468,10 +499,10 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) tree_sample_kernel(con
       }
     }
   }
-  cluster_wait();
+  if (!SINGLE) cluster_wait();
   int64_t none = -1;
   for (;;) {
-    if (rank == 0) {
+    if (!SINGLE && rank == 0) {
       __syncthreads();
       const uint32_t words = sizeof(Order) / 4;
       const uint32_t used = offsetof(Order, ids) / 4 + (sm.order.what == kDraw ? sm.order.gone : 0);
@@ -481,23 +512,46 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) tree_sample_kernel(con
           st_cluster_u32(mapa_shared(smem_u32(&sm.order) + 4 * w, to), reinterpret_cast<const uint32_t *>(&sm.order)[w]);
       }
     }
-    cluster_sync_all();
-    const int what = sm.order.what, row = sm.order.row, gone = sm.order.gone;
-    const u64 c = sm.order.c;
+    if (!SINGLE) cluster_sync_all();
+    const int what = SINGLE ? (int)kDraw : sm.order.what, row = sm.order.row, gone = SINGLE ? 0 : sm.order.gone;
+    const u64 c = SINGLE ? 0 : sm.order.c;
     if (what == kDone) break;
 
     // this warp's part of the row
     const float *pr = p.p + row * p.p_row, *qr = p.q + row * p.q_row;
     const int shift = ALIGNED ? (int)((row * p.p_row) & 3) : 0;
-    const Quads mine(p.vocab, shift, rank * WARPS + warp, parts_log2);
+    Quads mine(p.vocab, shift, rank * WARPS + warp, parts_log2);
+    if (SINGLE && row < 0) mine.hi = mine.lo;  // (no token: nothing to sum, and every barrier as ever)
     u64 sum = 0;
-    if (c == 0) {
+    if (c == 0 || c == kOne) {  // p, or max(p, q) - q
+      const bool both = c != 0;
+      for (int k0 = mine.lo + lane; k0 < mine.hi; k0 += 32 * kBitsQuads) {  // (so long the bits' sums hold)
+        uint32_t hi = 0, lo = 0;
+        const int k1 = min(k0 + 32 * kBitsQuads, mine.hi);
+        if (both) {
 #pragma unroll 4
-      for (int k = mine.lo + lane; k < mine.hi; k += 32) {
-        float x[4];
-        load_floats<ALIGNED>(pr, mine, k, p.vocab, x);
+          for (int k = k0; k < k1; k += 32) {
+            float x[4], y[4];
+            load_floats<ALIGNED>(pr, mine, k, p.vocab, x);
+            load_floats<ALIGNED>(qr, mine, k, p.vocab, y);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum += fixed(x[i]);
+            for (int i = 0; i < 4; ++i) {
+              const Bits d = bits_of(fminf(fmaxf(fmaxf(x[i], y[i]), 0.f), 1.f), sound(y[i]));
+              hi += d.hi_a - d.hi_b;
+              lo += d.lo_a - d.lo_b;
+            }
+          }
+        } else {
+#pragma unroll 4
+          for (int k = k0; k < k1; k += 32) {
+            float x[4];
+            load_floats<ALIGNED>(pr, mine, k, p.vocab, x);
+            const Bits d = bits_of(sound(x[0]), sound(x[1])), e = bits_of(sound(x[2]), sound(x[3]));
+            hi += d.hi_a + d.hi_b + (e.hi_a + e.hi_b) - 4 * kUpper;
+            lo += d.lo_a + d.lo_b + (e.lo_a + e.lo_b) - 4 * kLower;
+          }
+        }
+        sum += join_bits(hi, lo);
       }
     } else {
 #pragma unroll 4
@@ -517,6 +571,7 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) tree_sample_kernel(con
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
     if (lane == 0) sm.warps[warp] = sum;
     __syncthreads();
+    if (SINGLE) cluster_wait();
     if (tid < (int)S) {
       u64 all = 0;
 #pragma unroll
@@ -682,17 +737,20 @@ cudaError_t launch_probabilities(const uint16_t *logits, long long row, const fl
 }
 
 cudaError_t launch_tree_sample(const SampleCall &c) {
-  static PerDevice fits[2][2];
+  static PerDevice fits[2][2][2];
   const bool aligned = address(c.p, 16) && address(c.q, 16) && (!c.q || (c.q_row - c.p_row) % 4 == 0);
   const SampleParams p{c.p, c.q, c.p_row, c.q_row, c.draft, c.mask, c.starts, c.u, c.rows, c.tokens, c.vocab, c.max_tree,
                        c.path, c.count, c.token, c.err};
   // 16 warps a CTA while the rows' clusters are all there at once, 8 where that makes more of them
   const int s = ctas_of(c.rows, c.vocab, 32768, 1024, c.sm_count * 2);
-  if ((long long)c.rows * s * 2 <= c.sm_count * 2)
-    return launch_rows(aligned ? tree_sample_kernel<true, 16> : tree_sample_kernel<false, 16>, fits[0][aligned], c.rows, s, 512,
-                       c.device, c.stream, p);
-  return launch_rows(aligned ? tree_sample_kernel<true, 8> : tree_sample_kernel<false, 8>, fits[1][aligned], c.rows,
-                     ctas_of(c.rows, c.vocab, 32768, 1024, c.sm_count * 4), 256, c.device, c.stream, p);
+  const bool few = (long long)c.rows * s * 2 <= c.sm_count * 2, one = c.max_tree == 1;
+  void (*kern)(SampleParams);
+  if (one) kern = few ? aligned ? tree_sample_kernel<true, true, 16> : tree_sample_kernel<false, true, 16>
+                      : aligned ? tree_sample_kernel<true, true, 8> : tree_sample_kernel<false, true, 8>;
+  else kern = few ? aligned ? tree_sample_kernel<true, false, 16> : tree_sample_kernel<false, false, 16>
+                  : aligned ? tree_sample_kernel<true, false, 8> : tree_sample_kernel<false, false, 8>;
+  return launch_rows(kern, fits[one][few][aligned], c.rows, few ? s : ctas_of(c.rows, c.vocab, 32768, 1024, c.sm_count * 4),
+                     few ? 512 : 256, c.device, c.stream, p);
 }
 
 }  // namespace w4a16

@@ -486,8 +486,9 @@ int w4a16_probabilities(const uint16_t *logits, int64_t logits_row, const float 
  *   token  int64 [rows]  the token drawn (-1 for a row without new tokens)
  *
  * A NaN or negative probability counts as 0, one above 1 as 1; a drafted token
- * outside the vocabulary is passed over (W4A16_ERR_INDEX). Sums are 64-bit
- * integers in units of 2^-56, tests double: results do not depend on any order.
+ * outside the vocabulary is passed over (W4A16_ERR_INDEX). Probabilities are
+ * summed in whole multiples of 2^-46, tests are double: results do not depend on
+ * any order.
  */
 int w4a16_tree_sample(const float *p, int64_t p_row, const float *q, int64_t q_row, int vocab, const int64_t *draft,
                       const int64_t *mask, const int32_t *starts, const float *u, int rows, int tokens, int max_tree,
