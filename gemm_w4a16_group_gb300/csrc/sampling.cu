@@ -281,7 +281,7 @@ struct SampleParams {
 
 enum { kDone = 0, kSum = 1, kDraw = 2 };
 
-// What the first CTA of a cluster tells the others to do next
+// What a CTA does next
 struct Order {
   u64 c;
   int what, row, gone;  // row: of p and q; gone: children taken out
@@ -289,15 +289,22 @@ struct Order {
   int ids[kMaxTree];
 };
 
+// A node of the draft tree: its children, and what decides on itself
+struct Node {
+  u64 kids;
+  double px, qx;
+  float u;
+  int id;
+};
+static_assert(sizeof(Node) == 32, "four words of 64 bits");
+
 struct SampleSmem {
+  Node nodes[kMaxTree];
+  u64 fits;  // nodes that are accepted if they are asked first
+  int n, first;  // tokens of the row, the first of them
   Order order;
-  u64 sums[kMaxCluster], warps[16], fine[16];
-  // first CTA: nodes of the tree
-  u64 kids[kMaxTree], fits;  // fits: nodes that are accepted if they are asked first
-  double px[kMaxTree], qx[kMaxTree];
-  float u[kMaxTree];
-  int ids[kMaxTree], path[kMaxTree];
-  int accepted;
+  u64 sums[2][kMaxCluster], warps[16], fine[16];
+  int path[kMaxTree], accepted;
 };
 
 __device__ __forceinline__ float sound(float p) { return fminf(fmaxf(p, 0.f), 1.f); }  // (NaN: 0)
@@ -352,8 +359,9 @@ __device__ __forceinline__ void load_floats(const float *row, const Quads &q, in
   }
 }
 
-// The walk, as far as it gets without another sum over the vocabulary (one
-// thread of the first CTA; what it decides the others follow).
+// The walk, as far as it gets without another sum over the vocabulary. One thread
+// of every CTA walks: they have the same nodes and get the same sums, so they
+// need not wait for anybody's orders.
 struct Walk {
   u64 c, total;  // of the node that it stands on; total: the sum that `order` asked for
   u64 kids;
@@ -362,14 +370,14 @@ struct Walk {
 
   __device__ void stand(int i, const SampleSmem &sm) {
     node = i;
-    kids = sm.kids[i];
+    kids = sm.nodes[i].kids;
     c = 0;
     asked = gone = 0;
     known = false;
   }
-  __device__ void go(SampleSmem &sm, bool drawn, int first) {
+  __device__ void go(SampleSmem &sm, bool drawn) {
     Order &o = sm.order;
-    o.row = first + node;
+    o.row = sm.first + node;
     while (kids) {
       if (asked && !known) {
         o.what = kSum;
@@ -379,18 +387,19 @@ struct Walk {
       }
       const int i = __ffsll((long long)kids) - 1;
       kids &= kids - 1;
+      const Node &kid = sm.nodes[i];
       bool fits = sm.fits >> i & 1;
       if (asked) {
-        double r = sm.px[i];
-        if (drawn) r -= (double)c * 0x1p-56 * sm.qx[i];
+        double r = kid.px;
+        if (drawn) r -= (double)c * 0x1p-56 * kid.qx;
         for (int g = 0; g < gone; ++g)
-          if (o.ids[g] == sm.ids[i]) r = 0;
-        fits = (double)sm.u[i] * sm.qx[i] * ((double)total * 0x1p-56) < r;
+          if (o.ids[g] == kid.id) r = 0;
+        fits = (double)kid.u * kid.qx * ((double)total * 0x1p-56) < r;
       }
       if (fits) {
         sm.path[sm.accepted++] = i;
         stand(i, sm);
-        o.row = first + node;
+        o.row = sm.first + node;
         continue;
       }
       if (drawn) {
@@ -398,10 +407,10 @@ struct Walk {
         known = false;
       } else {
         bool twin = false;
-        for (int g = 0; g < gone; ++g) twin |= o.ids[g] == sm.ids[i];
+        for (int g = 0; g < gone; ++g) twin |= o.ids[g] == kid.id;
         if (!twin) {
-          o.ids[gone++] = sm.ids[i];
-          if (known) total -= min(total, fixed((float)sm.px[i]));
+          o.ids[gone++] = kid.id;
+          if (known) total -= min(total, fixed((float)kid.px));
         }
       }
       ++asked;
@@ -416,8 +425,8 @@ struct Walk {
     for (int g = 0; g < gone; ++g) {
       // (taken out one by one; px of a removed id is that of the child that was refused)
       for (int i = 0; i < kMaxTree; ++i)
-        if (sm.kids[node] >> i & 1 && sm.ids[i] == sm.order.ids[g]) {
-          total -= min(total, fixed((float)sm.px[i]));
+        if (sm.nodes[node].kids >> i & 1 && sm.nodes[i].id == sm.order.ids[g]) {
+          total -= min(total, fixed((float)sm.nodes[i].px));
           break;
         }
     }
@@ -440,81 +449,80 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) tree_sample_kernel(con
   const bool drawn = p.q != nullptr;
   const int parts_log2 = __ffs(S * WARPS) - 1;
   Walk walk;
-  int n = 0, s0 = 0;
   if (SINGLE) {
-    s0 = p.starts[b];
-    const int s1 = p.starts[b + 1];
-    n = s0 >= 0 && s1 == s0 + 1 && s1 <= p.tokens ? 1 : 0;
-    if (n != 1 && (s0 < 0 || s1 != s0 || s1 > p.tokens) && rank == 0 && tid == 0) atomicOr(p.err, kErrIndex);
     if (tid == 0) {
-      sm.accepted = n;
+      const int s0 = p.starts[b], s1 = p.starts[b + 1];
+      const bool sound = s0 >= 0 && s1 >= s0 && s1 - s0 <= 1 && s1 <= p.tokens;
+      if (!sound && rank == 0) atomicOr(p.err, kErrIndex);
+      sm.accepted = sound ? s1 - s0 : 0;
       sm.path[0] = 0;
-      sm.order.row = n ? s0 : -1;
-      sm.order.u = n ? p.u[s0] : 0.f;
+      sm.order.row = sm.accepted ? s0 : -1;
+      sm.order.u = sm.accepted ? p.u[s0] : 0.f;
     }
-    __syncthreads();
-  } else if (rank == 0) {
-    s0 = p.starts[b];
-    const int s1 = p.starts[b + 1];
-    n = s1 - s0;
-    if (s0 < 0 || n < 0 || n > p.max_tree || s1 > p.tokens) {
-      if (tid == 0) atomicOr(p.err, kErrIndex);
-      n = 0;
-    }
-    if (tid < kMaxTree) sm.kids[tid] = 0;
-    if (tid == 0) {
-      sm.accepted = 0;
-      sm.path[0] = 0;
-      sm.fits = 0;
-    }
-    __syncthreads();
-    if (tid < n) {
-      const u64 word = p.mask ? (u64)p.mask[s0 + tid] : ~0ull;
-      const u64 above = word & ((1ull << tid) - 1);
-      const int parent = above ? 63 - __clzll((long long)above) : -1;
-      sm.u[tid] = p.u[s0 + tid];
-      if (parent >= 0) {
-        const int64_t id = p.draft[s0 + tid];
-        if (id >= 0 && id < p.vocab) {
-          sm.ids[tid] = (int)id;
-          const double px = sound(p.p[(s0 + parent) * p.p_row + id]);
-          const double qx = drawn ? sound(p.q[(s0 + parent) * p.q_row + id]) : 1.0;
-          sm.px[tid] = px;
-          sm.qx[tid] = qx;
-          atomicOr(&sm.kids[parent], 1ull << tid);
-          if ((double)sm.u[tid] * qx < px) atomicOr(&sm.fits, 1ull << tid);
-        } else {
-          atomicOr(p.err, kErrIndex);
+  } else {
+    // the first CTA reads the tree, and the others get it from there (whatever may be written to its arrays meanwhile,
+    // all walk the same way)
+    if (rank == 0) {
+      const int s0 = p.starts[b], s1 = p.starts[b + 1];
+      const bool sound_row = s0 >= 0 && s1 >= s0 && s1 - s0 <= p.max_tree && s1 <= p.tokens;
+      const int n = sound_row ? s1 - s0 : 0;
+      if (!sound_row && tid == 0) atomicOr(p.err, kErrIndex);
+      if (tid < kMaxTree) sm.nodes[tid].kids = 0;
+      if (tid == 0) {
+        sm.fits = 0;
+        sm.n = n;
+        sm.first = s0;
+      }
+      __syncthreads();
+      if (tid < n) {
+        const u64 word = p.mask ? (u64)p.mask[s0 + tid] : ~0ull;
+        const u64 above = word & ((1ull << tid) - 1);
+        const int parent = above ? 63 - __clzll((long long)above) : -1;
+        const float u = p.u[s0 + tid];
+        sm.nodes[tid].u = u;
+        if (parent >= 0) {
+          const int64_t id = p.draft[s0 + tid];
+          if (id >= 0 && id < p.vocab) {
+            const double px = sound(p.p[(s0 + parent) * p.p_row + id]);
+            const double qx = drawn ? sound(p.q[(s0 + parent) * p.q_row + id]) : 1.0;
+            sm.nodes[tid].id = (int)id;
+            sm.nodes[tid].px = px;
+            sm.nodes[tid].qx = qx;
+            atomicOr(&sm.nodes[parent].kids, 1ull << tid);
+            if ((double)u * qx < px) atomicOr(&sm.fits, 1ull << tid);
+          } else {
+            atomicOr(p.err, kErrIndex);
+          }
         }
       }
+      __syncthreads();
     }
-    __syncthreads();
+    cluster_wait();
+    if (rank == 0) {
+      const uint32_t words = sm.n * 4 + 2;  // the nodes, and what stands behind them: fits, n and first
+      for (uint32_t i = tid; i < words * (S - 1); i += WARPS * 32) {
+        const uint32_t to = 1 + i / words, w = i % words, at = w < 2 ? kMaxTree * 4 + w : w - 2;
+        st_cluster_u64(mapa_shared(smem_u32(&sm) + 8 * at, to), reinterpret_cast<const u64 *>(&sm)[at]);
+      }
+    }
+    cluster_sync_all();
     if (tid == 0) {
+      sm.accepted = 0;
       sm.order.what = kDone;
-      if (n > 0) {
-        sm.accepted = 1;
-        sm.order.u = sm.u[0];
+      if (sm.n > 0) {
+        sm.path[sm.accepted++] = 0;
+        sm.order.u = sm.nodes[0].u;
         walk.stand(0, sm);
-        walk.go(sm, drawn, s0);
+        walk.go(sm, drawn);
       }
     }
   }
-  if (!SINGLE) cluster_wait();
   int64_t none = -1;
-  for (;;) {
-    if (!SINGLE && rank == 0) {
-      __syncthreads();
-      const uint32_t words = sizeof(Order) / 4;
-      const uint32_t used = offsetof(Order, ids) / 4 + (sm.order.what == kDraw ? sm.order.gone : 0);
-      for (uint32_t i = tid; i < used * S; i += WARPS * 32) {
-        const uint32_t to = i / used, w = i % used;
-        if (to && w < words)
-          st_cluster_u32(mapa_shared(smem_u32(&sm.order) + 4 * w, to), reinterpret_cast<const uint32_t *>(&sm.order)[w]);
-      }
-    }
-    if (!SINGLE) cluster_sync_all();
+  for (int pass = 0;; pass ^= 1) {
+    __syncthreads();
     const int what = SINGLE ? (int)kDraw : sm.order.what, row = sm.order.row, gone = SINGLE ? 0 : sm.order.gone;
     const u64 c = SINGLE ? 0 : sm.order.c;
+    const float u = sm.order.u;
     if (what == kDone) break;
 
     // this warp's part of the row
@@ -522,6 +530,11 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) tree_sample_kernel(con
     const int shift = ALIGNED ? (int)((row * p.p_row) & 3) : 0;
     Quads mine(p.vocab, shift, rank * WARPS + warp, parts_log2);
     if (SINGLE && row < 0) mine.hi = mine.lo;  // (no token: nothing to sum, and every barrier as ever)
+    if (ALIGNED && lane < 2 && (lane == 0 || c)) {  // all of the warp's part at once to L2; the loads below take it in turns
+      const int lo = max(mine.lo, mine.first), n = min(mine.hi, mine.first + mine.whole) - lo;
+      if (n > 0)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"((lane ? qr : pr) + 4 * lo - shift), "r"(16 * n) : "memory");
+    }
     u64 sum = 0;
     if (c == 0 || c == kOne) {  // p, or max(p, q) - q
       const bool both = c != 0;
@@ -576,25 +589,24 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) tree_sample_kernel(con
       u64 all = 0;
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) all += sm.warps[w];
-      st_cluster_u64(mapa_shared(smem_u32(&sm.sums[rank]), tid), all);
+      st_cluster_u64(mapa_shared(smem_u32(&sm.sums[pass][rank]), tid), all);
     }
-    const float u = sm.order.u;
-    cluster_sync_all();
+    cluster_sync_all();  // (the next pass's sums go elsewhere, so nobody waits for these to be read)
     u64 total = 0, before = 0;
     for (uint32_t i = 0; i < S; ++i) {
       if (i == rank) before = total;
-      total += sm.sums[i];
+      total += sm.sums[pass][i];
     }
     if (what == kSum) {
-      if (rank == 0 && tid == 0) {
+      if (tid == 0) {
         walk.learn(total, sm);
-        walk.go(sm, drawn, s0);
+        walk.go(sm, drawn);
       }
       continue;
     }
     if (total == 0) {  // nothing is left: p itself; nothing there either: no token
       if (c == 0 && gone == 0) break;
-      if (rank == 0 && tid == 0) {
+      if (tid == 0) {
         sm.order.c = 0;
         sm.order.gone = 0;
       }
@@ -603,7 +615,7 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) tree_sample_kernel(con
     none = 0;
     // the first element at which the running sum passes u * total
     const u64 goal = __umul64hi(total, __float2ull_rz(fminf(fmaxf(u, 0.f), 0.99999994f) * 18446744073709551616.f));
-    if (goal < before || goal - before >= sm.sums[rank]) break;
+    if (goal < before || goal - before >= sm.sums[pass][rank]) break;
     // in this CTA's slice: which warp's part of it, and all warps look through that
     u64 run = before;
     int part = 0;
