@@ -22,17 +22,24 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 
 // A row of `n` elements seen in quads: quad k holds elements 4k - shift .. +3,
 // so that whole quads are aligned wherever the row begins. [lo, hi) are the
-// quads of part `i` of 2^log2; whole quads: [first, first + whole).
+// quads of part `i` of 2^log2. Loads of whole quads carry no condition that a
+// branch would come of, so that many are on their way at once.
 struct Quads {
-  int shift, lo, hi, first, whole;
+  int shift, lo, hi;
+  int whole_lo, whole_hi;  // those of [lo, hi) that are whole; the others are the row's first and last one
   __device__ __forceinline__ Quads(int n, int shift, uint32_t i, int log2) : shift(shift) {
     const uint32_t all = ((uint32_t)(shift + n) + 3) / 4, each = (all + (1u << log2) - 1) >> log2;
     lo = (int)min(i * each, all);
     hi = (int)min(i * each + each, all);
-    first = shift ? 1 : 0;
-    whole = (shift + n) / 4 - first;
+    whole_lo = max(lo, shift ? 1 : 0);
+    whole_hi = max(min(hi, (shift + n) / 4), whole_lo);
   }
-  __device__ __forceinline__ bool is_whole(int k) const { return (uint32_t)(k - first) < (uint32_t)max(whole, 0); }
+  // quad u of the ones at the part's ends, or -1
+  __device__ __forceinline__ int end(int u) const {
+    if (u == 0) return lo < min(whole_lo, hi) ? lo : -1;
+    return whole_hi < hi && hi - 1 >= whole_lo ? hi - 1 : -1;
+  }
+  __device__ __forceinline__ bool is_whole(int k) const { return k >= whole_lo && k < whole_hi; }
 };
 
 // ---------------------------------------------------------------------------
@@ -53,11 +60,9 @@ struct ProbParams {
   int vocab;
 };
 
-// Four logits of the row, two to a word; -inf past its ends.
-template <bool ALIGNED>
-__device__ __forceinline__ uint2 load_quad(const uint16_t *row, const Quads &q, int k, int n) {
+// Four logits of the row, two to a word, one by one; -inf past its ends.
+__device__ __forceinline__ uint2 load_end(const uint16_t *row, const Quads &q, int k, int n) {
   const int j = 4 * k - q.shift;
-  if (ALIGNED && q.is_whole(k)) return *reinterpret_cast<const uint2 *>(row + j);
   uint32_t x[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) x[i] = j + i >= 0 && j + i < n ? row[j + i] : kNone & 0xFFFFu;
@@ -72,17 +77,23 @@ __device__ __forceinline__ void drop(uint2 &w, float floor) {
     if (bf16hi_to_f32(v[i]) < floor) v[i] = (v[i] & 0xFFFFu) | (kNone & 0xFFFF0000u);
   }
 }
+__device__ __forceinline__ void store_end(float *row, const Quads &q, int k, int n, float2 a, float2 b) {
+  const int j = 4 * k - q.shift;
+  const float v[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (j + i >= 0 && j + i < n) row[j + i] = v[i];
+}
+// ALIGNED: whole quads are. Otherwise every quad is moved one by one.
+template <bool ALIGNED>
+__device__ __forceinline__ uint2 load_quad(const uint16_t *row, const Quads &q, int k, int n) {
+  if (ALIGNED && q.is_whole(k)) return *reinterpret_cast<const uint2 *>(row + 4 * k - q.shift);
+  return load_end(row, q, k, n);
+}
 template <bool ALIGNED>
 __device__ __forceinline__ void store_quad(float *row, const Quads &q, int k, int n, float2 a, float2 b) {
-  const int j = 4 * k - q.shift;
-  if (ALIGNED && q.is_whole(k)) {
-    *reinterpret_cast<float4 *>(row + j) = make_float4(a.x, a.y, b.x, b.y);
-  } else {
-    const float v[4] = {a.x, a.y, b.x, b.y};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (j + i >= 0 && j + i < n) row[j + i] = v[i];
-  }
+  if (ALIGNED && q.is_whole(k)) *reinterpret_cast<float4 *>(row + 4 * k - q.shift) = make_float4(a.x, a.y, b.x, b.y);
+  else store_end(row, q, k, n, a, b);
 }
 
 __device__ __forceinline__ float exp2_fast(float y) {
@@ -133,7 +144,7 @@ __global__ void __launch_bounds__(kProbThreads, 4) probabilities_kernel(const Pr
   float *out = p.out + r * p.vocab;
   const Quads q(p.vocab, ALIGNED ? (int)(r * p.vocab & 3) : 0, rank, __ffs(S) - 1);
   const float t = p.temperature ? p.temperature[r] : 1.f, floor = p.floor ? p.floor[r] : -INFINITY;
-  const bool greedy = !(t > 0.f);
+  const bool greedy = !(t > 0.f), ends = q.whole_lo > q.lo || q.whole_hi < q.hi;
 
   // a logit of -inf stays -inf through difference and product, whatever the temperature
   const float lowest = -3.40282347e38f, a = greedy ? 1.f : fmaxf(fminf(__fdiv_rn(1.44269502f, t), 1e30f), 1e-44f);
@@ -145,7 +156,16 @@ __global__ void __launch_bounds__(kProbThreads, 4) probabilities_kernel(const Pr
 #pragma unroll
     for (int u = 0; u < kProbQuads; ++u) {
       const int k = k0 + u * kProbThreads + tid;
-      x[u] = k < q.hi ? load_quad<ALIGNED>(row, q, k, p.vocab) : make_uint2(kNone, kNone);
+      x[u] = make_uint2(kNone, kNone);
+      if (ALIGNED ? q.is_whole(k) : k < q.hi)
+        x[u] = ALIGNED ? *reinterpret_cast<const uint2 *>(row + 4 * k - q.shift) : load_end(row, q, k, p.vocab);
+    }
+    if (ALIGNED && ends) {
+#pragma unroll
+      for (int u = 0; u < kProbQuads; ++u) {
+        const int k = k0 + u * kProbThreads + tid;
+        if (k < q.hi && !q.is_whole(k)) x[u] = load_end(row, q, k, p.vocab);
+      }
     }
     if (floor > -INFINITY) {
 #pragma unroll
@@ -228,8 +248,12 @@ __global__ void __launch_bounds__(kProbThreads, 4) probabilities_kernel(const Pr
     for (int u = 0; u < kProbQuads; ++u) {
       const int k = q.lo + u * kProbThreads + tid;
       const float2 v = powers(x[u].x, minus, a2), w = powers(x[u].y, minus, a2);
-      if (k < q.hi)
-        store_quad<ALIGNED>(out, q, k, p.vocab, f32_halves(mul2(f32_pair(v.x, v.y), f2)), f32_halves(mul2(f32_pair(w.x, w.y), f2)));
+      const float2 a0 = f32_halves(mul2(f32_pair(v.x, v.y), f2)), b0 = f32_halves(mul2(f32_pair(w.x, w.y), f2));
+      if (ALIGNED ? q.is_whole(k) : k < q.hi) {
+        if (ALIGNED) *reinterpret_cast<float4 *>(out + 4 * k - q.shift) = make_float4(a0.x, a0.y, b0.x, b0.y);
+        else store_end(out, q, k, p.vocab, a0, b0);
+      }
+      if (ALIGNED && ends && k < q.hi && !q.is_whole(k)) store_end(out, q, k, p.vocab, a0, b0);
     }
     return;
   }
@@ -344,19 +368,11 @@ __device__ __forceinline__ u64 weight(float p, float q, u64 c) {
   return a > t ? a - t : 0;
 }
 
-template <bool ALIGNED>
-__device__ __forceinline__ void load_floats(const float *row, const Quads &q, int k, int n, float (&x)[4]) {
+// Four values of a row, one by one; 0 past its ends.
+__device__ __forceinline__ void load_ends(const float *row, const Quads &q, int k, int n, float (&x)[4]) {
   const int j = 4 * k - q.shift;
-  if (ALIGNED && q.is_whole(k)) {
-    const float4 v = *reinterpret_cast<const float4 *>(row + j);
-    x[0] = v.x;
-    x[1] = v.y;
-    x[2] = v.z;
-    x[3] = v.w;
-  } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = j + i >= 0 && j + i < n ? row[j + i] : 0.f;
-  }
+  for (int i = 0; i < 4; ++i) x[i] = j + i >= 0 && j + i < n ? row[j + i] : 0.f;
 }
 
 // The walk, as far as it gets without another sum over the vocabulary. One thread
@@ -529,51 +545,78 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) tree_sample_kernel(con
     const float *pr = p.p + row * p.p_row, *qr = p.q + row * p.q_row;
     const int shift = ALIGNED ? (int)((row * p.p_row) & 3) : 0;
     Quads mine(p.vocab, shift, rank * WARPS + warp, parts_log2);
-    if (SINGLE && row < 0) mine.hi = mine.lo;  // (no token: nothing to sum, and every barrier as ever)
-    if (ALIGNED && lane < 2 && (lane == 0 || c)) {  // all of the warp's part at once to L2; the loads below take it in turns
-      const int lo = max(mine.lo, mine.first), n = min(mine.hi, mine.first + mine.whole) - lo;
-      if (n > 0)
-        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"((lane ? qr : pr) + 4 * lo - shift), "r"(16 * n) : "memory");
-    }
+    if (SINGLE && row < 0) mine.hi = mine.whole_lo = mine.whole_hi = mine.lo;  // (no token: nothing to sum, and every barrier as ever)
     u64 sum = 0;
-    if (c == 0 || c == kOne) {  // p, or max(p, q) - q
-      const bool both = c != 0;
-      for (int k0 = mine.lo + lane; k0 < mine.hi; k0 += 32 * kBitsQuads) {  // (so long the bits' sums hold)
-        uint32_t hi = 0, lo = 0;
-        const int k1 = min(k0 + 32 * kBitsQuads, mine.hi);
-        if (both) {
-#pragma unroll 4
-          for (int k = k0; k < k1; k += 32) {
-            float x[4], y[4];
-            load_floats<ALIGNED>(pr, mine, k, p.vocab, x);
-            load_floats<ALIGNED>(qr, mine, k, p.vocab, y);
+    // the row's first and last quad, where they are not whole (not ALIGNED: all of them)
+    auto alone = [&](int k) {
+      float x[4], y[4] = {0.f, 0.f, 0.f, 0.f};
+      load_ends(pr, mine, k, p.vocab, x);
+      if (c) load_ends(qr, mine, k, p.vocab, y);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const Bits d = bits_of(fminf(fmaxf(fmaxf(x[i], y[i]), 0.f), 1.f), sound(y[i]));
-              hi += d.hi_a - d.hi_b;
-              lo += d.lo_a - d.lo_b;
-            }
-          }
-        } else {
-#pragma unroll 4
-          for (int k = k0; k < k1; k += 32) {
-            float x[4];
-            load_floats<ALIGNED>(pr, mine, k, p.vocab, x);
-            const Bits d = bits_of(sound(x[0]), sound(x[1])), e = bits_of(sound(x[2]), sound(x[3]));
+      for (int i = 0; i < 4; ++i) sum += c ? weight(x[i], y[i], c) : fixed(x[i]);
+    };
+    if (!ALIGNED) {
+      for (int k = mine.lo + lane; k < mine.hi; k += 32) alone(k);
+    } else {
+      if (lane < 2 && mine.end(lane) >= 0) alone(mine.end(lane));
+      const float4 *p4 = reinterpret_cast<const float4 *>(pr - shift), *q4 = reinterpret_cast<const float4 *>(qr - shift);
+      if (c == 0 || c == kOne) {  // p, or max(p, q) - q
+        for (int k0 = mine.whole_lo + lane; k0 < mine.whole_hi; k0 += 32 * kBitsQuads) {  // (so long the bits' sums hold)
+          uint32_t hi = 0, lo = 0;
+          const int k1 = min(k0 + 32 * kBitsQuads, mine.whole_hi);
+          auto add = [&](const float4 &x) {
+            const Bits d = bits_of(sound(x.x), sound(x.y)), e = bits_of(sound(x.z), sound(x.w));
             hi += d.hi_a + d.hi_b + (e.hi_a + e.hi_b) - 4 * kUpper;
             lo += d.lo_a + d.lo_b + (e.lo_a + e.lo_b) - 4 * kLower;
-          }
-        }
-        sum += join_bits(hi, lo);
-      }
-    } else {
-#pragma unroll 4
-      for (int k = mine.lo + lane; k < mine.hi; k += 32) {
-        float x[4], y[4];
-        load_floats<ALIGNED>(pr, mine, k, p.vocab, x);
-        load_floats<ALIGNED>(qr, mine, k, p.vocab, y);
+          };
+          auto add_left = [&](float x, float y) {
+            const Bits d = bits_of(fminf(fmaxf(fmaxf(x, y), 0.f), 1.f), sound(y));
+            hi += d.hi_a - d.hi_b;
+            lo += d.lo_a - d.lo_b;
+          };
+          constexpr int U = 4;  // quads on their way
+          int k = k0;
+          if (c == 0) {
+            for (; k + 32 * (2 * U - 1) < k1; k += 32 * 2 * U) {
+              float4 x[2 * U];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum += weight(x[i], y[i], c);
+              for (int i = 0; i < 2 * U; ++i) x[i] = p4[k + 32 * i];
+#pragma unroll
+              for (int i = 0; i < 2 * U; ++i) add(x[i]);
+            }
+            for (; k < k1; k += 32) add(p4[k]);
+          } else {
+            for (; k + 32 * (U - 1) < k1; k += 32 * U) {
+              float4 x[U], y[U];
+#pragma unroll
+              for (int i = 0; i < U; ++i) {
+                x[i] = p4[k + 32 * i];
+                y[i] = q4[k + 32 * i];
+              }
+#pragma unroll
+              for (int i = 0; i < U; ++i) {
+                add_left(x[i].x, y[i].x);
+                add_left(x[i].y, y[i].y);
+                add_left(x[i].z, y[i].z);
+                add_left(x[i].w, y[i].w);
+              }
+            }
+            for (; k < k1; k += 32) {
+              const float4 x = p4[k], y = q4[k];
+              add_left(x.x, y.x);
+              add_left(x.y, y.y);
+              add_left(x.z, y.z);
+              add_left(x.w, y.w);
+            }
+          }
+          sum += join_bits(hi, lo);
+        }
+      } else {
+#pragma unroll 2
+        for (int k = mine.whole_lo + lane; k < mine.whole_hi; k += 32) {
+          const float4 x = p4[k], y = q4[k];
+          sum += weight(x.x, y.x, c) + weight(x.y, y.y, c) + weight(x.z, y.z, c) + weight(x.w, y.w, c);
+        }
       }
     }
     for (int g = lane; g < gone; g += 32) {
@@ -625,8 +668,8 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) tree_sample_kernel(con
     const int lo = theirs.lo + warp * each, hi = min(lo + each, theirs.hi);
     auto weights = [&](int k, u64 (&v)[4]) {
       float x[4], y[4] = {0.f, 0.f, 0.f, 0.f};
-      load_floats<ALIGNED>(pr, theirs, k, p.vocab, x);
-      if (c) load_floats<ALIGNED>(qr, theirs, k, p.vocab, y);
+      load_ends(pr, theirs, k, p.vocab, x);
+      if (c) load_ends(qr, theirs, k, p.vocab, y);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[i] = c ? weight(x[i], y[i], c) : fixed(x[i]);
