@@ -361,11 +361,53 @@ __device__ __forceinline__ u64 fixed(float p) {
   return join_bits(x.hi_a - kUpper, x.lo_a - kLower);
 }
 
-// max(p - c q, 0)
-__device__ __forceinline__ u64 weight(float p, float q, u64 c) {
-  const u64 a = fixed(p), b = fixed(q);
-  const u64 t = c == kOne ? b : 2 * __umul64hi(b << (63 - kFrac), c);
-  return a > t ? a - t : 0;
+// max(p - c q, 0) of two elements, in units of 2^-46 (off by 0.2 of them in the mean, by 1.2 at most), added to sums of
+// bit patterns. c is the sum of two floats (48 bits). p and c q are split at multiples of 2^-23; what is below them is put
+// together with what the product rounds off, and its carry taken to the upper part. (As 64-bit products of whole numbers:
+// 32 trees of 8, 248,320 probabilities each, 39.7 us against 34.2.)
+struct Factor {
+  f32x2 high, minus_high, minus_low;
+  __device__ __forceinline__ explicit Factor(u64 c) {
+    const float h = __ull2float_rn(c), l = __ll2float_rn((long long)(c - __float2ull_rz(h)));
+    const float unit = 1.f / (float)kOne;
+    high = f32_pair(h * unit, h * unit);
+    minus_high = f32_pair(-h * unit, -h * unit);
+    minus_low = f32_pair(-l * unit, -l * unit);
+  }
+};
+__device__ __forceinline__ void add_cut(float p0, float p1, float q0, float q1, const Factor &c, uint32_t &hi, uint32_t &lo) {
+  const f32x2 one = f32_pair(1.f, 1.f), minus = f32_pair(-1.f, -1.f);
+  const f32x2 near = f32_pair(1.5f, 1.5f), minus_near = f32_pair(-1.5f, -1.5f);
+  const f32x2 small = f32_pair(__uint_as_float(kLower), __uint_as_float(kLower));
+  const f32x2 p = f32_pair(sound(p0), sound(p1)), q = f32_pair(sound(q0), sound(q1));
+  const f32x2 m = mul2(q, c.minus_high), e = fma2(q, c.high, m);  // -(c q), and what it lacks
+  const f32x2 p_hi = add2(add2(p, one), minus), m_hi = add2(add2(m, minus), one);
+  f32x2 h = add2(p_hi, m_hi), l = add2(fma2(p_hi, minus, p), fma2(m_hi, minus, m));
+  l = fma2(q, c.minus_low, fma2(e, minus, l));
+  const f32x2 carry = add2(add2(l, near), minus_near);
+  h = add2(h, carry);
+  l = fma2(carry, minus, l);
+  const float2 hf = f32_halves(h), lf = f32_halves(l), hw = f32_halves(add2(h, one)), lw = f32_halves(add2(l, small));
+  if (hf.x > -lf.x) {
+    hi += __float_as_uint(hw.x) - kUpper;
+    lo += __float_as_uint(lw.x) - kLower;
+  }
+  if (hf.y > -lf.y) {
+    hi += __float_as_uint(hw.y) - kUpper;
+    lo += __float_as_uint(lw.y) - kLower;
+  }
+}
+
+// max(p - c q, 0), as every sum has it; `factor` is c's
+__device__ __forceinline__ u64 weight(float p, float q, u64 c, const Factor &factor) {
+  if (c == 0) return fixed(p);
+  if (c == kOne) {
+    const u64 a = fixed(p), b = fixed(q);
+    return a > b ? a - b : 0;
+  }
+  uint32_t hi = 0, lo = 0;
+  add_cut(p, 0.f, q, 0.f, factor, hi, lo);
+  return join_bits(hi, lo);
 }
 
 // Four values of a row, one by one; 0 past its ends.
@@ -546,6 +588,7 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) tree_sample_kernel(con
     const int shift = ALIGNED ? (int)((row * p.p_row) & 3) : 0;
     Quads mine(p.vocab, shift, rank * WARPS + warp, parts_log2);
     if (SINGLE && row < 0) mine.hi = mine.whole_lo = mine.whole_hi = mine.lo;  // (no token: nothing to sum, and every barrier as ever)
+    const Factor factor(c);
     u64 sum = 0;
     // the row's first and last quad, where they are not whole (not ALIGNED: all of them)
     auto alone = [&](int k) {
@@ -553,70 +596,63 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) tree_sample_kernel(con
       load_ends(pr, mine, k, p.vocab, x);
       if (c) load_ends(qr, mine, k, p.vocab, y);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum += c ? weight(x[i], y[i], c) : fixed(x[i]);
+      for (int i = 0; i < 4; ++i) sum += weight(x[i], y[i], c, factor);
     };
     if (!ALIGNED) {
       for (int k = mine.lo + lane; k < mine.hi; k += 32) alone(k);
     } else {
       if (lane < 2 && mine.end(lane) >= 0) alone(mine.end(lane));
       const float4 *p4 = reinterpret_cast<const float4 *>(pr - shift), *q4 = reinterpret_cast<const float4 *>(qr - shift);
-      if (c == 0 || c == kOne) {  // p, or max(p, q) - q
-        for (int k0 = mine.whole_lo + lane; k0 < mine.whole_hi; k0 += 32 * kBitsQuads) {  // (so long the bits' sums hold)
-          uint32_t hi = 0, lo = 0;
-          const int k1 = min(k0 + 32 * kBitsQuads, mine.whole_hi);
+      for (int k0 = mine.whole_lo + lane; k0 < mine.whole_hi; k0 += 32 * kBitsQuads) {  // (so long the bits' sums hold)
+        uint32_t hi = 0, lo = 0;
+        const int k1 = min(k0 + 32 * kBitsQuads, mine.whole_hi);
+        constexpr int U = 4;  // quads of two rows on their way
+        int k = k0;
+        auto two_rows = [&](auto add) {
+          for (; k + 32 * (U - 1) < k1; k += 32 * U) {
+            float4 x[U], y[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+              x[i] = p4[k + 32 * i];
+              y[i] = q4[k + 32 * i];
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+              add(x[i].x, x[i].y, y[i].x, y[i].y);
+              add(x[i].z, x[i].w, y[i].z, y[i].w);
+            }
+          }
+          for (; k < k1; k += 32) {
+            const float4 x = p4[k], y = q4[k];
+            add(x.x, x.y, y.x, y.y);
+            add(x.z, x.w, y.z, y.w);
+          }
+        };
+        if (c == 0) {
           auto add = [&](const float4 &x) {
             const Bits d = bits_of(sound(x.x), sound(x.y)), e = bits_of(sound(x.z), sound(x.w));
             hi += d.hi_a + d.hi_b + (e.hi_a + e.hi_b) - 4 * kUpper;
             lo += d.lo_a + d.lo_b + (e.lo_a + e.lo_b) - 4 * kLower;
           };
-          auto add_left = [&](float x, float y) {
-            const Bits d = bits_of(fminf(fmaxf(fmaxf(x, y), 0.f), 1.f), sound(y));
-            hi += d.hi_a - d.hi_b;
-            lo += d.lo_a - d.lo_b;
-          };
-          constexpr int U = 4;  // quads on their way
-          int k = k0;
-          if (c == 0) {
-            for (; k + 32 * (2 * U - 1) < k1; k += 32 * 2 * U) {
-              float4 x[2 * U];
+          for (; k + 32 * (2 * U - 1) < k1; k += 32 * 2 * U) {
+            float4 x[2 * U];
 #pragma unroll
-              for (int i = 0; i < 2 * U; ++i) x[i] = p4[k + 32 * i];
+            for (int i = 0; i < 2 * U; ++i) x[i] = p4[k + 32 * i];
 #pragma unroll
-              for (int i = 0; i < 2 * U; ++i) add(x[i]);
-            }
-            for (; k < k1; k += 32) add(p4[k]);
-          } else {
-            for (; k + 32 * (U - 1) < k1; k += 32 * U) {
-              float4 x[U], y[U];
-#pragma unroll
-              for (int i = 0; i < U; ++i) {
-                x[i] = p4[k + 32 * i];
-                y[i] = q4[k + 32 * i];
-              }
-#pragma unroll
-              for (int i = 0; i < U; ++i) {
-                add_left(x[i].x, y[i].x);
-                add_left(x[i].y, y[i].y);
-                add_left(x[i].z, y[i].z);
-                add_left(x[i].w, y[i].w);
-              }
-            }
-            for (; k < k1; k += 32) {
-              const float4 x = p4[k], y = q4[k];
-              add_left(x.x, y.x);
-              add_left(x.y, y.y);
-              add_left(x.z, y.z);
-              add_left(x.w, y.w);
-            }
+            for (int i = 0; i < 2 * U; ++i) add(x[i]);
           }
-          sum += join_bits(hi, lo);
+          for (; k < k1; k += 32) add(p4[k]);
+        } else if (c == kOne) {  // max(p, q) - q
+          two_rows([&](float x0, float x1, float y0, float y1) {
+            const Bits d = bits_of(fminf(fmaxf(fmaxf(x0, y0), 0.f), 1.f), sound(y0));
+            const Bits e = bits_of(fminf(fmaxf(fmaxf(x1, y1), 0.f), 1.f), sound(y1));
+            hi += d.hi_a - d.hi_b + (e.hi_a - e.hi_b);
+            lo += d.lo_a - d.lo_b + (e.lo_a - e.lo_b);
+          });
+        } else {
+          two_rows([&](float x0, float x1, float y0, float y1) { add_cut(x0, x1, y0, y1, factor, hi, lo); });
         }
-      } else {
-#pragma unroll 2
-        for (int k = mine.whole_lo + lane; k < mine.whole_hi; k += 32) {
-          const float4 x = p4[k], y = q4[k];
-          sum += weight(x.x, y.x, c) + weight(x.y, y.y, c) + weight(x.z, y.z, c) + weight(x.w, y.w, c);
-        }
+        sum += join_bits(hi, lo);
       }
     }
     for (int g = lane; g < gone; g += 32) {
@@ -672,7 +708,7 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) tree_sample_kernel(con
       if (c) load_ends(qr, theirs, k, p.vocab, y);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[i] = c ? weight(x[i], y[i], c) : fixed(x[i]);
+        v[i] = weight(x[i], y[i], c, factor);
         for (int g = 0; g < gone; ++g)
           if (sm.order.ids[g] == 4 * k - shift + i) v[i] = 0;
       }
