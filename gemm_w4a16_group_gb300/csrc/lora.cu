@@ -984,9 +984,18 @@ __global__ void __launch_bounds__(512, 1) lora_prompt_expand_kernel(const __grid
 // ---------------------------------------------------------------------------
 int padded_rank(int rank, bool few) { return rank <= 8 && few ? 8 : rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
 
-// Few tokens take the first pair of kernels, 16 tokens a tile: a tile of 64
-// would mostly be empty.
-bool few(int tokens) { return tokens <= 512; }
+// Few tokens take the first pair of kernels, 16 tokens a tile, whose time goes by
+// tiles and columns; the prompts' tiles of 128 are late to begin and mostly empty
+// where many adapters share few tokens. Measured with rank 16, K 5,120, first
+// against second pair: 512 tokens of one adapter, 34,816 columns 29.8 | 30.6 us,
+// 768 51.5 | 38.5; 1,024 tokens, 7,168 columns 15.4 | 22.5; 1,024 rows of one
+// token and 48 adapters, 34,816 columns 100 | 144 (1,536: 106 | 149, 7,168 columns
+// and 2,048 tokens 46 | 58: there the second pair is kept for its smaller workspace).
+constexpr int kAlwaysFew = 512, kMostFew = 1024;
+bool few(int tokens, int outer, int groups) {
+  return tokens <= kAlwaysFew || (tokens <= kMostFew && (outer <= 8192 || tokens < 32LL * groups));
+}
+int groups_of(int adapters, int rows) { return adapters < rows ? adapters : rows; }
 
 // Few tokens: parts of K. As many CTAs as fit at once, but at least two steps of
 // 32 k for each warp (one token: 5.4 us, with one step 6.1, with four 6.1), and
@@ -1033,8 +1042,7 @@ cudaError_t launch(K kern, unsigned grid, int cluster, int smem, cudaStream_t st
 
 template <int RP>
 cudaError_t run_few(const LoraCall &c, const LoraParams &p, bool even) {
-  const int groups = c.adapters < c.rows ? c.adapters : c.rows;
-  const long long tiles = c.tokens / 16 + groups + 1;  // at most
+  const long long tiles = c.tokens / 16 + groups_of(c.adapters, c.rows) + 1;  // at most
   const long long shrink = tiles * p.ksplit, expand = tiles * ((c.outer + kColumns - 1) / kColumns);
   const long long cap = c.sm_count * 2;
   const cudaError_t e = launch(lora_shrink_kernel<RP>, (unsigned)(shrink < cap ? shrink : cap), 1,
@@ -1047,7 +1055,7 @@ cudaError_t run_few(const LoraCall &c, const LoraParams &p, bool even) {
 template <int RP>
 cudaError_t run_prompts(const LoraCall &c, const LoraParams &p, bool even) {
   const int cluster = cluster_of(c.tokens, c.inner, c.sm_count);
-  const long long clusters = most_clusters(c.tokens, c.adapters < c.rows ? c.adapters : c.rows);
+  const long long clusters = most_clusters(c.tokens, groups_of(c.adapters, c.rows));
   const cudaError_t e = launch(lora_prompt_shrink_kernel<RP>, (unsigned)(clusters * cluster), cluster,
                                PromptShrinkGeo<RP>::smem(c.adapters), c.stream, p);
   if (e != cudaSuccess) return e;
@@ -1056,18 +1064,23 @@ cudaError_t run_prompts(const LoraCall &c, const LoraParams &p, bool even) {
 }
 
 template <int RP>
-cudaError_t run(const LoraCall &c, const LoraParams &p, bool even) {
-  if (few(c.tokens)) return run_few<RP>(c, p, even);
+cudaError_t run(const LoraCall &c, const LoraParams &p, bool few, bool even) {
+  if (few) return run_few<RP>(c, p, even);
   return run_prompts<(RP < 16 ? 16 : RP)>(c, p, even);
 }
 
 }  // namespace
 
 size_t lora_workspace_bytes(int tokens, int rank, int inner) {
-  const size_t row = padded_rank(rank, few(tokens)) * sizeof(float);  // (two bf16 or one float32 a rank)
-  if (few(tokens)) return align_up((size_t)parts_of(tokens, rank, inner) * tokens * row, 256);
-  const int groups = tokens < kMaxAdapters ? tokens : kMaxAdapters;
-  return 256 + align_up(tokens * row, 256) + align_up((size_t)most_clusters(tokens, groups) * 2 * kListInts * sizeof(int), 256);
+  size_t bytes = 0;  // of the pair that needs more, of those that a call may take
+  if (tokens <= kMostFew)
+    bytes = align_up((size_t)parts_of(tokens, rank, inner) * tokens * padded_rank(rank, true) * sizeof(float), 256);
+  if (tokens > kAlwaysFew) {
+    const size_t lists = (size_t)most_clusters(tokens, groups_of(kMaxAdapters, tokens)) * 2 * kListInts * sizeof(int);
+    const size_t prompts = 256 + align_up((size_t)tokens * padded_rank(rank, false) * 4, 256) + align_up(lists, 256);
+    if (prompts > bytes) bytes = prompts;
+  }
+  return bytes;
 }
 
 cudaError_t launch_lora_add(const LoraCall &c) {
@@ -1077,7 +1090,8 @@ cudaError_t launch_lora_add(const LoraCall &c) {
                (reinterpret_cast<uintptr_t>(c.out) - reinterpret_cast<uintptr_t>(c.y)) % 16 == 0 && (c.out_row - c.y_row) % 8 == 0 &&
                    (c.y_row >= c.outer || c.tokens == 1)};
   uint8_t *ws = static_cast<uint8_t *>(c.workspace);
-  if (few(c.tokens)) {
+  const bool is_few = few(c.tokens, c.outer, groups_of(c.adapters, c.rows));
+  if (is_few) {
     p.ksplit = parts_of(c.tokens, c.rank, c.inner);
     p.parts = reinterpret_cast<float *>(ws);
   } else {
@@ -1087,12 +1101,12 @@ cudaError_t launch_lora_add(const LoraCall &c) {
   }
   const uintptr_t bits = reinterpret_cast<uintptr_t>(c.y) | reinterpret_cast<uintptr_t>(c.out);
   const bool even = bits % 16 == 0 && c.y_row % 8 == 0 && c.out_row % 8 == 0;
-  switch (padded_rank(c.rank, few(c.tokens))) {
-    case 8: return run<8>(c, p, even);
-    case 16: return run<16>(c, p, even);
-    case 32: return run<32>(c, p, even);
-    case 64: return run<64>(c, p, even);
-    default: return run<128>(c, p, even);
+  switch (padded_rank(c.rank, is_few)) {
+    case 8: return run<8>(c, p, is_few, even);
+    case 16: return run<16>(c, p, is_few, even);
+    case 32: return run<32>(c, p, is_few, even);
+    case 64: return run<64>(c, p, is_few, even);
+    default: return run<128>(c, p, is_few, even);
   }
 }
 

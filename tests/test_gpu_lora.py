@@ -52,6 +52,9 @@ def test_few_tokens(rank, sizes, which, inner, outer):
 @pytest.mark.parametrize("rank", [8, 16, 32, 64, 128])
 @pytest.mark.parametrize("sizes,which,inner,outer", [
     ([600], [0], 328, 515), ([300, 7, 513, 1], [1, -1, 0, 1], 1024, 264), ([65, 64, 63, 400], [0, 1, 0, 1], 96, 776),
+    ([1200], [0], 328, 515), ([300, 7, 913, 1], [1, -1, 0, 1], 1024, 264), ([65, 64, 63, 1000], [0, 1, 0, 1], 96, 776),
+    ([600, 80], [1, 0], 64, 8200), ([512], [1], 72, 40), ([513], [1], 72, 40), ([1023, 1], [1, 0], 72, 40), ([1024, 1], [1, 0], 72, 40),
+    ([9, 1050], [0, 1], 8, 1), ([1100], [0], 16, 130), ([3] * 350, [i % 2 for i in range(350)], 264, 140),
 ])
 def test_prompts(rank, sizes, which, inner, outer):
     p = Problem(sizes, which, rank, inner, outer, 2, seed=rank + 1)
@@ -85,7 +88,7 @@ def test_a_token_does_not_depend_on_the_others():
 
 
 def test_in_place_and_padding():
-    for sizes, which in (([3, 2, 4], [1, -1, 0]), ([200, 100, 300], [0, -1, 1])):
+    for sizes, which in (([3, 2, 4], [1, -1, 0]), ([200, 100, 300], [0, -1, 1]), ([400, 300, 600], [0, -1, 1])):
         p = Problem(sizes, which, 24, 320, 402, 2, pad=5)
         p.x[p.live:] = math.nan
         keep = p.y.clone()
@@ -139,6 +142,8 @@ def test_large_store_and_many_rows():
         p.check(p.run())
         p = Problem([500, 0, 180], [4095, 3, 4000], rank, 16, 24, 4096)
         p.check(p.run())
+        p = Problem([1500, 0, 180], [4095, 3, 4000], rank, 16, 24, 4096)
+        p.check(p.run())
 
 
 def test_bad_indices_are_left_out_and_reported():
@@ -177,7 +182,7 @@ def test_values_that_are_not_finite_stay_with_their_tokens():
 
 
 def test_streams_graphs_and_repeats():
-    for sizes, which in (([3, 1, 4], [0, 1, 0]), ([300, 300], [0, 1])):
+    for sizes, which in (([3, 1, 4], [0, 1, 0]), ([300, 300], [0, 1]), ([700, 400], [0, 1])):
         p = Problem(sizes, which, 32, 512, 1000, 2)
         want = p.run()
         side = torch.cuda.Stream()
