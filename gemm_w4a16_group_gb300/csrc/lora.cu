@@ -2,18 +2,29 @@
 //
 //   out[t] = y[t] + scale_e (x[t] A_e^T) B_e^T,   e the adapter of token t's row
 //
-// Two launches. `shrink` makes t = x A^T, the sum over K split over CTAs, whose
-// float32 parts go to the workspace; `expand` adds them up, applies the scale,
-// and adds t B^T to y. Tokens are taken together by adapter, up to 16 or 64 in a
-// tile, whichever rows they belong to, so that an adapter is read once for all
-// of its tokens (64: once for every 64). Which tokens those are every CTA works
-// out for itself from the rows' adapters: a count for each adapter, whose running
-// sums number the tiles.
+// Two launches. `shrink` makes t = x A^T, the sum over K split over CTAs;
+// `expand` applies the scale and adds t B^T to y. Tokens are taken together by
+// adapter, whichever rows they belong to, so that an adapter is read once for all
+// tokens of a tile. Which tokens those are every CTA works out for itself from
+// the rows' adapters: a count for each adapter, whose running sums number the
+// tiles.
 //
-// Products are mma.sync (m16n8k16): 16 ranks against every element are 8 to 32
-// FLOP a byte, a twentieth of the machine's balance, and the work is to move x,
-// y and the adapters. The k order of a fragment is free as long as both operands
-// agree, so a lane's 16 bytes of consecutive k serve two products as they come.
+// 16 ranks against every element are 8 to 32 FLOP a byte, a twentieth of the
+// machine's balance: the work is to move x, y and the adapters, and where tokens
+// are few, to begin early (expand has its part of B and y on their way before
+// shrink is done).
+//
+// - Few tokens: tiles of 16, products on mma.sync (m16n8k16), whose fragments
+//   come straight from memory or a warp's own copies; the parts of the sums over K
+//   go to the workspace as float32 and expand adds them up. The k order of a
+//   fragment is free as long as both operands agree, so a lane's 16 bytes of
+//   consecutive k serve two products as they come. One token of rank 16, 5,120
+//   by 5,120: 5.2 us; 48 tokens of 12 adapters of rank 64, 5,120 by 34,816: 21.7
+//   us, 3.2 TB/s.
+// - Prompts: tiles of 128, products on tcgen05, sums in TMEM; a cluster adds up
+//   the parts over K in distributed shared memory. 4,096 tokens of rank 16, 5,120
+//   by 34,816: 121 us, 5.1 TB/s; six prompts of 2,000 and rank 64, 5,120 by 7,168:
+//   75 us, 4.0 TB/s.
 #include "w4a16_internal.h"
 
 namespace w4a16 {
@@ -252,7 +263,9 @@ __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(const __grid_c
 // such that a lane ends up with eight consecutive columns of a token: y is read
 // and written 16 bytes at a time. B is what there is to read: every warp copies
 // its own columns to shared memory some units ahead, and begins before there is
-// a t.
+// a t. Small slots hide more of the latency as many of them than as more CTAs,
+// large ones the other way: rank 64 with three CTAs of two slots an SM 21.1 us, one
+// of four 24.4 (B straight to registers: 23.8; B brought to L2 by shrink: 26.7).
 // ---------------------------------------------------------------------------
 template <int RP>
 struct ExpandGeo {
@@ -302,8 +315,7 @@ __device__ __forceinline__ uint2 two_parts(float a, float b) {
   return make_uint2(hi, pack_bf16(fabsf(x) < INFINITY ? a - x : 0.f, fabsf(y) < INFINITY ? b - y : 0.f));
 }
 
-
-// eight columns of a row from column c on, `wide`: as one 16-byte access
+// Eight columns of a row from column c on, `wide`: as one 16-byte access
 __device__ __forceinline__ uint4 load8(const uint16_t *row, int c, int n, bool wide) {
   if (wide) return __ldcg(reinterpret_cast<const uint4 *>(row + c));
   uint32_t v[4] = {};
@@ -490,10 +502,9 @@ constexpr int kListInts = 68;   // a tile's tokens, adapter and number of tokens
 
 template <int RP>
 struct PromptShrinkGeo {
-  static constexpr int NR = RP < 16 ? 16 : RP;   // ranks of a product
-  static constexpr int X = 128 * 128, STAGE = X + NR * 128;  // bytes: rows of 64 k, swizzled
+  static constexpr int X = 128 * 128, STAGE = X + RP * 128;  // bytes: rows of 64 k, swizzled
   static constexpr int STAGES = RP <= 32 ? 5 : RP == 64 ? 4 : 3;
-  static constexpr int COLS = NR < 32 ? 32 : NR;  // of TMEM
+  static constexpr int COLS = RP < 32 ? 32 : RP;  // of TMEM
   static constexpr int PITCH = RP + 4;            // floats of a token's sums (they take the stages' place)
   static constexpr int OFF_LIST = STAGES * STAGE, OFF_BAR = OFF_LIST + 128 * 4, OFF_TILES = OFF_BAR + STAGES * 8 + 16;
   static_assert(128 * PITCH * 4 <= OFF_LIST && STAGE % 1024 == 0, "sums in the stages' place, stages on whole atoms");
@@ -567,8 +578,8 @@ __global__ void __launch_bounds__(kThreads, 2) lora_prompt_shrink_kernel(const _
       for (int r = 0; r < 4; ++r)
         if (xr[r]) copy16(at + r * 32 * 128, in ? xr[r] + k : p.x, in);
 #pragma unroll
-      for (int r = 0; r < (G::NR + 31) / 32; ++r)
-        if (G::NR >= 32 || r0 < G::NR) {
+      for (int r = 0; r < (RP + 31) / 32; ++r)
+        if (RP >= 32 || r0 < RP) {
           const bool there = in && r0 + r * 32 < p.rank;
           copy16(at + G::X + r * 32 * 128, there ? ar + r * 32 * p.a_row + k : p.a, there);
         }
@@ -594,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_prompt_shrink_kernel(const _
     fence_proxy_async_smem();
     __syncthreads();
     if (threadIdx.x == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(128, G::NR);
+      constexpr uint32_t idesc = idesc_bf16_f32(128, RP);
       const uint64_t x = sw128_desc(base + i % G::STAGES * G::STAGE), a = sw128_desc(base + i % G::STAGES * G::STAGE + G::X);
 #pragma unroll
       for (int k = 0; k < 4; ++k) tc_mma_f16(tmem, x + 2 * k, a + 2 * k, idesc, (uint32_t)(i | k));
@@ -612,10 +623,10 @@ __global__ void __launch_bounds__(kThreads, 2) lora_prompt_shrink_kernel(const _
   __syncthreads();  // (nobody writes sums before everybody's products are done)
   float *sums = reinterpret_cast<float *>(smem);
   {
-    const int row = (warp & 3) * 32 + lane, c0 = warp < 4 ? 0 : G::NR / 2;
+    const int row = (warp & 3) * 32 + lane, c0 = warp < 4 ? 0 : RP / 2;
 #pragma unroll
-    for (int q = 0; q < (G::NR >= 32 ? G::NR / 32 : 1); ++q) {
-      if (G::NR < 32 && warp >= 4) break;
+    for (int q = 0; q < (RP >= 32 ? RP / 32 : 1); ++q) {
+      if (RP < 32 && warp >= 4) break;
       float v[16];
       tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + c0 + q * 16, v);
 #pragma unroll
@@ -676,8 +687,9 @@ __device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&v)[16
 // serves the two), B comes for each step, the product is tcgen05's, 128 by NC, in
 // one of two TMEM buffers. y is copied to shared memory two steps ahead; the
 // products are added there in place, and a step later the sums leave in whole
-// rows. Bound by HBM, which does 6.0 - 6.2 TB/s of such rows read and written.
-// (With mma.sync and B in registers the warps had 460 - 560 instructions for
+// rows. Bound by HBM, which does 6.0 - 6.2 TB/s of such rows read and written (64
+// bytes of eight rows an instruction, as a fragment has them: 5.6); rank 16, 4,096
+// tokens of 34,816 columns: 103 us from a cold cache, 5.5 TB/s. (With mma.sync and B in registers the warps had 460 - 560 instructions for
 // 1,024 elements and ranks of 64 took 63 us where 16 took 36.)
 //
 // Rows need not begin on 16 bytes: element c of a row that begins s elements
@@ -1007,7 +1019,10 @@ int parts_of(int tokens, int rank, int inner) {
 }
 
 // Prompts: CTAs of a cluster, which share K: as many as bring 128 tokens each to
-// a wave (two CTAs per SM), while each keeps 512 k.
+// a wave (two CTAs per SM), while each keeps 512 k. Up to four: 4,096 tokens 144 us
+// with one, 128 with two, 121 with four or eight; six prompts of 2,000 92.7, 80.3,
+// 74.5 (two and more). Three, or five to eight, where they fit: 6,000 tokens 57 us
+// against 65 with three.
 int cluster_of(int tokens, int inner, int sm_count) {
   int s = 1;
   while (s < 4 && (long long)((tokens + 127) / 128) * s * 2 <= 2 * sm_count && inner >= 1024 * s) s *= 2;
