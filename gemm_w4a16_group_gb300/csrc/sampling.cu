@@ -44,9 +44,17 @@ struct Quads {
 
 // ---------------------------------------------------------------------------
 // probabilities: p_j = 2^((l_j - m) a) / sum_i 2^((l_i - m) a), a = log2(e) / T.
-// One pass: a thread holds the powers of its logits, relative to their own
-// maximum, in registers while the cluster agrees on maximum and sum. Slices
-// that do not fit are read twice.
+// One pass: a thread holds 64 logits in registers while its own powers' sum (each
+// relative to the thread's maximum) and the cluster's agree on one maximum and
+// sum, then makes the powers again. Slices that do not fit are read twice.
+//
+// 256 rows of 248,320 (127 MB read, 254 written): 82 us, 4.6 TB/s, where HBM would
+// take 57; a CTA loads, waits for its cluster and stores in turn, four of them an
+// SM, with 46 % of issue slots taken. Other shapes, as threads x quads x CTAs an
+// SM: 128 x 16 x 8 91 us, 256 x 8 x 6 94, 512 x 16 x 2 91, 512 x 8 x 3 112, 1024 x 8
+// x 1 138; clusters that go on to further rows with the next one's logits copied
+// ahead to shared memory 102. One row: 3.8 us, where a launch with a cluster barrier
+// is most of it.
 // ---------------------------------------------------------------------------
 constexpr int kProbThreads = 256;
 constexpr int kProbQuads = 16;  // of a thread
@@ -157,8 +165,8 @@ __global__ void __launch_bounds__(kProbThreads, 4) probabilities_kernel(const Pr
     for (int u = 0; u < kProbQuads; ++u) {
       const int k = k0 + u * kProbThreads + tid;
       x[u] = make_uint2(kNone, kNone);
-      if (ALIGNED ? q.is_whole(k) : k < q.hi)
-        x[u] = ALIGNED ? *reinterpret_cast<const uint2 *>(row + 4 * k - q.shift) : load_end(row, q, k, p.vocab);
+      if (!ALIGNED && k < q.hi) x[u] = load_end(row, q, k, p.vocab);
+      if (ALIGNED && q.is_whole(k)) x[u] = *reinterpret_cast<const uint2 *>(row + 4 * k - q.shift);
     }
     if (ALIGNED && ends) {
 #pragma unroll
@@ -249,11 +257,8 @@ __global__ void __launch_bounds__(kProbThreads, 4) probabilities_kernel(const Pr
       const int k = q.lo + u * kProbThreads + tid;
       const float2 v = powers(x[u].x, minus, a2), w = powers(x[u].y, minus, a2);
       const float2 a0 = f32_halves(mul2(f32_pair(v.x, v.y), f2)), b0 = f32_halves(mul2(f32_pair(w.x, w.y), f2));
-      if (ALIGNED ? q.is_whole(k) : k < q.hi) {
-        if (ALIGNED) *reinterpret_cast<float4 *>(out + 4 * k - q.shift) = make_float4(a0.x, a0.y, b0.x, b0.y);
-        else store_end(out, q, k, p.vocab, a0, b0);
-      }
-      if (ALIGNED && ends && k < q.hi && !q.is_whole(k)) store_end(out, q, k, p.vocab, a0, b0);
+      if (ALIGNED && q.is_whole(k)) *reinterpret_cast<float4 *>(out + 4 * k - q.shift) = make_float4(a0.x, a0.y, b0.x, b0.y);
+      else if ((!ALIGNED || ends) && k < q.hi) store_end(out, q, k, p.vocab, a0, b0);
     }
     return;
   }
@@ -287,6 +292,14 @@ __global__ void __launch_bounds__(kProbThreads, 4) probabilities_kernel(const Pr
 // on the order, and the token drawn is the one that 64-bit floats give, also where
 // the number falls next to one of 248,320 borders (they differ in less than one
 // draw of a million; 32-bit sums, off by 1e-7, in one of a hundred).
+//
+// A pass is one row of p, or one of p and one of q, over a cluster; its sums are
+// exchanged once, and every CTA then walks by itself to the next row to sum. 32
+// trees of 8 nodes over 248,320 tokens: 34 us, of which 5 are the tree's own loads
+// (the offsets, then the nodes, then their probabilities), 16 the first pass of
+// all rows (64 MB, 4 TB/s) and the rest further passes of rows with refusals, one
+// after the other on the few SMs that a cluster is on. One draw each for 64 tokens
+// over 128,000: 10.4 us, 3.1 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kFrac = 56;
 constexpr unsigned long long kOne = 1ull << kFrac;
@@ -804,7 +817,10 @@ cudaError_t launch_rows(void (*kern)(P), PerDevice &fits16, int rows, int want, 
 }
 
 // CTAs of a row: the fewest (a power of two) that leave each `most` elements at
-// most; with few rows more of them, up to `fit` in all, while each keeps `least`.
+// most; with few rows more of them, up to `fit` in all, while each keeps `least`
+// (probabilities of 24 rows of 32,001 with at least 4,096 5.9 us, 2,048 6.9, 8,192
+// 6.4; trees of 16 picked nodes over as many with 1,024 or 512 11.7, 2,048 12.4,
+// 4,096 13.0).
 int ctas_of(int rows, int vocab, int most, int least, int fit) {
   int s = 1;
   while (s < kMaxCluster && vocab > (long long)most * s) s *= 2;
@@ -832,7 +848,8 @@ cudaError_t launch_tree_sample(const SampleCall &c) {
   const bool aligned = address(c.p, 16) && address(c.q, 16) && (!c.q || (c.q_row - c.p_row) % 4 == 0);
   const SampleParams p{c.p, c.q, c.p_row, c.q_row, c.draft, c.mask, c.starts, c.u, c.rows, c.tokens, c.vocab, c.max_tree,
                        c.path, c.count, c.token, c.err};
-  // 16 warps a CTA while the rows' clusters are all there at once, 8 where that makes more of them
+  // 16 warps a CTA while the rows' clusters are all there at once (a chain of six 8.6 us against 10.3 with 8), 8 where that
+  // makes more of them (32 trees of eight 34 us against 45)
   const int s = ctas_of(c.rows, c.vocab, 32768, 1024, c.sm_count * 2);
   const bool few = (long long)c.rows * s * 2 <= c.sm_count * 2, one = c.max_tree == 1;
   void (*kern)(SampleParams);
