@@ -47,11 +47,15 @@ class Model:
     def norm(x):
         return (x.float() * torch.rsqrt(x.float().square().mean(-1, keepdim=True) + 1e-6)).to(torch.bfloat16)
 
-    def picks(self, tokens, cache, lengths, starts, mask, max_tree):
-        """The model's pick after each of `tokens`, whose keys and values join the cache."""
+    def hidden(self, tokens, cache, lengths, starts, mask, max_tree, beside=None):
+        """What the head reads after each of `tokens`, whose keys and values join the cache. `beside` (layer, input,
+        product) adds to each layer's first product what stands beside it."""
         x = self.embed[tokens]
         for i, (qkv, proj, gate_up, down) in enumerate(self.layers):
-            y = w4.gemm(self.norm(x), qkv, (HEADS + 2 * KV_HEADS) * DIM, HIDDEN, GROUP, True)
+            h = self.norm(x)
+            y = w4.gemm(h, qkv, (HEADS + 2 * KV_HEADS) * DIM, HIDDEN, GROUP, True)
+            if beside is not None:
+                beside(i, h, y)
             y = y.view(-1, HEADS + 2 * KV_HEADS, DIM)
             w4.kv_append(y[:, HEADS:HEADS + KV_HEADS], y[:, HEADS + KV_HEADS:], cache.k[i], cache.v[i], cache.table,
                          lengths, starts, **cache.scales)
@@ -60,7 +64,12 @@ class Model:
             x = x + w4.gemm(o.view(-1, HEADS * DIM), proj, HIDDEN, HEADS * DIM, GROUP, True)
             h = w4.gateup_silu(self.norm(x), gate_up, FFN, HIDDEN, GROUP, True)
             x = x + w4.gemm(h, down, HIDDEN, FFN, GROUP, True)
-        return w4.gemm_argmax(self.norm(x), self.head, VOCAB, HIDDEN, GROUP, True)[0]
+        return self.norm(x)
+
+    def picks(self, tokens, cache, lengths, starts, mask, max_tree):
+        """The model's pick after each of `tokens`, whose keys and values join the cache."""
+        x = self.hidden(tokens, cache, lengths, starts, mask, max_tree)
+        return w4.gemm_argmax(x, self.head, VOCAB, HIDDEN, GROUP, True)[0]
 
 
 class Cache:
