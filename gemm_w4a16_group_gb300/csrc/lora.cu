@@ -1086,10 +1086,15 @@ cudaError_t run(const LoraCall &c, const LoraParams &p, bool few, bool even) {
 
 }  // namespace
 
+// Of the pair that needs more, of those that a call of up to so many tokens may
+// take: what is enough for many tokens is enough for few.
 size_t lora_workspace_bytes(int tokens, int rank, int inner) {
-  size_t bytes = 0;  // of the pair that needs more, of those that a call may take
-  if (tokens <= kMostFew)
-    bytes = align_up((size_t)parts_of(tokens, rank, inner) * tokens * padded_rank(rank, true) * sizeof(float), 256);
+  size_t sums = 0;
+  for (int t = 16; t < 16 + tokens && t <= kMostFew; t += 16) {
+    const size_t n = (size_t)parts_of(t, rank, inner) * (t < tokens ? t : tokens);
+    if (n > sums) sums = n;
+  }
+  size_t bytes = align_up(sums * padded_rank(rank, true) * sizeof(float), 256);
   if (tokens > kAlwaysFew) {
     const size_t lists = (size_t)most_clusters(tokens, groups_of(kMaxAdapters, tokens)) * 2 * kListInts * sizeof(int);
     const size_t prompts = 256 + align_up((size_t)tokens * padded_rank(rank, false) * 4, 256) + align_up(lists, 256);

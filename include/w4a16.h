@@ -455,7 +455,8 @@ int w4a16_tree_accept(const int64_t *target, const int64_t *draft, const int64_t
  *
  * A row with nothing above -inf gets 0 throughout; a NaN (or +inf) that is kept
  * makes the row's kept probabilities NaN. A probability is off by less than 2^-17 +
- * 2^-23 (max - l_j) / T of itself; below 2^-126 it may be 0.
+ * 2^-23 (max - l_j) / T of itself; below 2^-126 it may be 0. out must not overlap
+ * what is read.
  */
 int w4a16_probabilities(const uint16_t *logits, int64_t logits_row, const float *temperature, const float *floor,
                         int tokens, int vocab, float *out, w4a16_stream_t stream);
@@ -486,9 +487,9 @@ int w4a16_probabilities(const uint16_t *logits, int64_t logits_row, const float 
  *   token  int64 [rows]  the token drawn (-1 for a row without new tokens)
  *
  * A NaN or negative probability counts as 0, one above 1 as 1; a drafted token
- * outside the vocabulary is passed over (W4A16_ERR_INDEX). Probabilities are
- * summed in whole multiples of 2^-46, tests are double: results do not depend on
- * any order.
+ * outside the vocabulary is passed over (W4A16_ERR_INDEX). Probabilities (and what
+ * refusals leave of each) are rounded to multiples of 2^-46 and summed exactly,
+ * tests are double: results do not depend on any order.
  */
 int w4a16_tree_sample(const float *p, int64_t p_row, const float *q, int64_t q_row, int vocab, const int64_t *draft,
                       const int64_t *mask, const int32_t *starts, const float *u, int rows, int tokens, int max_tree,
@@ -543,7 +544,8 @@ int w4a16_kv_reserve(int32_t *page_table, int max_pages, int table_rows, int32_t
  *   y, out     bf16 [tokens][outer], element (t, n) at t * row stride + n (row
  *              strides of y, out and x below 2^30 elements). out
  *              may be y (then rows without an adapter are not touched); it must
- *              not overlap y otherwise, nor a, b or x's other rows
+ *              not overlap y otherwise (other columns of the same wider rows
+ *              are apart), nor x, a or b
  *   x          bf16 [tokens][inner], x_row a multiple of 8, base 16-byte aligned
  *   a          bf16 [adapters][rank][inner], b bf16 [adapters][outer][rank]:
  *              strides multiples of 8, bases 16-byte aligned
@@ -554,11 +556,13 @@ int w4a16_kv_reserve(int32_t *page_table, int max_pages, int table_rows, int32_t
  *              multiple of 8; outer any
  *   workspace  w4a16_lora_workspace_bytes(tokens, rank, inner) bytes, 256-byte
  *              aligned, used only while the call runs on `stream`. A call makes
- *              two launches that share it
+ *              two launches that share it. (The size grows with each argument:
+ *              one for the largest call is enough for smaller ones)
  *
  * Sums are float32; x A^T goes into the second product with 16 bits of mantissa;
  * out is rounded once. Results are bitwise reproducible, and a token's does not
- * depend on the tokens beside it. Tokens at starts[rows] and above are not read
+ * depend on what the tokens beside it hold (on how many there are only by the order
+ * of its sums). Tokens at starts[rows] and above are not read
  * and not written. An adapter outside -1 .. adapters - 1 counts as -1, a row whose
  * offsets cannot be is left out (a token that descending offsets give to two rows
  * is either's); w4a16_kernel_status() then returns W4A16_ERR_INDEX.

@@ -57,7 +57,7 @@ def test_lora_add(L):
           [dict(rank=0), dict(rank=4), dict(rank=12), dict(rank=136), dict(rank=-8), dict(inner=0), dict(inner=36), dict(inner=-32),
            dict(outer=0), dict(outer=1 << 27), dict(tokens=0), dict(rows=0), dict(rows=65536), dict(adapters=0), dict(adapters=4097),
            dict(starts=None), dict(y_row=-64), dict(x_row=-32), dict(a_adapter=-8), dict(a_row=-8), dict(b_adapter=-8), dict(b_row=-8),
-           dict(out_row=-64), dict(out_row=63)],
+           dict(out_row=-64), dict(out_row=63), dict(y_row=1 << 30), dict(x_row=1 << 30), dict(out_row=1 << 30)],
           [dict(x=FAKE + 8), dict(a=FAKE + 8), dict(b=FAKE + 2), dict(workspace=FAKE + 128), dict(y=FAKE + 1), dict(out=FAR + 1),
            dict(scale=FAKE + 2), dict(adapter=FAKE + 2), dict(starts=FAKE + 2), dict(x_row=36), dict(a_adapter=516), dict(a_row=36),
            dict(b_adapter=1028), dict(b_row=20)])
@@ -89,6 +89,11 @@ def test_workspace_sizes(L):
                 n = w4.lora_workspace_bytes(tokens, rank, inner)
                 assert n % 256 == 0 and n >= tokens * padded * 4
                 assert n <= 32 * tokens * padded * 4 + 256 and n < 32 * 1024 * 1024 + 4 * tokens * padded * 4
+    for rank, inner in ((8, 64), (16, 5120), (64, 17408), (128, 17408)):  # one for the largest call is enough for all
+        sizes = [w4.lora_workspace_bytes(t, rank, inner) for t in range(1, 2100)]
+        assert sizes == sorted(sizes)
+        assert w4.lora_workspace_bytes(300, rank, inner) <= w4.lora_workspace_bytes(300, rank, inner + 512)
+        assert w4.lora_workspace_bytes(300, rank - 8 or 8, inner) <= w4.lora_workspace_bytes(300, rank, inner)
 
 
 # ---------------------------------------------------------------------------
