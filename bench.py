@@ -41,7 +41,7 @@ TRAFFIC_FILE = os.path.join(ROOT, "profiles", "traffic.json")
 
 
 # the cache operators' own sources: no workload here runs them
-CACHE_SOURCES = ("kv_pages.cu", "tree_attn.cu", "tree_attn.cuh", "tree_attn_tc.cu")
+CACHE_SOURCES = ("kv_pages.cu", "lora.cu", "sampling.cu", "tree_attn.cu", "tree_attn.cuh", "tree_attn_tc.cu")
 
 
 def kernel_source_hash() -> str:

@@ -124,6 +124,12 @@ __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {  // (of a
   return *reinterpret_cast<const uint32_t *>(&r);
 }
 
+// all ones in the halves of x that are the ones of `top` (0 and -0 are the same, and so are NaNs)
+__device__ __forceinline__ uint32_t same2(uint32_t x, uint32_t top) {
+  const __nv_bfloat162 a = *reinterpret_cast<__nv_bfloat162 *>(&x), b = *reinterpret_cast<__nv_bfloat162 *>(&top);
+  return __heq2_mask(a, b) | (__hisnan(b.x) ? ~__heq2_mask(a, a) : 0u);
+}
+
 __device__ __forceinline__ u64 key_max(u64 a, u64 b) { return a > b ? a : b; }
 
 // (maximum, sum of powers relative to it) over the first N lanes' parts; an empty part is (lowest, 0)
@@ -179,17 +185,25 @@ __global__ void __launch_bounds__(kProbThreads, 4) probabilities_kernel(const Pr
 #pragma unroll
       for (int u = 0; u < kProbQuads; ++u) drop(x[u], floor);
     }
-    if (greedy) {
+    if (greedy) {  // the thread's maximum, then the first element that is it (none: -inf)
+      uint32_t top = kNone;
 #pragma unroll
-      for (int u = 0; u < kProbQuads; ++u) {
-        // (most quads are behind the best one so far: a look at their maximum tells)
-        const uint32_t top = max2_nan(x[u].x, x[u].y);
-        const uint32_t high = max(order_key16(top), order_key16(top >> 16));
-        if (high <= (uint32_t)(best >> 32)) continue;
-        const uint32_t v[4] = {x[u].x & 0xFFFFu, x[u].x >> 16, x[u].y & 0xFFFFu, x[u].y >> 16};
+      for (int u = 0; u < kProbQuads; ++u) top = max2_nan(top, max2_nan(x[u].x, x[u].y));
+      top = max2_nan(top, top >> 16 | top << 16);
+      const uint32_t key = order_key16(top & 0xFFFFu);
+      if (top != kNone && key > (uint32_t)(best >> 32)) {
+        uint32_t at = 0, lo = 0, hi = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (v[i] != (kNone & 0xFFFFu)) best = key_max(best, argmax_key(v[i], 4 * (k0 + u * kProbThreads + tid) - q.shift + i));
+        for (int u = kProbQuads - 1; u >= 0; --u) {
+          const uint32_t l = same2(x[u].x, top), h = same2(x[u].y, top);
+          if (l | h) {
+            at = u;
+            lo = l;
+            hi = h;
+          }
+        }
+        const uint32_t i = lo ? (lo & 0xFFFFu ? 0 : 1) : hi & 0xFFFFu ? 2 : 3;
+        best = (u64)key << 32 | (0xFFFFFFFFu - (uint32_t)(4 * (k0 + (int)at * kProbThreads + tid) - q.shift + (int)i));
       }
       continue;
     }
@@ -221,14 +235,13 @@ __global__ void __launch_bounds__(kProbThreads, 4) probabilities_kernel(const Pr
     }
     cluster_wait();
     if (tid < (int)S) st_cluster_u64(mapa_shared(smem_u32(&slots[rank]), tid), best);
-    cluster_sync_all();
+    cluster_arrive();
+    for (int k = q.lo + tid; k < q.hi; k += kProbThreads) store_quad<ALIGNED>(out, q, k, p.vocab, make_float2(0.f, 0.f), make_float2(0.f, 0.f));
+    cluster_wait();
     best = 0;
     for (uint32_t i = 0; i < S; ++i) best = key_max(best, slots[i]);
-    const int first = best ? (int)(0xFFFFFFFFu - (uint32_t)best) : -4;
-    for (int k = q.lo + tid; k < q.hi; k += kProbThreads) {
-      const int at = first - (4 * k - q.shift);
-      store_quad<ALIGNED>(out, q, k, p.vocab, make_float2(at == 0, at == 1), make_float2(at == 2, at == 3));
-    }
+    const int first = best ? (int)(0xFFFFFFFFu - (uint32_t)best) : -4, mine = (first + q.shift) >> 2;
+    if (first >= 0 && mine >= q.lo && mine < q.hi && (mine - q.lo) % kProbThreads == tid) out[first] = 1.f;  // (over its own 0)
     return;
   }
   join<32>(m, s, a);
