@@ -632,15 +632,18 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) tree_sample_kernel(con
       for (int k0 = mine.whole_lo + lane; k0 < mine.whole_hi; k0 += 32 * kBitsQuads) {  // (so long the bits' sums hold)
         uint32_t hi = 0, lo = 0;
         const int k1 = min(k0 + 32 * kBitsQuads, mine.whole_hi);
-        constexpr int U = 4;  // quads of two rows on their way
-        int k = k0;
+        constexpr int U = 4;  // quads on their way (past the part: zeros, which add nothing)
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
         auto two_rows = [&](auto add) {
-          for (; k + 32 * (U - 1) < k1; k += 32 * U) {
+          for (int k = k0; k < k1; k += 32 * U) {
             float4 x[U], y[U];
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-              x[i] = p4[k + 32 * i];
-              y[i] = q4[k + 32 * i];
+              x[i] = y[i] = zero;
+              if (k + 32 * i < k1) {
+                x[i] = p4[k + 32 * i];
+                y[i] = q4[k + 32 * i];
+              }
             }
 #pragma unroll
             for (int i = 0; i < U; ++i) {
@@ -648,26 +651,22 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) tree_sample_kernel(con
               add(x[i].z, x[i].w, y[i].z, y[i].w);
             }
           }
-          for (; k < k1; k += 32) {
-            const float4 x = p4[k], y = q4[k];
-            add(x.x, x.y, y.x, y.y);
-            add(x.z, x.w, y.z, y.w);
-          }
         };
         if (c == 0) {
-          auto add = [&](const float4 &x) {
-            const Bits d = bits_of(sound(x.x), sound(x.y)), e = bits_of(sound(x.z), sound(x.w));
-            hi += d.hi_a + d.hi_b + (e.hi_a + e.hi_b) - 4 * kUpper;
-            lo += d.lo_a + d.lo_b + (e.lo_a + e.lo_b) - 4 * kLower;
-          };
-          for (; k + 32 * (2 * U - 1) < k1; k += 32 * 2 * U) {
-            float4 x[2 * U];
+          for (int k = k0; k < k1; k += 32 * U) {
+            float4 x[U];
 #pragma unroll
-            for (int i = 0; i < 2 * U; ++i) x[i] = p4[k + 32 * i];
+            for (int i = 0; i < U; ++i) {
+              x[i] = zero;
+              if (k + 32 * i < k1) x[i] = p4[k + 32 * i];
+            }
 #pragma unroll
-            for (int i = 0; i < 2 * U; ++i) add(x[i]);
+            for (int i = 0; i < U; ++i) {
+              const Bits d = bits_of(sound(x[i].x), sound(x[i].y)), e = bits_of(sound(x[i].z), sound(x[i].w));
+              hi += d.hi_a + d.hi_b + (e.hi_a + e.hi_b) - 4 * kUpper;
+              lo += d.lo_a + d.lo_b + (e.lo_a + e.lo_b) - 4 * kLower;
+            }
           }
-          for (; k < k1; k += 32) add(p4[k]);
         } else if (c == kOne) {  // max(p, q) - q
           two_rows([&](float x0, float x1, float y0, float y1) {
             const Bits d = bits_of(fminf(fmaxf(fmaxf(x0, y0), 0.f), 1.f), sound(y0));
