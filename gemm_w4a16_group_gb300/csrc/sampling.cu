@@ -48,12 +48,13 @@ struct Quads {
 // relative to the thread's maximum) and the cluster's agree on one maximum and
 // sum, then makes the powers again. Slices that do not fit are read twice.
 //
-// 256 rows of 248,320 (127 MB read, 254 written): 82 us, 4.6 TB/s, where HBM would
+// 256 rows of 248,320 (127 MB read, 254 written): 75 us, 5.1 TB/s, where HBM would
 // take 57; a CTA loads, waits for its cluster and stores in turn, four of them an
-// SM, with 46 % of issue slots taken. Other shapes, as threads x quads x CTAs an
-// SM: 128 x 16 x 8 91 us, 256 x 8 x 6 94, 512 x 16 x 2 91, 512 x 8 x 3 112, 1024 x 8
-// x 1 138; clusters that go on to further rows with the next one's logits copied
-// ahead to shared memory 102. One row: 3.8 us, where a launch with a cluster barrier
+// SM, with 46 % of issue slots taken (greedy rows, which need no powers: 70). Before
+// those had a path of their own it took 83, and in other shapes, as threads x quads
+// x CTAs an SM: 128 x 16 x 8 91 us, 256 x 8 x 6 94, 512 x 16 x 2 91, 512 x 8 x 3 112,
+// 1024 x 8 x 1 138; as clusters that go on to further rows with the next one's logits
+// copied ahead to shared memory 102. One row: 3.8 us, where a launch with a cluster barrier
 // is most of it.
 // ---------------------------------------------------------------------------
 constexpr int kProbThreads = 256;
@@ -308,11 +309,11 @@ __global__ void __launch_bounds__(kProbThreads, 4) probabilities_kernel(const Pr
 //
 // A pass is one row of p, or one of p and one of q, over a cluster; its sums are
 // exchanged once, and every CTA then walks by itself to the next row to sum. 32
-// trees of 8 nodes over 248,320 tokens: 34 us, of which 5 are the tree's own loads
-// (the offsets, then the nodes, then their probabilities), 16 the first pass of
-// all rows (64 MB, 4 TB/s) and the rest further passes of rows with refusals, one
+// trees of 8 nodes over 248,320 tokens: 31 us, of which 5 are the tree's own loads
+// (the offsets, then the nodes, then their probabilities), about 12 the first pass of
+// all rows (48 MB) and the rest further passes of rows with refusals, one
 // after the other on the few SMs that a cluster is on. One draw each for 64 tokens
-// over 128,000: 10.4 us, 3.1 TB/s.
+// over 128,000: 8.6 us, 3.8 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kFrac = 56;
 constexpr unsigned long long kOne = 1ull << kFrac;
@@ -521,7 +522,7 @@ struct Walk {
 // SINGLE: no row has a child (max_tree 1), so that every CTA knows what to do by
 // itself and the cluster need not be told.
 template <bool ALIGNED, bool SINGLE, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) tree_sample_kernel(const SampleParams p) {
+__global__ void __launch_bounds__(WARPS * 32, WARPS == 16 ? 1 : 4) tree_sample_kernel(const SampleParams p) {
   static_assert(WARPS <= 16 && (WARPS & (WARPS - 1)) == 0 && WARPS * 32 >= kMaxTree, "parts of a row, nodes of a tree");
   __shared__ SampleSmem sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -860,8 +861,8 @@ cudaError_t launch_tree_sample(const SampleCall &c) {
   const bool aligned = address(c.p, 16) && address(c.q, 16) && (!c.q || (c.q_row - c.p_row) % 4 == 0);
   const SampleParams p{c.p, c.q, c.p_row, c.q_row, c.draft, c.mask, c.starts, c.u, c.rows, c.tokens, c.vocab, c.max_tree,
                        c.path, c.count, c.token, c.err};
-  // 16 warps a CTA while the rows' clusters are all there at once (a chain of six 8.6 us against 10.3 with 8), 8 where that
-  // makes more of them (32 trees of eight 34 us against 45)
+  // 16 warps a CTA while every CTA has an SM to itself (a chain of six 7.5 us against 9.9 with 8), 8 where that makes more
+  // of them (32 trees of eight 31 us against 34)
   const int s = ctas_of(c.rows, c.vocab, 32768, 1024, c.sm_count * 2);
   const bool few = (long long)c.rows * s * 2 <= c.sm_count * 2, one = c.max_tree == 1;
   void (*kern)(SampleParams);
