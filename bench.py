@@ -40,7 +40,7 @@ L2_BYTES = 129 * 1024 * 1024
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "traffic.json")
 
 
-# the cache operators' own sources: no workload here runs them
+# sources of the verify step's other operators: no workload here runs them
 CACHE_SOURCES = ("kv_pages.cu", "lora.cu", "sampling.cu", "tree_attn.cu", "tree_attn.cuh", "tree_attn_tc.cu")
 
 

@@ -309,11 +309,11 @@ __global__ void __launch_bounds__(kProbThreads, 4) probabilities_kernel(const Pr
 //
 // A pass is one row of p, or one of p and one of q, over a cluster; its sums are
 // exchanged once, and every CTA then walks by itself to the next row to sum. 32
-// trees of 8 nodes over 248,320 tokens: 31 us, of which 5 are the tree's own loads
-// (the offsets, then the nodes, then their probabilities), about 12 the first pass of
-// all rows (48 MB) and the rest further passes of rows with refusals, one
-// after the other on the few SMs that a cluster is on. One draw each for 64 tokens
-// over 128,000: 8.6 us, 3.8 TB/s.
+// trees of 8 nodes over 248,320 tokens: 31 us. 18 are the tree's own loads (the
+// offsets, then the nodes, then their probabilities: 5 us) and the first pass of all
+// rows; the rest is further passes of rows with refusals, one after the other on the
+// few SMs that a cluster is on. One draw each for 64 tokens over 128,000: 8.6 us, 3.8
+// TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kFrac = 56;
 constexpr unsigned long long kOne = 1ull << kFrac;

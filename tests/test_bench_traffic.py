@@ -47,3 +47,9 @@ def test_a_changed_product_makes_them_stale(tree, name):
 def test_a_new_source_makes_them_stale(tree):
     (tree / "another.cu").write_text("// new\n")
     assert bench.stored_traffic("a") is None
+
+
+@pytest.mark.parametrize("name", ["lora.cu", "sampling.cu"])
+def test_the_sampled_steps_operators_are_no_part_of_them(tree, name):
+    change(tree / name)
+    assert bench.stored_traffic("a") == 7
