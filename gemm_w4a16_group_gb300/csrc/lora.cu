@@ -81,8 +81,8 @@ __device__ __forceinline__ int block_scan(int v, int *sums, int &total) {
   return before + inc - v;
 }
 
-// First token and number of tokens of row b; none where the offsets cannot be.
-__device__ __forceinline__ int row_tokens(const LoraParams &p, int b, int &first) {
+// First token and number of tokens of row b; none, and `bad`, where the offsets cannot be.
+__device__ __forceinline__ int row_tokens(const LoraParams &p, int b, int &first, bool &bad) {
   if (!p.starts) {
     first = b;
     return 1;
@@ -91,6 +91,7 @@ __device__ __forceinline__ int row_tokens(const LoraParams &p, int b, int &first
   const int end = p.starts[b + 1];
   if (first < 0 || end < first || end > p.tokens) {
     atomicOr(p.err, kErrIndex);
+    bad = true;
     return 0;
   }
   return end - first;
@@ -110,6 +111,7 @@ struct Tiles {
   int *count, *first, *sums;
   int bins;
   int mine, mine_at, mine_n;  // adapter, first token and number of tokens of row threadIdx.x (the block's first pass over the rows)
+  bool bad;  // a row of this thread's has offsets that cannot be
 
   static __host__ __device__ int ints(int adapters) { return 2 * adapters + 3 + kWarps; }
   __device__ Tiles(int *mem, int adapters)
@@ -119,16 +121,17 @@ struct Tiles {
   __device__ void make(const LoraParams &p) {
     mine = -1;
     mine_at = mine_n = 0;
+    bad = false;
     if ((int)threadIdx.x < p.rows) {
       mine = row_adapter(p, threadIdx.x);
-      mine_n = row_tokens(p, threadIdx.x, mine_at);
+      mine_n = row_tokens(p, threadIdx.x, mine_at, bad);
     }
     for (int e = threadIdx.x; e < bins; e += kThreads) count[e] = 0;
     __syncthreads();
     if (mine_n) atomicAdd(&count[mine], mine_n);
     for (int b = kThreads + threadIdx.x; b < p.rows; b += kThreads) {
       int s;
-      const int n = row_tokens(p, b, s);
+      const int n = row_tokens(p, b, s, bad);
       if (n) atomicAdd(&count[row_adapter(p, b)], n);
     }
     __syncthreads();
@@ -158,12 +161,13 @@ struct Tiles {
   // Tokens lo .. hi of adapter e, in the rows' order, into list (all threads)
   __device__ void tokens(const LoraParams &p, int e, int lo, int hi, int *list) const {
     int done = 0;
+    bool known;
     for (int b0 = 0; b0 < p.rows && done < hi; b0 += kThreads) {
       int s = mine_at, n = mine == e ? mine_n : 0, total;
       if (b0) {
         const int b = b0 + threadIdx.x;
         n = 0;
-        if (b < p.rows && row_adapter(p, b) == e) n = row_tokens(p, b, s);
+        if (b < p.rows && row_adapter(p, b) == e) n = row_tokens(p, b, s, known);
         __syncthreads();
       }
       const int at = done + block_scan(n, sums, total);
@@ -531,9 +535,12 @@ __global__ void __launch_bounds__(kThreads, 2) lora_prompt_shrink_kernel(const _
   grid_dependency_wait();
   grid_launch_dependents();
   tiles.make<2 * kTile>(p);
-  const int all = tiles.first[p.adapters + 1];
+  // Rows share no tokens, so there are as many clusters as tiles and more. Offsets that descend may claim tokens many
+  // times over: then there are no more tiles than lists, and none where their number may not have fitted 32 bits.
+  const bool wrapped = __syncthreads_or(tiles.bad) && (long long)p.rows * p.tokens >= 1ll << 31;
+  const int all = wrapped ? 0 : min(tiles.first[p.adapters + 1], (int)gridDim.x / parts);
   if (tile == 0 && part == 0 && threadIdx.x == 0) {
-    p.head[0] = 2 * tiles.first[p.adapters];
+    p.head[0] = 2 * min(tiles.first[p.adapters], all);
     p.head[1] = 2 * all;
   }
   if (tile >= all) return;  // (all CTAs of the cluster do, here and below)
@@ -1029,7 +1036,7 @@ int cluster_of(int tokens, int inner, int sm_count) {
   return s;
 }
 
-// Prompts: clusters at most, whatever the rows' adapters; each has two lists
+// Prompts: clusters at most, whatever the rows' adapters (no more groups than tokens); each has two lists
 long long most_clusters(int tokens, int groups) { return tokens / (2 * kTile) + (long long)groups + 1; }
 
 template <class K>
@@ -1070,7 +1077,7 @@ cudaError_t run_few(const LoraCall &c, const LoraParams &p, bool even) {
 template <int RP>
 cudaError_t run_prompts(const LoraCall &c, const LoraParams &p, bool even) {
   const int cluster = cluster_of(c.tokens, c.inner, c.sm_count);
-  const long long clusters = most_clusters(c.tokens, groups_of(c.adapters, c.rows));
+  const long long clusters = most_clusters(c.tokens, groups_of(groups_of(c.adapters, c.rows), c.tokens));
   const cudaError_t e = launch(lora_prompt_shrink_kernel<RP>, (unsigned)(clusters * cluster), cluster,
                                PromptShrinkGeo<RP>::smem(c.adapters), c.stream, p);
   if (e != cudaSuccess) return e;

@@ -564,8 +564,8 @@ int w4a16_kv_reserve(int32_t *page_table, int max_pages, int table_rows, int32_t
  * depend on what the tokens beside it hold (on how many there are only by the order
  * of its sums). Tokens at starts[rows] and above are not read
  * and not written. An adapter outside -1 .. adapters - 1 counts as -1, a row whose
- * offsets cannot be is left out (a token that descending offsets give to two rows
- * is either's); w4a16_kernel_status() then returns W4A16_ERR_INDEX.
+ * offsets cannot be is left out (what a token gets that descending offsets give to
+ * several rows is not defined); w4a16_kernel_status() then returns W4A16_ERR_INDEX.
  * ------------------------------------------------------------------------ */
 #define W4A16_MAX_ADAPTERS 4096
 #define W4A16_MAX_RANK 128

@@ -169,6 +169,26 @@ def test_bad_indices_are_left_out_and_reported():
                 assert ((keep[i].double().cpu() - want[0]).abs() <= bound[0]).all()
 
 
+def test_descending_offsets_that_claim_tokens_many_times():
+    """More tiles than a call of so many tokens has room for, and more tokens than 32 bits count."""
+    for tokens, rows, top in ((1400, 200, 700), (1400, 65535, 1400), (70000, 65535, 70000)):
+        gen = torch.Generator(device="cuda").manual_seed(rows)
+        bf16 = lambda *shape: torch.randn(shape, generator=gen, device="cuda").to(torch.bfloat16)  # noqa: E731
+        x, y, a, b = bf16(tokens, 16), bf16(tokens, 24), bf16(3, 8, 16), bf16(3, 24, 8)
+        starts = torch.zeros(rows + 1, dtype=torch.int32, device="cuda")
+        starts[1::2] = top  # 0, top, 0, top ..: every other row claims all of them
+        adapter = torch.full((rows,), 1, dtype=torch.int32, device="cuda")
+        for out in (torch.full_like(y, 5.0), y):
+            before = y.clone()
+            w4.lora_add(y, x, a, b, adapter, starts, out=out)
+            assert w4.kernel_status() == -6
+            want, bound = adapted(before, x, a, b, [1] * tokens, None)
+            kept = out == (before if out is y else 5.0)
+            assert (kept.cpu() | ((out.double().cpu() - want).abs() <= bound)).all() or out is y
+            assert kept[top:].all()
+            y.copy_(before)
+
+
 def test_values_that_are_not_finite_stay_with_their_tokens():
     p = Problem([3, 3, 3], [0, 1, -1], 16, 256, 128, 2)
     p.x[1, 5], p.x[7, 5] = math.inf, math.nan  # the second belongs to a row without an adapter
