@@ -438,6 +438,7 @@ __global__ void __launch_bounds__(kThreads, ExpandGeo<RP>::CTAS) lora_expand_ker
           v.x += u.x;
           v.y += u.y;
         }
+        if (r >= p.rank) v = make_float2(0.f, 0.f);  // (an infinite x times the padding's zeros is not a number)
         const uint2 both = two_parts(v.x * scale, v.y * scale);
         *reinterpret_cast<uint32_t *>(smem + row * G::ROW + r * 2) = both.x;
         *reinterpret_cast<uint32_t *>(smem + G::OFF_LO + row * G::ROW + r * 2) = both.y;
@@ -661,6 +662,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_prompt_shrink_kernel(const _
       v.z += u.z;
       v.w += u.w;
     }
+    if (r >= p.rank) v = make_float4(0.f, 0.f, 0.f, 0.f);  // (an infinite x times the padding's zeros is not a number)
     const uint2 a = two_parts(v.x * scale, v.y * scale), b = two_parts(v.z * scale, v.w * scale);
     uint16_t *out = p.low + (long long)list[row] * (2 * RP) + r;
     *reinterpret_cast<uint2 *>(out) = make_uint2(a.x, b.x);

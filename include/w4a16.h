@@ -464,7 +464,7 @@ int w4a16_probabilities(const uint16_t *logits, int64_t logits_row, const float 
 /*
  * Sampled acceptance: w4a16_tree_accept for a target that samples. p and q are
  * the target's and the drafter's probabilities after each token (float32,
- * element (t, j) at t * p_row + j; 0 <= p, q <= 1, a row's sum below 128). The
+ * element (t, j) at t * p_row + j; 0 <= p, q <= 1, a row's sum below 2). The
  * children of a node were drawn from q at it, each on its own; q NULL: they were
  * picked without chance (the likeliest tokens, a lookup). From node 0 (always
  * accepted) the walk asks the children of the node it stands on, lowest first:
@@ -562,7 +562,8 @@ int w4a16_kv_reserve(int32_t *page_table, int max_pages, int table_rows, int32_t
  * Sums are float32; x A^T goes into the second product with 16 bits of mantissa;
  * out is rounded once. Results are bitwise reproducible, and a token's does not
  * depend on what the tokens beside it hold (on how many there are only by the order
- * of its sums). Tokens at starts[rows] and above are not read
+ * of its sums). What is not finite stays with its token, or with its adapter and
+ * column. Tokens at starts[rows] and above are not read
  * and not written. An adapter outside -1 .. adapters - 1 counts as -1, a row whose
  * offsets cannot be is left out (what a token gets that descending offsets give to
  * several rows is not defined); w4a16_kernel_status() then returns W4A16_ERR_INDEX.

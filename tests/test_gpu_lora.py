@@ -201,6 +201,17 @@ def test_values_that_are_not_finite_stay_with_their_tokens():
     assert torch.equal(out[6:].view(torch.int16), p.y[6:].view(torch.int16))
 
 
+@pytest.mark.parametrize("tokens", [3, 1100])
+@pytest.mark.parametrize("rank", [8, 24, 40, 72])
+def test_an_infinite_input_times_positive_weights_is_infinite(tokens, rank):
+    """Ranks are padded inside with zeros, and infinity times those would not be a number."""
+    p = Problem([tokens], [1], rank, 72, 40, 2)
+    p.a, p.b = p.a.abs() + 0.1, p.b.abs() + 0.1
+    p.x[2, 7] = math.inf
+    out = p.run()
+    assert (out[2] == math.inf).all() and out[:2].isfinite().all() and out[3:].isfinite().all()
+
+
 def test_streams_graphs_and_repeats():
     for sizes, which in (([3, 1, 4], [0, 1, 0]), ([300, 300], [0, 1]), ([700, 400], [0, 1])):
         p = Problem(sizes, which, 32, 512, 1000, 2)
