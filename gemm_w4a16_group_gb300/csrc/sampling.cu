@@ -93,15 +93,25 @@ __device__ __forceinline__ void store_end(float *row, const Quads &q, int k, int
   for (int i = 0; i < 4; ++i)
     if (j + i >= 0 && j + i < n) row[j + i] = v[i];
 }
-// ALIGNED: whole quads are. Otherwise every quad is moved one by one.
-template <bool ALIGNED>
-__device__ __forceinline__ uint2 load_quad(const uint16_t *row, const Quads &q, int k, int n) {
-  if (ALIGNED && q.is_whole(k)) return *reinterpret_cast<const uint2 *>(row + 4 * k - q.shift);
-  return load_end(row, q, k, n);
+// Quads begin on 16 bytes of `out`. Where the row's logits are `off` of them after 8 bytes, a quad is in two words: its
+// own and the next.
+__device__ __forceinline__ uint2 from_words(uint2 w, uint2 next, int off) {
+  const uint32_t a = off & 2 ? w.y : w.x, b = off & 2 ? next.x : w.y, c = off & 2 ? next.y : next.x;
+  return make_uint2(__funnelshift_r(a, b, 16 * (off & 1)), __funnelshift_r(b, c, 16 * (off & 1)));
 }
-template <bool ALIGNED>
+__device__ __forceinline__ uint2 load_word(const uint16_t *row, const Quads &q, int k, int off) {
+  return *reinterpret_cast<const uint2 *>(row + 4 * k - q.shift - off);
+}
+__device__ __forceinline__ void store_whole(float *row, const Quads &q, int k, float2 a, float2 b) {
+  *reinterpret_cast<float4 *>(row + 4 * k - q.shift) = make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ uint2 load_quad(const uint16_t *row, const Quads &q, int k, int off, int n) {
+  if (!q.is_whole(k)) return load_end(row, q, k, n);
+  const uint2 w = load_word(row, q, k, off);
+  return from_words(w, off ? load_word(row, q, k + 1, off) : w, off);
+}
 __device__ __forceinline__ void store_quad(float *row, const Quads &q, int k, int n, float2 a, float2 b) {
-  if (ALIGNED && q.is_whole(k)) *reinterpret_cast<float4 *>(row + 4 * k - q.shift) = make_float4(a.x, a.y, b.x, b.y);
+  if (q.is_whole(k)) store_whole(row, q, k, a, b);
   else store_end(row, q, k, n, a, b);
 }
 
@@ -147,6 +157,9 @@ __device__ __forceinline__ void join(float &m, float &s, float a) {
 template <bool ALIGNED>
 __global__ void __launch_bounds__(kProbThreads, 4) probabilities_kernel(const ProbParams p) {
   constexpr int kWarps = kProbThreads / 32;
+  // !ALIGNED: a word's other half comes from the lane above, and the last lane's quads are the next warp's
+  constexpr int kStep = ALIGNED ? kProbThreads : kWarps * 31, kQuads = ALIGNED ? kProbQuads : kProbQuads + 1;
+  static_assert(kStep * kQuads >= kProbThreads * kProbQuads, "as much in a CTA's registers, however rows begin");
   __shared__ u64 slots[kMaxCluster], warps[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t S = cluster_nctarank(), rank = cluster_ctarank();
@@ -157,45 +170,54 @@ __global__ void __launch_bounds__(kProbThreads, 4) probabilities_kernel(const Pr
 
   const uint16_t *row = p.logits + r * p.row;
   float *out = p.out + r * p.vocab;
-  const Quads q(p.vocab, ALIGNED ? (int)(r * p.vocab & 3) : 0, rank, __ffs(S) - 1);
+  const Quads q(p.vocab, (int)(reinterpret_cast<uintptr_t>(out) >> 2 & 3), rank, __ffs(S) - 1);
+  const int off = ALIGNED ? 0 : (int)((reinterpret_cast<uintptr_t>(row) >> 1) - q.shift & 3);
   const float t = p.temperature ? p.temperature[r] : 1.f, floor = p.floor ? p.floor[r] : -INFINITY;
   const bool greedy = !(t > 0.f), ends = q.whole_lo > q.lo || q.whole_hi < q.hi;
 
   // a logit of -inf stays -inf through difference and product, whatever the temperature
   const float lowest = -3.40282347e38f, a = greedy ? 1.f : fmaxf(fminf(__fdiv_rn(1.44269502f, t), 1e30f), 1e-44f);
   const f32x2 a2 = f32_pair(a, a);
-  uint2 x[kProbQuads];
+  uint2 x[kQuads];
   float m = lowest, s = 0.f, mine = lowest;
   u64 best = 0;
-  for (int k0 = q.lo; k0 < q.hi; k0 += kProbThreads * kProbQuads) {
+  const int at0 = ALIGNED ? tid : warp * 31 + lane;
+  const bool own = ALIGNED || lane < 31;
+  for (int k0 = q.lo; k0 < q.hi; k0 += kStep * kQuads) {
 #pragma unroll
-    for (int u = 0; u < kProbQuads; ++u) {
-      const int k = k0 + u * kProbThreads + tid;
+    for (int u = 0; u < kQuads; ++u) {
+      const int k = k0 + u * kStep + at0;
       x[u] = make_uint2(kNone, kNone);
-      if (!ALIGNED && k < q.hi) x[u] = load_end(row, q, k, p.vocab);
-      if (ALIGNED && q.is_whole(k)) x[u] = *reinterpret_cast<const uint2 *>(row + 4 * k - q.shift);
+      if (k >= q.whole_lo && k < q.whole_hi + (off ? 1 : 0)) x[u] = load_word(row, q, k, off);
     }
-    if (ALIGNED && ends) {
+    if (!ALIGNED) {
 #pragma unroll
-      for (int u = 0; u < kProbQuads; ++u) {
-        const int k = k0 + u * kProbThreads + tid;
+      for (int u = 0; u < kQuads; ++u) {
+        const uint2 next = make_uint2(__shfl_down_sync(kFull, x[u].x, 1), __shfl_down_sync(kFull, x[u].y, 1));
+        x[u] = own && q.is_whole(k0 + u * kStep + at0) ? from_words(x[u], next, off) : make_uint2(kNone, kNone);
+      }
+    }
+    if (ends && own) {
+#pragma unroll
+      for (int u = 0; u < kQuads; ++u) {
+        const int k = k0 + u * kStep + at0;
         if (k < q.hi && !q.is_whole(k)) x[u] = load_end(row, q, k, p.vocab);
       }
     }
     if (floor > -INFINITY) {
 #pragma unroll
-      for (int u = 0; u < kProbQuads; ++u) drop(x[u], floor);
+      for (int u = 0; u < kQuads; ++u) drop(x[u], floor);
     }
     if (greedy) {  // the thread's maximum, then the first element that is it (none: -inf)
       uint32_t top = kNone;
 #pragma unroll
-      for (int u = 0; u < kProbQuads; ++u) top = max2_nan(top, max2_nan(x[u].x, x[u].y));
+      for (int u = 0; u < kQuads; ++u) top = max2_nan(top, max2_nan(x[u].x, x[u].y));
       top = max2_nan(top, top >> 16 | top << 16);
       const uint32_t key = order_key16(top & 0xFFFFu);
       if (top != kNone && key > (uint32_t)(best >> 32)) {
         uint32_t at = 0, lo = 0, hi = 0;
 #pragma unroll
-        for (int u = kProbQuads - 1; u >= 0; --u) {
+        for (int u = kQuads - 1; u >= 0; --u) {
           const uint32_t l = same2(x[u].x, top), h = same2(x[u].y, top);
           if (l | h) {
             at = u;
@@ -204,18 +226,18 @@ __global__ void __launch_bounds__(kProbThreads, 4) probabilities_kernel(const Pr
           }
         }
         const uint32_t i = lo ? (lo & 0xFFFFu ? 0 : 1) : hi & 0xFFFFu ? 2 : 3;
-        best = (u64)key << 32 | (0xFFFFFFFFu - (uint32_t)(4 * (k0 + (int)at * kProbThreads + tid) - q.shift + (int)i));
+        best = (u64)key << 32 | (0xFFFFFFFFu - (uint32_t)(4 * (k0 + (int)at * kStep + at0) - q.shift + (int)i));
       }
       continue;
     }
     uint32_t top = kNone;
 #pragma unroll
-    for (int u = 0; u < kProbQuads; ++u) top = max2(top, max2(x[u].x, x[u].y));
+    for (int u = 0; u < kQuads; ++u) top = max2(top, max2(x[u].x, x[u].y));
     mine = fmaxf(fmaxf(bf16lo_to_f32(top), bf16hi_to_f32(top)), lowest);
     const f32x2 minus = f32_pair(-mine, -mine);
     f32x2 sum = 0;
 #pragma unroll
-    for (int u = 0; u < kProbQuads; ++u) {
+    for (int u = 0; u < kQuads; ++u) {
       const float2 v = powers(x[u].x, minus, a2), w = powers(x[u].y, minus, a2);
       sum = add2(sum, add2(f32_pair(v.x, v.y), f32_pair(w.x, w.y)));
     }
@@ -237,7 +259,7 @@ __global__ void __launch_bounds__(kProbThreads, 4) probabilities_kernel(const Pr
     cluster_wait();
     if (tid < (int)S) st_cluster_u64(mapa_shared(smem_u32(&slots[rank]), tid), best);
     cluster_arrive();
-    for (int k = q.lo + tid; k < q.hi; k += kProbThreads) store_quad<ALIGNED>(out, q, k, p.vocab, make_float2(0.f, 0.f), make_float2(0.f, 0.f));
+    for (int k = q.lo + tid; k < q.hi; k += kProbThreads) store_quad(out, q, k, p.vocab, make_float2(0.f, 0.f), make_float2(0.f, 0.f));
     cluster_wait();
     best = 0;
     for (uint32_t i = 0; i < S; ++i) best = key_max(best, slots[i]);
@@ -264,28 +286,28 @@ __global__ void __launch_bounds__(kProbThreads, 4) probabilities_kernel(const Pr
   const float inv = s == 0.f ? 0.f : __fdiv_rn(1.f, s);
   // each thread's logits are still in registers, where the slice is one chunk and the sum is a number (else a dropped
   // logit's 0 has to be told from a kept one's)
-  if (q.hi - q.lo <= kProbThreads * kProbQuads && s == s) {
+  if (q.hi - q.lo <= kStep * kQuads && s == s) {
     const f32x2 f2 = f32_pair(inv, inv), minus = f32_pair(-m, -m);
 #pragma unroll
-    for (int u = 0; u < kProbQuads; ++u) {
-      const int k = q.lo + u * kProbThreads + tid;
+    for (int u = 0; u < kQuads; ++u) {
+      const int k = q.lo + u * kStep + at0;
       const float2 v = powers(x[u].x, minus, a2), w = powers(x[u].y, minus, a2);
       const float2 a0 = f32_halves(mul2(f32_pair(v.x, v.y), f2)), b0 = f32_halves(mul2(f32_pair(w.x, w.y), f2));
-      if (ALIGNED && q.is_whole(k)) *reinterpret_cast<float4 *>(out + 4 * k - q.shift) = make_float4(a0.x, a0.y, b0.x, b0.y);
-      else if ((!ALIGNED || ends) && k < q.hi) store_end(out, q, k, p.vocab, a0, b0);
+      if (own && q.is_whole(k)) store_whole(out, q, k, a0, b0);
+      else if (ends && own && k < q.hi) store_end(out, q, k, p.vocab, a0, b0);
     }
     return;
   }
   const f32x2 minus = f32_pair(-m, -m);
   for (int k = q.lo + tid; k < q.hi; k += kProbThreads) {
-    uint2 w = load_quad<ALIGNED>(row, q, k, p.vocab);
+    uint2 w = load_quad(row, q, k, off, p.vocab);
     drop(w, floor);
     float2 v[2] = {powers(w.x, minus, a2), powers(w.y, minus, a2)};
     v[0].x = bf16lo_to_f32(w.x) == -INFINITY ? 0.f : v[0].x * inv;
     v[0].y = bf16hi_to_f32(w.x) == -INFINITY ? 0.f : v[0].y * inv;
     v[1].x = bf16lo_to_f32(w.y) == -INFINITY ? 0.f : v[1].x * inv;
     v[1].y = bf16hi_to_f32(w.y) == -INFINITY ? 0.f : v[1].y * inv;
-    store_quad<ALIGNED>(out, q, k, p.vocab, v[0], v[1]);
+    store_quad(out, q, k, p.vocab, v[0], v[1]);
   }
 }
 
@@ -612,7 +634,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 16 ? 1 : 4) tree_sample_k
 
     // this warp's part of the row
     const float *pr = p.p + row * p.p_row, *qr = p.q + row * p.q_row;
-    const int shift = ALIGNED ? (int)((row * p.p_row) & 3) : 0;
+    const int shift = ALIGNED ? (int)(reinterpret_cast<uintptr_t>(pr) >> 2 & 3) : 0;
     Quads mine(p.vocab, shift, rank * WARPS + warp, parts_log2);
     if (SINGLE && row < 0) mine.hi = mine.whole_lo = mine.whole_hi = mine.lo;  // (no token: nothing to sum, and every barrier as ever)
     const Factor factor(c);
@@ -841,15 +863,14 @@ int ctas_of(int rows, int vocab, int most, int least, int fit) {
   return s;
 }
 
-bool address(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
 }  // namespace
 
 cudaError_t launch_probabilities(const uint16_t *logits, long long row, const float *temperature, const float *floor,
                                  int tokens, int vocab, float *out, int device, int sm_count, cudaStream_t stream) {
   static PerDevice fits[2];
-  // quads of logits and of probabilities are aligned together
-  const bool aligned = address(logits, 8) && address(out, 16) && (row - vocab) % 4 == 0;
+  // quads of logits and of probabilities are aligned together (columns of a wider head, 256 x 248,319 of 248,320, are not:
+  // 92 us against 77; moved one by one they took 159)
+  const bool aligned = ((reinterpret_cast<uintptr_t>(logits) >> 1) - (reinterpret_cast<uintptr_t>(out) >> 2)) % 4 == 0 && (row - vocab) % 4 == 0;
   const ProbParams p{logits, row, temperature, floor, out, vocab};
   const int s = ctas_of(tokens, vocab, kProbThreads * kProbQuads * 4, 4096, sm_count * 4);
   return launch_rows(aligned ? probabilities_kernel<true> : probabilities_kernel<false>, fits[aligned], tokens, s,
@@ -858,7 +879,8 @@ cudaError_t launch_probabilities(const uint16_t *logits, long long row, const fl
 
 cudaError_t launch_tree_sample(const SampleCall &c) {
   static PerDevice fits[2][2][2];
-  const bool aligned = address(c.p, 16) && address(c.q, 16) && (!c.q || (c.q_row - c.p_row) % 4 == 0);
+  // quads of p and of q are aligned together (else, element by element, 8 trees of 8 over 128,000 take 26 us, not 13)
+  const bool aligned = !c.q || (((reinterpret_cast<uintptr_t>(c.p) - reinterpret_cast<uintptr_t>(c.q)) / 4) % 4 == 0 && (c.q_row - c.p_row) % 4 == 0);
   const SampleParams p{c.p, c.q, c.p_row, c.q_row, c.draft, c.mask, c.starts, c.u, c.rows, c.tokens, c.vocab, c.max_tree,
                        c.path, c.count, c.token, c.err};
   // 16 warps a CTA while every CTA has an SM to itself (a chain of six 7.5 us against 9.9 with 8), 8 where that makes more

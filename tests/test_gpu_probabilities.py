@@ -131,6 +131,25 @@ def test_strides_and_alignment(vocab):
     assert torch.allclose(w4.probabilities(one)[4], w4.probabilities(x[:1])[0], rtol=2.0 ** -17, atol=0)
 
 
+@pytest.mark.parametrize("vocab", [5, 8, 1003, 16389, 33001, 262150])
+def test_columns_of_a_wider_head(vocab):
+    """Logits that begin anywhere, against every place of out; slices of one chunk and of more, masked and greedy rows."""
+    x = logits_of(7, 6, vocab)
+    t, floor = torch.tensor([0.5, 1.0, 0.0, 2.0, 1.0, 0.0], device="cuda"), x.float().mean(1)
+    want = check(x, t), check(x, t, floor)
+    for at in range(8):
+        for width in (vocab, vocab + 1, vocab + 3, vocab + 61):
+            store = torch.full((at + 6 * width + 3,), 99.0, dtype=BF16, device="cuda")  # (99: a maximum, were it read)
+            view = store[at:at + 6 * width].view(6, width)[:, :vocab]
+            view.copy_(x)
+            room = torch.full((6 * vocab + 8,), 7.0, device="cuda")
+            out = room[at // 2:at // 2 + 6 * vocab].view(6, vocab)
+            for fl, w in zip((None, floor), want):
+                w4.probabilities(view, t, fl, out=out)
+                assert torch.allclose(out, w, rtol=2.0 ** -17, atol=0)
+                assert (room[:at // 2] == 7).all() and (room[at // 2 + 6 * vocab:] == 7).all()
+
+
 def test_streams_graphs_and_repeats():
     x = logits_of(4, 6, 30001)
     want = w4.probabilities(x)

@@ -188,6 +188,13 @@ def test_strided_rows_and_alignment():
             other[:, q_lead:q_lead + 1001] = torch.from_numpy(q).cuda()
             got = w4.tree_sample(big[:, lead:lead + 1001], other[:, q_lead:q_lead + 1001], rest[0], rest[1], starts, uu, 5)
             assert all((g.cpu().numpy() == w).all() for g, w in zip(got, want))
+    for at, q_at in ((1, 1), (2, 2), (3, 3), (1, 3), (5, 2)):  # packed rows that begin off 16 bytes
+        room = [torch.full((8 * 1001 + 8,), 9.0, device="cuda") for _ in range(2)]
+        pp, qq = (r[k:k + 8 * 1001].view(8, 1001) for r, k in zip(room, (at, q_at)))
+        pp.copy_(torch.from_numpy(p))
+        qq.copy_(torch.from_numpy(q))
+        got = w4.tree_sample(pp, qq, rest[0], rest[1], starts, uu, 5)
+        assert all((g.cpu().numpy() == w).all() for g, w in zip(got, want))
 
 
 def test_bad_indices_are_skipped_and_reported():
