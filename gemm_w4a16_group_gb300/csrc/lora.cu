@@ -1041,11 +1041,14 @@ int cluster_of(int tokens, int inner, int sm_count) {
 // Prompts: clusters at most, whatever the rows' adapters (no more groups than tokens); each has two lists
 long long most_clusters(int tokens, int groups) { return tokens / (2 * kTile) + (long long)groups + 1; }
 
+// `most`: what the kernel may need of shared memory, asked for on its first launch on a device (every time: 0.4 us)
 template <class K>
-cudaError_t launch(K kern, unsigned grid, int cluster, int smem, cudaStream_t stream, const LoraParams &p, int threads = kThreads) {
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+cudaError_t launch(K kern, PerDevice &asked, int most, int device, unsigned grid, int cluster, int smem, cudaStream_t stream,
+                   const LoraParams &p, int threads = kThreads) {
+  if (smem > 48 * 1024 && !asked.v[device].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
+    asked.v[device].store(1, std::memory_order_release);
   }
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(grid, 1, 1);
@@ -1069,10 +1072,12 @@ cudaError_t run_few(const LoraCall &c, const LoraParams &p, bool even) {
   const long long tiles = c.tokens / 16 + groups_of(c.adapters, c.rows) + 1;  // at most
   const long long shrink = tiles * p.ksplit, expand = tiles * ((c.outer + kColumns - 1) / kColumns);
   const long long cap = c.sm_count * 2;
-  const cudaError_t e = launch(lora_shrink_kernel<RP>, (unsigned)(shrink < cap ? shrink : cap), 1,
+  static PerDevice first, second[2];
+  const cudaError_t e = launch(lora_shrink_kernel<RP>, first, ShrinkGeo<RP>::smem(kMaxAdapters), c.device, (unsigned)(shrink < cap ? shrink : cap), 1,
                                ShrinkGeo<RP>::smem(c.adapters), c.stream, p);
   if (e != cudaSuccess) return e;
-  return launch(even ? lora_expand_kernel<RP, true> : lora_expand_kernel<RP, false>,
+  return launch(even ? lora_expand_kernel<RP, true> : lora_expand_kernel<RP, false>, second[even],
+                ExpandGeo<RP>::smem(kMaxAdapters), c.device,
                 (unsigned)(expand < c.sm_count * ExpandGeo<RP>::CTAS ? expand : c.sm_count * ExpandGeo<RP>::CTAS), 1, ExpandGeo<RP>::smem(c.adapters), c.stream, p);
 }
 
@@ -1080,10 +1085,12 @@ template <int RP>
 cudaError_t run_prompts(const LoraCall &c, const LoraParams &p, bool even) {
   const int cluster = cluster_of(c.tokens, c.inner, c.sm_count);
   const long long clusters = most_clusters(c.tokens, groups_of(groups_of(c.adapters, c.rows), c.tokens));
-  const cudaError_t e = launch(lora_prompt_shrink_kernel<RP>, (unsigned)(clusters * cluster), cluster,
+  static PerDevice first, second[2];
+  const cudaError_t e = launch(lora_prompt_shrink_kernel<RP>, first, PromptShrinkGeo<RP>::smem(kMaxAdapters), c.device, (unsigned)(clusters * cluster), cluster,
                                PromptShrinkGeo<RP>::smem(c.adapters), c.stream, p);
   if (e != cudaSuccess) return e;
-  return launch(even ? lora_prompt_expand_kernel<RP, false> : lora_prompt_expand_kernel<RP, true>,
+  return launch(even ? lora_prompt_expand_kernel<RP, false> : lora_prompt_expand_kernel<RP, true>, second[even],
+                PromptExpandGeo<RP>::SMEM, c.device,
                 (unsigned)c.sm_count, 1, PromptExpandGeo<RP>::SMEM, c.stream, p, PromptExpandGeo<RP>::THREADS);
 }
 
