@@ -114,6 +114,26 @@ def test_columns_of_a_wider_product():
         assert torch.equal(wide[:, beside], before[:, beside])
 
 
+@pytest.mark.parametrize("tokens", [21, 1100])
+@pytest.mark.parametrize("outer", [31, 64, 300, 513])
+def test_rows_that_begin_anywhere(tokens, outer):
+    """y and out at every place after 16 bytes, alike and not, rows of one place and of many; what is beside them stays."""
+    p = Problem([tokens - 12, 12], [0, 1], 16, 64, outer, 2, seed=outer)
+    want = p.run()
+    p.check(want)
+    y = p.y
+    for lead in range(9):
+        for extra, out_lead, out_extra in ((0, lead, 0), (8, 0, 0), (3, 5, 16), (5, 7, 2)):
+            p.y = torch.full((tokens * (outer + extra) + 16,), 9.0, dtype=torch.bfloat16, device="cuda")[
+                lead:lead + tokens * (outer + extra)].view(tokens, outer + extra)[:, :outer]
+            p.y.copy_(y)
+            room = torch.full((tokens * (outer + out_extra) + 32,), 7.0, dtype=torch.bfloat16, device="cuda")
+            out = room[out_lead:out_lead + tokens * (outer + out_extra)].view(tokens, outer + out_extra)
+            assert torch.equal(p.run(out=out[:, :outer]), want)
+            assert (out[:, outer:] == 7).all() and (room[:out_lead] == 7).all() and (room[out_lead + out.numel():] == 7).all()
+            assert torch.equal(p.run(out=p.y), want)
+
+
 def test_strided_inputs():
     p = Problem([4, 9], [1, 0], 32, 256, 200, 2)
     want = p.run()
