@@ -1072,16 +1072,26 @@ __global__ void __launch_bounds__(512, 1) lora_prompt_expand_kernel(const __grid
 // ---------------------------------------------------------------------------
 int padded_rank(int rank, bool few) { return rank <= 8 && few ? 8 : rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
 
-// Few tokens take the first pair of kernels, 16 tokens a tile, whose time goes by
-// tiles and columns; the prompts' tiles of 128 are late to begin and mostly empty
-// where many adapters share few tokens. Measured with rank 16, K 5,120, first
-// against second pair: 512 tokens of one adapter, 34,816 columns 29.8 | 30.6 us,
-// 768 51.5 | 38.5; 1,024 tokens, 7,168 columns 15.4 | 22.5; 1,024 rows of one
-// token and 48 adapters, 34,816 columns 100 | 144 (1,536: 106 | 149, 7,168 columns
-// and 2,048 tokens 46 | 58: there the second pair is kept for its smaller workspace).
-constexpr int kAlwaysFew = 512, kMostFew = 1024;
-bool few(int tokens, int outer, int groups) {
-  return tokens <= kAlwaysFew || (tokens <= kMostFew && (outer <= 8192 || tokens < 32LL * groups));
+// Few tokens take the first pair of kernels, whose tiles of 16 read their adapter
+// anew; the prompts' tiles of 128 are late to begin, and mostly empty where many
+// adapters share few tokens. First | second pair, K 5,120, one adapter:
+//   columns  tokens  rank 16     rank 64     rank 128
+//    34,816     256  14.8 | 24   20.7 | 25.5  37 | 32 us
+//    34,816     512  29.8 | 30.6 34.2 | 33.3  85 | 45
+//    34,816     768  51.5 | 38.5 54   | 41   120 | 58
+//     7,168   1,024  15.4 | 22.5 22   | 23.9
+//     7,168   2,048  29.7 | 27.6 38.6 | 29.4
+//     1,024   1,536  11.4 | 19.3 16.9 | 20.2  26 | 23
+// and 1,024 rows of one token and 48 adapters, 34,816 columns 100 | 144 with rank 16,
+// 113 | 162 with 64. So the first pair has y up to 2^24 elements and products up to
+// 2^30 of tokens, ranks and columns (above rank 64, where an SM has one CTA of
+// expand, 2^29: 1,090 tokens, K 320, 7,232 columns 36 | 26), or fewer than 32 tokens
+// an adapter.
+constexpr int kAlwaysFew = 128, kMostFew = 2048;
+bool few(const LoraCall &c, int groups) {
+  if (c.tokens <= kAlwaysFew || c.tokens > kMostFew) return c.tokens <= kAlwaysFew;
+  const long long t = c.tokens;
+  return (t * c.outer <= 1 << 24 && t * c.rank * ((long long)c.inner + c.outer) <= 1 << (c.rank > 64 ? 29 : 30)) || t < 32LL * groups;
 }
 int groups_of(int adapters, int rows) { return adapters < rows ? adapters : rows; }
 
@@ -1193,7 +1203,7 @@ cudaError_t launch_lora_add(const LoraCall &c) {
                (reinterpret_cast<uintptr_t>(c.out) - reinterpret_cast<uintptr_t>(c.y)) % 16 == 0 && (c.out_row - c.y_row) % 8 == 0 &&
                    (c.y_row >= c.outer || c.tokens == 1)};
   uint8_t *ws = static_cast<uint8_t *>(c.workspace);
-  const bool is_few = few(c.tokens, c.outer, groups_of(c.adapters, c.rows));
+  const bool is_few = few(c, groups_of(c.adapters, c.rows));
   if (is_few) {
     p.ksplit = parts_of(c.tokens, c.rank, c.inner);
     p.parts = reinterpret_cast<float *>(ws);

@@ -54,7 +54,9 @@ def test_few_tokens(rank, sizes, which, inner, outer):
     ([600], [0], 328, 515), ([300, 7, 513, 1], [1, -1, 0, 1], 1024, 264), ([65, 64, 63, 400], [0, 1, 0, 1], 96, 776),
     ([1200], [0], 328, 515), ([300, 7, 913, 1], [1, -1, 0, 1], 1024, 264), ([65, 64, 63, 1000], [0, 1, 0, 1], 96, 776),
     ([600, 80], [1, 0], 64, 8200), ([512], [1], 72, 40), ([513], [1], 72, 40), ([1023, 1], [1, 0], 72, 40), ([1024, 1], [1, 0], 72, 40),
-    ([9, 1050], [0, 1], 8, 1), ([1100], [0], 16, 130), ([3] * 350, [i % 2 for i in range(350)], 264, 140),
+    ([9, 1050], [0, 1], 8, 1), ([1100], [0], 16, 130), ([2100], [0], 328, 515), ([300, 7, 1913, 1], [1, -1, 0, 1], 1024, 264),
+    ([65, 64, 63, 2000], [0, 1, 0, 1], 96, 776), ([9, 2050], [0, 1], 8, 1), ([2047, 1], [0, 1], 72, 40), ([2048, 1], [0, 1], 72, 40), ([3] * 700, [i % 2 for i in range(700)], 264, 140),
+    ([128], [0], 64, 70000), ([129, 1], [0, 1], 64, 70000), ([100, 300], [1, 0], 8, 45001), ([3] * 350, [i % 2 for i in range(350)], 264, 140),
 ])
 def test_prompts(rank, sizes, which, inner, outer):
     p = Problem(sizes, which, rank, inner, outer, 2, seed=rank + 1)
@@ -88,7 +90,7 @@ def test_a_token_does_not_depend_on_the_others():
 
 
 def test_in_place_and_padding():
-    for sizes, which in (([3, 2, 4], [1, -1, 0]), ([200, 100, 300], [0, -1, 1]), ([400, 300, 600], [0, -1, 1])):
+    for sizes, which in (([3, 2, 4], [1, -1, 0]), ([200, 100, 300], [0, -1, 1]), ([400, 300, 600], [0, -1, 1]), ([900, 600, 800], [0, -1, 1])):
         p = Problem(sizes, which, 24, 320, 402, 2, pad=5)
         p.x[p.live:] = math.nan
         keep = p.y.clone()
@@ -114,7 +116,7 @@ def test_columns_of_a_wider_product():
         assert torch.equal(wide[:, beside], before[:, beside])
 
 
-@pytest.mark.parametrize("tokens", [21, 1100])
+@pytest.mark.parametrize("tokens", [21, 1100, 2100])
 @pytest.mark.parametrize("outer", [31, 64, 300, 513])
 def test_rows_that_begin_anywhere(tokens, outer):
     """y and out at every place after 16 bytes, alike and not, rows of one place and of many; what is beside them stays."""
@@ -164,6 +166,8 @@ def test_large_store_and_many_rows():
         p.check(p.run())
         p = Problem([1500, 0, 180], [4095, 3, 4000], rank, 16, 24, 4096)
         p.check(p.run())
+        p = Problem([2500, 0, 180], [4095, 3, 4000], rank, 16, 24, 4096)
+        p.check(p.run())
 
 
 def test_bad_indices_are_left_out_and_reported():
@@ -191,7 +195,7 @@ def test_bad_indices_are_left_out_and_reported():
 
 def test_descending_offsets_that_claim_tokens_many_times():
     """More tiles than a call of so many tokens has room for, and more tokens than 32 bits count."""
-    for tokens, rows, top in ((1400, 200, 700), (1400, 65535, 1400), (70000, 65535, 70000)):
+    for tokens, rows, top in ((1400, 200, 700), (2400, 300, 700), (2400, 65535, 2400), (70000, 65535, 70000)):
         gen = torch.Generator(device="cuda").manual_seed(rows)
         bf16 = lambda *shape: torch.randn(shape, generator=gen, device="cuda").to(torch.bfloat16)  # noqa: E731
         x, y, a, b = bf16(tokens, 16), bf16(tokens, 24), bf16(3, 8, 16), bf16(3, 24, 8)
@@ -221,7 +225,7 @@ def test_values_that_are_not_finite_stay_with_their_tokens():
     assert torch.equal(out[6:].view(torch.int16), p.y[6:].view(torch.int16))
 
 
-@pytest.mark.parametrize("tokens", [3, 1100])
+@pytest.mark.parametrize("tokens", [3, 1100, 2100])
 @pytest.mark.parametrize("rank", [8, 24, 40, 72])
 def test_an_infinite_input_times_positive_weights_is_infinite(tokens, rank):
     """Ranks are padded inside with zeros, and infinity times those would not be a number."""
@@ -233,7 +237,7 @@ def test_an_infinite_input_times_positive_weights_is_infinite(tokens, rank):
 
 
 def test_streams_graphs_and_repeats():
-    for sizes, which in (([3, 1, 4], [0, 1, 0]), ([300, 300], [0, 1]), ([700, 400], [0, 1])):
+    for sizes, which in (([3, 1, 4], [0, 1, 0]), ([300, 300], [0, 1]), ([700, 400], [0, 1]), ([1700, 400], [0, 1])):
         p = Problem(sizes, which, 32, 512, 1000, 2)
         want = p.run()
         side = torch.cuda.Stream()

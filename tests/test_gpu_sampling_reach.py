@@ -54,7 +54,7 @@ def test_probabilities_far_apart_and_many():
     assert float(got[8600, 0]) == float(got[8600, vocab - 1]) == np.float32(1) / np.float32(vocab)
 
 
-@pytest.mark.parametrize("rows,each,far", [(2, 3, 1 << 29), (4, 275, (1 << 21) + 8), (3, 350, (1 << 21) + 5)])
+@pytest.mark.parametrize("rows,each,far", [(2, 3, 1 << 29), (4, 275, (1 << 21) + 8), (3, 350, (1 << 21) + 5), (4, 520, (1 << 20) + 8), (3, 700, (1 << 20) + 5)])
 def test_adapters_and_rows_far_apart(rows, each, far):
     """Tokens, adapters and columns of B past 2^31 elements, in place (few tokens, prompts, rows off 16 bytes)."""
     tokens, inner, outer, rank, store = rows * each, 64, 136, 16, 5
@@ -75,15 +75,15 @@ def test_adapters_and_rows_far_apart(rows, each, far):
 
 
 def test_values_that_are_not_finite_stay_with_their_tokens_in_prompts():
-    tokens, inner, outer = 1500, 128, 200
+    tokens, inner, outer = 2500, 128, 200
     gen = torch.Generator(device="cuda").manual_seed(0)
     bf16 = lambda *shape: torch.randn(shape, generator=gen, device="cuda").to(torch.bfloat16)  # noqa: E731
     x, y, a, b = bf16(tokens, inner), bf16(tokens, outer), bf16(2, 16, inner), bf16(2, outer, 16)
-    x[3, 5], x[1300, 7] = math.inf, math.nan  # the second belongs to a row without an adapter
+    x[3, 5], x[2300, 7] = math.inf, math.nan  # the second belongs to a row without an adapter
     y[705, 9] = math.nan
     a[1, 2, 3] = math.nan
     adapter = torch.tensor([0, 1, -1], dtype=torch.int32, device="cuda")
-    starts = torch.tensor([0, 700, 1200, 1500], dtype=torch.int32, device="cuda")
+    starts = torch.tensor([0, 700, 1200, 2500], dtype=torch.int32, device="cuda")
     out = w4.lora_add(y, x, a, b, adapter, starts)
     assert out[:3].isfinite().all() and out[4:700].isfinite().all() and not out[3].isfinite().any()
     assert out[700:1200].isnan().all()
@@ -119,7 +119,7 @@ def test_two_threads_on_one_stream():
     bf16 = lambda *shape: torch.randn(shape, generator=gen, device="cuda").to(torch.bfloat16)  # noqa: E731
     a, b = bf16(3, 32, 512), bf16(3, 768, 32)
     jobs = []
-    for sizes in ((1, 4, 9), (700, 600, 50)):
+    for sizes in ((1, 4, 9), (1700, 600, 50)):
         n, starts = sum(sizes), torch.tensor(np.cumsum((0,) + sizes), dtype=torch.int32, device="cuda")
         y, x, adapter = bf16(n, 768), bf16(n, 512), torch.tensor([2, 0, 1], dtype=torch.int32, device="cuda")
         p, u, draft = soft((n, 300), 1), torch.rand(n, generator=gen, device="cuda"), torch.randint(0, 300, (n,), generator=gen, device="cuda")
