@@ -1084,14 +1084,14 @@ int padded_rank(int rank, bool few) { return rank <= 8 && few ? 8 : rank <= 16 ?
 //     1,024   1,536  11.4 | 19.3 16.9 | 20.2  26 | 23
 // and 1,024 rows of one token and 48 adapters, 34,816 columns 100 | 144 with rank 16,
 // 113 | 162 with 64. So the first pair has y up to 2^24 elements and products up to
-// 2^30 of tokens, ranks and columns (above rank 64, where an SM has one CTA of
-// expand, 2^29: 1,090 tokens, K 320, 7,232 columns 36 | 26), or fewer than 32 tokens
-// an adapter.
+// 2^30 of tokens, ranks and K + columns (above rank 64, where an SM has one CTA of
+// expand, K + 2 columns: 1,090 tokens, K 320, 7,232 columns 36 | 26, but 515 tokens, K
+// 7,248, 2,854 columns 23 | 30), or fewer than 32 tokens an adapter.
 constexpr int kAlwaysFew = 128, kMostFew = 2048;
 bool few(const LoraCall &c, int groups) {
   if (c.tokens <= kAlwaysFew || c.tokens > kMostFew) return c.tokens <= kAlwaysFew;
-  const long long t = c.tokens;
-  return (t * c.outer <= 1 << 24 && t * c.rank * ((long long)c.inner + c.outer) <= 1 << (c.rank > 64 ? 29 : 30)) || t < 32LL * groups;
+  const long long t = c.tokens, columns = c.rank > 64 ? 2LL * c.outer : c.outer;
+  return (t * c.outer <= 1 << 24 && t * c.rank * (c.inner + columns) <= 1 << 30) || t < 32LL * groups;
 }
 int groups_of(int adapters, int rows) { return adapters < rows ? adapters : rows; }
 
