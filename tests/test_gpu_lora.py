@@ -64,6 +64,25 @@ def test_prompts(rank, sizes, which, inner, outer):
     assert w4.kernel_status() == 0
 
 
+@pytest.mark.parametrize("rank", [8, 16, 24, 64, 128])
+@pytest.mark.parametrize("tokens", [1, 17, 128])
+def test_few_tokens_keep_all_bits_between_the_products(tokens, rank):
+    """x A^T next to the middle of two bf16 values: 1 + m 2^-7 + 2^-8 and 2^-k more or less, which is exact in float32, as are
+    all sums here (B has one 1 a column). So the output is that value, rounded once."""
+    rng = np.random.default_rng(rank)
+    base, by = rng.integers(0, 128, rank), 2.0 ** -rng.integers(12, 22, rank) * rng.choice([-1, 1], rank)
+    a = np.zeros((1, rank, 64))
+    a[0, :, 3], a[0, :, 40], a[0, :, 9] = 1 + base / 128, 2.0 ** -8, by
+    want = torch.from_numpy(a.sum(2)).to(torch.bfloat16)
+    up = np.where(by > 0, base + 1, base)
+    assert np.array_equal(want.double().numpy()[0], 1 + up / 128)
+    a = torch.from_numpy(a).to(torch.bfloat16).cuda()
+    x, y = torch.ones((tokens, 64), dtype=torch.bfloat16, device="cuda"), torch.zeros((tokens, rank), dtype=torch.bfloat16, device="cuda")
+    b = torch.eye(rank, dtype=torch.bfloat16, device="cuda")[None].contiguous()
+    out = w4.lora_add(y, x, a, b, torch.zeros(tokens, dtype=torch.int32, device="cuda"))
+    assert torch.equal(out.cpu(), want.expand(tokens, rank))
+
+
 @pytest.mark.parametrize("sizes,which,rank,inner,outer,store", [
     ([1], [3], 16, 5120, 5120, 8), ([1] * 48, [i % 12 for i in range(48)], 64, 5120, 2049, 12), ([8, 3, 1, 5], [0, 1, -1, 0], 32, 17408, 640, 2),
 ])
