@@ -40,6 +40,11 @@ struct Quads {
     return whole_hi < hi && hi - 1 >= whole_lo ? hi - 1 : -1;
   }
   __device__ __forceinline__ bool is_whole(int k) const { return k >= whole_lo && k < whole_hi; }
+  // where quads begin `off` elements after words of four: the words that hold some of the whole quads, each of which has an
+  // element of the row (without a whole quad there is none, and the word at whole_hi may be past the row)
+  __device__ __forceinline__ bool in_word(int k, int off) const {
+    return k >= whole_lo && k < whole_hi + (off && whole_lo < whole_hi ? 1 : 0);
+  }
 };
 
 // ---------------------------------------------------------------------------
@@ -188,7 +193,7 @@ __global__ void __launch_bounds__(kProbThreads, 4) probabilities_kernel(const Pr
     for (int u = 0; u < kQuads; ++u) {
       const int k = k0 + u * kStep + at0;
       x[u] = make_uint2(kNone, kNone);
-      if (k >= q.whole_lo && k < q.whole_hi + (off ? 1 : 0)) x[u] = load_word(row, q, k, off);
+      if (q.in_word(k, off)) x[u] = load_word(row, q, k, off);
     }
     if (!ALIGNED) {
 #pragma unroll

@@ -150,6 +150,25 @@ def test_columns_of_a_wider_head(vocab):
                 assert (room[:at // 2] == 7).all() and (room[at // 2 + 6 * vocab:] == 7).all()
 
 
+@pytest.mark.parametrize("vocab", [1, 2, 3, 4])
+def test_a_few_columns_of_a_wider_head(vocab):
+    """Rows without a whole quad, at every place of logits and out."""
+    x = logits_of(vocab, 6, vocab)
+    t = torch.tensor([0.5, 1.0, 0.0, 2.0, 1.0, 0.0], device="cuda")
+    want, _ = reference(x, t)
+    for at in range(8):
+        for width in (vocab, vocab + 1, vocab + 2, vocab + 3, vocab + 4):
+            store = torch.full((at + 6 * width + 3,), 99.0, dtype=BF16, device="cuda")
+            view = store[at:at + 6 * width].view(6, width)[:, :vocab]
+            view.copy_(x)
+            for lead in range(4):
+                room = torch.full((6 * vocab + 8,), 7.0, device="cuda")
+                out = room[lead:lead + 6 * vocab].view(6, vocab)
+                check(view, t, out=out)
+                assert (room[:lead] == 7).all() and (room[lead + 6 * vocab:] == 7).all()
+                assert torch.equal(out.double().cpu().argmax(1), want.argmax(1))
+
+
 def test_streams_graphs_and_repeats():
     x = logits_of(4, 6, 30001)
     want = w4.probabilities(x)
