@@ -105,23 +105,98 @@ __device__ __forceinline__ int row_adapter(const LoraParams &p, int b) {
   return p.adapters;
 }
 
+// Offsets that descend: the tokens of row b that lie behind the ends of all rows before it, `end` the largest end before the
+// block's rows: first one, how many, and the largest end so far. (All threads call it, in the rows' order.) Whatever the
+// offsets, no token is counted twice so, and there are no more tiles than of ascending ones.
+__device__ int4 tokens_behind(const LoraParams &p, int b, int end, int *sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int first = 0;
+  bool known;
+  int n = b < p.rows ? row_tokens(p, b, first, known) : 0;
+  const int mine = n ? first + n : 0;
+  int upto = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(kFull, upto, o);
+    if (lane >= o) upto = max(upto, t);
+  }
+  __syncthreads();
+  if (lane == 31) sums[warp] = upto;
+  const int left = __shfl_up_sync(kFull, upto, 1);
+  int before = lane ? max(end, left) : end;
+  __syncthreads();
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before = max(before, sums[w]);
+    end = max(end, sums[w]);
+  }
+  __syncthreads();
+  if (n && first < before) {
+    n = max(mine - before, 0);
+    first = before;
+  }
+  return make_int4(first, n, end, 0);
+}
+
+// The adapters' counts of tokens, and the tokens of row threadIdx.x, where offsets descend; order[1] gets the largest end of
+// the block's first rows. (Out of line, as the next: in line they cost registers, up to 2 us of 24.)
+__device__ __noinline__ int2 count_again(const LoraParams &p, int *count, int *sums, int *order) {
+  for (int e = threadIdx.x; e <= p.adapters; e += kThreads) count[e] = 0;
+  int2 mine = make_int2(0, 0);
+  int end = 0;
+  for (int b0 = 0; b0 < p.rows; b0 += kThreads) {
+    const int4 row = tokens_behind(p, b0 + threadIdx.x, end, sums);
+    end = row.z;
+    if (row.y) atomicAdd(&count[row_adapter(p, b0 + threadIdx.x)], row.y);
+    if (b0 == 0) {
+      mine = make_int2(row.x, row.y);
+      if (threadIdx.x == 0) order[1] = end;
+    }
+  }
+  __syncthreads();
+  return mine;
+}
+
+// As Tiles::tokens, for the rows from kThreads on; `done` of the adapter's tokens are in rows before those
+__device__ __noinline__ void tokens_of_more_rows(const LoraParams &p, int e, int lo, int hi, int *list, int done, int *sums,
+                                                 const int *order) {
+  const bool descend = order[0];
+  int end = descend ? order[1] : 0;
+  bool known;
+  for (int b0 = kThreads; b0 < p.rows && done < hi; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    int s = 0, n = 0, total;
+    if (descend) {
+      const int4 row = tokens_behind(p, b, end, sums);
+      s = row.x;
+      n = row.y && row_adapter(p, b) == e ? row.y : 0;
+      end = row.z;
+    } else if (b < p.rows && row_adapter(p, b) == e) {
+      n = row_tokens(p, b, s, known);
+    }
+    __syncthreads();
+    const int at = done + block_scan(n, sums, total);
+    for (int i = max(lo, at); i < min(hi, at + n); ++i) list[i - lo] = s + i - at;
+    done += total;
+  }
+}
+
 // The tiles of a call, T tokens of one adapter each: count[e] tokens of adapter
 // e (the last bin: of none), tiles first[e] .. first[e + 1].
 struct Tiles {
   int *count, *first, *sums;
+  int *order;  // whether some row's offsets cannot be (the others may descend then), and the largest end of the block's first rows
   int bins;
   int mine, mine_at, mine_n;  // adapter, first token and number of tokens of row threadIdx.x (the block's first pass over the rows)
-  bool bad;  // a row of this thread's has offsets that cannot be
 
-  static __host__ __device__ int ints(int adapters) { return 2 * adapters + 3 + kWarps; }
+  static __host__ __device__ int ints(int adapters) { return 2 * adapters + 5 + kWarps; }
   __device__ Tiles(int *mem, int adapters)
-      : count(mem), first(mem + adapters + 1), sums(mem + 2 * adapters + 3), bins(adapters + 1) {}
+      : count(mem), first(mem + adapters + 1), sums(mem + 2 * adapters + 3), order(mem + 2 * adapters + 3 + kWarps), bins(adapters + 1) {}
 
   template <int T>
   __device__ void make(const LoraParams &p) {
     mine = -1;
     mine_at = mine_n = 0;
-    bad = false;
+    bool bad = false;
+    if (threadIdx.x == 0) order[0] = 0;
     if ((int)threadIdx.x < p.rows) {
       mine = row_adapter(p, threadIdx.x);
       mine_n = row_tokens(p, threadIdx.x, mine_at, bad);
@@ -134,7 +209,13 @@ struct Tiles {
       const int n = row_tokens(p, b, s, bad);
       if (n) atomicAdd(&count[row_adapter(p, b)], n);
     }
+    if (bad) order[0] = 1;
     __syncthreads();
+    if (order[0]) {
+      const int2 row = count_again(p, count, sums, order);
+      mine_at = row.x;
+      mine_n = row.y;
+    }
     const int each = (bins + kThreads - 1) / kThreads, e0 = threadIdx.x * each, e1 = min(e0 + each, bins);
     int n = 0, total;
     for (int e = e0; e < e1; ++e) n += (count[e] + T - 1) / T;
@@ -160,20 +241,10 @@ struct Tiles {
 
   // Tokens lo .. hi of adapter e, in the rows' order, into list (all threads)
   __device__ void tokens(const LoraParams &p, int e, int lo, int hi, int *list) const {
-    int done = 0;
-    bool known;
-    for (int b0 = 0; b0 < p.rows && done < hi; b0 += kThreads) {
-      int s = mine_at, n = mine == e ? mine_n : 0, total;
-      if (b0) {
-        const int b = b0 + threadIdx.x;
-        n = 0;
-        if (b < p.rows && row_adapter(p, b) == e) n = row_tokens(p, b, s, known);
-        __syncthreads();
-      }
-      const int at = done + block_scan(n, sums, total);
-      for (int i = max(lo, at); i < min(hi, at + n); ++i) list[i - lo] = s + i - at;
-      done += total;
-    }
+    int total;
+    const int n = mine == e ? mine_n : 0, at = block_scan(n, sums, total);
+    for (int i = max(lo, at); i < min(hi, at + n); ++i) list[i - lo] = mine_at + i - at;
+    if (total < hi && p.rows > kThreads) tokens_of_more_rows(p, e, lo, hi, list, total, sums, order);
     __syncthreads();
   }
 };
@@ -278,7 +349,9 @@ struct ExpandGeo {
   static constexpr int ROW = RP < 32 ? RP * 2 : RP == 32 ? 64 : RP * 2 + 64;  // bytes of a token's t, without bank conflicts
   static constexpr int CPR = RP / 8;                // 16-byte pieces of a row of B
   static constexpr int SLOT = 32 * RP * 2, SLOTS = RP <= 16 ? 8 : RP == 32 ? 3 : 2;
-  static constexpr int CTAS = RP <= 16 ? 2 : RP <= 64 ? 3 : 1;  // per SM
+  // CTAs per SM. Rank 64 with rows off 16 bytes does not fit a third of the registers (48 tokens of 12 adapters, 34,813 columns
+  // with 3 25.8 us, 2 25.0; 69 of 6, 5,121 columns 16.1 | 14.9)
+  static constexpr int ctas(bool even) { return RP <= 16 ? 2 : RP < 64 || (RP == 64 && even) ? 3 : RP == 64 ? 2 : 1; }
   static constexpr int PART = 16 * ROW, OFF_RING = 3 * PART, OFF_LIST = OFF_RING + kWarps * SLOTS * SLOT;
   static constexpr int OFF_TILES = OFF_LIST + 16 * 4;
   static int smem(int adapters) { return OFF_TILES + Tiles::ints(adapters) * 4; }
@@ -415,7 +488,7 @@ __device__ __forceinline__ void store_across(uint16_t *at, int t, uint4 v, bool 
 }
 
 template <int RP, bool EVEN>
-__global__ void __launch_bounds__(kThreads, ExpandGeo<RP>::CTAS) lora_expand_kernel(const __grid_constant__ LoraParams p) {
+__global__ void __launch_bounds__(kThreads, ExpandGeo<RP>::ctas(EVEN)) lora_expand_kernel(const __grid_constant__ LoraParams p) {
   using G = ExpandGeo<RP>;
   extern __shared__ __align__(16) uint8_t smem[];
   int *list = reinterpret_cast<int *>(smem + G::OFF_LIST);
@@ -618,12 +691,10 @@ __global__ void __launch_bounds__(kThreads, 2) lora_prompt_shrink_kernel(const _
   grid_dependency_wait();
   grid_launch_dependents();
   tiles.make<2 * kTile>(p);
-  // Rows share no tokens, so there are as many clusters as tiles and more. Offsets that descend may claim tokens many
-  // times over: then there are no more tiles than lists, and none where their number may not have fitted 32 bits.
-  const bool wrapped = __syncthreads_or(tiles.bad) && (long long)p.rows * p.tokens >= 1ll << 31;
-  const int all = wrapped ? 0 : min(tiles.first[p.adapters + 1], (int)gridDim.x / parts);
+  // No token is counted twice, so there are as many clusters (and lists) as tiles, and more
+  const int all = tiles.first[p.adapters + 1];
   if (tile == 0 && part == 0 && threadIdx.x == 0) {
-    p.head[0] = 2 * min(tiles.first[p.adapters], all);
+    p.head[0] = 2 * tiles.first[p.adapters];
     p.head[1] = 2 * all;
   }
   if (tile >= all) return;  // (all CTAs of the cluster do, here and below)
@@ -1170,7 +1241,7 @@ cudaError_t run_few(const LoraCall &c, const LoraParams &p, bool even) {
   if (e != cudaSuccess) return e;
   return launch(even ? lora_expand_kernel<RP, true> : lora_expand_kernel<RP, false>, second[even],
                 ExpandGeo<RP>::smem(kMaxAdapters), c.device,
-                (unsigned)(expand < c.sm_count * ExpandGeo<RP>::CTAS ? expand : c.sm_count * ExpandGeo<RP>::CTAS), 1, ExpandGeo<RP>::smem(c.adapters), c.stream, p);
+                (unsigned)(expand < c.sm_count * ExpandGeo<RP>::ctas(even) ? expand : c.sm_count * ExpandGeo<RP>::ctas(even)), 1, ExpandGeo<RP>::smem(c.adapters), c.stream, p);
 }
 
 template <int RP>

@@ -566,8 +566,9 @@ int w4a16_kv_reserve(int32_t *page_table, int max_pages, int table_rows, int32_t
  * its sums, and those 16 bits). What is not finite stays with its token, or with its adapter and
  * column. Tokens at starts[rows] and above are not read
  * and not written. An adapter outside -1 .. adapters - 1 counts as -1, a row whose
- * offsets cannot be is left out (what a token gets that descending offsets give to
- * several rows is not defined); w4a16_kernel_status() then returns W4A16_ERR_INDEX.
+ * offsets cannot be is left out, and where offsets descend, tokens of a row that lie
+ * before the end of an earlier one are that one's, or nobody's (then they are not
+ * written); w4a16_kernel_status() then returns W4A16_ERR_INDEX.
  * ------------------------------------------------------------------------ */
 #define W4A16_MAX_ADAPTERS 4096
 #define W4A16_MAX_RANK 128

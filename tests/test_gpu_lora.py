@@ -232,6 +232,44 @@ def test_descending_offsets_that_claim_tokens_many_times():
             y.copy_(before)
 
 
+def swapped(rows, each):
+    """Offsets of `rows` rows, some of which have changed places with the next."""
+    starts = np.arange(rows + 1) * each
+    for i in (3, 255, 256, 300, rows - 2):
+        starts[[i, i + 1]] = starts[[i + 1, i]]
+    return starts.tolist()
+
+
+@pytest.mark.parametrize("tokens,starts", [
+    (9, [0, 5, 2, 9]), (9, [4, 9, 0, 6]), (40, [0, 10, 30, 20, 40, 35, 40]), (600, [0, 400, 100, 500, 300, 600]),
+    (900, swapped(450, 2)), (2100, swapped(700, 3)), (4000, [0, 2000, 500, 4000]), (4000, [0, 1500, 4001, 1500, 4000]),
+    (70000, [0, 30000, 70000, 70001] + [70000] * 65000),
+])
+@pytest.mark.parametrize("rank", [8, 32])
+def test_offsets_in_no_order_cost_only_their_own_rows(tokens, starts, rank):
+    """Every token goes with the first sound row that reaches it from behind all earlier ends, and no other is written."""
+    gen = torch.Generator().manual_seed(tokens)
+    x, y, a, b = stored(gen, tokens, 16), stored(gen, tokens, 24), stored(gen, 3, rank, 16, std=0.25), stored(gen, 3, 24, rank, std=0.3)
+    adapter = torch.arange(len(starts) - 1) % 3 if len(starts) < 1000 else torch.arange(len(starts) - 1) % 2 + 1
+    owner, end = [-2] * tokens, 0
+    for s, t, e in zip(starts, starts[1:], adapter.tolist()):
+        if 0 <= s < t <= tokens:
+            for i in range(max(s, end), t):
+                owner[i] = e
+            end = max(end, t)
+    written = torch.tensor([e >= 0 for e in owner])
+    want, bound = adapted(y, x, a, b, owner, None)
+    x, y, a, b = (v.cuda() for v in (x, y, a, b))
+    args = x, a, b, adapter.int().cuda(), torch.tensor(starts, dtype=torch.int32, device="cuda")
+    out = w4.lora_add(y, *args, out=torch.full_like(y, 5.0))
+    assert w4.kernel_status() == -6
+    assert ((out.double().cpu() - want).abs() <= bound)[written].all() and (out.cpu()[~written] == 5).all()
+    before = y.clone()
+    w4.lora_add(y, *args, out=y)
+    assert w4.kernel_status() == -6
+    assert torch.equal(y.cpu()[written], out.cpu()[written]) and torch.equal(y.cpu()[~written], before.cpu()[~written])
+
+
 def test_values_that_are_not_finite_stay_with_their_tokens():
     p = Problem([3, 3, 3], [0, 1, -1], 16, 256, 128, 2)
     p.x[1, 5], p.x[7, 5] = math.inf, math.nan  # the second belongs to a row without an adapter
