@@ -44,7 +44,7 @@ struct LoraParams {
   int rows, tokens, adapters, rank, inner, outer, ksplit;
   uint16_t *out;
   float *parts;  // few tokens: x A^T in parts, [ksplit][tokens][RP]
-  // prompts: x A^T as two bf16 parts, [tokens][2][RP]; how many tiles there are (with an adapter, in all); the tiles
+  // prompts: x A^T in its bf16 parts, [tokens][parts][RP]; how many tiles there are (with an adapter, in all); the tiles
   uint16_t *low;
   int *head, *lists;
   int *err;
@@ -385,27 +385,25 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t *>(&b);
 }
-// Two values as two bf16 parts each (16 bits of mantissa): the upper ones, and
-// what they leave. (What an infinite value leaves is not a number: 0.)
-__device__ __forceinline__ uint2 two_parts(float a, float b) {
-  const uint32_t hi = pack_bf16(a, b);
-  const float x = bf16lo_to_f32(hi), y = bf16hi_to_f32(hi);
-  return make_uint2(hi, pack_bf16(fabsf(x) < INFINITY ? a - x : 0.f, fabsf(y) < INFINITY ? b - y : 0.f));
-}
-
 // The upper 16 bits of a value, as a bf16 value: cut, not rounded, and one step less where nothing would be left below. So
 // what is left is not 0 and has the same sign, and an infinite weight times the parts of a value is infinite, not inf - inf or
 // 0 inf. (Of infinity it is the largest bf16 value, and infinity is left.)
 __device__ __forceinline__ uint32_t upper_bits(float a) { return __float_as_uint(a) - (a != 0.f ? 1 : 0) & 0xFFFF0000u; }
-// Two values as three bf16 parts each, whose sum is the value
-__device__ __forceinline__ void three_parts(float a, float b, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
-  const uint32_t a0 = upper_bits(a), b0 = upper_bits(b);
-  a -= __uint_as_float(a0);
-  b -= __uint_as_float(b0);
-  const uint32_t a1 = upper_bits(a), b1 = upper_bits(b);
-  hi = __byte_perm(a0, b0, 0x7632);
-  mid = __byte_perm(a1, b1, 0x7632);
-  lo = pack_bf16(a - __uint_as_float(a1), b - __uint_as_float(b1));
+// Two values as bf16 parts each: three, whose sum is the value, or two, off by 2^-16 of it at most
+__device__ __forceinline__ void in_parts(float a, float b, uint32_t (&part)[3]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t x = upper_bits(a), y = upper_bits(b);
+    part[i] = __byte_perm(x, y, 0x7632);
+    a -= __uint_as_float(x);
+    b -= __uint_as_float(y);
+  }
+  part[2] = pack_bf16(a, b);
+}
+__device__ __forceinline__ void in_parts(float a, float b, uint32_t (&part)[2]) {
+  const uint32_t x = upper_bits(a), y = upper_bits(b);
+  part[0] = __byte_perm(x, y, 0x7632);
+  part[1] = pack_bf16(a - __uint_as_float(x), b - __uint_as_float(y));
 }
 
 // Eight columns of a row from column c on, `wide`: as one 16-byte access
@@ -590,8 +588,10 @@ __global__ void __launch_bounds__(kThreads, ExpandGeo<RP>::ctas(EVEN)) lora_expa
           v.y += u.y;
         }
         if (r >= p.rank) v = make_float2(0.f, 0.f);  // (an infinite x times the padding's zeros is not a number)
-        uint32_t *to = reinterpret_cast<uint32_t *>(smem + row * G::ROW + r * 2);
-        three_parts(v.x * scale, v.y * scale, to[0], to[G::PART / 4], to[2 * G::PART / 4]);
+        uint32_t part[3];
+        in_parts(v.x * scale, v.y * scale, part);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) *reinterpret_cast<uint32_t *>(smem + k * G::PART + row * G::ROW + r * 2) = part[k];
       }
       __syncthreads();
     }
@@ -655,8 +655,11 @@ __global__ void __launch_bounds__(kThreads, ExpandGeo<RP>::ctas(EVEN)) lora_expa
 // tcgen05 products (128 tokens by RP ranks, sums in TMEM): the warps only copy.
 // (With mma.sync, whose fragments come from shared memory, six prompts of rank 64
 // took 33 us here.) The parts of the sums meet over distributed shared memory, and
-// x A^T is written once, in its two bf16 parts.
+// x A^T is written once, in its bf16 parts: three up to rank 32, two above, where the products of the third would show (4,096
+// tokens, 34,816 columns, two | three parts: rank 16 117.2 | 118.1 us, 32 119.8 | 122.9, 64 126.8 | 136.1, 128 203 | 231; six
+// prompts of rank 64 74 | 80).
 // ---------------------------------------------------------------------------
+__host__ __device__ constexpr int parts_of_rank(int padded) { return padded <= 32 ? 3 : 2; }
 constexpr int kTile = 64;       // tokens of a list
 constexpr int kListInts = 68;   // a tile's tokens, adapter and number of tokens
 
@@ -816,10 +819,13 @@ __global__ void __launch_bounds__(kThreads, 2) lora_prompt_shrink_kernel(const _
       v.w += u.w;
     }
     if (r >= p.rank) v = make_float4(0.f, 0.f, 0.f, 0.f);  // (an infinite x times the padding's zeros is not a number)
-    const uint2 a = two_parts(v.x * scale, v.y * scale), b = two_parts(v.z * scale, v.w * scale);
-    uint16_t *out = p.low + (long long)list[row] * (2 * RP) + r;
-    *reinterpret_cast<uint2 *>(out) = make_uint2(a.x, b.x);
-    *reinterpret_cast<uint2 *>(out + RP) = make_uint2(a.y, b.y);
+    constexpr int P = parts_of_rank(RP);
+    uint32_t a[P], b[P];
+    in_parts(v.x * scale, v.y * scale, a);
+    in_parts(v.z * scale, v.w * scale, b);
+    uint16_t *out = p.low + (long long)list[row] * (P * RP) + r;
+#pragma unroll
+    for (int k = 0; k < P; ++k) *reinterpret_cast<uint2 *>(out + k * RP) = make_uint2(a[k], b[k]);
   }
   cluster_sync_all();  // (the others may still be reading this CTA's part)
 }
@@ -845,8 +851,8 @@ __device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&v)[16
 
 // ---------------------------------------------------------------------------
 // expand: a step is 128 tokens of one adapter and NC columns. x A^T of the
-// tokens stays in shared memory (both parts side by side, so that one row of B
-// serves the two), B comes for each step, the product is tcgen05's, 128 by NC, in
+// tokens stays in shared memory (its parts side by side, so that one row of B
+// serves all), B comes for each step, the product is tcgen05's, 128 by NC, in
 // one of two TMEM buffers. y is copied to shared memory two steps ahead; the
 // products are added there in place, and a step later the sums leave in whole
 // rows. Bound by HBM, which does 6.0 - 6.2 TB/s of such rows read and written (64
@@ -862,7 +868,8 @@ template <int RP>
 struct PromptExpandGeo {
   static constexpr int THREADS = 512;
   static constexpr int NC = RP <= 64 ? 128 : 64;
-  static constexpr int A_PANELS = (2 * RP + 63) / 64, A = A_PANELS * 128 * 128;  // of 64 k, rows of 128 bytes, swizzled
+  static constexpr int A_ROW = parts_of_rank(RP) * RP;  // k of a token's x A^T
+  static constexpr int A_PANELS = (A_ROW + 63) / 64, A = A_PANELS * 128 * 128;  // of 64 k, rows of 128 bytes, swizzled
   static constexpr int B_PANELS = (RP + 63) / 64, B_PANEL = NC * 128, B = B_PANELS * B_PANEL;
   static constexpr int PITCH = NC * 2 + 16;  // bytes of a token's y: NC places and up to 7 more, without bank conflicts
   static constexpr int OUT = 128 * PITCH;
@@ -923,10 +930,10 @@ __global__ void __launch_bounds__(512, 1) lora_prompt_expand_kernel(const __grid
   auto fetch_a = [&](int tile) {  // x A^T of a tile
     const int n = tokens_of(tile);
 #pragma unroll 4
-    for (int id = threadIdx.x; id < 128 * RP / 4; id += G::THREADS) {
-      const int r = id / (RP / 4), c = id % (RP / 4);
+    for (int id = threadIdx.x; id < 128 * G::A_ROW / 8; id += G::THREADS) {
+      const int r = id / (G::A_ROW / 8), c = id % (G::A_ROW / 8);
       if (r < n)
-        copy16(base + c / 8 * 128 * 128 + r * 128 + ((c % 8 ^ (r & 7)) << 4), p.low + (long long)token_of(tile, r) * (2 * RP) + c * 8);
+        copy16(base + c / 8 * 128 * 128 + r * 128 + ((c % 8 ^ (r & 7)) << 4), p.low + (long long)token_of(tile, r) * G::A_ROW + c * 8);
     }
   };
   auto fetch_b = [&](const Step &s) {
@@ -1032,7 +1039,7 @@ __global__ void __launch_bounds__(512, 1) lora_prompt_expand_kernel(const __grid
       constexpr uint32_t idesc = idesc_bf16_f32(128, G::NC);
       const uint32_t b = base + G::OFF_B + s.i % 3 * G::B, d = tmem + (issued & 1) * G::NC;
 #pragma unroll
-      for (int part = 0; part < 2; ++part)
+      for (int part = 0; part < parts_of_rank(RP); ++part)
 #pragma unroll
         for (int k = 0; k < RP; k += 16) {
           const int ka = part * RP + k;
@@ -1201,6 +1208,12 @@ int cluster_of(int tokens, int inner, int sm_count) {
   return s;
 }
 
+// Prompts: x A^T, after the numbers of tiles
+size_t low_bytes(int tokens, int rank) {
+  const int padded = padded_rank(rank, false);
+  return align_up((size_t)tokens * padded * parts_of_rank(padded) * sizeof(uint16_t), 256);
+}
+
 // Prompts: clusters at most, whatever the rows' adapters (no more groups than tokens); each has two lists
 long long most_clusters(int tokens, int groups) { return tokens / (2 * kTile) + (long long)groups + 1; }
 
@@ -1276,7 +1289,7 @@ size_t lora_workspace_bytes(int tokens, int rank, int inner) {
   size_t bytes = align_up(sums * padded_rank(rank, true) * sizeof(float), 256);
   if (tokens > kAlwaysFew) {
     const size_t lists = (size_t)most_clusters(tokens, groups_of(kMaxAdapters, tokens)) * 2 * kListInts * sizeof(int);
-    const size_t prompts = 256 + align_up((size_t)tokens * padded_rank(rank, false) * 4, 256) + align_up(lists, 256);
+    const size_t prompts = 256 + low_bytes(tokens, rank) + align_up(lists, 256);
     if (prompts > bytes) bytes = prompts;
   }
   return bytes;
@@ -1296,7 +1309,7 @@ cudaError_t launch_lora_add(const LoraCall &c) {
   } else {
     p.head = reinterpret_cast<int *>(ws);
     p.low = reinterpret_cast<uint16_t *>(ws + 256);
-    p.lists = reinterpret_cast<int *>(ws + 256 + align_up((size_t)c.tokens * padded_rank(c.rank, false) * 4, 256));
+    p.lists = reinterpret_cast<int *>(ws + 256 + low_bytes(c.tokens, c.rank));
   }
   const uintptr_t bits = reinterpret_cast<uintptr_t>(c.y) | reinterpret_cast<uintptr_t>(c.out);
   const bool even = bits % 16 == 0 && c.y_row % 8 == 0 && c.out_row % 8 == 0;

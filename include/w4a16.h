@@ -559,9 +559,9 @@ int w4a16_kv_reserve(int32_t *page_table, int max_pages, int table_rows, int32_t
  *              two launches that share it. (The size grows with each argument:
  *              one for the largest call is enough for smaller ones)
  *
- * Sums are float32; x A^T goes into the second product whole where tokens are few,
- * with 16 bits of mantissa in the kernels for prompts (never up to 128 tokens); out
- * is rounded once. Results are bitwise reproducible, and a token's does not
+ * Sums are float32; x A^T goes into the second product whole, or (above rank 32, in
+ * the kernels for prompts, so never up to 128 tokens) with 16 bits of mantissa; out is
+ * rounded once. Results are bitwise reproducible, and a token's does not
  * depend on what the tokens beside it hold (on how many there are by the order of
  * its sums, and those 16 bits). What is not finite stays with its token, or with its adapter and
  * column. Tokens at starts[rows] and above are not read

@@ -64,9 +64,8 @@ def test_prompts(rank, sizes, which, inner, outer):
     assert w4.kernel_status() == 0
 
 
-@pytest.mark.parametrize("rank", [8, 16, 24, 64, 128])
-@pytest.mark.parametrize("tokens", [1, 17, 128])
-def test_few_tokens_keep_all_bits_between_the_products(tokens, rank):
+@pytest.mark.parametrize("tokens,rank", [(n, r) for n in (1, 17, 128) for r in (8, 16, 24, 64, 128)] + [(n, r) for n in (1100, 2500) for r in (8, 16, 24, 32)])
+def test_all_bits_are_kept_between_the_products(tokens, rank):
     """x A^T next to the middle of two bf16 values: 1 + m 2^-7 + 2^-8 and 2^-k more or less, which is exact in float32, as are
     all sums here (B has one 1 a column). So the output is that value, rounded once."""
     rng = np.random.default_rng(rank)
@@ -291,6 +290,50 @@ def test_an_infinite_input_times_positive_weights_is_infinite(tokens, rank):
     p.x[2, 7] = math.inf
     out = p.run()
     assert (out[2] == math.inf).all() and out[:2].isfinite().all() and out[3:].isfinite().all()
+
+
+@pytest.mark.parametrize("tokens", [3, 150, 1100, 2500])
+@pytest.mark.parametrize("rank", [8, 16, 40, 64, 128])
+def test_an_infinite_weight_is_infinite(tokens, rank):
+    """A value of x A^T goes on in parts, none of which may be 0 or of the other sign: infinity times that would not be a
+    number. Values with 8 bits and with more, a large one, and an infinite one."""
+    p = Problem([tokens], [1], rank, 72, 40, 2, scaled=False)
+    p.x[:, 16:] = 0
+    p.x[1, 5] = math.inf                 # x A^T is infinite
+    p.x[2, :16] = 2.0 ** 60
+    p.a[1, 3] = 0
+    p.a[1, 3, 5], p.a[1, 3, 6] = 1.0, 0.01
+    p.x[0, :16] = 0
+    p.x[0, 5] = 1.5                      # 1.5, with nothing below
+    low = p.x.double() @ p.a[1].double().T
+    assert (low[:, 3] != 0).all()
+    for column, value in ((7, math.inf), (9, -math.inf)):
+        p.b[1, column] = 0
+        p.b[1, column, 3] = value
+    out = p.run()
+    for column, sign in ((7, 1.0), (9, -1.0)):
+        got = out[:, column].double()
+        want = torch.sign(low[:, 3]) * sign * math.inf
+        keep = torch.ones(tokens, dtype=torch.bool, device="cuda")
+        keep[1] = False                  # (its other values are infinite too, times a weight of 0: not a number)
+        assert torch.equal(got[keep], want[keep])
+    beside = [c for c in range(40) if c not in (7, 9)]
+    assert out[:, beside][keep].isfinite().all()
+
+
+@pytest.mark.parametrize("tokens", [3, 1100, 2500])
+def test_values_next_to_the_largest(tokens):
+    """x A^T between the largest bf16 value and the largest float32 value stays finite."""
+    y = torch.zeros((tokens, 16), dtype=torch.bfloat16, device="cuda")
+    x, a, b = (torch.zeros(s, dtype=torch.bfloat16, device="cuda") for s in ((tokens, 16), (1, 8, 16), (1, 16, 8)))
+    x[:, :2] = 2.0 ** 100
+    big = torch.finfo(torch.bfloat16).max
+    a[0, 0, 0], a[0, 0, 1] = big / 2.0 ** 100, 2.0 ** 19  # big + 2^119: next to the middle between big and 2^128
+    a[0, 0, 1] *= 1.5
+    b[0, :, 0] = 2.0 ** -100
+    out = w4.lora_add(y, x, a, b, torch.zeros(1, dtype=torch.int32, device="cuda"), torch.tensor([0, tokens], dtype=torch.int32, device="cuda"))
+    want = torch.tensor((big + 1.5 * 2.0 ** 119) * 2.0 ** -100, dtype=torch.float64).to(torch.bfloat16)
+    assert (out.cpu() == want).all()
 
 
 def test_streams_graphs_and_repeats():
