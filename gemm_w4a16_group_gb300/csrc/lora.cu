@@ -587,9 +587,9 @@ __global__ void __launch_bounds__(kThreads, ExpandGeo<RP>::ctas(EVEN)) lora_expa
           v.x += u.x;
           v.y += u.y;
         }
-        if (r >= p.rank) v = make_float2(0.f, 0.f);  // (an infinite x times the padding's zeros is not a number)
+        v = r < p.rank ? make_float2(v.x * scale, v.y * scale) : make_float2(0.f, 0.f);  // (infinity times the padding's zeros is not a number)
         uint32_t part[3];
-        in_parts(v.x * scale, v.y * scale, part);
+        in_parts(v.x, v.y, part);
 #pragma unroll
         for (int k = 0; k < 3; ++k) *reinterpret_cast<uint32_t *>(smem + k * G::PART + row * G::ROW + r * 2) = part[k];
       }
@@ -818,11 +818,11 @@ __global__ void __launch_bounds__(kThreads, 2) lora_prompt_shrink_kernel(const _
       v.z += u.z;
       v.w += u.w;
     }
-    if (r >= p.rank) v = make_float4(0.f, 0.f, 0.f, 0.f);  // (an infinite x times the padding's zeros is not a number)
+    v = r < p.rank ? make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale) : make_float4(0.f, 0.f, 0.f, 0.f);  // (as above)
     constexpr int P = parts_of_rank(RP);
     uint32_t a[P], b[P];
-    in_parts(v.x * scale, v.y * scale, a);
-    in_parts(v.z * scale, v.w * scale, b);
+    in_parts(v.x, v.y, a);
+    in_parts(v.z, v.w, b);
     uint16_t *out = p.low + (long long)list[row] * (P * RP) + r;
 #pragma unroll
     for (int k = 0; k < P; ++k) *reinterpret_cast<uint2 *>(out + k * RP) = make_uint2(a[k], b[k]);

@@ -322,6 +322,18 @@ def test_an_infinite_weight_is_infinite(tokens, rank):
 
 
 @pytest.mark.parametrize("tokens", [3, 1100, 2500])
+@pytest.mark.parametrize("rank", [8, 24, 40, 72])
+def test_an_infinite_scale_is_infinite(tokens, rank):
+    """As an infinite input: the zeros that ranks are padded with are not multiplied by it."""
+    p = Problem([tokens], [1], rank, 72, 40, 2)
+    p.a, p.b, p.x = p.a.abs() + 0.1, p.b.abs() + 0.1, p.x.abs() + 0.1
+    p.scale[1] = math.inf
+    assert (p.run() == math.inf).all()
+    p.scale[1] = -math.inf
+    assert (p.run() == -math.inf).all()
+
+
+@pytest.mark.parametrize("tokens", [3, 1100, 2500])
 def test_values_next_to_the_largest(tokens):
     """x A^T between the largest bf16 value and the largest float32 value stays finite."""
     y = torch.zeros((tokens, 16), dtype=torch.bfloat16, device="cuda")
