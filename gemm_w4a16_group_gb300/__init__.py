@@ -981,7 +981,8 @@ def _walk_outputs(rows, max_tree, like, dev, stream, handle):
 def tree_sample(p, q, draft, mask, starts, u, max_tree, path=None, count=None, token=None, stream=None):
     """Sampled acceptance down each row's draft tree: p and q float32 [tokens,
     vocab], the target's and the drafter's probabilities after each token (rows
-    may be strided; q None: the drafter picked its tokens without chance), u
+    may be strided, and sum to less than 2: one of 64 or more has no token and is
+    reported; q None: the drafter picked its tokens without chance), u
     float32 [tokens] random numbers in [0, 1), draft, mask and starts as in
     tree_accept. Returns (path, count, token) as tree_accept does, token drawn
     from what the refused children leave of p; accepted tokens and the drawn one

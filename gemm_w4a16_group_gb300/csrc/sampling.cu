@@ -343,7 +343,22 @@ __global__ void __launch_bounds__(kProbThreads, 4) probabilities_kernel(const Pr
 // TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kFrac = 56;
-constexpr unsigned long long kOne = 1ull << kFrac;
+constexpr u64 kOne = 1ull << kFrac;
+// Sums stop at 64, in whatever order they are taken, so that none wraps: rows of probabilities are far from it, and a row that
+// gets there has no token and is reported. So is a c of 128 (64 nodes whose rows sum to 2 keep below 126).
+constexpr u64 kMost = 64 * kOne;
+__device__ __forceinline__ u64 add_up(u64 a, u64 b) { return min(a + b, kMost); }  // (of at most 2^63 and kMost)
+// The sum of up to 16 such sums. The upper bits' sum is at least 16 (so the sum kMost), or the sum has not wrapped. (With
+// add_up, one step waiting for the other's comparison, a chain of 6 took 7.82 us, so 7.66, without a limit 7.48.)
+struct Total {
+  u64 sum = 0;
+  uint32_t upper = 0;
+  __device__ __forceinline__ void add(u64 x) {
+    sum += x;
+    upper += (uint32_t)(x >> 58);
+  }
+  __device__ __forceinline__ u64 value() const { return upper >= 16 ? kMost : min(sum, kMost); }
+};
 
 struct SampleParams {
   const float *p, *q;  // q null: children that were picked
@@ -357,7 +372,7 @@ struct SampleParams {
   int *err;
 };
 
-enum { kDone = 0, kSum = 1, kDraw = 2 };
+enum { kDone = 0, kSum = 1, kDraw = 2, kTooMuch = 3 };
 
 // What a CTA does next
 struct Order {
@@ -516,6 +531,10 @@ struct Walk {
       }
       if (drawn) {
         c += asked ? total : kOne;
+        if (c >= 2 * kMost) {
+          o.what = kTooMuch;
+          return;
+        }
         known = false;
       } else {
         bool twin = false;
@@ -636,6 +655,10 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 16 ? 1 : 4) tree_sample_k
     const u64 c = SINGLE ? 0 : sm.order.c;
     const float u = sm.order.u;
     if (what == kDone) break;
+    if (what == kTooMuch) {
+      if (rank == 0 && tid == 0) atomicOr(p.err, kErrIndex);
+      break;
+    }
 
     // this warp's part of the row
     const float *pr = p.p + row * p.p_row, *qr = p.q + row * p.q_row;
@@ -650,7 +673,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 16 ? 1 : 4) tree_sample_k
       load_ends(pr, mine, k, p.vocab, x);
       if (c) load_ends(qr, mine, k, p.vocab, y);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum += weight(x[i], y[i], c, factor);
+      for (int i = 0; i < 4; ++i) sum = add_up(sum, weight(x[i], y[i], c, factor));
     };
     if (!ALIGNED) {
       for (int k = mine.lo + lane; k < mine.hi; k += 32) alone(k);
@@ -705,29 +728,43 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 16 ? 1 : 4) tree_sample_k
         } else {
           two_rows([&](float x0, float x1, float y0, float y1) { add_cut(x0, x1, y0, y1, factor, hi, lo); });
         }
-        sum += join_bits(hi, lo);
+        sum = add_up(join_bits(hi, lo), sum);
       }
     }
-    for (int g = lane; g < gone; g += 32) {
-      const int id = sm.order.ids[g], k = (id + shift) >> 2;
-      if (k >= mine.lo && k < mine.hi) sum -= fixed(pr[id]);  // (of the warp's sum; a lane's own may wrap)
-    }
+    const uint32_t upper = __reduce_add_sync(kFull, (uint32_t)(sum >> 57));  // (as Total's, of 32)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    sum = upper >= 32 ? kMost : min(sum, kMost);
+    if (gone && sum < kMost) {  // (else they are not all of it)
+      u64 less = 0;
+      for (int g = lane; g < gone; g += 32) {
+        const int id = sm.order.ids[g], k = (id + shift) >> 2;
+        if (k >= mine.lo && k < mine.hi) less += fixed(pr[id]);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) less += __shfl_xor_sync(kFull, less, o);
+      sum -= less;
+    }
     if (lane == 0) sm.warps[warp] = sum;
     __syncthreads();
     if (SINGLE) cluster_wait();
     if (tid < (int)S) {
-      u64 all = 0;
+      Total all;
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) all += sm.warps[w];
-      st_cluster_u64(mapa_shared(smem_u32(&sm.sums[pass][rank]), tid), all);
+      for (int w = 0; w < WARPS; ++w) all.add(sm.warps[w]);
+      st_cluster_u64(mapa_shared(smem_u32(&sm.sums[pass][rank]), tid), all.value());
     }
     cluster_sync_all();  // (the next pass's sums go elsewhere, so nobody waits for these to be read)
-    u64 total = 0, before = 0;
+    Total whole;
+    u64 before = 0;
     for (uint32_t i = 0; i < S; ++i) {
-      if (i == rank) before = total;
-      total += sm.sums[pass][i];
+      if (i == rank) before = whole.sum;
+      whole.add(sm.sums[pass][i]);
+    }
+    const u64 total = whole.value();
+    if (total == kMost) {
+      if (rank == 0 && tid == 0) atomicOr(p.err, kErrIndex);
+      break;
     }
     if (what == kSum) {
       if (tid == 0) {

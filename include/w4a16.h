@@ -487,7 +487,9 @@ int w4a16_probabilities(const uint16_t *logits, int64_t logits_row, const float 
  *   token  int64 [rows]  the token drawn (-1 for a row without new tokens)
  *
  * A NaN or negative probability counts as 0, one above 1 as 1; a drafted token
- * outside the vocabulary is passed over (W4A16_ERR_INDEX). Probabilities (and what
+ * outside the vocabulary is passed over (W4A16_ERR_INDEX). A walk that meets a sum
+ * of 64 or a c of 128 ends there with token -1 (W4A16_ERR_INDEX too; rows that sum
+ * to less than 2 have neither). Probabilities (and what
  * refusals leave of each) are rounded to multiples of 2^-46 and summed exactly,
  * tests are double: results do not depend on any order.
  */

@@ -251,6 +251,58 @@ def test_accepted_and_drawn_tokens_are_distributed_as_the_target(drawn):
         assert abs(share - p1[j]) <= 5.5 * (p1[j] * (1 - p1[j]) / n) ** 0.5, (j, share, p1[j])
 
 
+@pytest.mark.parametrize("vocab", [64, 65, 300, 4097, 32000, 248320])
+@pytest.mark.parametrize("drawn", [True, False])
+def test_rows_that_sum_to_64_have_no_token_and_are_reported(vocab, drawn):
+    """Rows of ones: their sums would wrap at 256. The rows beside them, and nodes before them, stay as they are."""
+    rng = np.random.default_rng(vocab)
+    for size, words in ((1, [1]), (3, [1, 3, 7]), (3, [1, 3, 5])):
+        p, q = dist(rng, 3 * size, vocab), dist(rng, 3 * size, vocab)
+        draft, u = rng.integers(0, vocab, 3 * size), np.full(3 * size, 0.4, np.float32)
+        words = np.array(words * 3, np.uint64)
+        q[:, draft] = 1e-6  # children are accepted where p has anything there
+        last = size + (2 if list(words[:3]) == [1, 3, 7] else 1 if size > 1 else 0)
+        p[last] = 1.0  # the node at which the middle row's walk ends
+        path, count, token = call(p, q if drawn else None, draft, words, [size] * 3, np.where(np.arange(3 * size) % size, 0.0, u))
+        assert w4.kernel_status() == -6
+        for b in range(3):
+            s = slice(b * size, (b + 1) * size)
+            want, tok = sampled(p[s], q[s] if drawn else None, draft[s], words[s], np.where(np.arange(size), 0.0, u[s]).astype(np.float32), False)
+            assert path[b, :count[b]].tolist() == want
+            assert token[b] == (-1 if b == 1 else tok)
+
+
+def test_sums_up_to_64_are_kept():
+    """Rows that are no distributions, below that: by the rules all the same."""
+    vocab = 127
+    rng = np.random.default_rng(7)
+    p, q = np.full((9, vocab), 0.5, np.float32), dist(rng, 9, vocab)
+    words = np.array([1, 3, 5, 9] + [1] * 5, np.uint64)
+    draft = rng.integers(0, vocab, 9)
+    sizes = [4, 1, 1, 1, 1, 1]
+    u = np.array([0.9, 0.0, 1.0, 1.0, 0.0, 0.25, 0.5, 0.75, 0.99], np.float32)
+    for drawn in (q, None):
+        for first in (0.0, 0.6, 1.0):
+            u[1] = first
+            check(p, drawn, draft, words, sizes, u)
+
+
+def test_many_refusals_of_rows_that_sum_to_almost_2():
+    """c grows by the row's sum with each child that q and p leave nothing: to 125, or past 128 where rows sum to more."""
+    vocab, n = 70, 64
+    p = np.full((n, vocab), 1.99 / 64, np.float32)
+    p[:, 64:] = 0.0
+    q = np.zeros((n, vocab), np.float32)
+    words = np.array([1] + [1 | 1 << i for i in range(1, n)], np.uint64)
+    draft = np.full(n, 66)
+    u = np.full(n, 0.5, np.float32)
+    check(p, q, draft, words, [n], u)
+    path, count, token = call(p * 30, q, draft, words, [n], u)  # 59.7 a row
+    assert w4.kernel_status() == -6 and count.tolist() == [1] and token.tolist() == [-1]
+    for few in (2, 3):  # one or two refusals of such rows are counted
+        check(p[:few] * 30, q[:few], draft[:few], words[:few], [few], u[:few])
+
+
 def test_streams_graphs_and_repeats():
     p, q, draft, words, sizes, u = problem(6, [6, 2, 7], 2003, 3, True)
     up = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
