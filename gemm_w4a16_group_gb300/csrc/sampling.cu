@@ -40,11 +40,9 @@ struct Quads {
     return whole_hi < hi && hi - 1 >= whole_lo ? hi - 1 : -1;
   }
   __device__ __forceinline__ bool is_whole(int k) const { return k >= whole_lo && k < whole_hi; }
-  // where quads begin `off` elements after words of four: the words that hold some of the whole quads, each of which has an
-  // element of the row (without a whole quad there is none, and the word at whole_hi may be past the row)
-  __device__ __forceinline__ bool in_word(int k, int off) const {
-    return k >= whole_lo && k < whole_hi + (off && whole_lo < whole_hi ? 1 : 0);
-  }
+  // Where quads begin `off` elements after words of four: the end of the words, from whole_lo on, that hold some of the whole
+  // quads; each has an element of the row. (Without a whole quad there is none: the word at whole_hi may be past the row.)
+  __device__ __forceinline__ int words_end(int off) const { return whole_hi + (off && whole_lo < whole_hi ? 1 : 0); }
 };
 
 // ---------------------------------------------------------------------------
@@ -180,7 +178,8 @@ __global__ void __launch_bounds__(kProbThreads, 4) probabilities_kernel(const Pr
   const float t = p.temperature ? p.temperature[r] : 1.f, floor = p.floor ? p.floor[r] : -INFINITY;
   const bool greedy = !(t > 0.f), ends = q.whole_lo > q.lo || q.whole_hi < q.hi;
 
-  // a logit of -inf stays -inf through difference and product, whatever the temperature
+  // a logit of -inf stays -inf through difference and product, whatever the temperature (below 2^-127 as there, where the factor
+  // is still a number)
   const float lowest = -3.40282347e38f, a = greedy ? 1.f : fmaxf(fminf(__fdiv_rn(1.44269502f, t), 1e30f), 1e-44f);
   const f32x2 a2 = f32_pair(a, a);
   uint2 x[kQuads];
@@ -193,7 +192,7 @@ __global__ void __launch_bounds__(kProbThreads, 4) probabilities_kernel(const Pr
     for (int u = 0; u < kQuads; ++u) {
       const int k = k0 + u * kStep + at0;
       x[u] = make_uint2(kNone, kNone);
-      if (q.in_word(k, off)) x[u] = load_word(row, q, k, off);
+      if (k >= q.whole_lo && k < q.words_end(off)) x[u] = load_word(row, q, k, off);
     }
     if (!ALIGNED) {
 #pragma unroll

@@ -35,14 +35,16 @@ int main() {
             bad += (int)q.is_whole(k) + (q.end(0) == k) + (q.end(1) == k) != 1;
             bad += at + 4 <= 0 || at >= n;
           }
-          for (int off = 0; off < 4; ++off)
+          for (int off = 0; off < 4; ++off) {
+            auto in_word = [&](int k) { return k >= q.whole_lo && k < q.words_end(off); };
             for (int k = q.lo; q.lo < q.hi && k < q.hi + 2; ++k) {
               const int at = 4 * k - shift - off;  // the word's first element
-              if (q.in_word(k, off) && (at + 4 <= 0 || at >= n)) {
+              if (in_word(k) && (at + 4 <= 0 || at >= n)) {
                 if (!bad++) std::printf("n %%d shift %%d off %%d part %%u of 2^%%d: word %%d at element %%d\\n", n, shift, off, i, log2, k, at);
               }
-              if (q.is_whole(k)) bad += !q.in_word(k, off) || (off && !q.in_word(k + 1, off));
+              if (q.is_whole(k)) bad += !in_word(k) || (off && !in_word(k + 1));
             }
+          }
         }
         bad += next != (shift + n + 3) / 4;
       }
