@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kProbThreads, 4) probabilities_kernel(const Pr
 
   // a logit of -inf stays -inf through difference and product, whatever the temperature (below 2^-127 as there, where the factor
   // is still a number)
-  const float lowest = -3.40282347e38f, a = greedy ? 1.f : fmaxf(fminf(__fdiv_rn(1.44269502f, t), 1e30f), 1e-44f);
+  const float lowest = -3.40282347e38f, a = greedy ? 1.f : fmaxf(__fdiv_rn(1.44269502f, fmaxf(t, 5.87747175e-39f)), 1e-44f);
   const f32x2 a2 = f32_pair(a, a);
   uint2 x[kQuads];
   float m = lowest, s = 0.f, mine = lowest;

@@ -455,8 +455,8 @@ int w4a16_tree_accept(const int64_t *target, const int64_t *draft, const int64_t
  *
  * A row with nothing above -inf gets 0 throughout; a NaN (or +inf) that is kept
  * makes the row's kept probabilities NaN. A probability is off by less than 2^-17 +
- * 2^-23 (max - l_j) / T of itself; below 2^-126 it may be 0. out must not overlap
- * what is read.
+ * 2^-22 (max - l_j) / T of itself; below 2^-126 it may be 0. A T between 0 and 2^-127
+ * counts as 2^-127. out must not overlap what is read.
  */
 int w4a16_probabilities(const uint16_t *logits, int64_t logits_row, const float *temperature, const float *floor,
                         int tokens, int vocab, float *out, w4a16_stream_t stream);

@@ -2,6 +2,7 @@
 logits, values that are not numbers, odd widths and strides."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -70,6 +71,27 @@ def test_temperatures_at_the_ends():
     assert got[2, 5] == 0.5 and got[2, 700] == 0.5
     flat = w4.probabilities(x, torch.full((10,), math.inf, device="cuda"))
     assert ((flat - 1 / 777).abs() <= 2.0 ** -17 / 777).all()
+
+
+def test_the_smallest_temperatures():
+    """Logits as close together as their temperature is small, down to 2^-127; below that it counts as 2^-127.
+
+    The exponent (l - m) a, a = log2(e) / T, in float32: log2(e) is off by 2^-26, and the quotient, the difference and the
+    product are rounded once each, 3.25 2^-24 in all, which ln 2 log2(e) leaves as it is: less than 2^-22 (max - l) / T."""
+    low = 2.0 ** -127
+    got = w4.probabilities(torch.tensor([[0.0, -1e-31]], device="cuda").to(BF16), torch.tensor([1e-38], device="cuda"))
+    assert got.tolist() == [[1.0, 0.0]]
+    for t in (1e-20, 1e-30, 7e-31, 1e-35, 2.0 ** -126, 1e-38, low):
+        x = (torch.randn((1, 3001), generator=torch.Generator().manual_seed(1)) * 4 * t).to(BF16).cuda()
+        got = w4.probabilities(x, torch.tensor([t], device="cuda")).double()
+        x, t = x.double(), float(np.float32(t))
+        want = torch.softmax((x - x.max()) / t, -1)
+        assert ((got - want).abs() <= want * (2.0 ** -17 + 2.0 ** -22 * (x.max() - x) / t) + 2.0 ** -126).all()
+    x = torch.tensor([[0.0, -2.0 ** -133, -2.0 ** -130, -2.0 ** -126, -2.0 ** -120]], device="cuda").to(BF16)
+    want = w4.probabilities(x, torch.tensor([low], device="cuda"))
+    assert ((want.double() - torch.softmax(x.double() / low, -1)).abs() <= 2.0 ** -17).all()
+    for t in (1e-39, 1e-42, 1.5e-45):
+        assert torch.equal(w4.probabilities(x, torch.tensor([t], device="cuda")), want)
 
 
 def test_masked_logits():
