@@ -115,8 +115,9 @@ def decode(model, prompts, adapter, temperature, steps, trees, seed=1):
         for s, new in zip(said, users.verify() if trees else users.step()):
             s += new
         calls += 1
-    if w4.kernel_status() != 0:
-        raise RuntimeError(f"kernel status {w4.kernel_status()}")
+    status = w4.kernel_status()
+    if status != 0:
+        raise RuntimeError(f"kernel status {status}")
     return [s[:steps] for s in said], calls
 
 

@@ -171,8 +171,9 @@ def speculative(model, prompts, steps, truth, e4m3=False, seed=1):
             accepted = [int(tokens[int(starts[r]) + i]) for i in path[r, 1:int(count[r])].tolist()]
             said[b] += accepted + [int(token[r])]
         verifies += 1
-    if w4.kernel_status() != 0:
-        raise RuntimeError(f"kernel status {w4.kernel_status()}")
+    status = w4.kernel_status()
+    if status != 0:
+        raise RuntimeError(f"kernel status {status}")
     return [s[:steps] for s in said], verifies
 
 
