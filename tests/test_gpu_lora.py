@@ -154,6 +154,32 @@ def test_rows_that_begin_anywhere(tokens, outer):
             assert torch.equal(p.run(out=p.y), want)
 
 
+@pytest.mark.parametrize("rank", [24, 40, 56, 72, 120])
+@pytest.mark.parametrize("sizes,which,inner,outer", [
+    ([300, 7, 1913, 1], [1, -1, 0, 1], 1024, 264), ([2100], [0], 328, 515), ([129, 1], [0, 1], 64, 70000), ([600, 80], [1, 0], 64, 8201),
+])
+def test_prompts_of_padded_ranks(rank, sizes, which, inner, outer):
+    p = Problem(sizes, which, rank, inner, outer, 2, seed=rank)
+    p.check(p.run())
+    assert w4.kernel_status() == 0
+
+
+@pytest.mark.parametrize("rank", [16, 40, 128])
+@pytest.mark.parametrize("lead,outer,width", [(0, 256, 512), (256, 128, 512), (3, 101, 259), (7, 513, 640)])
+def test_columns_of_a_wider_product_of_prompts(rank, lead, outer, width):
+    """As test_columns_of_a_wider_product, for the kernels of prompts; rows without an adapter and padding stay too."""
+    p = Problem([900, 600, 800], [0, -1, 1], rank, 128, outer, 2, seed=lead, pad=3)
+    wide = torch.randn((p.tokens, width + lead), device="cuda").to(torch.bfloat16)
+    before = wide.clone()
+    view = wide[:, lead:lead + outer]
+    p.y = view.clone()
+    w4.lora_add(view, p.x, p.a, p.b, p.adapter, p.starts, p.scale, out=view)
+    p.check(view.contiguous())
+    beside = torch.ones(wide.shape[1], dtype=torch.bool)
+    beside[lead:lead + outer] = False
+    assert torch.equal(wide[:, beside], before[:, beside]) and torch.equal(wide[p.live:], before[p.live:])
+
+
 def test_strided_inputs():
     p = Problem([4, 9], [1, 0], 32, 256, 200, 2)
     want = p.run()
