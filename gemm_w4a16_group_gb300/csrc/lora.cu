@@ -19,8 +19,8 @@
 //   go to the workspace as float32 and expand adds them up. The k order of a
 //   fragment is free as long as both operands agree, so a lane's 16 bytes of
 //   consecutive k serve two products as they come. One token of rank 16, 5,120
-//   by 5,120: 5.2 us; 48 tokens of 12 adapters of rank 64, 5,120 by 34,816: 21.7
-//   us, 3.2 TB/s.
+//   by 5,120: 5.2 us; 48 tokens of 12 adapters of rank 64, 5,120 by 34,816: 23.2
+//   us, 3.0 TB/s.
 // - Prompts: tiles of 128, products on tcgen05, sums in TMEM; a cluster adds up
 //   the parts over K in distributed shared memory. 4,096 tokens of rank 16, 5,120
 //   by 34,816: 121 us, 5.1 TB/s; six prompts of 2,000 and rank 64, 5,120 by 7,168:
@@ -335,13 +335,15 @@ __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(const __grid_c
 // the tile's tokens. t goes into the product whole, as three bf16 parts (with two,
 // 16 bits of mantissa, one output in a thousand is the neighbour of what float32
 // gives, with three one in four thousand, by the order of sums; 48 tokens of 12
-// adapters 22.8 | 24.0 us, one token 5.26 | 5.35). The rows of B that a product's eight columns stand for are chosen
-// such that a lane ends up with eight consecutive columns of a token: y is read
-// and written 16 bytes at a time. B is what there is to read: every warp copies
-// its own columns to shared memory some units ahead, and begins before there is
-// a t. Small slots hide more of the latency as many of them than as more CTAs,
-// large ones the other way: rank 64 with three CTAs of two slots an SM 21.1 us, one
-// of four 24.4 (B straight to registers: 23.8; B brought to L2 by shrink: 26.7).
+// adapters of rank 16 11.9 | 12.3 us, of 64 22.8 | 23.2, of 128 32.2 | 35.0). The rows
+// of B that a product's eight columns stand for are chosen such that a lane ends up
+// with eight consecutive columns of a token: y is read and written 16 bytes at a time.
+// B is what there is to read: every warp copies its own columns to shared memory some
+// units ahead, and begins before there is a t. Small slots hide more of the latency as
+// many of them than as more CTAs, large ones the other way: rank 64 with three CTAs of
+// two slots an SM 23.5 us, two of three 24.9 (and, with t in two parts, one of four 24.4
+// where three of two took 21.1, B straight to registers 23.8, B brought to L2 by shrink
+// 26.7).
 // ---------------------------------------------------------------------------
 template <int RP>
 struct ExpandGeo {
@@ -387,7 +389,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 // The upper 16 bits of a value, as a bf16 value: cut, not rounded, and one step less where nothing would be left below. So
 // what is left is not 0 and has the same sign, and an infinite weight times the parts of a value is infinite, not inf - inf or
-// 0 inf. (Of infinity it is the largest bf16 value, and infinity is left.)
+// 0 inf (of values from 2^-95 on, whose last part is no smaller than 2^-126). Of infinity it is the largest bf16 value, and
+// infinity is left.
 __device__ __forceinline__ uint32_t upper_bits(float a) { return __float_as_uint(a) - (a != 0.f ? 1 : 0) & 0xFFFF0000u; }
 // Two values as bf16 parts each: three, whose sum is the value, or two, off by 2^-16 of it at most
 __device__ __forceinline__ void in_parts(float a, float b, uint32_t (&part)[3]) {
@@ -857,8 +860,9 @@ __device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&v)[16
 // products are added there in place, and a step later the sums leave in whole
 // rows. Bound by HBM, which does 6.0 - 6.2 TB/s of such rows read and written (64
 // bytes of eight rows an instruction, as a fragment has them: 5.6); rank 16, 4,096
-// tokens of 34,816 columns: 103 us from a cold cache, 5.5 TB/s. (With mma.sync and B in registers the warps had 460 - 560 instructions for
-// 1,024 elements and ranks of 64 took 63 us where 16 took 36.)
+// tokens of 34,816 columns: 103 us from a cold cache, 5.5 TB/s. (With mma.sync and B in
+// registers the warps had 460 - 560 instructions for 1,024 elements and ranks of 64 took
+// 63 us where 16 took 36.)
 //
 // Rows need not begin on 16 bytes: element c of a row that begins s elements
 // after such a boundary has place c + s, and places are moved eight at a time
@@ -1167,19 +1171,24 @@ int padded_rank(int rank, bool few) { return rank <= 8 && few ? 8 : rank <= 16 ?
 
 // Few tokens take the first pair of kernels, whose tiles of 16 read their adapter
 // anew; the prompts' tiles of 128 are late to begin, and mostly empty where many
-// adapters share few tokens. First | second pair, K 5,120, one adapter:
+// adapters share few tokens. First | second pair, K 5,120, one adapter, three
+// inputs in turn:
 //   columns  tokens  rank 16     rank 64     rank 128
-//    34,816     256  14.8 | 24   20.7 | 25.5  37 | 32 us
-//    34,816     512  29.8 | 30.6 34.2 | 33.3  85 | 45
-//    34,816     768  51.5 | 38.5 54   | 41   120 | 58
-//     7,168   1,024  15.4 | 22.5 22   | 23.9
-//     7,168   2,048  29.7 | 27.6 38.6 | 29.4
-//     1,024   1,536  11.4 | 19.3 16.9 | 20.2  26 | 23
-// and 1,024 rows of one token and 48 adapters, 34,816 columns 100 | 144 with rank 16,
-// 113 | 162 with 64. So the first pair has y up to 2^24 elements and products up to
+//    34,816     256  19.2 | 25.2 25.0 | 26.2  53 | 34 us
+//    34,816     512  30.8 | 32.1 39.0 | 33.5  94 | 45
+//    34,816     768  42.3 | 38.5 56.0 | 40.9 128 | 58
+//     7,168   1,024  20.0 | 23.4 26.0 | 24.2
+//     7,168   2,048  31.4 | 28.9 45.7 | 30.5
+//     1,024   1,536  11.1 | 19.2 16.8 | 19.9  31 | 23
+// and 1,024 rows of one token and 48 adapters, 34,816 columns 83 | 146 with rank 16,
+// 120 | 163 with 64. So the first pair has y up to 2^24 elements and products up to
 // 2^30 of tokens, ranks and K + columns (above rank 64, where an SM has one CTA of
-// expand, K + 2 columns: 1,090 tokens, K 320, 7,232 columns 36 | 26, but 515 tokens, K
-// 7,248, 2,854 columns 23 | 30), or fewer than 32 tokens an adapter.
+// expand, K + 2 columns: 1,090 tokens, K 320, 7,232 columns 45 | 26, but 515 tokens, K
+// 7,248, 2,854 columns 23 | 30). At three points of the table that is the slower side,
+// by 4 to 9 %. It also has calls of fewer than 32 tokens for each adapter that the rows
+// could have (as many as the store has, or as there are rows: which ones they have only
+// the device knows, so a prompt that is given as a row for each token, beside a large
+// store, takes it too).
 constexpr int kAlwaysFew = 128, kMostFew = 2048;
 bool few(const LoraCall &c, int groups) {
   if (c.tokens <= kAlwaysFew || c.tokens > kMostFew) return c.tokens <= kAlwaysFew;
@@ -1188,9 +1197,10 @@ bool few(const LoraCall &c, int groups) {
 }
 int groups_of(int adapters, int rows) { return adapters < rows ? adapters : rows; }
 
-// Few tokens: parts of K. As many CTAs as fit at once, but at least two steps of
-// 32 k for each warp (one token: 5.4 us, with one step 6.1, with four 6.1), and
-// no more than 32 sums for expand to add up.
+// Few tokens: parts of K. As many CTAs as fit at once (304: two on each of 152 SMs;
+// not asked of the device, because the workspace's size follows from it), but at least
+// two steps of 32 k for each warp (one token: 5.4 us, with one step 6.1, with four
+// 6.1), and no more than 32 sums for expand to add up.
 int parts_of(int tokens, int rank, int inner) {
   const int tiles = (tokens + 15) / 16, step = 2 * 32 * (rank > 64 ? kWarps / 2 : kWarps);
   const int want = 304 / tiles, most = (inner + step - 1) / step;

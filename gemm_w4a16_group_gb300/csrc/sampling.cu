@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kProbThreads, 4) probabilities_kernel(const Pr
 // trees of 8 nodes over 248,320 tokens: 31 us. 18 are the tree's own loads (the
 // offsets, then the nodes, then their probabilities: 5 us) and the first pass of all
 // rows; the rest is further passes of rows with refusals, one after the other on the
-// few SMs that a cluster is on. One draw each for 64 tokens over 128,000: 8.6 us, 3.8
+// few SMs that a cluster is on. One draw each for 64 tokens over 128,000: 8.9 us, 3.7
 // TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kFrac = 56;
@@ -924,7 +924,7 @@ cudaError_t launch_tree_sample(const SampleCall &c) {
   const bool aligned = !c.q || (((reinterpret_cast<uintptr_t>(c.p) - reinterpret_cast<uintptr_t>(c.q)) / 4) % 4 == 0 && (c.q_row - c.p_row) % 4 == 0);
   const SampleParams p{c.p, c.q, c.p_row, c.q_row, c.draft, c.mask, c.starts, c.u, c.rows, c.tokens, c.vocab, c.max_tree,
                        c.path, c.count, c.token, c.err};
-  // 16 warps a CTA while every CTA has an SM to itself (a chain of six 7.5 us against 9.9 with 8), 8 where that makes more
+  // 16 warps a CTA while every CTA has an SM to itself (a chain of six 7.5 us against 9.9 with 8, sums without a limit), 8 where that makes more
   // of them (32 trees of eight 31 us against 34)
   const int s = ctas_of(c.rows, c.vocab, 32768, 1024, c.sm_count * 2);
   const bool few = (long long)c.rows * s * 2 <= c.sm_count * 2, one = c.max_tree == 1;

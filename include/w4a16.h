@@ -563,14 +563,15 @@ int w4a16_kv_reserve(int32_t *page_table, int max_pages, int table_rows, int32_t
  *
  * Sums are float32; x A^T goes into the second product whole, or (above rank 32, in
  * the kernels for prompts, so never up to 128 tokens) with 16 bits of mantissa; out is
- * rounded once. Results are bitwise reproducible, and a token's does not
- * depend on what the tokens beside it hold (on how many there are by the order of
- * its sums, and those 16 bits). What is not finite stays with its token, or with its adapter and
- * column. Tokens at starts[rows] and above are not read
- * and not written. An adapter outside -1 .. adapters - 1 counts as -1, a row whose
- * offsets cannot be is left out, and where offsets descend, tokens of a row that lie
- * before the end of an earlier one are that one's, or nobody's (then they are not
- * written); w4a16_kernel_status() then returns W4A16_ERR_INDEX.
+ * rounded once. Results are bitwise reproducible, and a token's does not depend on
+ * what the tokens beside it hold (on how many there are by the order of its sums, and
+ * those 16 bits). What is not finite stays with its token, or with its adapter and
+ * column, and is what the formula says (an infinite weight times values of x A^T from
+ * 2^-95 on). Tokens at starts[rows] and above are not read and not written. An adapter
+ * outside -1 .. adapters - 1 counts as -1, a row whose offsets cannot be is left
+ * out, and where offsets descend, tokens of a row that lie before the end of an earlier
+ * one are that one's, or nobody's (then they are not written);
+ * w4a16_kernel_status() then returns W4A16_ERR_INDEX.
  * ------------------------------------------------------------------------ */
 #define W4A16_MAX_ADAPTERS 4096
 #define W4A16_MAX_RANK 128
